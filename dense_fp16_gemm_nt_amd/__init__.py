@@ -13,6 +13,10 @@ import ctypes
 import os
 import threading
 
+from . import attention
+from .attention import (attention_prompt, attention_prompt_workspace, attention_shared_prefix,
+                        attention_shared_prefix_workspace)
+
 PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(PKG, "libgemm_f16_nt.so")
 
@@ -95,6 +99,7 @@ def lib() -> ctypes.CDLL:
                                                    ctypes.POINTER(ctypes.c_uint32)]
             L.gemm_f16_nt_ring_plan.restype = i32
             L.gemm_f16_nt_ring_plan.argtypes = [i32, i64, ctypes.POINTER(ctypes.c_int), i64p, i64p]
+            attention.declare(L)
             _lib = L
     return _lib
 

@@ -1,0 +1,389 @@
+"""The attention operators on the GPU against the plain 64-bit form (attention_ref.py derives the bounds)."""
+import math
+import sys
+
+import pytest
+
+import dense_fp16_gemm_nt_amd as g
+from tests import attention_ref as ref
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+DEV = "cuda:0"
+TYPES = {"fp16": torch.float16, "bf16": torch.bfloat16}
+
+
+def say(*a):
+    print(*a, file=sys.stderr, flush=True)
+
+
+def rand(gen, dtype, *shape):
+    return torch.randn(*shape, generator=gen, dtype=torch.float32).to(TYPES[dtype])
+
+
+def cu(lens, first=0):
+    out = [first]
+    for n in lens:
+        out.append(out[-1] + n)
+    return out
+
+
+def ints(x):
+    return torch.tensor(x, dtype=torch.int32, device=DEV)
+
+
+def run_prompt(q, k, v, cq, ck, causal, scale=None, **kw):
+    say(f"[gpu] prompt q={tuple(q.shape)} k={tuple(k.shape)} {q.dtype} causal={causal} cu_q={cq[:9]} cu_k={ck[:9]}")
+    O, lse = g.attention_prompt(q.to(DEV), k.to(DEV), v.to(DEV), ints(cq), ints(ck), causal=causal, scale=scale,
+                                return_lse=True, **kw)
+    torch.cuda.synchronize()
+    return O.cpu(), lse.cpu()
+
+
+def check_prompt(q, k, v, cq, ck, causal, scale=None, **kw):
+    O, lse = run_prompt(q, k, v, cq, ck, causal, scale, **kw)
+    s = 1 / math.sqrt(q.shape[2]) if scale is None else scale
+    return ref.prompt(q, k, v, cq, ck, causal, s, O, lse, f"prompt {q.dtype} d={q.shape[2]} causal={causal}")
+
+
+LENS = [
+    ([1], [1]),
+    ([33], [33]),
+    ([1, 0, 2, 63, 64, 65, 127, 128, 129], [1, 0, 2, 63, 64, 65, 127, 128, 129]),
+    ([5, 40, 1, 0, 130], [200, 41, 700, 3, 131]),        # chunks behind earlier keys, single tokens, keys without queries
+    ([40, 3, 100, 7], [10, 0, 99, 1]),                   # fewer keys than queries, none at all
+]
+
+
+@pytest.mark.parametrize("lens", range(len(LENS)))
+@pytest.mark.parametrize("dtype", sorted(TYPES))
+@pytest.mark.parametrize("heads,kv_heads,d", [(4, 1, 128), (2, 2, 64), (6, 2, 96), (5, 5, 80), (3, 1, 8), (2, 1, 40), (1, 1, 120)])
+@pytest.mark.parametrize("causal", [True, False])
+def test_prompt(causal, heads, kv_heads, d, dtype, lens):
+    gen = torch.Generator().manual_seed(1000 + 7 * lens + d)
+    cq, ck = cu(LENS[lens][0]), cu(LENS[lens][1])
+    q, k, v = rand(gen, dtype, cq[-1], heads, d), rand(gen, dtype, ck[-1], kv_heads, d), rand(gen, dtype, ck[-1], kv_heads, d)
+    check_prompt(q, k, v, cq, ck, causal)
+
+
+@pytest.mark.parametrize("dtype", sorted(TYPES))
+@pytest.mark.parametrize("d", [64, 128])
+def test_prompt_many_sequences(d, dtype):
+    # more sequences than lanes look at in one go, some without a token
+    gen = torch.Generator().manual_seed(5)
+    lens = [(7 * i) % 23 for i in range(150)]
+    c = cu(lens)
+    q, k, v = (rand(gen, dtype, c[-1], h, d) for h in (4, 2, 2))
+    check_prompt(q, k, v, c, c, True)
+
+
+@pytest.mark.parametrize("dtype", sorted(TYPES))
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("n,m,heads,kv_heads,d", [(700, 700, 2, 1, 128), (1, 3000, 8, 2, 128), (3, 2501, 4, 4, 64),
+                                                  (130, 1999, 2, 2, 96), (65, 1030, 64, 1, 64)])
+def test_prompt_long_keys(n, m, heads, kv_heads, d, causal, dtype):
+    # few row tiles: the keys are split and joined
+    gen = torch.Generator().manual_seed(n + m)
+    q, k, v = rand(gen, dtype, n, heads, d), rand(gen, dtype, m, kv_heads, d), rand(gen, dtype, m, kv_heads, d)
+    need = g.attention_prompt_workspace(q.to(DEV), k.to(DEV), v.to(DEV), ints([0, n]), ints([0, m]))
+    assert need > 0 or m < 1000
+    check_prompt(q, k, v, [0, n], [0, m], causal)
+
+
+def test_prompt_peaked_and_large_scores():
+    # maxima that rise from tile to tile, scores of several hundred
+    gen = torch.Generator().manual_seed(9)
+    n, d = 300, 128
+    q, k, v = (rand(gen, "fp16", n, 2, d) for _ in range(3))
+    k = (k.float() * torch.linspace(0.1, 6, n)[:, None, None]).half()
+    check_prompt(q * 4, k, v, [0, n], [0, n], True)
+    check_prompt(q * 4, k.flip(0).contiguous(), v, [0, n], [0, n], False)
+
+
+@pytest.mark.parametrize("scale", [-0.1, 0.0, 1e-30, 0.5])
+def test_prompt_scales(scale):
+    gen = torch.Generator().manual_seed(11)
+    q, k, v = (rand(gen, "bf16", 150, h, 64) for h in (4, 2, 2))
+    check_prompt(q, k, v, [0, 150], [0, 150], True, scale=scale)
+
+
+@pytest.mark.parametrize("dtype", sorted(TYPES))
+def test_prompt_strides(dtype):
+    gen = torch.Generator().manual_seed(13)
+    c = cu([70, 129, 1])
+    H, Hk, d = 6, 2, 64
+    want = None
+    qkv = rand(gen, dtype, c[-1], H + 2 * Hk, d)
+    for layout in ("fused", "heads_first", "padded", "broadcast"):
+        x = qkv.to(DEV)
+        q, k, v = x[:, :H], x[:, H:H + Hk], x[:, H + Hk:]
+        O = torch.full((c[-1], H, d), float("nan"), dtype=TYPES[dtype], device=DEV)
+        if layout == "heads_first":
+            q, k, v = (t.transpose(0, 1).contiguous().transpose(0, 1) for t in (q, k, v))
+            O = O.transpose(0, 1).contiguous().transpose(0, 1)
+        elif layout == "padded":
+            pad = [torch.full((c[-1], t.shape[1], d + 24), float("nan"), dtype=t.dtype, device=DEV) for t in (q, k, v)]
+            for p, t in zip(pad, (q, k, v)):
+                p[:, :, 8:8 + d] = t
+            q, k, v = (p[:, :, 8:8 + d] for p in pad)
+            O = torch.full((c[-1], H, d + 8), float("nan"), dtype=TYPES[dtype], device=DEV)[:, :, :d]
+        elif layout == "broadcast":   # every query head of its own kv head, repeated without a copy
+            k, v = (t[:, :, None, :].expand(-1, -1, H // Hk, -1).as_strided(
+                (c[-1], Hk, H // Hk, d), (t.stride(0), t.stride(1), 0, 1)) for t in (k, v))
+            k, v = k[:, 0], v[:, 0]   # kv head 0 for the first H // Hk heads, head stride 0
+            q, O = q[:, :H // Hk], O[:, :H // Hk]
+        say(f"[gpu] prompt strides {layout} {dtype}")
+        out = g.attention_prompt(q, k, v, ints(c), causal=True, O=O)
+        torch.cuda.synchronize()
+        assert out is O
+        if want is None:
+            want = O.cpu()
+            ref.prompt(qkv[:, :H], qkv[:, H:H + Hk], qkv[:, H + Hk:], c, c, True, 1 / 8, want, None, "fused")
+        elif layout == "broadcast":
+            assert torch.equal(O.cpu(), want[:, :H // Hk])
+        else:
+            assert torch.equal(O.cpu(), want)
+
+
+@pytest.mark.parametrize("splits", [False, True])
+def test_prompt_rows_of_no_sequence(splits):
+    # tokens before the first and behind the last sequence: left as they were
+    gen = torch.Generator().manual_seed(17)
+    n, m, H, d = 200, 2000 if splits else 180, 2, 64
+    q, k, v = rand(gen, "fp16", n, H, d), rand(gen, "fp16", m, H, d), rand(gen, "fp16", m, H, d)
+    cq, ck = [20, 90, 90, 150], [5, m // 2, m // 2, m - 30]
+    O = torch.full((n, H, d), 7.0, dtype=torch.float16, device=DEV)
+    lse = torch.full((n, H), 7.0, device=DEV)
+    poison = torch.full_like(k, float("nan"))
+    poison[5:m - 30] = k[5:m - 30]
+    poison_v = torch.full_like(v, float("inf"))
+    poison_v[5:m - 30] = v[5:m - 30]
+    got, got_lse = run_prompt(q, poison, poison_v, cq, ck, False, O=O, lse=lse)
+    ref.prompt(q, k, v, cq, ck, False, 1 / 8, got, got_lse, "inner rows")
+    for x in (got, got_lse):
+        assert bool((x[:20] == 7).all()) and bool((x[150:] == 7).all())
+
+
+@pytest.mark.parametrize("d,dtype", [(128, "fp16"), (64, "bf16"), (96, "fp16")])
+def test_prompt_neighbours_with_infinities(d, dtype):
+    # every second sequence holds NaN and infinities: the others do not see them
+    gen = torch.Generator().manual_seed(19)
+    lens = [50, 30, 64, 10, 33, 100, 3]
+    c = cu(lens)
+    q, k, v = (rand(gen, dtype, c[-1], 2, d) for _ in range(3))
+    k2, v2, q2 = k.clone(), v.clone(), q.clone()
+    for b in range(1, len(lens), 2):
+        for x, bad in ((q2, float("nan")), (k2, float("inf")), (v2, float("nan"))):
+            x[c[b]:c[b + 1]] = bad
+    O, lse = run_prompt(q2, k2, v2, c, c, True)
+    for b in range(0, len(lens), 2):
+        s = slice(c[b], c[b + 1])
+        ref.prompt(q[s], k[s], v[s], [0, lens[b]], [0, lens[b]], True, 1 / math.sqrt(d), O[s], lse[s], f"sequence {b}")
+
+
+def test_prompt_offsets_that_make_no_sense():
+    # tables that fall, run past the tensors or are negative: clamped, and nothing outside is written
+    gen = torch.Generator().manual_seed(23)
+    q, k, v = (rand(gen, "fp16", 100, 2, 64).to(DEV) for _ in range(3))
+    whole = torch.full((140, 2, 64), 3.0, dtype=torch.float16, device=DEV)
+    for cq, ck in (([0, 1000, 50, 70], [0, 100, 100, 2 ** 31 - 1]), ([-5, 30, 20, 2 ** 31 - 1], [90, 10, -7, 50]),
+                   ([2 ** 31 - 1, -2 ** 31, 5, 5], [0, 0, 0, 0])):
+        say(f"[gpu] offsets {cq} {ck}")
+        g.attention_prompt(q, k, v, ints(cq), ints(ck), causal=True, O=whole[20:120])
+        torch.cuda.synchronize()
+        assert bool((whole[:20] == 3).all()) and bool((whole[120:] == 3).all())
+
+
+def test_prompt_past_32_bits():
+    # one sequence's keys span more than 4 GiB
+    gen = torch.Generator().manual_seed(29)
+    rows, stride, d = 700, 1 << 22, 64
+    big = torch.empty(rows * stride, dtype=torch.float16, device=DEV)
+    k, v = (big.as_strided((rows, 1, d), (stride, d, 1), o) for o in (0, 1 << 20))
+    hk, hv, q = (rand(gen, "fp16", n, 1, d) for n in (rows, rows, 40))
+    k.copy_(hk)
+    v.copy_(hv)
+    O, lse = g.attention_prompt(q.to(DEV), k, v, ints([0, 40]), ints([0, rows]), causal=True, return_lse=True)
+    torch.cuda.synchronize()
+    ref.prompt(q, hk, hv, [0, 40], [0, rows], True, 1 / 8, O.cpu(), lse.cpu(), "4 GiB cache")
+
+
+# ---------------------------------------------------------------------- shared prefix
+def shared_inputs(gen, dtype, B, P, N, H, Hk, d):
+    return (rand(gen, dtype, B, H, d), rand(gen, dtype, P, Hk, d), rand(gen, dtype, P, Hk, d), rand(gen, dtype, B, N, Hk, d),
+            rand(gen, dtype, B, N, Hk, d))
+
+
+def check_shared(q, kp, vp, ks, vs, lens, scale=None, dev=None, **kw):
+    say(f"[gpu] shared prefix q={tuple(q.shape)} kp={tuple(kp.shape)} ks={tuple(ks.shape)} {q.dtype} lens={lens[:9]}")
+    x = dev or [t.to(DEV) for t in (q, kp, vp, ks, vs)]
+    O, lse = g.attention_shared_prefix(*x, ints(lens), scale=scale, return_lse=True, **kw)
+    torch.cuda.synchronize()
+    s = 1 / math.sqrt(q.shape[2]) if scale is None else scale
+    ref.shared_prefix(q, kp, vp, ks, vs, lens, s, O.cpu(), lse.cpu(), f"shared prefix {q.dtype}")
+    return O.cpu(), lse.cpu()
+
+
+@pytest.mark.parametrize("dtype", sorted(TYPES))
+@pytest.mark.parametrize("heads,kv_heads,d", [(8, 2, 128), (3, 3, 64), (7, 1, 96), (40, 1, 128), (2, 2, 24), (150, 1, 64)])
+@pytest.mark.parametrize("B,P,N", [(1, 1, 1), (3, 64, 70), (5, 1000, 33), (2, 0, 40), (4, 130, 0), (2, 0, 0), (20, 65, 300), (1, 3001, 5)])
+def test_shared_prefix(B, P, N, heads, kv_heads, d, dtype):
+    gen = torch.Generator().manual_seed(B + P + N + d)
+    lens = [(N - 3 * b) % (N + 1) for b in range(B)]
+    check_shared(*shared_inputs(gen, dtype, B, P, N, heads, kv_heads, d), lens)
+
+
+def test_shared_prefix_slots():
+    # unused slots keep their rows, lengths past the slot count as all of it, stale rows hold NaN
+    gen = torch.Generator().manual_seed(31)
+    B, P, N, H, Hk, d = 7, 200, 90, 4, 2, 128
+    q, kp, vp, ks, vs = shared_inputs(gen, "bf16", B, P, N, H, Hk, d)
+    lens = [5, -1, 0, 90, 1000, -2 ** 31, 64]
+    for b, n in enumerate(lens):
+        ks[b, max(0, n):] = float("nan")
+        vs[b, max(0, n):] = float("inf")
+    O = torch.full((B, H, d), 5.0, dtype=torch.bfloat16, device=DEV)
+    lse = torch.full((B, H), 5.0, device=DEV)
+    got, got_lse = check_shared(q, kp, vp, ks, vs, lens, O=O, lse=lse)
+    for b in (1, 5):
+        assert bool((got[b] == 5).all()) and bool((got_lse[b] == 5).all())
+
+
+def test_shared_prefix_strides():
+    gen = torch.Generator().manual_seed(37)
+    B, P, N, H, Hk, d = 4, 129, 65, 8, 2, 64
+    q, kp, vp, ks, vs = shared_inputs(gen, "fp16", B, P, N, H, Hk, d)
+    lens = [65, 1, 0, 33]
+    a = check_shared(q, kp, vp, ks, vs, lens)
+    x = [t.to(DEV) for t in (q, kp, vp, ks, vs)]
+    x[1:3] = [t.transpose(0, 1).contiguous().transpose(0, 1) for t in x[1:3]]
+    x[3:5] = [t.transpose(1, 2).contiguous().transpose(1, 2) for t in x[3:5]]
+    b = check_shared(q, kp, vp, ks, vs, lens, dev=x)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+def test_shared_prefix_past_32_bits():
+    gen = torch.Generator().manual_seed(41)
+    rows, stride, d = 600, 1 << 22, 64
+    big = torch.empty(rows * stride, dtype=torch.float16, device=DEV)
+    kp, vp = (big.as_strided((rows, 1, d), (stride, d, 1), o) for o in (0, 1 << 20))
+    q, hk, hv, ks, vs = shared_inputs(gen, "fp16", 3, rows, 4, 2, 1, d)
+    kp.copy_(hk)
+    vp.copy_(hv)
+    check_shared(q, hk, hv, ks, vs, [4, 0, 2], dev=[q.to(DEV), kp, vp, ks.to(DEV), vs.to(DEV)])
+
+
+# ---------------------------------------------------------------------- together, streams, graphs
+@pytest.mark.parametrize("dtype", sorted(TYPES))
+def test_prefill_then_single_tokens(dtype):
+    """As they are used: a prompt read once, then every sequence's next tokens behind it.  Each single-token row is also
+    the last row of the whole sequence's prompt."""
+    gen = torch.Generator().manual_seed(43)
+    P, B, N, H, Hk, d = 333, 5, 6, 8, 2, 128
+    qkv = rand(gen, dtype, P, H + 2 * Hk, d)
+    own = rand(gen, dtype, B, N, H + 2 * Hk, d)
+    q, k, v = qkv[:, :H], qkv[:, H:H + Hk], qkv[:, H + Hk:]
+    check_prompt(q, k, v, [0, P], [0, P], True)
+    for n in range(1, N + 1):
+        lens = [n] * B
+        tok = own[:, n - 1, :H]
+        O, lse = check_shared(tok.contiguous(), k.contiguous(), v.contiguous(), own[:, :, H:H + Hk], own[:, :, H + Hk:], lens)
+        # the same rows through attention_prompt: one query against prefix and own keys
+        K = torch.cat([torch.cat([k, own[b, :n, H:H + Hk]]) for b in range(B)])
+        V = torch.cat([torch.cat([v, own[b, :n, H + Hk:]]) for b in range(B)])
+        check_prompt(tok.contiguous(), K, V, cu([1] * B), cu([P + n] * B), True)
+
+
+def _calls():
+    gen = torch.Generator().manual_seed(47)
+    c = cu([100, 40])
+    a = [rand(gen, "fp16", c[-1], h, 128).to(DEV) for h in (4, 2, 2)]
+    split = [rand(gen, "fp16", n, h, 128).to(DEV) for n, h in ((9, 4), (2000, 2), (2000, 2))]
+    s = [t.to(DEV) for t in shared_inputs(gen, "bf16", 6, 500, 40, 8, 2, 64)]
+    cua, cq, ck, lens = ints(c), ints([0, 9]), ints([0, 2000]), ints([40, 1, 0, 7, 40, 22])
+    return [lambda O=None: g.attention_prompt(*a, cua, O=O), lambda O=None: g.attention_prompt(*split, cq, ck, O=O),
+            lambda O=None: g.attention_shared_prefix(*s, lens, O=O)], [a, split, s]
+
+
+def test_repeats_and_side_stream():
+    calls, _ = _calls()
+    for f in calls:
+        want = f()
+        torch.cuda.synchronize()
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            got = [f() for _ in range(3)]
+        side.synchronize()
+        for x in got:
+            assert torch.equal(x, want)
+
+
+def test_captured_and_replayed():
+    """All calls in one graph, replayed with new inputs and eager calls between the replays."""
+    calls, inputs = _calls()
+    outs = [torch.empty_like(f()) for f in calls]
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for f, O in zip(calls, outs):
+            f(O)
+    for turn in range(4):
+        say(f"[gpu] replay {turn}")
+        for group in inputs:
+            for i, x in enumerate(group):
+                x.copy_(x.roll(1 + turn + i, 0))
+        want = [f() for f in calls]
+        torch.cuda.synchronize()
+        for O in outs:
+            O.fill_(float("nan"))
+        graph.replay()
+        extra = [f() for f in calls]   # eager calls behind the replay
+        torch.cuda.synchronize()
+        for a, b, e in zip(outs, want, extra):
+            assert torch.equal(a, b) and torch.equal(e, b)
+
+
+def test_given_workspace():
+    gen = torch.Generator().manual_seed(53)
+    q, k, v = (rand(gen, "fp16", n, h, 64).to(DEV) for n, h in ((3, 2), (3000, 1), (3000, 1)))
+    cq, ck = ints([0, 3]), ints([0, 3000])
+    need = g.attention_prompt_workspace(q, k, v, cq, ck)
+    assert need > 0
+    ws = torch.full((need + 64,), 0x7F, dtype=torch.uint8, device=DEV)
+    a = g.attention_prompt(q, k, v, cq, ck, workspace=ws[:need])
+    b = g.attention_prompt(q, k, v, cq, ck)
+    torch.cuda.synchronize()
+    assert torch.equal(a, b) and bool((ws[need:] == 0x7F).all())
+    with pytest.raises(g.GemmError):
+        g.attention_prompt(q, k, v, cq, ck, workspace=ws[:need - 16])
+
+
+def test_python_refusals():
+    q = torch.zeros(4, 2, 64, dtype=torch.float16, device=DEV)
+    k = torch.zeros(4, 1, 64, dtype=torch.float16, device=DEV)
+    c = ints([0, 4])
+    with pytest.raises(TypeError):
+        g.attention_prompt(q.float(), k.float(), k.float(), c)
+    with pytest.raises(TypeError):
+        g.attention_prompt(q, k.bfloat16(), k, c)
+    with pytest.raises(TypeError):
+        g.attention_prompt(q, k, k, c.long())
+    with pytest.raises(ValueError):
+        g.attention_prompt(q, k, k[:3], c)
+    with pytest.raises(ValueError):
+        g.attention_prompt(q, k, k.cpu(), c)
+    with pytest.raises(ValueError):
+        g.attention_prompt(q, torch.zeros(4, 3, 64, dtype=torch.float16, device=DEV), k, c)
+    with pytest.raises(ValueError):
+        g.attention_prompt(q.transpose(0, 2), k, k, c)
+    with pytest.raises(g.GemmError):
+        g.attention_prompt(q, k, k, c, O=q)                       # O overlaps Q
+    with pytest.raises(g.GemmError):
+        g.attention_prompt(q, k, k, c, scale=float("inf"))
+    with pytest.raises(g.GemmError):
+        x = torch.zeros(4, 2, 72, dtype=torch.float16, device=DEV)[:, :, 4:68]   # rows off 16-byte boundaries
+        g.attention_prompt(x, k, k, c)
+    with pytest.raises(ValueError):
+        g.attention_shared_prefix(q, k, k, torch.zeros(3, 2, 1, 64, dtype=torch.float16, device=DEV), k, ints([0] * 4))
