@@ -173,44 +173,90 @@ __device__ __forceinline__ void load_q(const Job& j, const Row& row, int half, u
     }
 }
 
-// A tile's loads into LDS, by all threads of the workgroup.  The buffer
-// resource starts at the tile's first row and ends with its last one inside
-// the sequence, so rows behind it (another sequence's, or stale ones) and the
-// elements behind the head size arrive as zeros whatever memory holds; the
-// base moves in 64 bits from tile to tile and offsets stay below 2^31.
+// 16 bytes a lane from a buffer to LDS, lane i's at dst + 16 i.  Written as
+// an instruction of its own, without registers that it could leave in
+// flight, because the compiler puts a wait for every outstanding
+// builtin load to LDS before each transposing read of LDS; the kernels wait
+// for their tiles themselves (vmcnt before the barrier that publishes one).
+__device__ __forceinline__ uint32_t lds_address(const char* p) { return (uint32_t)(uintptr_t)(const G16_LDS char*)p; }
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"  // M0 is written inside, on purpose
+__device__ __forceinline__ void load_to_lds(u32x4 rs, uint32_t dst, uint32_t off)
+{
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+                 :
+                 : "s"(dst), "v"(off), "s"(rs)
+                 : "memory", "m0");
+}
+#pragma clang diagnostic pop
+
+// A thread's part of a tile's loads into LDS: its place in the first
+// kThreads * 16 bytes of a tile, as a byte offset from the tile's first row.
+// Elements behind the head size lie past the end of every buffer.
 template <int D, bool IS_V>
-__device__ __forceinline__ void load_tile(const char* base, int64_t row_bytes, int keys, int tile, int d, char* lds,
-                                          int tid)
+__device__ __forceinline__ uint32_t tile_offset(int64_t row_bytes, int d, int tid)
+{
+    using S = Shape<D>;
+    const int r = tid / S::CHUNKS, pc = tid % S::CHUNKS;
+    const int lc = pc ^ (IS_V ? swz_v<D>(r) : swz_k<D>(r));   // both repeat every 16 rows
+    return lc * 8 < d ? (uint32_t)r * (uint32_t)row_bytes + (uint32_t)lc * 16u : 0x80000000u;
+}
+
+// A tile's loads, by all threads of the workgroup.  The buffer starts at the
+// tile's first row and ends with its last one inside the sequence, so rows
+// behind it (another sequence's, or stale ones) arrive as zeros whatever
+// memory holds; the base moves in 64 bits from tile to tile and offsets stay
+// below 2^31 (0x80000000 for what is past the head size).
+template <int D>
+__device__ __forceinline__ void load_tile(const char* base, int64_t row_bytes, int keys, int tile, int d, uint32_t off,
+                                          uint32_t dst)
 {
     using S = Shape<D>;
     const int key0 = tile * kTileKeys;
     const int n = keys - key0 < kTileKeys ? keys - key0 : kTileKeys;
     const uint32_t bytes = n > 0 ? (uint32_t)(n - 1) * (uint32_t)row_bytes + 2u * (uint32_t)d : 0u;
-    const __amdgpu_buffer_rsrc_t rs = make_rsrc(base + (int64_t)key0 * row_bytes, bytes);
-    const int r = tid / S::CHUNKS, pc = tid % S::CHUNKS;
-    const int lc = pc ^ (IS_V ? swz_v<D>(r) : swz_k<D>(r));   // both repeat every 16 rows
-    const uint32_t off = lc * 8 < d ? (uint32_t)r * (uint32_t)row_bytes + (uint32_t)lc * 16u : 0x80000000u;
-    char* dst = lds + __builtin_amdgcn_readfirstlane(tid >> 6) * 1024;
+    const uint64_t at = (uint64_t)(base + (int64_t)key0 * row_bytes);
+    const u32x4 rs = {(uint32_t)at, (uint32_t)(at >> 32) & 0xffffu, bytes, 0x00020000u};
 #pragma unroll
     for (int i = 0; i < S::LOADS; ++i)
-        buffer_load_lds_16(rs, dst + i * (kThreads * 16), off + (uint32_t)(i * S::LOAD_ROWS) * (uint32_t)row_bytes, 0);
+        load_to_lds(rs, dst + i * (kThreads * 16), off + (uint32_t)(i * S::LOAD_ROWS) * (uint32_t)row_bytes);
 }
 
-// S^T of one tile: s[b] holds keys 32 b .. of row l % 32.
-template <typename T, int D>
-__device__ __forceinline__ void scores(const char* kt, const u32x4 (&q)[Shape<D>::KSTEPS], int lane, f32x16 (&s)[2])
+// A lane's LDS addresses: of the fragments of a K tile's first 32 rows, and of
+// the transposing reads of a V tile's first rows.  The steps add constants.
+template <int D>
+struct Reads {
+    uint32_t k[Shape<D>::KSTEPS], v[Shape<D>::DBLOCKS];
+};
+
+template <int D>
+__device__ __forceinline__ Reads<D> reads_of(uint32_t lds, int lane)
 {
     using S = Shape<D>;
-    const int r = lane & 31, half = lane >> 5;
-    const int at = r * S::PITCH + ((half ^ swz_k<D>(r)) << 4);
+    Reads<D> x;
+    const int r = lane & 31, half = lane >> 5, i16 = lane & 15;
+    const int k = r * S::PITCH + ((half ^ swz_k<D>(r)) << 4);
+#pragma unroll
+    for (int i = 0; i < S::KSTEPS; ++i) x.k[i] = lds + (k ^ (i << 5));
+    const int chunk = (((lane >> 4) & 1) << 1) | ((i16 & 3) >> 1);
+    const int v = (4 * half + (i16 >> 2)) * S::PITCH + ((chunk ^ swz_v<D>(i16 >> 2)) << 4) + ((i16 & 1) << 3);
+#pragma unroll
+    for (int b = 0; b < S::DBLOCKS; ++b) x.v[b] = lds + (v ^ (b << 6));
+    return x;
+}
+
+// S^T of one tile, whose K rows are at byte `at` of LDS: s[b] holds keys 32 b ..
+// of row l % 32.
+template <typename T, int D>
+__device__ __forceinline__ void scores(const Reads<D>& x, uint32_t at, const u32x4 (&q)[Shape<D>::KSTEPS], f32x16 (&s)[2])
+{
+    using S = Shape<D>;
 #pragma unroll
     for (int b = 0; b < 2; ++b) {
         f32x16 acc = {};
 #pragma unroll
-        for (int i = 0; i < S::KSTEPS; ++i) {
-            const u32x4 k = *reinterpret_cast<const u32x4*>(kt + b * 32 * S::PITCH + (at ^ (i << 5)));
-            acc = T::mfma(k, q[i], acc);
-        }
+        for (int i = 0; i < S::KSTEPS; ++i)
+            acc = T::mfma(*reinterpret_cast<const G16_LDS u32x4*>(x.k[i] + at + b * 32 * S::PITCH), q[i], acc);
         s[b] = acc;
     }
 }
@@ -242,30 +288,37 @@ __device__ __forceinline__ void init(State<D>& st)
     for (int b = 0; b < Shape<D>::DBLOCKS; ++b) st.o[b] = f32x16{};
 }
 
-// Softmax weights of one tile: raises the row's maximum where it has to,
-// rescales what was summed so far, and leaves P^T as B operands p[kk] of the
-// keys 16 kk .. 16 kk + 15.
-template <typename T, int D>
-__device__ __forceinline__ void weights(f32x16 (&s)[2], float c, State<D>& st, u32x4 (&p)[4])
+// The maximum of a row's scores in a tile, in the units of m.
+__device__ __forceinline__ float top_score(const f32x16 (&s)[2], float c)
 {
     float mx = __builtin_fmaxf(s[0][0], s[1][0]);
 #pragma unroll
     for (int i = 1; i < 16; ++i) mx = max3(mx, s[0][i], s[1][i]);
-    mx = max_halves(mx) * c;
-    if (__builtin_amdgcn_ballot_w64(mx > st.m + kSlack) != 0) {
-        // each row goes by its own maximum alone, so a row's bits do not
-        // depend on the rows that share its wave
-        const float m = mx > st.m + kSlack ? mx : st.m;
-        const float a = m == st.m ? 1.f : exp2_(st.m - m);
-        st.m = m;
-        st.l *= a;
+    return max_halves(mx) * c;
+}
+
+// Raises a row's maximum where a tile's asks for it, and rescales what was
+// summed so far.  Each row goes by its own maximum alone, so a row's bits do
+// not depend on the rows that share its wave.
+template <int D>
+__device__ __forceinline__ void raise(float mx, State<D>& st)
+{
+    const float m = mx > st.m + kSlack ? mx : st.m;
+    const float a = m == st.m ? 1.f : exp2_(st.m - m);
+    st.m = m;
+    st.l *= a;
 #pragma unroll
-        for (int b = 0; b < Shape<D>::DBLOCKS; ++b)
+    for (int b = 0; b < Shape<D>::DBLOCKS; ++b)
 #pragma unroll
-            for (int i = 0; i < 16; ++i) st.o[b][i] *= a;
-    }
+        for (int i = 0; i < 16; ++i) st.o[b][i] *= a;
+}
+
+// Softmax weights of one tile: P^T as B operands p[kk] of the keys 16 kk ..
+// 16 kk + 15, and their sum.
+template <typename T, int D>
+__device__ __forceinline__ void weights(const f32x16 (&s)[2], float c, State<D>& st, u32x4 (&p)[4])
+{
     const float base = st.m == -__builtin_inff() ? 0.f : kShift - st.m;
-    float sum = 0.f;
 #pragma unroll
     for (int b = 0; b < 2; ++b)
 #pragma unroll
@@ -273,33 +326,26 @@ __device__ __forceinline__ void weights(f32x16 (&s)[2], float c, State<D>& st, u
             float e[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) e[i] = exp2_(__builtin_fmaf(s[b][8 * h + i], c, base));
-            sum += ((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7]));
-            u32x4 x;
+            st.l += ((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7]));
 #pragma unroll
-            for (int i = 0; i < 4; ++i) x[i] = T::pack(e[2 * i], e[2 * i + 1]);
-            p[2 * b + h] = x;
+            for (int i = 0; i < 4; ++i) p[2 * b + h][i] = T::pack(e[2 * i], e[2 * i + 1]);
         }
-    st.l += sum;
 }
 
-// O^T += V^T P^T over one tile.
+// O^T += V^T P^T over one tile, whose V rows are at byte `at` of LDS.
 template <typename T, int D>
-__device__ __forceinline__ void accumulate(const char* vt, const u32x4 (&p)[4], int lane, State<D>& st)
+__device__ __forceinline__ void accumulate(const Reads<D>& x, uint32_t at, const u32x4 (&p)[4], State<D>& st)
 {
     using S = Shape<D>;
-    const int half = lane >> 5, i16 = lane & 15;
-    const int key = 4 * half + (i16 >> 2);
-    const int chunk = (((lane >> 4) & 1) << 1) | ((i16 & 3) >> 1);
-    const int at = key * S::PITCH + ((chunk ^ swz_v<D>(i16 >> 2)) << 4) + ((i16 & 1) << 3);
 #pragma unroll
     for (int kk = 0; kk < 4; ++kk)
 #pragma unroll
         for (int b = 0; b < S::DBLOCKS; ++b) {
-            const char* a = vt + (at ^ (b << 6)) + kk * 16 * S::PITCH;
+            const uint32_t a = x.v[b] + at + kk * 16 * S::PITCH;
             const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((G16_LDS s16x4*)a);
             const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((G16_LDS s16x4*)(a + 8 * S::PITCH));
-            const u32x2 x = __builtin_bit_cast(u32x2, lo), y = __builtin_bit_cast(u32x2, hi);
-            st.o[b] = T::mfma(u32x4{x[0], x[1], y[0], y[1]}, p[kk], st.o[b]);
+            const u32x2 lo2 = __builtin_bit_cast(u32x2, lo), hi2 = __builtin_bit_cast(u32x2, hi);
+            st.o[b] = T::mfma(u32x4{lo2[0], lo2[1], hi2[0], hi2[1]}, p[kk], st.o[b]);
         }
 }
 
@@ -312,8 +358,7 @@ constexpr int lds_bytes()
 
 // All tiles of a job; the four waves share the K and V tiles.  Tile t + 1 of
 // K and t of V are in LDS when iteration t begins; K t + 2 and V t + 1 are
-// loaded while it runs, and the scores of t + 1 are computed beside the
-// softmax of t.
+// loaded while it runs.
 template <typename T, int D>
 __device__ __forceinline__ void run_tiles(const Job& j, const Row& row, char* smem, State<D>& st)
 {
@@ -324,39 +369,44 @@ __device__ __forceinline__ void run_tiles(const Job& j, const Row& row, char* sm
     init(st);
     if (j.tile0 >= j.tile1) return;
     const int first_limit = __builtin_amdgcn_readfirstlane(row.limit);   // the wave's smallest
-    auto kbuf = [&](int t) { return smem + ((t - j.tile0) & 1) * S::TILE; };
-    auto vbuf = [&](int t) { return smem + (2 + ((t - j.tile0) & 1)) * S::TILE; };
-    auto load_k = [&](int t) { load_tile<D, false>(j.k, j.k_row, j.keys, t, j.d, kbuf(t), tid); };
-    auto load_v = [&](int t) { load_tile<D, true>(j.v, j.v_row, j.keys, t, j.d, vbuf(t), tid); };
-    load_k(j.tile0);
-    load_v(j.tile0);
-    if (j.tile0 + 1 < j.tile1) load_k(j.tile0 + 1);
+    const uint32_t lds = lds_address(smem);
+    const Reads<D> x = reads_of<D>(lds, lane);
+    const uint32_t koff = tile_offset<D, false>(j.k_row, j.d, tid), voff = tile_offset<D, true>(j.v_row, j.d, tid);
+    const uint32_t dst = lds + __builtin_amdgcn_readfirstlane(tid >> 6) * 1024;
+    constexpr uint32_t K0 = 0, V0 = 2 * S::TILE;
+    auto load_k = [&](int t, uint32_t par) { load_tile<D>(j.k, j.k_row, j.keys, t, j.d, koff, dst + K0 + par * S::TILE); };
+    auto load_v = [&](int t, uint32_t par) { load_tile<D>(j.v, j.v_row, j.keys, t, j.d, voff, dst + V0 + par * S::TILE); };
+    load_k(j.tile0, 0);
+    load_v(j.tile0, 0);
+    if (j.tile0 + 1 < j.tile1) load_k(j.tile0 + 1, 1);
     wait_vmcnt<0>();
     wg_barrier();
     f32x16 cur[2], next[2];
-    scores<T, D>(kbuf(j.tile0), q, lane, cur);
-    auto step = [&](int t, f32x16 (&a)[2], f32x16 (&b)[2]) {
+    scores<T, D>(x, K0, q, cur);
+    auto step = [&](int t, uint32_t par, f32x16 (&a)[2], f32x16 (&b)[2]) {
         // this wave's reads of K t and V t - 1 are done and its loads of
         // K t + 1 and V t have landed; behind the barrier that holds for all
         wait_lgkmcnt0();
         wait_vmcnt<0>();
         wg_barrier();
-        if (t + 2 < j.tile1) load_k(t + 2);
+        if (t + 2 < j.tile1) load_k(t + 2, par);
         if (t + 1 < j.tile1) {
-            load_v(t + 1);
-            scores<T, D>(kbuf(t + 1), q, lane, b);
+            load_v(t + 1, 1 - par);
+            scores<T, D>(x, K0 + (1 - par) * S::TILE, q, b);
         }
         if ((t + 1) * kTileKeys > first_limit) mask(a, row.limit, t * kTileKeys, half);
+        const float mx = top_score(a, j.c);
+        if (__builtin_amdgcn_ballot_w64(mx > st.m + kSlack) != 0) raise<D>(mx, st);
         u32x4 p[4];
         weights<T, D>(a, j.c, st, p);
-        accumulate<T, D>(vbuf(t), p, lane, st);
+        accumulate<T, D>(x, V0 + par * S::TILE, p, st);
     };
     int t = j.tile0;
     for (; t + 1 < j.tile1; t += 2) {
-        step(t, cur, next);
-        step(t + 1, next, cur);
+        step(t, 0, cur, next);
+        step(t + 1, 1, next, cur);
     }
-    if (t < j.tile1) step(t, cur, next);
+    if (t < j.tile1) step(t, 0, cur, next);
 }
 
 // Partial results of a split job: for row x (of n) and part s, m and l at
