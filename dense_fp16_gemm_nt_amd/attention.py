@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import ctypes
 import math
+import struct
 
 F16 = 0
 BF16 = 1
@@ -33,53 +34,69 @@ class SharedPrefixDesc(ctypes.Structure):
                 + [("scale", ctypes.c_float)])
 
 
+def _packer(desc):
+    """The descriptor's layout as a struct.Struct: packing its fields into bytes takes a fifth of the time of building
+    the ctypes.Structure, which is most of what a small call costs on the host."""
+    codes = {ctypes.c_int32: "i", ctypes.c_int64: "q", ctypes.c_void_p: "P", ctypes.c_float: "f"}
+    return struct.Struct("@" + "".join(codes[t] for _, t in desc._fields_)).pack
+
+
+_pack_prompt, _pack_shared_prefix = _packer(PromptDesc), _packer(SharedPrefixDesc)
+
+
 def declare(L: ctypes.CDLL) -> None:
-    """Argument types of the attention entry points of the library."""
+    """Argument types of the attention entry points of the library; descriptors are passed as their bytes or by reference."""
     i64, vp, i32 = ctypes.c_int64, ctypes.c_void_p, ctypes.c_int
-    for name, desc in (("attn_prompt", PromptDesc), ("attn_shared_prefix", SharedPrefixDesc)):
-        p = ctypes.POINTER(desc)
+    for name in ("attn_prompt", "attn_shared_prefix"):
         f = getattr(L, name)
-        f.restype, f.argtypes = i32, [p, vp, i64, vp]
+        f.restype, f.argtypes = i32, [vp, vp, i64, vp]
         f = getattr(L, name + "_workspace")
-        f.restype, f.argtypes = i64, [p]
+        f.restype, f.argtypes = i64, [vp]
         f = getattr(L, name + "_check")
-        f.restype, f.argtypes = i32, [p]
+        f.restype, f.argtypes = i32, [vp]
 
 
-def _dtype(Q):
+def _query(Q):
+    """Type code, device and shape of Q."""
     import torch
 
-    if Q.dtype == torch.float16:
-        return F16
-    if Q.dtype == torch.bfloat16:
-        return BF16
-    raise TypeError(f"attention takes torch.float16 or torch.bfloat16, not {Q.dtype}")
+    dtype = Q.dtype
+    if dtype == torch.float16:
+        code = F16
+    elif dtype == torch.bfloat16:
+        code = BF16
+    else:
+        raise TypeError(f"attention takes torch.float16 or torch.bfloat16, not {dtype}")
+    if not Q.is_cuda:
+        raise ValueError("Q must be a device tensor")
+    if Q.dim() != 3:
+        raise ValueError(f"Q must have 3 dimensions; got {tuple(Q.shape)}")
+    return code, Q.device
 
 
-def _like(Q, name, X, dim):
-    """X is a device tensor of Q's type and device with `dim` dimensions, the last contiguous."""
-    if X.dtype != Q.dtype:
-        raise TypeError(f"{name} must be {Q.dtype} like Q, not {X.dtype}")
-    if X.device != Q.device:
-        raise ValueError(f"{name} is on {X.device}, Q on {Q.device}")
-    if X.dim() != dim:
-        raise ValueError(f"{name} must have {dim} dimensions; got {tuple(X.shape)}")
-    if X.stride(-1) != 1 and X.shape[-1] > 1:
+def _strides(name, X, shape, dtype, device):
+    """Strides of the dimensions before the last of a tensor that has to have this shape and type, the last contiguous;
+    0 where a dimension has one entry and its stride says nothing."""
+    if X.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype} like Q, not {X.dtype}")
+    if X.device != device:
+        raise ValueError(f"{name} is on {X.device}, Q on {device}")
+    if X.shape != shape:
+        raise ValueError(f"{name} must be {tuple(shape)}; got {tuple(X.shape)}")
+    st = X.stride()
+    if st[-1] != 1 and shape[-1] > 1:
         raise ValueError(f"{name}: last dimension must be contiguous")
+    return [s if n > 1 else 0 for n, s in zip(shape[:-1], st)]
 
 
-def _ints(Q, name, X, n):
+def _ints(name, X, n, device):
     import torch
 
     if X.dtype != torch.int32:
         raise TypeError(f"{name} must be torch.int32")
-    if X.device != Q.device or X.dim() != 1 or (n is not None and X.numel() != n) or not X.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous tensor{'' if n is None else f' of {n} values'} on {Q.device}")
-
-
-def _strides(X):
-    """Strides of the dimensions before the last; 0 where a dimension has one entry and its stride says nothing."""
-    return [s if n > 1 else 0 for n, s in zip(X.shape[:-1], X.stride()[:-1])]
+    if X.device != device or X.dim() != 1 or X.numel() != n or not X.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous tensor of {n} values on {device}")
+    return X.data_ptr()
 
 
 def _heads(H, Hk):
@@ -88,18 +105,18 @@ def _heads(H, Hk):
 
 
 def _scale(scale, d):
-    return 1.0 / math.sqrt(d) if scale is None else float(scale)
+    if scale is None:
+        return 1.0 / math.sqrt(d)
+    scale = float(scale)
+    return scale if abs(scale) < 3.4e38 else math.inf   # what fp32 does not hold is refused by the library
 
 
 def _outputs(Q, O, lse, return_lse):
+    """(O, lse), allocated where they are not given; lse may be None."""
     import torch
 
     if O is None:
-        O = torch.empty(Q.shape, dtype=Q.dtype, device=Q.device)
-    else:
-        _like(Q, "O", O, 3)
-        if O.shape != Q.shape:
-            raise ValueError(f"O must be {tuple(Q.shape)}; got {tuple(O.shape)}")
+        O = torch.empty_like(Q, memory_format=torch.contiguous_format)
     if lse is None:
         if return_lse:
             lse = torch.empty(Q.shape[:2], dtype=torch.float32, device=Q.device)
@@ -108,64 +125,64 @@ def _outputs(Q, O, lse, return_lse):
     return O, lse
 
 
-def _call(name, desc, Q, workspace):
-    """Runs an entry point on Q's device and current stream, with a workspace if it needs one."""
+def _call(name, desc, device, workspace):
+    """Runs an entry point on a device's current stream, with a workspace if it needs one."""
     import torch
 
     from . import OK, GemmError, lib
 
+    if device.index != torch.cuda.current_device():   # launches go to the current device
+        with torch.cuda.device(device):
+            return _call(name, desc, device, workspace)
     L = lib()
-    ref = ctypes.byref(desc)
-    dev = Q.device
-    if dev.index != torch.cuda.current_device():
-        with torch.cuda.device(dev):
-            return _call(name, desc, Q, workspace)
-    need = getattr(L, name + "_workspace")(ref)
-    if need < 0:
-        raise GemmError(int(need), name)
+    ws, have = None, 0
     if workspace is None:
+        need = getattr(L, name + "_workspace")(desc)
+        if need < 0:
+            raise GemmError(int(need), name)
         if need:
-            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-    elif workspace.device != dev or not workspace.is_contiguous():
-        raise ValueError(f"workspace must be a contiguous tensor on {dev}")
-    ws, have = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel() * workspace.element_size())
-    st = getattr(L, name)(ref, ws, have, torch.cuda.current_stream(dev).cuda_stream)
+            workspace = torch.empty(need, dtype=torch.uint8, device=device)
+    elif workspace.device != device or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on {device}")
+    if workspace is not None:
+        ws, have = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    st = getattr(L, name)(desc, ws, have, torch._C._cuda_getCurrentRawStream(device.index))
     if st != OK:
         raise GemmError(st, name)
 
 
-def _workspace_bytes(name, desc, Q):
+def _workspace_bytes(name, desc, device):
     import torch
 
     from . import GemmError, lib
 
-    with torch.cuda.device(Q.device):
-        n = getattr(lib(), name + "_workspace")(ctypes.byref(desc))
+    with torch.cuda.device(device):
+        n = getattr(lib(), name + "_workspace")(desc)
     if n < 0:
         raise GemmError(int(n), name + "_workspace")
     return int(n)
 
 
 def _prompt_desc(Q, K, V, cu_q, cu_k, causal, scale, O, lse):
-    dtype = _dtype(Q)
-    if not Q.is_cuda:
-        raise ValueError("Q must be a device tensor")
-    _like(Q, "Q", Q, 3)
-    _like(Q, "K", K, 3)
-    _like(Q, "V", V, 3)
-    Tq, H, d = Q.shape
-    Tk, Hk, dk = K.shape
-    if dk != d or V.shape != K.shape:
-        raise ValueError(f"Q, K and V do not match: {tuple(Q.shape)}, {tuple(K.shape)}, {tuple(V.shape)}")
+    """Descriptor bytes and device; without O the strides of a contiguous one, at an address that no tensor has."""
+    code, device = _query(Q)
+    dtype, shape = Q.dtype, Q.shape
+    Tq, H, d = shape
+    if K.dim() != 3:
+        raise ValueError(f"K must have 3 dimensions; got {tuple(K.shape)}")
+    kv = K.shape
+    Tk, Hk, dk = kv
+    if dk != d:
+        raise ValueError(f"Q and K do not match: {tuple(shape)}, {tuple(kv)}")
     _heads(H, Hk)
-    _ints(Q, "cu_q", cu_q, None)
-    if cu_q.numel() < 1:
+    n = cu_q.numel()
+    if n < 1:
         raise ValueError("cu_q needs a value more than there are sequences")
-    _ints(Q, "cu_k", cu_k, cu_q.numel())
-    qs, ks, vs, os = _strides(Q), _strides(K), _strides(V), _strides(O)
-    return PromptDesc(dtype, int(bool(causal)), H, Hk, d, cu_q.numel() - 1, Tq, Tk, Q.data_ptr(), K.data_ptr(), V.data_ptr(),
-                      O.data_ptr(), None if lse is None else lse.data_ptr(), cu_q.data_ptr(), cu_k.data_ptr(),
-                      qs[0], qs[1], ks[0], ks[1], vs[0], vs[1], os[0], os[1], _scale(scale, d))
+    cq, ck = _ints("cu_q", cu_q, n, device), _ints("cu_k", cu_k, n, device)
+    qs, ks, vs = _strides("Q", Q, shape, dtype, device), _strides("K", K, kv, dtype, device), _strides("V", V, kv, dtype, device)
+    os, o = ((H * d, d), 16) if O is None else (_strides("O", O, shape, dtype, device), O.data_ptr())
+    return _pack_prompt(code, 1 if causal else 0, H, Hk, d, n - 1, Tq, Tk, Q.data_ptr(), K.data_ptr(), V.data_ptr(), o,
+                        0 if lse is None else lse.data_ptr(), cq, ck, *qs, *ks, *vs, *os, _scale(scale, d)), device
 
 
 def attention_prompt(Q, K, V, cu_q, cu_k=None, *, causal=True, scale=None, O=None, lse=None, return_lse=False, workspace=None):
@@ -186,37 +203,35 @@ def attention_prompt(Q, K, V, cu_q, cu_k=None, *, causal=True, scale=None, O=Non
     attention_prompt_workspace(...) bytes, 16-byte aligned; allocated here
     when not given."""
     O, lse = _outputs(Q, O, lse, return_lse)
-    desc = _prompt_desc(Q, K, V, cu_q, cu_q if cu_k is None else cu_k, causal, scale, O, lse)
-    _call("attn_prompt", desc, Q, workspace)
+    desc, device = _prompt_desc(Q, K, V, cu_q, cu_q if cu_k is None else cu_k, causal, scale, O, lse)
+    _call("attn_prompt", desc, device, workspace)
     return (O, lse) if return_lse else O
 
 
 def attention_prompt_workspace(Q, K, V, cu_q, cu_k=None) -> int:
     """Bytes of workspace attention_prompt needs for tensors of these shapes (0: none)."""
-    desc = _prompt_desc(Q, K, V, cu_q, cu_q if cu_k is None else cu_k, True, None, Q, None)
-    desc.O, desc.o_row, desc.o_head = 16, desc.heads * desc.head_dim, desc.head_dim   # no output is looked at
-    return _workspace_bytes("attn_prompt", desc, Q)
+    return _workspace_bytes("attn_prompt", *_prompt_desc(Q, K, V, cu_q, cu_q if cu_k is None else cu_k, True, None, None, None))
 
 
 def _shared_desc(Q, Kp, Vp, Ks, Vs, lens, scale, O, lse):
-    dtype = _dtype(Q)
-    if not Q.is_cuda:
-        raise ValueError("Q must be a device tensor")
-    _like(Q, "Q", Q, 3)
-    for name, X, dim in (("Kp", Kp, 3), ("Vp", Vp, 3), ("Ks", Ks, 4), ("Vs", Vs, 4)):
-        _like(Q, name, X, dim)
-    B, H, d = Q.shape
-    P, Hk, dk = Kp.shape
-    N = Ks.shape[1]
-    if dk != d or Vp.shape != Kp.shape or tuple(Ks.shape) != (B, N, Hk, d) or Vs.shape != Ks.shape:
-        raise ValueError(f"Q, Kp, Vp, Ks and Vs do not match: {[tuple(X.shape) for X in (Q, Kp, Vp, Ks, Vs)]}")
+    code, device = _query(Q)
+    dtype, shape = Q.dtype, Q.shape
+    B, H, d = shape
+    if Kp.dim() != 3 or Ks.dim() != 4:
+        raise ValueError(f"Kp must have 3 and Ks 4 dimensions; got {tuple(Kp.shape)} and {tuple(Ks.shape)}")
+    kv, own = Kp.shape, Ks.shape
+    P, Hk, dk = kv
+    N = own[1]
+    if dk != d or own != (B, N, Hk, d):
+        raise ValueError(f"Q, Kp and Ks do not match: {tuple(shape)}, {tuple(kv)}, {tuple(own)}")
     _heads(H, Hk)
-    _ints(Q, "lens", lens, B)
-    q, kp, vp, ks, vs, o = (_strides(X) for X in (Q, Kp, Vp, Ks, Vs, O))
-    return SharedPrefixDesc(dtype, H, Hk, d, B, P, N, Q.data_ptr(), Kp.data_ptr(), Vp.data_ptr(), Ks.data_ptr(),
-                            Vs.data_ptr(), O.data_ptr(), None if lse is None else lse.data_ptr(), lens.data_ptr(),
-                            q[0], q[1], kp[0], kp[1], vp[0], vp[1], ks[0], ks[1], ks[2], vs[0], vs[1], vs[2], o[0], o[1],
-                            _scale(scale, d))
+    ln = _ints("lens", lens, B, device)
+    q, kp, vp = _strides("Q", Q, shape, dtype, device), _strides("Kp", Kp, kv, dtype, device), _strides("Vp", Vp, kv, dtype, device)
+    ks, vs = _strides("Ks", Ks, own, dtype, device), _strides("Vs", Vs, own, dtype, device)
+    os, o = ((H * d, d), 16) if O is None else (_strides("O", O, shape, dtype, device), O.data_ptr())
+    return _pack_shared_prefix(code, H, Hk, d, B, P, N, Q.data_ptr(), Kp.data_ptr(), Vp.data_ptr(), Ks.data_ptr(),
+                               Vs.data_ptr(), o, 0 if lse is None else lse.data_ptr(), ln, *q, *kp, *vp, *ks, *vs, *os,
+                               _scale(scale, d)), device
 
 
 def attention_shared_prefix(Q, Kp, Vp, Ks, Vs, lens, *, scale=None, O=None, lse=None, return_lse=False, workspace=None):
@@ -234,13 +249,11 @@ def attention_shared_prefix(Q, Kp, Vp, Ks, Vs, lens, *, scale=None, O=None, lse=
     attention_prompt does, with the same `scale`, `O`, `lse` and `workspace`
     (attention_shared_prefix_workspace(...) bytes)."""
     O, lse = _outputs(Q, O, lse, return_lse)
-    desc = _shared_desc(Q, Kp, Vp, Ks, Vs, lens, scale, O, lse)
-    _call("attn_shared_prefix", desc, Q, workspace)
+    desc, device = _shared_desc(Q, Kp, Vp, Ks, Vs, lens, scale, O, lse)
+    _call("attn_shared_prefix", desc, device, workspace)
     return (O, lse) if return_lse else O
 
 
 def attention_shared_prefix_workspace(Q, Kp, Vp, Ks, Vs, lens) -> int:
     """Bytes of workspace attention_shared_prefix needs for tensors of these shapes (0: none)."""
-    desc = _shared_desc(Q, Kp, Vp, Ks, Vs, lens, None, Q, None)
-    desc.O, desc.o_row, desc.o_head = 16, desc.heads * desc.head_dim, desc.head_dim   # no output is looked at
-    return _workspace_bytes("attn_shared_prefix", desc, Q)
+    return _workspace_bytes("attn_shared_prefix", *_shared_desc(Q, Kp, Vp, Ks, Vs, lens, None, None, None))

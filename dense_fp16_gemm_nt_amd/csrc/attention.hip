@@ -14,6 +14,9 @@
 
 #include "attn_core.hpp"
 #include "sched.hpp"
+#ifndef NOFEW
+#define NOFEW 0
+#endif
 
 using namespace g16;
 
@@ -21,10 +24,12 @@ namespace {
 
 using attn::BF16;
 using attn::F16;
+using attn::f32x2;
 using attn::Job;
 using attn::kThreads;
 using attn::kTileKeys;
 using attn::kTileRows;
+using attn::Keys;
 using attn::Parts;
 using attn::Row;
 using attn::State;
@@ -121,21 +126,24 @@ __device__ __forceinline__ Job prompt_job(const PromptArgs& g, const Tile& t, in
     j.c = g.c;
     j.flip = g.flip;
     j.zero_q = g.zero_q != 0;
-    // keys that the tile's last row may read
     int most = t.nk;
     if (g.causal) {
         const int last = (t.row0 + kTileRows < j.rows ? t.row0 + kTileRows : j.rows) - 1;
         const int lim = last / g.group + j.lead + 1;
         most = lim < 0 ? 0 : lim < t.nk ? lim : t.nk;
     }
+    j.most = most;
     const int n = (most + kTileKeys - 1) / kTileKeys;
     j.tile0 = (int)((int64_t)n * split / g.splits);
     j.tile1 = (int)((int64_t)n * (split + 1) / g.splits);
     return j;
 }
 
+#ifndef W64
+#define W64 2
+#endif
 template <typename T, int D, bool SPLIT>
-__global__ __launch_bounds__(kThreads, 2) void prompt_kernel(const PromptArgs g)
+__global__ __launch_bounds__(kThreads, D == 64 ? W64 : 2) void prompt_kernel(const PromptArgs g)
 {
     __shared__ __attribute__((aligned(256))) char smem[attn::lds_bytes<D>()];
     // a unit is a kv head and a split; consecutive workgroups go to the XCDs
@@ -157,8 +165,29 @@ __global__ __launch_bounds__(kThreads, 2) void prompt_kernel(const PromptArgs g)
     const Job j = prompt_job(g, tile, kv, split);
     const int lane = threadIdx.x & 63, half = lane >> 5;
     const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const Row row = attn::row_of(j, j.row0 + w * attn::kWaveRows + (lane & 31));
     State<D> st;
+    const int rows = j.rows - j.row0;
+    if (!NOFEW && rows <= attn::kWaveRows) {
+        // the rows of one wave (a single token, a short chunk): all waves
+        // take them and divide the keys
+        const Row row = attn::row_of(j, j.row0 + (lane & 31));
+        const Keys keys = {j.k, j.v, j.k_row, j.v_row, j.keys}, none = {};
+        const int n = attn::key_blocks(j.most);
+        attn::run_blocks<T, D>(j, keys, none, (int)((int64_t)n * split / g.splits), (int)((int64_t)n * (split + 1) / g.splits),
+                               row, smem, st);
+        attn::merge_waves<D>(st, row.valid, rows, g.d, smem, [&](int r, int e, float m, float l, f32x4 o) {
+            const int x = j.row0 + r;
+            const int64_t token = (int64_t)tile.q0 + x / g.group;
+            const int head = kv * g.group + x % g.group;
+            if constexpr (SPLIT)
+                attn::store_part4(g.parts, split, token * g.heads + head, g.d, e, m, l, o);
+            else
+                attn::store_row4<T>(g.o + token * g.o_row + head * g.o_head,
+                                    g.lse == nullptr ? nullptr : g.lse + token * g.heads + head, e, m, l, o);
+        });
+        return;
+    }
+    const Row row = attn::row_of(j, j.row0 + w * attn::kWaveRows + (lane & 31));
     attn::run_tiles<T, D>(j, row, smem, st);
     if (!row.valid) return;
     const int64_t token = (int64_t)tile.q0 + row.token;
@@ -170,23 +199,25 @@ __global__ __launch_bounds__(kThreads, 2) void prompt_kernel(const PromptArgs g)
                               g.lse == nullptr ? nullptr : g.lse + token * g.heads + head, half);
 }
 
-// Joins the splits: 8 rows for a workgroup, 32 lanes of 4 elements for a row.
-constexpr int kJoinRows = kThreads / 32;
+// Joins the splits: 32 lanes of 4 elements and GROUPS groups of parts for a row.
+template <int GROUPS>
+constexpr int kJoinRows = kThreads / 32 / GROUPS;
 
-template <typename T>
+template <typename T, int GROUPS>
 __global__ __launch_bounds__(kThreads) void prompt_join_kernel(const PromptArgs g)
 {
-    constexpr uint32_t kSub = kTileRows / kJoinRows;
+    constexpr uint32_t kSub = kTileRows / kJoinRows<GROUPS>;
     const uint32_t sub = blockIdx.x % kSub, x = blockIdx.x / kSub;
     const int kv = (int)(x % (uint32_t)g.kv_heads);
     const Tile tile = find_tile(g, (int)(x / (uint32_t)g.kv_heads));
     if (!tile.found) return;
-    const int r = tile.row0 + (int)sub * kJoinRows + (int)(threadIdx.x >> 5), e = (threadIdx.x & 31) * 4;
-    if (r >= tile.nq * g.group || e >= g.d) return;
+    const int r = tile.row0 + (int)sub * kJoinRows<GROUPS> + (int)(threadIdx.x >> 5) / GROUPS, e = (threadIdx.x & 31) * 4;
+    const bool there = r < tile.nq * g.group && e < g.d;
     const int64_t token = (int64_t)tile.q0 + r / g.group;
     const int head = kv * g.group + r % g.group;
-    attn::join_row<T>(g.parts, g.splits, token * g.heads + head, g.d, e, g.o + token * g.o_row + head * g.o_head,
-                      g.lse == nullptr ? nullptr : g.lse + token * g.heads + head);
+    attn::join_row<T, GROUPS>(g.parts, g.splits, there, token * g.heads + head, g.d, e,
+                              g.o + token * g.o_row + head * g.o_head,
+                              g.lse == nullptr ? nullptr : g.lse + token * g.heads + head);
 }
 
 // --------------------------------------------------------- shared prefix
@@ -202,10 +233,13 @@ struct SharedArgs {
     int64_t q_row, q_head, kp_row, kp_head, vp_row, vp_head;   // bytes
     int64_t ks_slot, ks_row, ks_head, vs_slot, vs_row, vs_head, o_row, o_head;
     int batch, prefix, slot_rows, heads, kv_heads, group, d;
-    int row_tiles;                     // of the prefix: batch * group rows
-    int own_tiles;                     // of a slot: group rows
-    int prefix_splits, own_splits;     // parts of each row: the prefix's, then its own keys'
-    uint32_t prefix_blocks;
+    int together;         // each slot's rows take prefix and own keys as one run (splits: prefix_splits)
+    int row_tiles;        // of the prefix: batch * group rows in tiles of 128, or of 32 where that is all
+    int own_tiles;        // of a slot: group rows in tiles of 32
+    int prefix_splits;    // parts of a row that come from the prefix ...
+    int own_splits;       // ... and from its own keys,
+    int own_blocks;       // this many blocks of 32 keys each
+    uint32_t prefix_wgs, own_wgs, round_prefix, round_own;
     float c;
     uint32_t flip;
     int zero_q;
@@ -218,6 +252,16 @@ __global__ __launch_bounds__(kThreads, 2) void shared_kernel(const SharedArgs g)
     __shared__ __attribute__((aligned(256))) char smem[attn::lds_bytes<D>()];
     const int lane = threadIdx.x & 63, half = lane >> 5;
     const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    // Workgroups on the prefix (matrix products) and on the slots' own keys
+    // (bytes from HBM) come in rounds: one on the prefix for each compute
+    // unit, then a share of the others, so that a compute unit works on both
+    // at once.
+    uint32_t i = blockIdx.x;
+    const uint32_t round = i / (g.round_prefix + g.round_own);
+    i -= round * (g.round_prefix + g.round_own);
+    const bool own = i >= g.round_prefix;
+    i = own ? i - g.round_prefix + round * g.round_own : i + round * g.round_prefix;
+    if (i >= (own ? g.own_wgs : g.prefix_wgs)) return;
     Job j;
     j.q_token = g.q_row;
     j.q_head = g.q_head;
@@ -227,62 +271,101 @@ __global__ __launch_bounds__(kThreads, 2) void shared_kernel(const SharedArgs g)
     j.c = g.c;
     j.flip = g.flip;
     j.zero_q = g.zero_q != 0;
-    int kv, part, slot0;
-    if (blockIdx.x < g.prefix_blocks) {
-        const uint32_t units = (uint32_t)g.kv_heads * (uint32_t)g.prefix_splits;
-        const uint32_t unit = blockIdx.x % units;
-        kv = (int)(unit / (uint32_t)g.prefix_splits);
-        part = (int)(unit % (uint32_t)g.prefix_splits);
-        slot0 = 0;
+    State<D> st;
+    if (!own) {
+        const uint32_t units = (uint32_t)g.kv_heads * (uint32_t)g.prefix_splits, tiles = (uint32_t)g.row_tiles;
+        uint32_t unit, t;
+        if (units % kNumXcd == 0) {   // the row tiles of a unit one after the other on one XCD: its L2 holds their keys
+            unit = i / kNumXcd / tiles * kNumXcd + i % kNumXcd;
+            t = i / kNumXcd % tiles;
+        } else {
+            unit = i / tiles;
+            t = i % tiles;
+        }
+        const int kv = (int)(unit / (uint32_t)g.prefix_splits), part = (int)(unit % (uint32_t)g.prefix_splits);
+        j.q = g.q + (int64_t)kv * g.group * g.q_head;
         j.k = g.kp + kv * g.kp_head;
         j.v = g.vp + kv * g.vp_head;
         j.k_row = g.kp_row;
         j.v_row = g.vp_row;
         j.rows = g.batch * g.group;
-        j.row0 = (int)(blockIdx.x / units) * kTileRows;
+        j.row0 = (int)t * kTileRows;
         j.keys = g.prefix;
-        const int n = (g.prefix + kTileKeys - 1) / kTileKeys;
+        if (j.rows <= attn::kWaveRows) {
+            const Row row = attn::row_of(j, lane & 31);
+            const Keys keys = {j.k, j.v, j.k_row, j.v_row, j.keys}, none = {};
+            const int n = attn::key_blocks(g.prefix);
+            attn::run_blocks<T, D>(j, keys, none, (int)((int64_t)n * part / g.prefix_splits),
+                                   (int)((int64_t)n * (part + 1) / g.prefix_splits), row, smem, st);
+            attn::merge_waves<D>(st, row.valid, j.rows, g.d, smem, [&](int r, int e, float m, float l, f32x4 o) {
+                const int64_t x = (int64_t)(r / g.group) * g.heads + kv * g.group + r % g.group;
+                attn::store_part4(g.parts, part, x, g.d, e, m, l, o);
+            });
+            return;
+        }
+        const int n = (int)(((int64_t)g.prefix + kTileKeys - 1) / kTileKeys);
         j.tile0 = (int)((int64_t)n * part / g.prefix_splits);
         j.tile1 = (int)((int64_t)n * (part + 1) / g.prefix_splits);
-    } else {
-        uint32_t x = blockIdx.x - g.prefix_blocks;
-        kv = (int)(x % (uint32_t)g.kv_heads);
-        x /= (uint32_t)g.kv_heads;
-        const int split = (int)(x % (uint32_t)g.own_splits);
-        x /= (uint32_t)g.own_splits;
-        j.row0 = (int)(x % (uint32_t)g.own_tiles) * kTileRows;
-        slot0 = (int)(x / (uint32_t)g.own_tiles);
-        part = g.prefix_splits + split;
-        const int len = g.lens[slot0];
-        if (len < 0) return;
-        j.k = g.ks + (int64_t)slot0 * g.ks_slot + kv * g.ks_head;
-        j.v = g.vs + (int64_t)slot0 * g.vs_slot + kv * g.vs_head;
-        j.k_row = g.ks_row;
-        j.v_row = g.vs_row;
-        j.rows = g.group;
-        j.keys = len < g.slot_rows ? len : g.slot_rows;
-        const int n = (j.keys + kTileKeys - 1) / kTileKeys;
-        j.tile0 = (int)((int64_t)n * split / g.own_splits);
-        j.tile1 = (int)((int64_t)n * (split + 1) / g.own_splits);
+        const Row row = attn::row_of(j, j.row0 + w * attn::kWaveRows + (lane & 31));
+        attn::run_tiles<T, D>(j, row, smem, st);
+        if (row.valid) attn::store_part<D>(st, g.d, g.parts, part, (int64_t)row.token * g.heads + kv * g.group + row.head, half);
+        return;
     }
-    j.q = g.q + (int64_t)slot0 * g.q_row + (int64_t)kv * g.group * g.q_head;
-    const Row row = attn::row_of(j, j.row0 + w * attn::kWaveRows + (lane & 31));
-    State<D> st;
-    attn::run_tiles<T, D>(j, row, smem, st);
-    if (!row.valid) return;
-    attn::store_part<D>(st, g.d, g.parts, part, (int64_t)(slot0 + row.token) * g.heads + kv * g.group + row.head, half);
+    const int kv = (int)(i % (uint32_t)g.kv_heads);
+    i /= (uint32_t)g.kv_heads;
+    const uint32_t splits = (uint32_t)(g.together ? g.prefix_splits : g.own_splits);
+    const int split = (int)(i % splits);
+    i /= splits;
+    j.row0 = (int)(i % (uint32_t)g.own_tiles) * attn::kWaveRows;
+    const int64_t slot = i / (uint32_t)g.own_tiles;
+    const int len = g.lens[slot];
+    if (len < 0) return;
+    const Keys mine = {g.ks + slot * g.ks_slot + kv * g.ks_head, g.vs + slot * g.vs_slot + kv * g.vs_head, g.ks_row, g.vs_row,
+                       len < g.slot_rows ? len : g.slot_rows};
+    const Keys before = {g.kp + kv * g.kp_head, g.vp + kv * g.vp_head, g.kp_row, g.vp_row, g.together ? g.prefix : 0};
+    j.q = g.q + slot * g.q_row + (int64_t)kv * g.group * g.q_head;
+    j.rows = g.group;
+    j.keys = INT32_MAX;   // the runs end themselves
+    const int rows = g.group - j.row0 < attn::kWaveRows ? g.group - j.row0 : attn::kWaveRows;
+    const int own_n = attn::key_blocks(mine.keys);
+    const int64_t x0 = slot * g.heads + kv * g.group + j.row0;
+    int part = split, block0, block1;
+    if (g.together) {
+        const int n = attn::key_blocks(g.prefix) + own_n;
+        block0 = (int)((int64_t)n * split / splits);
+        block1 = (int)((int64_t)n * (split + 1) / splits);
+    } else {
+        part += g.prefix_splits;
+        block0 = split * g.own_blocks;
+        block1 = block0 + g.own_blocks < own_n ? block0 + g.own_blocks : own_n;
+        if (block0 >= block1) {   // the slot is not that long
+            if ((int)threadIdx.x < rows)
+                *reinterpret_cast<f32x2*>(g.parts.ml + 2 * (part * g.parts.n + x0 + threadIdx.x)) =
+                    f32x2{-__builtin_inff(), 0.f};
+            return;
+        }
+    }
+    const Row row = attn::row_of(j, j.row0 + (lane & 31));
+    attn::run_blocks<T, D>(j, before, mine, block0, block1, row, smem, st);
+    attn::merge_waves<D>(st, row.valid, rows, g.d, smem, [&](int r, int e, float m, float l, f32x4 o) {
+        if (g.prefix_splits + g.own_splits == 1)
+            attn::store_row4<T>(g.o + slot * g.o_row + (int64_t)(kv * g.group + j.row0 + r) * g.o_head,
+                                g.lse == nullptr ? nullptr : g.lse + x0 + r, e, m, l, o);
+        else
+            attn::store_part4(g.parts, part, x0 + r, g.d, e, m, l, o);
+    });
 }
 
-template <typename T>
+template <typename T, int GROUPS>
 __global__ __launch_bounds__(kThreads) void shared_join_kernel(const SharedArgs g)
 {
-    const int64_t x = (int64_t)blockIdx.x * kJoinRows + (threadIdx.x >> 5);
+    const int64_t x = (int64_t)blockIdx.x * kJoinRows<GROUPS> + (threadIdx.x >> 5) / GROUPS;
     const int e = (threadIdx.x & 31) * 4;
     const int64_t b = x / g.heads;
-    if (b >= g.batch || e >= g.d || g.lens[b] < 0) return;
+    const bool there = b < g.batch && e < g.d && g.lens[b] >= 0;
     const int64_t head = x - b * g.heads;
-    attn::join_row<T>(g.parts, g.prefix_splits + g.own_splits, x, g.d, e, g.o + b * g.o_row + head * g.o_head,
-                      g.lse == nullptr ? nullptr : g.lse + x);
+    attn::join_row<T, GROUPS>(g.parts, g.prefix_splits + g.own_splits, there, x, g.d, e, g.o + b * g.o_row + head * g.o_head,
+                              g.lse == nullptr ? nullptr : g.lse + x);
 }
 
 // --------------------------------------------------------------- devices
@@ -443,6 +526,19 @@ int check_shared(const attn_shared_prefix_desc* d)
 // ----------------------------------------------------------------- plans
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
+#ifndef PT
+#define PT 32
+#endif
+#ifndef MINB
+#define MINB 16
+#define MAXB 64
+#define TB 32
+#define TN 8
+#endif
+constexpr int64_t kMinBlocks = MINB;
+constexpr int64_t kMaxBlocks = MAXB;
+constexpr int64_t kTogetherBlocks = TB, kTogetherBatch = TN;
+
 struct PromptPlan {
     int64_t tiles, splits, part_bytes;
 };
@@ -466,25 +562,42 @@ PromptPlan plan_prompt(const attn_prompt_desc* d, int cus)
 }
 
 struct SharedPlan {
-    int64_t row_tiles, own_tiles, prefix_splits, own_splits, prefix_blocks, own_blocks, part_bytes;
+    int64_t together, row_tiles, own_tiles, prefix_splits, own_splits, own_blocks, prefix_wgs, own_wgs, rounds, round_prefix, round_own,
+        part_bytes;
 };
 
 SharedPlan plan_shared(const attn_shared_prefix_desc* d, int cus)
 {
-    SharedPlan p;
-    const int64_t group = d->heads / d->kv_heads;
-    p.row_tiles = ceil_div(d->batch * group, kTileRows);
-    p.own_tiles = ceil_div(group, kTileRows);
-    int64_t s = ceil_div(2 * cus, p.row_tiles * d->kv_heads);
-    const int64_t most = ceil_div(d->prefix, 4 * kTileKeys);
-    p.prefix_splits = s < most ? s : most;
-    const int64_t own = ceil_div(2 * cus, p.own_tiles * d->kv_heads * d->batch);
-    const int64_t own_most = ceil_div(d->slot_rows, 4 * kTileKeys);
-    p.own_splits = own < own_most ? own : own_most;
-    if (p.prefix_splits + p.own_splits == 0) p.own_splits = 1;   // no key at all: one empty part
-    p.prefix_blocks = p.row_tiles * d->kv_heads * p.prefix_splits;
-    p.own_blocks = p.own_tiles * d->kv_heads * p.own_splits * d->batch;
-    p.part_bytes = (p.prefix_splits + p.own_splits) * d->batch * d->heads * (d->head_dim + 2) * 4;
+    SharedPlan p = {};
+    const int64_t group = d->heads / d->kv_heads, rows = d->batch * group;
+    const int64_t prefix_blocks = ceil_div(d->prefix, attn::kBlockKeys), slot_blocks = ceil_div(d->slot_rows, attn::kBlockKeys);
+    p.own_tiles = ceil_div(group, attn::kWaveRows);
+    const int64_t jobs = d->batch * d->kv_heads * p.own_tiles;
+    p.together = d->batch == 1 || prefix_blocks == 0 || (prefix_blocks <= kTogetherBlocks && d->batch <= kTogetherBatch);
+    if (p.together) {
+        const int64_t n = prefix_blocks + slot_blocks, most = n / kMinBlocks;
+        const int64_t want = 2 * cus / jobs;
+        p.prefix_splits = want < most ? want : most;
+        if (p.prefix_splits < 1) p.prefix_splits = 1;
+        p.own_wgs = jobs * p.prefix_splits;
+    } else {
+        const bool few = rows <= attn::kWaveRows;
+        p.row_tiles = few ? 1 : ceil_div(rows, kTileRows);
+        const int64_t want = ceil_div(2 * cus, p.row_tiles * d->kv_heads), most = ceil_div(prefix_blocks, few ? kMinBlocks : PT);
+        p.prefix_splits = want < most ? want : most;
+        p.prefix_wgs = p.row_tiles * d->kv_heads * p.prefix_splits;
+        const int64_t own_want = ceil_div(2 * cus, jobs);
+        int64_t per = ceil_div(slot_blocks, own_want);   // blocks of a part
+        per = per < kMinBlocks ? kMinBlocks : per > kMaxBlocks ? kMaxBlocks : per;
+        p.own_blocks = per;
+        p.own_splits = ceil_div(slot_blocks, per);
+        p.own_wgs = jobs * p.own_splits;
+    }
+    p.round_prefix = p.prefix_wgs < cus ? p.prefix_wgs : cus;
+    p.rounds = p.prefix_wgs == 0 ? 1 : ceil_div(p.prefix_wgs, p.round_prefix);
+    p.round_own = ceil_div(p.own_wgs, p.rounds);
+    const int64_t parts = p.prefix_splits + p.own_splits;
+    p.part_bytes = parts > 1 ? parts * d->batch * d->heads * (d->head_dim + 2) * 4 : 0;
     return p;
 }
 
@@ -523,6 +636,25 @@ struct PromptSplit {
 template <typename T, int D>
 struct SharedParts {
     static const void* f() { return (const void*)&shared_kernel<T, D>; }
+};
+
+// The joining kernel: as many groups as leave each at most 4 parts, up to 8,
+// since a group reads its parts one after the other.
+template <template <typename, int> class K>
+const void* pick_join(int dtype, int64_t parts, int64_t* rows)
+{
+    const int groups = parts <= 4 ? 1 : parts <= 8 ? 2 : parts <= 16 ? 4 : 8;
+    *rows = kThreads / 32 / groups;
+    if (dtype == ATTN_F16) return groups == 1 ? K<F16, 1>::f() : groups == 2 ? K<F16, 2>::f() : groups == 4 ? K<F16, 4>::f() : K<F16, 8>::f();
+    return groups == 1 ? K<BF16, 1>::f() : groups == 2 ? K<BF16, 2>::f() : groups == 4 ? K<BF16, 4>::f() : K<BF16, 8>::f();
+}
+template <typename T, int GROUPS>
+struct PromptJoin {
+    static const void* f() { return (const void*)&prompt_join_kernel<T, GROUPS>; }
+};
+template <typename T, int GROUPS>
+struct SharedJoin {
+    static const void* f() { return (const void*)&shared_join_kernel<T, GROUPS>; }
 };
 
 int check_workspace(const void* ws, int64_t have, int64_t need)
@@ -588,13 +720,14 @@ int attn_prompt(const attn_prompt_desc* d, void* workspace, int64_t workspace_by
     g.zero_q = sc.zero;
     g.parts = parts_in(workspace, p.splits, d->total_q * d->heads);
     const int64_t blocks = p.tiles * d->kv_heads * p.splits;
-    const int64_t join = p.tiles * d->kv_heads * (kTileRows / kJoinRows);
-    if (blocks > INT_MAX || (p.splits > 1 && join > INT_MAX)) return GEMM_F16_NT_UNSUPPORTED;
+    int64_t join_rows = 0;
+    const void* join = pick_join<PromptJoin>(d->dtype, p.splits, &join_rows);
+    const int64_t join_wgs = p.tiles * d->kv_heads * (kTileRows / join_rows);
+    if (blocks > INT_MAX || (p.splits > 1 && join_wgs > INT_MAX)) return GEMM_F16_NT_UNSUPPORTED;
     const hipStream_t s = (hipStream_t)stream;
     if (p.splits == 1) return launch(pick<PromptWhole>(d->dtype, d->head_dim), blocks, &g, s);
     if ((st = launch(pick<PromptSplit>(d->dtype, d->head_dim), blocks, &g, s)) != GEMM_F16_NT_OK) return st;
-    return launch(d->dtype == ATTN_F16 ? (const void*)&prompt_join_kernel<F16> : (const void*)&prompt_join_kernel<BF16>, join,
-                  &g, s);
+    return launch(join, join_wgs, &g, s);
 }
 
 int attn_shared_prefix_check(const attn_shared_prefix_desc* d) { return check_shared(d); }
@@ -648,21 +781,28 @@ int attn_shared_prefix(const attn_shared_prefix_desc* d, void* workspace, int64_
     g.kv_heads = d->kv_heads;
     g.group = d->heads / d->kv_heads;
     g.d = d->head_dim;
+    g.together = (int)p.together;
     g.row_tiles = (int)p.row_tiles;
     g.own_tiles = (int)p.own_tiles;
     g.prefix_splits = (int)p.prefix_splits;
     g.own_splits = (int)p.own_splits;
-    g.prefix_blocks = (uint32_t)p.prefix_blocks;
+    g.own_blocks = (int)p.own_blocks;
+    g.prefix_wgs = (uint32_t)p.prefix_wgs;
+    g.own_wgs = (uint32_t)p.own_wgs;
+    g.round_prefix = (uint32_t)p.round_prefix;
+    g.round_own = (uint32_t)p.round_own;
     g.c = sc.c;
     g.flip = sc.flip;
     g.zero_q = sc.zero;
     g.parts = parts_in(workspace, p.prefix_splits + p.own_splits, d->batch * d->heads);
-    const int64_t blocks = p.prefix_blocks + p.own_blocks;
+    const int64_t blocks = p.rounds * (p.round_prefix + p.round_own);
     if (blocks > INT_MAX) return GEMM_F16_NT_UNSUPPORTED;
     const hipStream_t s = (hipStream_t)stream;
-    if ((st = launch(pick<SharedParts>(d->dtype, d->head_dim), blocks, &g, s)) != GEMM_F16_NT_OK) return st;
-    return launch(d->dtype == ATTN_F16 ? (const void*)&shared_join_kernel<F16> : (const void*)&shared_join_kernel<BF16>,
-                  ceil_div(d->batch * d->heads, kJoinRows), &g, s);
+    st = launch(pick<SharedParts>(d->dtype, d->head_dim), blocks, &g, s);
+    if (st != GEMM_F16_NT_OK || p.part_bytes == 0) return st;
+    int64_t join_rows = 0;
+    const void* join = pick_join<SharedJoin>(d->dtype, p.prefix_splits + p.own_splits, &join_rows);
+    return launch(join, ceil_div(d->batch * d->heads, join_rows), &g, s);
 }
 
 }  // extern "C"

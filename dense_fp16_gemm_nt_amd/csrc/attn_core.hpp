@@ -55,6 +55,11 @@ struct F16 {
     {
         return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2){x, y}, f16x2));
     }
+    // s + the two halves of p
+    static __device__ __forceinline__ float sum2(uint32_t p, float s)
+    {
+        return __builtin_amdgcn_fdot2(__builtin_bit_cast(f16x2, p), f16x2{(_Float16)1.f, (_Float16)1.f}, s, false);
+    }
 };
 
 struct BF16 {
@@ -65,6 +70,10 @@ struct BF16 {
     static __device__ __forceinline__ uint32_t pack(float x, float y)
     {
         return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2){x, y}, bf16x2));
+    }
+    static __device__ __forceinline__ float sum2(uint32_t p, float s)
+    {
+        return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, p), bf16x2{(__bf16)1.f, (__bf16)1.f}, s, false);
     }
 };
 
@@ -128,6 +137,7 @@ struct Job {
     int rows, row0, group;
     int keys;            // keys of the sequence
     int lead;            // causal: row's keys are [0, token + lead + 1); otherwise INT32_MAX
+    int most;            // keys that the last row may read
     int tile0, tile1;
     int d;               // head size
     float c;             // |scale| * log2 e
@@ -245,31 +255,44 @@ __device__ __forceinline__ Reads<D> reads_of(uint32_t lds, int lane)
     return x;
 }
 
-// S^T of one tile, whose K rows are at byte `at` of LDS: s[b] holds keys 32 b ..
-// of row l % 32.
-template <typename T, int D>
-__device__ __forceinline__ void scores(const Reads<D>& x, uint32_t at, const u32x4 (&q)[Shape<D>::KSTEPS], f32x16 (&s)[2])
+// Waits for everything the wave has in flight (loads to LDS, LDS reads) and
+// for the other waves: what each of them loaded or wrote is then there for
+// all, and what each of them read may be overwritten.
+__device__ __forceinline__ void publish()
 {
-    using S = Shape<D>;
-#pragma unroll
-    for (int b = 0; b < 2; ++b) {
-        f32x16 acc = {};
-#pragma unroll
-        for (int i = 0; i < S::KSTEPS; ++i)
-            acc = T::mfma(*reinterpret_cast<const G16_LDS u32x4*>(x.k[i] + at + b * 32 * S::PITCH), q[i], acc);
-        s[b] = acc;
-    }
+    __builtin_amdgcn_sched_barrier(0);
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
 }
 
-// Scores of keys past a row's limit become -inf, whatever they were.
-__device__ __forceinline__ void mask(f32x16 (&s)[2], int limit, int key0, int half)
+// Waits until at most N of the wave's loads to LDS are in flight and its LDS
+// reads are done.
+template <int N>
+__device__ __forceinline__ void landed()
 {
-    const int n = limit - key0 - 4 * half;   // of the keys 32 b + 8 (i / 4) + i % 4
+    __builtin_amdgcn_sched_barrier(0);
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(N) : "memory");
+    __builtin_amdgcn_sched_barrier(0);
+}
+
+// S^T of 32 keys, whose K rows are at byte `at` of LDS: keys 8 (i / 4) +
+// 4 (l / 32) + i % 4 of row l % 32.
+template <typename T, int D>
+__device__ __forceinline__ f32x16 scores(const Reads<D>& x, uint32_t at, const u32x4 (&q)[Shape<D>::KSTEPS])
+{
+    f32x16 acc = {};
 #pragma unroll
-    for (int b = 0; b < 2; ++b)
+    for (int i = 0; i < Shape<D>::KSTEPS; ++i)
+        acc = T::mfma(*reinterpret_cast<const G16_LDS u32x4*>(x.k[i] + at), q[i], acc);
+    return acc;
+}
+
+// Scores of all but the first `keys` of 32 keys become -inf, whatever they were.
+__device__ __forceinline__ void mask(f32x16& s, int keys, int half)
+{
+    const int n = keys - 4 * half;
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
-            s[b][i] = (32 * b + 8 * (i / 4) + i % 4) < n ? s[b][i] : -__builtin_inff();
+    for (int i = 0; i < 16; ++i) s[i] = (8 * (i / 4) + i % 4) < n ? s[i] : -__builtin_inff();
 }
 
 // One row's running state: m (base 2), the lane's part of the sum, O^T.
@@ -288,13 +311,14 @@ __device__ __forceinline__ void init(State<D>& st)
     for (int b = 0; b < Shape<D>::DBLOCKS; ++b) st.o[b] = f32x16{};
 }
 
-// The maximum of a row's scores in a tile, in the units of m.
-__device__ __forceinline__ float top_score(const f32x16 (&s)[2], float c)
+// The maximum of a row's scores (of 32 keys for each block), in the units of m.
+template <int N>
+__device__ __forceinline__ float top_score(const f32x16 (&s)[N], float c)
 {
-    float mx = __builtin_fmaxf(s[0][0], s[1][0]);
+    float mx = s[0][0];
 #pragma unroll
-    for (int i = 1; i < 16; ++i) mx = max3(mx, s[0][i], s[1][i]);
-    return max_halves(mx) * c;
+    for (int i = 1; i < 16 * N - 1; i += 2) mx = max3(mx, s[i / 16][i % 16], s[(i + 1) / 16][(i + 1) % 16]);
+    return max_halves(__builtin_fmaxf(mx, s[N - 1][15])) * c;
 }
 
 // Raises a row's maximum where a tile's asks for it, and rescales what was
@@ -313,32 +337,38 @@ __device__ __forceinline__ void raise(float mx, State<D>& st)
         for (int i = 0; i < 16; ++i) st.o[b][i] *= a;
 }
 
-// Softmax weights of one tile: P^T as B operands p[kk] of the keys 16 kk ..
+// Softmax weights of 32 keys: P^T as B operands p[kk] of the keys 16 kk ..
 // 16 kk + 15, and their sum.
 template <typename T, int D>
-__device__ __forceinline__ void weights(const f32x16 (&s)[2], float c, State<D>& st, u32x4 (&p)[4])
+__device__ __forceinline__ void weights(const f32x16& s, float c, State<D>& st, u32x4 (&p)[2])
 {
     const float base = st.m == -__builtin_inff() ? 0.f : kShift - st.m;
 #pragma unroll
-    for (int b = 0; b < 2; ++b)
+    for (int h = 0; h < 2; ++h) {
+        float e[8];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            float e[8];
+        for (int i = 0; i < 8; ++i) e[i] = exp2_(__builtin_fmaf(s[8 * h + i], c, base));
+#if DOT2
 #pragma unroll
-            for (int i = 0; i < 8; ++i) e[i] = exp2_(__builtin_fmaf(s[b][8 * h + i], c, base));
-            st.l += ((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7]));
-#pragma unroll
-            for (int i = 0; i < 4; ++i) p[2 * b + h][i] = T::pack(e[2 * i], e[2 * i + 1]);
+        for (int i = 0; i < 4; ++i) {
+            p[h][i] = T::pack(e[2 * i], e[2 * i + 1]);
+            st.l = T::sum2(p[h][i], st.l);
         }
+#else
+        st.l += ((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7]));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) p[h][i] = T::pack(e[2 * i], e[2 * i + 1]);
+#endif
+    }
 }
 
-// O^T += V^T P^T over one tile, whose V rows are at byte `at` of LDS.
+// O^T += V^T P^T over 32 keys, whose V rows are at byte `at` of LDS.
 template <typename T, int D>
-__device__ __forceinline__ void accumulate(const Reads<D>& x, uint32_t at, const u32x4 (&p)[4], State<D>& st)
+__device__ __forceinline__ void accumulate(const Reads<D>& x, uint32_t at, const u32x4 (&p)[2], State<D>& st)
 {
     using S = Shape<D>;
 #pragma unroll
-    for (int kk = 0; kk < 4; ++kk)
+    for (int kk = 0; kk < 2; ++kk)
 #pragma unroll
         for (int b = 0; b < S::DBLOCKS; ++b) {
             const uint32_t a = x.v[b] + at + kk * 16 * S::PITCH;
@@ -349,13 +379,17 @@ __device__ __forceinline__ void accumulate(const Reads<D>& x, uint32_t at, const
         }
 }
 
-// LDS of a workgroup: two K tiles, then two V tiles.
+// LDS of a workgroup: two K and two V tiles, or a K and a V block of 32 keys
+// for each wave, or the waves' partial outputs.
+constexpr int kMergePad = 4;   // floats between rows, so that 32 rows at one element spread over the banks
 template <int D>
 constexpr int lds_bytes()
 {
-    return 4 * Shape<D>::TILE;
+    constexpr int tiles = 4 * Shape<D>::TILE, merge = kWaves * kWaveRows * (2 + D + kMergePad) * 4;
+    return tiles > merge ? tiles : merge;
 }
 
+// ---------------------------------------------------------------- many rows
 // All tiles of a job; the four waves share the K and V tiles.  Tile t + 1 of
 // K and t of V are in LDS when iteration t begins; K t + 2 and V t + 1 are
 // loaded while it runs.
@@ -373,33 +407,36 @@ __device__ __forceinline__ void run_tiles(const Job& j, const Row& row, char* sm
     const Reads<D> x = reads_of<D>(lds, lane);
     const uint32_t koff = tile_offset<D, false>(j.k_row, j.d, tid), voff = tile_offset<D, true>(j.v_row, j.d, tid);
     const uint32_t dst = lds + __builtin_amdgcn_readfirstlane(tid >> 6) * 1024;
-    constexpr uint32_t K0 = 0, V0 = 2 * S::TILE;
+    constexpr uint32_t K0 = 0, V0 = 2 * S::TILE, HALF = S::TILE / 2;
     auto load_k = [&](int t, uint32_t par) { load_tile<D>(j.k, j.k_row, j.keys, t, j.d, koff, dst + K0 + par * S::TILE); };
     auto load_v = [&](int t, uint32_t par) { load_tile<D>(j.v, j.v_row, j.keys, t, j.d, voff, dst + V0 + par * S::TILE); };
     load_k(j.tile0, 0);
     load_v(j.tile0, 0);
     if (j.tile0 + 1 < j.tile1) load_k(j.tile0 + 1, 1);
-    wait_vmcnt<0>();
-    wg_barrier();
+    publish();
     f32x16 cur[2], next[2];
-    scores<T, D>(x, K0, q, cur);
+    cur[0] = scores<T, D>(x, K0, q);
+    cur[1] = scores<T, D>(x, K0 + HALF, q);
     auto step = [&](int t, uint32_t par, f32x16 (&a)[2], f32x16 (&b)[2]) {
-        // this wave's reads of K t and V t - 1 are done and its loads of
-        // K t + 1 and V t have landed; behind the barrier that holds for all
-        wait_lgkmcnt0();
-        wait_vmcnt<0>();
-        wg_barrier();
+        // K t + 1 and V t have landed; K t and V t - 1 have been read
+        publish();
         if (t + 2 < j.tile1) load_k(t + 2, par);
         if (t + 1 < j.tile1) {
             load_v(t + 1, 1 - par);
-            scores<T, D>(x, K0 + (1 - par) * S::TILE, q, b);
+            b[0] = scores<T, D>(x, K0 + (1 - par) * S::TILE, q);
+            b[1] = scores<T, D>(x, K0 + (1 - par) * S::TILE + HALF, q);
         }
-        if ((t + 1) * kTileKeys > first_limit) mask(a, row.limit, t * kTileKeys, half);
+        if ((t + 1) * kTileKeys > first_limit) {
+            mask(a[0], row.limit - t * kTileKeys, half);
+            mask(a[1], row.limit - t * kTileKeys - 32, half);
+        }
         const float mx = top_score(a, j.c);
         if (__builtin_amdgcn_ballot_w64(mx > st.m + kSlack) != 0) raise<D>(mx, st);
-        u32x4 p[4];
-        weights<T, D>(a, j.c, st, p);
-        accumulate<T, D>(x, V0 + par * S::TILE, p, st);
+        u32x4 p0[2], p1[2];
+        weights<T, D>(a[0], j.c, st, p0);
+        weights<T, D>(a[1], j.c, st, p1);
+        accumulate<T, D>(x, V0 + par * S::TILE, p0, st);
+        accumulate<T, D>(x, V0 + par * S::TILE + HALF, p1, st);
     };
     int t = j.tile0;
     for (; t + 1 < j.tile1; t += 2) {
@@ -407,6 +444,94 @@ __device__ __forceinline__ void run_tiles(const Job& j, const Row& row, char* sm
         step(t + 1, 1, next, cur);
     }
     if (t < j.tile1) step(t, 0, cur, next);
+}
+
+// ----------------------------------------------------------------- few rows
+// Up to 32 rows against many keys: the keys' bytes are the work, so all four
+// waves take the same rows and deal blocks of 32 keys among them.  Each wave
+// loads its blocks into LDS of its own and waits for its own loads alone, so
+// a workgroup keeps 32 to 64 KiB in flight without a barrier in the loop.
+// The keys are one run or two, one after the other (a shared prefix and a
+// sequence's own keys).
+struct Keys {
+    const char* k;
+    const char* v;
+    int64_t k_row, v_row;   // bytes
+    int keys;
+};
+constexpr int kBlockKeys = 32;
+__device__ __forceinline__ int key_blocks(int keys) { return (int)(((int64_t)keys + kBlockKeys - 1) / kBlockKeys); }
+
+// Blocks [block0, block1) of the runs' blocks; row.limit counts keys of the
+// first run.
+template <typename T, int D>
+__device__ __forceinline__ void run_blocks(const Job& j, const Keys& one, const Keys& two, int block0, int block1,
+                                           const Row& row, char* smem, State<D>& st)
+{
+    using S = Shape<D>;
+    constexpr int ROWS = 64 / S::CHUNKS;        // rows of one load
+    constexpr int NL = kBlockKeys / ROWS;       // loads of a block
+    constexpr int COLS = S::CHUNKS == 16 ? 4 : 2;   // the swizzle of K differs from load to load, with this period
+    constexpr uint32_t HALF = S::TILE / 2;
+    const int lane = threadIdx.x & 63, half = lane >> 5, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    u32x4 q[S::KSTEPS];
+    load_q<D>(j, row, half, q);
+    init(st);
+    int at = block0 + w;
+    if (at >= block1) return;
+    const int first_limit = __builtin_amdgcn_readfirstlane(row.limit);
+    const int blocks1 = key_blocks(one.keys);
+    const uint32_t lds = lds_address(smem) + w * S::TILE;
+    const Reads<D> x = reads_of<D>(lds, lane);
+    const int r = lane / S::CHUNKS, pc = lane % S::CHUNKS;
+    uint32_t kcol[COLS];
+#pragma unroll
+    for (int i = 0; i < COLS; ++i) {
+        const int lc = pc ^ swz_k<D>(r + i * ROWS);
+        kcol[i] = lc * 8 < j.d ? lc * 16 : 0x80000000u;
+    }
+    const int vc = pc ^ swz_v<D>(r);
+    const uint32_t vcol = vc * 8 < j.d ? vc * 16 : 0x80000000u;
+    // a block past the last is loaded as zeros: the counts of loads in flight stay the same
+    auto load = [&](int blk, bool v) {
+        const bool second = blk >= blocks1;
+        const int key0 = (second ? blk - blocks1 : blk) * kBlockKeys;
+        const int keys = second ? two.keys : one.keys;
+        const int64_t row_bytes = v ? (second ? two.v_row : one.v_row) : (second ? two.k_row : one.k_row);
+        const char* base = v ? (second ? two.v : one.v) : (second ? two.k : one.k);
+        const int n = blk >= block1 ? 0 : keys - key0 < kBlockKeys ? keys - key0 : kBlockKeys;
+        const uint32_t bytes = n > 0 ? (uint32_t)(n - 1) * (uint32_t)row_bytes + 2u * (uint32_t)j.d : 0u;
+        const uint64_t a = (uint64_t)(base + (int64_t)key0 * row_bytes);
+        const u32x4 rs = {(uint32_t)a, (uint32_t)(a >> 32) & 0xffffu, bytes, 0x00020000u};
+        const uint32_t off = (uint32_t)r * (uint32_t)row_bytes;
+#pragma unroll
+        for (int i = 0; i < NL; ++i)
+            load_to_lds(rs, lds + (v ? HALF : 0) + i * 1024,
+                        off + (uint32_t)(i * ROWS) * (uint32_t)row_bytes + (v ? vcol : kcol[i % COLS]));
+    };
+    load(at, false);
+    load(at, true);
+    for (; at < block1; at += kWaves) {
+        landed<NL>();   // K; V may be in flight
+        f32x16 s[1] = {scores<T, D>(x, 0, q)};
+        landed<NL>();   // K has been read
+        load(at + kWaves, false);
+        const bool second = at >= blocks1;
+        const int key0 = (second ? at - blocks1 : at) * kBlockKeys;
+        const int n = (second ? two.keys : one.keys) - key0;
+        if (n < kBlockKeys || (!second && key0 + kBlockKeys > first_limit)) {
+            const int lim = row.limit - key0;
+            mask(s[0], second || n < lim ? n : lim, half);
+        }
+        const float mx = top_score(s, j.c);
+        if (__builtin_amdgcn_ballot_w64(mx > st.m + kSlack) != 0) raise<D>(mx, st);
+        u32x4 p[2];
+        weights<T, D>(s[0], j.c, st, p);
+        landed<NL>();   // V; the next K may be in flight
+        accumulate<T, D>(x, HALF, p, st);
+        landed<NL>();   // V has been read
+        load(at + kWaves, true);
+    }
 }
 
 // Partial results of a split job: for row x (of n) and part s, m and l at
@@ -417,25 +542,33 @@ struct Parts {
     int64_t n;
 };
 
+// Four elements of a row's output.
+template <typename T>
+__device__ __forceinline__ void store4(char* o, int e, f32x4 x)
+{
+    *reinterpret_cast<u32x2*>(o + 2 * e) = u32x2{T::pack(x[0], x[1]), T::pack(x[2], x[3])};
+}
+__device__ __forceinline__ float inverse(float l) { return l == 0.f ? 0.f : 1.f / l; }
+__device__ __forceinline__ float lse_of(float m, float l)
+{
+    return l == 0.f ? -__builtin_inff() : (m - kShift + __builtin_log2f(l)) * kLn2;
+}
+
 // The row's O, normalised and rounded, and its log-sum-exp.
 template <typename T, int D>
 __device__ __forceinline__ void store_row(const State<D>& st, int d, char* o, float* lse, int half)
 {
-    const float l = sum_halves(st.l);
-    const float inv = l == 0.f ? 0.f : 1.f / l;
+    const float l = sum_halves(st.l), inv = inverse(l);
 #pragma unroll
     for (int b = 0; b < Shape<D>::DBLOCKS; ++b)
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
             const int e = 32 * b + 8 * g + 4 * half;
-            if (e < d) {
-                u32x2 x;
-                x[0] = T::pack(st.o[b][4 * g] * inv, st.o[b][4 * g + 1] * inv);
-                x[1] = T::pack(st.o[b][4 * g + 2] * inv, st.o[b][4 * g + 3] * inv);
-                *reinterpret_cast<u32x2*>(o + 2 * e) = x;
-            }
+            if (e < d)
+                store4<T>(o, e, f32x4{st.o[b][4 * g] * inv, st.o[b][4 * g + 1] * inv, st.o[b][4 * g + 2] * inv,
+                                      st.o[b][4 * g + 3] * inv});
         }
-    if (lse != nullptr && half == 0) *lse = l == 0.f ? -__builtin_inff() : (st.m - kShift + __builtin_log2f(l)) * kLn2;
+    if (lse != nullptr && half == 0) *lse = lse_of(st.m, l);
 }
 
 template <int D>
@@ -457,30 +590,128 @@ __device__ __forceinline__ void store_part(const State<D>& st, int d, const Part
         }
 }
 
-// Joins `parts` partial results of row x and stores it; four elements from e on.
+// Four elements of a row whose sums are complete: the output, or a part.
 template <typename T>
-__device__ __forceinline__ void join_row(const Parts& w, int parts, int64_t x, int d, int e, char* o, float* lse)
+__device__ __forceinline__ void store_row4(char* o, float* lse, int e, float m, float l, f32x4 x)
 {
+    const float inv = inverse(l);
+    store4<T>(o, e, f32x4{x[0] * inv, x[1] * inv, x[2] * inv, x[3] * inv});
+    if (lse != nullptr && e == 0) *lse = lse_of(m, l);
+}
+__device__ __forceinline__ void store_part4(const Parts& w, int part, int64_t row, int d, int e, float m, float l, f32x4 x)
+{
+    const int64_t at = (int64_t)part * w.n + row;
+    if (e == 0) *reinterpret_cast<f32x2*>(w.ml + 2 * at) = f32x2{m, l};
+    *reinterpret_cast<f32x4*>(w.o + at * d + e) = x;
+}
+
+// Adds up what the four waves hold of the same rows and hands every four
+// elements of a row that is there to store(r, e, m, l, o).
+template <int D, typename F>
+__device__ __forceinline__ void merge_waves(const State<D>& st, bool valid, int rows, int d, char* smem, F store)
+{
+    constexpr int PITCH = D + kMergePad;
+    const int tid = threadIdx.x, lane = tid & 63, half = lane >> 5, r = lane & 31;
+    const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
+    f32x2* ml = reinterpret_cast<f32x2*>(smem);
+    float* o = reinterpret_cast<float*>(smem) + kWaves * kWaveRows * 2;
+    // a row's largest m of the waves that saw a key of it
+    auto top = [&](int row) {
+        float m = -__builtin_inff();
+#pragma unroll
+        for (int i = 0; i < kWaves; ++i) {
+            const f32x2 y = ml[i * kWaveRows + row];
+            m = y[1] == 0.f ? m : __builtin_fmaxf(m, y[0]);
+        }
+        return m;
+    };
+    const float l = sum_halves(st.l);
+    publish();   // the waves are done with their K and V blocks
+    if (half == 0) ml[w * kWaveRows + r] = f32x2{st.m, l};
+    publish();
+    if (valid) {
+        const float f = l == 0.f ? 0.f : exp2_(st.m - top(r));
+        float* to = o + (w * kWaveRows + r) * PITCH;
+#pragma unroll
+        for (int b = 0; b < Shape<D>::DBLOCKS; ++b)
+#pragma unroll
+            for (int g = 0; g < 4; ++g)
+                *reinterpret_cast<f32x4*>(to + 32 * b + 8 * g + 4 * half) = f32x4{
+                    st.o[b][4 * g] * f, st.o[b][4 * g + 1] * f, st.o[b][4 * g + 2] * f, st.o[b][4 * g + 3] * f};
+    }
+    publish();
+    for (int i = tid; i < rows * (D / 4); i += kThreads) {
+        const int row = i / (D / 4), e = i % (D / 4) * 4;
+        if (e >= d) continue;
+        const float m = top(row);
+        float sum = 0.f;
+        f32x4 x = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int k = 0; k < kWaves; ++k) {
+            const f32x2 y = ml[k * kWaveRows + row];
+            sum += y[1] == 0.f ? 0.f : exp2_(y[0] - m) * y[1];
+            const f32x4 z = *reinterpret_cast<const f32x4*>(o + (k * kWaveRows + row) * PITCH + e);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) x[c] += z[c];
+        }
+        store(row, e, m, sum, x);
+    }
+}
+
+// Joins `parts` partial results of row x, four elements from e on: GROUPS
+// groups of 32 lanes take every GROUPS-th part, their sums meet in LDS, and
+// the first group stores.  All threads of the workgroup call it; `there` says
+// whether the lane has a row and elements.
+template <typename T, int GROUPS>
+__device__ __forceinline__ void join_row(const Parts& w, int parts, bool there, int64_t x, int d, int e, char* o, float* lse)
+{
+    const int tid = threadIdx.x, grp = (tid >> 5) % GROUPS;
+    if (!there) {
+        x = 0;
+        e = 0;
+    }
     float m = -__builtin_inff();
-    for (int s = 0; s < parts; ++s) m = __builtin_fmaxf(m, w.ml[2 * ((int64_t)s * w.n + x)]);
+#pragma unroll 4
+    for (int s = grp; s < parts; s += GROUPS) {
+        const f32x2 ml = *reinterpret_cast<const f32x2*>(w.ml + 2 * ((int64_t)s * w.n + x));
+        m = ml[1] == 0.f ? m : __builtin_fmaxf(m, ml[0]);
+    }
     f32x4 acc = {0.f, 0.f, 0.f, 0.f};
     float l = 0.f;
-    for (int s = 0; s < parts; ++s) {
+#pragma unroll 4
+    for (int s = grp; s < parts; s += GROUPS) {
         const int64_t at = (int64_t)s * w.n + x;
         const f32x2 ml = *reinterpret_cast<const f32x2*>(w.ml + 2 * at);
-        if (ml[1] == 0.f) continue;
-        const float f = exp2_(ml[0] - m);
-        l += f * ml[1];
         const f32x4 y = *reinterpret_cast<const f32x4*>(w.o + at * d + e);
+        const bool some = ml[1] != 0.f;   // otherwise O holds whatever was there
+        const float f = exp2_(ml[0] - m);
+        l += some ? f * ml[1] : 0.f;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) acc[i] += f * y[i];
+        for (int i = 0; i < 4; ++i) acc[i] += some ? f * y[i] : 0.f;
     }
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-    u32x2 r;
-    r[0] = T::pack(acc[0] * inv, acc[1] * inv);
-    r[1] = T::pack(acc[2] * inv, acc[3] * inv);
-    *reinterpret_cast<u32x2*>(o + 2 * e) = r;
-    if (lse != nullptr && e == 0) *lse = l == 0.f ? -__builtin_inff() : (m - kShift + __builtin_log2f(l)) * kLn2;
+    if constexpr (GROUPS > 1) {
+        __shared__ f32x4 sums[kThreads];
+        __shared__ f32x2 mls[kThreads / 32];
+        sums[tid] = acc;
+        if ((tid & 31) == 0) mls[tid >> 5] = f32x2{m, l};
+        __syncthreads();
+        if (grp != 0) return;
+        const int first = tid >> 5;
+        m = -__builtin_inff();
+#pragma unroll
+        for (int i = 0; i < GROUPS; ++i) m = mls[first + i][1] == 0.f ? m : __builtin_fmaxf(m, mls[first + i][0]);
+        acc = f32x4{0.f, 0.f, 0.f, 0.f};
+        l = 0.f;
+#pragma unroll
+        for (int i = 0; i < GROUPS; ++i) {
+            const f32x2 ml = mls[first + i];
+            const float f = ml[1] == 0.f ? 0.f : exp2_(ml[0] - m);
+            l += f * ml[1];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) acc[c] += f * sums[tid + 32 * i][c];
+        }
+    }
+    if (there) store_row4<T>(o, lse, e, m, l, acc);
 }
 
 }  // namespace attn
