@@ -13,10 +13,6 @@ import ctypes
 import os
 import threading
 
-from . import attention
-from .attention import (attention_prompt, attention_prompt_workspace, attention_shared_prefix,
-                        attention_shared_prefix_workspace)
-
 PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(PKG, "libgemm_f16_nt.so")
 
@@ -386,3 +382,9 @@ def ring_plan(depth: int, steps: int):
     if st != OK:
         raise GemmError(st, "gemm_f16_nt_ring_plan")
     return stage, lap, refill
+
+
+# at the end: the attention binding uses what is defined above
+from . import attention  # noqa: E402
+from .attention import (attention_prompt, attention_prompt_workspace, attention_shared_prefix,  # noqa: E402
+                        attention_shared_prefix_workspace)

@@ -13,6 +13,8 @@ import ctypes
 import math
 import struct
 
+from . import OK, GemmError, lib
+
 F16 = 0
 BF16 = 1
 
@@ -77,24 +79,24 @@ def _query(Q):
 def _strides(name, X, shape, dtype, device):
     """Strides of the dimensions before the last of a tensor that has to have this shape and type, the last contiguous;
     0 where a dimension has one entry and its stride says nothing."""
-    if X.dtype != dtype:
+    if X.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype} like Q, not {X.dtype}")
     if X.device != device:
         raise ValueError(f"{name} is on {X.device}, Q on {device}")
     if X.shape != shape:
         raise ValueError(f"{name} must be {tuple(shape)}; got {tuple(X.shape)}")
-    st = X.stride()
-    if st[-1] != 1 and shape[-1] > 1:
+    *st, last = X.stride()
+    if last != 1 and shape[-1] > 1:
         raise ValueError(f"{name}: last dimension must be contiguous")
-    return [s if n > 1 else 0 for n, s in zip(shape[:-1], st)]
+    return st if min(shape) > 1 else [s if n > 1 else 0 for n, s in zip(shape, st)]
 
 
 def _ints(name, X, n, device):
     import torch
 
-    if X.dtype != torch.int32:
+    if X.dtype is not torch.int32:
         raise TypeError(f"{name} must be torch.int32")
-    if X.device != device or X.dim() != 1 or X.numel() != n or not X.is_contiguous():
+    if X.device != device or X.shape != (n,) or not X.is_contiguous():
         raise ValueError(f"{name} must be a contiguous tensor of {n} values on {device}")
     return X.data_ptr()
 
@@ -116,7 +118,7 @@ def _outputs(Q, O, lse, return_lse):
     import torch
 
     if O is None:
-        O = torch.empty_like(Q, memory_format=torch.contiguous_format)
+        O = torch.empty_like(Q) if Q.is_contiguous() else torch.empty_like(Q, memory_format=torch.contiguous_format)
     if lse is None:
         if return_lse:
             lse = torch.empty(Q.shape[:2], dtype=torch.float32, device=Q.device)
@@ -125,36 +127,39 @@ def _outputs(Q, O, lse, return_lse):
     return O, lse
 
 
+_entries = {}   # name -> (entry point, its workspace query) of the loaded library
+
+
 def _call(name, desc, device, workspace):
     """Runs an entry point on a device's current stream, with a workspace if it needs one."""
     import torch
 
-    from . import OK, GemmError, lib
-
     if device.index != torch.cuda.current_device():   # launches go to the current device
         with torch.cuda.device(device):
             return _call(name, desc, device, workspace)
-    L = lib()
+    if name not in _entries:
+        L = lib()
+        _entries[name] = getattr(L, name), getattr(L, name + "_workspace")
+    run, size = _entries[name]
     ws, have = None, 0
     if workspace is None:
-        need = getattr(L, name + "_workspace")(desc)
-        if need < 0:
-            raise GemmError(int(need), name)
-        if need:
-            workspace = torch.empty(need, dtype=torch.uint8, device=device)
+        have = size(desc)
+        if have < 0:
+            raise GemmError(int(have), name)
+        if have:
+            workspace = torch.empty(have, dtype=torch.uint8, device=device)
+            ws = workspace.data_ptr()
     elif workspace.device != device or not workspace.is_contiguous():
         raise ValueError(f"workspace must be a contiguous tensor on {device}")
-    if workspace is not None:
+    else:
         ws, have = workspace.data_ptr(), workspace.numel() * workspace.element_size()
-    st = getattr(L, name)(desc, ws, have, torch._C._cuda_getCurrentRawStream(device.index))
+    st = run(desc, ws, have, torch._C._cuda_getCurrentRawStream(device.index))
     if st != OK:
         raise GemmError(st, name)
 
 
 def _workspace_bytes(name, desc, device):
     import torch
-
-    from . import GemmError, lib
 
     with torch.cuda.device(device):
         n = getattr(lib(), name + "_workspace")(desc)

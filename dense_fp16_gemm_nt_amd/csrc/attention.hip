@@ -14,15 +14,13 @@
 
 #include "attn_core.hpp"
 #include "sched.hpp"
-#ifndef NOFEW
-#define NOFEW 0
-#endif
 
 using namespace g16;
 
 namespace {
 
 using attn::BF16;
+using attn::Div;
 using attn::F16;
 using attn::f32x2;
 using attn::Job;
@@ -44,9 +42,10 @@ struct PromptArgs {
     const int32_t* cu_q;
     const int32_t* cu_k;
     int64_t q_row, q_head, k_row, k_head, v_row, v_head, o_row, o_head;   // bytes
-    int batch, total_q, total_k, heads, kv_heads, group, d, causal;
-    int tiles;    // row tiles of one kv head, at most
-    int splits;
+    int batch, total_q, total_k, heads, kv_heads, d, causal;
+    Div group, splits, units;   // units: kv heads x splits, or an eighth of them (by_xcd)
+    Div join_kv;                // kv heads
+    int by_xcd;
     float c;
     uint32_t flip;
     int zero_q;
@@ -61,63 +60,104 @@ struct Tile {
 
 __device__ __forceinline__ int clampi(int x, int lo, int hi) { return x < lo ? lo : x > hi ? hi : x; }
 
-// Tile `t` of the sequences' tiles put one after the other.  Each lane looks
-// at one sequence, 64 at a time; offsets are clamped to the tensors, so that
-// a table that decreases or runs past them still names rows that exist.
-// Within a sequence the tiles come in falling order: under a causal mask
-// those have the most keys, and the longest work starts first.
-__device__ __forceinline__ Tile find_tile(const PromptArgs& g, int t)
+// A sequence's bounds and its number of tiles.  Offsets are clamped to the
+// tensors, so that a table that decreases or runs past them still names rows
+// that exist.
+struct Seq {
+    int q0, nq, k0, nk;
+    uint32_t tiles;
+};
+
+template <int ROWS>
+__device__ __forceinline__ Seq sequence(const PromptArgs& g, int b)
 {
+    const int a0 = g.cu_q[b], a1 = g.cu_q[b + 1], b0 = g.cu_k[b], b1 = g.cu_k[b + 1];
+    Seq s;
+    s.q0 = clampi(a0, 0, g.total_q);
+    s.nq = clampi(a1, s.q0, g.total_q) - s.q0;
+    s.k0 = clampi(b0, 0, g.total_k);
+    s.nk = clampi(b1, s.k0, g.total_k) - s.k0;
+    s.tiles = ((uint32_t)s.nq * g.group.d + ROWS - 1) / ROWS;
+    return s;
+}
+
+// Sum over this lane and those below it, by the lanes' own data paths (six
+// instructions; the same through LDS took 0.5 us of a workgroup's time).
+__device__ __forceinline__ uint32_t wave_scan(uint32_t x)
+{
+    auto add = [&](auto ctrl, auto rows) {
+        x += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, decltype(ctrl)::value, decltype(rows)::value, 0xf, false);
+    };
+    using std::integral_constant;
+    add(integral_constant<int, 0x111>(), integral_constant<int, 0xf>());   // 1, 2, 4 and 8 lanes up within 16
+    add(integral_constant<int, 0x112>(), integral_constant<int, 0xf>());
+    add(integral_constant<int, 0x114>(), integral_constant<int, 0xf>());
+    add(integral_constant<int, 0x118>(), integral_constant<int, 0xf>());
+    add(integral_constant<int, 0x142>(), integral_constant<int, 0xa>());   // lane 15 of a row of 16 to the next row,
+    add(integral_constant<int, 0x143>(), integral_constant<int, 0xc>());   // lane 31 to the upper half
+    return x;
+}
+
+// Tile `t` of the sequences' tiles put one after the other; each lane looks at
+// one sequence, 64 at a time.  Within a sequence the tiles come in falling
+// order: under a causal mask those have the most keys, and the longest work
+// starts first.  (The tiles of all sequences ordered by their keys were no
+// faster on packed lengths of 1 to 2900, 137 against 135 us: neighbours then
+// share no keys.)
+template <int ROWS>
+__device__ __forceinline__ Tile find_tile(const PromptArgs& g, uint32_t t)
+{
+    Tile r = {0, 0, 0, 0, 0, false};
+    if (g.batch == 1) {
+        const Seq s = sequence<ROWS>(g, 0);
+        r = Tile{s.q0, s.nq, s.k0, s.nk, (int)((s.tiles - 1 - t) * ROWS), t < s.tiles};
+        return r;
+    }
     const int lane = threadIdx.x & 63;
-    Tile r;
-    r.found = false;
-    r.q0 = r.nq = r.k0 = r.nk = r.row0 = 0;
-    int64_t before = 0;
+    uint32_t before = 0;
     for (int base = 0; base < g.batch; base += 64) {
-        const int b = base + lane;
-        int q0 = 0, q1 = 0;
-        if (b < g.batch) {
-            q0 = clampi(g.cu_q[b], 0, g.total_q);
-            q1 = clampi(g.cu_q[b + 1], q0, g.total_q);
-        }
-        const int mine = (int)(((int64_t)(q1 - q0) * g.group + kTileRows - 1) / kTileRows);
-        int64_t upto = mine;
-#pragma unroll
-        for (int s = 1; s < 64; s <<= 1) {
-            const int64_t y = __shfl_up(upto, s);
-            if (lane >= s) upto += y;
-        }
-        const uint64_t past = __builtin_amdgcn_ballot_w64(before + upto > t);
+        Seq s = {0, 0, 0, 0, 0};
+        if (base + lane < g.batch) s = sequence<ROWS>(g, base + lane);
+        const uint32_t upto = before + wave_scan(s.tiles);
+        const uint64_t past = __builtin_amdgcn_ballot_w64(upto > t);
         if (past != 0) {
             const int w = __builtin_ctzll(past);
             r.found = true;
-            r.q0 = __builtin_amdgcn_readlane(q0, w);
-            r.nq = __builtin_amdgcn_readlane(q1, w) - r.q0;
-            const int n = __builtin_amdgcn_readlane(mine, w);
-            const int64_t end = before + __shfl(upto, w);
-            r.row0 = __builtin_amdgcn_readfirstlane((int)(end - 1 - t)) * kTileRows;
-            (void)n;
-            const int sb = base + w;
-            r.k0 = clampi(g.cu_k[sb], 0, g.total_k);
-            r.nk = clampi(g.cu_k[sb + 1], r.k0, g.total_k) - r.k0;
+            r.q0 = __builtin_amdgcn_readlane(s.q0, w);
+            r.nq = __builtin_amdgcn_readlane(s.nq, w);
+            r.k0 = __builtin_amdgcn_readlane(s.k0, w);
+            r.nk = __builtin_amdgcn_readlane(s.nk, w);
+            r.row0 = (__builtin_amdgcn_readlane((int)upto, w) - 1 - (int)t) * ROWS;
             return r;
         }
-        before += __shfl(upto, 63);
+        before = (uint32_t)__builtin_amdgcn_readlane((int)upto, 63);
     }
     return r;
 }
 
-__device__ __forceinline__ Job prompt_job(const PromptArgs& g, const Tile& t, int kv, int split)
+// Part `i` of n things split evenly: [first, last).
+struct Range {
+    int first, last;
+};
+__device__ __forceinline__ Range part_of(int n, const Div& splits, int i)
+{
+    const int per = (int)splits.of((uint32_t)n + splits.d - 1);
+    const int first = i * per < n ? i * per : n;
+    return {first, first + per < n ? first + per : n};
+}
+
+template <int ROWS>
+__device__ __forceinline__ Job prompt_job(const PromptArgs& g, const Tile& t, int kv)
 {
     Job j;
-    j.q = g.q + (int64_t)t.q0 * g.q_row + (int64_t)kv * g.group * g.q_head;
+    j.q = g.q + (int64_t)t.q0 * g.q_row + (int64_t)kv * g.group.d * g.q_head;
     j.k = g.k + (int64_t)t.k0 * g.k_row + (int64_t)kv * g.k_head;
     j.v = g.v + (int64_t)t.k0 * g.v_row + (int64_t)kv * g.v_head;
     j.q_token = g.q_row;
     j.q_head = g.q_head;
     j.k_row = g.k_row;
     j.v_row = g.v_row;
-    j.rows = t.nq * g.group;
+    j.rows = t.nq * (int)g.group.d;
     j.row0 = t.row0;
     j.group = g.group;
     j.keys = t.nk;
@@ -126,59 +166,49 @@ __device__ __forceinline__ Job prompt_job(const PromptArgs& g, const Tile& t, in
     j.c = g.c;
     j.flip = g.flip;
     j.zero_q = g.zero_q != 0;
-    int most = t.nk;
+    j.most = t.nk;
     if (g.causal) {
-        const int last = (t.row0 + kTileRows < j.rows ? t.row0 + kTileRows : j.rows) - 1;
-        const int lim = last / g.group + j.lead + 1;
-        most = lim < 0 ? 0 : lim < t.nk ? lim : t.nk;
+        const int last = (j.rows - t.row0 > ROWS ? t.row0 + ROWS : j.rows) - 1;
+        j.most = clampi((int)g.group.of(last) + j.lead + 1, 0, t.nk);
     }
-    j.most = most;
-    const int n = (most + kTileKeys - 1) / kTileKeys;
-    j.tile0 = (int)((int64_t)n * split / g.splits);
-    j.tile1 = (int)((int64_t)n * (split + 1) / g.splits);
     return j;
 }
 
-#ifndef W64
-#define W64 2
-#endif
-template <typename T, int D, bool SPLIT>
-__global__ __launch_bounds__(kThreads, D == 64 ? W64 : 2) void prompt_kernel(const PromptArgs g)
+// W waves of 32 rows (four, or eight for long workgroups: see plan_prompt).
+// Heads of up to 64 elements leave registers for three waves on a SIMD.
+template <typename T, int D, bool SPLIT, int W>
+__global__ __launch_bounds__(64 * W, D == 64 && W == 4 ? 3 : 2) void prompt_kernel(const PromptArgs g)
 {
     __shared__ __attribute__((aligned(256))) char smem[attn::lds_bytes<D>()];
+    constexpr int ROWS = W * attn::kWaveRows;
     // a unit is a kv head and a split; consecutive workgroups go to the XCDs
     // in turn, and each XCD keeps to its own units, whose keys its L2 then
     // holds, with the tiles of the most keys first
-    const uint32_t units = (uint32_t)g.kv_heads * (uint32_t)g.splits;
-    uint32_t unit, t;
-    if (units % kNumXcd == 0) {
-        const uint32_t per = units / kNumXcd, i = blockIdx.x / kNumXcd;
-        unit = blockIdx.x % kNumXcd * per + i % per;
-        t = i / per;
-    } else {
-        unit = blockIdx.x % units;
-        t = blockIdx.x / units;
-    }
-    const int kv = (int)(unit / (uint32_t)g.splits), split = (int)(unit % (uint32_t)g.splits);
-    const Tile tile = find_tile(g, (int)t);
+    uint32_t i = blockIdx.x;
+    if (g.by_xcd) i /= kNumXcd;
+    const uint32_t t = g.units.of(i);
+    uint32_t unit = i - t * g.units.d;
+    if (g.by_xcd) unit += blockIdx.x % kNumXcd * g.units.d;
+    const int kv = (int)g.splits.of(unit), split = SPLIT ? (int)(unit - kv * g.splits.d) : 0;
+    const Tile tile = find_tile<ROWS>(g, t);
     if (!tile.found) return;
-    const Job j = prompt_job(g, tile, kv, split);
+    Job j = prompt_job<ROWS>(g, tile, kv);
     const int lane = threadIdx.x & 63, half = lane >> 5;
     const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     State<D> st;
     const int rows = j.rows - j.row0;
-    if (!NOFEW && rows <= attn::kWaveRows) {
+    if (W == attn::kWaves && rows <= attn::kWaveRows) {
         // the rows of one wave (a single token, a short chunk): all waves
         // take them and divide the keys
         const Row row = attn::row_of(j, j.row0 + (lane & 31));
         const Keys keys = {j.k, j.v, j.k_row, j.v_row, j.keys}, none = {};
         const int n = attn::key_blocks(j.most);
-        attn::run_blocks<T, D>(j, keys, none, (int)((int64_t)n * split / g.splits), (int)((int64_t)n * (split + 1) / g.splits),
-                               row, smem, st);
-        attn::merge_waves<D>(st, row.valid, rows, g.d, smem, [&](int r, int e, float m, float l, f32x4 o) {
-            const int x = j.row0 + r;
-            const int64_t token = (int64_t)tile.q0 + x / g.group;
-            const int head = kv * g.group + x % g.group;
+        const Range r = SPLIT ? part_of(n, g.splits, split) : Range{0, n};
+        attn::run_blocks<T, D>(j, keys, none, r.first, r.last, row, smem, st);
+        attn::merge_waves<D>(st, row.valid, rows, g.d, smem, [&](int y, int e, float m, float l, f32x4 o) {
+            const int x = j.row0 + y, token_in = (int)g.group.of(x);
+            const int64_t token = (int64_t)tile.q0 + token_in;
+            const int head = kv * (int)g.group.d + x - token_in * (int)g.group.d;
             if constexpr (SPLIT)
                 attn::store_part4(g.parts, split, token * g.heads + head, g.d, e, m, l, o);
             else
@@ -187,15 +217,18 @@ __global__ __launch_bounds__(kThreads, D == 64 ? W64 : 2) void prompt_kernel(con
         });
         return;
     }
+    const int n = (int)(((uint32_t)j.most + kTileKeys - 1) / kTileKeys);
+    const Range r = SPLIT ? part_of(n, g.splits, split) : Range{0, n};
+    j.tile0 = r.first;
+    j.tile1 = r.last;
     const Row row = attn::row_of(j, j.row0 + w * attn::kWaveRows + (lane & 31));
-    attn::run_tiles<T, D>(j, row, smem, st);
-    if (!row.valid) return;
+    attn::run_tiles<T, D, W>(j, row, smem, st);
     const int64_t token = (int64_t)tile.q0 + row.token;
-    const int head = kv * g.group + row.head;
+    const int head = kv * (int)g.group.d + row.head;
     if constexpr (SPLIT)
-        attn::store_part<D>(st, g.d, g.parts, split, token * g.heads + head, half);
+        attn::store_part<D>(st, row.valid, g.d, g.parts, split, token * g.heads + head, half);
     else
-        attn::store_row<T, D>(st, g.d, g.o + token * g.o_row + head * g.o_head,
+        attn::store_row<T, D>(st, row.valid, g.d, g.o + token * g.o_row + head * g.o_head,
                               g.lse == nullptr ? nullptr : g.lse + token * g.heads + head, half);
 }
 
@@ -207,15 +240,16 @@ template <typename T, int GROUPS>
 __global__ __launch_bounds__(kThreads) void prompt_join_kernel(const PromptArgs g)
 {
     constexpr uint32_t kSub = kTileRows / kJoinRows<GROUPS>;
-    const uint32_t sub = blockIdx.x % kSub, x = blockIdx.x / kSub;
-    const int kv = (int)(x % (uint32_t)g.kv_heads);
-    const Tile tile = find_tile(g, (int)(x / (uint32_t)g.kv_heads));
+    const uint32_t sub = blockIdx.x % kSub, x = blockIdx.x / kSub, t = g.join_kv.of(x);
+    const int kv = (int)(x - t * g.join_kv.d);
+    const Tile tile = find_tile<kTileRows>(g, t);
     if (!tile.found) return;
     const int r = tile.row0 + (int)sub * kJoinRows<GROUPS> + (int)(threadIdx.x >> 5) / GROUPS, e = (threadIdx.x & 31) * 4;
-    const bool there = r < tile.nq * g.group && e < g.d;
-    const int64_t token = (int64_t)tile.q0 + r / g.group;
-    const int head = kv * g.group + r % g.group;
-    attn::join_row<T, GROUPS>(g.parts, g.splits, there, token * g.heads + head, g.d, e,
+    const bool there = r < tile.nq * (int)g.group.d && e < g.d;
+    const int token_in = (int)g.group.of(r);
+    const int64_t token = (int64_t)tile.q0 + token_in;
+    const int head = kv * (int)g.group.d + r - token_in * (int)g.group.d;
+    attn::join_row<T, GROUPS>(g.parts, (int)g.splits.d, there, token * g.heads + head, g.d, e,
                               g.o + token * g.o_row + head * g.o_head,
                               g.lse == nullptr ? nullptr : g.lse + token * g.heads + head);
 }
@@ -232,14 +266,13 @@ struct SharedArgs {
     const int32_t* lens;
     int64_t q_row, q_head, kp_row, kp_head, vp_row, vp_head;   // bytes
     int64_t ks_slot, ks_row, ks_head, vs_slot, vs_row, vs_head, o_row, o_head;
-    int batch, prefix, slot_rows, heads, kv_heads, group, d;
-    int together;         // each slot's rows take prefix and own keys as one run (splits: prefix_splits)
-    int row_tiles;        // of the prefix: batch * group rows in tiles of 128, or of 32 where that is all
-    int own_tiles;        // of a slot: group rows in tiles of 32
-    int prefix_splits;    // parts of a row that come from the prefix ...
-    int own_splits;       // ... and from its own keys,
-    int own_blocks;       // this many blocks of 32 keys each
+    int batch, prefix, slot_rows, heads, d;
+    Div group, kv_heads, round, row_tiles, own_tiles, prefix_splits, own_splits;   // see SharedPlan
+    int together;
+    int parts_of_row;     // the prefix's, then those of the row's own keys, of
+    int own_blocks;       // blocks of 32 keys each
     uint32_t prefix_wgs, own_wgs, round_prefix, round_own;
+    int by_xcd;
     float c;
     uint32_t flip;
     int zero_q;
@@ -257,8 +290,8 @@ __global__ __launch_bounds__(kThreads, 2) void shared_kernel(const SharedArgs g)
     // unit, then a share of the others, so that a compute unit works on both
     // at once.
     uint32_t i = blockIdx.x;
-    const uint32_t round = i / (g.round_prefix + g.round_own);
-    i -= round * (g.round_prefix + g.round_own);
+    const uint32_t round = g.round.of(i);
+    i -= round * g.round.d;
     const bool own = i >= g.round_prefix;
     i = own ? i - g.round_prefix + round * g.round_own : i + round * g.round_prefix;
     if (i >= (own ? g.own_wgs : g.prefix_wgs)) return;
@@ -273,69 +306,71 @@ __global__ __launch_bounds__(kThreads, 2) void shared_kernel(const SharedArgs g)
     j.zero_q = g.zero_q != 0;
     State<D> st;
     if (!own) {
-        const uint32_t units = (uint32_t)g.kv_heads * (uint32_t)g.prefix_splits, tiles = (uint32_t)g.row_tiles;
-        uint32_t unit, t;
-        if (units % kNumXcd == 0) {   // the row tiles of a unit one after the other on one XCD: its L2 holds their keys
-            unit = i / kNumXcd / tiles * kNumXcd + i % kNumXcd;
-            t = i / kNumXcd % tiles;
+        uint32_t unit, t;   // a kv head and a part of the prefix, and rows
+        if (g.by_xcd) {     // the row tiles of a unit one after the other on one XCD: its L2 holds their keys
+            const uint32_t x = i / kNumXcd;
+            unit = g.row_tiles.of(x);
+            t = x - unit * g.row_tiles.d;
+            unit = unit * kNumXcd + i % kNumXcd;
         } else {
-            unit = i / tiles;
-            t = i % tiles;
+            unit = g.row_tiles.of(i);
+            t = i - unit * g.row_tiles.d;
         }
-        const int kv = (int)(unit / (uint32_t)g.prefix_splits), part = (int)(unit % (uint32_t)g.prefix_splits);
-        j.q = g.q + (int64_t)kv * g.group * g.q_head;
+        const int kv = (int)g.prefix_splits.of(unit), part = (int)(unit - kv * g.prefix_splits.d);
+        j.q = g.q + (int64_t)kv * g.group.d * g.q_head;
         j.k = g.kp + kv * g.kp_head;
         j.v = g.vp + kv * g.vp_head;
         j.k_row = g.kp_row;
         j.v_row = g.vp_row;
-        j.rows = g.batch * g.group;
+        j.rows = g.batch * (int)g.group.d;
         j.row0 = (int)t * kTileRows;
         j.keys = g.prefix;
         if (j.rows <= attn::kWaveRows) {
             const Row row = attn::row_of(j, lane & 31);
             const Keys keys = {j.k, j.v, j.k_row, j.v_row, j.keys}, none = {};
-            const int n = attn::key_blocks(g.prefix);
-            attn::run_blocks<T, D>(j, keys, none, (int)((int64_t)n * part / g.prefix_splits),
-                                   (int)((int64_t)n * (part + 1) / g.prefix_splits), row, smem, st);
+            const Range r = part_of(attn::key_blocks(g.prefix), g.prefix_splits, part);
+            attn::run_blocks<T, D>(j, keys, none, r.first, r.last, row, smem, st);
             attn::merge_waves<D>(st, row.valid, j.rows, g.d, smem, [&](int r, int e, float m, float l, f32x4 o) {
-                const int64_t x = (int64_t)(r / g.group) * g.heads + kv * g.group + r % g.group;
+                const int b = (int)g.group.of(r);
+                const int64_t x = (int64_t)b * g.heads + kv * (int)g.group.d + r - b * (int)g.group.d;
                 attn::store_part4(g.parts, part, x, g.d, e, m, l, o);
             });
             return;
         }
-        const int n = (int)(((int64_t)g.prefix + kTileKeys - 1) / kTileKeys);
-        j.tile0 = (int)((int64_t)n * part / g.prefix_splits);
-        j.tile1 = (int)((int64_t)n * (part + 1) / g.prefix_splits);
+        const Range r = part_of((int)(((uint32_t)g.prefix + kTileKeys - 1) / kTileKeys), g.prefix_splits, part);
+        j.tile0 = r.first;
+        j.tile1 = r.last;
         const Row row = attn::row_of(j, j.row0 + w * attn::kWaveRows + (lane & 31));
-        attn::run_tiles<T, D>(j, row, smem, st);
-        if (row.valid) attn::store_part<D>(st, g.d, g.parts, part, (int64_t)row.token * g.heads + kv * g.group + row.head, half);
+        attn::run_tiles<T, D, attn::kWaves>(j, row, smem, st);
+        attn::store_part<D>(st, row.valid, g.d, g.parts, part,
+                            (int64_t)row.token * g.heads + kv * (int)g.group.d + row.head, half);
         return;
     }
-    const int kv = (int)(i % (uint32_t)g.kv_heads);
-    i /= (uint32_t)g.kv_heads;
-    const uint32_t splits = (uint32_t)(g.together ? g.prefix_splits : g.own_splits);
-    const int split = (int)(i % splits);
-    i /= splits;
-    j.row0 = (int)(i % (uint32_t)g.own_tiles) * attn::kWaveRows;
-    const int64_t slot = i / (uint32_t)g.own_tiles;
+    uint32_t y = g.kv_heads.of(i);
+    const int kv = (int)(i - y * g.kv_heads.d);
+    const Div& splits = g.together ? g.prefix_splits : g.own_splits;
+    uint32_t z = splits.of(y);
+    const int split = (int)(y - z * splits.d);
+    const int64_t slot = g.own_tiles.of(z);
+    j.row0 = (int)(z - (uint32_t)slot * g.own_tiles.d) * attn::kWaveRows;
     const int len = g.lens[slot];
     if (len < 0) return;
     const Keys mine = {g.ks + slot * g.ks_slot + kv * g.ks_head, g.vs + slot * g.vs_slot + kv * g.vs_head, g.ks_row, g.vs_row,
                        len < g.slot_rows ? len : g.slot_rows};
     const Keys before = {g.kp + kv * g.kp_head, g.vp + kv * g.vp_head, g.kp_row, g.vp_row, g.together ? g.prefix : 0};
-    j.q = g.q + slot * g.q_row + (int64_t)kv * g.group * g.q_head;
-    j.rows = g.group;
+    j.q = g.q + slot * g.q_row + (int64_t)kv * g.group.d * g.q_head;
+    j.rows = (int)g.group.d;
     j.keys = INT32_MAX;   // the runs end themselves
-    const int rows = g.group - j.row0 < attn::kWaveRows ? g.group - j.row0 : attn::kWaveRows;
+    const int rows = j.rows - j.row0 < attn::kWaveRows ? j.rows - j.row0 : attn::kWaveRows;
     const int own_n = attn::key_blocks(mine.keys);
-    const int64_t x0 = slot * g.heads + kv * g.group + j.row0;
+    const int64_t x0 = slot * g.heads + kv * j.rows + j.row0;
     int part = split, block0, block1;
     if (g.together) {
-        const int n = attn::key_blocks(g.prefix) + own_n;
-        block0 = (int)((int64_t)n * split / splits);
-        block1 = (int)((int64_t)n * (split + 1) / splits);
+        const Range r = part_of(attn::key_blocks(g.prefix) + own_n, splits, split);
+        block0 = r.first;
+        block1 = r.last;
     } else {
-        part += g.prefix_splits;
+        part += (int)g.prefix_splits.d;
         block0 = split * g.own_blocks;
         block1 = block0 + g.own_blocks < own_n ? block0 + g.own_blocks : own_n;
         if (block0 >= block1) {   // the slot is not that long
@@ -348,8 +383,8 @@ __global__ __launch_bounds__(kThreads, 2) void shared_kernel(const SharedArgs g)
     const Row row = attn::row_of(j, j.row0 + (lane & 31));
     attn::run_blocks<T, D>(j, before, mine, block0, block1, row, smem, st);
     attn::merge_waves<D>(st, row.valid, rows, g.d, smem, [&](int r, int e, float m, float l, f32x4 o) {
-        if (g.prefix_splits + g.own_splits == 1)
-            attn::store_row4<T>(g.o + slot * g.o_row + (int64_t)(kv * g.group + j.row0 + r) * g.o_head,
+        if (g.parts_of_row == 1)
+            attn::store_row4<T>(g.o + slot * g.o_row + (int64_t)(kv * j.rows + j.row0 + r) * g.o_head,
                                 g.lse == nullptr ? nullptr : g.lse + x0 + r, e, m, l, o);
         else
             attn::store_part4(g.parts, part, x0 + r, g.d, e, m, l, o);
@@ -364,7 +399,7 @@ __global__ __launch_bounds__(kThreads) void shared_join_kernel(const SharedArgs 
     const int64_t b = x / g.heads;
     const bool there = b < g.batch && e < g.d && g.lens[b] >= 0;
     const int64_t head = x - b * g.heads;
-    attn::join_row<T, GROUPS>(g.parts, g.prefix_splits + g.own_splits, there, x, g.d, e, g.o + b * g.o_row + head * g.o_head,
+    attn::join_row<T, GROUPS>(g.parts, g.parts_of_row, there, x, g.d, e, g.o + b * g.o_row + head * g.o_head,
                               g.lse == nullptr ? nullptr : g.lse + x);
 }
 
@@ -526,44 +561,66 @@ int check_shared(const attn_shared_prefix_desc* d)
 // ----------------------------------------------------------------- plans
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-#ifndef PT
-#define PT 32
-#endif
-#ifndef MINB
-#define MINB 16
-#define MAXB 64
-#define TB 32
-#define TN 8
-#endif
-constexpr int64_t kMinBlocks = MINB;
-constexpr int64_t kMaxBlocks = MAXB;
-constexpr int64_t kTogetherBlocks = TB, kTogetherBatch = TN;
-
 struct PromptPlan {
-    int64_t tiles, splits, part_bytes;
+    int64_t waves, tiles, splits, part_bytes;
 };
 
 // Row tiles of one kv head: a packed batch has at most one ragged tile for
 // each sequence.  Where all tiles of all kv heads leave compute units without
-// work, the keys are split.
+// work, the keys are split, at least 256 of them to a part.
+//
+// Eight waves share a tile of K and V where workgroups are long: they read
+// half as many bytes into LDS, but a compute unit then holds one workgroup,
+// and nothing runs beside its beginning and end.  Measured on MI355X, eight
+// against four: 16384 tokens 1915 against 1960 us, 4096 148 against 155, 512
+// against 20000 keys 189 against 197; packed lengths of 1 to 2900 (16 tiles
+// of keys to a workgroup on average) 143 against 135, heads of 64 elements
+// (three workgroups of four waves to a compute unit) 155 against 153.
+constexpr int64_t kLongTiles = 24;
+
 PromptPlan plan_prompt(const attn_prompt_desc* d, int cus)
 {
     PromptPlan p;
     const int64_t group = d->heads / d->kv_heads;
     const int64_t seqs = d->batch < d->total_q ? d->batch : d->total_q;   // with a query
-    p.tiles = d->total_q * group / kTileRows + seqs;
-    const int64_t blocks = p.tiles * d->kv_heads;
-    const int64_t key_tiles = ceil_div(ceil_div(d->total_k, seqs), kTileKeys);
-    int64_t s = blocks >= cus ? 1 : 2 * cus / blocks;
-    if (s > key_tiles / 4) s = key_tiles / 4;
-    p.splits = s < 1 ? 1 : s;
+    const int64_t keys = ceil_div(d->total_k, seqs), queries = ceil_div(d->total_q, seqs);
+    auto plan = [&](int64_t waves) {
+        p.waves = waves;
+        p.tiles = d->total_q * group / (waves * attn::kWaveRows) + seqs;
+        const int64_t wgs = p.tiles * d->kv_heads, slots = waves == attn::kWaves ? 2 * cus : cus;
+        int64_t s = wgs >= cus ? 1 : slots / wgs;
+        if (s > keys / (4 * kTileKeys)) s = keys / (4 * kTileKeys);
+        p.splits = s < 1 ? 1 : s;
+    };
+    plan(2 * attn::kWaves);
+    const int64_t seen = d->causal ? keys - (queries < keys ? queries : keys) / 2 : keys;   // of a row, about
+    if (d->head_dim <= 64 || queries * group < 2 * kTileRows || seen < kLongTiles * kTileKeys * p.splits) plan(attn::kWaves);
     p.part_bytes = p.splits > 1 ? p.splits * d->total_q * d->heads * (d->head_dim + 2) * 4 : 0;
     return p;
 }
 
+// A row's keys come in parts: of the prefix, which row tiles of all slots'
+// rows (128, or up to 32 by the few-rows way) run through, and of its own
+// slot.  Where that needs no split (splits == 1 below) a slot's rows take a
+// short prefix and their own keys as one run instead, without a joining
+// launch: 3 x 500 + 64 keys 10.1 against 12.8 us, 32 x 200 + 100 8.6 against
+// 14.8, 64 x 500 + 500 20.6 against 22.5; with a split and for longer
+// prefixes the other way was faster (8 x 1000 + 300 14.1 against 15.1,
+// 4 x 8000 + 100 14.8 against 18.4).  One sequence alone has nobody to share
+// with.
+constexpr int64_t kMinBlocks = 16;      // of 32 keys, for a part
+constexpr int64_t kMaxBlocks = 64;      // of a slot's part, so that long and short slots even out
+constexpr int64_t kTogetherBlocks = 16;
+
 struct SharedPlan {
-    int64_t together, row_tiles, own_tiles, prefix_splits, own_splits, own_blocks, prefix_wgs, own_wgs, rounds, round_prefix, round_own,
-        part_bytes;
+    bool together;              // prefix and own keys as one run
+    int64_t row_tiles;          // of the prefix: batch * group rows in tiles of 128, or of 32 where that is all
+    int64_t own_tiles;          // of a slot: group rows in tiles of 32
+    int64_t prefix_splits;      // parts of the prefix, or of the one run
+    int64_t own_splits;         // parts of a slot, of own_blocks blocks of 32 keys each
+    int64_t own_blocks;
+    int64_t prefix_wgs, own_wgs, rounds, round_prefix, round_own;   // see shared_kernel
+    int64_t part_bytes;
 };
 
 SharedPlan plan_shared(const attn_shared_prefix_desc* d, int cus)
@@ -573,24 +630,26 @@ SharedPlan plan_shared(const attn_shared_prefix_desc* d, int cus)
     const int64_t prefix_blocks = ceil_div(d->prefix, attn::kBlockKeys), slot_blocks = ceil_div(d->slot_rows, attn::kBlockKeys);
     p.own_tiles = ceil_div(group, attn::kWaveRows);
     const int64_t jobs = d->batch * d->kv_heads * p.own_tiles;
-    p.together = d->batch == 1 || prefix_blocks == 0 || (prefix_blocks <= kTogetherBlocks && d->batch <= kTogetherBatch);
+    const int64_t run_want = 2 * cus / jobs, run_most = (prefix_blocks + slot_blocks) / kMinBlocks;
+    const int64_t run_splits = run_want < run_most ? run_want : run_most;
+    p.together = d->batch == 1 || prefix_blocks == 0 || (run_splits <= 1 && prefix_blocks <= kTogetherBlocks);
     if (p.together) {
-        const int64_t n = prefix_blocks + slot_blocks, most = n / kMinBlocks;
-        const int64_t want = 2 * cus / jobs;
-        p.prefix_splits = want < most ? want : most;
-        if (p.prefix_splits < 1) p.prefix_splits = 1;
+        p.prefix_splits = run_splits < 1 ? 1 : run_splits;
         p.own_wgs = jobs * p.prefix_splits;
     } else {
         const bool few = rows <= attn::kWaveRows;
         p.row_tiles = few ? 1 : ceil_div(rows, kTileRows);
-        const int64_t want = ceil_div(2 * cus, p.row_tiles * d->kv_heads), most = ceil_div(prefix_blocks, few ? kMinBlocks : PT);
+        // a part of the prefix in row tiles takes about as long as the slots'
+        // own keys do together, at some 0.8 us for 64 keys and 5.5 TB/s, but 4
+        // to 16 tiles of keys: fewer parts are joined sooner
+        const double own_us = (double)d->batch * d->slot_rows * d->kv_heads * d->head_dim * 4 / 5.5e6;
+        const int64_t tiles = own_us < 4 ? 4 : own_us > 16 ? 16 : (int64_t)own_us;
+        const int64_t want = ceil_div(2 * cus, p.row_tiles * d->kv_heads), most = ceil_div(prefix_blocks, few ? kMinBlocks : 2 * tiles);
         p.prefix_splits = want < most ? want : most;
         p.prefix_wgs = p.row_tiles * d->kv_heads * p.prefix_splits;
-        const int64_t own_want = ceil_div(2 * cus, jobs);
-        int64_t per = ceil_div(slot_blocks, own_want);   // blocks of a part
-        per = per < kMinBlocks ? kMinBlocks : per > kMaxBlocks ? kMaxBlocks : per;
-        p.own_blocks = per;
-        p.own_splits = ceil_div(slot_blocks, per);
+        const int64_t per = ceil_div(slot_blocks, ceil_div(2 * cus, jobs));
+        p.own_blocks = per < kMinBlocks ? kMinBlocks : per > kMaxBlocks ? kMaxBlocks : per;
+        p.own_splits = ceil_div(slot_blocks, p.own_blocks);
         p.own_wgs = jobs * p.own_splits;
     }
     p.round_prefix = p.prefix_wgs < cus ? p.prefix_wgs : cus;
@@ -612,10 +671,10 @@ Parts parts_in(void* ws, int64_t splits, int64_t rows)
 }
 int64_t parts_total(int64_t part_bytes) { return part_bytes == 0 ? 0 : part_bytes + 16; }
 
-int launch(const void* f, int64_t blocks, const void* args, hipStream_t s)
+int launch(const void* f, int64_t wgs, int threads, const void* args, hipStream_t s)
 {
     void* a[] = {const_cast<void*>(args)};
-    return hipLaunchKernel(f, dim3((unsigned)blocks), dim3(kThreads), a, 0, s) == hipSuccess ? GEMM_F16_NT_OK : GEMM_F16_NT_LAUNCH;
+    return hipLaunchKernel(f, dim3((unsigned)wgs), dim3(threads), a, 0, s) == hipSuccess ? GEMM_F16_NT_OK : GEMM_F16_NT_LAUNCH;
 }
 
 // The instantiation for a type and head size.
@@ -625,13 +684,20 @@ const void* pick(int dtype, int64_t d)
     if (dtype == ATTN_F16) return d <= 64 ? K<F16, 64>::f() : d <= 96 ? K<F16, 96>::f() : K<F16, 128>::f();
     return d <= 64 ? K<BF16, 64>::f() : d <= 96 ? K<BF16, 96>::f() : K<BF16, 128>::f();
 }
-template <typename T, int D>
-struct PromptWhole {
-    static const void* f() { return (const void*)&prompt_kernel<T, D, false>; }
-};
-template <typename T, int D>
-struct PromptSplit {
-    static const void* f() { return (const void*)&prompt_kernel<T, D, true>; }
+template <bool SPLIT>
+struct Prompt {
+    template <typename T, int D>
+    struct Short {
+        static const void* f() { return (const void*)&prompt_kernel<T, D, SPLIT, attn::kWaves>; }
+    };
+    template <typename T, int D>
+    struct Long {   // heads of up to 64 elements have no eight-wave form
+        static const void* f() { return (const void*)&prompt_kernel<T, D == 64 ? 96 : D, SPLIT, 2 * attn::kWaves>; }
+    };
+    static const void* f(const attn_prompt_desc* d, int64_t waves)
+    {
+        return waves == attn::kWaves ? pick<Short>(d->dtype, d->head_dim) : pick<Long>(d->dtype, d->head_dim);
+    }
 };
 template <typename T, int D>
 struct SharedParts {
@@ -710,24 +776,28 @@ int attn_prompt(const attn_prompt_desc* d, void* workspace, int64_t workspace_by
     g.total_k = (int)d->total_k;
     g.heads = d->heads;
     g.kv_heads = d->kv_heads;
-    g.group = d->heads / d->kv_heads;
+    g.group = attn::div_by(d->heads / d->kv_heads);
     g.d = d->head_dim;
     g.causal = d->causal;
-    g.tiles = (int)p.tiles;
-    g.splits = (int)p.splits;
+    const int64_t units = d->kv_heads * p.splits;
+    g.by_xcd = units % kNumXcd == 0;
+    g.units = attn::div_by(g.by_xcd ? units / kNumXcd : units);
+    g.splits = attn::div_by(p.splits);
+    g.join_kv = attn::div_by(d->kv_heads);
     g.c = sc.c;
     g.flip = sc.flip;
     g.zero_q = sc.zero;
     g.parts = parts_in(workspace, p.splits, d->total_q * d->heads);
-    const int64_t blocks = p.tiles * d->kv_heads * p.splits;
+    const int64_t wgs = p.tiles * units;
     int64_t join_rows = 0;
     const void* join = pick_join<PromptJoin>(d->dtype, p.splits, &join_rows);
-    const int64_t join_wgs = p.tiles * d->kv_heads * (kTileRows / join_rows);
-    if (blocks > INT_MAX || (p.splits > 1 && join_wgs > INT_MAX)) return GEMM_F16_NT_UNSUPPORTED;
+    const int64_t join_wgs = (d->total_q * g.group.d / kTileRows + d->batch) * d->kv_heads * (kTileRows / join_rows);
+    if (wgs > INT_MAX || (p.splits > 1 && join_wgs > INT_MAX)) return GEMM_F16_NT_UNSUPPORTED;
     const hipStream_t s = (hipStream_t)stream;
-    if (p.splits == 1) return launch(pick<PromptWhole>(d->dtype, d->head_dim), blocks, &g, s);
-    if ((st = launch(pick<PromptSplit>(d->dtype, d->head_dim), blocks, &g, s)) != GEMM_F16_NT_OK) return st;
-    return launch(join, join_wgs, &g, s);
+    const int threads = 64 * (int)p.waves;
+    if (p.splits == 1) return launch(Prompt<false>::f(d, p.waves), wgs, threads, &g, s);
+    if ((st = launch(Prompt<true>::f(d, p.waves), wgs, threads, &g, s)) != GEMM_F16_NT_OK) return st;
+    return launch(join, join_wgs, kThreads, &g, s);
 }
 
 int attn_shared_prefix_check(const attn_shared_prefix_desc* d) { return check_shared(d); }
@@ -778,31 +848,34 @@ int attn_shared_prefix(const attn_shared_prefix_desc* d, void* workspace, int64_
     g.prefix = (int)d->prefix;
     g.slot_rows = (int)d->slot_rows;
     g.heads = d->heads;
-    g.kv_heads = d->kv_heads;
-    g.group = d->heads / d->kv_heads;
     g.d = d->head_dim;
+    g.group = attn::div_by(d->heads / d->kv_heads);
+    g.kv_heads = attn::div_by(d->kv_heads);
     g.together = (int)p.together;
-    g.row_tiles = (int)p.row_tiles;
-    g.own_tiles = (int)p.own_tiles;
-    g.prefix_splits = (int)p.prefix_splits;
-    g.own_splits = (int)p.own_splits;
+    g.row_tiles = attn::div_by(p.row_tiles);
+    g.own_tiles = attn::div_by(p.own_tiles);
+    g.prefix_splits = attn::div_by(p.prefix_splits);
+    g.own_splits = attn::div_by(p.own_splits);
+    g.parts_of_row = (int)(p.prefix_splits + p.own_splits);
     g.own_blocks = (int)p.own_blocks;
     g.prefix_wgs = (uint32_t)p.prefix_wgs;
     g.own_wgs = (uint32_t)p.own_wgs;
     g.round_prefix = (uint32_t)p.round_prefix;
     g.round_own = (uint32_t)p.round_own;
+    g.round = attn::div_by(p.round_prefix + p.round_own);
+    g.by_xcd = d->kv_heads * p.prefix_splits % kNumXcd == 0;
     g.c = sc.c;
     g.flip = sc.flip;
     g.zero_q = sc.zero;
     g.parts = parts_in(workspace, p.prefix_splits + p.own_splits, d->batch * d->heads);
-    const int64_t blocks = p.rounds * (p.round_prefix + p.round_own);
-    if (blocks > INT_MAX) return GEMM_F16_NT_UNSUPPORTED;
+    const int64_t wgs = p.rounds * (p.round_prefix + p.round_own);
+    if (wgs > INT_MAX) return GEMM_F16_NT_UNSUPPORTED;
     const hipStream_t s = (hipStream_t)stream;
-    st = launch(pick<SharedParts>(d->dtype, d->head_dim), blocks, &g, s);
+    st = launch(pick<SharedParts>(d->dtype, d->head_dim), wgs, kThreads, &g, s);
     if (st != GEMM_F16_NT_OK || p.part_bytes == 0) return st;
     int64_t join_rows = 0;
     const void* join = pick_join<SharedJoin>(d->dtype, p.prefix_splits + p.own_splits, &join_rows);
-    return launch(join, ceil_div(d->batch * d->heads, join_rows), &g, s);
+    return launch(join, ceil_div(d->batch * d->heads, join_rows), kThreads, &g, s);
 }
 
 }  // extern "C"

@@ -25,6 +25,8 @@
 // weight, as for V itself); the denominator adds the unrounded p.
 #pragma once
 
+#include <utility>
+
 #include "common.hpp"
 
 namespace g16 {
@@ -55,11 +57,6 @@ struct F16 {
     {
         return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2){x, y}, f16x2));
     }
-    // s + the two halves of p
-    static __device__ __forceinline__ float sum2(uint32_t p, float s)
-    {
-        return __builtin_amdgcn_fdot2(__builtin_bit_cast(f16x2, p), f16x2{(_Float16)1.f, (_Float16)1.f}, s, false);
-    }
 };
 
 struct BF16 {
@@ -70,10 +67,6 @@ struct BF16 {
     static __device__ __forceinline__ uint32_t pack(float x, float y)
     {
         return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2){x, y}, bf16x2));
-    }
-    static __device__ __forceinline__ float sum2(uint32_t p, float s)
-    {
-        return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, p), bf16x2{(__bf16)1.f, (__bf16)1.f}, s, false);
     }
 };
 
@@ -126,7 +119,30 @@ __device__ __forceinline__ float sum_halves(float x)
     return __builtin_bit_cast(float, (uint32_t)r[0]) + __builtin_bit_cast(float, (uint32_t)r[1]);
 }
 
-// What a workgroup computes: kTileRows rows from row0 on of a sequence's
+// Division by a number that a launch knows (Granlund and Montgomery, "Division
+// by invariant integers using multiplication", PLDI 1994): n / d for n < 2^31
+// is the high half of n * mul, shifted.  A division of two registers costs
+// some 40 instructions, and a short prompt's workgroup is mostly such work.
+struct Div {
+    uint32_t d, mul, shift;
+    __host__ __device__ __forceinline__ uint32_t of(uint32_t n) const
+    {
+        return d < 2 ? n : (uint32_t)(((uint64_t)n * mul) >> 32) >> shift;
+    }
+};
+
+inline Div div_by(int64_t by)
+{
+    Div x = {(uint32_t)by, 0, 0};
+    if (x.d < 2) return x;
+    uint32_t bits = 0;
+    while ((uint64_t(1) << bits) < x.d) ++bits;   // 2^bits >= d
+    x.mul = (uint32_t)((uint64_t(1) << (31 + bits)) / x.d + 1);
+    x.shift = bits - 1;
+    return x;
+}
+
+// What a workgroup computes: rows from row0 on of a sequence's
 // `rows` = tokens * group rows for one kv head (row r: token r / group, query
 // head r % group of the kv head), against keys [64 tile0, 64 tile1).
 struct Job {
@@ -134,7 +150,8 @@ struct Job {
     const char* k;       // key 0 of the kv head
     const char* v;
     int64_t q_token, q_head, k_row, v_row;   // strides in bytes
-    int rows, row0, group;
+    int rows, row0;
+    Div group;
     int keys;            // keys of the sequence
     int lead;            // causal: row's keys are [0, token + lead + 1); otherwise INT32_MAX
     int most;            // keys that the last row may read
@@ -157,15 +174,17 @@ __device__ __forceinline__ Row row_of(const Job& j, int r)
     Row x;
     x.valid = r < j.rows;
     const int rr = x.valid ? r : 0;
-    x.token = (int)((uint32_t)rr / (uint32_t)j.group);
-    x.head = rr - x.token * j.group;
+    x.token = (int)j.group.of(rr);
+    x.head = rr - x.token * (int)j.group.d;
     // a row that is not there masks nothing; its output is not stored
     const int64_t lim = j.lead == INT32_MAX ? (int64_t)j.keys : (int64_t)x.token + j.lead + 1;
     x.limit = !x.valid ? INT32_MAX : (int)(lim < 0 ? 0 : lim < j.keys ? lim : j.keys);
     return x;
 }
 
-// The wave's Q fragments: lane l holds row l % 32, elements 16 s + 8 (l / 32) .. + 7.
+// The wave's Q fragments: lane l holds row l % 32, elements 16 s + 8 (l / 32)
+// .. + 7.  Rows that are not there and elements behind the head size are read
+// as ones that are and cleared, so that all loads are in flight together.
 template <int D>
 __device__ __forceinline__ void load_q(const Job& j, const Row& row, int half, u32x4 (&q)[Shape<D>::KSTEPS])
 {
@@ -173,17 +192,17 @@ __device__ __forceinline__ void load_q(const Job& j, const Row& row, int half, u
 #pragma unroll
     for (int s = 0; s < Shape<D>::KSTEPS; ++s) {
         const int e = 16 * s + 8 * half;
-        u32x4 x = {0, 0, 0, 0};
-        if (row.valid && e < j.d && !j.zero_q) {
-            x = *reinterpret_cast<const u32x4*>(p + 2 * e);
+        q[s] = *reinterpret_cast<const u32x4*>(p + (e < j.d ? 2 * e : 0));
+    }
 #pragma unroll
-            for (int i = 0; i < 4; ++i) x[i] ^= j.flip;
-        }
-        q[s] = x;
+    for (int s = 0; s < Shape<D>::KSTEPS; ++s) {
+        const uint32_t keep = row.valid && 16 * s + 8 * half < j.d && !j.zero_q ? 0xffffffffu : 0u;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) q[s][i] = (q[s][i] & keep) ^ j.flip;
     }
 }
 
-// 16 bytes a lane from a buffer to LDS, lane i's at dst + 16 i.  Written as
+// 16 bytes a lane from a buffer to LDS, lane i's at dst + AT + 16 i.  Written as
 // an instruction of its own, without registers that it could leave in
 // flight, because the compiler puts a wait for every outstanding
 // builtin load to LDS before each transposing read of LDS; the kernels wait
@@ -191,46 +210,59 @@ __device__ __forceinline__ void load_q(const Job& j, const Row& row, int half, u
 __device__ __forceinline__ uint32_t lds_address(const char* p) { return (uint32_t)(uintptr_t)(const G16_LDS char*)p; }
 #pragma clang diagnostic push
 #pragma clang diagnostic ignored "-Winline-asm"  // M0 is written inside, on purpose
+template <int AT>
 __device__ __forceinline__ void load_to_lds(u32x4 rs, uint32_t dst, uint32_t off)
 {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+    asm volatile("s_add_u32 m0, %0, %3\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
                  :
-                 : "s"(dst), "v"(off), "s"(rs)
-                 : "memory", "m0");
+                 : "s"(dst), "v"(off), "s"(rs), "n"(AT)
+                 : "memory", "m0", "scc");
 }
 #pragma clang diagnostic pop
 
-// A thread's part of a tile's loads into LDS: its place in the first
-// kThreads * 16 bytes of a tile, as a byte offset from the tile's first row.
-// Elements behind the head size lie past the end of every buffer.
-template <int D, bool IS_V>
-__device__ __forceinline__ uint32_t tile_offset(int64_t row_bytes, int d, int tid)
-{
+// The loads of a K or V tile after tile, by all threads of a workgroup.  The
+// buffer starts at a tile's first row and ends with its last one inside the
+// sequence, so rows behind it (another sequence's, or stale ones) arrive as
+// zeros whatever memory holds, and so do the elements behind the head size,
+// whose offset lies past the end of every buffer.  The base moves in 64 bits
+// from tile to tile; offsets stay below 2^31.
+template <int D, int W>
+struct Loader {
     using S = Shape<D>;
-    const int r = tid / S::CHUNKS, pc = tid % S::CHUNKS;
-    const int lc = pc ^ (IS_V ? swz_v<D>(r) : swz_k<D>(r));   // both repeat every 16 rows
-    return lc * 8 < d ? (uint32_t)r * (uint32_t)row_bytes + (uint32_t)lc * 16u : 0x80000000u;
-}
+    static constexpr int THREADS = 64 * W, LOADS = S::TILE / (THREADS * 16), LOAD_ROWS = THREADS / S::CHUNKS;
+    uint32_t off[LOADS];   // a thread's 16 bytes from the tile's first row on
+    uint64_t at;              // the next tile
+    int left;                 // keys from there on
+    uint32_t row_bytes, last; // bytes from a row to the next, and of a row's head
 
-// A tile's loads, by all threads of the workgroup.  The buffer starts at the
-// tile's first row and ends with its last one inside the sequence, so rows
-// behind it (another sequence's, or stale ones) arrive as zeros whatever
-// memory holds; the base moves in 64 bits from tile to tile and offsets stay
-// below 2^31 (0x80000000 for what is past the head size).
-template <int D>
-__device__ __forceinline__ void load_tile(const char* base, int64_t row_bytes, int keys, int tile, int d, uint32_t off,
-                                          uint32_t dst)
-{
-    using S = Shape<D>;
-    const int key0 = tile * kTileKeys;
-    const int n = keys - key0 < kTileKeys ? keys - key0 : kTileKeys;
-    const uint32_t bytes = n > 0 ? (uint32_t)(n - 1) * (uint32_t)row_bytes + 2u * (uint32_t)d : 0u;
-    const uint64_t at = (uint64_t)(base + (int64_t)key0 * row_bytes);
-    const u32x4 rs = {(uint32_t)at, (uint32_t)(at >> 32) & 0xffffu, bytes, 0x00020000u};
+    __device__ __forceinline__ void start(const char* base, int64_t pitch, int keys, int tile, int d, int tid, bool v)
+    {
+        const int r = tid / S::CHUNKS, pc = tid % S::CHUNKS;
+        const int lc = pc ^ (v ? swz_v<D>(r) : swz_k<D>(r));   // both repeat every 16 rows
+        row_bytes = (uint32_t)pitch;
+        last = 2u * (uint32_t)d;
 #pragma unroll
-    for (int i = 0; i < S::LOADS; ++i)
-        load_to_lds(rs, dst + i * (kThreads * 16), off + (uint32_t)(i * S::LOAD_ROWS) * (uint32_t)row_bytes);
-}
+        for (int i = 0; i < LOADS; ++i)
+            off[i] = lc * 8 < d ? (uint32_t)(r + i * LOAD_ROWS) * row_bytes + (uint32_t)lc * 16u : 0x80000000u;
+        at = (uint64_t)(base + (int64_t)tile * kTileKeys * pitch);
+        left = keys - tile * kTileKeys;
+    }
+    template <int... I>
+    __device__ __forceinline__ void issue(u32x4 rs, uint32_t dst, std::integer_sequence<int, I...>)
+    {
+        (load_to_lds<I * THREADS * 16>(rs, dst, off[I]), ...);
+    }
+    // the next tile into the buffer at dst (the wave's first 1024 bytes of it)
+    __device__ __forceinline__ void next(uint32_t dst)
+    {
+        const int n = left < kTileKeys ? left : kTileKeys;
+        const uint32_t bytes = n > 0 ? (uint32_t)(n - 1) * row_bytes + last : 0u;
+        issue(u32x4{(uint32_t)at, (uint32_t)(at >> 32) & 0xffffu, bytes, 0x00020000u}, dst,
+              std::make_integer_sequence<int, LOADS>());
+        at += (uint64_t)kTileKeys * row_bytes;
+        left -= kTileKeys;
+    }
+};
 
 // A lane's LDS addresses: of the fragments of a K tile's first 32 rows, and of
 // the transposing reads of a V tile's first rows.  The steps add constants.
@@ -311,14 +343,25 @@ __device__ __forceinline__ void init(State<D>& st)
     for (int b = 0; b < Shape<D>::DBLOCKS; ++b) st.o[b] = f32x16{};
 }
 
-// The maximum of a row's scores (of 32 keys for each block), in the units of m.
+// The maximum of a row's scores (of 32 keys for each block), in the units of
+// m.  A tree: a chain would wait for each instruction's result in turn.
 template <int N>
 __device__ __forceinline__ float top_score(const f32x16 (&s)[N], float c)
 {
-    float mx = s[0][0];
+    float a[5 * N], b = s[0][15];
 #pragma unroll
-    for (int i = 1; i < 16 * N - 1; i += 2) mx = max3(mx, s[i / 16][i % 16], s[(i + 1) / 16][(i + 1) % 16]);
-    return max_halves(__builtin_fmaxf(mx, s[N - 1][15])) * c;
+    for (int i = 0; i < N; ++i) {
+#pragma unroll
+        for (int k = 0; k < 5; ++k) a[5 * i + k] = max3(s[i][3 * k], s[i][3 * k + 1], s[i][3 * k + 2]);
+        b = i == 0 ? b : __builtin_fmaxf(b, s[i][15]);
+    }
+    if constexpr (N == 1) {
+        b = max3(b, max3(a[0], a[1], a[2]), __builtin_fmaxf(a[3], a[4]));
+    } else {
+        const float x = max3(a[0], a[1], a[2]), y = max3(a[3], a[4], a[5]), z = max3(a[6], a[7], a[8]);
+        b = max3(b, a[9], max3(x, y, z));
+    }
+    return max_halves(b) * c;
 }
 
 // Raises a row's maximum where a tile's asks for it, and rescales what was
@@ -338,27 +381,34 @@ __device__ __forceinline__ void raise(float mx, State<D>& st)
 }
 
 // Softmax weights of 32 keys: P^T as B operands p[kk] of the keys 16 kk ..
-// 16 kk + 15, and their sum.
-template <typename T, int D>
+// 16 kk + 15, and their sum (of the weights before their rounding: the
+// log-sum-exp has to hold in fp32).  LEAN takes them pair by pair, which costs
+// a little time (16384 tokens, d 128: 1924 against 1877 us) and saves the
+// registers that let three waves share a SIMD for d 64 (154 against 183;
+// 4096 tokens, 32 heads: 154 against 159 us).
+template <typename T, int D, bool LEAN = false>
 __device__ __forceinline__ void weights(const f32x16& s, float c, State<D>& st, u32x4 (&p)[2])
 {
     const float base = st.m == -__builtin_inff() ? 0.f : kShift - st.m;
+    auto weight = [&](int i) { return exp2_(__builtin_fmaf(s[i], c, base)); };
+    if constexpr (LEAN) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        float e[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) e[i] = exp2_(__builtin_fmaf(s[8 * h + i], c, base));
-#if DOT2
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            p[h][i] = T::pack(e[2 * i], e[2 * i + 1]);
-            st.l = T::sum2(p[h][i], st.l);
+        for (int i = 0; i < 8; ++i) {
+            const float x = weight(2 * i), y = weight(2 * i + 1);
+            p[i / 4][i % 4] = T::pack(x, y);
+            st.l += x + y;
+            if (i % 2 == 1) asm volatile("" : "+v"(st.l));   // not put off
         }
-#else
-        st.l += ((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7]));
+    } else {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) p[h][i] = T::pack(e[2 * i], e[2 * i + 1]);
-#endif
+        for (int h = 0; h < 2; ++h) {
+            float e[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) e[i] = weight(8 * h + i);
+            st.l += ((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7]));
+#pragma unroll
+            for (int i = 0; i < 4; ++i) p[h][i] = T::pack(e[2 * i], e[2 * i + 1]);
+        }
     }
 }
 
@@ -393,26 +443,26 @@ constexpr int lds_bytes()
 // All tiles of a job; the four waves share the K and V tiles.  Tile t + 1 of
 // K and t of V are in LDS when iteration t begins; K t + 2 and V t + 1 are
 // loaded while it runs.
-template <typename T, int D>
+template <typename T, int D, int W>
 __device__ __forceinline__ void run_tiles(const Job& j, const Row& row, char* smem, State<D>& st)
 {
     using S = Shape<D>;
     const int tid = threadIdx.x, lane = tid & 63, half = lane >> 5;
-    u32x4 q[S::KSTEPS];
-    load_q<D>(j, row, half, q);
     init(st);
     if (j.tile0 >= j.tile1) return;
     const int first_limit = __builtin_amdgcn_readfirstlane(row.limit);   // the wave's smallest
     const uint32_t lds = lds_address(smem);
     const Reads<D> x = reads_of<D>(lds, lane);
-    const uint32_t koff = tile_offset<D, false>(j.k_row, j.d, tid), voff = tile_offset<D, true>(j.v_row, j.d, tid);
     const uint32_t dst = lds + __builtin_amdgcn_readfirstlane(tid >> 6) * 1024;
     constexpr uint32_t K0 = 0, V0 = 2 * S::TILE, HALF = S::TILE / 2;
-    auto load_k = [&](int t, uint32_t par) { load_tile<D>(j.k, j.k_row, j.keys, t, j.d, koff, dst + K0 + par * S::TILE); };
-    auto load_v = [&](int t, uint32_t par) { load_tile<D>(j.v, j.v_row, j.keys, t, j.d, voff, dst + V0 + par * S::TILE); };
-    load_k(j.tile0, 0);
-    load_v(j.tile0, 0);
-    if (j.tile0 + 1 < j.tile1) load_k(j.tile0 + 1, 1);
+    Loader<D, W> k, v;
+    k.start(j.k, j.k_row, j.keys, j.tile0, j.d, tid, false);
+    v.start(j.v, j.v_row, j.keys, j.tile0, j.d, tid, true);
+    k.next(dst + K0);
+    v.next(dst + V0);
+    if (j.tile0 + 1 < j.tile1) k.next(dst + K0 + S::TILE);
+    u32x4 q[S::KSTEPS];
+    load_q<D>(j, row, half, q);
     publish();
     f32x16 cur[2], next[2];
     cur[0] = scores<T, D>(x, K0, q);
@@ -420,9 +470,9 @@ __device__ __forceinline__ void run_tiles(const Job& j, const Row& row, char* sm
     auto step = [&](int t, uint32_t par, f32x16 (&a)[2], f32x16 (&b)[2]) {
         // K t + 1 and V t have landed; K t and V t - 1 have been read
         publish();
-        if (t + 2 < j.tile1) load_k(t + 2, par);
+        if (t + 2 < j.tile1) k.next(dst + K0 + par * S::TILE);
         if (t + 1 < j.tile1) {
-            load_v(t + 1, 1 - par);
+            v.next(dst + V0 + (1 - par) * S::TILE);
             b[0] = scores<T, D>(x, K0 + (1 - par) * S::TILE, q);
             b[1] = scores<T, D>(x, K0 + (1 - par) * S::TILE + HALF, q);
         }
@@ -433,8 +483,8 @@ __device__ __forceinline__ void run_tiles(const Job& j, const Row& row, char* sm
         const float mx = top_score(a, j.c);
         if (__builtin_amdgcn_ballot_w64(mx > st.m + kSlack) != 0) raise<D>(mx, st);
         u32x4 p0[2], p1[2];
-        weights<T, D>(a[0], j.c, st, p0);
-        weights<T, D>(a[1], j.c, st, p1);
+        weights<T, D, D == 64>(a[0], j.c, st, p0);
+        weights<T, D, D == 64>(a[1], j.c, st, p1);
         accumulate<T, D>(x, V0 + par * S::TILE, p0, st);
         accumulate<T, D>(x, V0 + par * S::TILE + HALF, p1, st);
     };
@@ -474,8 +524,6 @@ __device__ __forceinline__ void run_blocks(const Job& j, const Keys& one, const 
     constexpr int COLS = S::CHUNKS == 16 ? 4 : 2;   // the swizzle of K differs from load to load, with this period
     constexpr uint32_t HALF = S::TILE / 2;
     const int lane = threadIdx.x & 63, half = lane >> 5, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    u32x4 q[S::KSTEPS];
-    load_q<D>(j, row, half, q);
     init(st);
     int at = block0 + w;
     if (at >= block1) return;
@@ -506,9 +554,11 @@ __device__ __forceinline__ void run_blocks(const Job& j, const Keys& one, const 
         const uint32_t off = (uint32_t)r * (uint32_t)row_bytes;
 #pragma unroll
         for (int i = 0; i < NL; ++i)
-            load_to_lds(rs, lds + (v ? HALF : 0) + i * 1024,
-                        off + (uint32_t)(i * ROWS) * (uint32_t)row_bytes + (v ? vcol : kcol[i % COLS]));
+            load_to_lds<0>(rs, lds + (v ? HALF : 0) + i * 1024,
+                           off + (uint32_t)(i * ROWS) * (uint32_t)row_bytes + (v ? vcol : kcol[i % COLS]));
     };
+    u32x4 q[S::KSTEPS];
+    load_q<D>(j, row, half, q);   // ahead of the blocks: the first wait is for these and K
     load(at, false);
     load(at, true);
     for (; at < block1; at += kWaves) {
@@ -554,40 +604,65 @@ __device__ __forceinline__ float lse_of(float m, float l)
     return l == 0.f ? -__builtin_inff() : (m - kShift + __builtin_log2f(l)) * kLn2;
 }
 
-// The row's O, normalised and rounded, and its log-sum-exp.
+// Calls f(e, block, group) for a lane's groups of accumulator registers that
+// lie inside the head size; e is group g's first element of the pair (g, g + STEP).
+template <int D, int STEP, typename F>
+__device__ __forceinline__ void each_group(int d, int half, F f)
+{
+    auto all = [&](auto whole) {
+#pragma unroll
+        for (int b = 0; b < Shape<D>::DBLOCKS; ++b)
+#pragma unroll
+            for (int g = 0; g < 4; g += STEP) {
+                const int e = 32 * b + 8 * g + (STEP == 2 ? 8 : 4) * half;
+                if (decltype(whole)::value || e < d) f(e, b, g);
+            }
+    };
+    if (d == D)   // the usual case, without a branch for each group
+        all(std::true_type());
+    else
+        all(std::false_type());
+}
+
+// The row's O, normalised and rounded, and its log-sum-exp.  Lanes l and
+// l + 32 hold the two halves of each 8 elements; they exchange halves of two
+// groups, so that each stores 16 bytes.
 template <typename T, int D>
-__device__ __forceinline__ void store_row(const State<D>& st, int d, char* o, float* lse, int half)
+__device__ __forceinline__ void store_row(const State<D>& st, bool valid, int d, char* o, float* lse, int half)
 {
     const float l = sum_halves(st.l), inv = inverse(l);
+    u32x4 x[Shape<D>::DBLOCKS][2];
 #pragma unroll
     for (int b = 0; b < Shape<D>::DBLOCKS; ++b)
 #pragma unroll
-        for (int g = 0; g < 4; ++g) {
-            const int e = 32 * b + 8 * g + 4 * half;
-            if (e < d)
-                store4<T>(o, e, f32x4{st.o[b][4 * g] * inv, st.o[b][4 * g + 1] * inv, st.o[b][4 * g + 2] * inv,
-                                      st.o[b][4 * g + 3] * inv});
-        }
+        for (int g = 0; g < 4; g += 2)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const f32x16& y = st.o[b];
+                const auto z = __builtin_amdgcn_permlane32_swap(
+                    T::pack(y[4 * g + 2 * i] * inv, y[4 * g + 2 * i + 1] * inv),
+                    T::pack(y[4 * g + 4 + 2 * i] * inv, y[4 * g + 5 + 2 * i] * inv), false, false);
+                x[b][g / 2][i] = z[0];
+                x[b][g / 2][i + 2] = z[1];
+            }
+    if (!valid) return;
+    each_group<D, 2>(d, half, [&](int e, int b, int g) { *reinterpret_cast<u32x4*>(o + 2 * e) = x[b][g / 2]; });
     if (lse != nullptr && half == 0) *lse = lse_of(st.m, l);
 }
 
 template <int D>
-__device__ __forceinline__ void store_part(const State<D>& st, int d, const Parts& w, int part, int64_t x, int half)
+__device__ __forceinline__ void store_part(const State<D>& st, bool valid, int d, const Parts& w, int part, int64_t x, int half)
 {
     const float l = sum_halves(st.l);
+    if (!valid) return;
     const int64_t at = (int64_t)part * w.n + x;
     if (half == 0) *reinterpret_cast<f32x2*>(w.ml + 2 * at) = f32x2{st.m, l};
     if (l == 0.f) return;   // no key: nothing reads this part's O
     float* o = w.o + at * d;
-#pragma unroll
-    for (int b = 0; b < Shape<D>::DBLOCKS; ++b)
-#pragma unroll
-        for (int g = 0; g < 4; ++g) {
-            const int e = 32 * b + 8 * g + 4 * half;
-            if (e < d)
-                *reinterpret_cast<f32x4*>(o + e) =
-                    f32x4{st.o[b][4 * g], st.o[b][4 * g + 1], st.o[b][4 * g + 2], st.o[b][4 * g + 3]};
-        }
+    each_group<D, 1>(d, half, [&](int e, int b, int g) {
+        const f32x16& y = st.o[b];
+        *reinterpret_cast<f32x4*>(o + e) = f32x4{y[4 * g], y[4 * g + 1], y[4 * g + 2], y[4 * g + 3]};
+    });
 }
 
 // Four elements of a row whose sums are complete: the output, or a part.
