@@ -11,6 +11,7 @@
 #include <climits>
 #include <cmath>
 #include <cstring>
+#include <initializer_list>
 
 #include "attn_core.hpp"
 #include "sched.hpp"
@@ -197,14 +198,18 @@ __global__ __launch_bounds__(64 * W, D == 64 && W == 4 ? 3 : 2) void prompt_kern
     const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     State<D> st;
     const int rows = j.rows - j.row0;
-    if (W == attn::kWaves && rows <= attn::kWaveRows) {
-        // the rows of one wave (a single token, a short chunk): all waves
+    if (rows <= attn::kWaveRows) {
+        // the rows of one wave (a single token, a short chunk): four waves
         // take them and divide the keys
         const Row row = attn::row_of(j, j.row0 + (lane & 31));
         const Keys keys = {j.k, j.v, j.k_row, j.v_row, j.keys}, none = {};
         const int n = attn::key_blocks(j.most);
         const Range r = SPLIT ? part_of(n, g.splits, split) : Range{0, n};
-        attn::run_blocks<T, D>(j, keys, none, r.first, r.last, row, smem, st);
+        attn::run_blocks<T, D, 2>(j, keys, none, r.first, r.last, row, smem, st);
+        if (g.causal && attn::spoilt<D>(st)) {
+            attn::landed<0>();
+            attn::run_blocks<T, D, 2, true>(j, keys, none, r.first, r.last, row, smem, st);
+        }
         attn::merge_waves<D>(st, row.valid, rows, g.d, smem, [&](int y, int e, float m, float l, f32x4 o) {
             const int x = j.row0 + y, token_in = (int)g.group.of(x);
             const int64_t token = (int64_t)tile.q0 + token_in;
@@ -223,6 +228,7 @@ __global__ __launch_bounds__(64 * W, D == 64 && W == 4 ? 3 : 2) void prompt_kern
     j.tile1 = r.last;
     const Row row = attn::row_of(j, j.row0 + w * attn::kWaveRows + (lane & 31));
     attn::run_tiles<T, D, W>(j, row, smem, st);
+    if (g.causal && attn::any_wave<W>(attn::spoilt<D>(st), smem)) attn::run_tiles_careful<T, D, W>(j, row, smem, st);
     const int64_t token = (int64_t)tile.q0 + row.token;
     const int head = kv * (int)g.group.d + row.head;
     if constexpr (SPLIT)
@@ -273,6 +279,7 @@ struct SharedArgs {
     int own_blocks;       // blocks of 32 keys each
     uint32_t prefix_wgs, own_wgs, round_prefix, round_own;
     int by_xcd;
+    int rounded;          // the prefix goes through row tiles
     float c;
     uint32_t flip;
     int zero_q;
@@ -329,7 +336,7 @@ __global__ __launch_bounds__(kThreads, 2) void shared_kernel(const SharedArgs g)
             const Row row = attn::row_of(j, lane & 31);
             const Keys keys = {j.k, j.v, j.k_row, j.v_row, j.keys}, none = {};
             const Range r = part_of(attn::key_blocks(g.prefix), g.prefix_splits, part);
-            attn::run_blocks<T, D>(j, keys, none, r.first, r.last, row, smem, st);
+            attn::run_blocks<T, D, 2>(j, keys, none, r.first, r.last, row, smem, st);
             attn::merge_waves<D>(st, row.valid, j.rows, g.d, smem, [&](int r, int e, float m, float l, f32x4 o) {
                 const int b = (int)g.group.of(r);
                 const int64_t x = (int64_t)b * g.heads + kv * (int)g.group.d + r - b * (int)g.group.d;
@@ -381,7 +388,11 @@ __global__ __launch_bounds__(kThreads, 2) void shared_kernel(const SharedArgs g)
         }
     }
     const Row row = attn::row_of(j, j.row0 + (lane & 31));
-    attn::run_blocks<T, D>(j, before, mine, block0, block1, row, smem, st);
+    // beside a prefix whose weights are rounded once, so are these
+    if (g.rounded)
+        attn::run_blocks<T, D, 1>(j, before, mine, block0, block1, row, smem, st);
+    else
+        attn::run_blocks<T, D, 2>(j, before, mine, block0, block1, row, smem, st);
     attn::merge_waves<D>(st, row.valid, rows, g.d, smem, [&](int r, int e, float m, float l, f32x4 o) {
         if (g.parts_of_row == 1)
             attn::store_row4<T>(g.o + slot * g.o_row + (int64_t)(kv * j.rows + j.row0 + r) * g.o_head,
@@ -512,7 +523,10 @@ int check_prompt(const attn_prompt_desc* d)
     if (d->Q == nullptr || d->O == nullptr || d->cu_q == nullptr || d->cu_k == nullptr) return GEMM_F16_NT_INVALID_ARG;
     if (d->total_k > 0 && (d->K == nullptr || d->V == nullptr)) return GEMM_F16_NT_INVALID_ARG;
     if (!rows_apart(d->total_q, d->o_row, d->heads, d->o_head, hd)) return GEMM_F16_NT_INVALID_ARG;
-    if (overlaps(d->O, eo, d->Q, eq) || overlaps(d->O, eo, d->K, ek) || overlaps(d->O, eo, d->V, ev))
+    const int64_t el = d->lse == nullptr ? 0 : d->total_q * d->heads * 4;
+    if (overlaps(d->O, eo, d->Q, eq) || overlaps(d->O, eo, d->K, ek) || overlaps(d->O, eo, d->V, ev) ||
+        overlaps(d->lse, el, d->O, eo) || overlaps(d->lse, el, d->Q, eq) || overlaps(d->lse, el, d->K, ek) ||
+        overlaps(d->lse, el, d->V, ev))
         return GEMM_F16_NT_INVALID_ARG;
     if (!aligned16(d->Q, {d->q_row, d->q_head}) || !aligned16(d->O, {d->o_row, d->o_head}) ||
         !aligned16(d->K, {d->k_row, d->k_head}) || !aligned16(d->V, {d->v_row, d->v_head}))
@@ -545,6 +559,10 @@ int check_shared(const attn_shared_prefix_desc* d)
     if (!rows_apart(d->batch, d->o_row, d->heads, d->o_head, hd)) return GEMM_F16_NT_INVALID_ARG;
     if (overlaps(d->O, eo, d->Q, eq) || overlaps(d->O, eo, d->Kp, ekp) || overlaps(d->O, eo, d->Vp, evp) ||
         overlaps(d->O, eo, d->Ks, eks) || overlaps(d->O, eo, d->Vs, evs))
+        return GEMM_F16_NT_INVALID_ARG;
+    const int64_t el = d->lse == nullptr ? 0 : d->batch * d->heads * 4;
+    if (overlaps(d->lse, el, d->O, eo) || overlaps(d->lse, el, d->Q, eq) || overlaps(d->lse, el, d->Kp, ekp) ||
+        overlaps(d->lse, el, d->Vp, evp) || overlaps(d->lse, el, d->Ks, eks) || overlaps(d->lse, el, d->Vs, evs))
         return GEMM_F16_NT_INVALID_ARG;
     if (!aligned16(d->Q, {d->q_row, d->q_head}) || !aligned16(d->O, {d->o_row, d->o_head}) ||
         !aligned16(d->Kp, {d->kp_row, d->kp_head}) || !aligned16(d->Vp, {d->vp_row, d->vp_head}) ||
@@ -864,6 +882,7 @@ int attn_shared_prefix(const attn_shared_prefix_desc* d, void* workspace, int64_
     g.round_own = (uint32_t)p.round_own;
     g.round = attn::div_by(p.round_prefix + p.round_own);
     g.by_xcd = d->kv_heads * p.prefix_splits % kNumXcd == 0;
+    g.rounded = !p.together && d->batch * (d->heads / d->kv_heads) > attn::kWaveRows;
     g.c = sc.c;
     g.flip = sc.flip;
     g.zero_q = sc.zero;

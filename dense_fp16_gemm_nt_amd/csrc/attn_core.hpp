@@ -22,7 +22,9 @@
 // Rounding: scores, maxima, sums and the output accumulate in fp32.  P is
 // rounded once to the operands' 16-bit type because the matrix cores take no
 // wider operand at their full rate (relative error at most eps / 2 for each
-// weight, as for V itself); the denominator adds the unrounded p.
+// weight, as for V itself); the denominator adds the unrounded p.  Where no
+// more than 32 rows meet the keys the matrix cores have time: P goes as two
+// operands there, its rounding and the rest.
 #pragma once
 
 #include <utility>
@@ -52,14 +54,20 @@ struct F16 {
     {
         return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
     }
+    static constexpr uint32_t kInf = 0x7c00, kOne = 0x3c00, k128 = 0x5800, k16384 = 0x7400;
     // two fp32 to fp16, nearest even
     static __device__ __forceinline__ uint32_t pack(float x, float y)
     {
         return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2){x, y}, f16x2));
     }
+    static __device__ __forceinline__ f32x2 unpack(uint32_t p)
+    {
+        return __builtin_convertvector(__builtin_bit_cast(f16x2, p), f32x2);
+    }
 };
 
 struct BF16 {
+    static constexpr uint32_t kInf = 0x7f80, kOne = 0x3f80, k128 = 0x4300, k16384 = 0x4680;
     static __device__ __forceinline__ f32x16 mfma(u32x4 a, u32x4 b, f32x16 c)
     {
         return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
@@ -67,6 +75,10 @@ struct BF16 {
     static __device__ __forceinline__ uint32_t pack(float x, float y)
     {
         return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2){x, y}, bf16x2));
+    }
+    static __device__ __forceinline__ f32x2 unpack(uint32_t p)
+    {
+        return f32x2{__builtin_bit_cast(float, p << 16), __builtin_bit_cast(float, p & 0xffff0000u)};
     }
 };
 
@@ -412,21 +424,108 @@ __device__ __forceinline__ void weights(const f32x16& s, float c, State<D>& st, 
     }
 }
 
-// O^T += V^T P^T over 32 keys, whose V rows are at byte `at` of LDS.
+// The same weights as two operands each, p[0] and what its rounding left,
+// p[1]: for the few rows whose products are not what they wait for.
 template <typename T, int D>
-__device__ __forceinline__ void accumulate(const Reads<D>& x, uint32_t at, const u32x4 (&p)[2], State<D>& st)
+__device__ __forceinline__ void weights_whole(const f32x16& s, float c, State<D>& st, u32x4 (&p)[2][2])
+{
+    const float base = st.m == -__builtin_inff() ? 0.f : kShift - st.m;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float x = exp2_(__builtin_fmaf(s[2 * i], c, base)), y = exp2_(__builtin_fmaf(s[2 * i + 1], c, base));
+        st.l += x + y;
+        const uint32_t r = T::pack(x, y);
+        const f32x2 z = T::unpack(r);
+        p[0][i / 4][i % 4] = r;
+        p[1][i / 4][i % 4] = T::pack(x - z[0], y - z[1]);
+    }
+}
+
+// The fragment of V^T for keys 16 kk .. and elements 32 b .., whose rows are at
+// byte `at` of LDS.
+template <int D>
+__device__ __forceinline__ u32x4 read_v(const Reads<D>& x, uint32_t at, int kk, int b)
 {
     using S = Shape<D>;
+    const uint32_t a = x.v[b] + at + kk * 16 * S::PITCH;
+    const u32x2 lo = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((G16_LDS s16x4*)a));
+    const u32x2 hi = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((G16_LDS s16x4*)(a + 8 * S::PITCH)));
+    return u32x4{lo[0], lo[1], hi[0], hi[1]};
+}
+
+// O^T += V^T P^T over 32 keys, whose V rows are at byte `at` of LDS; P as N
+// operands.
+template <typename T, int D, int N>
+__device__ __forceinline__ void accumulate(const Reads<D>& x, uint32_t at, const u32x4 (&p)[N][2], State<D>& st)
+{
 #pragma unroll
     for (int kk = 0; kk < 2; ++kk)
 #pragma unroll
-        for (int b = 0; b < S::DBLOCKS; ++b) {
-            const uint32_t a = x.v[b] + at + kk * 16 * S::PITCH;
-            const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((G16_LDS s16x4*)a);
-            const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((G16_LDS s16x4*)(a + 8 * S::PITCH));
-            const u32x2 lo2 = __builtin_bit_cast(u32x2, lo), hi2 = __builtin_bit_cast(u32x2, hi);
-            st.o[b] = T::mfma(u32x4{lo2[0], lo2[1], hi2[0], hi2[1]}, p[kk], st.o[b]);
+        for (int b = 0; b < Shape<D>::DBLOCKS; ++b) {
+            const u32x4 v = read_v<D>(x, at, kk, b);
+#pragma unroll
+            for (int n = 0; n < N; ++n) st.o[b] = T::mfma(v, p[n][kk], st.o[b]);
         }
+}
+
+// A product with V is not blind to a masked key: weight 0 times an infinity is
+// NaN.  Keys that no row may read are not loaded; under a causal mask one row
+// of a tile reads a key that another may not, and if that key's V is not
+// finite the other's sum is spoilt.  Such sums show at the end as O that is
+// not finite; the job is then done again, careful: V's finite elements are
+// multiplied as ever, and the others are counted for each row over the keys it
+// may read (of the first `keys` of the 32), by kind (+inf, -inf, NaN as 1, 128
+// and 16384: up to 32 of each stay apart in an fp32 sum), and added as they are.
+template <typename T, int D, int N>
+__device__ __forceinline__ void accumulate_careful(const Reads<D>& x, uint32_t at, const u32x4 (&p)[N][2], int keys, int half,
+                                                   State<D>& st)
+{
+    u32x4 allowed[2];
+#pragma unroll
+    for (int kk = 0; kk < 2; ++kk)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int key = 16 * kk + 8 * (i / 2) + 4 * half + 2 * (i % 2);
+            allowed[kk][i] = (key < keys ? T::kOne : 0u) | (key + 1 < keys ? T::kOne << 16 : 0u);
+        }
+#pragma unroll
+    for (int b = 0; b < Shape<D>::DBLOCKS; ++b) {
+        f32x16 count = {};
+#pragma unroll
+        for (int kk = 0; kk < 2; ++kk) {
+            u32x4 v = read_v<D>(x, at, kk, b), odd = {0, 0, 0, 0};
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const uint32_t h = v[i / 2] >> (16 * (i % 2)) & 0xffffu, size = h & 0x7fffu;
+                if (size >= T::kInf) {
+                    v[i / 2] &= i % 2 == 0 ? 0xffff0000u : 0x0000ffffu;
+                    odd[i / 2] |= (size > T::kInf ? T::k16384 : (h & 0x8000u) != 0 ? T::k128 : T::kOne) << (16 * (i % 2));
+                }
+            }
+#pragma unroll
+            for (int n = 0; n < N; ++n) st.o[b] = T::mfma(v, p[n][kk], st.o[b]);
+            count = T::mfma(odd, allowed[kk], count);
+        }
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const int n = (int)count[i];
+            if ((n & 127) != 0) st.o[b][i] += __builtin_inff();
+            if ((n >> 7 & 127) != 0) st.o[b][i] -= __builtin_inff();
+            if (n >> 14 != 0) st.o[b][i] = __builtin_nanf("");
+        }
+    }
+}
+
+// Whether some element of the wave's O is not finite.
+template <int D>
+__device__ __forceinline__ bool spoilt(const State<D>& st)
+{
+    float z = 0.f;
+#pragma unroll
+    for (int b = 0; b < Shape<D>::DBLOCKS; ++b)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) z = __builtin_fmaf(st.o[b][i], 0.f, z);
+    return __builtin_amdgcn_ballot_w64(!(z == 0.f)) != 0;
 }
 
 // LDS of a workgroup: two K and two V tiles, or a K and a V block of 32 keys
@@ -482,9 +581,9 @@ __device__ __forceinline__ void run_tiles(const Job& j, const Row& row, char* sm
         }
         const float mx = top_score(a, j.c);
         if (__builtin_amdgcn_ballot_w64(mx > st.m + kSlack) != 0) raise<D>(mx, st);
-        u32x4 p0[2], p1[2];
-        weights<T, D, D == 64>(a[0], j.c, st, p0);
-        weights<T, D, D == 64>(a[1], j.c, st, p1);
+        u32x4 p0[1][2], p1[1][2];
+        weights<T, D, D == 64>(a[0], j.c, st, p0[0]);
+        weights<T, D, D == 64>(a[1], j.c, st, p1[0]);
         accumulate<T, D>(x, V0 + par * S::TILE, p0, st);
         accumulate<T, D>(x, V0 + par * S::TILE + HALF, p1, st);
     };
@@ -494,6 +593,53 @@ __device__ __forceinline__ void run_tiles(const Job& j, const Row& row, char* sm
         step(t + 1, 1, next, cur);
     }
     if (t < j.tile1) step(t, 0, cur, next);
+}
+
+// The same for a job whose V is not all finite, one tile after the other.
+template <typename T, int D, int W>
+__device__ __forceinline__ void run_tiles_careful(const Job& j, const Row& row, char* smem, State<D>& st)
+{
+    using S = Shape<D>;
+    const int tid = threadIdx.x, lane = tid & 63, half = lane >> 5;
+    init(st);
+    const uint32_t lds = lds_address(smem);
+    const Reads<D> x = reads_of<D>(lds, lane);
+    const uint32_t dst = lds + __builtin_amdgcn_readfirstlane(tid >> 6) * 1024;
+    Loader<D, W> k, v;
+    k.start(j.k, j.k_row, j.keys, j.tile0, j.d, tid, false);
+    v.start(j.v, j.v_row, j.keys, j.tile0, j.d, tid, true);
+    u32x4 q[S::KSTEPS];
+    load_q<D>(j, row, half, q);
+    for (int t = j.tile0; t < j.tile1; ++t) {
+        publish();
+        k.next(dst);
+        v.next(dst + S::TILE);
+        publish();
+        for (int b = 0; b < 2; ++b) {
+            const int keys = row.limit - t * kTileKeys - 32 * b;
+            f32x16 s[1] = {scores<T, D>(x, b * (S::TILE / 2), q)};
+            mask(s[0], keys, half);
+            const float mx = top_score(s, j.c);
+            if (__builtin_amdgcn_ballot_w64(mx > st.m + kSlack) != 0) raise<D>(mx, st);
+            u32x4 p[1][2];
+            weights<T, D>(s[0], j.c, st, p[0]);
+            accumulate_careful<T, D>(x, S::TILE + b * (S::TILE / 2), p, keys, half, st);
+        }
+    }
+}
+
+// Whether `x` holds for some wave of the workgroup.
+template <int W>
+__device__ __forceinline__ bool any_wave(bool x, char* smem)
+{
+    int* flags = reinterpret_cast<int*>(smem);
+    publish();
+    if ((threadIdx.x & 63) == 0) flags[threadIdx.x >> 6] = x;
+    publish();
+    int any = 0;
+#pragma unroll
+    for (int i = 0; i < W; ++i) any |= flags[i];
+    return __builtin_amdgcn_readfirstlane(any) != 0;
 }
 
 // ----------------------------------------------------------------- few rows
@@ -513,8 +659,8 @@ constexpr int kBlockKeys = 32;
 __device__ __forceinline__ int key_blocks(int keys) { return (int)(((int64_t)keys + kBlockKeys - 1) / kBlockKeys); }
 
 // Blocks [block0, block1) of the runs' blocks; row.limit counts keys of the
-// first run.
-template <typename T, int D>
+// first run.  P goes as N operands (2: its rounding and the rest).
+template <typename T, int D, int N, bool CAREFUL = false>
 __device__ __forceinline__ void run_blocks(const Job& j, const Keys& one, const Keys& two, int block0, int block1,
                                            const Row& row, char* smem, State<D>& st)
 {
@@ -525,7 +671,7 @@ __device__ __forceinline__ void run_blocks(const Job& j, const Keys& one, const 
     constexpr uint32_t HALF = S::TILE / 2;
     const int lane = threadIdx.x & 63, half = lane >> 5, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     init(st);
-    int at = block0 + w;
+    int at = w < kWaves ? block0 + w : block1;   // a larger workgroup's other waves take none
     if (at >= block1) return;
     const int first_limit = __builtin_amdgcn_readfirstlane(row.limit);
     const int blocks1 = key_blocks(one.keys);
@@ -568,17 +714,21 @@ __device__ __forceinline__ void run_blocks(const Job& j, const Keys& one, const 
         load(at + kWaves, false);
         const bool second = at >= blocks1;
         const int key0 = (second ? at - blocks1 : at) * kBlockKeys;
-        const int n = (second ? two.keys : one.keys) - key0;
-        if (n < kBlockKeys || (!second && key0 + kBlockKeys > first_limit)) {
-            const int lim = row.limit - key0;
-            mask(s[0], second || n < lim ? n : lim, half);
-        }
+        const int n = (second ? two.keys : one.keys) - key0, lim = row.limit - key0;
+        const int readable = second || n < lim ? n : lim;
+        if (n < kBlockKeys || (!second && key0 + kBlockKeys > first_limit)) mask(s[0], readable, half);
         const float mx = top_score(s, j.c);
         if (__builtin_amdgcn_ballot_w64(mx > st.m + kSlack) != 0) raise<D>(mx, st);
-        u32x4 p[2];
-        weights<T, D>(s[0], j.c, st, p);
+        u32x4 p[N][2];
+        if constexpr (N == 2)
+            weights_whole<T, D>(s[0], j.c, st, p);
+        else
+            weights<T, D>(s[0], j.c, st, p[0]);
         landed<NL>();   // V; the next K may be in flight
-        accumulate<T, D>(x, HALF, p, st);
+        if constexpr (CAREFUL)
+            accumulate_careful<T, D>(x, HALF, p, readable, half, st);
+        else
+            accumulate<T, D>(x, HALF, p, st);
         landed<NL>();   // V has been read
         load(at + kWaves, true);
     }
@@ -702,20 +852,22 @@ __device__ __forceinline__ void merge_waves(const State<D>& st, bool valid, int 
     };
     const float l = sum_halves(st.l);
     publish();   // the waves are done with their K and V blocks
-    if (half == 0) ml[w * kWaveRows + r] = f32x2{st.m, l};
+    if (half == 0 && w < kWaves) ml[w * kWaveRows + r] = f32x2{st.m, l};
     publish();
-    if (valid) {
-        const float f = l == 0.f ? 0.f : exp2_(st.m - top(r));
+    if (valid && w < kWaves) {
+        const float f = exp2_(st.m - top(r));
+        const bool some = l != 0.f;
         float* to = o + (w * kWaveRows + r) * PITCH;
 #pragma unroll
         for (int b = 0; b < Shape<D>::DBLOCKS; ++b)
 #pragma unroll
             for (int g = 0; g < 4; ++g)
-                *reinterpret_cast<f32x4*>(to + 32 * b + 8 * g + 4 * half) = f32x4{
-                    st.o[b][4 * g] * f, st.o[b][4 * g + 1] * f, st.o[b][4 * g + 2] * f, st.o[b][4 * g + 3] * f};
+                *reinterpret_cast<f32x4*>(to + 32 * b + 8 * g + 4 * half) =
+                    some ? f32x4{st.o[b][4 * g] * f, st.o[b][4 * g + 1] * f, st.o[b][4 * g + 2] * f, st.o[b][4 * g + 3] * f}
+                         : f32x4{0.f, 0.f, 0.f, 0.f};
     }
     publish();
-    for (int i = tid; i < rows * (D / 4); i += kThreads) {
+    for (int i = tid; i < rows * (D / 4); i += blockDim.x) {
         const int row = i / (D / 4), e = i % (D / 4) * 4;
         if (e >= d) continue;
         const float m = top(row);

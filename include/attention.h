@@ -20,8 +20,8 @@
  * Strides are in elements.  Elements of a head are contiguous, Q, K, V and O
  * and all their strides are on 16-byte boundaries (multiples of 8 elements),
  * strides are >= 0 (0 repeats an input), and a row of keys or values is less
- * than 2^23 elements from the next.  O must not overlap an input, and its
- * rows and heads must not overlap each other.
+ * than 2^23 elements from the next.  O and lse must not overlap an input or
+ * each other, and O's rows and heads must not overlap each other.
  *
  * Calls are asynchronous and stream-ordered: they validate, enqueue and
  * return; validation comes before any HIP call, and an invalid call launches

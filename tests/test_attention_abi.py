@@ -2,6 +2,7 @@
 import ctypes
 import os
 import re
+import subprocess
 
 import pytest
 
@@ -20,6 +21,13 @@ def test_library_exports_every_declared_symbol():
     L = ctypes.CDLL(g.LIB_PATH)
     for n in names:
         assert hasattr(L, n), n
+
+
+def test_header_is_plain_c(tmp_path):
+    src = tmp_path / "user.c"
+    src.write_text('#include "attention.h"\nint main(void) { attn_prompt_desc d = {0}; return sizeof d == 0 ? ATTN_BF16 : attn_prompt_check(&d); }\n')
+    subprocess.run(["gcc", "-std=c11", "-Wall", "-Wextra", "-Werror", "-fsyntax-only", "-I", os.path.join(ROOT, "include"), str(src)],
+                   check=True)
 
 
 @pytest.mark.parametrize("struct,desc", [("attn_prompt_desc", a.PromptDesc), ("attn_shared_prefix_desc", a.SharedPrefixDesc)])
@@ -83,6 +91,8 @@ OK, INVALID, UNSUPPORTED = g.OK, g.INVALID_ARG, g.UNSUPPORTED
     ({"cu_k": 6 * BASE + 2}, UNSUPPORTED),
     ({"lse": 7 * BASE}, OK),
     ({"lse": 7 * BASE + 1}, UNSUPPORTED),
+    ({"lse": 4 * BASE}, INVALID),                # lse over O
+    ({"lse": 2 * BASE + 1024}, INVALID),
     ({"Q": BASE + 8}, UNSUPPORTED),
     ({"Q": BASE + 1}, UNSUPPORTED),
     ({"K": 2 * BASE + 2}, UNSUPPORTED),
@@ -131,6 +141,8 @@ def test_prompt_arguments(change, want):
     ({"Vs": 0}, INVALID),
     ({"lens": 0}, INVALID),
     ({"lens": 7 * BASE + 1}, UNSUPPORTED),
+    ({"lse": 6 * BASE}, INVALID),
+    ({"lse": 8 * BASE}, OK),
     ({"Ks": 4 * BASE + 4}, UNSUPPORTED),
     ({"ks_slot": 6404}, UNSUPPORTED),
     ({"vs_slot": -8}, INVALID),

@@ -91,6 +91,43 @@ def test_prompt_long_keys(n, m, heads, kv_heads, d, causal, dtype):
     check_prompt(q, k, v, [0, n], [0, m], causal)
 
 
+@pytest.mark.parametrize("d,dtype", [(128, "bf16"), (96, "fp16"), (64, "fp16")])
+@pytest.mark.parametrize("causal", [True, False])
+def test_prompt_mixed_batch(causal, d, dtype):
+    # a long prompt, chunks and single tokens behind long caches in one call
+    gen = torch.Generator().manual_seed(d)
+    cq, ck = cu([1500, 1, 3, 70, 1]), cu([2600, 3000, 2500, 2111, 1])
+    q, k, v = rand(gen, dtype, cq[-1], 4, d), rand(gen, dtype, ck[-1], 2, d), rand(gen, dtype, ck[-1], 2, d)
+    check_prompt(q, k, v, cq, ck, causal)
+
+
+def test_prompt_without_keys():
+    q = torch.ones(5, 2, 64, dtype=torch.float16, device=DEV)
+    none = torch.empty(0, 2, 64, dtype=torch.float16, device=DEV)
+    O, lse = g.attention_prompt(q, none, none, ints([0, 2, 5]), ints([0, 0, 0]), return_lse=True)
+    torch.cuda.synchronize()
+    assert bool((O == 0).all()) and bool((lse == -float("inf")).all())
+    assert g.attention_prompt(q[:0], none, none, ints([0, 0])).shape == (0, 2, 64)
+    kept = torch.full_like(q, 3.0)
+    g.attention_prompt(q, none, none, ints([0]), O=kept)   # no sequence
+    torch.cuda.synchronize()
+    assert bool((kept == 3).all())
+
+
+def test_rows_do_not_depend_on_their_neighbours():
+    # the same sequence alone and packed between others: the same bits where the same kernel takes it
+    gen = torch.Generator().manual_seed(59)
+    lens = [300, 180, 300]
+    c = cu(lens)
+    q, k, v = (rand(gen, "bf16", c[-1], 2, 128).to(DEV) for _ in range(3))
+    packed = g.attention_prompt(q, k, v, ints(c))
+    q[:c[1]] *= 30   # other values around it
+    k[c[2]:] *= 30
+    again = g.attention_prompt(q, k, v, ints(c))
+    torch.cuda.synchronize()
+    assert torch.equal(packed[c[1]:c[2]], again[c[1]:c[2]])
+
+
 def test_prompt_peaked_and_large_scores():
     # maxima that rise from tile to tile, scores of several hundred
     gen = torch.Generator().manual_seed(9)
@@ -180,6 +217,47 @@ def test_prompt_neighbours_with_infinities(d, dtype):
     for b in range(0, len(lens), 2):
         s = slice(c[b], c[b + 1])
         ref.prompt(q[s], k[s], v[s], [0, lens[b]], [0, lens[b]], True, 1 / math.sqrt(d), O[s], lse[s], f"sequence {b}")
+
+
+@pytest.mark.parametrize("d,dtype", [(128, "fp16"), (64, "bf16"), (96, "bf16"), (72, "fp16")])
+@pytest.mark.parametrize("n,m,heads,kv_heads", [(300, 300, 2, 1), (40, 700, 4, 4), (9, 300, 2, 1), (5, 2500, 4, 2), (600, 4000, 2, 2)])
+def test_prompt_infinities_behind_the_mask(n, m, heads, kv_heads, d, dtype):
+    """Values that are not finite, at keys that early rows of the sequence may not read: those rows do not see them, the
+    later ones get infinity or NaN in the elements where they stand and finite sums in the others."""
+    gen = torch.Generator().manual_seed(n + m + d)
+    q, k, v = rand(gen, dtype, n, heads, d), rand(gen, dtype, m, kv_heads, d), rand(gen, dtype, m, kv_heads, d)
+    inf = float("inf")
+    base = m - n   # key of query 0
+    bad = [(base + n // 4, 1, inf), (base + n // 3, 2, -inf), (base + n // 2, 3, float("nan")), (base + n - 1, 1, -inf),
+           (base + n // 2 + 1, d - 1, inf), (base + n - 2, 2, -inf)]
+    poisoned = v.clone()
+    clean = v.clone()
+    expect = torch.zeros(n, kv_heads, d)   # what the odd values add
+    for key, e, x in bad:
+        poisoned[key, 0, e] = x
+        clean[key, 0, e] = 0
+        expect[max(0, key - base):, 0, e] += x
+    O, lse = run_prompt(q, k, poisoned, [0, n], [0, m], True)
+    odd = ~torch.isfinite(expect.repeat_interleave(heads // kv_heads, 1))
+    want = expect.repeat_interleave(heads // kv_heads, 1)
+    assert torch.equal(torch.isnan(O) & odd, torch.isnan(want)) and torch.equal(torch.isfinite(O), ~odd)
+    assert torch.equal(O.float()[torch.isinf(want)], want[torch.isinf(want)])
+    # the rest against the sums without them
+    full, flse = run_prompt(q, k, clean, [0, n], [0, m], True)
+    ref.prompt(q, k, clean, [0, n], [0, m], True, 1 / math.sqrt(d), full, flse, "without the odd values")
+    ref.prompt(q, k, clean, [0, n], [0, m], True, 1 / math.sqrt(d), torch.where(odd, full, O), lse, "beside the odd values")
+
+
+@pytest.mark.parametrize("n,m", [(200, 200), (6, 900)])
+def test_prompt_keys_that_are_not_numbers_behind_the_mask(n, m):
+    gen = torch.Generator().manual_seed(n)
+    q, k, v = (rand(gen, "bf16", x, 2, 64) for x in (n, m, m))
+    at = m - 3
+    k[at] = float("nan")
+    O, lse = run_prompt(q, k, v, [0, n], [0, m], True)
+    keep = n - (m - at)   # rows that do not read it
+    ref.prompt(q[:keep], k[:at], v[:at], [0, keep], [0, at], True, 1 / 8, O[:keep], lse[:keep], "rows before it")
+    assert bool(torch.isnan(O[keep:].float()).all()) and bool(torch.isnan(lse[keep:]).all())
 
 
 def test_prompt_offsets_that_make_no_sense():
