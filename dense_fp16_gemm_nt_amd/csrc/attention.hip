@@ -584,16 +584,17 @@ struct PromptPlan {
 };
 
 // Row tiles of one kv head: a packed batch has at most one ragged tile for
-// each sequence.  Where all tiles of all kv heads leave compute units without
+// each sequence (and one sequence no more than its rows fill).  Where all tiles of all kv heads leave compute units without
 // work, the keys are split, at least 256 of them to a part.
 //
 // Eight waves share a tile of K and V where workgroups are long: they read
 // half as many bytes into LDS, but a compute unit then holds one workgroup,
 // and nothing runs beside its beginning and end.  Measured on MI355X, eight
-// against four: 16384 tokens 1915 against 1960 us, 4096 148 against 155, 512
-// against 20000 keys 189 against 197; packed lengths of 1 to 2900 (16 tiles
-// of keys to a workgroup on average) 143 against 135, heads of 64 elements
-// (three workgroups of four waves to a compute unit) 155 against 153.
+// against four: 16384 tokens 1941 against 2007 us, 4096 151 against 160, 512
+// against 20000 keys 175 against 185; packed lengths of 333 to 1999 with
+// heads of 96 (16 tiles of keys to a workgroup on average) 50.8 against 46.1,
+// of 1 to 2900 138.7 against 138.3, heads of 64 elements (three workgroups of
+// four waves to a compute unit) 155 against 153.
 constexpr int64_t kLongTiles = 24;
 
 PromptPlan plan_prompt(const attn_prompt_desc* d, int cus)
@@ -604,7 +605,8 @@ PromptPlan plan_prompt(const attn_prompt_desc* d, int cus)
     const int64_t keys = ceil_div(d->total_k, seqs), queries = ceil_div(d->total_q, seqs);
     auto plan = [&](int64_t waves) {
         p.waves = waves;
-        p.tiles = d->total_q * group / (waves * attn::kWaveRows) + seqs;
+        const int64_t rows = waves * attn::kWaveRows;
+        p.tiles = seqs == 1 ? ceil_div(d->total_q * group, rows) : d->total_q * group / rows + seqs;
         const int64_t wgs = p.tiles * d->kv_heads, slots = waves == attn::kWaves ? 2 * cus : cus;
         int64_t s = wgs >= cus ? 1 : slots / wgs;
         if (s > keys / (4 * kTileKeys)) s = keys / (4 * kTileKeys);
