@@ -676,7 +676,9 @@ SharedPlan plan_shared(const attn_shared_prefix_desc* d, int cus)
     p.rounds = p.prefix_wgs == 0 ? 1 : ceil_div(p.prefix_wgs, p.round_prefix);
     p.round_own = ceil_div(p.own_wgs, p.rounds);
     const int64_t parts = p.prefix_splits + p.own_splits;
-    p.part_bytes = parts > 1 ? parts * d->batch * d->heads * (d->head_dim + 2) * 4 : 0;
+    // one run in one part stores its rows itself; a prefix alone (slots without
+    // rows) leaves them to the join even then, which knows the slots in use
+    p.part_bytes = !p.together || parts > 1 ? parts * d->batch * d->heads * (d->head_dim + 2) * 4 : 0;
     return p;
 }
 

@@ -312,6 +312,32 @@ def test_shared_prefix(B, P, N, heads, kv_heads, d, dtype):
     check_shared(*shared_inputs(gen, dtype, B, P, N, heads, kv_heads, d), lens)
 
 
+@pytest.mark.parametrize("B,heads,kv_heads,P,lens", [
+    (130, 256, 256, 600, [0, 5, -1]),    # enough row tiles and kv heads that the prefix is one part
+    (2, 512, 512, 550, [0, -1]),         # the same by the few-rows way
+])
+def test_shared_prefix_without_slot_rows(B, heads, kv_heads, P, lens):
+    gen = torch.Generator().manual_seed(P)
+    q, kp, vp = rand(gen, "fp16", B, heads, 8), rand(gen, "fp16", P, kv_heads, 8), rand(gen, "fp16", P, kv_heads, 8)
+    none = torch.empty(B, 0, kv_heads, 8, dtype=torch.float16)
+    lens = [lens[b % len(lens)] for b in range(B)]
+    O = torch.full((B, heads, 8), 3.0, dtype=torch.float16, device=DEV)
+    say(f"[gpu] shared prefix without slot rows B={B} heads={heads} P={P}")
+    need = g.attention_shared_prefix_workspace(q.to(DEV), kp.to(DEV), vp.to(DEV), none.to(DEV), none.to(DEV), ints(lens))
+    assert need >= B * heads * 10 * 4, "no room for the prefix's part"
+    _, lse = g.attention_shared_prefix(q.to(DEV), kp.to(DEV), vp.to(DEV), none.to(DEV), none.to(DEV), ints(lens), O=O,
+                                       return_lse=True)
+    torch.cuda.synchronize()
+    for b in range(B):
+        if lens[b] < 0:
+            assert bool((O[b] == 3).all())
+    # a head's keys are one sequence's for all rows of the batch
+    for h in range(0, heads, 17):
+        used = [b for b in range(B) if lens[b] >= 0]
+        o, l, parts, lb = ref.attend(q[used, h].double(), kp[:, h].double(), vp[:, h].double(), 8 ** -0.5, None)
+        ref.check_rows(O[used, h].cpu(), lse[used, h].cpu(), o, l, parts, lb, torch.float16, f"head {h}")
+
+
 def test_shared_prefix_slots():
     # unused slots keep their rows, lengths past the slot count as all of it, stale rows hold NaN
     gen = torch.Generator().manual_seed(31)
