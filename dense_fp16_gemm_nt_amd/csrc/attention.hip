@@ -8,7 +8,6 @@
 
 #include <atomic>
 #include <cfloat>
-#include <climits>
 #include <cmath>
 #include <cstring>
 #include <initializer_list>
@@ -102,9 +101,9 @@ __device__ __forceinline__ uint32_t wave_scan(uint32_t x)
 // Tile `t` of the sequences' tiles put one after the other; each lane looks at
 // one sequence, 64 at a time.  Within a sequence the tiles come in falling
 // order: under a causal mask those have the most keys, and the longest work
-// starts first.  (The tiles of all sequences ordered by their keys were no
-// faster on packed lengths of 1 to 2900, 137 against 135 us: neighbours then
-// share no keys.)
+// starts first.  (The tiles of all sequences ordered by their keys took 131
+// against 132 us on packed lengths of 1 to 2900 and 46 against 44 with heads of
+// 96: neighbours then share no keys.)
 template <int ROWS>
 __device__ __forceinline__ Tile find_tile(const PromptArgs& g, uint32_t t)
 {
@@ -440,6 +439,14 @@ int device_cus(int* cus)
 constexpr int64_t kMaxRowStride = int64_t(1) << 23;   // a tile of 64 rows spans less than 2^30 bytes
 constexpr int64_t kMaxIndex = (int64_t(1) << 31) - 1024;
 constexpr int64_t kMaxStride = int64_t(1) << 40;      // elements; keeps every offset inside 63 bits
+constexpr int64_t kMaxBlocks = 64;   // of 32 keys, of a slot's part, so that long and short slots even out
+// A launch holds less than 2^32 threads.  This many units of work (row tiles
+// of 128 and slots' parts of 64 blocks of keys, times kv heads) keep every
+// launch of a call, of workgroups of 512 threads and of the joins too, at half
+// of that or less.
+constexpr int64_t kMaxUnits = int64_t(1) << 22;
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 bool overlaps(const void* a, int64_t abytes, const void* b, int64_t bbytes)
 {
@@ -534,7 +541,9 @@ int check_prompt(const attn_prompt_desc* d)
     if (((uintptr_t)d->cu_q | (uintptr_t)d->cu_k | (uintptr_t)d->lse) & 3) return GEMM_F16_NT_UNSUPPORTED;
     if (d->k_row >= kMaxRowStride || d->v_row >= kMaxRowStride) return GEMM_F16_NT_UNSUPPORTED;
     const int64_t group = d->heads / d->kv_heads;
-    if (d->total_k > kMaxIndex || d->total_q > kMaxIndex / group) return GEMM_F16_NT_UNSUPPORTED;
+    if (d->batch > kMaxIndex || d->total_k > kMaxIndex || d->total_q > kMaxIndex / group) return GEMM_F16_NT_UNSUPPORTED;
+    const int64_t seqs = d->batch < d->total_q ? d->batch : d->total_q;
+    if (d->total_q * group / kTileRows + seqs > kMaxUnits / d->kv_heads) return GEMM_F16_NT_UNSUPPORTED;
     return GEMM_F16_NT_OK;
 }
 
@@ -573,12 +582,13 @@ int check_shared(const attn_shared_prefix_desc* d)
         d->vs_row >= kMaxRowStride)
         return GEMM_F16_NT_UNSUPPORTED;
     if (d->prefix > kMaxIndex || d->slot_rows > kMaxIndex || d->batch > kMaxIndex / d->heads) return GEMM_F16_NT_UNSUPPORTED;
+    const int64_t group = d->heads / hk, parts = d->slot_rows / (kMaxBlocks * attn::kBlockKeys) + 1;
+    if (ceil_div(d->batch * group, kTileRows) + d->batch * ceil_div(group, attn::kWaveRows) * parts > kMaxUnits / hk)
+        return GEMM_F16_NT_UNSUPPORTED;
     return GEMM_F16_NT_OK;
 }
 
 // ----------------------------------------------------------------- plans
-int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
-
 struct PromptPlan {
     int64_t waves, tiles, splits, part_bytes;
 };
@@ -629,7 +639,6 @@ PromptPlan plan_prompt(const attn_prompt_desc* d, int cus)
 // 4 x 8000 + 100 14.8 against 18.4).  One sequence alone has nobody to share
 // with.
 constexpr int64_t kMinBlocks = 16;      // of 32 keys, for a part
-constexpr int64_t kMaxBlocks = 64;      // of a slot's part, so that long and short slots even out
 constexpr int64_t kTogetherBlocks = 16;
 
 struct SharedPlan {
@@ -811,15 +820,15 @@ int attn_prompt(const attn_prompt_desc* d, void* workspace, int64_t workspace_by
     g.zero_q = sc.zero;
     g.parts = parts_in(workspace, p.splits, d->total_q * d->heads);
     const int64_t wgs = p.tiles * units;
-    int64_t join_rows = 0;
-    const void* join = pick_join<PromptJoin>(d->dtype, p.splits, &join_rows);
-    const int64_t join_wgs = (d->total_q * g.group.d / kTileRows + d->batch) * d->kv_heads * (kTileRows / join_rows);
-    if (wgs > INT_MAX || (p.splits > 1 && join_wgs > INT_MAX)) return GEMM_F16_NT_UNSUPPORTED;
     const hipStream_t s = (hipStream_t)stream;
     const int threads = 64 * (int)p.waves;
     if (p.splits == 1) return launch(Prompt<false>::f(d, p.waves), wgs, threads, &g, s);
     if ((st = launch(Prompt<true>::f(d, p.waves), wgs, threads, &g, s)) != GEMM_F16_NT_OK) return st;
-    return launch(join, join_wgs, kThreads, &g, s);
+    int64_t join_rows = 0;
+    const void* join = pick_join<PromptJoin>(d->dtype, p.splits, &join_rows);
+    const int64_t seqs = d->batch < d->total_q ? d->batch : d->total_q;
+    const int64_t join_tiles = d->total_q * g.group.d / kTileRows + seqs;
+    return launch(join, join_tiles * d->kv_heads * (kTileRows / join_rows), kThreads, &g, s);
 }
 
 int attn_shared_prefix_check(const attn_shared_prefix_desc* d) { return check_shared(d); }
@@ -892,7 +901,6 @@ int attn_shared_prefix(const attn_shared_prefix_desc* d, void* workspace, int64_
     g.zero_q = sc.zero;
     g.parts = parts_in(workspace, p.prefix_splits + p.own_splits, d->batch * d->heads);
     const int64_t wgs = p.rounds * (p.round_prefix + p.round_own);
-    if (wgs > INT_MAX) return GEMM_F16_NT_UNSUPPORTED;
     const hipStream_t s = (hipStream_t)stream;
     st = launch(pick<SharedParts>(d->dtype, d->head_dim), wgs, kThreads, &g, s);
     if (st != GEMM_F16_NT_OK || p.part_bytes == 0) return st;

@@ -11,7 +11,10 @@
  * softmax weights are rounded to the operands' type before the product with
  * V, and O is rounded once, to nearest even.  A row that no key is left for
  * gets O = +0 and lse = -inf.  lse, where asked for, is the natural
- * logarithm of sum_j exp(scale * q . k_j), fp32.
+ * logarithm of sum_j exp(scale * q . k_j), fp32.  A negative scale is taken
+ * as it is; for scale 0 every score is 0, whatever Q and K hold.
+ *
+ * The calls compute results, not gradients.
  *
  * Keys that a mask or a length leaves out have no part in the results of
  * the rows they are left out for, whatever they hold (infinities and NaN
@@ -20,7 +23,11 @@
  * Strides are in elements.  Elements of a head are contiguous, Q, K, V and O
  * and all their strides are on 16-byte boundaries (multiples of 8 elements),
  * strides are >= 0 (0 repeats an input), and a row of keys or values is less
- * than 2^23 elements from the next.  O and lse must not overlap an input or
+ * than 2^23 elements from the next.  A call has at most 2^22 units of work,
+ * kv_heads times (total_q * group / 128 + sequences) for attn_prompt and
+ * kv_heads times (batch * group / 128 + batch * ceil(group / 32) *
+ * (slot_rows / 2048 + 1)) for attn_shared_prefix, with group = heads /
+ * kv_heads; more is UNSUPPORTED.  O and lse must not overlap an input or
  * each other, and O's rows and heads must not overlap each other.
  *
  * Calls are asynchronous and stream-ordered: they validate, enqueue and
@@ -57,7 +64,8 @@ extern "C" {
  * values each, not decreasing).  With `causal`, query i of n reads keys
  * j <= i + (keys - n): the last query reads every key, so a chunk of a prompt
  * runs against all keys so far, and a single new token against its cache.
- * Rows of O and lse that belong to no sequence are left as they were. */
+ * Rows of O and lse that belong to no sequence are left as they were.  Each
+ * workgroup looks through the sequences, 64 at a time, for its own. */
 typedef struct attn_prompt_desc {
     int32_t dtype;  /* ATTN_F16 or ATTN_BF16 */
     int32_t causal; /* 0 or 1 */

@@ -162,6 +162,39 @@ def test_shared_prefix_arguments(change, want):
         assert L.attn_shared_prefix_workspace(ctypes.byref(d)) == want
 
 
+FAR = 1 << 50   # O above everything the inputs span
+MANY = dict(q_row=0, o_row=1 << 10, O=FAR, k_row=0, v_row=0)
+
+
+@pytest.mark.parametrize("change,want", [
+    # kv_heads (2) x (total_q * group (4) / 128 + sequences) units, at most 2^22
+    (dict(MANY, batch=1, total_q=(1 << 26) - 32), OK),
+    (dict(MANY, batch=1, total_q=1 << 26), UNSUPPORTED),
+    (dict(MANY, batch=1 << 20, total_q=1 << 20), OK),
+    (dict(MANY, batch=1 << 21, total_q=1 << 21), UNSUPPORTED),
+    (dict(MANY, batch=1 << 30, total_q=5), OK),    # at most five of them have a query
+    (dict(MANY, batch=(1 << 31) - 1, total_q=5), UNSUPPORTED),   # a count of them by 64 would pass 32 bits
+])
+def test_prompt_most_work(change, want):
+    assert g.lib().attn_prompt_check(ctypes.byref(prompt(**change))) == want
+
+
+ONE_SLOT = dict(q_row=0, ks_slot=0, vs_slot=0, ks_row=0, vs_row=0, O=FAR)
+
+
+@pytest.mark.parametrize("change,want", [
+    # kv_heads (2) x (batch * group (4) / 128 + batch * (slot_rows / 2048 + 1)) units, at most 2^22
+    (dict(ONE_SLOT, batch=1 << 20), OK),
+    (dict(ONE_SLOT, batch=1 << 21), UNSUPPORTED),
+    (dict(ONE_SLOT, batch=1 << 20, slot_rows=2047), OK),
+    (dict(ONE_SLOT, batch=1 << 20, slot_rows=2048), UNSUPPORTED),
+    (dict(ONE_SLOT, batch=4, slot_rows=1 << 30), UNSUPPORTED),
+    (dict(ONE_SLOT, batch=3, slot_rows=1 << 30), OK),
+])
+def test_shared_prefix_most_work(change, want):
+    assert g.lib().attn_shared_prefix_check(ctypes.byref(shared(**change))) == want
+
+
 def test_null_descriptors():
     L = g.lib()
     assert L.attn_prompt_check(None) == INVALID and L.attn_shared_prefix_check(None) == INVALID
