@@ -5,7 +5,8 @@
 with a common prefix.  Both take fp16 or bf16 device tensors, check their
 metadata, pass device pointers and the current HIP stream, and raise on a
 non-zero status.  Lengths and offsets stay on the device: neither call
-synchronises.
+synchronises.  Neither has a gradient: results are not part of an autograd
+graph.
 """
 from __future__ import annotations
 
