@@ -449,6 +449,63 @@ def test_captured_and_replayed():
             assert torch.equal(a, b) and torch.equal(e, b)
 
 
+def test_captured_with_other_lengths():
+    """The lengths are device tensors: a graph captured for a padded batch serves others, single tokens, empty sequences
+    and slots not in use, and leaves the rows behind the last sequence alone."""
+    gen = torch.Generator().manual_seed(61)
+    q, k, v = (rand(gen, "bf16", n, h, 96) for n, h in ((300, 6), (2400, 2), (2400, 2)))
+    s = shared_inputs(gen, "fp16", 5, 700, 90, 4, 2, 128)
+    cq, ck, lens = ints([0, 300, 300, 300, 300]), ints([0, 2400, 2400, 2400, 2400]), ints([90] * 5)
+    dq, dk, dv = q.to(DEV), k.to(DEV), v.to(DEV)
+    ds = [t.to(DEV) for t in s]
+    O, Os = torch.empty_like(dq), torch.empty_like(ds[0])
+    lse, ls = torch.empty(300, 6, device=DEV), torch.empty(5, 4, device=DEV)
+
+    def both():
+        g.attention_prompt(dq, dk, dv, cq, ck, O=O, lse=lse)
+        g.attention_shared_prefix(*ds, lens, O=Os, lse=ls)
+
+    both()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        both()
+    for a, b, c in [([0, 1, 2, 3, 4], [0, 700, 700, 1500, 2399], [0, 1, 90, -1, 33]),
+                    ([0, 0, 129, 129, 200], [0, 5, 600, 601, 700], [-1, -1, -1, -1, -1]),
+                    ([0, 300, 300, 300, 300], [0, 2400, 2400, 2400, 2400], [90, 500, 3, 64, 32]),
+                    ([0, 0, 0, 0, 0], [0, 0, 0, 0, 0], [0, 0, 0, 0, 0])]:
+        say(f"[gpu] replay with cu_q={a} cu_k={b} lens={c}")
+        for x, y in ((cq, a), (ck, b), (lens, c)):
+            x.copy_(ints(y))
+        for x in (O, Os, lse, ls):
+            x.fill_(3.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        ref.prompt(q, k, v, a, b, True, 96 ** -0.5, O.cpu(), lse.cpu(), "replayed prompt")
+        assert bool((O[a[-1]:] == 3).all()) and bool((lse[a[-1]:] == 3).all())
+        ref.shared_prefix(*s, c, 128 ** -0.5, Os.cpu(), ls.cpu(), "replayed shared prefix")
+        for i, n in enumerate(c):
+            assert n >= 0 or (bool((Os[i] == 3).all()) and bool((ls[i] == 3).all()))
+
+
+def test_calls_that_overlap_in_time():
+    """Split calls on two streams at once, each with parts of its own."""
+    calls, _ = _calls()
+    want = [f() for f in calls]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = [[], []]
+    for turn in range(10):
+        for i, st in enumerate(streams):
+            with torch.cuda.stream(st):
+                got[i].append([f() for f in (calls if i == 0 else calls[::-1])])
+    torch.cuda.synchronize()
+    for i in range(2):
+        for outs in got[i]:
+            for a, b in zip(outs if i == 0 else outs[::-1], want):
+                assert torch.equal(a, b)
+
+
 def test_given_workspace():
     gen = torch.Generator().manual_seed(53)
     q, k, v = (rand(gen, "fp16", n, h, 64).to(DEV) for n, h in ((3, 2), (3000, 1), (3000, 1)))
