@@ -59,14 +59,26 @@ def declare(L: ctypes.CDLL) -> None:
         f.restype, f.argtypes = i32, [vp]
 
 
-def _query(Q):
-    """Type code, device and shape of Q."""
+_torch = None
+
+
+def _module():
+    """torch, which the package loads with the first call that needs it.  Not by an import statement in each function:
+    with those and a second look at tensors made here a call of 128 tokens took 10.6 us on the host instead of 9.7."""
+    global _torch
     import torch
 
+    _torch = torch
+    return torch
+
+
+def _query(Q):
+    """Type code and device of Q."""
+    torch = _torch or _module()
     dtype = Q.dtype
-    if dtype == torch.float16:
+    if dtype is torch.float16:
         code = F16
-    elif dtype == torch.bfloat16:
+    elif dtype is torch.bfloat16:
         code = BF16
     else:
         raise TypeError(f"attention takes torch.float16 or torch.bfloat16, not {dtype}")
@@ -78,14 +90,19 @@ def _query(Q):
 
 
 def _strides(name, X, shape, dtype, device):
-    """Strides of the dimensions before the last of a tensor that has to have this shape and type, the last contiguous;
-    0 where a dimension has one entry and its stride says nothing."""
+    """Strides of a tensor that has to have this shape and type, as _steps has them."""
     if X.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype} like Q, not {X.dtype}")
     if X.device != device:
         raise ValueError(f"{name} is on {X.device}, Q on {device}")
     if X.shape != shape:
         raise ValueError(f"{name} must be {tuple(shape)}; got {tuple(X.shape)}")
+    return _steps(name, X, shape)
+
+
+def _steps(name, X, shape):
+    """Strides of the dimensions before the last, which has to be contiguous; 0 where a dimension has one entry and its
+    stride says nothing."""
     *st, last = X.stride()
     if last != 1 and shape[-1] > 1:
         raise ValueError(f"{name}: last dimension must be contiguous")
@@ -93,9 +110,7 @@ def _strides(name, X, shape, dtype, device):
 
 
 def _ints(name, X, n, device):
-    import torch
-
-    if X.dtype is not torch.int32:
+    if X.dtype is not (_torch or _module()).int32:
         raise TypeError(f"{name} must be torch.int32")
     if X.device != device or X.shape != (n,) or not X.is_contiguous():
         raise ValueError(f"{name} must be a contiguous tensor of {n} values on {device}")
@@ -116,8 +131,7 @@ def _scale(scale, d):
 
 def _outputs(Q, O, lse, return_lse):
     """(O, lse), allocated where they are not given; lse may be None."""
-    import torch
-
+    torch = _torch or _module()
     if O is None:
         O = torch.empty_like(Q) if Q.is_contiguous() else torch.empty_like(Q, memory_format=torch.contiguous_format)
     if lse is None:
@@ -133,8 +147,7 @@ _entries = {}   # name -> (entry point, its workspace query) of the loaded libra
 
 def _call(name, desc, device, workspace):
     """Runs an entry point on a device's current stream, with a workspace if it needs one."""
-    import torch
-
+    torch = _torch or _module()
     if device.index != torch.cuda.current_device():   # launches go to the current device
         with torch.cuda.device(device):
             return _call(name, desc, device, workspace)
@@ -160,17 +173,16 @@ def _call(name, desc, device, workspace):
 
 
 def _workspace_bytes(name, desc, device):
-    import torch
-
-    with torch.cuda.device(device):
+    with (_torch or _module()).cuda.device(device):
         n = getattr(lib(), name + "_workspace")(desc)
     if n < 0:
         raise GemmError(int(n), name + "_workspace")
     return int(n)
 
 
-def _prompt_desc(Q, K, V, cu_q, cu_k, causal, scale, O, lse):
-    """Descriptor bytes and device; without O the strides of a contiguous one, at an address that no tensor has."""
+def _prompt_desc(Q, K, V, cu_q, cu_k, causal, scale, O, lse, given):
+    """Descriptor bytes and device; an O that was not given is contiguous, and without one the address is one that no
+    tensor has."""
     code, device = _query(Q)
     dtype, shape = Q.dtype, Q.shape
     Tq, H, d = shape
@@ -184,11 +196,12 @@ def _prompt_desc(Q, K, V, cu_q, cu_k, causal, scale, O, lse):
     n = cu_q.numel()
     if n < 1:
         raise ValueError("cu_q needs a value more than there are sequences")
-    cq, ck = _ints("cu_q", cu_q, n, device), _ints("cu_k", cu_k, n, device)
-    qs, ks, vs = _strides("Q", Q, shape, dtype, device), _strides("K", K, kv, dtype, device), _strides("V", V, kv, dtype, device)
-    os, o = ((H * d, d), 16) if O is None else (_strides("O", O, shape, dtype, device), O.data_ptr())
-    return _pack_prompt(code, 1 if causal else 0, H, Hk, d, n - 1, Tq, Tk, Q.data_ptr(), K.data_ptr(), V.data_ptr(), o,
-                        0 if lse is None else lse.data_ptr(), cq, ck, *qs, *ks, *vs, *os, _scale(scale, d)), device
+    cq = _ints("cu_q", cu_q, n, device)
+    ck = cq if cu_k is cu_q else _ints("cu_k", cu_k, n, device)
+    qs, ks, vs = _steps("Q", Q, shape), _strides("K", K, kv, dtype, device), _strides("V", V, kv, dtype, device)
+    os = _strides("O", O, shape, dtype, device) if given else (H * d, d)
+    return _pack_prompt(code, 1 if causal else 0, H, Hk, d, n - 1, Tq, Tk, Q.data_ptr(), K.data_ptr(), V.data_ptr(),
+                        16 if O is None else O.data_ptr(), 0 if lse is None else lse.data_ptr(), cq, ck, *qs, *ks, *vs, *os, _scale(scale, d)), device
 
 
 def attention_prompt(Q, K, V, cu_q, cu_k=None, *, causal=True, scale=None, O=None, lse=None, return_lse=False, workspace=None):
@@ -208,18 +221,19 @@ def attention_prompt(Q, K, V, cu_q, cu_k=None, *, causal=True, scale=None, O=Non
     values there).  `workspace`: a device tensor of at least
     attention_prompt_workspace(...) bytes, 16-byte aligned; allocated here
     when not given."""
+    given = O is not None
     O, lse = _outputs(Q, O, lse, return_lse)
-    desc, device = _prompt_desc(Q, K, V, cu_q, cu_q if cu_k is None else cu_k, causal, scale, O, lse)
+    desc, device = _prompt_desc(Q, K, V, cu_q, cu_q if cu_k is None else cu_k, causal, scale, O, lse, given)
     _call("attn_prompt", desc, device, workspace)
     return (O, lse) if return_lse else O
 
 
 def attention_prompt_workspace(Q, K, V, cu_q, cu_k=None) -> int:
     """Bytes of workspace attention_prompt needs for tensors of these shapes (0: none)."""
-    return _workspace_bytes("attn_prompt", *_prompt_desc(Q, K, V, cu_q, cu_q if cu_k is None else cu_k, True, None, None, None))
+    return _workspace_bytes("attn_prompt", *_prompt_desc(Q, K, V, cu_q, cu_q if cu_k is None else cu_k, True, None, None, None, False))
 
 
-def _shared_desc(Q, Kp, Vp, Ks, Vs, lens, scale, O, lse):
+def _shared_desc(Q, Kp, Vp, Ks, Vs, lens, scale, O, lse, given):
     code, device = _query(Q)
     dtype, shape = Q.dtype, Q.shape
     B, H, d = shape
@@ -232,11 +246,11 @@ def _shared_desc(Q, Kp, Vp, Ks, Vs, lens, scale, O, lse):
         raise ValueError(f"Q, Kp and Ks do not match: {tuple(shape)}, {tuple(kv)}, {tuple(own)}")
     _heads(H, Hk)
     ln = _ints("lens", lens, B, device)
-    q, kp, vp = _strides("Q", Q, shape, dtype, device), _strides("Kp", Kp, kv, dtype, device), _strides("Vp", Vp, kv, dtype, device)
+    q, kp, vp = _steps("Q", Q, shape), _strides("Kp", Kp, kv, dtype, device), _strides("Vp", Vp, kv, dtype, device)
     ks, vs = _strides("Ks", Ks, own, dtype, device), _strides("Vs", Vs, own, dtype, device)
-    os, o = ((H * d, d), 16) if O is None else (_strides("O", O, shape, dtype, device), O.data_ptr())
+    os = _strides("O", O, shape, dtype, device) if given else (H * d, d)
     return _pack_shared_prefix(code, H, Hk, d, B, P, N, Q.data_ptr(), Kp.data_ptr(), Vp.data_ptr(), Ks.data_ptr(),
-                               Vs.data_ptr(), o, 0 if lse is None else lse.data_ptr(), ln, *q, *kp, *vp, *ks, *vs, *os,
+                               Vs.data_ptr(), 16 if O is None else O.data_ptr(), 0 if lse is None else lse.data_ptr(), ln, *q, *kp, *vp, *ks, *vs, *os,
                                _scale(scale, d)), device
 
 
@@ -254,12 +268,13 @@ def attention_shared_prefix(Q, Kp, Vp, Ks, Vs, lens, *, scale=None, O=None, lse=
     Returns O (batch, heads, d), or (O, lse) with `return_lse`, as
     attention_prompt does, with the same `scale`, `O`, `lse` and `workspace`
     (attention_shared_prefix_workspace(...) bytes)."""
+    given = O is not None
     O, lse = _outputs(Q, O, lse, return_lse)
-    desc, device = _shared_desc(Q, Kp, Vp, Ks, Vs, lens, scale, O, lse)
+    desc, device = _shared_desc(Q, Kp, Vp, Ks, Vs, lens, scale, O, lse, given)
     _call("attn_shared_prefix", desc, device, workspace)
     return (O, lse) if return_lse else O
 
 
 def attention_shared_prefix_workspace(Q, Kp, Vp, Ks, Vs, lens) -> int:
     """Bytes of workspace attention_shared_prefix needs for tensors of these shapes (0: none)."""
-    return _workspace_bytes("attn_shared_prefix", *_shared_desc(Q, Kp, Vp, Ks, Vs, lens, None, None, None))
+    return _workspace_bytes("attn_shared_prefix", *_shared_desc(Q, Kp, Vp, Ks, Vs, lens, None, None, None, False))
