@@ -659,8 +659,9 @@ constexpr int kBlockKeys = 32;
 __device__ __forceinline__ int key_blocks(int keys) { return (int)(((int64_t)keys + kBlockKeys - 1) / kBlockKeys); }
 
 // Blocks [block0, block1) of the runs' blocks; row.limit counts keys of the
-// first run.  P goes as N operands (2: its rounding and the rest).
-template <typename T, int D, int N, bool CAREFUL = false>
+// first run.  P goes as N operands (2: its rounding and the rest).  DEAL: how
+// many waves share the blocks (1: each wave has rows and blocks of its own).
+template <typename T, int D, int N, bool CAREFUL = false, int DEAL = kWaves>
 __device__ __forceinline__ void run_blocks(const Job& j, const Keys& one, const Keys& two, int block0, int block1,
                                            const Row& row, char* smem, State<D>& st)
 {
@@ -671,7 +672,7 @@ __device__ __forceinline__ void run_blocks(const Job& j, const Keys& one, const 
     constexpr uint32_t HALF = S::TILE / 2;
     const int lane = threadIdx.x & 63, half = lane >> 5, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     init(st);
-    int at = w < kWaves ? block0 + w : block1;   // a larger workgroup's other waves take none
+    int at = DEAL == 1 ? block0 : w < DEAL ? block0 + w : block1;   // a larger workgroup's other waves take none
     if (at >= block1) return;
     const int first_limit = __builtin_amdgcn_readfirstlane(row.limit);
     const int blocks1 = key_blocks(one.keys);
@@ -707,11 +708,11 @@ __device__ __forceinline__ void run_blocks(const Job& j, const Keys& one, const 
     load_q<D>(j, row, half, q);   // ahead of the blocks: the first wait is for these and K
     load(at, false);
     load(at, true);
-    for (; at < block1; at += kWaves) {
+    for (; at < block1; at += DEAL) {
         landed<NL>();   // K; V may be in flight
         f32x16 s[1] = {scores<T, D>(x, 0, q)};
         landed<NL>();   // K has been read
-        load(at + kWaves, false);
+        load(at + DEAL, false);
         const bool second = at >= blocks1;
         const int key0 = (second ? at - blocks1 : at) * kBlockKeys;
         const int n = (second ? two.keys : one.keys) - key0, lim = row.limit - key0;
@@ -730,7 +731,7 @@ __device__ __forceinline__ void run_blocks(const Job& j, const Keys& one, const 
         else
             accumulate<T, D>(x, HALF, p, st);
         landed<NL>();   // V has been read
-        load(at + kWaves, true);
+        load(at + DEAL, true);
     }
 }
 

@@ -338,6 +338,26 @@ def test_shared_prefix_without_slot_rows(B, heads, kv_heads, P, lens):
         ref.check_rows(O[used, h].cpu(), lse[used, h].cpu(), o, l, parts, lb, torch.float16, f"head {h}")
 
 
+@pytest.mark.parametrize("dtype", sorted(TYPES))
+@pytest.mark.parametrize("B,heads,kv_heads,d,P,N", [(65, 24, 8, 128, 530, 70), (131, 10, 5, 80, 600, 256), (37, 32, 16, 64, 1000, 1),
+                                                    (130, 66, 2, 96, 520, 33)])
+def test_shared_prefix_many_short_slots(B, heads, kv_heads, d, P, N, dtype):
+    # a wave to a slot and kv head; some slots empty, full, longer than there are rows, or not in use
+    gen = torch.Generator().manual_seed(B)
+    lens = [(0, N, 1, -1, N + 5, N // 2, N - 1)[b % 7] for b in range(B)]
+    q, kp, vp, ks, vs = shared_inputs(gen, dtype, B, P, N, heads, kv_heads, d)
+    for b, n in enumerate(lens):
+        ks[b, max(n, 0):] = float("nan")
+        vs[b, max(n, 0):] = float("inf")
+    O, lse = (torch.full((B, heads) + s, 3.0, dtype=t, device=DEV) for s, t in (((d,), TYPES[dtype]), ((), torch.float32)))
+    say(f"[gpu] many short slots B={B} heads={heads}/{kv_heads} d={d} P={P} N={N} {dtype}")
+    g.attention_shared_prefix(*[t.to(DEV) for t in (q, kp, vp, ks, vs)], ints(lens), O=O, lse=lse)
+    torch.cuda.synchronize()
+    ref.shared_prefix(q, kp, vp, ks, vs, lens, d ** -0.5, O.cpu(), lse.cpu(), f"many short slots {dtype} d={d}")
+    for b, n in enumerate(lens):
+        assert n >= 0 or (bool((O[b] == 3).all()) and bool((lse[b] == 3).all()))
+
+
 def test_shared_prefix_slots():
     # unused slots keep their rows, lengths past the slot count as all of it, stale rows hold NaN
     gen = torch.Generator().manual_seed(31)
