@@ -606,8 +606,11 @@ struct PromptPlan {
 };
 
 // Row tiles of one kv head: a packed batch has at most one ragged tile for
-// each sequence (and one sequence no more than its rows fill).  Where all tiles of all kv heads leave compute units without
-// work, the keys are split, at least 256 of them to a part.
+// each sequence (and one sequence no more than its rows fill).  Where all
+// tiles of all kv heads leave compute units without work, the keys are split,
+// at least 256 of them (of a sequence of the batch's mean length) to a part.
+// Splitting uneven batches by the longest sequence they may hold, in parts of
+// at least 256, was no faster: the join costs 5 us and the parts' bytes.
 //
 // Eight waves share a tile of K and V where workgroups are long: they read
 // half as many bytes into LDS, but a compute unit then holds one workgroup,
@@ -616,7 +619,11 @@ struct PromptPlan {
 // against 20000 keys 175 against 185; packed lengths of 333 to 1999 with
 // heads of 96 (16 tiles of keys to a workgroup on average) 50.8 against 46.1,
 // of 1 to 2900 138.7 against 138.3, heads of 64 elements (three workgroups of
-// four waves to a compute unit) 155 against 153.
+// four waves to a compute unit) 155 against 153.  With one workgroup to a
+// compute unit the last round has to be well filled too, 5/6 of all rounds'
+// places: 32 query and 8 key/value heads, causal, 3500 tokens (86%) 98 against
+// 108 us, 5000 (82%) 202 against 195; without a mask 2048 (100%) 64 against 68,
+// 3000 (73%) 156 against 142, 2400 (59%) 128 against 112.
 constexpr int64_t kLongTiles = 24;
 
 PromptPlan plan_prompt(const attn_prompt_desc* d, int cus)
@@ -636,7 +643,10 @@ PromptPlan plan_prompt(const attn_prompt_desc* d, int cus)
     };
     plan(2 * attn::kWaves);
     const int64_t seen = d->causal ? keys - (queries < keys ? queries : keys) / 2 : keys;   // of a row, about
-    if (d->head_dim <= 64 || queries * group < 2 * kTileRows || seen < kLongTiles * kTileKeys * p.splits) plan(attn::kWaves);
+    const int64_t wgs = p.tiles * d->kv_heads * p.splits;
+    const bool full = 6 * wgs >= 5 * cus * ceil_div(wgs, cus);
+    if (d->head_dim <= 64 || queries * group < 2 * kTileRows || !full || seen < kLongTiles * kTileKeys * p.splits)
+        plan(attn::kWaves);
     p.part_bytes = p.splits > 1 ? p.splits * d->total_q * d->heads * (d->head_dim + 2) * 4 : 0;
     return p;
 }

@@ -248,6 +248,44 @@ def test_prompt_infinities_behind_the_mask(n, m, heads, kv_heads, d, dtype):
     ref.prompt(q, k, clean, [0, n], [0, m], True, 1 / math.sqrt(d), torch.where(odd, full, O), lse, "beside the odd values")
 
 
+# Enough rows and keys that eight waves share a tile (on 256 compute units): unsplit, split, and a batch whose short
+# sequences run beside long ones in workgroups of that size.
+LONG = {
+    "unsplit": ([1800], [2700], 32, 16),
+    "split": ([300], [6500], 48, 12),
+    "batch": ([2000, 1, 40, 900, 0], [3500, 3000, 2111, 900, 40], 18, 9),
+}
+
+
+@pytest.mark.parametrize("kind", sorted(LONG))
+@pytest.mark.parametrize("d,dtype", [(128, "fp16"), (96, "bf16"), (120, "bf16")])
+@pytest.mark.parametrize("causal", [True, False])
+def test_prompt_long_workgroups(causal, d, dtype, kind):
+    q_lens, k_lens, heads, kv_heads = LONG[kind]
+    gen = torch.Generator().manual_seed(67 + d)
+    cq, ck = cu(q_lens), cu(k_lens)
+    q, k, v = rand(gen, dtype, cq[-1], heads, d), rand(gen, dtype, ck[-1], kv_heads, d), rand(gen, dtype, ck[-1], kv_heads, d)
+    O, lse = run_prompt(q, k, v, cq, ck, causal)
+    # the 64-bit form for two kv heads
+    G = heads // kv_heads
+    for j in (0, kv_heads - 1):
+        h = slice(j * G, (j + 1) * G)
+        ref.prompt(q[:, h], k[:, j:j + 1], v[:, j:j + 1], cq, ck, causal, d ** -0.5, O[:, h], lse[:, h], f"{kind}, kv head {j}")
+    # a head's result does not depend on the others: the same with two kv heads alone, by smaller workgroups
+    two = [0, kv_heads - 1]
+    hs = [j * G + i for j in two for i in range(G)]
+    O2, lse2 = run_prompt(q[:, hs], k[:, two], v[:, two], cq, ck, causal)
+    # each is off by u of the weights' sum of |v| and u of the output, twice that between them, and as much again for fp32
+    u = torch.finfo(TYPES[dtype]).eps / 2
+    assert bool(((O[:, hs].double() - O2.double()).abs() <= 4 * u * (O2.double().abs() + v.double().abs().max())).all())
+
+
+@pytest.mark.parametrize("kind,d,dtype", [("unsplit", 128, "bf16"), ("split", 96, "fp16")])
+def test_prompt_long_workgroups_with_infinities(kind, d, dtype):
+    (n,), (m,), heads, kv_heads = LONG[kind]
+    test_prompt_infinities_behind_the_mask(n, m, heads, kv_heads, d, dtype)
+
+
 @pytest.mark.parametrize("n,m", [(200, 200), (6, 900)])
 def test_prompt_keys_that_are_not_numbers_behind_the_mask(n, m):
     gen = torch.Generator().manual_seed(n)
