@@ -394,9 +394,17 @@ __global__ __launch_bounds__(kThreads, 2) void shared_kernel(const SharedArgs g)
     }
     const Row row = attn::row_of(j, j.row0 + (lane & 31));
     if (g.solo) {
-        attn::run_blocks<T, D, 1, false, 1>(j, before, mine, block0, block1, row, smem, st);
+        const int head = kv * j.rows + row.head;
+        if (g.together)
+            attn::run_blocks<T, D, 2, false, 1>(j, before, mine, block0, block1, row, smem, st);
+        else
+            attn::run_blocks<T, D, 1, false, 1>(j, before, mine, block0, block1, row, smem, st);
         attn::landed<0>();   // the loads past the last block
-        attn::store_part<D>(st, row.valid, g.d, g.parts, part, slot * g.heads + kv * j.rows + row.head, half);
+        if (g.together)
+            attn::store_row<T, D>(st, row.valid, g.d, g.o + slot * g.o_row + (int64_t)head * g.o_head,
+                                  g.lse == nullptr ? nullptr : g.lse + slot * g.heads + head, half);
+        else
+            attn::store_part<D>(st, row.valid, g.d, g.parts, part, slot * g.heads + head, half);
         return;
     }
     // beside a prefix whose weights are rounded once, so are these
@@ -667,7 +675,10 @@ constexpr int64_t kTogetherBlocks = 16;
 // four waves, and a quarter of the workgroups find their work.  125 x 32 kv
 // heads of 80 with up to 25 own keys behind 1512 shared ones 21.4 against 42.1
 // us; with up to 169 (6 blocks) 86.6 against 87.6, with up to 257 (9 blocks)
-// 22.2 against 21.1.
+// 22.2 against 21.1.  Where a short prefix goes with the slot's own keys a
+// workgroup's waves have to come in two rounds at least: 128 x 8 kv heads, 100
+// and up to 30 keys, 10.6 against 15.0 us, 128 x 32, 200 and up to 25, 31.9
+// against 55.2; but 64 x 8, 130 and up to 90, 13.0 against 10.6.
 constexpr int64_t kSoloBlocks = 8;
 
 struct SharedPlan {
@@ -695,7 +706,8 @@ SharedPlan plan_shared(const attn_shared_prefix_desc* d, int cus)
     p.together = d->batch == 1 || prefix_blocks == 0 || (run_splits <= 1 && prefix_blocks <= kTogetherBlocks);
     if (p.together) {
         p.prefix_splits = run_splits < 1 ? 1 : run_splits;
-        p.own_wgs = jobs * p.prefix_splits;
+        p.own_jobs = jobs * p.prefix_splits;
+        p.solo = p.prefix_splits == 1 && prefix_blocks + slot_blocks <= kSoloBlocks && jobs >= 4 * cus;
     } else {
         const bool few = rows <= attn::kWaveRows;
         p.row_tiles = few ? 1 : ceil_div(rows, kTileRows);
@@ -712,8 +724,8 @@ SharedPlan plan_shared(const attn_shared_prefix_desc* d, int cus)
         p.own_splits = ceil_div(slot_blocks, p.own_blocks);
         p.own_jobs = jobs * p.own_splits;
         p.solo = !few && p.own_splits == 1 && slot_blocks <= kSoloBlocks && jobs >= 2 * cus;
-        p.own_wgs = p.solo ? ceil_div(p.own_jobs, attn::kWaves) : p.own_jobs;
     }
+    p.own_wgs = p.solo ? ceil_div(p.own_jobs, attn::kWaves) : p.own_jobs;
     p.round_prefix = p.prefix_wgs < cus ? p.prefix_wgs : cus;
     p.rounds = p.prefix_wgs == 0 ? 1 : ceil_div(p.prefix_wgs, p.round_prefix);
     p.round_own = ceil_div(p.own_wgs, p.rounds);

@@ -396,6 +396,13 @@ def test_shared_prefix_many_short_slots(B, heads, kv_heads, d, P, N, dtype):
         assert n >= 0 or (bool((O[b] == 3).all()) and bool((lse[b] == 3).all()))
 
 
+@pytest.mark.parametrize("dtype", sorted(TYPES))
+@pytest.mark.parametrize("B,heads,kv_heads,d,P,N", [(65, 32, 16, 128, 61, 40), (131, 16, 8, 80, 0, 200), (33, 32, 32, 64, 200, 30),
+                                                    (65, 264, 8, 96, 33, 1), (128, 8, 8, 128, 256, 0)])
+def test_shared_prefix_many_slots_behind_a_short_prefix(B, heads, kv_heads, d, P, N, dtype):
+    test_shared_prefix_many_short_slots(B, heads, kv_heads, d, P, N, dtype)
+
+
 def test_shared_prefix_slots():
     # unused slots keep their rows, lengths past the slot count as all of it, stale rows hold NaN
     gen = torch.Generator().manual_seed(31)
