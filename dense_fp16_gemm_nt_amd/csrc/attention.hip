@@ -46,7 +46,7 @@ struct PromptArgs {
     Div group, splits, units;   // units: kv heads x splits, or an eighth of them (by_xcd)
     Div join_kv;                // kv heads
     int by_xcd;
-    float c;
+    float c, slack;
     uint32_t flip;
     int zero_q;
     Parts parts;
@@ -164,6 +164,7 @@ __device__ __forceinline__ Job prompt_job(const PromptArgs& g, const Tile& t, in
     j.lead = g.causal ? t.nk - t.nq : INT32_MAX;
     j.d = g.d;
     j.c = g.c;
+    j.slack = g.slack;
     j.flip = g.flip;
     j.zero_q = g.zero_q != 0;
     j.most = t.nk;
@@ -209,7 +210,7 @@ __global__ __launch_bounds__(64 * W, D == 64 && W == 4 ? 3 : 2) void prompt_kern
             attn::landed<0>();
             attn::run_blocks<T, D, 2, true>(j, keys, none, r.first, r.last, row, smem, st);
         }
-        attn::merge_waves<D>(st, row.valid, rows, g.d, smem, [&](int y, int e, float m, float l, f32x4 o) {
+        attn::merge_waves<D>(j, st, row.valid, rows, smem, [&](int y, int e, float m, float l, f32x4 o) {
             const int x = j.row0 + y, token_in = (int)g.group.of(x);
             const int64_t token = (int64_t)tile.q0 + token_in;
             const int head = kv * (int)g.group.d + x - token_in * (int)g.group.d;
@@ -217,7 +218,7 @@ __global__ __launch_bounds__(64 * W, D == 64 && W == 4 ? 3 : 2) void prompt_kern
                 attn::store_part4(g.parts, split, token * g.heads + head, g.d, e, m, l, o);
             else
                 attn::store_row4<T>(g.o + token * g.o_row + head * g.o_head,
-                                    g.lse == nullptr ? nullptr : g.lse + token * g.heads + head, e, m, l, o);
+                                    g.lse == nullptr ? nullptr : g.lse + token * g.heads + head, g.c, e, m, l, o);
         });
         return;
     }
@@ -233,7 +234,7 @@ __global__ __launch_bounds__(64 * W, D == 64 && W == 4 ? 3 : 2) void prompt_kern
     if constexpr (SPLIT)
         attn::store_part<D>(st, row.valid, g.d, g.parts, split, token * g.heads + head, half);
     else
-        attn::store_row<T, D>(st, row.valid, g.d, g.o + token * g.o_row + head * g.o_head,
+        attn::store_row<T, D>(j, st, row.valid, g.o + token * g.o_row + head * g.o_head,
                               g.lse == nullptr ? nullptr : g.lse + token * g.heads + head, half);
 }
 
@@ -254,7 +255,7 @@ __global__ __launch_bounds__(kThreads) void prompt_join_kernel(const PromptArgs 
     const int token_in = (int)g.group.of(r);
     const int64_t token = (int64_t)tile.q0 + token_in;
     const int head = kv * (int)g.group.d + r - token_in * (int)g.group.d;
-    attn::join_row<T, GROUPS>(g.parts, (int)g.splits.d, there, token * g.heads + head, g.d, e,
+    attn::join_row<T, GROUPS>(g.parts, (int)g.splits.d, there, token * g.heads + head, g.c, g.d, e,
                               g.o + token * g.o_row + head * g.o_head,
                               g.lse == nullptr ? nullptr : g.lse + token * g.heads + head);
 }
@@ -281,7 +282,7 @@ struct SharedArgs {
     int rounded;          // the prefix goes through row tiles
     int solo;             // a wave takes what a workgroup would of the slots' own keys
     uint32_t own_jobs;    // of these
-    float c;
+    float c, slack;
     uint32_t flip;
     int zero_q;
     Parts parts;
@@ -310,6 +311,7 @@ __global__ __launch_bounds__(kThreads, 2) void shared_kernel(const SharedArgs g)
     j.lead = INT32_MAX;
     j.d = g.d;
     j.c = g.c;
+    j.slack = g.slack;
     j.flip = g.flip;
     j.zero_q = g.zero_q != 0;
     State<D> st;
@@ -338,7 +340,7 @@ __global__ __launch_bounds__(kThreads, 2) void shared_kernel(const SharedArgs g)
             const Keys keys = {j.k, j.v, j.k_row, j.v_row, j.keys}, none = {};
             const Range r = part_of(attn::key_blocks(g.prefix), g.prefix_splits, part);
             attn::run_blocks<T, D, 2>(j, keys, none, r.first, r.last, row, smem, st);
-            attn::merge_waves<D>(st, row.valid, j.rows, g.d, smem, [&](int r, int e, float m, float l, f32x4 o) {
+            attn::merge_waves<D>(j, st, row.valid, j.rows, smem, [&](int r, int e, float m, float l, f32x4 o) {
                 const int b = (int)g.group.of(r);
                 const int64_t x = (int64_t)b * g.heads + kv * (int)g.group.d + r - b * (int)g.group.d;
                 attn::store_part4(g.parts, part, x, g.d, e, m, l, o);
@@ -401,7 +403,7 @@ __global__ __launch_bounds__(kThreads, 2) void shared_kernel(const SharedArgs g)
             attn::run_blocks<T, D, 1, false, 1>(j, before, mine, block0, block1, row, smem, st);
         attn::landed<0>();   // the loads past the last block
         if (g.together)
-            attn::store_row<T, D>(st, row.valid, g.d, g.o + slot * g.o_row + (int64_t)head * g.o_head,
+            attn::store_row<T, D>(j, st, row.valid, g.o + slot * g.o_row + (int64_t)head * g.o_head,
                                   g.lse == nullptr ? nullptr : g.lse + slot * g.heads + head, half);
         else
             attn::store_part<D>(st, row.valid, g.d, g.parts, part, slot * g.heads + head, half);
@@ -412,10 +414,10 @@ __global__ __launch_bounds__(kThreads, 2) void shared_kernel(const SharedArgs g)
         attn::run_blocks<T, D, 1>(j, before, mine, block0, block1, row, smem, st);
     else
         attn::run_blocks<T, D, 2>(j, before, mine, block0, block1, row, smem, st);
-    attn::merge_waves<D>(st, row.valid, rows, g.d, smem, [&](int r, int e, float m, float l, f32x4 o) {
+    attn::merge_waves<D>(j, st, row.valid, rows, smem, [&](int r, int e, float m, float l, f32x4 o) {
         if (g.parts_of_row == 1)
             attn::store_row4<T>(g.o + slot * g.o_row + (int64_t)(kv * j.rows + j.row0 + r) * g.o_head,
-                                g.lse == nullptr ? nullptr : g.lse + x0 + r, e, m, l, o);
+                                g.lse == nullptr ? nullptr : g.lse + x0 + r, g.c, e, m, l, o);
         else
             attn::store_part4(g.parts, part, x0 + r, g.d, e, m, l, o);
     });
@@ -429,7 +431,7 @@ __global__ __launch_bounds__(kThreads) void shared_join_kernel(const SharedArgs 
     const int64_t b = x / g.heads;
     const bool there = b < g.batch && e < g.d && g.lens[b] >= 0;
     const int64_t head = x - b * g.heads;
-    attn::join_row<T, GROUPS>(g.parts, g.parts_of_row, there, x, g.d, e, g.o + b * g.o_row + head * g.o_head,
+    attn::join_row<T, GROUPS>(g.parts, g.parts_of_row, there, x, g.c, g.d, e, g.o + b * g.o_row + head * g.o_head,
                               g.lse == nullptr ? nullptr : g.lse + x);
 }
 
@@ -519,7 +521,7 @@ bool rows_apart(int64_t rows, int64_t row, int64_t heads, int64_t head, int64_t 
 }
 
 struct Scale {
-    float c;
+    float c, slack;
     uint32_t flip;
     int zero;
 };
@@ -530,8 +532,8 @@ struct Scale {
 Scale scale_of(float scale)
 {
     const float c = std::fabs(scale) * 1.4426950408889634f;
-    if (c < FLT_MIN) return {1.f, 0u, 1};
-    return {c, scale < 0.f ? 0x80008000u : 0u, 0};
+    if (c < FLT_MIN) return {1.f, attn::kSlack, 0u, 1};
+    return {c, attn::kSlack / c, scale < 0.f ? 0x80008000u : 0u, 0};
 }
 
 int check_prompt(const attn_prompt_desc* d)
@@ -861,6 +863,7 @@ int attn_prompt(const attn_prompt_desc* d, void* workspace, int64_t workspace_by
     g.splits = attn::div_by(p.splits);
     g.join_kv = attn::div_by(d->kv_heads);
     g.c = sc.c;
+    g.slack = sc.slack;
     g.flip = sc.flip;
     g.zero_q = sc.zero;
     g.parts = parts_in(workspace, p.splits, d->total_q * d->heads);
@@ -944,6 +947,7 @@ int attn_shared_prefix(const attn_shared_prefix_desc* d, void* workspace, int64_
     g.by_xcd = d->kv_heads * p.prefix_splits % kNumXcd == 0;
     g.rounded = !p.together && d->batch * (d->heads / d->kv_heads) > attn::kWaveRows;
     g.c = sc.c;
+    g.slack = sc.slack;
     g.flip = sc.flip;
     g.zero_q = sc.zero;
     g.parts = parts_in(workspace, p.prefix_splits + p.own_splits, d->batch * d->heads);

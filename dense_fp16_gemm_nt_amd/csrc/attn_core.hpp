@@ -11,13 +11,19 @@
 // to match (ds_read_b64_tr_b16 transposes 4 keys x 16 elements on the way
 // out of LDS).  P therefore never passes through LDS.
 //
-// Softmax runs in base 2: p = 2^(c s - (m - kShift)), c = scale * log2 e,
-// with m a running row maximum of c s.  m is raised only where a tile's
-// maximum exceeds it by more than kSlack, so most tiles skip the rescaling of
-// the accumulator (64 multiplications); p then reaches at most
+// Softmax runs in base 2: p = 2^(c (s - m) + kShift), c = scale * log2 e,
+// with m a running row maximum of the scores s = q . k.  m is raised only where
+// a tile's maximum exceeds it by more than kSlack / c, so most tiles skip the
+// rescaling of the accumulator (64 multiplications); p then reaches at most
 // 2^(kShift + kSlack) = 2^15, inside fp16.  kShift = 7 keeps weights down to
 // 2^-31 of the largest above fp16's smallest subnormal (2^-24).  Numerator
 // and denominator carry the same factor.
+//
+// The exponent is one fused c s + (kShift - c m), whose second part is rounded
+// once for a raised m.  That is off by half a step of c m, which for |c m| up to
+// kFar is at most 2^-14.  Where a row's maximum is farther from 0 (a step of
+// fp32 is 64 at 10^9, and a weight 2^64 times off) its scores are taken as
+// s - m first.
 //
 // Rounding: scores, maxima, sums and the output accumulate in fp32.  P is
 // rounded once to the operands' 16-bit type because the matrix cores take no
@@ -47,6 +53,7 @@ constexpr int kTileRows = kWaveRows * kWaves;
 constexpr int kThreads = 64 * kWaves;
 constexpr float kShift = 7.0f;
 constexpr float kSlack = 8.0f;
+constexpr float kFar = 1024.0f;   // 2^10
 constexpr float kLn2 = 0.693147180559945309f;
 
 struct F16 {
@@ -169,7 +176,7 @@ struct Job {
     int most;            // keys that the last row may read
     int tile0, tile1;
     int d;               // head size
-    float c;             // |scale| * log2 e
+    float c, slack;      // |scale| * log2 e, and kSlack / c
     uint32_t flip;       // sign bits flipped in Q (a negative scale)
     bool zero_q;         // scale = 0: every score is 0
 };
@@ -339,26 +346,28 @@ __device__ __forceinline__ void mask(f32x16& s, int keys, int half)
     for (int i = 0; i < 16; ++i) s[i] = (8 * (i / 4) + i % 4) < n ? s[i] : -__builtin_inff();
 }
 
-// One row's running state: m (base 2), the lane's part of the sum, O^T.
+// One row's running state: the maximum m of its scores, the score above which
+// m is raised, kShift - c m, the lane's part of the sum, O^T.  A row whose m is
+// far from 0 has `over` = -inf and `base` = kShift.
 template <int D>
 struct State {
-    float m, l;
+    float m, over, base, l;
     f32x16 o[Shape<D>::DBLOCKS];
 };
 
 template <int D>
 __device__ __forceinline__ void init(State<D>& st)
 {
-    st.m = -__builtin_inff();
+    st.m = st.over = -__builtin_inff();
+    st.base = 0.f;   // until there is a key every score is -inf
     st.l = 0.f;
 #pragma unroll
     for (int b = 0; b < Shape<D>::DBLOCKS; ++b) st.o[b] = f32x16{};
 }
 
-// The maximum of a row's scores (of 32 keys for each block), in the units of
-// m.  A tree: a chain would wait for each instruction's result in turn.
+// The maximum of a row's scores (of 32 keys for each block).  A tree: a chain would wait for each instruction's result in turn.
 template <int N>
-__device__ __forceinline__ float top_score(const f32x16 (&s)[N], float c)
+__device__ __forceinline__ float top_score(const f32x16 (&s)[N])
 {
     float a[5 * N], b = s[0][15];
 #pragma unroll
@@ -373,23 +382,43 @@ __device__ __forceinline__ float top_score(const f32x16 (&s)[N], float c)
         const float x = max3(a[0], a[1], a[2]), y = max3(a[3], a[4], a[5]), z = max3(a[6], a[7], a[8]);
         b = max3(b, a[9], max3(x, y, z));
     }
-    return max_halves(b) * c;
+    return max_halves(b);
 }
 
 // Raises a row's maximum where a tile's asks for it, and rescales what was
-// summed so far.  Each row goes by its own maximum alone, so a row's bits do
-// not depend on the rows that share its wave.
-template <int D>
-__device__ __forceinline__ void raise(float mx, State<D>& st)
+// summed so far; the tile's scores of a row far from 0 become s - m.  Each row
+// goes by its own maximum alone, so a row's bits do not depend on the rows that
+// share its wave.
+template <int D, int N>
+__device__ __forceinline__ void raise(const Job& j, float mx, f32x16 (&s)[N], State<D>& st)
 {
-    const float m = mx > st.m + kSlack ? mx : st.m;
-    const float a = m == st.m ? 1.f : exp2_(st.m - m);
+    const bool up = mx > st.over;
+    const float m = up ? __builtin_fmaxf(mx, st.m) : st.m;
+    const float a = m == st.m ? 1.f : exp2_((st.m - m) * j.c);
+    const bool far = up && !(__builtin_fabsf(m * j.c) <= kFar);   // a row far from 0 has every tile with a key raise it
+    if (up) {
+        st.over = far ? -__builtin_inff() : m + j.slack;
+        st.base = far ? kShift : __builtin_fmaf(-m, j.c, kShift);
+    }
     st.m = m;
     st.l *= a;
+    const float off = far ? m : 0.f;
+#pragma unroll
+    for (int b = 0; b < N; ++b)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) s[b][i] -= off;
 #pragma unroll
     for (int b = 0; b < Shape<D>::DBLOCKS; ++b)
 #pragma unroll
         for (int i = 0; i < 16; ++i) st.o[b][i] *= a;
+}
+
+// What every tile of keys begins with.
+template <int D, int N>
+__device__ __forceinline__ void follow(const Job& j, f32x16 (&s)[N], State<D>& st)
+{
+    const float mx = top_score(s);
+    if (__builtin_amdgcn_ballot_w64(mx > st.over) != 0) raise<D>(j, mx, s, st);
 }
 
 // Softmax weights of 32 keys: P^T as B operands p[kk] of the keys 16 kk ..
@@ -401,8 +430,7 @@ __device__ __forceinline__ void raise(float mx, State<D>& st)
 template <typename T, int D, bool LEAN = false>
 __device__ __forceinline__ void weights(const f32x16& s, float c, State<D>& st, u32x4 (&p)[2])
 {
-    const float base = st.m == -__builtin_inff() ? 0.f : kShift - st.m;
-    auto weight = [&](int i) { return exp2_(__builtin_fmaf(s[i], c, base)); };
+    auto weight = [&](int i) { return exp2_(__builtin_fmaf(s[i], c, st.base)); };
     if constexpr (LEAN) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
@@ -429,10 +457,9 @@ __device__ __forceinline__ void weights(const f32x16& s, float c, State<D>& st, 
 template <typename T, int D>
 __device__ __forceinline__ void weights_whole(const f32x16& s, float c, State<D>& st, u32x4 (&p)[2][2])
 {
-    const float base = st.m == -__builtin_inff() ? 0.f : kShift - st.m;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        const float x = exp2_(__builtin_fmaf(s[2 * i], c, base)), y = exp2_(__builtin_fmaf(s[2 * i + 1], c, base));
+        const float x = exp2_(__builtin_fmaf(s[2 * i], c, st.base)), y = exp2_(__builtin_fmaf(s[2 * i + 1], c, st.base));
         st.l += x + y;
         const uint32_t r = T::pack(x, y);
         const f32x2 z = T::unpack(r);
@@ -579,8 +606,7 @@ __device__ __forceinline__ void run_tiles(const Job& j, const Row& row, char* sm
             mask(a[0], row.limit - t * kTileKeys, half);
             mask(a[1], row.limit - t * kTileKeys - 32, half);
         }
-        const float mx = top_score(a, j.c);
-        if (__builtin_amdgcn_ballot_w64(mx > st.m + kSlack) != 0) raise<D>(mx, st);
+        follow<D>(j, a, st);
         u32x4 p0[1][2], p1[1][2];
         weights<T, D, D == 64>(a[0], j.c, st, p0[0]);
         weights<T, D, D == 64>(a[1], j.c, st, p1[0]);
@@ -619,8 +645,7 @@ __device__ __forceinline__ void run_tiles_careful(const Job& j, const Row& row, 
             const int keys = row.limit - t * kTileKeys - 32 * b;
             f32x16 s[1] = {scores<T, D>(x, b * (S::TILE / 2), q)};
             mask(s[0], keys, half);
-            const float mx = top_score(s, j.c);
-            if (__builtin_amdgcn_ballot_w64(mx > st.m + kSlack) != 0) raise<D>(mx, st);
+            follow<D>(j, s, st);
             u32x4 p[1][2];
             weights<T, D>(s[0], j.c, st, p[0]);
             accumulate_careful<T, D>(x, S::TILE + b * (S::TILE / 2), p, keys, half, st);
@@ -718,8 +743,7 @@ __device__ __forceinline__ void run_blocks(const Job& j, const Keys& one, const 
         const int n = (second ? two.keys : one.keys) - key0, lim = row.limit - key0;
         const int readable = second || n < lim ? n : lim;
         if (n < kBlockKeys || (!second && key0 + kBlockKeys > first_limit)) mask(s[0], readable, half);
-        const float mx = top_score(s, j.c);
-        if (__builtin_amdgcn_ballot_w64(mx > st.m + kSlack) != 0) raise<D>(mx, st);
+        follow<D>(j, s, st);
         u32x4 p[N][2];
         if constexpr (N == 2)
             weights_whole<T, D>(s[0], j.c, st, p);
@@ -735,8 +759,8 @@ __device__ __forceinline__ void run_blocks(const Job& j, const Keys& one, const 
     }
 }
 
-// Partial results of a split job: for row x (of n) and part s, m and l at
-// ml[(s n + x) 2] and the unscaled O at o[(s n + x) d].
+// Partial results of a split job: for row x (of n) and part s, m (a score) and
+// l at ml[(s n + x) 2] and the unscaled O at o[(s n + x) d].
 struct Parts {
     float* ml;
     float* o;
@@ -750,9 +774,9 @@ __device__ __forceinline__ void store4(char* o, int e, f32x4 x)
     *reinterpret_cast<u32x2*>(o + 2 * e) = u32x2{T::pack(x[0], x[1]), T::pack(x[2], x[3])};
 }
 __device__ __forceinline__ float inverse(float l) { return l == 0.f ? 0.f : 1.f / l; }
-__device__ __forceinline__ float lse_of(float m, float l)
+__device__ __forceinline__ float lse_of(float m, float l, float c)
 {
-    return l == 0.f ? -__builtin_inff() : (m - kShift + __builtin_log2f(l)) * kLn2;
+    return l == 0.f ? -__builtin_inff() : __builtin_fmaf(m, c, __builtin_log2f(l) - kShift) * kLn2;
 }
 
 // Calls f(e, block, group) for a lane's groups of accumulator registers that
@@ -779,7 +803,7 @@ __device__ __forceinline__ void each_group(int d, int half, F f)
 // l + 32 hold the two halves of each 8 elements; they exchange halves of two
 // groups, so that each stores 16 bytes.
 template <typename T, int D>
-__device__ __forceinline__ void store_row(const State<D>& st, bool valid, int d, char* o, float* lse, int half)
+__device__ __forceinline__ void store_row(const Job& j, const State<D>& st, bool valid, char* o, float* lse, int half)
 {
     const float l = sum_halves(st.l), inv = inverse(l);
     u32x4 x[Shape<D>::DBLOCKS][2];
@@ -797,8 +821,8 @@ __device__ __forceinline__ void store_row(const State<D>& st, bool valid, int d,
                 x[b][g / 2][i + 2] = z[1];
             }
     if (!valid) return;
-    each_group<D, 2>(d, half, [&](int e, int b, int g) { *reinterpret_cast<u32x4*>(o + 2 * e) = x[b][g / 2]; });
-    if (lse != nullptr && half == 0) *lse = lse_of(st.m, l);
+    each_group<D, 2>(j.d, half, [&](int e, int b, int g) { *reinterpret_cast<u32x4*>(o + 2 * e) = x[b][g / 2]; });
+    if (lse != nullptr && half == 0) *lse = lse_of(st.m, l, j.c);
 }
 
 template <int D>
@@ -818,11 +842,11 @@ __device__ __forceinline__ void store_part(const State<D>& st, bool valid, int d
 
 // Four elements of a row whose sums are complete: the output, or a part.
 template <typename T>
-__device__ __forceinline__ void store_row4(char* o, float* lse, int e, float m, float l, f32x4 x)
+__device__ __forceinline__ void store_row4(char* o, float* lse, float c, int e, float m, float l, f32x4 x)
 {
     const float inv = inverse(l);
     store4<T>(o, e, f32x4{x[0] * inv, x[1] * inv, x[2] * inv, x[3] * inv});
-    if (lse != nullptr && e == 0) *lse = lse_of(m, l);
+    if (lse != nullptr && e == 0) *lse = lse_of(m, l, c);
 }
 __device__ __forceinline__ void store_part4(const Parts& w, int part, int64_t row, int d, int e, float m, float l, f32x4 x)
 {
@@ -834,7 +858,7 @@ __device__ __forceinline__ void store_part4(const Parts& w, int part, int64_t ro
 // Adds up what the four waves hold of the same rows and hands every four
 // elements of a row that is there to store(r, e, m, l, o).
 template <int D, typename F>
-__device__ __forceinline__ void merge_waves(const State<D>& st, bool valid, int rows, int d, char* smem, F store)
+__device__ __forceinline__ void merge_waves(const Job& j, const State<D>& st, bool valid, int rows, char* smem, F store)
 {
     constexpr int PITCH = D + kMergePad;
     const int tid = threadIdx.x, lane = tid & 63, half = lane >> 5, r = lane & 31;
@@ -856,7 +880,7 @@ __device__ __forceinline__ void merge_waves(const State<D>& st, bool valid, int 
     if (half == 0 && w < kWaves) ml[w * kWaveRows + r] = f32x2{st.m, l};
     publish();
     if (valid && w < kWaves) {
-        const float f = exp2_(st.m - top(r));
+        const float f = exp2_((st.m - top(r)) * j.c);
         const bool some = l != 0.f;
         float* to = o + (w * kWaveRows + r) * PITCH;
 #pragma unroll
@@ -870,14 +894,14 @@ __device__ __forceinline__ void merge_waves(const State<D>& st, bool valid, int 
     publish();
     for (int i = tid; i < rows * (D / 4); i += blockDim.x) {
         const int row = i / (D / 4), e = i % (D / 4) * 4;
-        if (e >= d) continue;
+        if (e >= j.d) continue;
         const float m = top(row);
         float sum = 0.f;
         f32x4 x = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int k = 0; k < kWaves; ++k) {
             const f32x2 y = ml[k * kWaveRows + row];
-            sum += y[1] == 0.f ? 0.f : exp2_(y[0] - m) * y[1];
+            sum += y[1] == 0.f ? 0.f : exp2_((y[0] - m) * j.c) * y[1];
             const f32x4 z = *reinterpret_cast<const f32x4*>(o + (k * kWaveRows + row) * PITCH + e);
 #pragma unroll
             for (int c = 0; c < 4; ++c) x[c] += z[c];
@@ -891,7 +915,7 @@ __device__ __forceinline__ void merge_waves(const State<D>& st, bool valid, int 
 // the first group stores.  All threads of the workgroup call it; `there` says
 // whether the lane has a row and elements.
 template <typename T, int GROUPS>
-__device__ __forceinline__ void join_row(const Parts& w, int parts, bool there, int64_t x, int d, int e, char* o, float* lse)
+__device__ __forceinline__ void join_row(const Parts& w, int parts, bool there, int64_t x, float c, int d, int e, char* o, float* lse)
 {
     const int tid = threadIdx.x, grp = (tid >> 5) % GROUPS;
     if (!there) {
@@ -912,7 +936,7 @@ __device__ __forceinline__ void join_row(const Parts& w, int parts, bool there, 
         const f32x2 ml = *reinterpret_cast<const f32x2*>(w.ml + 2 * at);
         const f32x4 y = *reinterpret_cast<const f32x4*>(w.o + at * d + e);
         const bool some = ml[1] != 0.f;   // otherwise O holds whatever was there
-        const float f = exp2_(ml[0] - m);
+        const float f = exp2_((ml[0] - m) * c);
         l += some ? f * ml[1] : 0.f;
 #pragma unroll
         for (int i = 0; i < 4; ++i) acc[i] += some ? f * y[i] : 0.f;
@@ -933,13 +957,13 @@ __device__ __forceinline__ void join_row(const Parts& w, int parts, bool there, 
 #pragma unroll
         for (int i = 0; i < GROUPS; ++i) {
             const f32x2 ml = mls[first + i];
-            const float f = ml[1] == 0.f ? 0.f : exp2_(ml[0] - m);
+            const float f = ml[1] == 0.f ? 0.f : exp2_((ml[0] - m) * c);
             l += f * ml[1];
 #pragma unroll
-            for (int c = 0; c < 4; ++c) acc[c] += f * sums[tid + 32 * i][c];
+            for (int k = 0; k < 4; ++k) acc[k] += f * sums[tid + 32 * i][k];
         }
     }
-    if (there) store_row4<T>(o, lse, e, m, l, acc);
+    if (there) store_row4<T>(o, lse, c, e, m, l, acc);
 }
 
 }  // namespace attn

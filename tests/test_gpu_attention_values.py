@@ -1,0 +1,153 @@
+"""The attention operators far from ordinary values, each on every way that a call can take through the kernels."""
+import math
+import sys
+
+import pytest
+
+import dense_fp16_gemm_nt_amd as g
+from tests import attention_ref as ref
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+DEV = "cuda:0"
+TYPES = {"fp16": torch.float16, "bf16": torch.bfloat16}
+
+# (queries, keys, heads, kv heads, d, causal) of one prompt
+PROMPTS = {
+    "tiles": (150, 210, 4, 2, 128, True),
+    "tiles, no mask": (150, 210, 2, 2, 64, False),
+    "tiles, parts": (200, 1500, 2, 1, 96, False),
+    "eight waves": (2048, 3001, 32, 32, 128, True),
+    "eight waves, parts": (2048, 4099, 16, 16, 96, False),
+    "few rows": (5, 170, 4, 1, 64, True),
+    "few rows, parts": (3, 3001, 4, 2, 128, False),
+}
+# (batch, prefix, slot rows, heads, kv heads, d)
+SHARED = {
+    "one run": (3, 100, 70, 8, 2, 128),
+    "one run, a wave each": (65, 61, 40, 32, 16, 64),
+    "one run, parts": (1, 3001, 5, 4, 1, 96),
+    "few rows": (4, 2000, 40, 4, 2, 64),
+    "row tiles": (40, 1000, 300, 4, 2, 128),
+    "row tiles, a wave each": (131, 600, 60, 10, 5, 80),
+}
+
+
+def ints(x):
+    return torch.tensor(x, dtype=torch.int32, device=DEV)
+
+
+def lens_of(B, N):
+    return [(N, 1, N // 2, N - 1, N + 3)[b % 5] for b in range(B)]
+
+
+class Case:
+    """One call: its keys laid out as the operator takes them, and for each kv head the plain problems it stands for."""
+
+    def __init__(self, way):
+        self.way = way
+        kind, name = way.split(": ")
+        self.prompt = kind == "prompt"
+        if self.prompt:
+            self.n, self.m, self.heads, self.kv_heads, self.d, self.causal = PROMPTS[name]
+            self.rows, self.keys = self.n, self.m
+        else:
+            self.B, self.P, self.N, self.heads, self.kv_heads, self.d = SHARED[name]
+            self.rows, self.keys = self.B, self.P + self.B * self.N
+        self.G = self.heads // self.kv_heads
+
+    def run(self, q, k, v, scale, **kw):
+        """q (rows, heads, d), k and v (keys, kv heads, d) on the host; a batch's keys are the prefix, then the slots."""
+        print(f"[gpu] {self.way} {q.dtype} scale {scale}", file=sys.stderr, flush=True)
+        q, k, v = (x.to(DEV) for x in (q, k, v))
+        if self.prompt:
+            O, lse = g.attention_prompt(q, k, v, ints([0, self.n]), ints([0, self.m]), causal=self.causal, scale=scale,
+                                        return_lse=True, **kw)
+        else:
+            def slots(x):
+                return x[self.P:].reshape(self.B, self.N, self.kv_heads, self.d)
+            O, lse = g.attention_shared_prefix(q, k[:self.P], v[:self.P], slots(k), slots(v), ints(lens_of(self.B, self.N)),
+                                               scale=scale, return_lse=True, **kw)
+        torch.cuda.synchronize()
+        return O.cpu(), lse.cpu()
+
+    def problems(self, q, k, v):
+        """(rows of O, heads, q, k, v, allowed) in 64 bits; of many heads and rows a few."""
+        for j in sorted({0, self.kv_heads - 1}):
+            h = slice(j * self.G, (j + 1) * self.G)
+            if self.prompt:
+                rows = torch.arange(self.n) if self.n <= 300 else torch.arange(self.n - 150, self.n)
+                qq = q[rows][:, h].double().reshape(-1, self.d)
+                allowed = torch.ones(len(rows), self.m, dtype=torch.bool)
+                if self.causal:
+                    allowed = torch.arange(self.m)[None, :] <= rows[:, None] + (self.m - self.n)
+                yield rows, h, qq, k[:, j].double(), v[:, j].double(), allowed.repeat_interleave(self.G, 0)
+                continue
+            for b, n in enumerate(lens_of(self.B, self.N)):
+                if b % 7 not in (0, 1, 4) and b != self.B - 1:
+                    continue
+                at = self.P + b * self.N
+                kk, vv = (torch.cat([x[:self.P, j], x[at:at + min(n, self.N), j]]).double() for x in (k, v))
+                yield torch.tensor([b]), h, q[b, h].double(), kk, vv, torch.ones(self.G, kk.shape[0], dtype=torch.bool)
+
+
+WAYS = [f"prompt: {x}" for x in PROMPTS] + [f"shared: {x}" for x in SHARED]
+
+
+def rand(gen, dtype, *shape):
+    return torch.randn(*shape, generator=gen, dtype=torch.float32).to(TYPES[dtype])
+
+
+def check(case, q, k, v, scale, O, lse, e_weight=None):
+    """Against the 64-bit form.  e_weight: how far a weight may be off, relative, where the scores are exact."""
+    for rows, h, qq, kk, vv, allowed in case.problems(q, k, v):
+        o, l, parts, lb = ref.attend(qq, kk, vv, scale, allowed)
+        if e_weight is not None:
+            mass = parts[0]
+            parts = (mass, (e_weight + 2 * (kk.shape[0] + 8) * 2.0 ** -22) * mass + allowed.double() @ vv.abs() * 2.0 ** -32)
+        ref.check_rows(O[rows][:, h].reshape(-1, case.d), lse[rows][:, h].reshape(-1), o, l, parts, lb, q.dtype, case.way)
+
+
+# ---------------------------------------------------------------- large scores
+@pytest.mark.parametrize("x", [5748, 16256, -65504])
+@pytest.mark.parametrize("dtype", sorted(TYPES))
+@pytest.mark.parametrize("way", WAYS)
+def test_equal_large_scores(way, dtype, x):
+    """All scores of a row are the same 10^8 to 10^11 in size: its weights are the same, whatever an fp32 step is there."""
+    case = Case(way)
+    gen = torch.Generator().manual_seed(71)
+    q = torch.full((case.rows, case.heads, case.d), float(abs(x))).to(TYPES[dtype])
+    k = torch.full((case.keys, case.kv_heads, case.d), float(x)).to(TYPES[dtype])
+    v = rand(gen, dtype, case.keys, case.kv_heads, case.d)
+    O, lse = case.run(q, k, v, None)
+    check(case, q, k, v, case.d ** -0.5, O, lse, 2.0 ** -20)
+
+
+@pytest.mark.parametrize("far", [2048, -2048])
+@pytest.mark.parametrize("dtype", sorted(TYPES))
+@pytest.mark.parametrize("way", WAYS)
+def test_large_scores_that_rise(way, dtype, far):
+    """Scores of +-2^22 plus whole numbers that rise from key to key, every one exact in fp32, so that softmax goes by
+    their differences.  Every second row has ordinary scores.
+
+    A weight's exponent x = (score - maximum) log2 e is off by 3 roundings of 2^-24 |x|, where |x| <= 40 counts: 2^-17 of
+    the weight, with the exponential and the rescalings of a running maximum, which fall by 2^-8 each."""
+    case = Case(way)
+    gen = torch.Generator().manual_seed(73)
+    q = torch.zeros(case.rows, case.heads, case.d)
+    q[..., 0], q[..., 1], q[..., 2] = far, 256, 1
+    q[1::2, :, :2] = 0
+    q[1::2, :, 2] = 1 / 64
+    level = torch.arange(case.keys)
+    if not case.prompt:   # the slots go on from the prefix's last key
+        level[case.P:] = case.P + (level[case.P:] - case.P) % case.N
+    level = (level // 3)[:, None] + torch.randint(0, 6, (case.keys, case.kv_heads), generator=gen)
+    k = torch.zeros(case.keys, case.kv_heads, case.d)
+    k[..., 0], k[..., 1], k[..., 2] = 2048, level // 256, level % 256
+    q, k = q.to(TYPES[dtype]), k.to(TYPES[dtype])
+    v = rand(gen, dtype, case.keys, case.kv_heads, case.d)
+    O, lse = case.run(q, k, v, 1.0)
+    check(case, q, k, v, 1.0, O, lse, 2.0 ** -17)
+    O, lse = case.run(q, k.flip(0), v, 1.0)
+    check(case, q, k.flip(0), v, 1.0, O, lse, 2.0 ** -17)
