@@ -15,9 +15,14 @@
 // with m a running row maximum of the scores s = q . k.  m is raised only where
 // a tile's maximum exceeds it by more than kSlack / c, so most tiles skip the
 // rescaling of the accumulator (64 multiplications); p then reaches at most
-// 2^(kShift + kSlack) = 2^15, inside fp16.  kShift = 7 keeps weights down to
-// 2^-31 of the largest above fp16's smallest subnormal (2^-24).  Numerator
-// and denominator carry the same factor.
+// 2^(kShift + kSlack).  Numerator and denominator carry the same factor, and the
+// type decides on it.  fp16 has little room below 1: kShift = 7 keeps p at 2^15
+// or less and weights down to 2^-31 of the largest above the smallest subnormal
+// (2^-24).  bf16 has fp32's exponents, and so has O, which is summed before it
+// is divided: kShift = -16 keeps p at 2^-8 or less, so that O stays finite for V
+// up to the type's largest value as long as a row's weights, the largest as 1,
+// add up to 256 or less; and w v has 8 bits or more above fp32's smallest
+// subnormal (2^-149) where it is 2^-125 or more.
 //
 // The exponent is one fused c s + (kShift - c m), whose second part is rounded
 // once for a raised m.  That is off by half a step of c m, which for |c m| up to
@@ -51,12 +56,12 @@ constexpr int kWaveRows = 32;    // query rows of one wave
 constexpr int kWaves = 4;        // waves of one workgroup
 constexpr int kTileRows = kWaveRows * kWaves;
 constexpr int kThreads = 64 * kWaves;
-constexpr float kShift = 7.0f;
 constexpr float kSlack = 8.0f;
 constexpr float kFar = 1024.0f;   // 2^10
 constexpr float kLn2 = 0.693147180559945309f;
 
 struct F16 {
+    static constexpr float kShift = 7.0f;
     static __device__ __forceinline__ f32x16 mfma(u32x4 a, u32x4 b, f32x16 c)
     {
         return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
@@ -74,6 +79,7 @@ struct F16 {
 };
 
 struct BF16 {
+    static constexpr float kShift = -16.0f;
     static constexpr uint32_t kInf = 0x7f80, kOne = 0x3f80, k128 = 0x4300, k16384 = 0x4680;
     static __device__ __forceinline__ f32x16 mfma(u32x4 a, u32x4 b, f32x16 c)
     {
@@ -389,7 +395,7 @@ __device__ __forceinline__ float top_score(const f32x16 (&s)[N])
 // summed so far; the tile's scores of a row far from 0 become s - m.  Each row
 // goes by its own maximum alone, so a row's bits do not depend on the rows that
 // share its wave.
-template <int D, int N>
+template <typename T, int D, int N>
 __device__ __forceinline__ void raise(const Job& j, float mx, f32x16 (&s)[N], State<D>& st)
 {
     const bool up = mx > st.over;
@@ -398,7 +404,7 @@ __device__ __forceinline__ void raise(const Job& j, float mx, f32x16 (&s)[N], St
     const bool far = up && !(__builtin_fabsf(m * j.c) <= kFar);   // a row far from 0 has every tile with a key raise it
     if (up) {
         st.over = far ? -__builtin_inff() : m + j.slack;
-        st.base = far ? kShift : __builtin_fmaf(-m, j.c, kShift);
+        st.base = far ? T::kShift : __builtin_fmaf(-m, j.c, T::kShift);
     }
     st.m = m;
     st.l *= a;
@@ -414,11 +420,11 @@ __device__ __forceinline__ void raise(const Job& j, float mx, f32x16 (&s)[N], St
 }
 
 // What every tile of keys begins with.
-template <int D, int N>
+template <typename T, int D, int N>
 __device__ __forceinline__ void follow(const Job& j, f32x16 (&s)[N], State<D>& st)
 {
     const float mx = top_score(s);
-    if (__builtin_amdgcn_ballot_w64(mx > st.over) != 0) raise<D>(j, mx, s, st);
+    if (__builtin_amdgcn_ballot_w64(mx > st.over) != 0) raise<T, D>(j, mx, s, st);
 }
 
 // Softmax weights of 32 keys: P^T as B operands p[kk] of the keys 16 kk ..
@@ -606,7 +612,7 @@ __device__ __forceinline__ void run_tiles(const Job& j, const Row& row, char* sm
             mask(a[0], row.limit - t * kTileKeys, half);
             mask(a[1], row.limit - t * kTileKeys - 32, half);
         }
-        follow<D>(j, a, st);
+        follow<T, D>(j, a, st);
         u32x4 p0[1][2], p1[1][2];
         weights<T, D, D == 64>(a[0], j.c, st, p0[0]);
         weights<T, D, D == 64>(a[1], j.c, st, p1[0]);
@@ -645,7 +651,7 @@ __device__ __forceinline__ void run_tiles_careful(const Job& j, const Row& row, 
             const int keys = row.limit - t * kTileKeys - 32 * b;
             f32x16 s[1] = {scores<T, D>(x, b * (S::TILE / 2), q)};
             mask(s[0], keys, half);
-            follow<D>(j, s, st);
+            follow<T, D>(j, s, st);
             u32x4 p[1][2];
             weights<T, D>(s[0], j.c, st, p[0]);
             accumulate_careful<T, D>(x, S::TILE + b * (S::TILE / 2), p, keys, half, st);
@@ -743,7 +749,7 @@ __device__ __forceinline__ void run_blocks(const Job& j, const Keys& one, const 
         const int n = (second ? two.keys : one.keys) - key0, lim = row.limit - key0;
         const int readable = second || n < lim ? n : lim;
         if (n < kBlockKeys || (!second && key0 + kBlockKeys > first_limit)) mask(s[0], readable, half);
-        follow<D>(j, s, st);
+        follow<T, D>(j, s, st);
         u32x4 p[N][2];
         if constexpr (N == 2)
             weights_whole<T, D>(s[0], j.c, st, p);
@@ -774,9 +780,10 @@ __device__ __forceinline__ void store4(char* o, int e, f32x4 x)
     *reinterpret_cast<u32x2*>(o + 2 * e) = u32x2{T::pack(x[0], x[1]), T::pack(x[2], x[3])};
 }
 __device__ __forceinline__ float inverse(float l) { return l == 0.f ? 0.f : 1.f / l; }
+template <typename T>
 __device__ __forceinline__ float lse_of(float m, float l, float c)
 {
-    return l == 0.f ? -__builtin_inff() : __builtin_fmaf(m, c, __builtin_log2f(l) - kShift) * kLn2;
+    return l == 0.f ? -__builtin_inff() : __builtin_fmaf(m, c, __builtin_log2f(l) - T::kShift) * kLn2;
 }
 
 // Calls f(e, block, group) for a lane's groups of accumulator registers that
@@ -822,7 +829,7 @@ __device__ __forceinline__ void store_row(const Job& j, const State<D>& st, bool
             }
     if (!valid) return;
     each_group<D, 2>(j.d, half, [&](int e, int b, int g) { *reinterpret_cast<u32x4*>(o + 2 * e) = x[b][g / 2]; });
-    if (lse != nullptr && half == 0) *lse = lse_of(st.m, l, j.c);
+    if (lse != nullptr && half == 0) *lse = lse_of<T>(st.m, l, j.c);
 }
 
 template <int D>
@@ -846,7 +853,7 @@ __device__ __forceinline__ void store_row4(char* o, float* lse, float c, int e, 
 {
     const float inv = inverse(l);
     store4<T>(o, e, f32x4{x[0] * inv, x[1] * inv, x[2] * inv, x[3] * inv});
-    if (lse != nullptr && e == 0) *lse = lse_of(m, l, c);
+    if (lse != nullptr && e == 0) *lse = lse_of<T>(m, l, c);
 }
 __device__ __forceinline__ void store_part4(const Parts& w, int part, int64_t row, int d, int e, float m, float l, f32x4 x)
 {

@@ -151,3 +151,52 @@ def test_large_scores_that_rise(way, dtype, far):
     check(case, q, k, v, 1.0, O, lse, 2.0 ** -17)
     O, lse = case.run(q, k.flip(0), v, 1.0)
     check(case, q, k.flip(0), v, 1.0, O, lse, 2.0 ** -17)
+
+
+# ---------------------------------------------------------------- values near the ends of the range
+@pytest.mark.parametrize("exponent", [120, -60])
+@pytest.mark.parametrize("way", WAYS)
+def test_values_times_a_power_of_two(way, exponent):
+    """V times 2^e gives O times 2^e, bit for bit, as long as 2^e V is well inside bf16's range."""
+    case = Case(way)
+    gen = torch.Generator().manual_seed(79)
+    q, k = rand(gen, "bf16", case.rows, case.heads, case.d) * 2, rand(gen, "bf16", case.keys, case.kv_heads, case.d)
+    v = rand(gen, "bf16", case.keys, case.kv_heads, case.d)
+    one, lse = case.run(q, k, v, None)
+    check(case, q, k, v, case.d ** -0.5, one, lse)
+    far, lse2 = case.run(q, k, (v.double() * 2.0 ** exponent).bfloat16(), None)
+    assert torch.equal(far.double(), one.double() * 2.0 ** exponent) and torch.equal(lse, lse2)
+
+
+@pytest.mark.parametrize("way", WAYS)
+def test_small_values(way):
+    """V times 2^-100 against the plain form.  A product is off by 2^-150 at most where O's sum has no smaller bits; beside
+    a largest weight of 2^-16 at least, and times 2^100 again, that is 2^-34 for each key, 2^-22 for 4099 of them, where
+    the bound has 2^-9 of the weighted sum of |v|."""
+    case = Case(way)
+    gen = torch.Generator().manual_seed(79)
+    q, k = rand(gen, "bf16", case.rows, case.heads, case.d) * 2, rand(gen, "bf16", case.keys, case.kv_heads, case.d)
+    v = rand(gen, "bf16", case.keys, case.kv_heads, case.d)
+    far, lse = case.run(q, k, (v.double() * 2.0 ** -100).bfloat16(), None)
+    check(case, q, k, v, case.d ** -0.5, (far.double() * 2.0 ** 100).bfloat16(), lse)
+
+
+@pytest.mark.parametrize("keys", [1, 2, 100])
+@pytest.mark.parametrize("queries", [1, 40])
+@pytest.mark.parametrize("dtype", sorted(TYPES))
+def test_largest_values(dtype, queries, keys):
+    """Up to 100 keys of the type's largest value: their mean, which is that value again; with signs in turn, 0 for two."""
+    gen = torch.Generator().manual_seed(83)
+    top = torch.finfo(TYPES[dtype]).max
+    q = rand(gen, dtype, queries, 2, 64).to(DEV)
+    k = torch.zeros(keys, 2, 64, dtype=TYPES[dtype], device=DEV)
+    v = torch.full_like(k, top)
+    cq, ck = ints([0, queries]), ints([0, keys])
+    print(f"[gpu] largest values {dtype} {queries} {keys}", file=sys.stderr, flush=True)
+    O = g.attention_prompt(q, k, v, cq, ck, causal=False)
+    assert bool((O == top).all())
+    none = torch.empty(queries, 0, 2, 64, dtype=TYPES[dtype], device=DEV)
+    assert bool((g.attention_shared_prefix(q, k, v, none, none, ints([0] * queries)) == top).all())
+    if keys == 2:
+        v[1] = -top
+        assert bool((g.attention_prompt(q, k, v, cq, ck, causal=False) == 0).all())
