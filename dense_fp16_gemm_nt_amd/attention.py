@@ -228,9 +228,12 @@ def attention_prompt(Q, K, V, cu_q, cu_k=None, *, causal=True, scale=None, O=Non
     return (O, lse) if return_lse else O
 
 
-def attention_prompt_workspace(Q, K, V, cu_q, cu_k=None) -> int:
-    """Bytes of workspace attention_prompt needs for tensors of these shapes (0: none)."""
-    return _workspace_bytes("attn_prompt", *_prompt_desc(Q, K, V, cu_q, cu_q if cu_k is None else cu_k, True, None, None, None, False))
+def attention_prompt_workspace(Q, K, V, cu_q, cu_k=None, *, causal=None) -> int:
+    """Bytes of workspace attention_prompt needs for tensors of these shapes (0: none): with a causal mask, without one,
+    or, when `causal` is not given, enough for either."""
+    masks = (True, False) if causal is None else (causal,)
+    return max(_workspace_bytes("attn_prompt", *_prompt_desc(Q, K, V, cu_q, cu_q if cu_k is None else cu_k, m, None, None, None, False))
+               for m in masks)
 
 
 def _shared_desc(Q, Kp, Vp, Ks, Vs, lens, scale, O, lse, given):

@@ -41,7 +41,7 @@
  * in a second launch.  They need attn_*_workspace(...) bytes of device
  * memory (16-byte aligned, not overlapping the other arguments; contents are
  * scratch, nothing needs clearing).  The size follows from the descriptor's
- * sizes alone, not from lengths in device memory.  Calls that may overlap in
+ * sizes and `causal` alone, not from lengths in device memory.  Calls that may overlap in
  * time need a workspace each.
  */
 #ifndef ATTENTION_H

@@ -200,3 +200,24 @@ def test_largest_values(dtype, queries, keys):
     if keys == 2:
         v[1] = -top
         assert bool((g.attention_prompt(q, k, v, cq, ck, causal=False) == 0).all())
+
+
+# ---------------------------------------------------------------- workspace
+@pytest.mark.parametrize("n,m,heads,kv_heads", [(1024, 3072, 32, 8), (960, 3072, 32, 8), (3328, 3328, 32, 32), (1, 5000, 8, 2),
+                                                (40, 40, 2, 2)])
+def test_prompt_takes_the_workspace_that_was_asked_for(n, m, heads, kv_heads):
+    """Exactly as many bytes as attention_prompt_workspace names are enough with and without a mask."""
+    gen = torch.Generator().manual_seed(103)
+    q, k, v = (rand(gen, "bf16", x, h, 128).to(DEV) for x, h in ((n, heads), (m, kv_heads), (m, kv_heads)))
+    cq, ck = ints([0, n]), ints([0, m])
+    either = g.attention_prompt_workspace(q, k, v, cq, ck)
+    for causal in (True, False):
+        need = g.attention_prompt_workspace(q, k, v, cq, ck, causal=causal)
+        print(f"[gpu] workspace {n} {m} causal={causal}: {need} bytes, {either} for either", file=sys.stderr, flush=True)
+        assert need <= either
+        b = g.attention_prompt(q, k, v, cq, ck, causal=causal)
+        for size in (need, either):
+            ws = torch.full((size + 64,), 0x7F, dtype=torch.uint8, device=DEV)
+            a = g.attention_prompt(q, k, v, cq, ck, causal=causal, workspace=ws[:size])
+            torch.cuda.synchronize()
+            assert torch.equal(a, b) and bool((ws[size:] == 0x7F).all())
