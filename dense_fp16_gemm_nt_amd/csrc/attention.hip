@@ -48,7 +48,7 @@ struct PromptArgs {
     int by_xcd;
     float c, slack;
     uint32_t flip;
-    int zero_q;
+    int zero;
     Parts parts;
 };
 
@@ -166,7 +166,7 @@ __device__ __forceinline__ Job prompt_job(const PromptArgs& g, const Tile& t, in
     j.c = g.c;
     j.slack = g.slack;
     j.flip = g.flip;
-    j.zero_q = g.zero_q != 0;
+    j.zero = g.zero != 0;
     j.most = t.nk;
     if (g.causal) {
         const int last = (j.rows - t.row0 > ROWS ? t.row0 + ROWS : j.rows) - 1;
@@ -284,7 +284,7 @@ struct SharedArgs {
     uint32_t own_jobs;    // of these
     float c, slack;
     uint32_t flip;
-    int zero_q;
+    int zero;
     Parts parts;
 };
 
@@ -313,7 +313,7 @@ __global__ __launch_bounds__(kThreads, 2) void shared_kernel(const SharedArgs g)
     j.c = g.c;
     j.slack = g.slack;
     j.flip = g.flip;
-    j.zero_q = g.zero_q != 0;
+    j.zero = g.zero != 0;
     State<D> st;
     if (!own) {
         uint32_t unit, t;   // a kv head and a part of the prefix, and rows
@@ -865,7 +865,7 @@ int attn_prompt(const attn_prompt_desc* d, void* workspace, int64_t workspace_by
     g.c = sc.c;
     g.slack = sc.slack;
     g.flip = sc.flip;
-    g.zero_q = sc.zero;
+    g.zero = sc.zero;
     g.parts = parts_in(workspace, p.splits, d->total_q * d->heads);
     const int64_t wgs = p.tiles * units;
     const hipStream_t s = (hipStream_t)stream;
@@ -949,7 +949,7 @@ int attn_shared_prefix(const attn_shared_prefix_desc* d, void* workspace, int64_
     g.c = sc.c;
     g.slack = sc.slack;
     g.flip = sc.flip;
-    g.zero_q = sc.zero;
+    g.zero = sc.zero;
     g.parts = parts_in(workspace, p.prefix_splits + p.own_splits, d->batch * d->heads);
     const int64_t wgs = p.rounds * (p.round_prefix + p.round_own);
     const hipStream_t s = (hipStream_t)stream;

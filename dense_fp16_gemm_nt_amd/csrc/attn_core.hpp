@@ -184,7 +184,7 @@ struct Job {
     int d;               // head size
     float c, slack;      // |scale| * log2 e, and kSlack / c
     uint32_t flip;       // sign bits flipped in Q (a negative scale)
-    bool zero_q;         // scale = 0: every score is 0
+    bool zero;           // scale = 0: every score is 0, so Q and K are taken as zeros
 };
 
 // What a lane knows of its row.
@@ -221,7 +221,7 @@ __device__ __forceinline__ void load_q(const Job& j, const Row& row, int half, u
     }
 #pragma unroll
     for (int s = 0; s < Shape<D>::KSTEPS; ++s) {
-        const uint32_t keep = row.valid && 16 * s + 8 * half < j.d && !j.zero_q ? 0xffffffffu : 0u;
+        const uint32_t keep = row.valid && 16 * s + 8 * half < j.d && !j.zero ? 0xffffffffu : 0u;
 #pragma unroll
         for (int i = 0; i < 4; ++i) q[s][i] = (q[s][i] & keep) ^ j.flip;
     }
@@ -260,7 +260,8 @@ struct Loader {
     int left;                 // keys from there on
     uint32_t row_bytes, last; // bytes from a row to the next, and of a row's head
 
-    __device__ __forceinline__ void start(const char* base, int64_t pitch, int keys, int tile, int d, int tid, bool v)
+    // The first tile to load; where `zero` all of them arrive as zeros.
+    __device__ __forceinline__ void start(const char* base, int64_t pitch, int keys, int tile, int d, int tid, bool v, bool zero)
     {
         const int r = tid / S::CHUNKS, pc = tid % S::CHUNKS;
         const int lc = pc ^ (v ? swz_v<D>(r) : swz_k<D>(r));   // both repeat every 16 rows
@@ -270,7 +271,7 @@ struct Loader {
         for (int i = 0; i < LOADS; ++i)
             off[i] = lc * 8 < d ? (uint32_t)(r + i * LOAD_ROWS) * row_bytes + (uint32_t)lc * 16u : 0x80000000u;
         at = (uint64_t)(base + (int64_t)tile * kTileKeys * pitch);
-        left = keys - tile * kTileKeys;
+        left = zero ? 0 : keys - tile * kTileKeys;
     }
     template <int... I>
     __device__ __forceinline__ void issue(u32x4 rs, uint32_t dst, std::integer_sequence<int, I...>)
@@ -588,8 +589,8 @@ __device__ __forceinline__ void run_tiles(const Job& j, const Row& row, char* sm
     const uint32_t dst = lds + __builtin_amdgcn_readfirstlane(tid >> 6) * 1024;
     constexpr uint32_t K0 = 0, V0 = 2 * S::TILE, HALF = S::TILE / 2;
     Loader<D, W> k, v;
-    k.start(j.k, j.k_row, j.keys, j.tile0, j.d, tid, false);
-    v.start(j.v, j.v_row, j.keys, j.tile0, j.d, tid, true);
+    k.start(j.k, j.k_row, j.keys, j.tile0, j.d, tid, false, j.zero);
+    v.start(j.v, j.v_row, j.keys, j.tile0, j.d, tid, true, false);
     k.next(dst + K0);
     v.next(dst + V0);
     if (j.tile0 + 1 < j.tile1) k.next(dst + K0 + S::TILE);
@@ -638,8 +639,8 @@ __device__ __forceinline__ void run_tiles_careful(const Job& j, const Row& row, 
     const Reads<D> x = reads_of<D>(lds, lane);
     const uint32_t dst = lds + __builtin_amdgcn_readfirstlane(tid >> 6) * 1024;
     Loader<D, W> k, v;
-    k.start(j.k, j.k_row, j.keys, j.tile0, j.d, tid, false);
-    v.start(j.v, j.v_row, j.keys, j.tile0, j.d, tid, true);
+    k.start(j.k, j.k_row, j.keys, j.tile0, j.d, tid, false, j.zero);
+    v.start(j.v, j.v_row, j.keys, j.tile0, j.d, tid, true, false);
     u32x4 q[S::KSTEPS];
     load_q<D>(j, row, half, q);
     for (int t = j.tile0; t < j.tile1; ++t) {
@@ -725,7 +726,7 @@ __device__ __forceinline__ void run_blocks(const Job& j, const Keys& one, const 
         const int keys = second ? two.keys : one.keys;
         const int64_t row_bytes = v ? (second ? two.v_row : one.v_row) : (second ? two.k_row : one.k_row);
         const char* base = v ? (second ? two.v : one.v) : (second ? two.k : one.k);
-        const int n = blk >= block1 ? 0 : keys - key0 < kBlockKeys ? keys - key0 : kBlockKeys;
+        const int n = blk >= block1 || (j.zero && !v) ? 0 : keys - key0 < kBlockKeys ? keys - key0 : kBlockKeys;
         const uint32_t bytes = n > 0 ? (uint32_t)(n - 1) * (uint32_t)row_bytes + 2u * (uint32_t)j.d : 0u;
         const uint64_t a = (uint64_t)(base + (int64_t)key0 * row_bytes);
         const u32x4 rs = {(uint32_t)a, (uint32_t)(a >> 32) & 0xffffu, bytes, 0x00020000u};

@@ -202,6 +202,22 @@ def test_largest_values(dtype, queries, keys):
         assert bool((g.attention_prompt(q, k, v, cq, ck, causal=False) == 0).all())
 
 
+# ---------------------------------------------------------------- scale 0
+@pytest.mark.parametrize("scale", [0.0, 1e-39])
+@pytest.mark.parametrize("dtype", sorted(TYPES))
+@pytest.mark.parametrize("way", WAYS)
+def test_scale_zero_whatever_q_and_k_hold(way, dtype, scale):
+    case = Case(way)
+    gen = torch.Generator().manual_seed(89)
+    q, k, v = (rand(gen, dtype, *s, case.d) for s in ((case.rows, case.heads), (case.keys, case.kv_heads),
+                                                      (case.keys, case.kv_heads)))
+    zeros = torch.zeros_like(k)
+    k[::3, :, 1], k[1::3, :, 2], k[2::5] = math.inf, math.nan, -math.inf
+    q[::2, :, 3], q[1::4] = math.nan, math.inf
+    O, lse = case.run(q, k, v, scale)
+    check(case, torch.zeros_like(q), zeros, v, 1.0, O, lse)
+
+
 # ---------------------------------------------------------------- workspace
 @pytest.mark.parametrize("n,m,heads,kv_heads", [(1024, 3072, 32, 8), (960, 3072, 32, 8), (3328, 3328, 32, 32), (1, 5000, 8, 2),
                                                 (40, 40, 2, 2)])
