@@ -43,6 +43,7 @@ struct PromptArgs {
     const int32_t* cu_k;
     int64_t q_row, q_head, k_row, k_head, v_row, v_head, o_row, o_head;   // bytes
     int batch, total_q, total_k, heads, kv_heads, d, causal;
+    int careful;   // rows may meet keys that they do not read: see accumulate_careful
     Div group, splits, units;   // units: kv heads x splits, or an eighth of them (by_xcd)
     Div join_kv;                // kv heads
     int by_xcd;
@@ -205,8 +206,8 @@ __global__ __launch_bounds__(64 * W, D == 64 && W == 4 ? 3 : 2) void prompt_kern
         const Keys keys = {j.k, j.v, j.k_row, j.v_row, j.keys}, none = {};
         const int n = attn::key_blocks(j.most);
         const Range r = SPLIT ? part_of(n, g.splits, split) : Range{0, n};
-        attn::run_blocks<T, D, 2>(j, keys, none, r.first, r.last, row, smem, st);
-        if (g.causal && attn::spoilt<D>(st)) {
+        attn::run_blocks<T, D, 2, false, false>(j, keys, none, r.first, r.last, row, smem, st);
+        if (g.careful && attn::spoilt<D>(st)) {
             attn::landed<0>();
             attn::run_blocks<T, D, 2, true>(j, keys, none, r.first, r.last, row, smem, st);
         }
@@ -228,7 +229,10 @@ __global__ __launch_bounds__(64 * W, D == 64 && W == 4 ? 3 : 2) void prompt_kern
     j.tile1 = r.last;
     const Row row = attn::row_of(j, j.row0 + w * attn::kWaveRows + (lane & 31));
     attn::run_tiles<T, D, W>(j, row, smem, st);
-    if (g.causal && attn::any_wave<W>(attn::spoilt<D>(st), smem)) attn::run_tiles_careful<T, D, W>(j, row, smem, st);
+    if (g.careful && attn::any_wave<W>(attn::spoilt<D>(st), smem)) {
+        attn::init(st);
+        attn::run_tiles_careful<T, D, W>(j, row, smem, st);
+    }
     const int64_t token = (int64_t)tile.q0 + row.token;
     const int head = kv * (int)g.group.d + row.head;
     if constexpr (SPLIT)
@@ -351,7 +355,14 @@ __global__ __launch_bounds__(kThreads, 2) void shared_kernel(const SharedArgs g)
         j.tile0 = r.first;
         j.tile1 = r.last;
         const Row row = attn::row_of(j, j.row0 + w * attn::kWaveRows + (lane & 31));
+        // a last tile whose end holds rows of V that are no keys goes by itself
+        const int ragged = attn::overlap(j.v_row, j.d) && j.tile1 > j.tile0 && (int64_t)j.tile1 * kTileKeys > g.prefix;
+        j.tile1 -= ragged;
         attn::run_tiles<T, D, attn::kWaves>(j, row, smem, st);
+        if (ragged) {
+            j.tile0 = j.tile1++;
+            attn::run_tiles_careful<T, D, attn::kWaves>(j, row, smem, st);
+        }
         attn::store_part<D>(st, row.valid, g.d, g.parts, part,
                             (int64_t)row.token * g.heads + kv * (int)g.group.d + row.head, half);
         return;
@@ -398,9 +409,9 @@ __global__ __launch_bounds__(kThreads, 2) void shared_kernel(const SharedArgs g)
     if (g.solo) {
         const int head = kv * j.rows + row.head;
         if (g.together)
-            attn::run_blocks<T, D, 2, false, 1>(j, before, mine, block0, block1, row, smem, st);
+            attn::run_blocks<T, D, 2, false, true, 1>(j, before, mine, block0, block1, row, smem, st);
         else
-            attn::run_blocks<T, D, 1, false, 1>(j, before, mine, block0, block1, row, smem, st);
+            attn::run_blocks<T, D, 1, false, true, 1>(j, before, mine, block0, block1, row, smem, st);
         attn::landed<0>();   // the loads past the last block
         if (g.together)
             attn::store_row<T, D>(j, st, row.valid, g.o + slot * g.o_row + (int64_t)head * g.o_head,
@@ -857,6 +868,7 @@ int attn_prompt(const attn_prompt_desc* d, void* workspace, int64_t workspace_by
     g.group = attn::div_by(d->heads / d->kv_heads);
     g.d = d->head_dim;
     g.causal = d->causal;
+    g.careful = d->causal != 0 || d->v_row < d->head_dim;
     const int64_t units = d->kv_heads * p.splits;
     g.by_xcd = units % kNumXcd == 0;
     g.units = attn::div_by(g.by_xcd ? units / kNumXcd : units);

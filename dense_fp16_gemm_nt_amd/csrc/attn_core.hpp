@@ -503,9 +503,10 @@ __device__ __forceinline__ void accumulate(const Reads<D>& x, uint32_t at, const
 }
 
 // A product with V is not blind to a masked key: weight 0 times an infinity is
-// NaN.  Keys that no row may read are not loaded; under a causal mask one row
-// of a tile reads a key that another may not, and if that key's V is not
-// finite the other's sum is spoilt.  Such sums show at the end as O that is
+// NaN.  Keys that no row may read are not loaded, unless V's rows are closer than
+// they are long (overlap): rows behind the last then begin before its end.
+// Under a causal mask one row of a tile reads a key that another may not.  If
+// such a key's V is not finite a sum is spoilt that it has no part in.  Such sums show at the end as O that is
 // not finite; the job is then done again, careful: V's finite elements are
 // multiplied as ever, and the others are counted for each row over the keys it
 // may read (of the first `keys` of the 32), by kind (+inf, -inf, NaN as 1, 128
@@ -549,6 +550,9 @@ __device__ __forceinline__ void accumulate_careful(const Reads<D>& x, uint32_t a
         }
     }
 }
+
+// Whether V's rows, a stride of bytes apart, are closer than they are long.
+__device__ __forceinline__ bool overlap(int64_t v_row, int d) { return v_row < 2 * d; }
 
 // Whether some element of the wave's O is not finite.
 template <int D>
@@ -628,13 +632,13 @@ __device__ __forceinline__ void run_tiles(const Job& j, const Row& row, char* sm
     if (t < j.tile1) step(t, 0, cur, next);
 }
 
-// The same for a job whose V is not all finite, one tile after the other.
+// The same for a job whose V is not all finite, one tile after the other;
+// begins with what `st` holds.
 template <typename T, int D, int W>
 __device__ __forceinline__ void run_tiles_careful(const Job& j, const Row& row, char* smem, State<D>& st)
 {
     using S = Shape<D>;
     const int tid = threadIdx.x, lane = tid & 63, half = lane >> 5;
-    init(st);
     const uint32_t lds = lds_address(smem);
     const Reads<D> x = reads_of<D>(lds, lane);
     const uint32_t dst = lds + __builtin_amdgcn_readfirstlane(tid >> 6) * 1024;
@@ -691,9 +695,10 @@ constexpr int kBlockKeys = 32;
 __device__ __forceinline__ int key_blocks(int keys) { return (int)(((int64_t)keys + kBlockKeys - 1) / kBlockKeys); }
 
 // Blocks [block0, block1) of the runs' blocks; row.limit counts keys of the
-// first run.  P goes as N operands (2: its rounding and the rest).  DEAL: how
+// first run.  P goes as N operands (2: its rounding and the rest).  CAREFUL: as
+// run_tiles_careful; without it V's rows may overlap where CLEAR.  DEAL: how
 // many waves share the blocks (1: each wave has rows and blocks of its own).
-template <typename T, int D, int N, bool CAREFUL = false, int DEAL = kWaves>
+template <typename T, int D, int N, bool CAREFUL = false, bool CLEAR = !CAREFUL, int DEAL = kWaves>
 __device__ __forceinline__ void run_blocks(const Job& j, const Keys& one, const Keys& two, int block0, int block1,
                                            const Row& row, char* smem, State<D>& st)
 {
@@ -757,6 +762,9 @@ __device__ __forceinline__ void run_blocks(const Job& j, const Keys& one, const 
         else
             weights<T, D>(s[0], j.c, st, p[0]);
         landed<NL>();   // V; the next K may be in flight
+        if (CLEAR && n < kBlockKeys && overlap(second ? two.v_row : one.v_row, j.d))   // each lane what it loaded
+            for (int i = r; i < kBlockKeys; i += ROWS)
+                if (i >= n) *reinterpret_cast<G16_LDS u32x4*>(lds + HALF + i * S::PITCH + pc * 16) = u32x4{0, 0, 0, 0};
         if constexpr (CAREFUL)
             accumulate_careful<T, D>(x, HALF, p, readable, half, st);
         else

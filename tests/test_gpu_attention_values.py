@@ -218,6 +218,64 @@ def test_scale_zero_whatever_q_and_k_hold(way, dtype, scale):
     check(case, torch.zeros_like(q), zeros, v, 1.0, O, lse)
 
 
+# ---------------------------------------------------------------- rows that overlap
+@pytest.mark.parametrize("step", [0, 8])
+@pytest.mark.parametrize("dtype", sorted(TYPES))
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("n,m", [(150, 210), (3, 45), (130, 1500), (2, 2990)])
+@pytest.mark.parametrize("d", [64, 96, 128])
+def test_prompt_rows_of_values_that_overlap(d, n, m, causal, dtype, step):
+    """V's rows a step apart that is shorter than they are (0: one row for all keys).  The last row ends with an infinity;
+    no key behind it, of the tile's rest, may bring it to another element."""
+    gen = torch.Generator().manual_seed(97)
+    H = 2
+    q, k = rand(gen, dtype, n, H, d), rand(gen, dtype, m, H, d)
+    flat = rand(gen, dtype, H, (m - 1) * step + d)
+
+    def view(x):
+        return x.as_strided((m, H, d), (step, x.shape[1], 1))
+
+    flat[:, -1] = math.inf
+    print(f"[gpu] overlapping values {n} {m} {causal} {dtype} {step}", file=sys.stderr, flush=True)
+    O, lse = g.attention_prompt(q.to(DEV), k.to(DEV), view(flat.to(DEV)), ints([0, n]), ints([0, m]), causal=causal, return_lse=True)
+    O, lse = O.cpu(), lse.cpu()
+    # it stands in the last element of the last key alone (step 0: of every key)
+    sees = torch.zeros(n, dtype=torch.bool)
+    sees[-1 if causal and step else 0:] = True
+    assert not bool(torch.isfinite(O[sees][..., -1]).any()) and bool(torch.isfinite(O[~sees]).all())
+    v = view(flat).clone()
+    v[..., -1], O[..., -1] = 0, 0
+    ref.prompt(q, k, v, [0, n], [0, m], causal, d ** -0.5, O, lse, "overlapping values")
+
+
+@pytest.mark.parametrize("step", [0, 8])
+@pytest.mark.parametrize("dtype", sorted(TYPES))
+@pytest.mark.parametrize("B,P,N,heads,kv_heads", [(3, 100, 70, 4, 2), (65, 61, 40, 32, 16), (1, 3001, 5, 4, 1), (4, 2001, 40, 4, 2),
+                                                  (40, 1001, 301, 4, 2), (131, 601, 61, 10, 5)])
+@pytest.mark.parametrize("d", [64, 96, 128])
+def test_shared_prefix_rows_of_values_that_overlap(d, B, P, N, heads, kv_heads, dtype, step):
+    gen = torch.Generator().manual_seed(101)
+    q, kp, ks = rand(gen, dtype, B, heads, d), rand(gen, dtype, P, kv_heads, d), rand(gen, dtype, B, N, kv_heads, d)
+    fp, fs = rand(gen, dtype, kv_heads, (P - 1) * step + d), rand(gen, dtype, B, kv_heads, (N - 1) * step + d)
+    lens = [(N, N - 1, N // 2, 1)[b % 4] for b in range(B)]
+
+    def views(p, s):
+        return (p.as_strided((P, kv_heads, d), (step, p.shape[1], 1)),
+                s.as_strided((B, N, kv_heads, d), (kv_heads * s.shape[2], step, s.shape[2], 1)))
+
+    fp[:, -1] = math.inf
+    for b, n in enumerate(lens):   # the last element of the slot's last readable row, and all behind it
+        fs[b, :, (n - 1) * step + d - 1:] = math.inf
+    print(f"[gpu] overlapping values B={B} P={P} N={N} {dtype} {step}", file=sys.stderr, flush=True)
+    vp, vs = views(fp.to(DEV), fs.to(DEV))
+    O, lse = g.attention_shared_prefix(q.to(DEV), kp.to(DEV), vp, ks.to(DEV), vs, ints(lens), return_lse=True)
+    O, lse = O.cpu(), lse.cpu()
+    assert not bool(torch.isfinite(O[..., -1]).any())
+    vp, vs = (x.clone() for x in views(fp, fs))
+    O[..., -1], vp[..., -1], vs[..., -1] = 0, 0, 0
+    ref.shared_prefix(q, kp, vp, ks, vs, lens, d ** -0.5, O, lse, "overlapping values")
+
+
 # ---------------------------------------------------------------- workspace
 @pytest.mark.parametrize("n,m,heads,kv_heads", [(1024, 3072, 32, 8), (960, 3072, 32, 8), (3328, 3328, 32, 32), (1, 5000, 8, 2),
                                                 (40, 40, 2, 2)])
