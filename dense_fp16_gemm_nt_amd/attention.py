@@ -124,7 +124,7 @@ def _heads(H, Hk):
 
 def _scale(scale, d):
     if scale is None:
-        return 1.0 / math.sqrt(d)
+        return 1.0 / math.sqrt(d) if d else 1.0   # heads without elements are refused by the library
     scale = float(scale)
     return scale if abs(scale) < 3.4e38 else math.inf   # what fp32 does not hold is refused by the library
 

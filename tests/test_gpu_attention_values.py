@@ -295,3 +295,12 @@ def test_prompt_takes_the_workspace_that_was_asked_for(n, m, heads, kv_heads):
             a = g.attention_prompt(q, k, v, cq, ck, causal=causal, workspace=ws[:size])
             torch.cuda.synchronize()
             assert torch.equal(a, b) and bool((ws[size:] == 0x7F).all())
+
+
+# ---------------------------------------------------------------- refusals
+def test_heads_without_elements_are_refused_by_the_library():
+    x = torch.zeros(4, 2, 0, dtype=torch.float16, device=DEV)
+    with pytest.raises(g.GemmError):
+        g.attention_prompt(x, x, x, ints([0, 4]))
+    with pytest.raises(g.GemmError):
+        g.attention_shared_prefix(x, x, x, x[:, None], x[:, None], ints([0] * 4))
