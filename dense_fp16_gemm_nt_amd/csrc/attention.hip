@@ -475,8 +475,9 @@ constexpr int64_t kMaxStride = int64_t(1) << 40;      // elements; keeps every o
 constexpr int64_t kMaxBlocks = 64;   // of 32 keys, of a slot's part, so that long and short slots even out
 // A launch holds less than 2^32 threads.  This many units of work (row tiles
 // of 128 and slots' parts of 64 blocks of keys, times kv heads) keep every
-// launch of a call, of workgroups of 512 threads and of the joins too, at half
-// of that or less.
+// launch of a call, of workgroups of 512 threads, at half of that or less, and
+// the joins at 4/5: 32 heads to a kv head and two parts are most, with
+// 2^22 / (32 / 128 + 1) slots and kv heads of 32 rows, 8 rows to 256 threads.
 constexpr int64_t kMaxUnits = int64_t(1) << 22;
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }

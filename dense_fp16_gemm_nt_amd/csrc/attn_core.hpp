@@ -431,9 +431,9 @@ __device__ __forceinline__ void follow(const Job& j, f32x16 (&s)[N], State<D>& s
 // Softmax weights of 32 keys: P^T as B operands p[kk] of the keys 16 kk ..
 // 16 kk + 15, and their sum (of the weights before their rounding: the
 // log-sum-exp has to hold in fp32).  LEAN takes them pair by pair, which costs
-// a little time (16384 tokens, d 128: 1924 against 1877 us) and saves the
-// registers that let three waves share a SIMD for d 64 (154 against 183;
-// 4096 tokens, 32 heads: 154 against 159 us).
+// a little time (16384 tokens, d 128: 1924 against 1877 us) and saves some 29
+// registers, which lets three waves share a SIMD for d 64 (164 of the 168 that
+// they may have; 4096 tokens, 32 heads: 154 against 159 us).
 template <typename T, int D, bool LEAN = false>
 __device__ __forceinline__ void weights(const f32x16& s, float c, State<D>& st, u32x4 (&p)[2])
 {

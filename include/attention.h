@@ -9,7 +9,13 @@
  *
  * Scores, softmax statistics, sums and the output accumulate in fp32; the
  * softmax weights are rounded to the operands' type before the product with
- * V, and O is rounded once, to nearest even.  A row that no key is left for
+ * V (where no more than 32 rows meet the keys the rest of that rounding goes
+ * as a second operand), and O is rounded once, to nearest even.  Scores may be
+ * as large as fp32 holds.  O is finite for finite V: in fp16 always, in bf16
+ * where a row's weights, the largest taken as 1, add up to 256 or less, or V
+ * stays that much below the type's largest value.  A value of V that is not
+ * finite, at a key that a row reads, makes that element of the row's O an
+ * infinity or NaN.  A row that no key is left for
  * gets O = +0 and lse = -inf.  lse, where asked for, is the natural
  * logarithm of sum_j exp(scale * q . k_j), fp32.  A negative scale is taken
  * as it is; for scale 0 every score is 0, whatever Q and K hold.
@@ -28,7 +34,8 @@
  * kv_heads times (batch * group / 128 + batch * ceil(group / 32) *
  * (slot_rows / 2048 + 1)) for attn_shared_prefix, with group = heads /
  * kv_heads; more is UNSUPPORTED.  O and lse must not overlap an input or
- * each other, and O's rows and heads must not overlap each other.
+ * each other, where a tensor counts as all memory from its first to its last
+ * element; and O's rows and heads must not overlap each other.
  *
  * Calls are asynchronous and stream-ordered: they validate, enqueue and
  * return; validation comes before any HIP call, and an invalid call launches
