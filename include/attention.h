@@ -10,7 +10,7 @@
  * Scores, softmax statistics, sums and the output accumulate in fp32; the
  * softmax weights are rounded to the operands' type before the product with
  * V (where no more than 32 rows meet the keys the rest of that rounding goes
- * as a second operand), and O is rounded once, to nearest even.  Scores may be
+ * as a second operand), and O is rounded once, to nearest even.  q . k may be
  * as large as fp32 holds.  O is finite for finite V: in fp16 always, in bf16
  * where a row's weights, the largest taken as 1, add up to 256 or less, or V
  * stays that much below the type's largest value.  A value of V that is not
