@@ -96,6 +96,7 @@ def lib() -> ctypes.CDLL:
             L.gemm_f16_nt_ring_plan.restype = i32
             L.gemm_f16_nt_ring_plan.argtypes = [i32, i64, ctypes.POINTER(ctypes.c_int), i64p, i64p]
             attention.declare(L)
+            grouped.declare(L)
             _lib = L
     return _lib
 
@@ -384,7 +385,9 @@ def ring_plan(depth: int, steps: int):
     return stage, lap, refill
 
 
-# at the end: the attention binding uses what is defined above
-from . import attention  # noqa: E402
+# at the end: these bindings use what is defined above
+from . import attention, grouped  # noqa: E402
 from .attention import (attention_prompt, attention_prompt_workspace, attention_shared_prefix,  # noqa: E402
                         attention_shared_prefix_workspace)
+from .grouped import (adapter_product, adapter_product_workspace, grouped_product, grouped_product_grad_input,  # noqa: E402
+                      grouped_product_grad_weight)

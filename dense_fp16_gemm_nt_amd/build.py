@@ -1,5 +1,5 @@
-"""Build the HIP library (gfx950) in-tree: dense_fp16_gemm_nt_amd/libgemm_f16_nt.so (the products and
-the attention operators), and the matrix-core calibration kernel the profiling tools use (libmfma_calib.so)."""
+"""Build the HIP library (gfx950) in-tree: dense_fp16_gemm_nt_amd/libgemm_f16_nt.so (the products, the
+attention operators and the grouped products), and the matrix-core calibration kernel the profiling tools use (libmfma_calib.so)."""
 from __future__ import annotations
 
 import os
@@ -9,7 +9,7 @@ from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
-SOURCES = [os.path.join(PKG, "csrc", name) for name in ("gemm_f16_nt.hip", "attention.hip")]
+SOURCES = [os.path.join(PKG, "csrc", name) for name in ("gemm_f16_nt.hip", "attention.hip", "grouped.hip")]
 LIB = os.path.join(PKG, "libgemm_f16_nt.so")
 ARCH = "gfx950"
 

@@ -6,16 +6,15 @@
 
 #include <hip/hip_runtime.h>
 
-#include <atomic>
 #include <cfloat>
 #include <cmath>
-#include <cstring>
-#include <initializer_list>
 
 #include "attn_core.hpp"
+#include "host.hpp"
 #include "sched.hpp"
 
 using namespace g16;
+using namespace g16::host;
 
 namespace {
 
@@ -446,32 +445,9 @@ __global__ __launch_bounds__(kThreads) void shared_join_kernel(const SharedArgs 
                               g.lse == nullptr ? nullptr : g.lse + x);
 }
 
-// --------------------------------------------------------------- devices
-constexpr int kMaxDevices = 64;
-std::atomic<int> g_cus[kMaxDevices];   // compute units; 0 unknown, -1 not gfx950
-
-int device_cus(int* cus)
-{
-    int dev = 0;
-    if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= kMaxDevices) return GEMM_F16_NT_DEVICE;
-    int n = g_cus[dev].load(std::memory_order_relaxed);
-    if (n == 0) {
-        hipDeviceProp_t prop;
-        n = -1;
-        if (hipGetDeviceProperties(&prop, dev) == hipSuccess && std::strncmp(prop.gcnArchName, "gfx950", 6) == 0 &&
-            prop.multiProcessorCount > 0)
-            n = prop.multiProcessorCount;
-        g_cus[dev].store(n, std::memory_order_relaxed);   // threads that ask at once store the same
-    }
-    if (n < 0) return GEMM_F16_NT_DEVICE;
-    *cus = n;
-    return GEMM_F16_NT_OK;
-}
-
 // ------------------------------------------------------------ validation
 constexpr int64_t kMaxRowStride = int64_t(1) << 23;   // a tile of 64 rows spans less than 2^30 bytes
 constexpr int64_t kMaxIndex = (int64_t(1) << 31) - 1024;
-constexpr int64_t kMaxStride = int64_t(1) << 40;      // elements; keeps every offset inside 63 bits
 constexpr int64_t kMaxBlocks = 64;   // of 32 keys, of a slot's part, so that long and short slots even out
 // A launch holds less than 2^32 threads.  This many units of work (row tiles
 // of 128 and slots' parts of 64 blocks of keys, times kv heads) keep every
@@ -479,40 +455,6 @@ constexpr int64_t kMaxBlocks = 64;   // of 32 keys, of a slot's part, so that lo
 // the joins at 4/5: 32 heads to a kv head and two parts are most, with
 // 2^22 / (32 / 128 + 1) slots and kv heads of 32 rows, 8 rows to 256 threads.
 constexpr int64_t kMaxUnits = int64_t(1) << 22;
-
-int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
-
-bool overlaps(const void* a, int64_t abytes, const void* b, int64_t bbytes)
-{
-    if (abytes <= 0 || bbytes <= 0) return false;
-    const uintptr_t a0 = (uintptr_t)a, b0 = (uintptr_t)b;
-    return a0 < b0 + (uintptr_t)bbytes && b0 < a0 + (uintptr_t)abytes;
-}
-
-struct Axis {
-    int64_t n, stride;
-};
-
-// Bytes from a tensor's first to its last element; 0 if it has none, -1 for
-// a bad stride.
-int64_t extent(int64_t d, std::initializer_list<Axis> axes)
-{
-    __int128 last = d - 1;
-    for (const Axis& a : axes) {
-        if (a.n == 0) return 0;
-        if (a.stride < 0 || a.stride > kMaxStride) return -1;
-        last += (__int128)(a.n - 1) * a.stride;
-    }
-    const __int128 bytes = 2 * (last + 1);
-    return bytes < ((__int128)1 << 60) ? (int64_t)bytes : -1;
-}
-
-bool aligned16(const void* p, std::initializer_list<int64_t> strides)
-{
-    uint64_t all = (uintptr_t)p >> 1 | ((uintptr_t)p & 1);
-    for (int64_t s : strides) all |= (uint64_t)s;
-    return (all & 7) == 0;
-}
 
 // Heads, head size, type and scale.
 int check_common(int dtype, int64_t heads, int64_t kv_heads, int64_t d, float scale)
@@ -761,12 +703,6 @@ Parts parts_in(void* ws, int64_t splits, int64_t rows)
 }
 int64_t parts_total(int64_t part_bytes) { return part_bytes == 0 ? 0 : part_bytes + 16; }
 
-int launch(const void* f, int64_t wgs, int threads, const void* args, hipStream_t s)
-{
-    void* a[] = {const_cast<void*>(args)};
-    return hipLaunchKernel(f, dim3((unsigned)wgs), dim3(threads), a, 0, s) == hipSuccess ? GEMM_F16_NT_OK : GEMM_F16_NT_LAUNCH;
-}
-
 // The instantiation for a type and head size.
 template <template <typename, int> class K>
 const void* pick(int dtype, int64_t d)
@@ -812,13 +748,6 @@ template <typename T, int GROUPS>
 struct SharedJoin {
     static const void* f() { return (const void*)&shared_join_kernel<T, GROUPS>; }
 };
-
-int check_workspace(const void* ws, int64_t have, int64_t need)
-{
-    if (need == 0) return GEMM_F16_NT_OK;
-    if (ws == nullptr || have < need) return GEMM_F16_NT_INVALID_ARG;
-    return ((uintptr_t)ws & 15) != 0 ? GEMM_F16_NT_UNSUPPORTED : GEMM_F16_NT_OK;
-}
 
 }  // namespace
 

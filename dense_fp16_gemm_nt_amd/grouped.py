@@ -1,0 +1,279 @@
+"""Products of many matrices in one call: ctypes binding of ``include/grouped.h``.
+
+``grouped_product`` multiplies rows that are sorted by the matrix they go
+through (a layer of experts), ``grouped_product_grad_input`` and
+``grouped_product_grad_weight`` are its gradients, and ``adapter_product`` is
+one projection for all rows with the low-rank adapters of many requests beside
+it.  All take fp16 or bf16 device tensors, check their metadata, pass device
+pointers and the current HIP stream, and raise on a non-zero status.  Offsets
+stay on the device: no call synchronises.  None is part of an autograd graph.
+"""
+from __future__ import annotations
+
+import ctypes
+import struct
+
+from . import OK, GemmError, lib
+
+F16 = 0
+BF16 = 1
+
+
+class GroupedDesc(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int32) for n in ("dtype", "b_fp32")]
+                + [(n, ctypes.c_int64) for n in ("groups", "rows", "N", "K")]
+                + [(n, ctypes.c_void_p) for n in ("A", "B", "D")]
+                + [(n, ctypes.c_int64) for n in ("lda", "ldb", "stride_b", "ldd")]
+                + [("cu", ctypes.c_void_p)])
+
+
+class AdapterDesc(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int32) for n in ("dtype", "rank")]
+                + [(n, ctypes.c_int64) for n in ("adapters", "requests", "rows", "N", "K")]
+                + [(n, ctypes.c_void_p) for n in ("A", "B", "D", "down", "up", "scales", "cu", "ids")]
+                + [(n, ctypes.c_int64) for n in ("lda", "ldb", "ldd", "ld_down", "stride_down", "ld_up", "stride_up")])
+
+
+def _packer(desc):
+    """The descriptor's layout as a struct.Struct: packing bytes takes a fifth of the time of a ctypes.Structure."""
+    codes = {ctypes.c_int32: "i", ctypes.c_int64: "q", ctypes.c_void_p: "P"}
+    return struct.Struct("@" + "".join(codes[t] for _, t in desc._fields_)).pack
+
+
+_pack_grouped, _pack_adapter = _packer(GroupedDesc), _packer(AdapterDesc)
+
+
+def declare(L: ctypes.CDLL) -> None:
+    """Argument types of the entry points of the library; descriptors are passed as their bytes or by reference."""
+    i64, vp, i32 = ctypes.c_int64, ctypes.c_void_p, ctypes.c_int
+    for name in ("grouped_nt", "grouped_nn", "grouped_tn"):
+        f = getattr(L, name)
+        f.restype, f.argtypes = i32, [vp, vp]
+        f = getattr(L, name + "_check")
+        f.restype, f.argtypes = i32, [vp]
+    L.adapter_nt.restype, L.adapter_nt.argtypes = i32, [vp, vp, i64, vp]
+    L.adapter_nt_workspace.restype, L.adapter_nt_workspace.argtypes = i64, [vp]
+    L.adapter_nt_check.restype, L.adapter_nt_check.argtypes = i32, [vp]
+
+
+_torch = None
+
+
+def _module():
+    """torch, which the package loads with the first call that needs it (and not by an import statement in each function,
+    which is slower)."""
+    global _torch
+    import torch
+
+    _torch = torch
+    return torch
+
+
+def _first(name, X, dims):
+    """Type code, type and device of the tensor that the others have to match."""
+    torch = _torch or _module()
+    dtype = X.dtype
+    if dtype is torch.float16:
+        code = F16
+    elif dtype is torch.bfloat16:
+        code = BF16
+    else:
+        raise TypeError(f"{name} must be torch.float16 or torch.bfloat16, not {dtype}")
+    if not X.is_cuda:
+        raise ValueError(f"{name} must be a device tensor")
+    if X.dim() != dims:
+        raise ValueError(f"{name} must have {dims} dimensions; got {tuple(X.shape)}")
+    return code, dtype, X.device
+
+
+def _match(name, X, shape, dtype, device):
+    if X.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, not {X.dtype}")
+    if X.device != device:
+        raise ValueError(f"{name} is on {X.device}, the other tensors on {device}")
+    if X.shape != shape:
+        raise ValueError(f"{name} must be {tuple(shape)}; got {tuple(X.shape)}")
+
+
+def _pitch(name, X):
+    """Elements from a row of a 2-D tensor, or of each matrix of a 3-D one, to the next."""
+    st, shape = X.stride(), X.shape
+    width = shape[-1]
+    if width > 1 and st[-1] != 1:
+        raise ValueError(f"{name}: last dimension must be contiguous")
+    if shape[-2] > 1 and X.numel():
+        if st[-2] < width:
+            raise ValueError(f"{name}: rows must not overlap")
+        return st[-2]
+    return width   # a stride that says nothing
+
+
+def _matrices(name, X):
+    """(row pitch, stride from a matrix to the next) of a 3-D tensor."""
+    ld = _pitch(name, X)
+    return ld, X.stride(0) if X.shape[0] > 1 and X.numel() else X.shape[1] * ld
+
+
+def _ints(name, X, n, device):
+    if X.dtype is not (_torch or _module()).int32:
+        raise TypeError(f"{name} must be torch.int32")
+    if X.device != device or X.shape != (n,) or not X.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous tensor of {n} values on {device}")
+    return X.data_ptr()
+
+
+def _run(name, desc, device, *workspace):
+    """Runs an entry point on a device's current stream."""
+    torch = _torch or _module()
+    if device.index != torch.cuda.current_device():   # launches go to the current device
+        with torch.cuda.device(device):
+            return _run(name, desc, device, *workspace)
+    st = getattr(lib(), name)(desc, *workspace, torch._C._cuda_getCurrentRawStream(device.index))
+    if st != OK:
+        raise GemmError(st, name)
+
+
+def _groups(cu):
+    n = cu.numel()
+    if n < 1:
+        raise ValueError("cu needs a value more than there are groups")
+    return n - 1
+
+
+def grouped_product(A, B, cu, *, D=None):
+    """D[r] = B[e] @ A[r] for the rows r = cu[e] .. cu[e + 1] - 1 of each group e.
+
+    A (rows, K) and B (groups, N, K), fp16 or bf16, last dimensions contiguous,
+    other strides as the C-ABI takes them; cu: groups + 1 int32 offsets on the
+    device, not decreasing.  N and K are multiples of 8.  Returns D (rows, N).
+    Rows of no group are left as they were in a given D (one allocated here
+    holds arbitrary values there)."""
+    code, dtype, device = _first("A", A, 2)
+    rows, K = A.shape
+    if B.dim() != 3:
+        raise ValueError(f"B must have 3 dimensions; got {tuple(B.shape)}")
+    G, N = _groups(cu), B.shape[1]
+    _match("B", B, (G, N, K), dtype, device)
+    if D is None:
+        D = _torch.empty((rows, N), dtype=dtype, device=device)
+    else:
+        _match("D", D, (rows, N), dtype, device)
+    ldb, sb = _matrices("B", B)
+    desc = _pack_grouped(code, 0, G, rows, N, K, A.data_ptr(), B.data_ptr(), D.data_ptr(), _pitch("A", A), ldb, sb, _pitch("D", D),
+                         _ints("cu", cu, G + 1, device))
+    _run("grouped_nt", desc, device)
+    return D
+
+
+def grouped_product_grad_input(G, B, cu, *, dA=None):
+    """The gradient of grouped_product for A: dA[r] = B[e].T @ G[r], G (rows, N)
+    being the gradient for D and B (groups, N, K) the matrices.  Returns dA
+    (rows, K); rows of no group are left as they were in a given dA."""
+    code, dtype, device = _first("G", G, 2)
+    rows, N = G.shape
+    if B.dim() != 3:
+        raise ValueError(f"B must have 3 dimensions; got {tuple(B.shape)}")
+    groups, K = _groups(cu), B.shape[2]
+    _match("B", B, (groups, N, K), dtype, device)
+    if dA is None:
+        dA = _torch.empty((rows, K), dtype=dtype, device=device)
+    else:
+        _match("dA", dA, (rows, K), dtype, device)
+    ldb, sb = _matrices("B", B)
+    desc = _pack_grouped(code, 0, groups, rows, N, K, dA.data_ptr(), B.data_ptr(), G.data_ptr(), _pitch("dA", dA), ldb, sb, _pitch("G", G),
+                         _ints("cu", cu, groups + 1, device))
+    _run("grouped_nn", desc, device)
+    return dA
+
+
+def grouped_product_grad_weight(G, A, cu, *, dB=None, dtype=None):
+    """The gradient of grouped_product for B: dB[e] = sum of the outer products
+    of G[r] and A[r] over the rows of group e (zeros without rows), G (rows, N)
+    being the gradient for D and A (rows, K) its input.  Returns dB (groups, N,
+    K) in the operands' type, or in torch.float32 where `dtype` or a given dB
+    says so."""
+    code, own, device = _first("G", G, 2)
+    rows, N = G.shape
+    if A.dim() != 2:
+        raise ValueError(f"A must have 2 dimensions; got {tuple(A.shape)}")
+    groups, K = _groups(cu), A.shape[1]
+    _match("A", A, (rows, K), own, device)
+    if dtype is None:
+        dtype = own if dB is None else dB.dtype
+    if dtype is not own and dtype is not _torch.float32:
+        raise TypeError(f"dB must be {own} or torch.float32, not {dtype}")
+    if dB is None:
+        dB = _torch.empty((groups, N, K), dtype=dtype, device=device)
+    else:
+        _match("dB", dB, (groups, N, K), dtype, device)
+    ldb, sb = _matrices("dB", dB)
+    desc = _pack_grouped(code, 0 if dtype is own else 1, groups, rows, N, K, A.data_ptr(), dB.data_ptr(), G.data_ptr(), _pitch("A", A), ldb, sb,
+                         _pitch("G", G), _ints("cu", cu, groups + 1, device))
+    _run("grouped_tn", desc, device)
+    return dB
+
+
+def _adapter_desc(A, B, down, up, cu, adapters, scales, D):
+    """Descriptor bytes, device and workspace bytes; D None: the address is one that no tensor has."""
+    code, dtype, device = _first("A", A, 2)
+    rows, K = A.shape
+    if B.dim() != 2 or down.dim() != 3 or up.dim() != 3:
+        raise ValueError(f"B must have 2, down and up 3 dimensions; got {tuple(B.shape)}, {tuple(down.shape)}, {tuple(up.shape)}")
+    N, (count, rank, _), requests = B.shape[0], down.shape, _groups(cu)
+    _match("B", B, (N, K), dtype, device)
+    _match("down", down, (count, rank, K), dtype, device)
+    _match("up", up, (count, N, rank), dtype, device)
+    if scales is not None:
+        _match("scales", scales, (count,), _torch.float32, device)
+        if not scales.is_contiguous():
+            raise ValueError("scales must be contiguous")
+    if D is not None:
+        _match("D", D, (rows, N), dtype, device)
+    (ldn, sdn), (lup, sup) = _matrices("down", down), _matrices("up", up)
+    desc = _pack_adapter(code, rank, count, requests, rows, N, K, A.data_ptr(), B.data_ptr(), 16 if D is None else D.data_ptr(), down.data_ptr(),
+                         up.data_ptr(), 0 if scales is None else scales.data_ptr(), _ints("cu", cu, requests + 1, device),
+                         _ints("adapters", adapters, requests, device), _pitch("A", A), _pitch("B", B), N if D is None else _pitch("D", D),
+                         ldn, sdn, lup, sup)
+    return desc, device
+
+
+def _adapter_bytes(desc):
+    n = lib().adapter_nt_workspace(desc)
+    if n < 0:
+        raise GemmError(int(n), "adapter_nt_workspace")
+    return int(n)
+
+
+def adapter_product(A, B, down, up, cu, adapters, scales=None, *, D=None, workspace=None):
+    """D[r] = B @ A[r] + scales[a] * up[a] @ (down[a] @ A[r]), a = adapters[b] for the
+    rows r = cu[b] .. cu[b + 1] - 1 of request b.
+
+    A (rows, K), B (N, K) shared by all rows, down (adapters, rank, K) and up
+    (adapters, N, rank), fp16 or bf16; rank is a multiple of 8 up to 128
+    (adapters of a smaller rank are padded with zeros).  cu: requests + 1 int32
+    offsets, adapters: int32, both on the device; -1 means no adapter.  scales:
+    float32 for each adapter, 1 when not given.  Returns D (rows, N); rows of
+    no request are left as they were in a given D.  `workspace`: a device
+    tensor of at least adapter_product_workspace(...) bytes, 16-byte aligned;
+    allocated here when not given."""
+    _first("A", A, 2)
+    if D is None:
+        if B.dim() != 2:
+            raise ValueError(f"B must have 2 dimensions; got {tuple(B.shape)}")
+        D = _torch.empty((A.shape[0], B.shape[0]), dtype=A.dtype, device=A.device)
+    desc, device = _adapter_desc(A, B, down, up, cu, adapters, scales, D)
+    if workspace is None:
+        have = _adapter_bytes(desc)
+        if have:
+            workspace = _torch.empty(have, dtype=_torch.uint8, device=device)
+    elif workspace.device != device or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on {device}")
+    else:
+        have = workspace.numel() * workspace.element_size()
+    _run("adapter_nt", desc, device, None if workspace is None else workspace.data_ptr(), have)
+    return D
+
+
+def adapter_product_workspace(A, B, down, up, cu, adapters, scales=None) -> int:
+    """Bytes of workspace adapter_product needs for tensors of these shapes."""
+    return _adapter_bytes(_adapter_desc(A, B, down, up, cu, adapters, scales, None)[0])
