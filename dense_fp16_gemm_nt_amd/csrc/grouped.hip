@@ -171,65 +171,76 @@ __device__ __forceinline__ void load_all(const char* const* p, uint32_t dst, std
     (load_to_lds_from<I * STEP>(p[I], dst), ...);
 }
 
-// Adds the adapters' second products to a tile: the requests that its rows
-// belong to, one after the other, make a contraction of `rank` each, in which
-// a row meets its own request's part and zeros elsewhere.
-template <typename T, class C>
-__device__ __forceinline__ void add_adapters(const Args& g, const Work& wk, uint32_t lds, uint32_t lds_wave, int tid,
-                                             const grp::Frags<C, false, C::BM, C::FM>& fx, const grp::Frags<C, false, C::BN, C::FN>& fy, Acc<C>& acc)
+// ADAPT: the adapters' second products are more of the contraction.  The
+// requests with an adapter that a tile's rows belong to, one after the other,
+// have `rank` elements of it each, in which a row meets its own request's part
+// and zeros elsewhere.  A table in LDS says which they are.
+struct Entry {
+    int16_t first, end;   // rows of the tile
+    int32_t id;
+};
+
+// Fills the table and returns how many requests there are; by one wave.
+template <int BM>
+__device__ __forceinline__ int fill_table(const Args& g, const Work& wk, Entry* table)
+{
+    const int lane = threadIdx.x & 63, end = wk.rows < BM ? wk.rows : BM;
+    int count = 0;
+    for (int base = 0; base < g.groups; base += 64) {
+        const int b = base + lane;
+        int lo = end, hi = end, id = -1;
+        if (b < g.groups) {
+            lo = clampi(g.cu[b] - wk.row0, 0, end);
+            hi = clampi(g.cu[b + 1] - wk.row0, lo, end);
+            id = g.ids[b];
+        }
+        const bool there = hi > lo && (uint32_t)id < (uint32_t)g.adapters;
+        const uint64_t all = __builtin_amdgcn_ballot_w64(there);
+        const int at = count + __builtin_popcountll(all & ((uint64_t(1) << lane) - 1));
+        // a table of offsets that does not decrease has at most a request for each row
+        if (there && at < BM) table[at] = Entry{(int16_t)lo, (int16_t)hi, id};
+        count += __builtin_popcountll(all);
+        if (__builtin_amdgcn_ballot_w64(b < g.groups && lo >= end) != 0) break;   // requests behind the tile
+    }
+    return count < BM ? count : BM;
+}
+
+// The loads of step s of the requests' part of the contraction.
+template <class C>
+__device__ __forceinline__ void load_requests(const Args& g, const Work& wk, const Entry* table, int count, int s, uint32_t dst, int tid)
 {
     using SX = grp::Side<C, false, C::BM>;
     using SY = grp::Side<C, false, C::BN>;
-    const int lane = tid & 63, end = wk.row0 + (wk.rows < C::BM ? wk.rows : C::BM);
-    int b0 = 0, count = 0;   // the requests with rows of the tile, and those without rows between them
-    for (int base = 0; base < g.groups; base += 64) {
-        const int b = base + lane;
-        const bool there = b < g.groups;
-        const int lo = there ? g.cu[b] : INT32_MAX, hi = there ? g.cu[b + 1] : INT32_MAX;
-        b0 += __builtin_popcountll(__builtin_amdgcn_ballot_w64(there && hi <= wk.row0));
-        const int n = __builtin_popcountll(__builtin_amdgcn_ballot_w64(there && hi > wk.row0 && lo < end));
-        count += n;
-        if (n == 0 && count > 0) break;
-    }
-    const int chunks = count * (int)g.rank_chunks.d, steps = (chunks + C::BK / 8 - 1) / (C::BK / 8);
-    for (int s = 0; s < steps; ++s) {
-        const char* px[SX::LOADS];
-        const char* py[SY::LOADS];
-        auto where = [&](int chunk, int* in) {   // the request of a chunk, or -1
-            const int at = s * (C::BK / 8) + chunk;
-            const int q = (int)g.rank_chunks.of((uint32_t)at);
-            *in = at - q * (int)g.rank_chunks.d;
-            return q < count && b0 + q < g.groups ? b0 + q : -1;
-        };
+    const char* px[SX::LOADS];
+    const char* py[SY::LOADS];
+    auto where = [&](int chunk, int* in) {
+        const int at = s * (C::BK / 8) + chunk, q = (int)g.rank_chunks.of((uint32_t)at);
+        *in = at - q * (int)g.rank_chunks.d;
+        return q < count ? table[q] : Entry{0, 0, -1};
+    };
 #pragma unroll
-        for (int i = 0; i < SX::LOADS; ++i) {
-            int in;
-            const int b = where(SX::chunk(i, tid), &in), r = wk.row0 + SX::row(i, tid);
-            px[i] = (const char*)g_nothing;
-            if (b >= 0 && r < end && r >= g.cu[b] && r < g.cu[b + 1] && (uint32_t)g.ids[b] < (uint32_t)g.adapters)
-                px[i] = g.low + ((int64_t)r * g.rank_chunks.d + in) * 16;
-        }
-#pragma unroll
-        for (int i = 0; i < SY::LOADS; ++i) {
-            int in;
-            const int b = where(SY::chunk(i, tid), &in), r = wk.col0 + SY::row(i, tid);
-            const int id = b >= 0 ? g.ids[b] : -1;
-            py[i] = (const char*)g_nothing;
-            if ((uint32_t)id < (uint32_t)g.adapters && r < g.cols) py[i] = g.up + (int64_t)id * g.up_mat + (int64_t)r * g.up_ld + 16 * in;
-        }
-        grp::publish<0>();   // everyone is done with the ring's first stage
-        load_all<C::THREADS * 16>(px, lds_wave, std::make_integer_sequence<int, SX::LOADS>());
-        load_all<C::THREADS * 16>(py, lds_wave + C::X_BYTES, std::make_integer_sequence<int, SY::LOADS>());
-        grp::publish<0>();
-        grp::multiply<T, C>(fx, fy, 0, acc);
+    for (int i = 0; i < SX::LOADS; ++i) {
+        int in;
+        const Entry e = where(SX::chunk(i, tid), &in);
+        const int r = SX::row(i, tid);
+        px[i] = r >= e.first && r < e.end ? g.low + ((int64_t)(wk.row0 + r) * g.rank_chunks.d + in) * 16 : (const char*)g_nothing;
     }
+#pragma unroll
+    for (int i = 0; i < SY::LOADS; ++i) {
+        int in;
+        const Entry e = where(SY::chunk(i, tid), &in);
+        const int r = wk.col0 + SY::row(i, tid);
+        py[i] = e.id >= 0 && r < g.cols ? g.up + (int64_t)e.id * g.up_mat + (int64_t)r * g.up_ld + 16 * in : (const char*)g_nothing;
+    }
+    load_all<C::THREADS * 16>(px, dst, std::make_integer_sequence<int, SX::LOADS>());
+    load_all<C::THREADS * 16>(py, dst + C::X_BYTES, std::make_integer_sequence<int, SY::LOADS>());
 }
 
 template <typename T, class C, int MODE, bool F32>
 __global__ __launch_bounds__(C::THREADS, C::PER_CU * C::WAVES / 4) void tile_kernel(const Args g)
 {
     constexpr bool XC = MODE == TN, YC = MODE == NN || MODE == TN;
-    __shared__ __attribute__((aligned(1024))) char smem[C::LDS];
+    __shared__ __attribute__((aligned(1024))) char smem[C::LDS + (MODE == ADAPT ? C::BM * sizeof(Entry) + 16 : 0)];
     const Work wk = find_work<C::BM, C::BN, MODE>(g);
     if (!wk.found) return;
     const int tid = threadIdx.x, lane = tid & 63;
@@ -267,8 +278,7 @@ __global__ __launch_bounds__(C::THREADS, C::PER_CU * C::WAVES / 4) void tile_ker
     // Step s is loaded into stage s % STAGES while the STAGES - 1 steps before
     // it are multiplied; steps behind the last load zeros, so that every wait
     // counts the same loads.
-    const int steps = (depth + C::BK - 1) / C::BK;
-    int left = depth;
+    int steps = (depth + C::BK - 1) / C::BK, left = depth;
     uint32_t fill = 0;
     auto load = [&] {
         x.next(mine + fill, left, tid);
@@ -276,17 +286,40 @@ __global__ __launch_bounds__(C::THREADS, C::PER_CU * C::WAVES / 4) void tile_ker
         left -= C::BK;
         fill = fill == (C::STAGES - 1) * C::STAGE ? 0 : fill + C::STAGE;
     };
+    Entry* table = reinterpret_cast<Entry*>(smem + C::LDS);
+    int requests = 0, next = 0;   // ADAPT: of the tile; the next step of theirs
+    auto load_more = [&] {
+        if (MODE == ADAPT && left <= 0 && requests > 0) {
+            load_requests<C>(g, wk, table, requests, next++, mine + fill, tid);
+            fill = fill == (C::STAGES - 1) * C::STAGE ? 0 : fill + C::STAGE;
+        } else {
+            load();
+        }
+    };
+    if constexpr (MODE == ADAPT) {
+        const int own = steps < C::STAGES - 1 ? steps : C::STAGES - 1;
+        for (int s = 0; s < own; ++s) load();
+        int* count = reinterpret_cast<int*>(table + C::BM);
+        if (w == 0) {
+            const int n = fill_table<C::BM>(g, wk, table);
+            if (lane == 0) *count = n;
+        }
+        __syncthreads();
+        requests = __builtin_amdgcn_readfirstlane(*count);
+        for (int s = own; s < C::STAGES - 1; ++s) load_more();
+        steps += (requests * (int)g.rank_chunks.d + C::BK / 8 - 1) / (C::BK / 8);
+    } else {
 #pragma unroll
-    for (int s = 0; s < C::STAGES - 1; ++s) load();
+        for (int s = 0; s < C::STAGES - 1; ++s) load();
+    }
     const bool busy = MODE == TN || wk.rows > wm * C::FM * 32;   // the wave has rows
     uint32_t stage = 0;
     for (int s = 0; s < steps; ++s) {
         grp::publish<(C::STAGES - 2) * C::LOADS>();
-        load();
+        load_more();
         if (busy) grp::multiply<T, C>(fx, fy, stage, acc);
         stage = stage == (C::STAGES - 1) * C::STAGE ? 0 : stage + C::STAGE;
     }
-    if constexpr (MODE == ADAPT) add_adapters<T, C>(g, wk, lds, mine, tid, fx, fy, acc);
     grp::publish<0>();
     grp::add_waves<C>(smem, k, lane, acc);
     if (k > 0) return;
@@ -308,54 +341,78 @@ constexpr int64_t kMaxRows = (int64_t(1) << 31) - 1024;
 constexpr int64_t kMaxGroups = int64_t(1) << 22;
 constexpr int64_t kMaxTiles = int64_t(1) << 22;       // workgroups of a launch, at most 512 threads each: less than 2^32 threads
 
+// Shapes of tiles: rows x columns x contraction, waves along these, stages,
+// workgroups of a compute unit.
+using Tiny = Cfg<16, 16, 512, 1, 1, 4, 4, 1>;
 using Small = Cfg<32, 32, 256, 1, 1, 4, 4, 1>;
 using Flat = Cfg<32, 128, 64, 1, 4, 1, 4, 2>;
+using Low64 = Cfg<32, 64, 128, 1, 1, 4, 6, 1>;
+using Low128 = Cfg<32, 128, 128, 1, 1, 4, 4, 1>;
+using Square = Cfg<64, 64, 128, 2, 2, 1, 4, 1>;
 using Middle = Cfg<128, 128, 64, 2, 2, 1, 2, 2>;
 using Large = Cfg<256, 256, 64, 2, 4, 1, 2, 1>;
 
-template <typename T, int MODE, bool F32>
-const void* kernel(int shape)
+struct Shape {
+    int bm, bn, threads;
+    const void* f;
+};
+
+template <typename T, class C, int MODE, bool F32 = false>
+Shape shape()
 {
-    if constexpr (MODE != TN) {
-        if (shape == 0) return (const void*)&tile_kernel<T, Small, MODE, F32>;
-        if (shape == 1) return (const void*)&tile_kernel<T, Flat, MODE, F32>;
-    }
-    if constexpr (MODE != LOW) {
-        if (shape == 3) return (const void*)&tile_kernel<T, Large, MODE, F32>;
-    }
-    return (const void*)&tile_kernel<T, Middle, MODE, F32>;
+    return {C::BM, C::BN, C::THREADS, (const void*)&tile_kernel<T, C, MODE, F32>};
 }
 
-template <int MODE, bool F32 = false>
-int run(int dtype, const Args& args, int shape, int cus, hipStream_t s)
+// Tiles by the rows that a group has on average, and for few rows by the
+// workgroups that they make.
+template <typename T, int MODE>
+Shape pick(int64_t rows, int64_t groups, int64_t cols, int cus)
 {
-    static constexpr int kBm[] = {32, 32, 128, 256}, kBn[] = {32, 128, 128, 256}, kThreads[] = {256, 256, 256, 512};
+    const int64_t used = groups < rows ? groups : rows, mean = ceil_div(rows, used);
+    if (mean <= 16 && used * ceil_div(cols, 32) < 2 * cus) return shape<T, Tiny, MODE>();
+    if constexpr (MODE == ADAPT) {
+        if (mean <= 32) return shape<T, Small, MODE>();
+        if (mean <= 64) return shape<T, Square, MODE>();
+    } else {
+        if (mean <= 48) return used * ceil_div(mean, 32) * ceil_div(cols, 128) < 2 * cus ? shape<T, Small, MODE>() : shape<T, Flat, MODE>();
+    }
+    const int64_t large = (rows + 255 * used) / 256 * ceil_div(cols, 256);
+    return mean > 160 && large >= cus ? shape<T, Large, MODE>() : shape<T, Middle, MODE>();
+}
+
+template <typename T>
+Shape pick_low(int64_t rows, int64_t requests, int rank)
+{
+    const int64_t used = requests < rows ? requests : rows;
+    if (ceil_div(rows, used) <= 16) return shape<T, Tiny, LOW>();
+    return rank <= 32 ? shape<T, Small, LOW>() : rank <= 64 ? shape<T, Low64, LOW>() : shape<T, Low128, LOW>();
+}
+
+template <typename T, bool F32>
+Shape pick_tn(int64_t rows, int64_t groups, int64_t n, int64_t k, int cus)
+{
+    const int64_t large = groups * ceil_div(n, 256) * ceil_div(k, 256);
+    return rows > 192 * groups && large >= cus ? shape<T, Large, TN, F32>() : shape<T, Middle, TN, F32>();
+}
+
+template <int MODE>
+int run(const Shape& c, const Args& args, hipStream_t s)
+{
     Args g = args;
-    const int64_t ct = ceil_div(g.cols, kBn[shape]);
+    const int64_t ct = ceil_div(g.cols, c.bn);
     g.col_tiles = attn::div_by(ct);
     int64_t wgs;
     if (MODE == TN) {
-        const int64_t t = ct * ceil_div(g.x_cols, kBm[shape]), padded = t < 8 * kNumXcd ? t : ceil_div(t, kNumXcd) * kNumXcd;
+        const int64_t t = ct * ceil_div(g.x_cols, c.bm), padded = t < 8 * kNumXcd ? t : ceil_div(t, kNumXcd) * kNumXcd;
         g.group_tiles = (uint32_t)t;
         g.per_group = attn::div_by(padded);
         wgs = padded * g.groups;
     } else {
         const int64_t used = MODE == ADAPT ? 1 : g.groups < g.rows ? g.groups : g.rows;   // groups with rows
-        wgs = (g.rows + used * (kBm[shape] - 1)) / kBm[shape] * ct;
+        wgs = (g.rows + used * (c.bm - 1)) / c.bm * ct;
     }
     if (wgs > kMaxTiles) return GEMM_F16_NT_UNSUPPORTED;
-    (void)cus;
-    const void* f = dtype == GROUPED_F16 ? kernel<F16, MODE, F32>(shape) : kernel<BF16, MODE, F32>(shape);
-    return launch(f, wgs, kThreads[shape], &g, s);
-}
-
-// Tiles by the rows that a group has on average.
-int shape_of(int64_t rows, int64_t groups, int64_t cols, int cus)
-{
-    const int64_t used = groups < rows ? groups : rows, mean = ceil_div(rows, used);
-    if (mean <= 48) return used * ceil_div(mean, 32) * ceil_div(cols, 128) < 2 * cus ? 0 : 1;
-    const int64_t large = (rows + 255 * used) / 256 * ceil_div(cols, 256);
-    return mean > 160 && large >= cus ? 3 : 2;
+    return launch(c.f, wgs, c.threads, &g, s);
 }
 
 bool widths_ok(int64_t n, int64_t k) { return n % 8 == 0 && k % 8 == 0 && n < kMaxWidth && k < kMaxWidth; }
@@ -462,7 +519,8 @@ int grouped_nt(const grouped_desc* d, void* stream)
     g.rows = (int)d->rows;
     g.cols = (int)d->N;
     g.depth = (int)d->K;
-    return run<NT>(d->dtype, g, shape_of(d->rows, d->groups, d->N, cus), cus, (hipStream_t)stream);
+    return run<NT>(d->dtype == GROUPED_F16 ? pick<F16, NT>(d->rows, d->groups, d->N, cus) : pick<BF16, NT>(d->rows, d->groups, d->N, cus), g,
+                   (hipStream_t)stream);
 }
 
 int grouped_nn(const grouped_desc* d, void* stream)
@@ -484,7 +542,8 @@ int grouped_nn(const grouped_desc* d, void* stream)
     g.rows = (int)d->rows;
     g.cols = (int)d->K;
     g.depth = (int)d->N;
-    return run<NN>(d->dtype, g, shape_of(d->rows, d->groups, d->K, cus), cus, (hipStream_t)stream);
+    return run<NN>(d->dtype == GROUPED_F16 ? pick<F16, NN>(d->rows, d->groups, d->K, cus) : pick<BF16, NN>(d->rows, d->groups, d->K, cus), g,
+                   (hipStream_t)stream);
 }
 
 int grouped_tn(const grouped_desc* d, void* stream)
@@ -507,9 +566,10 @@ int grouped_tn(const grouped_desc* d, void* stream)
     g.rows = (int)d->rows;
     g.x_cols = (int)d->N;
     g.cols = (int)d->K;
-    const int64_t large = d->groups * ceil_div(d->N, 256) * ceil_div(d->K, 256);
-    const int shape = d->rows > 192 * d->groups && large >= cus ? 3 : 2;
-    return d->b_fp32 ? run<TN, true>(d->dtype, g, shape, cus, (hipStream_t)stream) : run<TN>(d->dtype, g, shape, cus, (hipStream_t)stream);
+    const int64_t m = d->rows, e = d->groups, n = d->N, k = d->K;
+    const Shape c = d->dtype == GROUPED_F16 ? (d->b_fp32 ? pick_tn<F16, true>(m, e, n, k, cus) : pick_tn<F16, false>(m, e, n, k, cus))
+                                            : (d->b_fp32 ? pick_tn<BF16, true>(m, e, n, k, cus) : pick_tn<BF16, false>(m, e, n, k, cus));
+    return run<TN>(c, g, (hipStream_t)stream);
 }
 
 int64_t adapter_nt_workspace(const adapter_desc* d)
@@ -526,7 +586,7 @@ int adapter_nt(const adapter_desc* d, void* workspace, int64_t workspace_bytes, 
     if ((st = check_workspace(workspace, workspace_bytes, low_bytes(d))) != GEMM_F16_NT_OK) return st;
     int cus = 0;
     if ((st = device_cus(&cus)) != GEMM_F16_NT_OK) return st;
-    const bool adapted = low_bytes(d) > 0;
+    const bool adapted = low_bytes(d) > 0, f16 = d->dtype == GROUPED_F16;
     Args g = {};
     g.x = (const char*)d->A;
     g.cu = d->cu;
@@ -546,7 +606,9 @@ int adapter_nt(const adapter_desc* d, void* workspace, int64_t workspace_bytes, 
         l.d = (char*)workspace;
         l.d_ld = 2 * d->rank;
         l.cols = (int)d->rank;
-        if ((st = run<LOW>(d->dtype, l, d->rank <= 32 ? 0 : 1, cus, (hipStream_t)stream)) != GEMM_F16_NT_OK) return st;
+        if ((st = run<LOW>(f16 ? pick_low<F16>(d->rows, d->requests, d->rank) : pick_low<BF16>(d->rows, d->requests, d->rank), l, (hipStream_t)stream)) !=
+            GEMM_F16_NT_OK)
+            return st;
     }
     g.y = (const char*)d->B;
     g.y_ld = 2 * d->ldb;
@@ -557,7 +619,7 @@ int adapter_nt(const adapter_desc* d, void* workspace, int64_t workspace_bytes, 
     g.up = (const char*)d->up;
     g.up_ld = 2 * d->ld_up;
     g.up_mat = 2 * d->stride_up;
-    return run<ADAPT>(d->dtype, g, shape_of(d->rows, 1, d->N, cus), cus, (hipStream_t)stream);
+    return run<ADAPT>(f16 ? pick<F16, ADAPT>(d->rows, 1, d->N, cus) : pick<BF16, ADAPT>(d->rows, 1, d->N, cus), g, (hipStream_t)stream);
 }
 
 }  // extern "C"

@@ -39,7 +39,8 @@ template <int BM_, int BN_, int BK_, int WM_, int WN_, int WK_, int STAGES_, int
 struct Cfg {
     static constexpr int BM = BM_, BN = BN_, BK = BK_, WM = WM_, WN = WN_, WK = WK_, STAGES = STAGES_, PER_CU = PER_CU_;
     static constexpr int WAVES = WM * WN * WK, THREADS = 64 * WAVES;
-    static constexpr int FM = BM / WM / 32, FN = BN / WN / 32;   // 32 x 32 blocks of a wave
+    // 32 x 32 blocks of a wave; a side of 16 is half a block, whose other half repeats it and is not stored
+    static constexpr int FM = BM == 16 ? 1 : BM / WM / 32, FN = BN == 16 ? 1 : BN / WN / 32;
     static constexpr int KSUB = BK / 16 / WK;                    // products of a block and step
     static constexpr int X_BYTES = BM * BK * 2, Y_BYTES = BN * BK * 2, STAGE = X_BYTES + Y_BYTES;
     static constexpr int LDS = STAGES * STAGE;
@@ -137,10 +138,10 @@ struct Frags {
         for (int n = 0; n < N; ++n) {
             if (COLS) {
                 const int r = k0 + 8 * half + (i16 >> 2);   // k0 is a multiple of 16
-                const int c = (first + 32 * n) / 8 + (((lane >> 4) & 1) << 1) + ((i16 & 3) >> 1);
+                const int c = (first + 32 * n) / 8 + (EXT == 16 ? 0 : ((lane >> 4) & 1) << 1) + ((i16 & 3) >> 1);
                 a[n] = lds + r * L::PITCH + ((c ^ L::swz(r)) << 4) + ((i16 & 1) << 3);
             } else {
-                const int r = first + (lane & 31), c = k0 / 8 + 2 * n + half;
+                const int r = first + (lane & (EXT == 16 ? 15 : 31)), c = k0 / 8 + 2 * n + half;
                 a[n] = lds + r * L::PITCH + ((c ^ L::swz(r)) << 4);
             }
         }
@@ -250,7 +251,7 @@ __device__ __forceinline__ void store(char* lds, char* d, int64_t ld, int rows, 
         for (int q = 0; q < 32 / PER; ++q) {
             const int y = q * PER + lane / CH, c = lane % CH;
             const u32x4 v = *reinterpret_cast<const u32x4*>(lds + y * PITCH + ((c ^ (y % CH)) << 4));
-            if (32 * i + y < rows && c * (16 / SIZE) < cols)
+            if ((C::BM > 16 || y < 16) && (C::BN > 16 || c * (16 / SIZE) < 16) && 32 * i + y < rows && c * (16 / SIZE) < cols)
                 *reinterpret_cast<u32x4*>(d + (int64_t)(32 * i + y) * ld + 16 * c) = v;
         }
         __builtin_amdgcn_wave_barrier();
