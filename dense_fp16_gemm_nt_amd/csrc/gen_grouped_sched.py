@@ -1,0 +1,333 @@
+"""Generate the instruction schedules of the grouped products' large tiles (grouped_ring.hpp).
+
+The k loops are inline assembly, as those of the four-wave ring are, and for
+the same reason: with one wave to a SIMD nothing hides a stalled instruction
+stream, so the order of matrix-core instructions, LDS reads, loads to LDS and
+waits is fixed here.  Run it after changing a schedule:
+
+    python gen_grouped_sched.py            # writes grouped_sched.inc
+
+Output tile 256 x 256, 64-wide steps of the contraction, 4 waves of 128 x 128
+(8 x 8 blocks of v_mfma_f32_16x16x32, each block's two 32-wide sub-steps back
+to back), two LDS stages.  The A side (rows of the output) and the B side
+(columns) are each in one of two layouts:
+
+  r   by rows: the contraction is contiguous.  LDS rows of 128 bytes, one for
+      each row of the side; a fragment is one ds_read_b128;
+  c   by columns: the side's own index is contiguous.  LDS rows of 512 bytes,
+      one for each element of the contraction; a fragment is two
+      ds_read_b64_tr_b16, each 4 elements of the contraction for 16 columns
+      and 4 groups of lanes.
+
+Four loops are generated: RR, RC and CC (the grouped products NT, NN and TN)
+with 16-bit outputs, and CC with 32-bit outputs.  Each is a macro with the
+operands' type, "f16" or "bf16", as its argument.
+
+LDS: the A side's stages at 0 and 32 KiB, the B side's at 64 and 96 KiB, so
+that one address and an instruction offset reach both stages, then 8 KiB for
+each wave's epilogue.  Registers are those of the four-wave ring's fourth form:
+accumulators a0..a255, A fragments v64..v127, two sets of B fragments
+v128..v255, whose idle set serves the epilogue.
+
+A step j of the contraction: the late rows' A fragments of this step; a
+release barrier (this wave's and all others' reads of the stage are done); the
+16 loads of step j + 2 into it, spread out; a publish barrier (the loads of
+step j + 1 have landed everywhere); the fragment reads of step j + 1: B blocks
+into the other set, A rows as their rows of this step are done.
+
+The contraction need not be a multiple of 64.  A side by rows then begins
+before its first element, by as much as is missing, and step 0's chunks that
+lie before it get offsets past the buffer's end (%[hm0], %[hm1]), which load
+zeros; a side by columns beside it begins that many rows early, and those
+rows' offsets are masked likewise.  With both sides by columns the rows behind
+the last load zeros by themselves: the buffers end there.
+
+Operands: load offsets %[axQ], %[bxQ] (less 1024 * (Q mod 4), the instruction
+offset of the load); fragment addresses %[raN], %[rbN] (N: sub-step by rows,
+block by columns); resources %[rsa], %[rsb], %[rsd]; the wave's LDS load base
+%[lb]; the steps' byte offsets %[koa], %[kha], %[kob], %[khb] (next step and
+the one after; the first of each is 0 on entry), advanced by 128 by rows and
+by %[sta], %[stb] by columns; the count %[rem] of steps, at least 2; epilogue
+%[ewJ], %[erQ], %[soQ], %[gstr], scratch %[sdo]; RC: %[hk] masked rows and
+%[kr], the lane's row of its first load.
+"""
+from __future__ import annotations
+
+import os
+import sys
+
+import gen_ring4_sched as ring4
+from gen_ring4_sched import KSUB, LOAD3, NB, NLOAD, NQ, a4, areg, b4, epi_set4, head_reg, late_rows4, mfma_block
+
+STAGE_BYTES = 32768     # of one side
+SIDE_B = 65536
+HALF_C = 32 * 512       # bytes of 32 LDS rows by columns
+
+
+def side_steps(op: str, layout: str) -> str:
+    return "128" if layout == "r" else f"%[st{op}]"
+
+
+class Emitter(ring4.Emitter):
+    def __init__(self, la: str, lb: str, out32: bool) -> None:
+        super().__init__()
+        self.layout = {"a": la, "b": lb}
+        self.out32 = out32
+
+    @staticmethod
+    def m0(op: str, q: int, stage: int) -> str:
+        return f"s_add_u32 m0, %[lb], {stage * STAGE_BYTES + (SIDE_B if op == 'b' else 0) + 4096 * (q // 4)}"
+
+    @staticmethod
+    def load(op: str, q: int, koff: str, reg: str | None = None) -> str:
+        imm = 1024 * (q % 4)
+        off = f" offset:{imm}" if imm else ""
+        return f"buffer_load_dwordx4 {reg or f'%[{op}x{q}]'}, %[rs{op}], %[{koff}{op}] offen{off} lds"
+
+    def parts(self, op: str) -> tuple:
+        """The instructions of a fragment read."""
+        return (None,) if self.layout[op] == "r" else (0, 1)
+
+    def read(self, op: str, h: int, idx: int, stage: int, p: int, part) -> None:
+        reg = a4(h, idx) if op == "a" else b4(p, h, idx)
+        key = (op, h, idx, p if op == "b" else None)
+        if part is None:
+            off = stage * STAGE_BYTES + 2048 * idx
+            self.op(f"ds_read_b128 {reg}, %[r{op}{h}] offset:{off}")
+            self.lgkm.append(key)
+            return
+        first = int(reg[2:].split(":")[0]) + 2 * part
+        off = stage * STAGE_BYTES + h * HALF_C + 2048 * part
+        self.op(f"ds_read_b64_tr_b16 v[{first}:{first + 1}], %[r{op}{idx}] offset:{off}")
+        self.lgkm.append(key if part == 1 else ("first half", *key))
+
+    def mfma(self, p: int, h: int, i: int, j: int, first: bool) -> None:
+        self.wait_frag(("a", h, i, None), ("b", h, j, p))
+        c = areg(i, j)
+        self.op(f"v_mfma_f32_16x16x32_@T@ {c}, {b4(p, h, j)}, {a4(h, i)}, {'0' if first else c}")
+
+    # --- epilogue: rows of 16, as soon as their last products are done -------
+    def group(self, i: int, t: int) -> list[tuple[str, bool]]:
+        if not self.out32:
+            return [(text.replace("v_cvt_pk_f16_f32", "v_cvt_pk_@T@_f32"), lds) for text, lds in ring4.epilogue_group(i, t, t + 32)]
+        # 32-bit outputs: four columns of a row from each lane, 64 bytes of 16
+        # rows to a store; ordinary stores, so that L2 joins the halves of lines
+        out: list[tuple[str, bool]] = []
+        base = t + 32 * (i % 2)
+        for j in range(NB):
+            v, b = base + 4 * j, NB * i + j
+            out += [(f"v_accvgpr_read_b32 v{v + r}, a{4 * b + r}", False) for r in range(4)]
+            off = f" offset:{64 * j}" if j else ""
+            out.append((f"buffer_store_dwordx4 v[{v}:{v + 3}], %[so0], %[rsd], %[sdo] offen{off}", False))
+        out.append(("s_add_u32 %[sdo], %[sdo], %[gstr]", False))
+        return out
+
+    def epi_after(self, g: int, per_slot: int, delay: int, t: int) -> None:
+        while self.epi_next < NB and g >= 2 * NB * self.epi_next + 2 * NB - 1 + delay:
+            self.epi_q += self.group(self.epi_next, t)
+            self.epi_next += 1
+        for _ in range(min(per_slot, len(self.epi_q))):
+            self.epi_emit(*self.epi_q.pop(0))
+
+    def epi_rest(self, t: int) -> None:
+        for _ in range(3):
+            self.op("s_nop 7")
+        while self.epi_next < NB:
+            self.epi_q += self.group(self.epi_next, t)
+            self.epi_next += 1
+        while self.epi_q:
+            self.epi_emit(*self.epi_q.pop(0))
+
+
+def emit_step(e: Emitter, stage: int, first: bool, ahead: bool, has_next: bool, last: bool, tail: list[str], p: dict) -> None:
+    """One step reading `stage`.  ahead: it loads step j + 2; has_next: step j + 1 exists; last: with the epilogue."""
+    ng = KSUB * NQ
+    gaps: list[list[tuple]] = [[] for _ in range(ng)]
+    late = late_rows4(p)
+    rel, pub, every, limit = p["rel"], p["pub"], p["load_every"], p["read_limit"]
+
+    def first_free(g: int) -> int:
+        while gaps[g]:
+            g += 1
+        return g
+
+    if not last:
+        br = [t for t in tail if t.startswith(("s_cbranch", "s_branch"))]
+        rest = [t for t in tail if t not in br]
+        assert tail == rest + br, "branches close the tail"
+        for k, t in enumerate(rest):
+            gaps[ng - 1 - len(rest) + k].append(("text", t))
+        for t in br:
+            gaps[ng - 1].append(("text", t))
+    if not first:
+        g = 0
+        for i in late:
+            for h in range(KSUB):
+                for part in e.parts("a"):
+                    gaps[g].append(("read", ("a", h, i, stage, stage, part)))
+                    g += 1
+        assert g < rel - 1, "late reads after the release"
+    if ahead:
+        gaps[rel - 1].append(("text", "s_waitcnt lgkmcnt(0)", "clear"))
+        gaps[rel].append(("text", "s_barrier"))
+    if has_next:
+        gaps[pub - 1].append(("wait",))
+        gaps[pub].append(("text", "s_barrier"))
+    loads = []
+    if ahead:
+        prev, group = -1, None
+        for k, (op, q) in enumerate(LOAD3):
+            g = first_free(max(rel + 1 + every * k, prev + 1))
+            if (op, q // 4) != group:
+                m = next((x for x in range(g - 1, max(prev, rel), -1) if not gaps[x]), None)
+                if m is None:
+                    m = first_free(max(prev, rel) + 1)
+                    g = first_free(m + 1)
+                gaps[m].append(("text", Emitter.m0(op, q, stage)))
+                group = (op, q // 4)
+            gaps[g].append(("text", Emitter.load(op, q, "kh")))
+            loads.append(g)
+            prev = g
+        assert prev < ng - 8, "loads run into the tail"
+    if has_next:
+        young = sum(1 for g in loads if g < pub - 1)   # loads of step j + 2 need not have landed
+        gaps[pub - 1] = [("text", f"s_waitcnt vmcnt({young}) lgkmcnt(0)", "clear")]
+        reads = [(pub + 1, ("a", h, 0, part)) for h in range(KSUB) if 0 not in late for part in e.parts("a")]
+        reads += [(pub + 1, ("b", h, j, part)) for j in range(NB) for h in range(KSUB) for part in e.parts("b")]
+        reads += [(max(pub + 1, 2 * NB * i + 2 * NB + p["a_delay"]), ("a", h, i, part)) for i in range(1, NB) if i not in late
+                  for h in range(KSUB) for part in e.parts("a")]
+        reads.sort(key=lambda r: r[0])
+        g = at = pub + 1
+        for n, (earliest, (op, h, idx, part)) in enumerate(reads):
+            at = max(at, earliest)
+            open_gaps = [x for x in range(at, limit) if not gaps[x]]
+            crowded = len(reads) - n > len(open_gaps)   # two to a gap where one each does not fit
+            g = next((x for x in range(at, limit) if len(gaps[x]) < (2 if crowded else 1) and all(it[0] == "read" for it in gaps[x])), None)
+            assert g is not None, "next-step reads beyond the read limit"
+            gaps[g].append(("read", (op, h, idx, stage ^ 1, stage ^ 1, part)))
+            at = g
+        gaps[first_free(g + p["f0_lat"])].append(("text", "s_waitcnt lgkmcnt(0)", "clear"))
+    texts = [(g, it[1]) for g in range(ng) for it in gaps[g] if it[0] == "text"]
+    writers = [g for g, t in texts if t.startswith(("s_add_u32", "s_sub_u32"))]
+    compares = [g for g, t in texts if t.startswith("s_cmp")]
+    assert not compares or max(writers, default=-1) < min(compares), "SCC clobbered before the branch"
+
+    t_base = epi_set4(stage)
+    for g in range(ng):
+        pq, h = divmod(g, 2)
+        i, j = mfma_block(pq, "snake")
+        if last and g == 0:
+            e.epi_start("snake")
+        e.mfma(stage, h, i, j, first and h == 0)
+        if last:
+            e.epi_after(g, p["epi_slot"], p["epi_delay"], t_base)
+        for it in gaps[g]:
+            if it[0] == "read":
+                e.read(*it[1])
+            else:
+                e.op(it[1])
+                if len(it) > 2:
+                    e.lgkm.clear()
+    if last:
+        e.epi_rest(t_base)
+        for t in tail:
+            e.op(t)
+
+
+def generate(la: str, lb: str, p: dict, out32: bool = False) -> str:
+    e = Emitter(la, lb, out32)
+    layout = e.layout
+    head = {op: "none" if la == "c" else layout[op] for op in "ab"}
+    for op, q in LOAD3:
+        if head[op] == "r":
+            e.op(f"v_or_b32 v{head_reg(op, q)}, %[{op}x{q}], %[hm{q % 2}]")
+    if head["b"] == "c":   # rows 2 q further on for load q
+        e.op("v_bfrev_b32 v80, 1")   # 0x80000000
+        for q in range(8):
+            e.op(f"s_sub_i32 %[khb], %[hk], {2 * q}")
+            e.op("v_cmp_gt_i32 vcc, %[khb], %[kr]")
+            e.op(f"v_cndmask_b32 v{head_reg('b', q)}, %[bx{q}], v80, vcc")
+    for step in (0, 1):
+        if step:
+            for op in "ab":
+                e.op(f"s_add_u32 %[ko{op}], %[ko{op}], {side_steps(op, layout[op])}")
+        for op, q in LOAD3:
+            if q % 4 == 0:
+                e.op(Emitter.m0(op, q, step))
+                e.op("s_nop 0")   # M0 write -> LDS-DMA read of M0
+            e.op(Emitter.load(op, q, "ko", f"v{head_reg(op, q)}" if step == 0 and head[op] != "none" else None))
+    for op in "ab":
+        e.op(f"s_add_u32 %[kh{op}], %[ko{op}], {side_steps(op, layout[op])}")
+    e.op(f"s_waitcnt vmcnt({NLOAD})")
+    e.op("s_barrier")
+    order = [("a", h, 0) for h in range(KSUB)] + [("b", h, j) for j in range(NB) for h in range(KSUB)]
+    order += [("a", h, i) for i in range(1, NB) for h in range(KSUB)]
+    for op, h, idx in order:
+        for part in e.parts(op):
+            e.read(op, h, idx, 0, 0, part)
+    pro = list(e.lgkm)
+
+    adv = [f"s_add_u32 %[{k}{op}], %[{k}{op}], {side_steps(op, layout[op])}" for k in ("kh",) for op in "ab"]
+    sub, cmp2 = "s_sub_u32 %[rem], %[rem], 1", "s_cmp_eq_u32 %[rem], 2"
+
+    def step(stage, first, ahead, has_next, last, tail):
+        e.lgkm = list(pro) if first else []
+        emit_step(e, stage, first, ahead, has_next, last, tail, p)
+
+    e.op(cmp2)
+    e.op("s_cbranch_scc1 5f")
+    step(0, True, True, True, False, adv + [sub, cmp2, "s_cbranch_scc1 6f"])
+    e.label("1")
+    step(1, False, True, True, False, adv + [sub, cmp2, "s_cbranch_scc1 8f"])
+    step(0, False, True, True, False, adv + [sub, cmp2, "s_cbranch_scc1 6f", "s_branch 1b"])
+    e.label("5")
+    step(0, True, False, True, False, [sub, "s_branch 2f"])     # two steps in all
+    e.label("6")
+    step(1, False, False, True, False, [sub, "s_branch 3f"])    # the step before the last, in stage 1
+    e.label("8")
+    step(0, False, False, True, False, [sub])                   # the same in stage 0
+    e.label("2")
+    step(1, False, False, False, True, ["s_branch 4f"])         # the last step
+    e.label("3")
+    step(0, False, False, False, True, [])
+    e.label("4")
+    return "\n".join(e.lines)
+
+
+# Loads of step j + 2 all go out in step j, so that they have the rest of it
+# and the next step up to the publish barrier to land.
+ROWS = {"rel": 12, "load_every": 6, "pub": 64, "a_delay": 1, "read_limit": 112, "f0_lat": 8, "epi_slot": 8, "epi_delay": 2}
+MIXED = {**ROWS, "pub": 56}
+COLS = {**ROWS, "rel": 14, "pub": 48}
+
+LOOPS = {   # macro: A side, B side, schedule, 32-bit outputs
+    "G16_GROUPED_RR": ("r", "r", ROWS, False),
+    "G16_GROUPED_RC": ("r", "c", MIXED, False),
+    "G16_GROUPED_CC": ("c", "c", COLS, False),
+    "G16_GROUPED_CC32": ("c", "c", COLS, True),
+}
+
+
+def as_macro(name: str, text: str) -> str:
+    body = []
+    for ln in text.split("\n"):
+        body.append('    "' + ln.replace("@T@", '" TYPE "') + '\\n"')
+    return f"#define {name}(TYPE) \\\n" + " \\\n".join(body) + "\n"
+
+
+def main() -> int:
+    out = os.path.join(os.path.dirname(os.path.abspath(__file__)), "grouped_sched.inc")
+    lines = 0
+    with open(out, "w") as f:
+        f.write("// Generated by gen_grouped_sched.py.  Do not edit.\n")
+        for name, (la, lb, p, out32) in LOOPS.items():
+            text = generate(la, lb, p, out32)
+            lines += len(text.split("\n"))
+            f.write(f"// {name}: {ring4.params_line(p)}.\n")
+            f.write(as_macro(name, text))
+    print(out, lines, "lines")
+    return 0
+
+
+if __name__ == "__main__":
+    sys.exit(main())

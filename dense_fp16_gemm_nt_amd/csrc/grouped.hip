@@ -7,6 +7,7 @@
 #include <hip/hip_runtime.h>
 
 #include "grouped_core.hpp"
+#include "grouped_ring.hpp"
 #include "host.hpp"
 
 using namespace g16;
@@ -88,68 +89,80 @@ struct Work {
 
 constexpr uint32_t kGroupTiles = 4;   // row tiles that neighbours share columns over
 
-// Rows in tiles of BM, those of all groups one after the other.  Each lane
-// looks at one group, 64 at a time.
+// Row tiles of BM, those of all groups one after the other.  Each lane looks at
+// one group, 64 at a time; with up to 64 groups it keeps what it saw.
+template <int BM, int MODE>
+struct Groups {
+    Rows s;
+    uint32_t tiles, upto, total;
+
+    __device__ __forceinline__ void look(const Args& g, int e, int groups)
+    {
+        s = Rows{0, 0};
+        if (e < groups) {
+            if (MODE == ADAPT) {   // requests are neighbours: one run of rows
+                const int a = clampi(g.cu[0], 0, g.rows);
+                s = Rows{a, clampi(g.cu[g.groups], a, g.rows) - a};
+            } else {
+                s = rows_of(g, e);
+                if (MODE == LOW && (uint32_t)g.ids[e] >= (uint32_t)g.adapters) s.count = 0;
+            }
+        }
+        tiles = (uint32_t)(s.count + BM - 1) / BM;
+        upto = wave_scan(tiles);
+    }
+    __device__ __forceinline__ void start(const Args& g)
+    {
+        const int groups = MODE == ADAPT ? 1 : g.groups, lane = threadIdx.x & 63;
+        total = 0;
+        for (int base = 0; base < groups; base += 64) {
+            look(g, base + lane, groups);
+            total += (uint32_t)__builtin_amdgcn_readlane((int)upto, 63);
+        }
+    }
+    // Tile t of `total`.
+    __device__ __forceinline__ Work find(const Args& g, uint32_t t)
+    {
+        const int groups = MODE == ADAPT ? 1 : g.groups, lane = threadIdx.x & 63;
+        uint32_t before = 0;
+        for (int base = 0; base < groups; base += 64) {
+            if (groups > 64) look(g, base + lane, groups);
+            const uint64_t past = __builtin_amdgcn_ballot_w64(before + upto > t);
+            if (past != 0) {
+                const int w = __builtin_ctzll(past);
+                const int first = __builtin_amdgcn_readlane(s.first, w), count = __builtin_amdgcn_readlane(s.count, w);
+                const uint32_t start = before + (uint32_t)__builtin_amdgcn_readlane((int)upto, w) - (uint32_t)__builtin_amdgcn_readlane((int)tiles, w);
+                const int tile0 = (int)(t - start) * BM;
+                return Work{base + w, first + tile0, count - tile0, tile0, 0, true};
+            }
+            before += (uint32_t)__builtin_amdgcn_readlane((int)upto, 63);
+        }
+        return Work{0, 0, 0, 0, 0, false};
+    }
+};
+
 template <int BM, int BN, int MODE>
 __device__ __forceinline__ Work find_work(const Args& g)
 {
-    Work r = {0, 0, 0, 0, 0, false};
-    const int lane = threadIdx.x & 63;
+    uint32_t ti, tj;
     if (MODE == TN) {
         const uint32_t e = g.per_group.of(blockIdx.x), i = blockIdx.x - e * g.per_group.d;
         // whole rounds of the XCDs: each has a part of the group's tiles of its own
         const uint32_t t = g.per_group.d == g.group_tiles ? i : (uint32_t)xcd_slot(i, g.per_group.d);
-        if (t >= g.group_tiles) return r;
-        uint32_t ti, tj;
+        if (t >= g.group_tiles) return Work{0, 0, 0, 0, 0, false};
         grouped_tile_in<uint32_t>(t, g.group_tiles / g.col_tiles.d, g.col_tiles.d, kGroupTiles, &ti, &tj);
         const Rows s = rows_of(g, (int)e);
         return Work{(int)e, s.first, s.count, (int)ti * BM, (int)tj * BN, true};
     }
-    auto tiles_of = [&](int e, Rows& s) {
-        if (MODE == ADAPT) {   // requests are neighbours: one run of rows
-            const int a = clampi(g.cu[0], 0, g.rows);
-            s = Rows{a, clampi(g.cu[g.groups], a, g.rows) - a};
-            return e == 0 ? (uint32_t)(s.count + BM - 1) / BM : 0u;
-        }
-        s = rows_of(g, e);
-        if (MODE == LOW && (uint32_t)g.ids[e] >= (uint32_t)g.adapters) s.count = 0;
-        return (uint32_t)(s.count + BM - 1) / BM;
-    };
-    const int groups = MODE == ADAPT ? 1 : g.groups;
-    Rows s = {0, 0};
-    uint32_t total = 0, tiles = 0, upto = 0;
-    for (int base = 0; base < groups; base += 64) {
-        tiles = base + lane < groups ? tiles_of(base + lane, s) : 0;
-        upto = wave_scan(tiles);
-        total += (uint32_t)__builtin_amdgcn_readlane((int)upto, 63);
-    }
-    const uint32_t all = total * g.col_tiles.d;
-    if (blockIdx.x >= all) return r;
+    Groups<BM, MODE> groups;
+    groups.start(g);
+    const uint32_t all = groups.total * g.col_tiles.d;
+    if (blockIdx.x >= all) return Work{0, 0, 0, 0, 0, false};
     // each XCD has a run of neighbouring tiles, whose rows and columns its L2 holds
     const uint32_t t = (uint32_t)xcd_slot(blockIdx.x, all);
-    uint32_t ti, tj;
-    grouped_tile_in<uint32_t>(t, total, g.col_tiles.d, kGroupTiles, &ti, &tj);
-    uint32_t before = 0;
-    for (int base = 0; base < groups; base += 64) {
-        if (groups > 64) {
-            tiles = base + lane < groups ? tiles_of(base + lane, s) : 0;
-            upto = wave_scan(tiles);
-        }
-        const uint64_t past = __builtin_amdgcn_ballot_w64(before + upto > ti);
-        if (past != 0) {
-            const int w = __builtin_ctzll(past);
-            r.found = true;
-            r.group = base + w;
-            const int first = __builtin_amdgcn_readlane(s.first, w), count = __builtin_amdgcn_readlane(s.count, w);
-            const int start = (int)(ti - before) - (__builtin_amdgcn_readlane((int)upto, w) - __builtin_amdgcn_readlane((int)tiles, w));
-            r.tile0 = start * BM;
-            r.row0 = first + r.tile0;
-            r.rows = count - r.tile0;
-            r.col0 = (int)tj * BN;
-            return r;
-        }
-        before += (uint32_t)__builtin_amdgcn_readlane((int)upto, 63);
-    }
+    grouped_tile_in<uint32_t>(t, groups.total, g.col_tiles.d, kGroupTiles, &ti, &tj);
+    Work r = groups.find(g, ti);
+    r.col0 = (int)tj * BN;
     return r;
 }
 
@@ -335,6 +348,100 @@ __global__ __launch_bounds__(C::THREADS, C::PER_CU * C::WAVES / 4) void tile_ker
     grp::store<T, C, F32>(smem + AFTER + (wm * C::WN + wn) * STAGING, d, g.d_ld, rows, cols, scale, acc, lane);
 }
 
+// Large tiles of NT, NN and TN: a workgroup for each compute unit walks them.
+template <typename T, int MODE, bool F32>
+__global__ __launch_bounds__(256, 1) void ring_kernel(const Args g)
+{
+    constexpr bool XC = MODE == TN, YC = MODE == NN || MODE == TN;
+    constexpr int TILE = grp::kRingTile, STEP = grp::kRingStep;
+    __shared__ __attribute__((aligned(1024))) char smem[grp::kRingLds];
+    const int lane = threadIdx.x & 63;
+    const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wm = w / 2 * 128, wn = w % 2 * 128;
+    const uint32_t lds = attn::lds_address(smem), lb = lds + 8192u * (uint32_t)w;
+
+    Groups<TILE, MODE> groups;
+    uint32_t total;
+    if (MODE == TN) {
+        total = (uint32_t)g.groups * g.group_tiles;
+    } else {
+        groups.start(g);
+        total = groups.total * g.col_tiles.d;
+    }
+    uint32_t slot = (uint32_t)xcd_slot(blockIdx.x, gridDim.x);
+    if (slot >= total) return;
+
+    grp::RingSide<XC> a;
+    grp::RingSide<YC> b;
+    grp::RingStore out;
+    a.start(lds, g.x_ld, wm, w, lane);
+    b.start(lds + 65536, g.y_ld, wn, w, lane);
+    out.template start<F32>(lds, g.d_ld, w, lane);
+    const uint32_t sta = (uint32_t)(STEP * g.x_ld), stb = (uint32_t)(STEP * g.y_ld);
+    // the contraction's first step is the partial one: see gen_grouped_sched.py
+    uint32_t kt = (uint32_t)(g.depth + STEP - 1) / STEP;
+    const int hk = MODE == TN ? 0 : (int)kt * STEP - g.depth, kr = 16 * w + lane / 32;
+    uint32_t hm[2];
+#pragma unroll
+    for (int q = 0; q < 2; ++q) hm[q] = 8 * ((lane & 7) ^ grp::RingSide<false>::swz(8 * q + lane / 8)) < hk ? grp::kBeyond : 0u;
+
+    for (; slot < total; slot += gridDim.x) {
+        uint32_t ti, tj;
+        Work wk;
+        if (MODE == TN) {
+            const uint32_t e = g.per_group.of(slot);
+            grouped_tile_in<uint32_t>(slot - e * g.group_tiles, g.group_tiles / g.col_tiles.d, g.col_tiles.d, kGroupTiles, &ti, &tj);
+            const Rows s = rows_of(g, (int)e);
+            wk = Work{(int)e, s.first, s.count, (int)clamped_origin(ti, TILE, g.x_cols), 0, true};
+            kt = (uint32_t)(s.count + STEP - 1) / STEP;
+            if (kt < 2) kt = 2;
+        } else {
+            grouped_tile_in<uint32_t>(slot, groups.total, g.col_tiles.d, kGroupTiles, &ti, &tj);
+            wk = groups.find(g, ti);
+        }
+        wk.col0 = (int)clamped_origin(tj, TILE, g.cols);
+
+        u32x4 rsa, rsb;
+        int rows = 128;   // of the wave
+        const char* d;
+        if (MODE == TN) {
+            const int64_t n = wk.rows;
+            rsa = grp::ring_rsrc(g.x + wk.row0 * g.x_ld + 2 * (int64_t)wk.tile0, n == 0 ? 0 : (n - 1) * g.x_ld + 2 * TILE);
+            rsb = grp::ring_rsrc(g.y + wk.row0 * g.y_ld + 2 * (int64_t)wk.col0, n == 0 ? 0 : (n - 1) * g.y_ld + 2 * TILE);
+            d = g.d + wk.group * g.d_mat + (int64_t)(wk.tile0 + wm) * g.d_ld;
+        } else {
+            const int64_t n = wk.rows < TILE ? wk.rows : TILE;
+            const char* mat = g.y + wk.group * g.y_mat;
+            rsa = grp::ring_rsrc(g.x + wk.row0 * g.x_ld - 2 * hk, (n - 1) * g.x_ld + 2 * (int64_t)(g.depth + hk));
+            if (MODE == NT)
+                rsb = grp::ring_rsrc(mat + wk.col0 * g.y_ld - 2 * hk, (TILE - 1) * g.y_ld + 2 * (int64_t)(g.depth + hk));
+            else
+                rsb = grp::ring_rsrc(mat + 2 * (int64_t)wk.col0 - hk * g.y_ld, (int64_t)(g.depth + hk - 1) * g.y_ld + 2 * TILE);
+            rows = clampi((int)n - wm, 0, 128);
+            d = g.d + (int64_t)(wk.row0 + wm) * g.d_ld;
+        }
+        const u32x4 rsd = grp::ring_rsrc(d + (int64_t)(wk.col0 + wn) * (F32 ? 4 : 2), rows == 0 ? 0 : (rows - 1) * g.d_ld + 128 * (F32 ? 4 : 2));
+        uint32_t koa = 0, kob = 0, kha, khb, rem = kt, sdo;
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"   // M0 is written inside, on purpose
+#define G16_GROUPED_BLOCK(LOOP, ...) \
+    if constexpr (std::is_same<T, F16>::value) \
+        asm volatile(LOOP("f16") : G16_GROUPED_STATE : G16_GROUPED_COMMON, __VA_ARGS__ : G16_GROUPED_CLOBBERS); \
+    else \
+        asm volatile(LOOP("bf16") : G16_GROUPED_STATE : G16_GROUPED_COMMON, __VA_ARGS__ : G16_GROUPED_CLOBBERS)
+        if constexpr (MODE == NT) {
+            G16_GROUPED_BLOCK(G16_GROUPED_RR, G16_GROUPED_STAGED, G16_GROUPED_A_ROWS, G16_GROUPED_B_ROWS);
+        } else if constexpr (MODE == NN) {
+            G16_GROUPED_BLOCK(G16_GROUPED_RC, G16_GROUPED_STAGED, G16_GROUPED_A_ROWS, G16_GROUPED_B_COLS, [hk] "s"(hk), [kr] "v"(kr));
+        } else if constexpr (F32) {
+            G16_GROUPED_BLOCK(G16_GROUPED_CC32, G16_GROUPED_A_COLS, G16_GROUPED_B_COLS);
+        } else {
+            G16_GROUPED_BLOCK(G16_GROUPED_CC, G16_GROUPED_STAGED, G16_GROUPED_A_COLS, G16_GROUPED_B_COLS);
+        }
+#pragma clang diagnostic pop
+        wg_barrier();   // every wave is done reading the ring before the next tile's loads
+    }
+}
+
 // ------------------------------------------------------------ validation
 constexpr int64_t kMaxWidth = int64_t(1) << 22;       // elements of a row and its pitch: a tile of 256 rows spans less than 2^31 bytes
 constexpr int64_t kMaxRows = (int64_t(1) << 31) - 1024;
@@ -355,29 +462,50 @@ using Large = Cfg<256, 256, 64, 2, 4, 1, 2, 1>;
 struct Shape {
     int bm, bn, threads;
     const void* f;
+    bool walks;   // a workgroup for each compute unit at most
 };
 
 template <typename T, class C, int MODE, bool F32 = false>
 Shape shape()
 {
-    return {C::BM, C::BN, C::THREADS, (const void*)&tile_kernel<T, C, MODE, F32>};
+    return {C::BM, C::BN, C::THREADS, (const void*)&tile_kernel<T, C, MODE, F32>, false};
+}
+template <typename T, int MODE, bool F32 = false>
+Shape ring_shape()
+{
+    return {grp::kRingTile, grp::kRingTile, 256, (const void*)&ring_kernel<T, MODE, F32>, true};
+}
+
+// What the large tiles' kernel takes: see grouped_ring.hpp.
+constexpr int64_t kRingPitch = int64_t(1) << 21;
+bool ring_takes(int mode, const Args& g)
+{
+    const int64_t pitch = 2 * kRingPitch;
+    if (g.cols < grp::kRingTile || g.x_ld >= pitch || g.y_ld >= pitch || g.d_ld >= 2 * pitch) return false;
+    if (mode == TN) {
+        const int64_t reach = (int64_t)g.rows + 3 * grp::kRingStep;
+        return g.x_cols >= grp::kRingTile && reach * g.x_ld < (int64_t(1) << 32) && reach * g.y_ld < (int64_t(1) << 32);
+    }
+    return g.depth > grp::kRingStep && (mode == NT || ((int64_t)g.depth + 2 * grp::kRingStep) * g.y_ld < (int64_t(1) << 31));
 }
 
 // Tiles by the rows that a group has on average, and for few rows by the
 // workgroups that they make.
 template <typename T, int MODE>
-Shape pick(int64_t rows, int64_t groups, int64_t cols, int cus)
+Shape pick(const Args& g, int cus)
 {
+    const int64_t rows = g.rows, groups = MODE == ADAPT ? 1 : g.groups, cols = g.cols;
     const int64_t used = groups < rows ? groups : rows, mean = ceil_div(rows, used);
     if (mean <= 16 && used * ceil_div(cols, 32) < 2 * cus) return shape<T, Tiny, MODE>();
+    const int64_t large = (rows + 255 * used) / 256 * ceil_div(cols, 256);
     if constexpr (MODE == ADAPT) {
         if (mean <= 32) return shape<T, Small, MODE>();
         if (mean <= 64) return shape<T, Square, MODE>();
+        return mean > 160 && large >= cus ? shape<T, Large, MODE>() : shape<T, Middle, MODE>();
     } else {
         if (mean <= 48) return used * ceil_div(mean, 32) * ceil_div(cols, 128) < 2 * cus ? shape<T, Small, MODE>() : shape<T, Flat, MODE>();
+        return mean > 160 && large >= cus && ring_takes(MODE, g) ? ring_shape<T, MODE>() : shape<T, Middle, MODE>();
     }
-    const int64_t large = (rows + 255 * used) / 256 * ceil_div(cols, 256);
-    return mean > 160 && large >= cus ? shape<T, Large, MODE>() : shape<T, Middle, MODE>();
 }
 
 template <typename T>
@@ -389,21 +517,22 @@ Shape pick_low(int64_t rows, int64_t requests, int rank)
 }
 
 template <typename T, bool F32>
-Shape pick_tn(int64_t rows, int64_t groups, int64_t n, int64_t k, int cus)
+Shape pick_tn(const Args& g, int cus)
 {
-    const int64_t large = groups * ceil_div(n, 256) * ceil_div(k, 256);
-    return rows > 192 * groups && large >= cus ? shape<T, Large, TN, F32>() : shape<T, Middle, TN, F32>();
+    const int64_t large = (int64_t)g.groups * ceil_div(g.x_cols, 256) * ceil_div(g.cols, 256);
+    return g.rows > 192 * (int64_t)g.groups && large >= cus && ring_takes(TN, g) ? ring_shape<T, TN, F32>() : shape<T, Middle, TN, F32>();
 }
 
 template <int MODE>
-int run(const Shape& c, const Args& args, hipStream_t s)
+int run(const Shape& c, const Args& args, int cus, hipStream_t s)
 {
     Args g = args;
     const int64_t ct = ceil_div(g.cols, c.bn);
     g.col_tiles = attn::div_by(ct);
     int64_t wgs;
     if (MODE == TN) {
-        const int64_t t = ct * ceil_div(g.x_cols, c.bm), padded = t < 8 * kNumXcd ? t : ceil_div(t, kNumXcd) * kNumXcd;
+        const int64_t t = ct * ceil_div(g.x_cols, c.bm);
+        const int64_t padded = c.walks || t < 8 * kNumXcd ? t : ceil_div(t, kNumXcd) * kNumXcd;
         g.group_tiles = (uint32_t)t;
         g.per_group = attn::div_by(padded);
         wgs = padded * g.groups;
@@ -412,6 +541,7 @@ int run(const Shape& c, const Args& args, hipStream_t s)
         wgs = (g.rows + used * (c.bm - 1)) / c.bm * ct;
     }
     if (wgs > kMaxTiles) return GEMM_F16_NT_UNSUPPORTED;
+    if (c.walks && wgs > cus) wgs = cus;
     return launch(c.f, wgs, c.threads, &g, s);
 }
 
@@ -519,8 +649,7 @@ int grouped_nt(const grouped_desc* d, void* stream)
     g.rows = (int)d->rows;
     g.cols = (int)d->N;
     g.depth = (int)d->K;
-    return run<NT>(d->dtype == GROUPED_F16 ? pick<F16, NT>(d->rows, d->groups, d->N, cus) : pick<BF16, NT>(d->rows, d->groups, d->N, cus), g,
-                   (hipStream_t)stream);
+    return run<NT>(d->dtype == GROUPED_F16 ? pick<F16, NT>(g, cus) : pick<BF16, NT>(g, cus), g, cus, (hipStream_t)stream);
 }
 
 int grouped_nn(const grouped_desc* d, void* stream)
@@ -542,8 +671,7 @@ int grouped_nn(const grouped_desc* d, void* stream)
     g.rows = (int)d->rows;
     g.cols = (int)d->K;
     g.depth = (int)d->N;
-    return run<NN>(d->dtype == GROUPED_F16 ? pick<F16, NN>(d->rows, d->groups, d->K, cus) : pick<BF16, NN>(d->rows, d->groups, d->K, cus), g,
-                   (hipStream_t)stream);
+    return run<NN>(d->dtype == GROUPED_F16 ? pick<F16, NN>(g, cus) : pick<BF16, NN>(g, cus), g, cus, (hipStream_t)stream);
 }
 
 int grouped_tn(const grouped_desc* d, void* stream)
@@ -566,10 +694,10 @@ int grouped_tn(const grouped_desc* d, void* stream)
     g.rows = (int)d->rows;
     g.x_cols = (int)d->N;
     g.cols = (int)d->K;
-    const int64_t m = d->rows, e = d->groups, n = d->N, k = d->K;
-    const Shape c = d->dtype == GROUPED_F16 ? (d->b_fp32 ? pick_tn<F16, true>(m, e, n, k, cus) : pick_tn<F16, false>(m, e, n, k, cus))
-                                            : (d->b_fp32 ? pick_tn<BF16, true>(m, e, n, k, cus) : pick_tn<BF16, false>(m, e, n, k, cus));
-    return run<TN>(c, g, (hipStream_t)stream);
+    const bool f16 = d->dtype == GROUPED_F16;
+    const Shape c = d->b_fp32 ? (f16 ? pick_tn<F16, true>(g, cus) : pick_tn<BF16, true>(g, cus))
+                              : (f16 ? pick_tn<F16, false>(g, cus) : pick_tn<BF16, false>(g, cus));
+    return run<TN>(c, g, cus, (hipStream_t)stream);
 }
 
 int64_t adapter_nt_workspace(const adapter_desc* d)
@@ -606,9 +734,8 @@ int adapter_nt(const adapter_desc* d, void* workspace, int64_t workspace_bytes, 
         l.d = (char*)workspace;
         l.d_ld = 2 * d->rank;
         l.cols = (int)d->rank;
-        if ((st = run<LOW>(f16 ? pick_low<F16>(d->rows, d->requests, d->rank) : pick_low<BF16>(d->rows, d->requests, d->rank), l, (hipStream_t)stream)) !=
-            GEMM_F16_NT_OK)
-            return st;
+        const Shape c = f16 ? pick_low<F16>(d->rows, d->requests, d->rank) : pick_low<BF16>(d->rows, d->requests, d->rank);
+        if ((st = run<LOW>(c, l, cus, (hipStream_t)stream)) != GEMM_F16_NT_OK) return st;
     }
     g.y = (const char*)d->B;
     g.y_ld = 2 * d->ldb;
@@ -619,7 +746,7 @@ int adapter_nt(const adapter_desc* d, void* workspace, int64_t workspace_bytes, 
     g.up = (const char*)d->up;
     g.up_ld = 2 * d->ld_up;
     g.up_mat = 2 * d->stride_up;
-    return run<ADAPT>(f16 ? pick<F16, ADAPT>(d->rows, 1, d->N, cus) : pick<BF16, ADAPT>(d->rows, 1, d->N, cus), g, (hipStream_t)stream);
+    return run<ADAPT>(f16 ? pick<F16, ADAPT>(g, cus) : pick<BF16, ADAPT>(g, cus), g, cus, (hipStream_t)stream);
 }
 
 }  // extern "C"

@@ -83,6 +83,11 @@ CASES = [
     ([1000, 3, 257, 0, 255, 900, 256, 1500], 2056, 136),
     ([1111, 2222], 8, 64),
     ([5000], 2048, 328),
+    ([1000, 3, 257, 0, 255, 900, 256, 1500, 2000, 513], 4104, 264),   # large tiles: rows, or both sides, by columns too
+    ([1000, 3, 257, 0, 255, 900, 256, 1500, 2000, 513], 264, 4104),
+    ([3000, 1, 64, 65, 129, 2900], 4096, 72),
+    ([3000, 1, 64, 65, 129, 2900], 320, 4096),
+    ([300] * 70, 1024, 256),
 ]
 
 
@@ -119,7 +124,7 @@ def test_whole_numbers(pad, dtype, case):
 
 
 @pytest.mark.parametrize("dtype", sorted(TYPES))
-@pytest.mark.parametrize("lens,n,k", [([7], 96, 1000), ([3, 0, 40], 136, 520), ([100, 90], 264, 328), ([700, 300, 411], 2048, 2056)])
+@pytest.mark.parametrize("lens,n,k", [([7], 96, 1000), ([3, 0, 40], 136, 520), ([100, 90], 264, 328), ([700, 300, 411], 2048, 2056), ([3000, 2500, 1], 4096, 4104)])
 def test_values(lens, n, k, dtype):
     A, G, B, cu = inputs(real, 5, dtype, lens, n, k)
     say(f"[gpu] grouped values {dtype} N={n} K={k} lens={lens}")

@@ -1,0 +1,234 @@
+"""Host checks of the generated k loops of the grouped products' large tiles (csrc/grouped_sched.inc).
+
+A simulator runs each loop's control flow for a range of step counts and checks what keeps its waves together:
+
+* every step of both sides is loaded once, to the stage step % 2, at the step's own offset, and none behind the last;
+* a load goes into a stage only after a barrier that follows the completion of all reads of the stage's contents;
+* a fragment read sees a stage whose loads of one step were all waited for (vmcnt) and then published by a barrier;
+* every product takes the fragments of its own step, sub-step and block, whose reads were waited for (lgkmcnt; LDS reads
+  complete in order), and a block's products follow each other from zero on;
+* the epilogue reads each accumulator once, long enough after its last product, and stores each row group at its own offset;
+* the committed include is what the generator writes.
+
+All four waves run the same stream, so a barrier is the point where all waves' waited-for loads become visible.
+"""
+import importlib.util
+import os
+import re
+import sys
+
+import pytest
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+CSRC = os.path.join(ROOT, "dense_fp16_gemm_nt_amd", "csrc")
+
+
+def _gen():
+    sys.path.insert(0, CSRC)
+    try:
+        spec = importlib.util.spec_from_file_location("gen_grouped_sched", os.path.join(CSRC, "gen_grouped_sched.py"))
+        mod = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(mod)
+    finally:
+        sys.path.remove(CSRC)
+    return mod
+
+
+GEN = _gen()
+NB = 8
+LOAD = re.compile(r"buffer_load_dwordx4 (\S+), %\[rs([ab])\], %\[(ko|kh)([ab])\] offen(?: offset:(\d+))? lds$")
+READ_R = re.compile(r"ds_read_b128 v\[(\d+):\d+\], %\[r([ab])([01])\] offset:(\d+)$")
+READ_C = re.compile(r"ds_read_b64_tr_b16 v\[(\d+):(\d+)\], %\[r([ab])([0-7])\] offset:(\d+)$")
+MFMA = re.compile(r"v_mfma_f32_16x16x32_@T@ a\[(\d+):\d+\], v\[(\d+):\d+\], v\[(\d+):\d+\], (0|a\[\d+:\d+\])$")
+
+
+class Sim:
+    def __init__(self, text, la, lb, out32, kt):
+        self.lines, self.kt, self.out32 = text.split("\n"), kt, out32
+        self.layout = {"a": la, "b": lb}
+        self.labels = {}
+        for i, ln in enumerate(self.lines):
+            if re.match(r"^\d+:$", ln):
+                self.labels.setdefault(ln[:-1], []).append(i)
+
+    def target(self, ref, pc):
+        c = self.labels[ref[:-1]]
+        return min(x for x in c if x > pc) if ref[-1] == "f" else max(x for x in c if x < pc)
+
+    def run(self):
+        kt = self.kt
+        s = {"koa": 0, "kob": 0}            # offsets in steps
+        rem, scc, m0, sdo = kt, 0, None, None
+        vm = []                             # loads and stores in issue order
+        content = {}                        # (side, stage, load) -> (step, "flight" | "landed" | "visible")
+        loaded = set()
+        lgkm = []                           # LDS operations in issue order
+        unread = {}                         # (side, stage) -> "open" | "done" (reads since the last barrier, completed or not)
+        frag, half = {}, {}                 # first VGPR -> (side, step, sub-step, block) once complete
+        head = {}
+        done = {}                           # accumulator block -> products so far
+        final, read_acc, stores, barriers = {}, set(), 0, 0
+        clock, pc, steps = 0, 0, 0
+
+        def complete(n):
+            while len(lgkm) > n:
+                op = lgkm.pop(0)
+                if op[0] == "read":
+                    _, reg, what, part = op
+                    if part is None:
+                        frag[reg] = what
+                    elif part == 0:
+                        half[reg] = what
+                    else:
+                        assert half.pop(reg) == what
+                        frag[reg] = what
+            if not lgkm:
+                for k in unread:
+                    unread[k] = "done"
+
+        while pc < len(self.lines):
+            ln = self.lines[pc]
+            steps += 1
+            assert steps < 100000
+            nop = re.match(r"s_nop (\d+)$", ln)
+            clock += int(nop.group(1)) + 1 if nop else 4 if ln.startswith("v_mfma") else 1
+            if m := re.match(r"s_cmp_eq_u32 %\[rem\], (\d+)$", ln):
+                scc = int(rem == int(m.group(1)))
+            elif ln.startswith("s_cbranch_scc1 "):
+                if scc:
+                    pc = self.target(ln.split()[1], pc)
+                    continue
+            elif ln.startswith("s_branch "):
+                pc = self.target(ln.split()[1], pc)
+                continue
+            elif ln == "s_sub_u32 %[rem], %[rem], 1":
+                rem -= 1
+            elif m := re.match(r"s_add_u32 m0, %\[lb\], (\d+)$", ln):
+                m0 = (int(m.group(1)), pc)
+            elif m := re.match(r"s_add_u32 %\[(k[oh])([ab])\], %\[(k[oh])([ab])\], (\S+)$", ln):
+                assert m.group(2) == m.group(4)
+                assert m.group(5) == ("128" if self.layout[m.group(2)] == "r" else f"%[st{m.group(2)}]")
+                s[m.group(1) + m.group(2)] = s[m.group(3) + m.group(4)] + 1
+            elif ln == "s_mov_b32 %[sdo], 0":
+                sdo = 0
+            elif ln == "s_add_u32 %[sdo], %[sdo], %[gstr]":
+                sdo += 1
+            elif m := re.match(r"v_or_b32 v(\d+), %\[([ab])x(\d)\], %\[hm([01])\]$", ln):
+                assert self.layout[m.group(2)] == "r" and int(m.group(4)) == int(m.group(3)) % 2
+                head[m.group(1)] = (m.group(2), int(m.group(3)))
+            elif m := re.match(r"s_sub_i32 %\[khb\], %\[hk\], (\d+)$", ln):
+                masked = int(m.group(1))
+            elif ln in ("v_cmp_gt_i32 vcc, %[khb], %[kr]", "v_bfrev_b32 v80, 1"):
+                pass
+            elif m := re.match(r"v_cndmask_b32 v(\d+), %\[bx(\d)\], v80, vcc$", ln):
+                assert masked == 2 * int(m.group(2)) and self.layout["b"] == "c"
+                head[m.group(1)] = ("b", int(m.group(2)))
+            elif m := LOAD.match(ln):
+                reg, op, kreg, kop, imm = m.groups()
+                assert op == kop and m0 is not None and pc - m0[1] > 1
+                r = re.match(r"%\[([ab])x(\d)\]$", reg)
+                side, q = (r.group(1), int(r.group(2))) if r else head[reg[1:]]
+                at, imm = m0[0], int(imm or 0)
+                assert side == op and imm == 1024 * (q % 4)
+                at -= 65536 if op == "b" else 0
+                stage, at = divmod(at + imm, 32768)
+                assert stage in (0, 1) and at == 1024 * q
+                step = s[kreg + op]
+                assert step < kt and step % 2 == stage, "a step behind the last, or in the wrong stage"
+                assert (r is None) == (step == 0 and self.layout["a"] == "r"), "step 0 alone goes by masked offsets"
+                assert (op, step, q) not in loaded
+                loaded.add((op, step, q))
+                assert (op, stage) not in unread, "a load into a stage that is still read"
+                content[op, stage, q] = (step, "flight")
+                vm.append(("load", (op, stage, q)))
+            elif m := re.match(r"s_waitcnt (?:vmcnt\((\d+)\))?\s*(?:lgkmcnt\((\d+)\))?$", ln):
+                if m.group(1) is not None:
+                    while len(vm) > int(m.group(1)):
+                        kind, key = vm.pop(0)
+                        if kind == "load":
+                            content[key] = (content[key][0], "landed")
+                if m.group(2) is not None:
+                    complete(int(m.group(2)))
+            elif ln == "s_barrier":
+                barriers += 1
+                assert not lgkm, "LDS operations in flight across a barrier"
+                for key, (step, state) in list(content.items()):
+                    if state == "landed":
+                        content[key] = (step, "visible")
+                unread = {k: v for k, v in unread.items() if v != "done"}
+            elif (m := READ_R.match(ln)) or READ_C.match(ln):
+                if m:
+                    reg, op, h, off = int(m.group(1)), m.group(2), int(m.group(3)), int(m.group(4))
+                    assert self.layout[op] == "r"
+                    stage, off = divmod(off, 32768)
+                    idx, odd = divmod(off, 2048)
+                    part = None
+                    assert odd == 0 and idx < NB
+                else:
+                    m = READ_C.match(ln)
+                    reg, op, idx, off = int(m.group(1)), m.group(3), int(m.group(4)), int(m.group(5))
+                    assert self.layout[op] == "c" and int(m.group(2)) == reg + 1
+                    stage, off = divmod(off, 32768)
+                    h, off = divmod(off, 32 * 512)
+                    part = {0: 0, 4 * 512: 1}[off]
+                    reg -= 2 * part
+                held = {content[op, stage, q] for q in range(8)}
+                assert len(held) == 1, "a stage of two steps"
+                step, state = held.pop()
+                assert state == "visible"
+                frag.pop(reg, None)
+                lgkm.append(("read", reg, (op, step, h, idx), part))
+                unread[op, stage] = "open"
+            elif m := MFMA.match(ln):
+                acc, b, a = int(m.group(1)), int(m.group(2)), int(m.group(3))
+                block, n = acc // 4, done.get(acc // 4, 0)
+                i, j = divmod(block, NB)
+                assert frag.get(a) == ("a", n // 2, n % 2, i), (pc, frag.get(a), n, i)
+                assert frag.get(b) == ("b", n // 2, n % 2, j)
+                assert (m.group(4) == "0") == (n == 0) and (n == 0 or m.group(4) == f"a[{acc}:{acc + 3}]")
+                done[block] = n + 1
+                if n + 1 == 2 * kt:
+                    final[block] = clock - 4   # its own issue is 4 wait states at least
+            elif m := re.match(r"v_accvgpr_read_b32 v(\d+), a(\d+)$", ln):
+                acc = int(m.group(2))
+                assert acc not in read_acc and clock - final[acc // 4] >= 11, "an accumulator read too early or twice"
+                read_acc.add(acc)
+                for base in [x for x in frag if x <= int(m.group(1)) < x + 4]:
+                    del frag[base]
+            elif ln.startswith("v_cvt_pk_@T@_f32 "):
+                pass
+            elif ln.startswith("ds_write_b64 "):
+                lgkm.append(("write",))
+            elif ln.startswith("ds_read_b128 ") and "%[er" in ln:
+                assert not any(x[0] == "write" for x in lgkm)
+                lgkm.append(("staged",))
+            elif ln.startswith("buffer_store_dwordx4 "):
+                assert sdo is not None and sdo == stores // (8 if self.out32 else 4)
+                assert self.out32 or not lgkm
+                vm.append(("store", None))
+                stores += 1
+            elif nop or re.match(r"^\d+:$", ln):
+                pass
+            else:
+                raise AssertionError(f"unknown instruction {ln}")
+            pc += 1
+        return dict(loaded=loaded, done=done, read=read_acc, stores=stores, barriers=barriers, rem=rem)
+
+
+@pytest.mark.parametrize("name", sorted(GEN.LOOPS))
+@pytest.mark.parametrize("kt", [2, 3, 4, 5, 6, 7, 12, 33])
+def test_loop(name, kt):
+    la, lb, p, out32 = GEN.LOOPS[name]
+    r = Sim(GEN.generate(la, lb, p, out32), la, lb, out32, kt).run()
+    assert r["loaded"] == {(op, s, q) for op in "ab" for s in range(kt) for q in range(8)}
+    assert r["done"] == {b: 2 * kt for b in range(64)}
+    assert r["read"] == set(range(256))
+    assert r["stores"] == (64 if out32 else 32)
+    assert r["barriers"] == 2 * kt - 2   # one for step 0, a release for each step that loads, a publish for each but the last
+
+
+def test_committed_include():
+    want = "// Generated by gen_grouped_sched.py.  Do not edit.\n"
+    for name, (la, lb, p, out32) in GEN.LOOPS.items():
+        want += f"// {name}: {GEN.ring4.params_line(p)}.\n" + GEN.as_macro(name, GEN.generate(la, lb, p, out32))
+    assert open(os.path.join(CSRC, "grouped_sched.inc")).read() == want
