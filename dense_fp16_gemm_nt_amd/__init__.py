@@ -390,4 +390,5 @@ from . import attention, grouped  # noqa: E402
 from .attention import (attention_prompt, attention_prompt_workspace, attention_shared_prefix,  # noqa: E402
                         attention_shared_prefix_workspace)
 from .grouped import (adapter_product, adapter_product_workspace, grouped_product, grouped_product_grad_input,  # noqa: E402
-                      grouped_product_grad_weight)
+                      grouped_product_grad_input_workspace, grouped_product_grad_weight, grouped_product_grad_weight_workspace,
+                      grouped_product_workspace)

@@ -19,9 +19,10 @@ to back), two LDS stages.  The A side (rows of the output) and the B side
       ds_read_b64_tr_b16, each 4 elements of the contraction for 16 columns
       and 4 groups of lanes.
 
-Four loops are generated: RR, RC and CC (the grouped products NT, NN and TN)
-with 16-bit outputs, and CC with 32-bit outputs.  Each is a macro with the
-operands' type, "f16" or "bf16", as its argument.
+Three loops are generated: RR, RC and CC, for the grouped products NT, NN and
+TN.  Each is a macro with the operands' type, "f16" or "bf16", as its argument,
+and ends with one of two epilogues: outputs rounded to that type, or, where
+%[wide] is not 0, in 32 bits.
 
 LDS: the A side's stages at 0 and 32 KiB, the B side's at 64 and 96 KiB, so
 that one address and an instruction offset reach both stages, then 8 KiB for
@@ -48,8 +49,8 @@ block by columns); resources %[rsa], %[rsb], %[rsd]; the wave's LDS load base
 %[lb]; the steps' byte offsets %[koa], %[kha], %[kob], %[khb] (next step and
 the one after; the first of each is 0 on entry), advanced by 128 by rows and
 by %[sta], %[stb] by columns; the count %[rem] of steps, at least 2; epilogue
-%[ewJ], %[erQ], %[soQ], %[gstr], scratch %[sdo]; RC: %[hk] masked rows and
-%[kr], the lane's row of its first load.
+%[ewJ], %[erQ], %[soQ], or %[sw] with %[wide], %[gstr], scratch %[sdo]; RC:
+%[hk] masked rows and %[kr], the lane's row of its first load.
 """
 from __future__ import annotations
 
@@ -69,10 +70,10 @@ def side_steps(op: str, layout: str) -> str:
 
 
 class Emitter(ring4.Emitter):
-    def __init__(self, la: str, lb: str, out32: bool) -> None:
+    def __init__(self, la: str, lb: str) -> None:
         super().__init__()
         self.layout = {"a": la, "b": lb}
-        self.out32 = out32
+        self.wide = False
 
     @staticmethod
     def m0(op: str, q: int, stage: int) -> str:
@@ -108,7 +109,7 @@ class Emitter(ring4.Emitter):
 
     # --- epilogue: rows of 16, as soon as their last products are done -------
     def group(self, i: int, t: int) -> list[tuple[str, bool]]:
-        if not self.out32:
+        if not self.wide:
             return [(text.replace("v_cvt_pk_f16_f32", "v_cvt_pk_@T@_f32"), lds) for text, lds in ring4.epilogue_group(i, t, t + 32)]
         # 32-bit outputs: four columns of a row from each lane, 64 bytes of 16
         # rows to a store; ordinary stores, so that L2 joins the halves of lines
@@ -118,7 +119,7 @@ class Emitter(ring4.Emitter):
             v, b = base + 4 * j, NB * i + j
             out += [(f"v_accvgpr_read_b32 v{v + r}, a{4 * b + r}", False) for r in range(4)]
             off = f" offset:{64 * j}" if j else ""
-            out.append((f"buffer_store_dwordx4 v[{v}:{v + 3}], %[so0], %[rsd], %[sdo] offen{off}", False))
+            out.append((f"buffer_store_dwordx4 v[{v}:{v + 3}], %[sw], %[rsd], %[sdo] offen{off}", False))
         out.append(("s_add_u32 %[sdo], %[sdo], %[gstr]", False))
         return out
 
@@ -234,8 +235,8 @@ def emit_step(e: Emitter, stage: int, first: bool, ahead: bool, has_next: bool, 
             e.op(t)
 
 
-def generate(la: str, lb: str, p: dict, out32: bool = False) -> str:
-    e = Emitter(la, lb, out32)
+def generate(la: str, lb: str, p: dict) -> str:
+    e = Emitter(la, lb)
     layout = e.layout
     head = {op: "none" if la == "c" else layout[op] for op in "ab"}
     for op, q in LOAD3:
@@ -286,10 +287,15 @@ def generate(la: str, lb: str, p: dict, out32: bool = False) -> str:
     step(1, False, False, True, False, [sub, "s_branch 3f"])    # the step before the last, in stage 1
     e.label("8")
     step(0, False, False, True, False, [sub])                   # the same in stage 0
-    e.label("2")
-    step(1, False, False, False, True, ["s_branch 4f"])         # the last step
-    e.label("3")
-    step(0, False, False, False, True, [])
+    for name, stage, narrow in (("2", 1, "9"), ("3", 0, "10")):  # the last step
+        e.label(name)
+        e.op("s_cmp_eq_u32 %[wide], 0")
+        e.op(f"s_cbranch_scc1 {narrow}f")
+        e.wide = True
+        step(stage, False, False, False, True, ["s_branch 4f"])
+        e.label(narrow)
+        e.wide = False
+        step(stage, False, False, False, True, ["s_branch 4f"] if stage else [])
     e.label("4")
     return "\n".join(e.lines)
 
@@ -300,11 +306,10 @@ ROWS = {"rel": 12, "load_every": 6, "pub": 64, "a_delay": 1, "read_limit": 112, 
 MIXED = {**ROWS, "pub": 56}
 COLS = {**ROWS, "rel": 14, "pub": 48}
 
-LOOPS = {   # macro: A side, B side, schedule, 32-bit outputs
-    "G16_GROUPED_RR": ("r", "r", ROWS, False),
-    "G16_GROUPED_RC": ("r", "c", MIXED, False),
-    "G16_GROUPED_CC": ("c", "c", COLS, False),
-    "G16_GROUPED_CC32": ("c", "c", COLS, True),
+LOOPS = {   # macro: A side, B side, schedule
+    "G16_GROUPED_RR": ("r", "r", ROWS),
+    "G16_GROUPED_RC": ("r", "c", MIXED),
+    "G16_GROUPED_CC": ("c", "c", COLS),
 }
 
 
@@ -320,8 +325,8 @@ def main() -> int:
     lines = 0
     with open(out, "w") as f:
         f.write("// Generated by gen_grouped_sched.py.  Do not edit.\n")
-        for name, (la, lb, p, out32) in LOOPS.items():
-            text = generate(la, lb, p, out32)
+        for name, (la, lb, p) in LOOPS.items():
+            text = generate(la, lb, p)
             lines += len(text.split("\n"))
             f.write(f"// {name}: {ring4.params_line(p)}.\n")
             f.write(as_macro(name, text))

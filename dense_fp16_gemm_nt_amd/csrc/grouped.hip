@@ -41,6 +41,9 @@ struct Args {
     Div col_tiles;
     Div per_group;       // TN: tiles of a group, padded to whole rounds of the XCDs
     uint32_t group_tiles;
+    Div splits;          // parts of the contraction, whose sums a second launch joins
+    float* parts;
+    uint32_t walkers;    // workgroups of the launch of large tiles
     // adapters
     const int32_t* ids;
     const float* scales;
@@ -141,29 +144,67 @@ struct Groups {
     }
 };
 
+// Tile `t` of all tiles in the order that the launches share.
 template <int BM, int BN, int MODE>
-__device__ __forceinline__ Work find_work(const Args& g)
+__device__ __forceinline__ Work tile_at(const Args& g, Groups<BM, MODE>& groups, uint32_t t)
 {
     uint32_t ti, tj;
+    Work r;
     if (MODE == TN) {
-        const uint32_t e = g.per_group.of(blockIdx.x), i = blockIdx.x - e * g.per_group.d;
-        // whole rounds of the XCDs: each has a part of the group's tiles of its own
-        const uint32_t t = g.per_group.d == g.group_tiles ? i : (uint32_t)xcd_slot(i, g.per_group.d);
-        if (t >= g.group_tiles) return Work{0, 0, 0, 0, 0, false};
-        grouped_tile_in<uint32_t>(t, g.group_tiles / g.col_tiles.d, g.col_tiles.d, kGroupTiles, &ti, &tj);
+        const uint32_t e = t / g.group_tiles;
+        grouped_tile_in<uint32_t>(t - e * g.group_tiles, g.group_tiles / g.col_tiles.d, g.col_tiles.d, kGroupTiles, &ti, &tj);
         const Rows s = rows_of(g, (int)e);
-        return Work{(int)e, s.first, s.count, (int)ti * BM, (int)tj * BN, true};
+        r = Work{(int)e, s.first, s.count, (int)ti * BM, 0, true};
+    } else {
+        grouped_tile_in<uint32_t>(t, groups.total, g.col_tiles.d, kGroupTiles, &ti, &tj);
+        r = groups.find(g, ti);
     }
-    Groups<BM, MODE> groups;
-    groups.start(g);
-    const uint32_t all = groups.total * g.col_tiles.d;
-    if (blockIdx.x >= all) return Work{0, 0, 0, 0, 0, false};
-    // each XCD has a run of neighbouring tiles, whose rows and columns its L2 holds
-    const uint32_t t = (uint32_t)xcd_slot(blockIdx.x, all);
-    grouped_tile_in<uint32_t>(t, groups.total, g.col_tiles.d, kGroupTiles, &ti, &tj);
-    Work r = groups.find(g, ti);
     r.col0 = (int)tj * BN;
     return r;
+}
+
+// How many tiles there are.
+template <int BM, int MODE>
+__device__ __forceinline__ uint32_t all_tiles(const Args& g, Groups<BM, MODE>& groups)
+{
+    if (MODE == TN) return (uint32_t)g.groups * g.group_tiles;
+    groups.start(g);
+    return groups.total * g.col_tiles.d;
+}
+
+// A workgroup's tile and part; `slot` is the place of its sums among the parts'.
+template <int BM, int BN, int MODE, bool SPLIT>
+__device__ __forceinline__ Work find_work(const Args& g, uint32_t* part, uint32_t* slot)
+{
+    Groups<BM, MODE> groups;
+    const uint32_t all = all_tiles<BM, MODE>(g, groups);
+    uint32_t t;
+    *part = 0;
+    if (MODE == TN) {
+        uint32_t i = blockIdx.x;
+        if (SPLIT) {
+            const uint32_t launch = g.per_group.d * (uint32_t)g.groups;
+            *part = i / launch;
+            i -= *part * launch;
+        }
+        const uint32_t e = g.per_group.of(i);
+        i -= e * g.per_group.d;
+        // whole rounds of the XCDs: each has a part of the group's tiles of its own
+        t = g.per_group.d == g.group_tiles ? i : (uint32_t)xcd_slot(i, g.per_group.d);
+        if (t >= g.group_tiles) return Work{0, 0, 0, 0, 0, false};
+        t += e * g.group_tiles;
+    } else {
+        const uint32_t n = SPLIT ? all * g.splits.d : all;
+        if (blockIdx.x >= n) return Work{0, 0, 0, 0, 0, false};
+        // each XCD has a run of neighbouring tiles, whose rows and columns its L2 holds
+        t = (uint32_t)xcd_slot(blockIdx.x, n);
+        if (SPLIT) {
+            *part = t / all;
+            t -= *part * all;
+        }
+    }
+    *slot = *part * all + t;
+    return tile_at<BM, BN, MODE>(g, groups, t);
 }
 
 // 16 zero bytes for chunks that belong to no request.
@@ -249,12 +290,14 @@ __device__ __forceinline__ void load_requests(const Args& g, const Work& wk, con
     load_all<C::THREADS * 16>(py, dst + C::X_BYTES, std::make_integer_sequence<int, SY::LOADS>());
 }
 
-template <typename T, class C, int MODE, bool F32>
+// SPLIT: sums of a part of the contraction, in fp32, for the launch that joins them.
+template <typename T, class C, int MODE, bool F32, bool SPLIT>
 __global__ __launch_bounds__(C::THREADS, C::PER_CU * C::WAVES / 4) void tile_kernel(const Args g)
 {
     constexpr bool XC = MODE == TN, YC = MODE == NN || MODE == TN;
     __shared__ __attribute__((aligned(1024))) char smem[C::LDS + (MODE == ADAPT ? C::BM * sizeof(Entry) + 16 : 0)];
-    const Work wk = find_work<C::BM, C::BN, MODE>(g);
+    uint32_t part, slot;
+    const Work wk = find_work<C::BM, C::BN, MODE, SPLIT>(g, &part, &slot);
     if (!wk.found) return;
     const int tid = threadIdx.x, lane = tid & 63;
     const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -292,6 +335,13 @@ __global__ __launch_bounds__(C::THREADS, C::PER_CU * C::WAVES / 4) void tile_ker
     // it are multiplied; steps behind the last load zeros, so that every wait
     // counts the same loads.
     int steps = (depth + C::BK - 1) / C::BK, left = depth;
+    if (SPLIT) {
+        const int per = (int)g.splits.of((uint32_t)steps + g.splits.d - 1), first = (int)part * per;
+        steps = clampi(steps - first, 0, per);
+        x.skip(first);
+        y.skip(first);
+        left = clampi(depth - first * C::BK, 0, steps * C::BK);
+    }
     uint32_t fill = 0;
     auto load = [&] {
         x.next(mine + fill, left, tid);
@@ -309,7 +359,7 @@ __global__ __launch_bounds__(C::THREADS, C::PER_CU * C::WAVES / 4) void tile_ker
             load();
         }
     };
-    if constexpr (MODE == ADAPT) {
+    if (MODE == ADAPT && (!SPLIT || part + 1 == g.splits.d)) {   // the requests go with the last part
         const int own = steps < C::STAGES - 1 ? steps : C::STAGES - 1;
         for (int s = 0; s < own; ++s) load();
         int* count = reinterpret_cast<int*>(table + C::BM);
@@ -322,7 +372,6 @@ __global__ __launch_bounds__(C::THREADS, C::PER_CU * C::WAVES / 4) void tile_ker
         for (int s = own; s < C::STAGES - 1; ++s) load_more();
         steps += (requests * (int)g.rank_chunks.d + C::BK / 8 - 1) / (C::BK / 8);
     } else {
-#pragma unroll
         for (int s = 0; s < C::STAGES - 1; ++s) load();
     }
     const bool busy = MODE == TN || wk.rows > wm * C::FM * 32;   // the wave has rows
@@ -337,18 +386,101 @@ __global__ __launch_bounds__(C::THREADS, C::PER_CU * C::WAVES / 4) void tile_ker
     grp::add_waves<C>(smem, k, lane, acc);
     if (k > 0) return;
 
-    float scale = 1.f;
-    if (MODE == LOW && g.scales != nullptr) scale = g.scales[g.ids[wk.group]];
     const int r0 = wm * C::FM * 32, c0 = wn * C::FN * 32, rows = (MODE == TN ? g.x_cols - wk.tile0 : wk.rows) - r0, cols = g.cols - wk.col0 - c0;
-    char* d = g.d + (MODE == TN ? (int64_t)wk.group * g.d_mat + (int64_t)(wk.tile0 + r0) * g.d_ld : (int64_t)(wk.row0 + r0) * g.d_ld) +
-              (int64_t)(wk.col0 + c0) * (F32 ? 4 : 2);
-    constexpr int STAGING = C::FN * 32 * 32 * (F32 ? 4 : 2);
+    constexpr bool WIDE = F32 || SPLIT;
+    constexpr int STAGING = C::FN * 32 * 32 * (WIDE ? 4 : 2);
     constexpr int AFTER = (C::WK - 1) * C::FM * C::FN * 4096;   // the other waves' sums
     static_assert(AFTER + C::WM * C::WN * STAGING <= C::LDS, "LDS budget");
-    grp::store<T, C, F32>(smem + AFTER + (wm * C::WN + wn) * STAGING, d, g.d_ld, rows, cols, scale, acc, lane);
+    char* staging = smem + AFTER + (wm * C::WN + wn) * STAGING;
+    if constexpr (SPLIT) {
+        char* d = (char*)(g.parts + (int64_t)slot * (C::BM * C::BN) + r0 * C::BN + c0);
+        grp::store<T, C, true>(staging, d, 4 * C::BN, rows, cols, 1.f, acc, lane);
+    } else {
+        float scale = 1.f;
+        if (MODE == LOW && g.scales != nullptr) scale = g.scales[g.ids[wk.group]];
+        char* d = g.d + (MODE == TN ? (int64_t)wk.group * g.d_mat + (int64_t)(wk.tile0 + r0) * g.d_ld : (int64_t)(wk.row0 + r0) * g.d_ld) +
+                  (int64_t)(wk.col0 + c0) * (F32 ? 4 : 2);
+        grp::store<T, C, F32>(staging, d, g.d_ld, rows, cols, scale, acc, lane);
+    }
+}
+
+// Eight columns of a row: the parts' sums added up in order, scaled, rounded once.
+template <typename T, bool F32>
+__device__ __forceinline__ void join8(const float* at, int64_t step, int parts, float scale, char* d)
+{
+    f32x4 lo = {0.f, 0.f, 0.f, 0.f}, hi = lo;
+    for (int p = 0; p < parts; ++p, at += step) {
+        lo += *reinterpret_cast<const f32x4*>(at);
+        hi += *reinterpret_cast<const f32x4*>(at + 4);
+    }
+    lo *= scale;
+    hi *= scale;
+    if constexpr (F32) {
+        *reinterpret_cast<f32x4*>(d) = lo;
+        *reinterpret_cast<f32x4*>(d + 16) = hi;
+    } else {
+        *reinterpret_cast<u32x4*>(d) = u32x4{T::pack(lo[0], lo[1]), T::pack(lo[2], lo[3]), T::pack(hi[0], hi[1]), T::pack(hi[2], hi[3])};
+    }
+}
+
+// Joins the parts of every tile; a workgroup has 2048 elements of one.
+template <typename T, class C, int MODE, bool F32>
+__global__ __launch_bounds__(256) void join_kernel(const Args g)
+{
+    constexpr uint32_t SUB = C::BM * C::BN / 2048;
+    static_assert(C::BM * C::BN % 2048 == 0 && C::BN <= 2048, "whole rows for a workgroup");
+    Groups<C::BM, MODE> groups;
+    const uint32_t all = all_tiles<C::BM, MODE>(g, groups), t = blockIdx.x / SUB;
+    if (t >= all) return;
+    const Work wk = tile_at<C::BM, C::BN, MODE>(g, groups, t);
+    if (!wk.found) return;
+    const int x = (int)(blockIdx.x % SUB) * 2048 + (int)threadIdx.x * 8, r = x / C::BN, c = x % C::BN;
+    const int rows = MODE == TN ? g.x_cols - wk.tile0 : wk.rows;
+    if (r >= rows || wk.col0 + c >= g.cols) return;
+    float scale = 1.f;
+    if (MODE == LOW && g.scales != nullptr) scale = g.scales[g.ids[wk.group]];
+    char* d = g.d + (MODE == TN ? (int64_t)wk.group * g.d_mat + (int64_t)(wk.tile0 + r) * g.d_ld : (int64_t)(wk.row0 + r) * g.d_ld) +
+              (int64_t)(wk.col0 + c) * (F32 ? 4 : 2);
+    join8<T, F32>(g.parts + (int64_t)t * (C::BM * C::BN) + x, (int64_t)all * (C::BM * C::BN), (int)g.splits.d, scale, d);
 }
 
 // Large tiles of NT, NN and TN: a workgroup for each compute unit walks them.
+//
+// The tiles that are left for the last round, where they are half a round or
+// less, are divided along the contraction, so that all workgroups have a part;
+// a second launch joins the parts.  (8192 rows over 6 matrices, 560 tiles of
+// 224 steps: 2.19 rounds instead of 3.)
+struct Walk {
+    uint32_t total, full, rest, parts;   // tiles, those of whole rounds, the others, and the parts of each of these
+    __device__ __forceinline__ void start(uint32_t tiles, uint32_t walkers, bool split)
+    {
+        total = tiles;
+        rest = tiles % walkers;
+        full = tiles - rest;
+        parts = split && rest > 0 ? walkers / rest : 1;
+    }
+    // parts of a tile of so many steps
+    __device__ __forceinline__ uint32_t of(uint32_t steps) const
+    {
+        const uint32_t most = steps / 4;   // of four steps or more
+        return parts < most ? parts : most > 1 ? most : 1;
+    }
+};
+
+// A tile's steps, and its place: tiles at the end of a side move back.
+template <int MODE>
+__device__ __forceinline__ uint32_t place_large(const Args& g, Work& wk)
+{
+    wk.col0 = (int)clamped_origin(wk.col0 / grp::kRingTile, grp::kRingTile, g.cols);
+    int depth = g.depth;
+    if (MODE == TN) {
+        wk.tile0 = (int)clamped_origin(wk.tile0 / grp::kRingTile, grp::kRingTile, g.x_cols);
+        depth = wk.rows;
+    }
+    const uint32_t steps = (uint32_t)(depth + grp::kRingStep - 1) / grp::kRingStep;
+    return steps < 2 ? 2 : steps;
+}
+
 template <typename T, int MODE, bool F32>
 __global__ __launch_bounds__(256, 1) void ring_kernel(const Args g)
 {
@@ -360,67 +492,78 @@ __global__ __launch_bounds__(256, 1) void ring_kernel(const Args g)
     const uint32_t lds = attn::lds_address(smem), lb = lds + 8192u * (uint32_t)w;
 
     Groups<TILE, MODE> groups;
-    uint32_t total;
-    if (MODE == TN) {
-        total = (uint32_t)g.groups * g.group_tiles;
-    } else {
-        groups.start(g);
-        total = groups.total * g.col_tiles.d;
-    }
-    uint32_t slot = (uint32_t)xcd_slot(blockIdx.x, gridDim.x);
-    if (slot >= total) return;
+    Walk walk;
+    walk.start(all_tiles<TILE, MODE>(g, groups), gridDim.x, g.parts != nullptr);
+    const uint32_t items = walk.full + walk.rest * walk.parts;
 
     grp::RingSide<XC> a;
     grp::RingSide<YC> b;
     grp::RingStore out;
     a.start(lds, g.x_ld, wm, w, lane);
     b.start(lds + 65536, g.y_ld, wn, w, lane);
-    out.template start<F32>(lds, g.d_ld, w, lane);
+    constexpr int64_t PART_LD = 4 * TILE;
+    out.start(lds, g.d_ld, F32 ? g.d_ld : PART_LD, w, lane);
     const uint32_t sta = (uint32_t)(STEP * g.x_ld), stb = (uint32_t)(STEP * g.y_ld);
-    // the contraction's first step is the partial one: see gen_grouped_sched.py
-    uint32_t kt = (uint32_t)(g.depth + STEP - 1) / STEP;
-    const int hk = MODE == TN ? 0 : (int)kt * STEP - g.depth, kr = 16 * w + lane / 32;
-    uint32_t hm[2];
-#pragma unroll
-    for (int q = 0; q < 2; ++q) hm[q] = 8 * ((lane & 7) ^ grp::RingSide<false>::swz(8 * q + lane / 8)) < hk ? grp::kBeyond : 0u;
+    const int kr = 16 * w + lane / 32;
 
-    for (; slot < total; slot += gridDim.x) {
-        uint32_t ti, tj;
-        Work wk;
-        if (MODE == TN) {
-            const uint32_t e = g.per_group.of(slot);
-            grouped_tile_in<uint32_t>(slot - e * g.group_tiles, g.group_tiles / g.col_tiles.d, g.col_tiles.d, kGroupTiles, &ti, &tj);
-            const Rows s = rows_of(g, (int)e);
-            wk = Work{(int)e, s.first, s.count, (int)clamped_origin(ti, TILE, g.x_cols), 0, true};
-            kt = (uint32_t)(s.count + STEP - 1) / STEP;
-            if (kt < 2) kt = 2;
-        } else {
-            grouped_tile_in<uint32_t>(slot, groups.total, g.col_tiles.d, kGroupTiles, &ti, &tj);
-            wk = groups.find(g, ti);
+    for (uint32_t slot = (uint32_t)xcd_slot(blockIdx.x, gridDim.x); slot < items; slot += gridDim.x) {
+        uint32_t t = slot, part = 0;
+        if (slot >= walk.full) {
+            t = slot - walk.full;
+            part = t / walk.rest;
+            t = walk.full + t - part * walk.rest;
         }
-        wk.col0 = (int)clamped_origin(tj, TILE, g.cols);
+        Work wk = tile_at<TILE, TILE, MODE>(g, groups, t);
+        uint32_t rem = place_large<MODE>(g, wk);
+        // the contraction's first step is the partial one: see gen_grouped_sched.py
+        int hk = MODE == TN ? 0 : (int)rem * STEP - g.depth;
+        const uint32_t parts = slot < walk.full ? 1 : walk.of(rem);
+        if (part >= parts) continue;
+        const uint32_t first = part * rem / parts;
+        rem = grp::uniform((part + 1) * rem / parts - first);
 
-        u32x4 rsa, rsb;
+        const char *x, *y, *d;
+        int64_t x_bytes, y_bytes;
         int rows = 128;   // of the wave
-        const char* d;
         if (MODE == TN) {
             const int64_t n = wk.rows;
-            rsa = grp::ring_rsrc(g.x + wk.row0 * g.x_ld + 2 * (int64_t)wk.tile0, n == 0 ? 0 : (n - 1) * g.x_ld + 2 * TILE);
-            rsb = grp::ring_rsrc(g.y + wk.row0 * g.y_ld + 2 * (int64_t)wk.col0, n == 0 ? 0 : (n - 1) * g.y_ld + 2 * TILE);
+            x = g.x + wk.row0 * g.x_ld + 2 * (int64_t)wk.tile0;
+            y = g.y + wk.row0 * g.y_ld + 2 * (int64_t)wk.col0;
+            x_bytes = n == 0 ? 0 : (n - 1) * g.x_ld + 2 * TILE;
+            y_bytes = n == 0 ? 0 : (n - 1) * g.y_ld + 2 * TILE;
             d = g.d + wk.group * g.d_mat + (int64_t)(wk.tile0 + wm) * g.d_ld;
         } else {
-            const int64_t n = wk.rows < TILE ? wk.rows : TILE;
-            const char* mat = g.y + wk.group * g.y_mat;
-            rsa = grp::ring_rsrc(g.x + wk.row0 * g.x_ld - 2 * hk, (n - 1) * g.x_ld + 2 * (int64_t)(g.depth + hk));
-            if (MODE == NT)
-                rsb = grp::ring_rsrc(mat + wk.col0 * g.y_ld - 2 * hk, (TILE - 1) * g.y_ld + 2 * (int64_t)(g.depth + hk));
-            else
-                rsb = grp::ring_rsrc(mat + 2 * (int64_t)wk.col0 - hk * g.y_ld, (int64_t)(g.depth + hk - 1) * g.y_ld + 2 * TILE);
+            const int64_t n = wk.rows < TILE ? wk.rows : TILE, length = g.depth + hk;
+            x = g.x + wk.row0 * g.x_ld - 2 * hk;
+            x_bytes = (n - 1) * g.x_ld + 2 * length;
+            y = g.y + wk.group * g.y_mat + (MODE == NT ? wk.col0 * g.y_ld - 2 * hk : 2 * (int64_t)wk.col0 - hk * g.y_ld);
+            y_bytes = MODE == NT ? (TILE - 1) * g.y_ld + 2 * length : (length - 1) * g.y_ld + 2 * TILE;
             rows = clampi((int)n - wm, 0, 128);
             d = g.d + (int64_t)(wk.row0 + wm) * g.d_ld;
         }
-        const u32x4 rsd = grp::ring_rsrc(d + (int64_t)(wk.col0 + wn) * (F32 ? 4 : 2), rows == 0 ? 0 : (rows - 1) * g.d_ld + 128 * (F32 ? 4 : 2));
-        uint32_t koa = 0, kob = 0, kha, khb, rem = kt, sdo;
+        if (first > 0) {   // a later part
+            const int64_t dx = (int64_t)first * (XC ? STEP * g.x_ld : 2 * STEP), dy = (int64_t)first * (YC ? STEP * g.y_ld : 2 * STEP);
+            x += dx;
+            y += dy;
+            x_bytes -= dx < x_bytes ? dx : x_bytes;
+            y_bytes -= dy < y_bytes ? dy : y_bytes;
+            hk = 0;
+        }
+        uint32_t hm[2];
+#pragma unroll
+        for (int q = 0; q < 2; ++q) hm[q] = 8 * ((lane & 7) ^ grp::RingSide<false>::swz(8 * q + lane / 8)) < hk ? grp::kBeyond : 0u;
+        const uint32_t wide = F32 ? 1u : grp::uniform(parts) - 1u;   // not 0: outputs in 32 bits
+        int64_t d_ld = g.d_ld;
+        d += (int64_t)(wk.col0 + wn) * (F32 ? 4 : 2);
+        if (parts > 1) {
+            d_ld = PART_LD;
+            d = (const char*)(g.parts + (int64_t)(slot - walk.full) * (TILE * TILE) + wm * TILE + wn);
+        }
+        if (F32 && parts > 1) out.sw = (uint32_t)((lane & 15) * PART_LD + 16 * (lane >> 4));   // the last of the workgroup's items
+        const u32x4 rsa = grp::ring_rsrc(x, x_bytes), rsb = grp::ring_rsrc(y, y_bytes);
+        const u32x4 rsd = grp::ring_rsrc(d, rows == 0 ? 0 : (rows - 1) * d_ld + 128 * (F32 || parts > 1 ? 4 : 2));
+        const uint32_t gstr = grp::uniform((uint32_t)(16 * d_ld)), masked = grp::uniform((uint32_t)hk);
+        uint32_t koa = 0, kob = 0, kha, khb, sdo;
 #pragma clang diagnostic push
 #pragma clang diagnostic ignored "-Winline-asm"   // M0 is written inside, on purpose
 #define G16_GROUPED_BLOCK(LOOP, ...) \
@@ -429,16 +572,36 @@ __global__ __launch_bounds__(256, 1) void ring_kernel(const Args g)
     else \
         asm volatile(LOOP("bf16") : G16_GROUPED_STATE : G16_GROUPED_COMMON, __VA_ARGS__ : G16_GROUPED_CLOBBERS)
         if constexpr (MODE == NT) {
-            G16_GROUPED_BLOCK(G16_GROUPED_RR, G16_GROUPED_STAGED, G16_GROUPED_A_ROWS, G16_GROUPED_B_ROWS);
+            G16_GROUPED_BLOCK(G16_GROUPED_RR, G16_GROUPED_A_ROWS, G16_GROUPED_B_ROWS);
         } else if constexpr (MODE == NN) {
-            G16_GROUPED_BLOCK(G16_GROUPED_RC, G16_GROUPED_STAGED, G16_GROUPED_A_ROWS, G16_GROUPED_B_COLS, [hk] "s"(hk), [kr] "v"(kr));
-        } else if constexpr (F32) {
-            G16_GROUPED_BLOCK(G16_GROUPED_CC32, G16_GROUPED_A_COLS, G16_GROUPED_B_COLS);
+            G16_GROUPED_BLOCK(G16_GROUPED_RC, G16_GROUPED_A_ROWS, G16_GROUPED_B_COLS, [hk] "s"(masked), [kr] "v"(kr));
         } else {
-            G16_GROUPED_BLOCK(G16_GROUPED_CC, G16_GROUPED_STAGED, G16_GROUPED_A_COLS, G16_GROUPED_B_COLS);
+            G16_GROUPED_BLOCK(G16_GROUPED_CC, G16_GROUPED_A_COLS, G16_GROUPED_B_COLS);
         }
 #pragma clang diagnostic pop
         wg_barrier();   // every wave is done reading the ring before the next tile's loads
+    }
+}
+
+// Joins what ring_kernel divided; a workgroup takes 2048 elements of a tile at a time.
+template <typename T, int MODE, bool F32>
+__global__ __launch_bounds__(256) void ring_join_kernel(const Args g)
+{
+    constexpr int TILE = grp::kRingTile;
+    constexpr uint32_t SUB = TILE * TILE / 2048;
+    Groups<TILE, MODE> groups;
+    Walk walk;
+    walk.start(all_tiles<TILE, MODE>(g, groups), g.walkers, true);
+    if (walk.parts < 2) return;
+    for (uint32_t i = blockIdx.x; i < walk.rest * SUB; i += gridDim.x) {
+        const uint32_t t = i / SUB;
+        Work wk = tile_at<TILE, TILE, MODE>(g, groups, walk.full + t);
+        const uint32_t parts = walk.of(place_large<MODE>(g, wk));
+        const int x = (int)(i % SUB) * 2048 + (int)threadIdx.x * 8, r = x / TILE, c = x % TILE;
+        if (parts < 2 || (MODE != TN && r >= wk.rows)) continue;
+        char* d = g.d + (MODE == TN ? (int64_t)wk.group * g.d_mat + (int64_t)(wk.tile0 + r) * g.d_ld : (int64_t)(wk.row0 + r) * g.d_ld) +
+                  (int64_t)(wk.col0 + c) * (F32 ? 4 : 2);
+        join8<T, F32>(g.parts + (int64_t)t * (TILE * TILE) + x, (int64_t)walk.rest * (TILE * TILE), (int)parts, 1.f, d);
     }
 }
 
@@ -453,28 +616,52 @@ constexpr int64_t kMaxTiles = int64_t(1) << 22;       // workgroups of a launch,
 using Tiny = Cfg<16, 16, 512, 1, 1, 4, 4, 1>;
 using Small = Cfg<32, 32, 256, 1, 1, 4, 4, 1>;
 using Flat = Cfg<32, 128, 64, 1, 4, 1, 4, 2>;
-using Low64 = Cfg<32, 64, 128, 1, 1, 4, 6, 1>;
-using Low128 = Cfg<32, 128, 128, 1, 1, 4, 4, 1>;
-using Square = Cfg<64, 64, 128, 2, 2, 1, 4, 1>;
+using Square = Cfg<64, 64, 64, 2, 2, 1, 4, 2>;
+using Oblong = Cfg<64, 128, 64, 2, 2, 1, 3, 2>;
 using Middle = Cfg<128, 128, 64, 2, 2, 1, 2, 2>;
 using Large = Cfg<256, 256, 64, 2, 4, 1, 2, 1>;
 
-struct Shape {
-    int bm, bn, threads;
-    const void* f;
-    bool walks;   // a workgroup for each compute unit at most
+// A shape's kernels, and what it takes: microseconds for 1024 of the
+// contraction with one and with two workgroups on a compute unit, all of them
+// busy (measured on MI355X, operands in L2).
+struct Form {
+    int bm, bn, bk, threads, per_cu;
+    float one, two;
+    const void *whole, *split, *join;
 };
 
-template <typename T, class C, int MODE, bool F32 = false>
-Shape shape()
+template <typename T, int MODE, bool F32, class C, bool PARTS>
+Form form(float one, float two)
 {
-    return {C::BM, C::BN, C::THREADS, (const void*)&tile_kernel<T, C, MODE, F32>, false};
+    Form f = {C::BM, C::BN, C::BK, C::THREADS, C::PER_CU, one, two, (const void*)&tile_kernel<T, C, MODE, F32, false>, nullptr, nullptr};
+    if constexpr (PARTS) {
+        f.split = (const void*)&tile_kernel<T, C, MODE, F32, true>;
+        f.join = (const void*)&join_kernel<T, C, MODE, F32>;
+    }
+    return f;
 }
-template <typename T, int MODE, bool F32 = false>
-Shape ring_shape()
-{
-    return {grp::kRingTile, grp::kRingTile, 256, (const void*)&ring_kernel<T, MODE, F32>, true};
-}
+
+constexpr int kMaxForms = 7;
+template <typename T, int MODE, bool F32>
+struct Forms {
+    Form f[kMaxForms];
+    int n = 0;
+    Forms()
+    {
+        if constexpr (MODE != TN) {
+            f[n++] = form<T, MODE, F32, Tiny, false>(1.3f, 1.3f);
+            f[n++] = form<T, MODE, F32, Small, false>(2.0f, 2.0f);
+        }
+        if constexpr (MODE == NT || MODE == NN) f[n++] = form<T, MODE, F32, Flat, false>(5.4f, 7.8f);
+        f[n++] = form<T, MODE, F32, Square, true>(5.0f, 6.4f);
+        if constexpr (MODE != TN) f[n++] = form<T, MODE, F32, Oblong, true>(6.8f, 10.0f);
+        if constexpr (MODE != LOW) f[n++] = form<T, MODE, F32, Middle, true>(11.2f, 16.2f);
+        if constexpr (MODE == ADAPT) f[n++] = form<T, MODE, F32, Large, false>(28.f, 28.f);
+        if constexpr (MODE == NT || MODE == NN || MODE == TN)
+            f[n++] = Form{grp::kRingTile, grp::kRingTile, grp::kRingStep, 256, 0, 20.6f, 20.6f, (const void*)&ring_kernel<T, MODE, F32>, nullptr,
+                          (const void*)&ring_join_kernel<T, MODE, F32>};
+    }
+};
 
 // What the large tiles' kernel takes: see grouped_ring.hpp.
 constexpr int64_t kRingPitch = int64_t(1) << 21;
@@ -489,67 +676,129 @@ bool ring_takes(int mode, const Args& g)
     return g.depth > grp::kRingStep && (mode == NT || ((int64_t)g.depth + 2 * grp::kRingStep) * g.y_ld < (int64_t(1) << 31));
 }
 
-// Tiles by the rows that a group has on average, and for few rows by the
-// workgroups that they make.
-template <typename T, int MODE>
-Shape pick(const Args& g, int cus)
+struct Plan {
+    const Form* form;
+    int64_t wgs, splits, part_bytes;
+    bool walks;
+};
+
+constexpr int64_t kMaxSplits = 16;
+
+// The shape and the parts of the contraction that a model of the time finds
+// best: rounds of the compute units, each with what starting a workgroup costs
+// and the contraction's share, not less than the operands take from memory;
+// and for parts their bytes and the second launch.  The number of tiles is the
+// device's to know where there are several groups: half a tile for each group
+// is taken as lost.
+template <int MODE>
+Plan plan(const Form* forms, int n, const Args& g, int cus, int* status)
 {
-    const int64_t rows = g.rows, groups = MODE == ADAPT ? 1 : g.groups, cols = g.cols;
-    const int64_t used = groups < rows ? groups : rows, mean = ceil_div(rows, used);
-    if (mean <= 16 && used * ceil_div(cols, 32) < 2 * cus) return shape<T, Tiny, MODE>();
-    const int64_t large = (rows + 255 * used) / 256 * ceil_div(cols, 256);
-    if constexpr (MODE == ADAPT) {
-        if (mean <= 32) return shape<T, Small, MODE>();
-        if (mean <= 64) return shape<T, Square, MODE>();
-        return mean > 160 && large >= cus ? shape<T, Large, MODE>() : shape<T, Middle, MODE>();
-    } else {
-        if (mean <= 48) return used * ceil_div(mean, 32) * ceil_div(cols, 128) < 2 * cus ? shape<T, Small, MODE>() : shape<T, Flat, MODE>();
-        return mean > 160 && large >= cus && ring_takes(MODE, g) ? ring_shape<T, MODE>() : shape<T, Middle, MODE>();
+    const int64_t used = MODE == ADAPT ? 1 : g.groups < g.rows ? g.groups : g.rows;   // groups with rows, at most
+    const double depth = MODE == TN ? (g.groups > 0 ? (double)g.rows / g.groups : 0.) : g.depth;
+    // matrices, rows read and rows written, at 5.5 TB/s
+    const double mats = MODE == TN ? (double)g.groups * g.x_cols * g.cols : (double)used * g.cols * depth;
+    const double rows = MODE == TN ? (double)g.rows * (g.x_cols + g.cols) : (double)g.rows * (depth + g.cols);
+    const double memory = (mats + rows) * 2 / 5.5e6;
+    Plan best = {nullptr, 0, 1, 0, false};
+    double best_us = 1e300;
+    for (int i = 0; i < n; ++i) {
+        const Form& f = forms[i];
+        const bool ring = f.per_cu == 0;
+        if (ring && !ring_takes(MODE, g)) continue;
+        const int64_t ct = ceil_div(g.cols, f.bn);
+        int64_t most;    // tiles, at most
+        double tiles;    // and as expected
+        if (MODE == TN) {
+            const int64_t t = ct * ceil_div(g.x_cols, f.bm);
+            most = g.groups * (ring || t < 8 * kNumXcd ? t : ceil_div(t, kNumXcd) * kNumXcd);
+            tiles = (double)g.groups * t;
+        } else {
+            most = (g.rows + used * (f.bm - 1)) / f.bm * ct;
+            const double r = used == 1 ? ceil_div(g.rows, f.bm) : (double)g.rows / f.bm + 0.5 * used;
+            tiles = (r < used ? used : r) * ct;
+        }
+        if (most > kMaxTiles) continue;
+        if (ring) {
+            const double d = (depth < 128 ? 128 : depth) / 1024 * f.one + 6.5;
+            const int64_t count = (int64_t)(tiles + 0.5), rest = count % cus;
+            double us = (count / cus) * d;
+            const bool split = rest > 0 && rest <= cus / 2 && depth >= 512 && count < 16 * cus;
+            if (split) {
+                const double parts = cus / rest;
+                us += d / parts + 8 + (double)rest * parts * f.bm * f.bn * 8 / 8e6;
+            } else if (rest > 0) {
+                us += d;
+            }
+            if (us < memory + 3) us = memory + 3;
+            if (us < best_us) {
+                best_us = us;
+                // where the device alone knows the tiles, parts are made possible for it
+                const bool known = MODE == TN || used == 1;
+                const bool parts = known ? split : depth >= 512 && count < 16 * cus;
+                best = Plan{&f, most < cus ? most : cus, 1, parts ? (int64_t)cus * f.bm * f.bn * 4 : 0, true};
+            }
+            continue;
+        }
+        const double slots = (double)cus * f.per_cu;
+        for (int64_t s = 1; s <= (f.split == nullptr ? 1 : kMaxSplits); s += s < 4 ? 1 : s / 2) {
+            const int64_t steps = ceil_div((int64_t)depth, f.bk * s);
+            if (s > 1 && (steps < 4 || most * s > kMaxTiles)) break;
+            const double d = (double)(steps * f.bk) / 1024, wgs = tiles * s;
+            const double full = (double)(int64_t)(wgs / slots), rest = wgs - full * slots;
+            double us = 1.5 + full * (2.3 + f.two * d);
+            if (rest > 0) us += 2.3 + (rest > cus ? f.two : f.one) * d;
+            if (us < memory + 3) us = memory + 3;
+            if (s > 1) us += 6 + wgs * f.bm * f.bn * 8 / 8e6;
+            if (us < best_us) {
+                best_us = us;
+                best = Plan{&f, most * s, s, s > 1 ? most * s * f.bm * f.bn * 4 : 0, false};
+            }
+        }
     }
+    *status = best.form == nullptr ? GEMM_F16_NT_UNSUPPORTED : GEMM_F16_NT_OK;
+    return best;
 }
 
-template <typename T>
-Shape pick_low(int64_t rows, int64_t requests, int rank)
+template <int MODE, bool F32 = false>
+Plan plan_for(int dtype, const Args& g, int cus, int* status)
 {
-    const int64_t used = requests < rows ? requests : rows;
-    if (ceil_div(rows, used) <= 16) return shape<T, Tiny, LOW>();
-    return rank <= 32 ? shape<T, Small, LOW>() : rank <= 64 ? shape<T, Low64, LOW>() : shape<T, Low128, LOW>();
-}
-
-template <typename T, bool F32>
-Shape pick_tn(const Args& g, int cus)
-{
-    const int64_t large = (int64_t)g.groups * ceil_div(g.x_cols, 256) * ceil_div(g.cols, 256);
-    return g.rows > 192 * (int64_t)g.groups && large >= cus && ring_takes(TN, g) ? ring_shape<T, TN, F32>() : shape<T, Middle, TN, F32>();
+    static const Forms<F16, MODE, F32> f16;
+    static const Forms<BF16, MODE, F32> bf16;
+    return dtype == GROUPED_F16 ? plan<MODE>(f16.f, f16.n, g, cus, status) : plan<MODE>(bf16.f, bf16.n, g, cus, status);
 }
 
 template <int MODE>
-int run(const Shape& c, const Args& args, int cus, hipStream_t s)
+int run(const Plan& p, const Args& args, void* parts, int cus, hipStream_t s)
 {
     Args g = args;
-    const int64_t ct = ceil_div(g.cols, c.bn);
+    const Form& f = *p.form;
+    const int64_t ct = ceil_div(g.cols, f.bn);
     g.col_tiles = attn::div_by(ct);
-    int64_t wgs;
+    g.splits = attn::div_by(p.splits);
+    g.parts = p.part_bytes > 0 ? (float*)parts : nullptr;
+    g.walkers = (uint32_t)p.wgs;
     if (MODE == TN) {
-        const int64_t t = ct * ceil_div(g.x_cols, c.bm);
-        const int64_t padded = c.walks || t < 8 * kNumXcd ? t : ceil_div(t, kNumXcd) * kNumXcd;
+        const int64_t t = ct * ceil_div(g.x_cols, f.bm);
         g.group_tiles = (uint32_t)t;
-        g.per_group = attn::div_by(padded);
-        wgs = padded * g.groups;
-    } else {
-        const int64_t used = MODE == ADAPT ? 1 : g.groups < g.rows ? g.groups : g.rows;   // groups with rows
-        wgs = (g.rows + used * (c.bm - 1)) / c.bm * ct;
+        g.per_group = attn::div_by(p.walks || t < 8 * kNumXcd ? t : ceil_div(t, kNumXcd) * kNumXcd);
     }
-    if (wgs > kMaxTiles) return GEMM_F16_NT_UNSUPPORTED;
-    if (c.walks && wgs > cus) wgs = cus;
-    return launch(c.f, wgs, c.threads, &g, s);
+    int st = launch(p.splits > 1 ? f.split : f.whole, p.wgs, f.threads, &g, s);
+    if (st != GEMM_F16_NT_OK || g.parts == nullptr) return st;
+    const int64_t pieces = p.walks ? 4 * cus : p.wgs / p.splits * (f.bm * f.bn / 2048);
+    return launch(f.join, pieces, 256, &g, s);
 }
 
 bool widths_ok(int64_t n, int64_t k) { return n % 8 == 0 && k % 8 == 0 && n < kMaxWidth && k < kMaxWidth; }
 
 enum Written { A_, B_, D_ };
 
-int check_grouped(const grouped_desc* d, Written out)
+struct Span {
+    const void* p;
+    int64_t bytes;
+};
+
+// GEMM_F16_NT_OK, 1 where a valid call has nothing to write, or an error.
+int check_grouped(const grouped_desc* d, Written out, Span work = {nullptr, 0})
 {
     if (d == nullptr) return GEMM_F16_NT_INVALID_ARG;
     if (d->dtype != GROUPED_F16 && d->dtype != GROUPED_BF16) return GEMM_F16_NT_INVALID_ARG;
@@ -566,11 +815,10 @@ int check_grouped(const grouped_desc* d, Written out)
         if (d->cu == nullptr) return GEMM_F16_NT_INVALID_ARG;
         if ((ea > 0 && d->A == nullptr) || (eb > 0 && d->B == nullptr) || (ed > 0 && d->D == nullptr)) return GEMM_F16_NT_INVALID_ARG;
         if (out == B_ && d->groups > 1 && d->stride_b < (d->N - 1) * d->ldb + d->K) return GEMM_F16_NT_INVALID_ARG;
-        const void* w = out == A_ ? d->A : out == B_ ? d->B : d->D;
-        const int64_t we = out == A_ ? ea : out == B_ ? eb : ed;
-        if ((out != A_ && overlaps(w, we, d->A, ea)) || (out != B_ && overlaps(w, we, d->B, eb)) ||
-            (out != D_ && overlaps(w, we, d->D, ed)) || (d->groups < kMaxGroups && overlaps(w, we, d->cu, 4 * (d->groups + 1))))
-            return GEMM_F16_NT_INVALID_ARG;
+        const Span all[] = {{d->A, ea}, {d->B, eb}, {d->D, ed}, {d->cu, d->groups < kMaxGroups ? 4 * (d->groups + 1) : 0}};
+        for (int i = 0; i < 4; ++i)
+            if ((i != (int)out && overlaps(all[out].p, all[out].bytes, all[i].p, all[i].bytes)) || overlaps(work.p, work.bytes, all[i].p, all[i].bytes))
+                return GEMM_F16_NT_INVALID_ARG;
     }
     if (out != B_ && d->b_fp32) return GEMM_F16_NT_UNSUPPORTED;
     if (!widths_ok(d->N, d->K) || d->lda >= kMaxWidth || d->ldb >= kMaxWidth || d->ldd >= kMaxWidth) return GEMM_F16_NT_UNSUPPORTED;
@@ -578,11 +826,6 @@ int check_grouped(const grouped_desc* d, Written out)
     if (!aligned16(d->A, {d->lda}) || !aligned16(d->D, {d->ldd}) || !aligned16(d->B, {d->ldb, d->stride_b})) return GEMM_F16_NT_UNSUPPORTED;
     return ((uintptr_t)d->cu & 3) != 0 ? GEMM_F16_NT_UNSUPPORTED : none ? 1 : GEMM_F16_NT_OK;
 }
-
-struct Span {
-    const void* p;
-    int64_t bytes;
-};
 
 int check_adapters(const adapter_desc* d, Span work = {nullptr, 0})
 {
@@ -619,7 +862,115 @@ int check_adapters(const adapter_desc* d, Span work = {nullptr, 0})
     return none ? 1 : GEMM_F16_NT_OK;
 }
 
-int64_t low_bytes(const adapter_desc* d) { return d->adapters == 0 ? 0 : 2 * d->rows * d->rank; }
+int64_t low_bytes(const adapter_desc* d) { return d->adapters == 0 ? 0 : ceil_div(2 * d->rows * d->rank, 256) * 256; }
+
+// Arguments of a call: written is D for NT, A for NN, B for TN.
+Args grouped_args(const grouped_desc* d, int mode)
+{
+    Args g = {};
+    g.cu = d->cu;
+    g.groups = (int)d->groups;
+    g.rows = (int)d->rows;
+    g.x = (const char*)(mode == NT ? d->A : d->D);
+    g.x_ld = 2 * (mode == NT ? d->lda : d->ldd);
+    g.y = (const char*)(mode == TN ? d->A : d->B);
+    g.y_ld = 2 * (mode == TN ? d->lda : d->ldb);
+    g.y_mat = 2 * d->stride_b;
+    const int64_t size = d->b_fp32 ? 4 : 2;
+    g.d = (char*)(mode == NT ? d->D : mode == NN ? d->A : d->B);
+    g.d_ld = mode == NT ? 2 * d->ldd : mode == NN ? 2 * d->lda : size * d->ldb;
+    g.d_mat = size * d->stride_b;
+    g.cols = (int)(mode == NT ? d->N : d->K);
+    g.x_cols = (int)d->N;
+    g.depth = (int)(mode == NT ? d->K : d->N);
+    return g;
+}
+
+int plan_grouped(const grouped_desc* d, int mode, const Args& g, Plan* p, int* cus)
+{
+    int st = device_cus(cus);
+    if (st != GEMM_F16_NT_OK) return st;
+    *p = mode == NT ? plan_for<NT>(d->dtype, g, *cus, &st) : mode == NN ? plan_for<NN>(d->dtype, g, *cus, &st)
+         : d->b_fp32 ? plan_for<TN, true>(d->dtype, g, *cus, &st) : plan_for<TN>(d->dtype, g, *cus, &st);
+    return st;
+}
+
+template <int MODE>
+int64_t grouped_bytes(const grouped_desc* d, Written out)
+{
+    int st = check_grouped(d, out), cus = 0;
+    if (st != GEMM_F16_NT_OK) return st > 0 ? 0 : st;
+    const Args g = grouped_args(d, MODE);
+    Plan p;
+    if ((st = plan_grouped(d, MODE, g, &p, &cus)) != GEMM_F16_NT_OK) return st;
+    return p.part_bytes;
+}
+
+template <int MODE>
+int grouped_run(const grouped_desc* d, Written out, void* workspace, int64_t workspace_bytes, void* stream)
+{
+    int st = check_grouped(d, out), cus = 0;
+    if (st != GEMM_F16_NT_OK) return st > 0 ? GEMM_F16_NT_OK : st;
+    const Args g = grouped_args(d, MODE);
+    Plan p;
+    if ((st = plan_grouped(d, MODE, g, &p, &cus)) != GEMM_F16_NT_OK) return st;
+    if ((st = check_workspace(workspace, workspace_bytes, p.part_bytes)) != GEMM_F16_NT_OK) return st;
+    if ((st = check_grouped(d, out, {workspace, p.part_bytes})) != GEMM_F16_NT_OK) return st;
+    return run<MODE>(p, g, workspace, cus, (hipStream_t)stream);
+}
+
+// The two launches of adapter_nt: the projections onto the rank, to the
+// workspace, and the rest.  Parts of both lie behind the first's results.
+struct AdapterCall {
+    Args low, rest;
+    Plan low_plan, plan;
+    bool adapted;
+    int cus;
+    int64_t bytes;
+};
+
+int plan_adapters(const adapter_desc* d, AdapterCall* c)
+{
+    int st = device_cus(&c->cus);
+    if (st != GEMM_F16_NT_OK) return st;
+    c->adapted = low_bytes(d) > 0;
+    Args g = {};
+    g.x = (const char*)d->A;
+    g.cu = d->cu;
+    g.x_ld = 2 * d->lda;
+    g.groups = (int)d->requests;
+    g.rows = (int)d->rows;
+    g.depth = (int)d->K;
+    g.ids = d->ids;
+    g.scales = d->scales;
+    g.adapters = c->adapted ? (int)d->adapters : 0;
+    g.rank_chunks = attn::div_by(c->adapted ? d->rank / 8 : 1);
+    c->bytes = 0;
+    if (c->adapted) {
+        c->low = g;
+        c->low.y = (const char*)d->down;
+        c->low.y_ld = 2 * d->ld_down;
+        c->low.y_mat = 2 * d->stride_down;
+        c->low.d_ld = 2 * d->rank;
+        c->low.cols = d->rank;
+        c->low_plan = plan_for<LOW>(d->dtype, c->low, c->cus, &st);
+        if (st != GEMM_F16_NT_OK) return st;
+        c->bytes = c->low_plan.part_bytes;
+    }
+    g.y = (const char*)d->B;
+    g.y_ld = 2 * d->ldb;
+    g.d = (char*)d->D;
+    g.d_ld = 2 * d->ldd;
+    g.cols = (int)d->N;
+    g.up = (const char*)d->up;
+    g.up_ld = 2 * d->ld_up;
+    g.up_mat = 2 * d->stride_up;
+    c->rest = g;
+    c->plan = plan_for<ADAPT>(d->dtype, g, c->cus, &st);
+    if (c->plan.part_bytes > c->bytes) c->bytes = c->plan.part_bytes;
+    c->bytes += low_bytes(d);
+    return st;
+}
 
 }  // namespace
 
@@ -630,123 +981,46 @@ int grouped_nn_check(const grouped_desc* d) { const int st = check_grouped(d, A_
 int grouped_tn_check(const grouped_desc* d) { const int st = check_grouped(d, B_); return st > 0 ? GEMM_F16_NT_OK : st; }
 int adapter_nt_check(const adapter_desc* d) { const int st = check_adapters(d); return st > 0 ? GEMM_F16_NT_OK : st; }
 
-int grouped_nt(const grouped_desc* d, void* stream)
-{
-    int st = check_grouped(d, D_);
-    if (st != GEMM_F16_NT_OK) return st > 0 ? GEMM_F16_NT_OK : st;
-    int cus = 0;
-    if ((st = device_cus(&cus)) != GEMM_F16_NT_OK) return st;
-    Args g = {};
-    g.x = (const char*)d->A;
-    g.y = (const char*)d->B;
-    g.d = (char*)d->D;
-    g.cu = d->cu;
-    g.x_ld = 2 * d->lda;
-    g.y_ld = 2 * d->ldb;
-    g.y_mat = 2 * d->stride_b;
-    g.d_ld = 2 * d->ldd;
-    g.groups = (int)d->groups;
-    g.rows = (int)d->rows;
-    g.cols = (int)d->N;
-    g.depth = (int)d->K;
-    return run<NT>(d->dtype == GROUPED_F16 ? pick<F16, NT>(g, cus) : pick<BF16, NT>(g, cus), g, cus, (hipStream_t)stream);
-}
+int64_t grouped_nt_workspace(const grouped_desc* d) { return grouped_bytes<NT>(d, D_); }
+int64_t grouped_nn_workspace(const grouped_desc* d) { return grouped_bytes<NN>(d, A_); }
+int64_t grouped_tn_workspace(const grouped_desc* d) { return grouped_bytes<TN>(d, B_); }
 
-int grouped_nn(const grouped_desc* d, void* stream)
+int grouped_nt(const grouped_desc* d, void* workspace, int64_t workspace_bytes, void* stream)
 {
-    int st = check_grouped(d, A_);
-    if (st != GEMM_F16_NT_OK) return st > 0 ? GEMM_F16_NT_OK : st;
-    int cus = 0;
-    if ((st = device_cus(&cus)) != GEMM_F16_NT_OK) return st;
-    Args g = {};
-    g.x = (const char*)d->D;
-    g.y = (const char*)d->B;
-    g.d = (char*)d->A;
-    g.cu = d->cu;
-    g.x_ld = 2 * d->ldd;
-    g.y_ld = 2 * d->ldb;
-    g.y_mat = 2 * d->stride_b;
-    g.d_ld = 2 * d->lda;
-    g.groups = (int)d->groups;
-    g.rows = (int)d->rows;
-    g.cols = (int)d->K;
-    g.depth = (int)d->N;
-    return run<NN>(d->dtype == GROUPED_F16 ? pick<F16, NN>(g, cus) : pick<BF16, NN>(g, cus), g, cus, (hipStream_t)stream);
+    return grouped_run<NT>(d, D_, workspace, workspace_bytes, stream);
 }
-
-int grouped_tn(const grouped_desc* d, void* stream)
+int grouped_nn(const grouped_desc* d, void* workspace, int64_t workspace_bytes, void* stream)
 {
-    int st = check_grouped(d, B_);
-    if (st != GEMM_F16_NT_OK) return st > 0 ? GEMM_F16_NT_OK : st;
-    int cus = 0;
-    if ((st = device_cus(&cus)) != GEMM_F16_NT_OK) return st;
-    Args g = {};
-    g.x = (const char*)d->D;
-    g.y = (const char*)d->A;
-    g.d = (char*)d->B;
-    g.cu = d->cu;
-    g.x_ld = 2 * d->ldd;
-    g.y_ld = 2 * d->lda;
-    const int64_t size = d->b_fp32 ? 4 : 2;
-    g.d_ld = size * d->ldb;
-    g.d_mat = size * d->stride_b;
-    g.groups = (int)d->groups;
-    g.rows = (int)d->rows;
-    g.x_cols = (int)d->N;
-    g.cols = (int)d->K;
-    const bool f16 = d->dtype == GROUPED_F16;
-    const Shape c = d->b_fp32 ? (f16 ? pick_tn<F16, true>(g, cus) : pick_tn<BF16, true>(g, cus))
-                              : (f16 ? pick_tn<F16, false>(g, cus) : pick_tn<BF16, false>(g, cus));
-    return run<TN>(c, g, cus, (hipStream_t)stream);
+    return grouped_run<NN>(d, A_, workspace, workspace_bytes, stream);
+}
+int grouped_tn(const grouped_desc* d, void* workspace, int64_t workspace_bytes, void* stream)
+{
+    return grouped_run<TN>(d, B_, workspace, workspace_bytes, stream);
 }
 
 int64_t adapter_nt_workspace(const adapter_desc* d)
 {
-    const int st = check_adapters(d);
-    return st < 0 ? st : st > 0 ? 0 : low_bytes(d);
+    int st = check_adapters(d);
+    if (st != GEMM_F16_NT_OK) return st > 0 ? 0 : st;
+    AdapterCall c;
+    return (st = plan_adapters(d, &c)) != GEMM_F16_NT_OK ? st : c.bytes;
 }
 
 int adapter_nt(const adapter_desc* d, void* workspace, int64_t workspace_bytes, void* stream)
 {
     int st = check_adapters(d);
     if (st != GEMM_F16_NT_OK) return st > 0 ? GEMM_F16_NT_OK : st;
-    if ((st = check_adapters(d, {workspace, low_bytes(d)})) != GEMM_F16_NT_OK) return st;
-    if ((st = check_workspace(workspace, workspace_bytes, low_bytes(d))) != GEMM_F16_NT_OK) return st;
-    int cus = 0;
-    if ((st = device_cus(&cus)) != GEMM_F16_NT_OK) return st;
-    const bool adapted = low_bytes(d) > 0, f16 = d->dtype == GROUPED_F16;
-    Args g = {};
-    g.x = (const char*)d->A;
-    g.cu = d->cu;
-    g.x_ld = 2 * d->lda;
-    g.groups = (int)d->requests;
-    g.rows = (int)d->rows;
-    g.depth = (int)d->K;
-    g.ids = d->ids;
-    g.scales = d->scales;
-    g.adapters = adapted ? (int)d->adapters : 0;
-    g.rank_chunks = attn::div_by(adapted ? d->rank / 8 : 1);
-    if (adapted) {
-        Args l = g;
-        l.y = (const char*)d->down;
-        l.y_ld = 2 * d->ld_down;
-        l.y_mat = 2 * d->stride_down;
-        l.d = (char*)workspace;
-        l.d_ld = 2 * d->rank;
-        l.cols = (int)d->rank;
-        const Shape c = f16 ? pick_low<F16>(d->rows, d->requests, d->rank) : pick_low<BF16>(d->rows, d->requests, d->rank);
-        if ((st = run<LOW>(c, l, cus, (hipStream_t)stream)) != GEMM_F16_NT_OK) return st;
+    AdapterCall c;
+    if ((st = plan_adapters(d, &c)) != GEMM_F16_NT_OK) return st;
+    if ((st = check_workspace(workspace, workspace_bytes, c.bytes)) != GEMM_F16_NT_OK) return st;
+    if ((st = check_adapters(d, {workspace, c.bytes})) != GEMM_F16_NT_OK) return st;
+    char* parts = (char*)workspace + low_bytes(d);
+    if (c.adapted) {
+        c.low.d = (char*)workspace;
+        if ((st = run<LOW>(c.low_plan, c.low, parts, c.cus, (hipStream_t)stream)) != GEMM_F16_NT_OK) return st;
     }
-    g.y = (const char*)d->B;
-    g.y_ld = 2 * d->ldb;
-    g.d = (char*)d->D;
-    g.d_ld = 2 * d->ldd;
-    g.cols = (int)d->N;
-    g.low = (const char*)workspace;
-    g.up = (const char*)d->up;
-    g.up_ld = 2 * d->ld_up;
-    g.up_mat = 2 * d->stride_up;
-    return run<ADAPT>(f16 ? pick<F16, ADAPT>(g, cus) : pick<BF16, ADAPT>(g, cus), g, cus, (hipStream_t)stream);
+    c.rest.low = (const char*)workspace;
+    return run<ADAPT>(c.plan, c.rest, parts, c.cus, (hipStream_t)stream);
 }
 
 }  // extern "C"

@@ -93,6 +93,8 @@ struct Side {
             off[i] = COLS && 8 * c >= ext ? kBeyond : (uint32_t)row(i, tid) * ld + 16u * (uint32_t)c;
         }
     }
+    // leaves out the first steps
+    __device__ __forceinline__ void skip(int steps) { at += (uint64_t)steps * (COLS ? (uint64_t)C::BK * ld : (uint64_t)(2 * C::BK)); }
     template <int... I>
     __device__ __forceinline__ void issue(u32x4 rs, uint32_t dst, const uint32_t (&o)[LOADS], std::integer_sequence<int, I...>)
     {

@@ -54,18 +54,20 @@ struct RingSide {
     }
 };
 
+// A value that is the same for all lanes, as an operand in scalar registers.
+__device__ __forceinline__ uint32_t uniform(uint32_t x) { return (uint32_t)__builtin_amdgcn_readfirstlane((int)x); }
+
 __device__ __forceinline__ u32x4 ring_rsrc(const char* base, int64_t bytes)
 {
     const uint64_t at = (uint64_t)base;
-    return u32x4{(uint32_t)at, (uint32_t)(at >> 32) & 0xffffu, (uint32_t)bytes, 0x00020000u};
+    return u32x4{uniform((uint32_t)at), uniform((uint32_t)(at >> 32) & 0xffffu), uniform((uint32_t)bytes), 0x00020000u};
 }
 
 // What a block needs beside its sides.
 struct RingStore {
-    uint32_t ew[8], er[4], so[4], gstr;
+    uint32_t ew[8], er[4], so[4], sw;   // sw: of outputs in 32 bits
 
-    template <bool F32>
-    __device__ __forceinline__ void start(uint32_t lds, int64_t pitch, int w, int lane)
+    __device__ __forceinline__ void start(uint32_t lds, int64_t pitch, int64_t wide_pitch, int w, int lane)
     {
         const uint32_t epi = lds + 131072u + 8192u * (uint32_t)w;
 #pragma unroll
@@ -77,9 +79,9 @@ struct RingStore {
         for (int q = 0; q < 4; ++q) {
             const int r = 4 * q + (lane >> 4), c = lane & 15;
             er[q] = epi + r * 256 + ((c ^ r) << 4);
-            so[q] = F32 ? (uint32_t)((lane & 15) * pitch + 16 * (lane >> 4)) : (uint32_t)(r * pitch + 16 * c);
+            so[q] = (uint32_t)(r * pitch + 16 * c);
         }
-        gstr = (uint32_t)(16 * pitch);
+        sw = (uint32_t)((lane & 15) * wide_pitch + 16 * (lane >> 4));
     }
 };
 
@@ -87,11 +89,10 @@ struct RingStore {
 #define G16_GROUPED_COMMON \
     [ax0] "v"(a.x[0]), [ax1] "v"(a.x[1]), [ax2] "v"(a.x[2]), [ax3] "v"(a.x[3]), [ax4] "v"(a.x[4]), [ax5] "v"(a.x[5]), [ax6] "v"(a.x[6]), \
     [ax7] "v"(a.x[7]), [bx0] "v"(b.x[0]), [bx1] "v"(b.x[1]), [bx2] "v"(b.x[2]), [bx3] "v"(b.x[3]), [bx4] "v"(b.x[4]), [bx5] "v"(b.x[5]), \
-    [bx6] "v"(b.x[6]), [bx7] "v"(b.x[7]), [so0] "v"(out.so[0]), [rsa] "s"(rsa), [rsb] "s"(rsb), [rsd] "s"(rsd), [lb] "s"(lb), [gstr] "s"(out.gstr)
-#define G16_GROUPED_STAGED \
+    [bx6] "v"(b.x[6]), [bx7] "v"(b.x[7]), [rsa] "s"(rsa), [rsb] "s"(rsb), [rsd] "s"(rsd), [lb] "s"(lb), [gstr] "s"(gstr), [wide] "s"(wide), \
     [ew0] "v"(out.ew[0]), [ew1] "v"(out.ew[1]), [ew2] "v"(out.ew[2]), [ew3] "v"(out.ew[3]), [ew4] "v"(out.ew[4]), [ew5] "v"(out.ew[5]), \
     [ew6] "v"(out.ew[6]), [ew7] "v"(out.ew[7]), [er0] "v"(out.er[0]), [er1] "v"(out.er[1]), [er2] "v"(out.er[2]), [er3] "v"(out.er[3]), \
-    [so1] "v"(out.so[1]), [so2] "v"(out.so[2]), [so3] "v"(out.so[3])
+    [so0] "v"(out.so[0]), [so1] "v"(out.so[1]), [so2] "v"(out.so[2]), [so3] "v"(out.so[3]), [sw] "v"(out.sw)
 #define G16_GROUPED_A_ROWS [ra0] "v"(a.r[0]), [ra1] "v"(a.r[1]), [hm0] "v"(hm[0]), [hm1] "v"(hm[1])
 #define G16_GROUPED_B_ROWS [rb0] "v"(b.r[0]), [rb1] "v"(b.r[1])
 #define G16_GROUPED_A_COLS \

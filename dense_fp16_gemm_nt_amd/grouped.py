@@ -46,14 +46,13 @@ _pack_grouped, _pack_adapter = _packer(GroupedDesc), _packer(AdapterDesc)
 def declare(L: ctypes.CDLL) -> None:
     """Argument types of the entry points of the library; descriptors are passed as their bytes or by reference."""
     i64, vp, i32 = ctypes.c_int64, ctypes.c_void_p, ctypes.c_int
-    for name in ("grouped_nt", "grouped_nn", "grouped_tn"):
+    for name in ("grouped_nt", "grouped_nn", "grouped_tn", "adapter_nt"):
         f = getattr(L, name)
-        f.restype, f.argtypes = i32, [vp, vp]
+        f.restype, f.argtypes = i32, [vp, vp, i64, vp]
+        f = getattr(L, name + "_workspace")
+        f.restype, f.argtypes = i64, [vp]
         f = getattr(L, name + "_check")
         f.restype, f.argtypes = i32, [vp]
-    L.adapter_nt.restype, L.adapter_nt.argtypes = i32, [vp, vp, i64, vp]
-    L.adapter_nt_workspace.restype, L.adapter_nt_workspace.argtypes = i64, [vp]
-    L.adapter_nt_check.restype, L.adapter_nt_check.argtypes = i32, [vp]
 
 
 _torch = None
@@ -122,15 +121,42 @@ def _ints(name, X, n, device):
     return X.data_ptr()
 
 
-def _run(name, desc, device, *workspace):
-    """Runs an entry point on a device's current stream."""
+_entries = {}   # name -> (entry point, its workspace query) of the loaded library
+
+
+def _run(name, desc, device, workspace):
+    """Runs an entry point on a device's current stream, with a workspace if it needs one."""
     torch = _torch or _module()
     if device.index != torch.cuda.current_device():   # launches go to the current device
         with torch.cuda.device(device):
-            return _run(name, desc, device, *workspace)
-    st = getattr(lib(), name)(desc, *workspace, torch._C._cuda_getCurrentRawStream(device.index))
+            return _run(name, desc, device, workspace)
+    if name not in _entries:
+        L = lib()
+        _entries[name] = getattr(L, name), getattr(L, name + "_workspace")
+    run, size = _entries[name]
+    ws, have = None, 0
+    if workspace is None:
+        have = size(desc)
+        if have < 0:
+            raise GemmError(int(have), name)
+        if have:
+            workspace = torch.empty(have, dtype=torch.uint8, device=device)
+            ws = workspace.data_ptr()
+    elif workspace.device != device or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on {device}")
+    else:
+        ws, have = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    st = run(desc, ws, have, torch._C._cuda_getCurrentRawStream(device.index))
     if st != OK:
         raise GemmError(st, name)
+
+
+def _workspace_bytes(name, desc, device):
+    with (_torch or _module()).cuda.device(device):
+        n = getattr(lib(), name + "_workspace")(desc)
+    if n < 0:
+        raise GemmError(int(n), name + "_workspace")
+    return int(n)
 
 
 def _groups(cu):
@@ -140,81 +166,115 @@ def _groups(cu):
     return n - 1
 
 
-def grouped_product(A, B, cu, *, D=None):
-    """D[r] = B[e] @ A[r] for the rows r = cu[e] .. cu[e + 1] - 1 of each group e.
-
-    A (rows, K) and B (groups, N, K), fp16 or bf16, last dimensions contiguous,
-    other strides as the C-ABI takes them; cu: groups + 1 int32 offsets on the
-    device, not decreasing.  N and K are multiples of 8.  Returns D (rows, N).
-    Rows of no group are left as they were in a given D (one allocated here
-    holds arbitrary values there)."""
+def _product_desc(A, B, cu, D):
+    """Descriptor bytes and device; without a D its address is one that no tensor has."""
     code, dtype, device = _first("A", A, 2)
     rows, K = A.shape
     if B.dim() != 3:
         raise ValueError(f"B must have 3 dimensions; got {tuple(B.shape)}")
     G, N = _groups(cu), B.shape[1]
     _match("B", B, (G, N, K), dtype, device)
-    if D is None:
-        D = _torch.empty((rows, N), dtype=dtype, device=device)
-    else:
+    if D is not None:
         _match("D", D, (rows, N), dtype, device)
     ldb, sb = _matrices("B", B)
-    desc = _pack_grouped(code, 0, G, rows, N, K, A.data_ptr(), B.data_ptr(), D.data_ptr(), _pitch("A", A), ldb, sb, _pitch("D", D),
-                         _ints("cu", cu, G + 1, device))
-    _run("grouped_nt", desc, device)
+    return _pack_grouped(code, 0, G, rows, N, K, A.data_ptr(), B.data_ptr(), 16 if D is None else D.data_ptr(), _pitch("A", A), ldb, sb,
+                         N if D is None else _pitch("D", D), _ints("cu", cu, G + 1, device)), device
+
+
+def grouped_product(A, B, cu, *, D=None, workspace=None):
+    """D[r] = B[e] @ A[r] for the rows r = cu[e] .. cu[e + 1] - 1 of each group e.
+
+    A (rows, K) and B (groups, N, K), fp16 or bf16, last dimensions contiguous,
+    other strides as the C-ABI takes them; cu: groups + 1 int32 offsets on the
+    device, not decreasing.  N and K are multiples of 8.  Returns D (rows, N).
+    Rows of no group are left as they were in a given D (one allocated here
+    holds arbitrary values there).  `workspace`: a device tensor of at least
+    grouped_product_workspace(...) bytes, 16-byte aligned; allocated here when
+    not given."""
+    if D is None:
+        _first("A", A, 2)
+        D = _torch.empty((A.shape[0], B.shape[1] if B.dim() == 3 else 0), dtype=A.dtype, device=A.device)
+    _run("grouped_nt", *_product_desc(A, B, cu, D), workspace)
     return D
 
 
-def grouped_product_grad_input(G, B, cu, *, dA=None):
-    """The gradient of grouped_product for A: dA[r] = B[e].T @ G[r], G (rows, N)
-    being the gradient for D and B (groups, N, K) the matrices.  Returns dA
-    (rows, K); rows of no group are left as they were in a given dA."""
+def grouped_product_workspace(A, B, cu) -> int:
+    """Bytes of workspace grouped_product needs for tensors of these shapes (0: none)."""
+    return _workspace_bytes("grouped_nt", *_product_desc(A, B, cu, None))
+
+
+def _grad_input_desc(G, B, cu, dA):
     code, dtype, device = _first("G", G, 2)
     rows, N = G.shape
     if B.dim() != 3:
         raise ValueError(f"B must have 3 dimensions; got {tuple(B.shape)}")
     groups, K = _groups(cu), B.shape[2]
     _match("B", B, (groups, N, K), dtype, device)
-    if dA is None:
-        dA = _torch.empty((rows, K), dtype=dtype, device=device)
-    else:
+    if dA is not None:
         _match("dA", dA, (rows, K), dtype, device)
     ldb, sb = _matrices("B", B)
-    desc = _pack_grouped(code, 0, groups, rows, N, K, dA.data_ptr(), B.data_ptr(), G.data_ptr(), _pitch("dA", dA), ldb, sb, _pitch("G", G),
-                         _ints("cu", cu, groups + 1, device))
-    _run("grouped_nn", desc, device)
+    return _pack_grouped(code, 0, groups, rows, N, K, 16 if dA is None else dA.data_ptr(), B.data_ptr(), G.data_ptr(),
+                         K if dA is None else _pitch("dA", dA), ldb, sb, _pitch("G", G), _ints("cu", cu, groups + 1, device)), device
+
+
+def grouped_product_grad_input(G, B, cu, *, dA=None, workspace=None):
+    """The gradient of grouped_product for A: dA[r] = B[e].T @ G[r], G (rows, N)
+    being the gradient for D and B (groups, N, K) the matrices.  Returns dA
+    (rows, K); rows of no group are left as they were in a given dA.
+    `workspace` as for grouped_product."""
+    if dA is None:
+        _first("G", G, 2)
+        dA = _torch.empty((G.shape[0], B.shape[2] if B.dim() == 3 else 0), dtype=G.dtype, device=G.device)
+    _run("grouped_nn", *_grad_input_desc(G, B, cu, dA), workspace)
     return dA
 
 
-def grouped_product_grad_weight(G, A, cu, *, dB=None, dtype=None):
-    """The gradient of grouped_product for B: dB[e] = sum of the outer products
-    of G[r] and A[r] over the rows of group e (zeros without rows), G (rows, N)
-    being the gradient for D and A (rows, K) its input.  Returns dB (groups, N,
-    K) in the operands' type, or in torch.float32 where `dtype` or a given dB
-    says so."""
+def grouped_product_grad_input_workspace(G, B, cu) -> int:
+    """Bytes of workspace grouped_product_grad_input needs for tensors of these shapes (0: none)."""
+    return _workspace_bytes("grouped_nn", *_grad_input_desc(G, B, cu, None))
+
+
+def _grad_weight_desc(G, A, cu, dB, dtype):
     code, own, device = _first("G", G, 2)
     rows, N = G.shape
     if A.dim() != 2:
         raise ValueError(f"A must have 2 dimensions; got {tuple(A.shape)}")
     groups, K = _groups(cu), A.shape[1]
     _match("A", A, (rows, K), own, device)
-    if dtype is None:
-        dtype = own if dB is None else dB.dtype
     if dtype is not own and dtype is not _torch.float32:
         raise TypeError(f"dB must be {own} or torch.float32, not {dtype}")
-    if dB is None:
-        dB = _torch.empty((groups, N, K), dtype=dtype, device=device)
-    else:
+    ldb, sb = K, N * K
+    if dB is not None:
         _match("dB", dB, (groups, N, K), dtype, device)
-    ldb, sb = _matrices("dB", dB)
-    desc = _pack_grouped(code, 0 if dtype is own else 1, groups, rows, N, K, A.data_ptr(), dB.data_ptr(), G.data_ptr(), _pitch("A", A), ldb, sb,
-                         _pitch("G", G), _ints("cu", cu, groups + 1, device))
-    _run("grouped_tn", desc, device)
+        ldb, sb = _matrices("dB", dB)
+    return _pack_grouped(code, 0 if dtype is own else 1, groups, rows, N, K, A.data_ptr(), 16 if dB is None else dB.data_ptr(), G.data_ptr(),
+                         _pitch("A", A), ldb, sb, _pitch("G", G), _ints("cu", cu, groups + 1, device)), device
+
+
+def grouped_product_grad_weight(G, A, cu, *, dB=None, dtype=None, workspace=None):
+    """The gradient of grouped_product for B: dB[e] = sum of the outer products
+    of G[r] and A[r] over the rows of group e (zeros without rows), G (rows, N)
+    being the gradient for D and A (rows, K) its input.  Returns dB (groups, N,
+    K) in the operands' type, or in torch.float32 where `dtype` or a given dB
+    says so.  `workspace` as for grouped_product."""
+    if dB is None:
+        _, own, device = _first("G", G, 2)
+        dtype = own if dtype is None else dtype
+        if dtype is own or dtype is _torch.float32:   # others are refused below
+            dB = _torch.empty((_groups(cu), G.shape[1], A.shape[1] if A.dim() == 2 else 0), dtype=dtype, device=device)
+    elif dtype is None:
+        dtype = dB.dtype
+    _run("grouped_tn", *_grad_weight_desc(G, A, cu, dB, dtype), workspace)
     return dB
 
 
+def grouped_product_grad_weight_workspace(G, A, cu, *, dtype=None) -> int:
+    """Bytes of workspace grouped_product_grad_weight needs for tensors of these shapes (0: none)."""
+    return _workspace_bytes("grouped_tn", *_grad_weight_desc(G, A, cu, None, G.dtype if dtype is None else dtype))
+
+
 def _adapter_desc(A, B, down, up, cu, adapters, scales, D):
-    """Descriptor bytes, device and workspace bytes; D None: the address is one that no tensor has."""
+    """As _product_desc."""
     code, dtype, device = _first("A", A, 2)
     rows, K = A.shape
     if B.dim() != 2 or down.dim() != 3 or up.dim() != 3:
@@ -237,13 +297,6 @@ def _adapter_desc(A, B, down, up, cu, adapters, scales, D):
     return desc, device
 
 
-def _adapter_bytes(desc):
-    n = lib().adapter_nt_workspace(desc)
-    if n < 0:
-        raise GemmError(int(n), "adapter_nt_workspace")
-    return int(n)
-
-
 def adapter_product(A, B, down, up, cu, adapters, scales=None, *, D=None, workspace=None):
     """D[r] = B @ A[r] + scales[a] * up[a] @ (down[a] @ A[r]), a = adapters[b] for the
     rows r = cu[b] .. cu[b + 1] - 1 of request b.
@@ -261,19 +314,10 @@ def adapter_product(A, B, down, up, cu, adapters, scales=None, *, D=None, worksp
         if B.dim() != 2:
             raise ValueError(f"B must have 2 dimensions; got {tuple(B.shape)}")
         D = _torch.empty((A.shape[0], B.shape[0]), dtype=A.dtype, device=A.device)
-    desc, device = _adapter_desc(A, B, down, up, cu, adapters, scales, D)
-    if workspace is None:
-        have = _adapter_bytes(desc)
-        if have:
-            workspace = _torch.empty(have, dtype=_torch.uint8, device=device)
-    elif workspace.device != device or not workspace.is_contiguous():
-        raise ValueError(f"workspace must be a contiguous tensor on {device}")
-    else:
-        have = workspace.numel() * workspace.element_size()
-    _run("adapter_nt", desc, device, None if workspace is None else workspace.data_ptr(), have)
+    _run("adapter_nt", *_adapter_desc(A, B, down, up, cu, adapters, scales, D), workspace)
     return D
 
 
 def adapter_product_workspace(A, B, down, up, cu, adapters, scales=None) -> int:
     """Bytes of workspace adapter_product needs for tensors of these shapes."""
-    return _adapter_bytes(_adapter_desc(A, B, down, up, cu, adapters, scales, None)[0])
+    return _workspace_bytes("adapter_nt", *_adapter_desc(A, B, down, up, cu, adapters, scales, None))

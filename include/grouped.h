@@ -30,6 +30,14 @@
  * return; validation comes before any HIP call, and an invalid call launches
  * nothing.  The library keeps nothing between calls; the same inputs give the
  * same bits.  Status codes are those of gemm_f16_nt.h.
+ *
+ * Workspace: calls with few tiles and a long contraction divide it among
+ * workgroups and join the parts in a second launch; adapter_nt keeps the
+ * low-rank projections.  They need ..._workspace(...) bytes of device memory
+ * (16-byte aligned, not overlapping the other arguments; contents are scratch,
+ * nothing needs clearing).  The size follows from the descriptor's sizes and
+ * strides alone, not from the tables in device memory.  Calls that may overlap
+ * in time need a workspace each.
  */
 #ifndef GROUPED_H
 #define GROUPED_H
@@ -67,9 +75,15 @@ typedef struct grouped_desc {
     const int32_t* cu;
 } grouped_desc;
 
-int grouped_nt(const grouped_desc* d, void* stream);
-int grouped_nn(const grouped_desc* d, void* stream);
-int grouped_tn(const grouped_desc* d, void* stream);
+int grouped_nt(const grouped_desc* d, void* workspace, int64_t workspace_bytes, void* stream);
+int grouped_nn(const grouped_desc* d, void* workspace, int64_t workspace_bytes, void* stream);
+int grouped_tn(const grouped_desc* d, void* workspace, int64_t workspace_bytes, void* stream);
+
+/* Bytes of workspace a call needs on the current device (0: none), or a
+ * negative status. */
+int64_t grouped_nt_workspace(const grouped_desc* d);
+int64_t grouped_nn_workspace(const grouped_desc* d);
+int64_t grouped_tn_workspace(const grouped_desc* d);
 
 /* The status a call would return before launching anything; no HIP call. */
 int grouped_nt_check(const grouped_desc* d);
@@ -106,10 +120,6 @@ typedef struct adapter_desc {
     int64_t lda, ldb, ldd, ld_down, stride_down, ld_up, stride_up;
 } adapter_desc;
 
-/* Workspace: adapter_nt_workspace(...) bytes of device memory (16-byte
- * aligned, not overlapping the other arguments; contents are scratch, nothing
- * needs clearing).  The size follows from the descriptor alone.  Calls that
- * may overlap in time need a workspace each. */
 int adapter_nt(const adapter_desc* d, void* workspace, int64_t workspace_bytes, void* stream);
 int64_t adapter_nt_workspace(const adapter_desc* d);
 int adapter_nt_check(const adapter_desc* d);

@@ -88,6 +88,14 @@ CASES = [
     ([3000, 1, 64, 65, 129, 2900], 4096, 72),
     ([3000, 1, 64, 65, 129, 2900], 320, 4096),
     ([300] * 70, 1024, 256),
+    ([207, 50], 264, 6152),                                # few tiles, a long contraction: in parts
+    ([100, 0, 33], 6152, 264),
+    ([3000, 0, 2500, 7], 72, 136),
+    ([4352], 4104, 2056),                                  # a small last round of large tiles, in parts
+    ([4352], 2056, 4104),
+    ([700], 4352, 4352),
+    ([2200], 4352, 4352),
+    ([4000, 9, 352], 1032, 4104),
 ]
 
 
@@ -121,6 +129,21 @@ def test_whole_numbers(pad, dtype, case):
             assert bool(torch.isnan(whole_dB[:, n:]).all()) and bool(torch.isnan(whole_dB[:, :, k:]).all())
     if pad:
         assert bool(torch.isnan(D._base[:, n:]).all()) and bool(torch.isnan(dA._base[:, k:]).all())
+
+
+def test_parts_are_reached():
+    # among the cases above are some, for each direction, whose contraction is divided: they need room for the parts
+    need = {"nt": [], "nn": [], "tn": []}
+    for lens, n, k in CASES:
+        A, G, B = (torch.empty(s, dtype=torch.float16, device=DEV) for s in ((sum(lens), k), (sum(lens), n), (len(lens), n, k)))
+        cu = ints(starts(lens))
+        need["nt"].append(g.grouped_product_workspace(A, B, cu))
+        need["nn"].append(g.grouped_product_grad_input_workspace(G, B, cu))
+        need["tn"].append(g.grouped_product_grad_weight_workspace(G, A, cu))
+    say(f"[gpu] workspaces {need}")
+    for name, sizes in need.items():
+        large = torch.cuda.get_device_properties(DEV).multi_processor_count << 18   # a part of a large tile for each compute unit
+        assert any(0 < s < large for s in sizes) and large in sizes and sizes[0] == 0, name
 
 
 @pytest.mark.parametrize("dtype", sorted(TYPES))

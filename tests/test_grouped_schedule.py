@@ -43,8 +43,8 @@ MFMA = re.compile(r"v_mfma_f32_16x16x32_@T@ a\[(\d+):\d+\], v\[(\d+):\d+\], v\[(
 
 
 class Sim:
-    def __init__(self, text, la, lb, out32, kt):
-        self.lines, self.kt, self.out32 = text.split("\n"), kt, out32
+    def __init__(self, text, la, lb, wide, kt):
+        self.lines, self.kt, self.wide = text.split("\n"), kt, wide
         self.layout = {"a": la, "b": lb}
         self.labels = {}
         for i, ln in enumerate(self.lines):
@@ -94,6 +94,8 @@ class Sim:
             clock += int(nop.group(1)) + 1 if nop else 4 if ln.startswith("v_mfma") else 1
             if m := re.match(r"s_cmp_eq_u32 %\[rem\], (\d+)$", ln):
                 scc = int(rem == int(m.group(1)))
+            elif ln == "s_cmp_eq_u32 %[wide], 0":
+                scc = int(not self.wide)
             elif ln.startswith("s_cbranch_scc1 "):
                 if scc:
                     pc = self.target(ln.split()[1], pc)
@@ -203,8 +205,9 @@ class Sim:
                 assert not any(x[0] == "write" for x in lgkm)
                 lgkm.append(("staged",))
             elif ln.startswith("buffer_store_dwordx4 "):
-                assert sdo is not None and sdo == stores // (8 if self.out32 else 4)
-                assert self.out32 or not lgkm
+                assert sdo is not None and sdo == stores // (8 if self.wide else 4)
+                assert self.wide or not lgkm
+                assert ("%[sw]" in ln) == self.wide
                 vm.append(("store", None))
                 stores += 1
             elif nop or re.match(r"^\d+:$", ln):
@@ -216,19 +219,20 @@ class Sim:
 
 
 @pytest.mark.parametrize("name", sorted(GEN.LOOPS))
+@pytest.mark.parametrize("wide", [False, True])
 @pytest.mark.parametrize("kt", [2, 3, 4, 5, 6, 7, 12, 33])
-def test_loop(name, kt):
-    la, lb, p, out32 = GEN.LOOPS[name]
-    r = Sim(GEN.generate(la, lb, p, out32), la, lb, out32, kt).run()
+def test_loop(name, wide, kt):
+    la, lb, p = GEN.LOOPS[name]
+    r = Sim(GEN.generate(la, lb, p), la, lb, wide, kt).run()
     assert r["loaded"] == {(op, s, q) for op in "ab" for s in range(kt) for q in range(8)}
     assert r["done"] == {b: 2 * kt for b in range(64)}
     assert r["read"] == set(range(256))
-    assert r["stores"] == (64 if out32 else 32)
+    assert r["stores"] == (64 if wide else 32)
     assert r["barriers"] == 2 * kt - 2   # one for step 0, a release for each step that loads, a publish for each but the last
 
 
 def test_committed_include():
     want = "// Generated by gen_grouped_sched.py.  Do not edit.\n"
-    for name, (la, lb, p, out32) in GEN.LOOPS.items():
-        want += f"// {name}: {GEN.ring4.params_line(p)}.\n" + GEN.as_macro(name, GEN.generate(la, lb, p, out32))
+    for name, (la, lb, p) in GEN.LOOPS.items():
+        want += f"// {name}: {GEN.ring4.params_line(p)}.\n" + GEN.as_macro(name, GEN.generate(la, lb, p))
     assert open(os.path.join(CSRC, "grouped_sched.inc")).read() == want
