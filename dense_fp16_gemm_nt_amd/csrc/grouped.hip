@@ -47,7 +47,9 @@ struct Args {
     // adapters
     const int32_t* ids;
     const float* scales;
-    const char* low;     // LOW's results, rows of `rank`
+    char* low;           // LOW's results, rows of `rank`; FUSED: 32 such rows for each workgroup
+    const char* down;    // FUSED
+    int64_t down_ld, down_mat;
     const char* up;
     int64_t up_ld, up_mat;
     int adapters;
@@ -259,9 +261,60 @@ __device__ __forceinline__ int fill_table(const Args& g, const Work& wk, Entry* 
     return count < BM ? count : BM;
 }
 
-// The loads of step s of the requests' part of the contraction.
+// FUSED: the rows' projections onto the rank by the workgroup itself, for a
+// tile of few rows and few requests: a second launch before this one costs 8
+// us, a request's 32 ranks about 0.7 us for each 1024 of the contraction.  The
+// waves divide the contraction, with fragments straight from memory, and add
+// their sums in LDS.  `low` gets them, rounded.
+template <typename T, class C>
+__device__ __forceinline__ void project(const Args& g, const Work& wk, const Entry* table, int count, float* lds, char* low, int w, int lane)
+{
+    static_assert(C::WAVES == 4, "four waves divide the contraction");
+    const int rank = 8 * (int)g.rank_chunks.d, half = lane >> 5, m = lane & 31;
+    const int rows = wk.rows < 32 ? wk.rows : 32, per = (g.depth + 63) / 64 * 16;   // of a wave, whole steps of 16
+    const int k0 = w * per, k1 = k0 + per < g.depth ? k0 + per : g.depth;
+    const char* x = g.x + (int64_t)(wk.row0 + (m < rows ? m : 0)) * g.x_ld;
+    for (int q = 0; q < count; ++q) {
+        const Entry e = table[q];
+        const float scale = g.scales != nullptr ? g.scales[e.id] : 1.f;
+        for (int r0 = 0; r0 < rank; r0 += 32) {
+            const char* y = g.down + (int64_t)e.id * g.down_mat + (int64_t)(r0 + m < rank ? r0 + m : 0) * g.down_ld;
+            f32x16 acc = {};
+            for (int k = k0; k < k1; k += 128) {
+                u32x4 a[8], b[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {   // elements behind the wave's last are read as its first and cleared
+                    const int at = k + 16 * i + 8 * half, from = at < k1 ? at : k0;
+                    a[i] = *reinterpret_cast<const u32x4*>(x + 2 * from);
+                    b[i] = *reinterpret_cast<const u32x4*>(y + 2 * from);
+                }
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const uint32_t keep = k + 16 * i + 8 * half < k1 ? 0xffffffffu : 0u;
+                    acc = T::mfma(b[i] & keep, a[i] & keep, acc);
+                }
+            }
+            __syncthreads();   // the sums of the round before have been read
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                *reinterpret_cast<f32x4*>(lds + ((w * 4 + i) * 64 + lane) * 4) = f32x4{acc[4 * i], acc[4 * i + 1], acc[4 * i + 2], acc[4 * i + 3]};
+            __syncthreads();
+            // wave w has ranks 8 w + 4 half .. + 3 of row m
+            f32x4 v = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v += *reinterpret_cast<const f32x4*>(lds + ((i * 4 + w) * 64 + lane) * 4);
+            v *= scale;
+            const int r = r0 + 8 * w + 4 * half;
+            if (m >= e.first && m < e.end && r < rank)
+                *reinterpret_cast<u32x2*>(low + ((int64_t)m * rank + r) * 2) = u32x2{T::pack(v[0], v[1]), T::pack(v[2], v[3])};
+        }
+    }
+}
+
+// The loads of step s of the requests' part of the contraction; `low` is the
+// tile's first row.
 template <class C>
-__device__ __forceinline__ void load_requests(const Args& g, const Work& wk, const Entry* table, int count, int s, uint32_t dst, int tid)
+__device__ __forceinline__ void load_requests(const Args& g, const Work& wk, const Entry* table, int count, const char* low, int s, uint32_t dst, int tid)
 {
     using SX = grp::Side<C, false, C::BM>;
     using SY = grp::Side<C, false, C::BN>;
@@ -277,7 +330,7 @@ __device__ __forceinline__ void load_requests(const Args& g, const Work& wk, con
         int in;
         const Entry e = where(SX::chunk(i, tid), &in);
         const int r = SX::row(i, tid);
-        px[i] = r >= e.first && r < e.end ? g.low + ((int64_t)(wk.row0 + r) * g.rank_chunks.d + in) * 16 : (const char*)g_nothing;
+        px[i] = r >= e.first && r < e.end ? low + ((int64_t)r * g.rank_chunks.d + in) * 16 : (const char*)g_nothing;
     }
 #pragma unroll
     for (int i = 0; i < SY::LOADS; ++i) {
@@ -291,11 +344,11 @@ __device__ __forceinline__ void load_requests(const Args& g, const Work& wk, con
 }
 
 // SPLIT: sums of a part of the contraction, in fp32, for the launch that joins them.
-template <typename T, class C, int MODE, bool F32, bool SPLIT>
+template <typename T, class C, int MODE, bool F32, bool SPLIT, bool FUSED>
 __global__ __launch_bounds__(C::THREADS, C::PER_CU * C::WAVES / 4) void tile_kernel(const Args g)
 {
     constexpr bool XC = MODE == TN, YC = MODE == NN || MODE == TN;
-    __shared__ __attribute__((aligned(1024))) char smem[C::LDS + (MODE == ADAPT ? C::BM * sizeof(Entry) + 16 : 0)];
+    __shared__ __attribute__((aligned(1024))) char smem[C::LDS + (MODE == ADAPT ? C::BM * sizeof(Entry) + 16 : 0) + (FUSED ? 16384 : 0)];
     uint32_t part, slot;
     const Work wk = find_work<C::BM, C::BN, MODE, SPLIT>(g, &part, &slot);
     if (!wk.found) return;
@@ -351,9 +404,10 @@ __global__ __launch_bounds__(C::THREADS, C::PER_CU * C::WAVES / 4) void tile_ker
     };
     Entry* table = reinterpret_cast<Entry*>(smem + C::LDS);
     int requests = 0, next = 0;   // ADAPT: of the tile; the next step of theirs
+    char* low = MODE != ADAPT ? nullptr : g.low + (FUSED ? (int64_t)blockIdx.x * 32 : (int64_t)wk.row0) * (16 * g.rank_chunks.d);
     auto load_more = [&] {
         if (MODE == ADAPT && left <= 0 && requests > 0) {
-            load_requests<C>(g, wk, table, requests, next++, mine + fill, tid);
+            load_requests<C>(g, wk, table, requests, low, next++, mine + fill, tid);
             fill = fill == (C::STAGES - 1) * C::STAGE ? 0 : fill + C::STAGE;
         } else {
             load();
@@ -369,6 +423,10 @@ __global__ __launch_bounds__(C::THREADS, C::PER_CU * C::WAVES / 4) void tile_ker
         }
         __syncthreads();
         requests = __builtin_amdgcn_readfirstlane(*count);
+        if constexpr (FUSED) {
+            project<T, C>(g, wk, table, requests, reinterpret_cast<float*>(smem + C::LDS + C::BM * sizeof(Entry) + 16), low, w, lane);
+            grp::publish<0>();   // what the waves wrote is there for all of them
+        }
         for (int s = own; s < C::STAGES - 1; ++s) load_more();
         steps += (requests * (int)g.rank_chunks.d + C::BK / 8 - 1) / (C::BK / 8);
     } else {
@@ -627,15 +685,16 @@ using Large = Cfg<256, 256, 64, 2, 4, 1, 2, 1>;
 struct Form {
     int bm, bn, bk, threads, per_cu;
     float one, two;
-    const void *whole, *split, *join;
+    const void *whole, *split, *join, *fused;
 };
 
-template <typename T, int MODE, bool F32, class C, bool PARTS>
+template <typename T, int MODE, bool F32, class C, bool PARTS, bool FUSED = false>
 Form form(float one, float two)
 {
-    Form f = {C::BM, C::BN, C::BK, C::THREADS, C::PER_CU, one, two, (const void*)&tile_kernel<T, C, MODE, F32, false>, nullptr, nullptr};
+    Form f = {C::BM, C::BN, C::BK, C::THREADS, C::PER_CU, one, two, (const void*)&tile_kernel<T, C, MODE, F32, false, false>, nullptr, nullptr, nullptr};
+    if constexpr (FUSED && MODE == ADAPT) f.fused = (const void*)&tile_kernel<T, C, MODE, F32, false, true>;
     if constexpr (PARTS) {
-        f.split = (const void*)&tile_kernel<T, C, MODE, F32, true>;
+        f.split = (const void*)&tile_kernel<T, C, MODE, F32, true, false>;
         f.join = (const void*)&join_kernel<T, C, MODE, F32>;
     }
     return f;
@@ -649,8 +708,8 @@ struct Forms {
     Forms()
     {
         if constexpr (MODE != TN) {
-            f[n++] = form<T, MODE, F32, Tiny, false>(1.3f, 1.3f);
-            f[n++] = form<T, MODE, F32, Small, false>(2.0f, 2.0f);
+            f[n++] = form<T, MODE, F32, Tiny, false, true>(1.3f, 1.3f);
+            f[n++] = form<T, MODE, F32, Small, false, true>(2.0f, 2.0f);
         }
         if constexpr (MODE == NT || MODE == NN) f[n++] = form<T, MODE, F32, Flat, false>(5.4f, 7.8f);
         f[n++] = form<T, MODE, F32, Square, true>(5.0f, 6.4f);
@@ -659,7 +718,7 @@ struct Forms {
         if constexpr (MODE == ADAPT) f[n++] = form<T, MODE, F32, Large, false>(28.f, 28.f);
         if constexpr (MODE == NT || MODE == NN || MODE == TN)
             f[n++] = Form{grp::kRingTile, grp::kRingTile, grp::kRingStep, 256, 0, 20.6f, 20.6f, (const void*)&ring_kernel<T, MODE, F32>, nullptr,
-                          (const void*)&ring_join_kernel<T, MODE, F32>};
+                          (const void*)&ring_join_kernel<T, MODE, F32>, nullptr};
     }
 };
 
@@ -680,6 +739,7 @@ struct Plan {
     const Form* form;
     int64_t wgs, splits, part_bytes;
     bool walks;
+    double us;
 };
 
 constexpr int64_t kMaxSplits = 16;
@@ -690,8 +750,11 @@ constexpr int64_t kMaxSplits = 16;
 // and for parts their bytes and the second launch.  The number of tiles is the
 // device's to know where there are several groups: half a tile for each group
 // is taken as lost.
+//
+// fused_us: what the adapters' projections add to a workgroup that computes
+// them itself, where it can, and then only such shapes; below 0 otherwise.
 template <int MODE>
-Plan plan(const Form* forms, int n, const Args& g, int cus, int* status)
+Plan plan(const Form* forms, int n, const Args& g, int cus, double fused_us, int* status)
 {
     const int64_t used = MODE == ADAPT ? 1 : g.groups < g.rows ? g.groups : g.rows;   // groups with rows, at most
     const double depth = MODE == TN ? (g.groups > 0 ? (double)g.rows / g.groups : 0.) : g.depth;
@@ -699,12 +762,11 @@ Plan plan(const Form* forms, int n, const Args& g, int cus, int* status)
     const double mats = MODE == TN ? (double)g.groups * g.x_cols * g.cols : (double)used * g.cols * depth;
     const double rows = MODE == TN ? (double)g.rows * (g.x_cols + g.cols) : (double)g.rows * (depth + g.cols);
     const double memory = (mats + rows) * 2 / 5.5e6;
-    Plan best = {nullptr, 0, 1, 0, false};
-    double best_us = 1e300;
+    Plan best = {nullptr, 0, 1, 0, false, 1e300};
     for (int i = 0; i < n; ++i) {
         const Form& f = forms[i];
         const bool ring = f.per_cu == 0;
-        if (ring && !ring_takes(MODE, g)) continue;
+        if ((ring && !ring_takes(MODE, g)) || (fused_us >= 0 && (f.fused == nullptr || g.rows > f.bm))) continue;
         const int64_t ct = ceil_div(g.cols, f.bn);
         int64_t most;    // tiles, at most
         double tiles;    // and as expected
@@ -730,29 +792,26 @@ Plan plan(const Form* forms, int n, const Args& g, int cus, int* status)
                 us += d;
             }
             if (us < memory + 3) us = memory + 3;
-            if (us < best_us) {
-                best_us = us;
+            if (us < best.us) {
                 // where the device alone knows the tiles, parts are made possible for it
                 const bool known = MODE == TN || used == 1;
                 const bool parts = known ? split : depth >= 512 && count < 16 * cus;
-                best = Plan{&f, most < cus ? most : cus, 1, parts ? (int64_t)cus * f.bm * f.bn * 4 : 0, true};
+                best = Plan{&f, parts || most > cus ? cus : most, 1, parts ? (int64_t)cus * f.bm * f.bn * 4 : 0, true, us};
             }
             continue;
         }
         const double slots = (double)cus * f.per_cu;
-        for (int64_t s = 1; s <= (f.split == nullptr ? 1 : kMaxSplits); s += s < 4 ? 1 : s / 2) {
+        const double start = fused_us >= 0 ? 2.3 + fused_us : 2.3;
+        for (int64_t s = 1; s <= (f.split == nullptr || fused_us >= 0 ? 1 : kMaxSplits); s += s < 4 ? 1 : s / 2) {
             const int64_t steps = ceil_div((int64_t)depth, f.bk * s);
             if (s > 1 && (steps < 4 || most * s > kMaxTiles)) break;
             const double d = (double)(steps * f.bk) / 1024, wgs = tiles * s;
             const double full = (double)(int64_t)(wgs / slots), rest = wgs - full * slots;
-            double us = 1.5 + full * (2.3 + f.two * d);
-            if (rest > 0) us += 2.3 + (rest > cus ? f.two : f.one) * d;
-            if (us < memory + 3) us = memory + 3;
+            double us = 1.5 + full * (start + f.two * d);
+            if (rest > 0) us += start + (rest > cus ? f.two : f.one) * d;
+            if (us < memory + start + 0.7) us = memory + start + 0.7;
             if (s > 1) us += 6 + wgs * f.bm * f.bn * 8 / 8e6;
-            if (us < best_us) {
-                best_us = us;
-                best = Plan{&f, most * s, s, s > 1 ? most * s * f.bm * f.bn * 4 : 0, false};
-            }
+            if (us < best.us) best = Plan{&f, most * s, s, s > 1 ? most * s * f.bm * f.bn * 4 : 0, false, us};
         }
     }
     *status = best.form == nullptr ? GEMM_F16_NT_UNSUPPORTED : GEMM_F16_NT_OK;
@@ -760,15 +819,15 @@ Plan plan(const Form* forms, int n, const Args& g, int cus, int* status)
 }
 
 template <int MODE, bool F32 = false>
-Plan plan_for(int dtype, const Args& g, int cus, int* status)
+Plan plan_for(int dtype, const Args& g, int cus, int* status, double fused_us = -1)
 {
     static const Forms<F16, MODE, F32> f16;
     static const Forms<BF16, MODE, F32> bf16;
-    return dtype == GROUPED_F16 ? plan<MODE>(f16.f, f16.n, g, cus, status) : plan<MODE>(bf16.f, bf16.n, g, cus, status);
+    return dtype == GROUPED_F16 ? plan<MODE>(f16.f, f16.n, g, cus, fused_us, status) : plan<MODE>(bf16.f, bf16.n, g, cus, fused_us, status);
 }
 
 template <int MODE>
-int run(const Plan& p, const Args& args, void* parts, int cus, hipStream_t s)
+int run(const Plan& p, const Args& args, void* parts, int cus, hipStream_t s, bool fused = false)
 {
     Args g = args;
     const Form& f = *p.form;
@@ -782,7 +841,7 @@ int run(const Plan& p, const Args& args, void* parts, int cus, hipStream_t s)
         g.group_tiles = (uint32_t)t;
         g.per_group = attn::div_by(p.walks || t < 8 * kNumXcd ? t : ceil_div(t, kNumXcd) * kNumXcd);
     }
-    int st = launch(p.splits > 1 ? f.split : f.whole, p.wgs, f.threads, &g, s);
+    int st = launch(fused ? f.fused : p.splits > 1 ? f.split : f.whole, p.wgs, f.threads, &g, s);
     if (st != GEMM_F16_NT_OK || g.parts == nullptr) return st;
     const int64_t pieces = p.walks ? 4 * cus : p.wgs / p.splits * (f.bm * f.bn / 2048);
     return launch(f.join, pieces, 256, &g, s);
@@ -862,8 +921,6 @@ int check_adapters(const adapter_desc* d, Span work = {nullptr, 0})
     return none ? 1 : GEMM_F16_NT_OK;
 }
 
-int64_t low_bytes(const adapter_desc* d) { return d->adapters == 0 ? 0 : ceil_div(2 * d->rows * d->rank, 256) * 256; }
-
 // Arguments of a call: written is D for NT, A for NN, B for TN.
 Args grouped_args(const grouped_desc* d, int mode)
 {
@@ -919,21 +976,22 @@ int grouped_run(const grouped_desc* d, Written out, void* workspace, int64_t wor
     return run<MODE>(p, g, workspace, cus, (hipStream_t)stream);
 }
 
-// The two launches of adapter_nt: the projections onto the rank, to the
-// workspace, and the rest.  Parts of both lie behind the first's results.
+// The launches of adapter_nt: the projections onto the rank, to the workspace,
+// and the rest, or both in one.  Parts of both lie behind the projections.
 struct AdapterCall {
     Args low, rest;
     Plan low_plan, plan;
-    bool adapted;
+    bool adapted, fused;
     int cus;
-    int64_t bytes;
+    int64_t low_bytes, bytes;   // of the projections, and of all of the workspace
 };
 
 int plan_adapters(const adapter_desc* d, AdapterCall* c)
 {
     int st = device_cus(&c->cus);
     if (st != GEMM_F16_NT_OK) return st;
-    c->adapted = low_bytes(d) > 0;
+    c->adapted = d->adapters > 0 && d->rank > 0;
+    c->fused = false;
     Args g = {};
     g.x = (const char*)d->A;
     g.cu = d->cu;
@@ -945,7 +1003,8 @@ int plan_adapters(const adapter_desc* d, AdapterCall* c)
     g.scales = d->scales;
     g.adapters = c->adapted ? (int)d->adapters : 0;
     g.rank_chunks = attn::div_by(c->adapted ? d->rank / 8 : 1);
-    c->bytes = 0;
+    c->low_bytes = 0;
+    int64_t parts = 0;
     if (c->adapted) {
         c->low = g;
         c->low.y = (const char*)d->down;
@@ -955,8 +1014,12 @@ int plan_adapters(const adapter_desc* d, AdapterCall* c)
         c->low.cols = d->rank;
         c->low_plan = plan_for<LOW>(d->dtype, c->low, c->cus, &st);
         if (st != GEMM_F16_NT_OK) return st;
-        c->bytes = c->low_plan.part_bytes;
+        c->low_bytes = ceil_div(2 * d->rows * d->rank, 256) * 256;
+        parts = c->low_plan.part_bytes;
     }
+    g.down = (const char*)d->down;
+    g.down_ld = 2 * d->ld_down;
+    g.down_mat = 2 * d->stride_down;
     g.y = (const char*)d->B;
     g.y_ld = 2 * d->ldb;
     g.d = (char*)d->D;
@@ -967,9 +1030,22 @@ int plan_adapters(const adapter_desc* d, AdapterCall* c)
     g.up_mat = 2 * d->stride_up;
     c->rest = g;
     c->plan = plan_for<ADAPT>(d->dtype, g, c->cus, &st);
-    if (c->plan.part_bytes > c->bytes) c->bytes = c->plan.part_bytes;
-    c->bytes += low_bytes(d);
-    return st;
+    if (st != GEMM_F16_NT_OK) return st;
+    if (c->adapted && d->rows <= 32) {
+        // a launch less (about 3 us and what the projections take) against their share in every workgroup
+        const int64_t passes = (d->requests < d->rows ? d->requests : d->rows) * ceil_div(d->rank, 32);
+        int fst = GEMM_F16_NT_OK;
+        const Plan f = plan_for<ADAPT>(d->dtype, g, c->cus, &fst, 1.0 + passes * (0.6 + 0.7 * (double)d->K / 1024));
+        if (fst == GEMM_F16_NT_OK && f.us < c->plan.us + c->low_plan.us + 2) {
+            c->fused = true;
+            c->plan = f;
+            c->low_bytes = ceil_div(f.wgs * 32 * 2 * d->rank, 256) * 256;
+            parts = 0;
+        }
+    }
+    if (c->plan.part_bytes > parts) parts = c->plan.part_bytes;
+    c->bytes = c->low_bytes + parts;
+    return GEMM_F16_NT_OK;
 }
 
 }  // namespace
@@ -1014,13 +1090,13 @@ int adapter_nt(const adapter_desc* d, void* workspace, int64_t workspace_bytes, 
     if ((st = plan_adapters(d, &c)) != GEMM_F16_NT_OK) return st;
     if ((st = check_workspace(workspace, workspace_bytes, c.bytes)) != GEMM_F16_NT_OK) return st;
     if ((st = check_adapters(d, {workspace, c.bytes})) != GEMM_F16_NT_OK) return st;
-    char* parts = (char*)workspace + low_bytes(d);
-    if (c.adapted) {
+    char* parts = (char*)workspace + c.low_bytes;
+    if (c.adapted && !c.fused) {
         c.low.d = (char*)workspace;
         if ((st = run<LOW>(c.low_plan, c.low, parts, c.cus, (hipStream_t)stream)) != GEMM_F16_NT_OK) return st;
     }
-    c.rest.low = (const char*)workspace;
-    return run<ADAPT>(c.plan, c.rest, parts, c.cus, (hipStream_t)stream);
+    c.rest.low = (char*)workspace;
+    return run<ADAPT>(c.plan, c.rest, parts, c.cus, (hipStream_t)stream, c.fused);
 }
 
 }  // extern "C"
