@@ -47,8 +47,8 @@ struct Args {
     // adapters
     const int32_t* ids;
     const float* scales;
-    char* low;           // LOW's results, rows of `rank`; FUSED: 32 such rows for each workgroup
-    const char* down;    // FUSED
+    const char* low;     // LOW's results, rows of `rank`
+    const char* down;
     int64_t down_ld, down_mat;
     const char* up;
     int64_t up_ld, up_mat;
@@ -261,56 +261,6 @@ __device__ __forceinline__ int fill_table(const Args& g, const Work& wk, Entry* 
     return count < BM ? count : BM;
 }
 
-// FUSED: the rows' projections onto the rank by the workgroup itself, for a
-// tile of few rows and few requests: a second launch before this one costs 8
-// us, a request's 32 ranks about 0.7 us for each 1024 of the contraction.  The
-// waves divide the contraction, with fragments straight from memory, and add
-// their sums in LDS.  `low` gets them, rounded.
-template <typename T, class C>
-__device__ __forceinline__ void project(const Args& g, const Work& wk, const Entry* table, int count, float* lds, char* low, int w, int lane)
-{
-    static_assert(C::WAVES == 4, "four waves divide the contraction");
-    const int rank = 8 * (int)g.rank_chunks.d, half = lane >> 5, m = lane & 31;
-    const int rows = wk.rows < 32 ? wk.rows : 32, per = (g.depth + 63) / 64 * 16;   // of a wave, whole steps of 16
-    const int k0 = w * per, k1 = k0 + per < g.depth ? k0 + per : g.depth;
-    const char* x = g.x + (int64_t)(wk.row0 + (m < rows ? m : 0)) * g.x_ld;
-    for (int q = 0; q < count; ++q) {
-        const Entry e = table[q];
-        const float scale = g.scales != nullptr ? g.scales[e.id] : 1.f;
-        for (int r0 = 0; r0 < rank; r0 += 32) {
-            const char* y = g.down + (int64_t)e.id * g.down_mat + (int64_t)(r0 + m < rank ? r0 + m : 0) * g.down_ld;
-            f32x16 acc = {};
-            for (int k = k0; k < k1; k += 128) {
-                u32x4 a[8], b[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {   // elements behind the wave's last are read as its first and cleared
-                    const int at = k + 16 * i + 8 * half, from = at < k1 ? at : k0;
-                    a[i] = *reinterpret_cast<const u32x4*>(x + 2 * from);
-                    b[i] = *reinterpret_cast<const u32x4*>(y + 2 * from);
-                }
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const uint32_t keep = k + 16 * i + 8 * half < k1 ? 0xffffffffu : 0u;
-                    acc = T::mfma(b[i] & keep, a[i] & keep, acc);
-                }
-            }
-            __syncthreads();   // the sums of the round before have been read
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                *reinterpret_cast<f32x4*>(lds + ((w * 4 + i) * 64 + lane) * 4) = f32x4{acc[4 * i], acc[4 * i + 1], acc[4 * i + 2], acc[4 * i + 3]};
-            __syncthreads();
-            // wave w has ranks 8 w + 4 half .. + 3 of row m
-            f32x4 v = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) v += *reinterpret_cast<const f32x4*>(lds + ((i * 4 + w) * 64 + lane) * 4);
-            v *= scale;
-            const int r = r0 + 8 * w + 4 * half;
-            if (m >= e.first && m < e.end && r < rank)
-                *reinterpret_cast<u32x2*>(low + ((int64_t)m * rank + r) * 2) = u32x2{T::pack(v[0], v[1]), T::pack(v[2], v[3])};
-        }
-    }
-}
-
 // The loads of step s of the requests' part of the contraction; `low` is the
 // tile's first row.
 template <class C>
@@ -344,11 +294,11 @@ __device__ __forceinline__ void load_requests(const Args& g, const Work& wk, con
 }
 
 // SPLIT: sums of a part of the contraction, in fp32, for the launch that joins them.
-template <typename T, class C, int MODE, bool F32, bool SPLIT, bool FUSED>
+template <typename T, class C, int MODE, bool F32, bool SPLIT>
 __global__ __launch_bounds__(C::THREADS, C::PER_CU * C::WAVES / 4) void tile_kernel(const Args g)
 {
     constexpr bool XC = MODE == TN, YC = MODE == NN || MODE == TN;
-    __shared__ __attribute__((aligned(1024))) char smem[C::LDS + (MODE == ADAPT ? C::BM * sizeof(Entry) + 16 : 0) + (FUSED ? 16384 : 0)];
+    __shared__ __attribute__((aligned(1024))) char smem[C::LDS + (MODE == ADAPT ? C::BM * sizeof(Entry) + 16 : 0)];
     uint32_t part, slot;
     const Work wk = find_work<C::BM, C::BN, MODE, SPLIT>(g, &part, &slot);
     if (!wk.found) return;
@@ -404,7 +354,7 @@ __global__ __launch_bounds__(C::THREADS, C::PER_CU * C::WAVES / 4) void tile_ker
     };
     Entry* table = reinterpret_cast<Entry*>(smem + C::LDS);
     int requests = 0, next = 0;   // ADAPT: of the tile; the next step of theirs
-    char* low = MODE != ADAPT ? nullptr : g.low + (FUSED ? (int64_t)blockIdx.x * 32 : (int64_t)wk.row0) * (16 * g.rank_chunks.d);
+    const char* low = MODE != ADAPT ? nullptr : g.low + (int64_t)wk.row0 * (16 * g.rank_chunks.d);
     auto load_more = [&] {
         if (MODE == ADAPT && left <= 0 && requests > 0) {
             load_requests<C>(g, wk, table, requests, low, next++, mine + fill, tid);
@@ -423,10 +373,6 @@ __global__ __launch_bounds__(C::THREADS, C::PER_CU * C::WAVES / 4) void tile_ker
         }
         __syncthreads();
         requests = __builtin_amdgcn_readfirstlane(*count);
-        if constexpr (FUSED) {
-            project<T, C>(g, wk, table, requests, reinterpret_cast<float*>(smem + C::LDS + C::BM * sizeof(Entry) + 16), low, w, lane);
-            grp::publish<0>();   // what the waves wrote is there for all of them
-        }
         for (int s = own; s < C::STAGES - 1; ++s) load_more();
         steps += (requests * (int)g.rank_chunks.d + C::BK / 8 - 1) / (C::BK / 8);
     } else {
@@ -460,6 +406,141 @@ __global__ __launch_bounds__(C::THREADS, C::PER_CU * C::WAVES / 4) void tile_ker
                   (int64_t)(wk.col0 + c0) * (F32 ? 4 : 2);
         grp::store<T, C, F32>(staging, d, g.d_ld, rows, cols, scale, acc, lane);
     }
+}
+
+// Up to 16 rows of few requests (some users' next tokens): the adapters'
+// projections come with the shared one, as further columns of the same
+// product, whose tile has 16 rows of the shared matrix and RB blocks of 16 rows
+// of `down`, so many of each request.  Their sums are the second product's
+// operand as they lie in the accumulators: the order of that contraction is
+// free, and `up` is read to match.  What bounds it is the latency of a chain:
+// arguments, the first loads, the bytes (24 to 40 KiB in flight on a compute
+// unit), the sums of four waves.  So the shared matrix is asked for before the
+// requests' rows are known, which are read as scalars, by themselves.
+template <typename T, int RB>
+__global__ __launch_bounds__(256, 1) void single_kernel(const Args g)
+{
+    using C = Cfg<16, 16 + 16 * RB, 256, 1, 1, 4, RB == 1 ? 6 : 4, 1>;
+    static_assert(RB == 1 || RB == 3, "whole blocks of 32 columns, and four stages of them");
+    constexpr int FN = (RB + 1) / 2;
+    using W = grp::Side<C, false, 16>;
+    using X = grp::Side<C, false, 16>;
+    using L = grp::Tile<false, 16, C::BK>;
+    constexpr int LATE = (1 + RB) * X::LOADS, LOADS = W::LOADS + LATE;   // of a step
+    __shared__ __attribute__((aligned(1024))) char smem[C::STAGES * C::STAGE];
+    const int tid = threadIdx.x, lane = tid & 63, half = lane >> 5;
+    const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const uint32_t lds = attn::lds_address(smem), mine = lds + 1024u * (uint32_t)w;
+    const int col0 = (int)xcd_slot(blockIdx.x, gridDim.x) * 16;
+
+    // stage: 16 rows of the shared matrix, RB x 16 of `down`, 16 of A
+    constexpr uint32_t PIECE = 16 * C::BK * 2;
+    W y;
+    y.start(g.y + (int64_t)col0 * g.y_ld, g.y_ld, g.cols - col0, tid);
+    int y_left = g.depth;
+#pragma unroll
+    for (int s = 0; s < C::STAGES - 1; ++s, y_left -= C::BK) y.next(mine + s * C::STAGE, y_left, tid);
+
+    typedef const __attribute__((address_space(4))) int32_t* Scalars;
+    const Scalars cu = (Scalars)(uintptr_t)g.cu, ids = (Scalars)(uintptr_t)g.ids;
+    const int row0 = clampi(cu[0], 0, g.rows), rows = clampi(cu[g.groups], row0, g.rows) - row0;
+    const int rank = 8 * (int)g.rank_chunks.d, each = (rank + 15) / 16;   // blocks of a request
+    X x, down[RB];
+    x.start(g.x + (int64_t)row0 * g.x_ld, g.x_ld, rows, tid);
+    int first[RB], end[RB];   // the rows of a block's request
+    float scale[RB];
+    u32x4 u[RB] = {};         // `up` for the lane's column, in the order of the accumulators
+    const bool mine_up = w == 0 && (lane & 31) < 16 && col0 + (lane & 31) < g.cols;
+#pragma unroll
+    for (int b = 0; b < RB; ++b) {
+        const int q = b / each, part = b - q * each;
+        const bool there = q < g.groups;
+        first[b] = there ? cu[q] - row0 : 0;
+        end[b] = there ? cu[q + 1] - row0 : 0;
+        const int id = there ? ids[q] : -1;
+        const bool adapted = (uint32_t)id < (uint32_t)g.adapters;
+        if (!adapted) end[b] = first[b];
+        const int64_t at = adapted ? id : 0;
+        down[b].start(g.down + at * g.down_mat + (int64_t)(16 * part) * g.down_ld, g.down_ld, adapted ? rank - 16 * part : 0, tid);
+        scale[b] = adapted && g.scales != nullptr ? ((const __attribute__((address_space(4))) float*)(uintptr_t)g.scales)[at] : 1.f;
+        const char* up = g.up + at * g.up_mat + (int64_t)(col0 + (lane & 31)) * g.up_ld + 32 * part + 8 * half;
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+            if (mine_up && adapted && 16 * part + 8 * e < rank) {
+                const u32x2 v = *reinterpret_cast<const u32x2*>(up + 16 * e);
+                u[b][2 * e] = v[0];
+                u[b][2 * e + 1] = v[1];
+            }
+    }
+    int left = g.depth;
+    auto late = [&](uint32_t at) {
+#pragma unroll
+        for (int b = 0; b < RB; ++b) down[b].next(at + (1 + b) * PIECE, left, tid);
+        x.next(at + (1 + RB) * PIECE, left, tid);
+        left -= C::BK;
+    };
+#pragma unroll
+    for (int s = 0; s < C::STAGES - 1; ++s) late(mine + s * C::STAGE);
+
+    // fragments: rows l % 16 of A and l % 32 of the rest
+    uint32_t fx[C::KSUB], fy[C::KSUB];
+#pragma unroll
+    for (int n = 0; n < C::KSUB; ++n) {
+        const int c = w * (C::BK / C::WK / 8) + 2 * n + half, r = lane & 15;
+        const uint32_t at = lds + (uint32_t)(r * L::PITCH + ((c ^ L::swz(r)) << 4));
+        fx[n] = at + (1 + RB) * PIECE;
+        fy[n] = at + (lane & 16 ? PIECE : 0);
+    }
+    f32x16 acc[FN];
+#pragma unroll
+    for (int j = 0; j < FN; ++j) acc[j] = f32x16{};
+    const int steps = (g.depth + C::BK - 1) / C::BK;
+    uint32_t stage = 0, fill = (C::STAGES - 1) * C::STAGE;
+    for (int s = 0; s < steps; ++s) {
+        // the first stages' loads came in another order: of the later ones no
+        // more than those of the stages behind may be in flight
+        if (s < C::STAGES - 1)
+            grp::publish<(C::STAGES - 2) * LATE>();
+        else
+            grp::publish<(C::STAGES - 2) * LOADS>();
+        y.next(mine + fill, y_left, tid);
+        y_left -= C::BK;
+        late(mine + fill);
+        fill = stage;
+#pragma unroll
+        for (int n = 0; n < C::KSUB; ++n) {
+            const u32x4 a = *reinterpret_cast<const G16_LDS u32x4*>((uintptr_t)(fx[n] + stage));
+#pragma unroll
+            for (int j = 0; j < FN; ++j) {
+                const u32x4 b = *reinterpret_cast<const G16_LDS u32x4*>((uintptr_t)(fy[n] + stage + 2 * j * PIECE));
+                acc[j] = T::mfma(b, a, acc[j]);
+            }
+        }
+        stage = stage == (C::STAGES - 1) * C::STAGE ? 0 : stage + C::STAGE;
+    }
+    grp::publish<0>();
+    using A = Cfg<32, 32 * FN, 256, 1, 1, 4, 2, 1>;   // of whole blocks, for what follows
+    static_assert(3 * FN * 4096 + 4096 <= (int)sizeof(smem), "LDS budget");
+    Acc<A> sums;
+#pragma unroll
+    for (int j = 0; j < FN; ++j) sums[0][j] = acc[j];
+    grp::add_waves<A>(smem, w, lane, sums);
+    if (w > 0) return;
+    f32x16 d = sums[0][0];
+    const int m = lane & 31;
+#pragma unroll
+    for (int b = 0; b < RB; ++b) {
+        const f32x16& h = sums[0][(b + 1) / 2];
+        const int at = (b + 1) % 2 * 8;
+        const uint32_t keep = m >= first[b] && m < end[b] ? 0xffffffffu : 0u;
+        u32x4 low;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) low[i] = T::pack(h[at + 2 * i] * scale[b], h[at + 2 * i + 1] * scale[b]) & keep;
+        d = T::mfma(u[b], low, d);
+    }
+    using O = Cfg<16, 16, 512, 1, 1, 4, 4, 1>;
+    Acc<O> out = {{d}};
+    grp::store<T, O, false>(smem + 3 * FN * 4096, g.d + (int64_t)row0 * g.d_ld + 2 * (int64_t)col0, g.d_ld, rows, g.cols - col0, 1.f, out, lane);
 }
 
 // Eight columns of a row: the parts' sums added up in order, scaled, rounded once.
@@ -685,16 +766,15 @@ using Large = Cfg<256, 256, 64, 2, 4, 1, 2, 1>;
 struct Form {
     int bm, bn, bk, threads, per_cu;
     float one, two;
-    const void *whole, *split, *join, *fused;
+    const void *whole, *split, *join;
 };
 
-template <typename T, int MODE, bool F32, class C, bool PARTS, bool FUSED = false>
+template <typename T, int MODE, bool F32, class C, bool PARTS>
 Form form(float one, float two)
 {
-    Form f = {C::BM, C::BN, C::BK, C::THREADS, C::PER_CU, one, two, (const void*)&tile_kernel<T, C, MODE, F32, false, false>, nullptr, nullptr, nullptr};
-    if constexpr (FUSED && MODE == ADAPT) f.fused = (const void*)&tile_kernel<T, C, MODE, F32, false, true>;
+    Form f = {C::BM, C::BN, C::BK, C::THREADS, C::PER_CU, one, two, (const void*)&tile_kernel<T, C, MODE, F32, false>, nullptr, nullptr};
     if constexpr (PARTS) {
-        f.split = (const void*)&tile_kernel<T, C, MODE, F32, true, false>;
+        f.split = (const void*)&tile_kernel<T, C, MODE, F32, true>;
         f.join = (const void*)&join_kernel<T, C, MODE, F32>;
     }
     return f;
@@ -708,8 +788,8 @@ struct Forms {
     Forms()
     {
         if constexpr (MODE != TN) {
-            f[n++] = form<T, MODE, F32, Tiny, false, true>(1.3f, 1.3f);
-            f[n++] = form<T, MODE, F32, Small, false, true>(2.0f, 2.0f);
+            f[n++] = form<T, MODE, F32, Tiny, false>(1.3f, 1.3f);
+            f[n++] = form<T, MODE, F32, Small, false>(2.0f, 2.0f);
         }
         if constexpr (MODE == NT || MODE == NN) f[n++] = form<T, MODE, F32, Flat, false>(5.4f, 7.8f);
         f[n++] = form<T, MODE, F32, Square, true>(5.0f, 6.4f);
@@ -718,7 +798,7 @@ struct Forms {
         if constexpr (MODE == ADAPT) f[n++] = form<T, MODE, F32, Large, false>(28.f, 28.f);
         if constexpr (MODE == NT || MODE == NN || MODE == TN)
             f[n++] = Form{grp::kRingTile, grp::kRingTile, grp::kRingStep, 256, 0, 20.6f, 20.6f, (const void*)&ring_kernel<T, MODE, F32>, nullptr,
-                          (const void*)&ring_join_kernel<T, MODE, F32>, nullptr};
+                          (const void*)&ring_join_kernel<T, MODE, F32>};
     }
 };
 
@@ -750,11 +830,8 @@ constexpr int64_t kMaxSplits = 16;
 // and for parts their bytes and the second launch.  The number of tiles is the
 // device's to know where there are several groups: half a tile for each group
 // is taken as lost.
-//
-// fused_us: what the adapters' projections add to a workgroup that computes
-// them itself, where it can, and then only such shapes; below 0 otherwise.
 template <int MODE>
-Plan plan(const Form* forms, int n, const Args& g, int cus, double fused_us, int* status)
+Plan plan(const Form* forms, int n, const Args& g, int cus, int* status)
 {
     const int64_t used = MODE == ADAPT ? 1 : g.groups < g.rows ? g.groups : g.rows;   // groups with rows, at most
     const double depth = MODE == TN ? (g.groups > 0 ? (double)g.rows / g.groups : 0.) : g.depth;
@@ -766,7 +843,7 @@ Plan plan(const Form* forms, int n, const Args& g, int cus, double fused_us, int
     for (int i = 0; i < n; ++i) {
         const Form& f = forms[i];
         const bool ring = f.per_cu == 0;
-        if ((ring && !ring_takes(MODE, g)) || (fused_us >= 0 && (f.fused == nullptr || g.rows > f.bm))) continue;
+        if (ring && !ring_takes(MODE, g)) continue;
         const int64_t ct = ceil_div(g.cols, f.bn);
         int64_t most;    // tiles, at most
         double tiles;    // and as expected
@@ -801,15 +878,14 @@ Plan plan(const Form* forms, int n, const Args& g, int cus, double fused_us, int
             continue;
         }
         const double slots = (double)cus * f.per_cu;
-        const double start = fused_us >= 0 ? 2.3 + fused_us : 2.3;
-        for (int64_t s = 1; s <= (f.split == nullptr || fused_us >= 0 ? 1 : kMaxSplits); s += s < 4 ? 1 : s / 2) {
+        for (int64_t s = 1; s <= (f.split == nullptr ? 1 : kMaxSplits); s += s < 4 ? 1 : s / 2) {
             const int64_t steps = ceil_div((int64_t)depth, f.bk * s);
             if (s > 1 && (steps < 4 || most * s > kMaxTiles)) break;
             const double d = (double)(steps * f.bk) / 1024, wgs = tiles * s;
             const double full = (double)(int64_t)(wgs / slots), rest = wgs - full * slots;
-            double us = 1.5 + full * (start + f.two * d);
-            if (rest > 0) us += start + (rest > cus ? f.two : f.one) * d;
-            if (us < memory + start + 0.7) us = memory + start + 0.7;
+            double us = 1.5 + full * (2.3 + f.two * d);
+            if (rest > 0) us += 2.3 + (rest > cus ? f.two : f.one) * d;
+            if (us < memory + 3) us = memory + 3;
             if (s > 1) us += 6 + wgs * f.bm * f.bn * 8 / 8e6;
             if (us < best.us) best = Plan{&f, most * s, s, s > 1 ? most * s * f.bm * f.bn * 4 : 0, false, us};
         }
@@ -819,15 +895,15 @@ Plan plan(const Form* forms, int n, const Args& g, int cus, double fused_us, int
 }
 
 template <int MODE, bool F32 = false>
-Plan plan_for(int dtype, const Args& g, int cus, int* status, double fused_us = -1)
+Plan plan_for(int dtype, const Args& g, int cus, int* status)
 {
     static const Forms<F16, MODE, F32> f16;
     static const Forms<BF16, MODE, F32> bf16;
-    return dtype == GROUPED_F16 ? plan<MODE>(f16.f, f16.n, g, cus, fused_us, status) : plan<MODE>(bf16.f, bf16.n, g, cus, fused_us, status);
+    return dtype == GROUPED_F16 ? plan<MODE>(f16.f, f16.n, g, cus, status) : plan<MODE>(bf16.f, bf16.n, g, cus, status);
 }
 
 template <int MODE>
-int run(const Plan& p, const Args& args, void* parts, int cus, hipStream_t s, bool fused = false)
+int run(const Plan& p, const Args& args, void* parts, int cus, hipStream_t s)
 {
     Args g = args;
     const Form& f = *p.form;
@@ -841,7 +917,7 @@ int run(const Plan& p, const Args& args, void* parts, int cus, hipStream_t s, bo
         g.group_tiles = (uint32_t)t;
         g.per_group = attn::div_by(p.walks || t < 8 * kNumXcd ? t : ceil_div(t, kNumXcd) * kNumXcd);
     }
-    int st = launch(fused ? f.fused : p.splits > 1 ? f.split : f.whole, p.wgs, f.threads, &g, s);
+    int st = launch(p.splits > 1 ? f.split : f.whole, p.wgs, f.threads, &g, s);
     if (st != GEMM_F16_NT_OK || g.parts == nullptr) return st;
     const int64_t pieces = p.walks ? 4 * cus : p.wgs / p.splits * (f.bm * f.bn / 2048);
     return launch(f.join, pieces, 256, &g, s);
@@ -981,7 +1057,8 @@ int grouped_run(const grouped_desc* d, Written out, void* workspace, int64_t wor
 struct AdapterCall {
     Args low, rest;
     Plan low_plan, plan;
-    bool adapted, fused;
+    bool adapted;
+    const void* single;   // all in one launch
     int cus;
     int64_t low_bytes, bytes;   // of the projections, and of all of the workspace
 };
@@ -991,7 +1068,7 @@ int plan_adapters(const adapter_desc* d, AdapterCall* c)
     int st = device_cus(&c->cus);
     if (st != GEMM_F16_NT_OK) return st;
     c->adapted = d->adapters > 0 && d->rank > 0;
-    c->fused = false;
+    c->single = nullptr;
     Args g = {};
     g.x = (const char*)d->A;
     g.cu = d->cu;
@@ -1031,16 +1108,21 @@ int plan_adapters(const adapter_desc* d, AdapterCall* c)
     c->rest = g;
     c->plan = plan_for<ADAPT>(d->dtype, g, c->cus, &st);
     if (st != GEMM_F16_NT_OK) return st;
-    if (c->adapted && d->rows <= 32) {
-        // a launch less (about 3 us and what the projections take) against their share in every workgroup
-        const int64_t passes = (d->requests < d->rows ? d->requests : d->rows) * ceil_div(d->rank, 32);
-        int fst = GEMM_F16_NT_OK;
-        const Plan f = plan_for<ADAPT>(d->dtype, g, c->cus, &fst, 1.0 + passes * (0.6 + 0.7 * (double)d->K / 1024));
-        if (fst == GEMM_F16_NT_OK && f.us < c->plan.us + c->low_plan.us + 2) {
-            c->fused = true;
-            c->plan = f;
-            c->low_bytes = ceil_div(f.wgs * 32 * 2 * d->rank, 256) * 256;
-            parts = 0;
+    const int64_t blocks = d->requests * ceil_div(d->rank, 16);
+    if (c->adapted && d->rows <= 16 && blocks <= 3) {
+        // rounds of the compute units, each with what starting a workgroup
+        // costs and its tile's share of the contraction.  Measured on MI355X:
+        // 4096 x 4096, one request of rank 16 10.2 us (two launches 22), three
+        // 16.0, 1024 x 1024 5.0 and 7.5 (13); 14336 x 4096 34.4 and, in two
+        // launches, 39.6.  Seven blocks took as long as two launches do.
+        const double us = 1.5 + (double)ceil_div(ceil_div(d->N, 16), c->cus) * (2.0 + (blocks == 1 ? 1.65 : 3.0) * (double)d->K / 1024);
+        if (us < c->plan.us + c->low_plan.us + 2) {
+            if (d->dtype == GROUPED_F16)
+                c->single = blocks == 1 ? (const void*)&single_kernel<F16, 1> : (const void*)&single_kernel<F16, 3>;
+            else
+                c->single = blocks == 1 ? (const void*)&single_kernel<BF16, 1> : (const void*)&single_kernel<BF16, 3>;
+            c->bytes = 0;
+            return GEMM_F16_NT_OK;
         }
     }
     if (c->plan.part_bytes > parts) parts = c->plan.part_bytes;
@@ -1090,13 +1172,14 @@ int adapter_nt(const adapter_desc* d, void* workspace, int64_t workspace_bytes, 
     if ((st = plan_adapters(d, &c)) != GEMM_F16_NT_OK) return st;
     if ((st = check_workspace(workspace, workspace_bytes, c.bytes)) != GEMM_F16_NT_OK) return st;
     if ((st = check_adapters(d, {workspace, c.bytes})) != GEMM_F16_NT_OK) return st;
+    if (c.single != nullptr) return launch(c.single, ceil_div(c.rest.cols, 16), 256, &c.rest, (hipStream_t)stream);
     char* parts = (char*)workspace + c.low_bytes;
-    if (c.adapted && !c.fused) {
+    if (c.adapted) {
         c.low.d = (char*)workspace;
         if ((st = run<LOW>(c.low_plan, c.low, parts, c.cus, (hipStream_t)stream)) != GEMM_F16_NT_OK) return st;
     }
-    c.rest.low = (char*)workspace;
-    return run<ADAPT>(c.plan, c.rest, parts, c.cus, (hipStream_t)stream, c.fused);
+    c.rest.low = (const char*)workspace;
+    return run<ADAPT>(c.plan, c.rest, parts, c.cus, (hipStream_t)stream);
 }
 
 }  // extern "C"

@@ -72,11 +72,8 @@ def _first(name, X, dims):
     """Type code, type and device of the tensor that the others have to match."""
     torch = _torch or _module()
     dtype = X.dtype
-    if dtype is torch.float16:
-        code = F16
-    elif dtype is torch.bfloat16:
-        code = BF16
-    else:
+    code = F16 if dtype is torch.float16 else BF16 if dtype is torch.bfloat16 else None
+    if code is None:
         raise TypeError(f"{name} must be torch.float16 or torch.bfloat16, not {dtype}")
     if not X.is_cuda:
         raise ValueError(f"{name} must be a device tensor")
@@ -85,36 +82,45 @@ def _first(name, X, dims):
     return code, dtype, X.device
 
 
-def _match(name, X, shape, dtype, device):
+def _rows(name, X, shape, dtype, device):
+    """Elements from a row to the next of a 2-D tensor that has to have this shape and type."""
+    st = X.stride()
+    if X.shape == shape and st[1] == 1 and st[0] >= shape[1] and shape[0] > 1 and X.dtype is dtype and X.device == device:
+        return st[0]
+    return _explain(name, X, shape, dtype, device)[-1]
+
+
+def _matrices(name, X, shape, dtype, device):
+    """Elements from a row to the next, and from a matrix to the next, of a 3-D tensor that has to have this shape and type."""
+    st = X.stride()
+    if X.shape == shape and st[2] == 1 and st[1] >= shape[2] and shape[1] > 1 and shape[0] > 1 and X.dtype is dtype and X.device == device:
+        return st[1], st[0]
+    between, ld = _explain(name, X, shape, dtype, device)
+    return ld, between
+
+
+def _explain(name, X, shape, dtype, device):
+    """(stride of the first dimension, row pitch), where a look at the tensor does not settle them: says what is wrong, and
+    leaves out strides of dimensions with one entry, which say nothing."""
     if X.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, not {X.dtype}")
     if X.device != device:
         raise ValueError(f"{name} is on {X.device}, the other tensors on {device}")
     if X.shape != shape:
         raise ValueError(f"{name} must be {tuple(shape)}; got {tuple(X.shape)}")
-
-
-def _pitch(name, X):
-    """Elements from a row of a 2-D tensor, or of each matrix of a 3-D one, to the next."""
-    st, shape = X.stride(), X.shape
-    width = shape[-1]
-    if width > 1 and st[-1] != 1:
+    st, width, there = X.stride(), shape[-1], X.numel() > 0
+    if there and width > 1 and st[-1] != 1:
         raise ValueError(f"{name}: last dimension must be contiguous")
-    if shape[-2] > 1 and X.numel():
-        if st[-2] < width:
+    ld = width
+    if there and shape[-2] > 1:
+        ld = st[-2]
+        if ld < width:
             raise ValueError(f"{name}: rows must not overlap")
-        return st[-2]
-    return width   # a stride that says nothing
-
-
-def _matrices(name, X):
-    """(row pitch, stride from a matrix to the next) of a 3-D tensor."""
-    ld = _pitch(name, X)
-    return ld, X.stride(0) if X.shape[0] > 1 and X.numel() else X.shape[1] * ld
+    return st[0] if there and shape[0] > 1 else shape[-2] * ld, ld
 
 
 def _ints(name, X, n, device):
-    if X.dtype is not (_torch or _module()).int32:
+    if X.dtype is not _torch.int32:
         raise TypeError(f"{name} must be torch.int32")
     if X.device != device or X.shape != (n,) or not X.is_contiguous():
         raise ValueError(f"{name} must be a contiguous tensor of {n} values on {device}")
@@ -173,12 +179,10 @@ def _product_desc(A, B, cu, D):
     if B.dim() != 3:
         raise ValueError(f"B must have 3 dimensions; got {tuple(B.shape)}")
     G, N = _groups(cu), B.shape[1]
-    _match("B", B, (G, N, K), dtype, device)
-    if D is not None:
-        _match("D", D, (rows, N), dtype, device)
-    ldb, sb = _matrices("B", B)
-    return _pack_grouped(code, 0, G, rows, N, K, A.data_ptr(), B.data_ptr(), 16 if D is None else D.data_ptr(), _pitch("A", A), ldb, sb,
-                         N if D is None else _pitch("D", D), _ints("cu", cu, G + 1, device)), device
+    ldb, sb = _matrices("B", B, (G, N, K), dtype, device)
+    return _pack_grouped(code, 0, G, rows, N, K, A.data_ptr(), B.data_ptr(), 16 if D is None else D.data_ptr(),
+                         _rows("A", A, (rows, K), dtype, device), ldb, sb, N if D is None else _rows("D", D, (rows, N), dtype, device),
+                         _ints("cu", cu, G + 1, device)), device
 
 
 def grouped_product(A, B, cu, *, D=None, workspace=None):
@@ -191,9 +195,8 @@ def grouped_product(A, B, cu, *, D=None, workspace=None):
     holds arbitrary values there).  `workspace`: a device tensor of at least
     grouped_product_workspace(...) bytes, 16-byte aligned; allocated here when
     not given."""
-    if D is None:
-        _first("A", A, 2)
-        D = _torch.empty((A.shape[0], B.shape[1] if B.dim() == 3 else 0), dtype=A.dtype, device=A.device)
+    if D is None and A.dim() == 2 and B.dim() == 3:   # other tensors are refused below
+        D = A.new_empty((A.shape[0], B.shape[1]))
     _run("grouped_nt", *_product_desc(A, B, cu, D), workspace)
     return D
 
@@ -209,12 +212,10 @@ def _grad_input_desc(G, B, cu, dA):
     if B.dim() != 3:
         raise ValueError(f"B must have 3 dimensions; got {tuple(B.shape)}")
     groups, K = _groups(cu), B.shape[2]
-    _match("B", B, (groups, N, K), dtype, device)
-    if dA is not None:
-        _match("dA", dA, (rows, K), dtype, device)
-    ldb, sb = _matrices("B", B)
+    ldb, sb = _matrices("B", B, (groups, N, K), dtype, device)
     return _pack_grouped(code, 0, groups, rows, N, K, 16 if dA is None else dA.data_ptr(), B.data_ptr(), G.data_ptr(),
-                         K if dA is None else _pitch("dA", dA), ldb, sb, _pitch("G", G), _ints("cu", cu, groups + 1, device)), device
+                         K if dA is None else _rows("dA", dA, (rows, K), dtype, device), ldb, sb, _rows("G", G, (rows, N), dtype, device),
+                         _ints("cu", cu, groups + 1, device)), device
 
 
 def grouped_product_grad_input(G, B, cu, *, dA=None, workspace=None):
@@ -222,9 +223,8 @@ def grouped_product_grad_input(G, B, cu, *, dA=None, workspace=None):
     being the gradient for D and B (groups, N, K) the matrices.  Returns dA
     (rows, K); rows of no group are left as they were in a given dA.
     `workspace` as for grouped_product."""
-    if dA is None:
-        _first("G", G, 2)
-        dA = _torch.empty((G.shape[0], B.shape[2] if B.dim() == 3 else 0), dtype=G.dtype, device=G.device)
+    if dA is None and G.dim() == 2 and B.dim() == 3:   # other tensors are refused below
+        dA = G.new_empty((G.shape[0], B.shape[2]))
     _run("grouped_nn", *_grad_input_desc(G, B, cu, dA), workspace)
     return dA
 
@@ -240,15 +240,14 @@ def _grad_weight_desc(G, A, cu, dB, dtype):
     if A.dim() != 2:
         raise ValueError(f"A must have 2 dimensions; got {tuple(A.shape)}")
     groups, K = _groups(cu), A.shape[1]
-    _match("A", A, (rows, K), own, device)
     if dtype is not own and dtype is not _torch.float32:
         raise TypeError(f"dB must be {own} or torch.float32, not {dtype}")
     ldb, sb = K, N * K
     if dB is not None:
-        _match("dB", dB, (groups, N, K), dtype, device)
-        ldb, sb = _matrices("dB", dB)
+        ldb, sb = _matrices("dB", dB, (groups, N, K), dtype, device)
     return _pack_grouped(code, 0 if dtype is own else 1, groups, rows, N, K, A.data_ptr(), 16 if dB is None else dB.data_ptr(), G.data_ptr(),
-                         _pitch("A", A), ldb, sb, _pitch("G", G), _ints("cu", cu, groups + 1, device)), device
+                         _rows("A", A, (rows, K), own, device), ldb, sb, _rows("G", G, (rows, N), own, device),
+                         _ints("cu", cu, groups + 1, device)), device
 
 
 def grouped_product_grad_weight(G, A, cu, *, dB=None, dtype=None, workspace=None):
@@ -257,13 +256,10 @@ def grouped_product_grad_weight(G, A, cu, *, dB=None, dtype=None, workspace=None
     being the gradient for D and A (rows, K) its input.  Returns dB (groups, N,
     K) in the operands' type, or in torch.float32 where `dtype` or a given dB
     says so.  `workspace` as for grouped_product."""
-    if dB is None:
-        _, own, device = _first("G", G, 2)
-        dtype = own if dtype is None else dtype
-        if dtype is own or dtype is _torch.float32:   # others are refused below
-            dB = _torch.empty((_groups(cu), G.shape[1], A.shape[1] if A.dim() == 2 else 0), dtype=dtype, device=device)
-    elif dtype is None:
-        dtype = dB.dtype
+    if dtype is None:
+        dtype = G.dtype if dB is None else dB.dtype
+    if dB is None and G.dim() == 2 and A.dim() == 2 and dtype in (G.dtype, (_torch or _module()).float32):   # others are refused below
+        dB = G.new_empty((_groups(cu), G.shape[1], A.shape[1]), dtype=dtype)
     _run("grouped_tn", *_grad_weight_desc(G, A, cu, dB, dtype), workspace)
     return dB
 
@@ -280,20 +276,18 @@ def _adapter_desc(A, B, down, up, cu, adapters, scales, D):
     if B.dim() != 2 or down.dim() != 3 or up.dim() != 3:
         raise ValueError(f"B must have 2, down and up 3 dimensions; got {tuple(B.shape)}, {tuple(down.shape)}, {tuple(up.shape)}")
     N, (count, rank, _), requests = B.shape[0], down.shape, _groups(cu)
-    _match("B", B, (N, K), dtype, device)
-    _match("down", down, (count, rank, K), dtype, device)
-    _match("up", up, (count, N, rank), dtype, device)
+    ldb = _rows("B", B, (N, K), dtype, device)
+    ldn, sdn = _matrices("down", down, (count, rank, K), dtype, device)
+    lup, sup = _matrices("up", up, (count, N, rank), dtype, device)
+    factors = 0
     if scales is not None:
-        _match("scales", scales, (count,), _torch.float32, device)
-        if not scales.is_contiguous():
-            raise ValueError("scales must be contiguous")
-    if D is not None:
-        _match("D", D, (rows, N), dtype, device)
-    (ldn, sdn), (lup, sup) = _matrices("down", down), _matrices("up", up)
+        if scales.dtype is not _torch.float32 or scales.device != device or scales.shape != (count,) or not scales.is_contiguous():
+            raise ValueError(f"scales must be a contiguous float32 tensor of {count} values on {device}")
+        factors = scales.data_ptr()
     desc = _pack_adapter(code, rank, count, requests, rows, N, K, A.data_ptr(), B.data_ptr(), 16 if D is None else D.data_ptr(), down.data_ptr(),
-                         up.data_ptr(), 0 if scales is None else scales.data_ptr(), _ints("cu", cu, requests + 1, device),
-                         _ints("adapters", adapters, requests, device), _pitch("A", A), _pitch("B", B), N if D is None else _pitch("D", D),
-                         ldn, sdn, lup, sup)
+                         up.data_ptr(), factors, _ints("cu", cu, requests + 1, device), _ints("adapters", adapters, requests, device),
+                         _rows("A", A, (rows, K), dtype, device), ldb, N if D is None else _rows("D", D, (rows, N), dtype, device), ldn, sdn,
+                         lup, sup)
     return desc, device
 
 
@@ -309,11 +303,8 @@ def adapter_product(A, B, down, up, cu, adapters, scales=None, *, D=None, worksp
     no request are left as they were in a given D.  `workspace`: a device
     tensor of at least adapter_product_workspace(...) bytes, 16-byte aligned;
     allocated here when not given."""
-    _first("A", A, 2)
-    if D is None:
-        if B.dim() != 2:
-            raise ValueError(f"B must have 2 dimensions; got {tuple(B.shape)}")
-        D = _torch.empty((A.shape[0], B.shape[0]), dtype=A.dtype, device=A.device)
+    if D is None and A.dim() == 2 and B.dim() == 2:   # other tensors are refused below
+        D = A.new_empty((A.shape[0], B.shape[0]))
     _run("adapter_nt", *_adapter_desc(A, B, down, up, cu, adapters, scales, D), workspace)
     return D
 

@@ -165,6 +165,13 @@ def test_values(lens, n, k, dtype):
 ADAPTERS = [
     ([1], [0], 8, 8, 8),
     ([1], [-1], 64, 72, 16),
+    ([16], [2], 40, 2000, 16),                             # one request of few rows
+    ([3], [1], 4104, 1032, 48),
+    ([7], [3], 264, 256, 24),
+    ([0], [1], 64, 64, 8),
+    ([2, 0, 5, 1, 1, 0, 3], [1, 0, -1, 3, 7, 2, 0], 72, 264, 16),
+    ([1, 1], [2, 2], 520, 1024, 40),
+    ([17], [2], 136, 520, 40),
     ([1] * 40, [b % 7 - 1 for b in range(40)], 136, 264, 16),
     ([1] * 130, [b % 3 for b in range(130)], 264, 128, 24),
     ([3, 0, 40, 1, 1, 0, 0, 17], [1, 0, 2, 2, -1, 9, 1, 0], 520, 520, 128),
