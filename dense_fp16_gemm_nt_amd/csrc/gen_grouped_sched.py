@@ -43,6 +43,13 @@ zeros; a side by columns beside it begins that many rows early, and those
 rows' offsets are masked likewise.  With both sides by columns the rows behind
 the last load zeros by themselves: the buffers end there.
 
+RR can begin with a step of another product, whose operands have rows of their
+own (the second product of a low-rank adapter, up to 64 elements of its
+contraction): where %[ext] is not 0, step 0 is loaded from %[rsa0] (rows of 128
+bytes, lane offsets %[ha0], %[ha1] for even and odd loads) and %[rsb0] (lane
+offsets %[hb0], %[hb1], %[sb8] bytes for 8 rows), and the contraction's first
+step, with its masks, is step 1.
+
 Operands: load offsets %[axQ], %[bxQ] (less 1024 * (Q mod 4), the instruction
 offset of the load); fragment addresses %[raN], %[rbN] (N: sub-step by rows,
 block by columns); resources %[rsa], %[rsb], %[rsd]; the wave's LDS load base
@@ -239,6 +246,14 @@ def generate(la: str, lb: str, p: dict) -> str:
     e = Emitter(la, lb)
     layout = e.layout
     head = {op: "none" if la == "c" else layout[op] for op in "ab"}
+
+    def loads(step: int, masked: bool) -> None:
+        for op, q in LOAD3:
+            if q % 4 == 0:
+                e.op(Emitter.m0(op, q, step))
+                e.op("s_nop 0")   # M0 write -> LDS-DMA read of M0
+            e.op(Emitter.load(op, q, "ko", f"v{head_reg(op, q)}" if masked and head[op] != "none" else None))
+
     for op, q in LOAD3:
         if head[op] == "r":
             e.op(f"v_or_b32 v{head_reg(op, q)}, %[{op}x{q}], %[hm{q % 2}]")
@@ -248,15 +263,30 @@ def generate(la: str, lb: str, p: dict) -> str:
             e.op(f"s_sub_i32 %[khb], %[hk], {2 * q}")
             e.op("v_cmp_gt_i32 vcc, %[khb], %[kr]")
             e.op(f"v_cndmask_b32 v{head_reg('b', q)}, %[bx{q}], v80, vcc")
-    for step in (0, 1):
-        if step:
-            for op in "ab":
-                e.op(f"s_add_u32 %[ko{op}], %[ko{op}], {side_steps(op, layout[op])}")
-        for op, q in LOAD3:
+    if layout == {"a": "r", "b": "r"}:
+        e.op("s_cmp_eq_u32 %[ext], 0")
+        e.op("s_cbranch_scc1 11f")
+        for q in range(8):
             if q % 4 == 0:
-                e.op(Emitter.m0(op, q, step))
-                e.op("s_nop 0")   # M0 write -> LDS-DMA read of M0
-            e.op(Emitter.load(op, q, "ko", f"v{head_reg(op, q)}" if step == 0 and head[op] != "none" else None))
+                e.op(f"s_mov_b32 %[kha], {4096 * (q // 4)}")
+                e.op(Emitter.m0("a", q, 0))
+                e.op("s_nop 0")
+            off = f" offset:{1024 * (q % 4)}" if q % 4 else ""
+            e.op(f"buffer_load_dwordx4 %[ha{q % 2}], %[rsa0], %[kha] offen{off} lds")
+        for q in range(8):
+            e.op(f"s_mul_i32 %[khb], %[sb8], {q}")
+            e.op(f"s_add_u32 m0, %[lb], {SIDE_B + 1024 * q}")
+            e.op("s_nop 0")
+            e.op(f"buffer_load_dwordx4 %[hb{q % 2}], %[rsb0], %[khb] offen lds")
+        loads(1, True)
+        e.op("s_branch 12f")
+        e.label("11")
+    loads(0, True)
+    for op in "ab":
+        e.op(f"s_add_u32 %[ko{op}], %[ko{op}], {side_steps(op, layout[op])}")
+    loads(1, False)
+    if layout == {"a": "r", "b": "r"}:
+        e.label("12")
     for op in "ab":
         e.op(f"s_add_u32 %[kh{op}], %[ko{op}], {side_steps(op, layout[op])}")
     e.op(f"s_waitcnt vmcnt({NLOAD})")

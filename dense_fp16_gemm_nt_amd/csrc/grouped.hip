@@ -24,8 +24,9 @@ using grp::F16;
 // What a launch computes.  NT, NN and TN are the three products of a group;
 // LOW the adapters' projections onto their rank, a product NT whose matrix a
 // table chooses and whose result is scaled; ADAPT the shared projection, with
-// the adapters' second products added to the same sums.
-enum Mode { NT, NN, TN, LOW, ADAPT };
+// the adapters' second products added to the same sums; EACH the same in large
+// tiles, which have rows of one request each.
+enum Mode { NT, NN, TN, LOW, ADAPT, EACH };
 
 struct Args {
     const char* x;
@@ -38,6 +39,8 @@ struct Args {
     int cols;            // of D
     int x_cols;          // TN: rows of a group's D, which are columns of X
     int depth;           // the contraction, except for TN
+    int low_rows;        // LOW: rows of `down`; columns behind them are zeros
+    int rank;            // EACH
     Div col_tiles;
     Div per_group;       // TN: tiles of a group, padded to whole rounds of the XCDs
     uint32_t group_tiles;
@@ -320,7 +323,7 @@ __global__ __launch_bounds__(C::THREADS, C::PER_CU * C::WAVES / 4) void tile_ker
         if (MODE == NN)
             y.start(mat + 2 * (int64_t)wk.col0, g.y_ld, g.cols - wk.col0, tid);
         else
-            y.start(mat + (int64_t)wk.col0 * g.y_ld, g.y_ld, g.cols - wk.col0, tid);
+            y.start(mat + (int64_t)wk.col0 * g.y_ld, g.y_ld, (MODE == LOW ? g.low_rows : g.cols) - wk.col0, tid);
     }
     const uint32_t lds = attn::lds_address(smem), mine = lds + 1024u * (uint32_t)w;
     grp::Frags<C, XC, C::BM, C::FM> fx;
@@ -616,7 +619,8 @@ __device__ __forceinline__ uint32_t place_large(const Args& g, Work& wk)
         wk.tile0 = (int)clamped_origin(wk.tile0 / grp::kRingTile, grp::kRingTile, g.x_cols);
         depth = wk.rows;
     }
-    const uint32_t steps = (uint32_t)(depth + grp::kRingStep - 1) / grp::kRingStep;
+    uint32_t steps = (uint32_t)(depth + grp::kRingStep - 1) / grp::kRingStep;
+    if (MODE == EACH) steps += (uint32_t)g.ids[wk.group] < (uint32_t)g.adapters;   // the adapter's second product is a step
     return steps < 2 ? 2 : steps;
 }
 
@@ -644,6 +648,13 @@ __global__ __launch_bounds__(256, 1) void ring_kernel(const Args g)
     out.start(lds, g.d_ld, F32 ? g.d_ld : PART_LD, w, lane);
     const uint32_t sta = (uint32_t)(STEP * g.x_ld), stb = (uint32_t)(STEP * g.y_ld);
     const int kr = 16 * w + lane / 32;
+    uint32_t ha[2], hb[2];   // EACH: see gen_grouped_sched.py
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+        const int r = 64 * w + lane / 8, c = (lane & 7) ^ grp::RingSide<false>::swz(8 * q + lane / 8);
+        ha[q] = (uint32_t)(r * 128 + 16 * c);
+        hb[q] = MODE == EACH && 8 * c < g.rank ? (uint32_t)(r * g.up_ld + 16 * c) : grp::kBeyond;
+    }
 
     for (uint32_t slot = (uint32_t)xcd_slot(blockIdx.x, gridDim.x); slot < items; slot += gridDim.x) {
         uint32_t t = slot, part = 0;
@@ -655,7 +666,8 @@ __global__ __launch_bounds__(256, 1) void ring_kernel(const Args g)
         Work wk = tile_at<TILE, TILE, MODE>(g, groups, t);
         uint32_t rem = place_large<MODE>(g, wk);
         // the contraction's first step is the partial one: see gen_grouped_sched.py
-        int hk = MODE == TN ? 0 : (int)rem * STEP - g.depth;
+        int hk = MODE == TN ? 0 : (g.depth + STEP - 1) / STEP * STEP - g.depth;
+        uint32_t ext = MODE == EACH && (int)rem * STEP > g.depth + hk ? 1 : 0;
         const uint32_t parts = slot < walk.full ? 1 : walk.of(rem);
         if (part >= parts) continue;
         const uint32_t first = part * rem / parts;
@@ -675,18 +687,20 @@ __global__ __launch_bounds__(256, 1) void ring_kernel(const Args g)
             const int64_t n = wk.rows < TILE ? wk.rows : TILE, length = g.depth + hk;
             x = g.x + wk.row0 * g.x_ld - 2 * hk;
             x_bytes = (n - 1) * g.x_ld + 2 * length;
-            y = g.y + wk.group * g.y_mat + (MODE == NT ? wk.col0 * g.y_ld - 2 * hk : 2 * (int64_t)wk.col0 - hk * g.y_ld);
-            y_bytes = MODE == NT ? (TILE - 1) * g.y_ld + 2 * length : (length - 1) * g.y_ld + 2 * TILE;
+            y = g.y + wk.group * g.y_mat + (MODE != NN ? wk.col0 * g.y_ld - 2 * hk : 2 * (int64_t)wk.col0 - hk * g.y_ld);
+            y_bytes = MODE != NN ? (TILE - 1) * g.y_ld + 2 * length : (length - 1) * g.y_ld + 2 * TILE;
             rows = clampi((int)n - wm, 0, 128);
             d = g.d + (int64_t)(wk.row0 + wm) * g.d_ld;
         }
         if (first > 0) {   // a later part
-            const int64_t dx = (int64_t)first * (XC ? STEP * g.x_ld : 2 * STEP), dy = (int64_t)first * (YC ? STEP * g.y_ld : 2 * STEP);
+            const int64_t skip = first - ext;
+            const int64_t dx = skip * (XC ? STEP * g.x_ld : 2 * STEP), dy = skip * (YC ? STEP * g.y_ld : 2 * STEP);
             x += dx;
             y += dy;
             x_bytes -= dx < x_bytes ? dx : x_bytes;
             y_bytes -= dy < y_bytes ? dy : y_bytes;
-            hk = 0;
+            if (skip > 0) hk = 0;
+            ext = 0;
         }
         uint32_t hm[2];
 #pragma unroll
@@ -710,8 +724,16 @@ __global__ __launch_bounds__(256, 1) void ring_kernel(const Args g)
         asm volatile(LOOP("f16") : G16_GROUPED_STATE : G16_GROUPED_COMMON, __VA_ARGS__ : G16_GROUPED_CLOBBERS); \
     else \
         asm volatile(LOOP("bf16") : G16_GROUPED_STATE : G16_GROUPED_COMMON, __VA_ARGS__ : G16_GROUPED_CLOBBERS)
-        if constexpr (MODE == NT) {
-            G16_GROUPED_BLOCK(G16_GROUPED_RR, G16_GROUPED_A_ROWS, G16_GROUPED_B_ROWS);
+        if constexpr (MODE == NT || MODE == EACH) {
+            u32x4 rsa0 = rsa, rsb0 = rsb;
+            if (MODE == EACH) {
+                const int64_t n = wk.rows < TILE ? wk.rows : TILE;
+                rsa0 = grp::ring_rsrc(g.low + (int64_t)wk.row0 * 128, n * 128);
+                rsb0 = grp::ring_rsrc(g.up + (ext ? (int64_t)g.ids[wk.group] * g.up_mat : 0) + wk.col0 * g.up_ld, (TILE - 1) * g.up_ld + 2 * g.rank);
+            }
+            const uint32_t sb8 = grp::uniform((uint32_t)(8 * g.up_ld));
+            ext = grp::uniform(ext);
+            G16_GROUPED_BLOCK(G16_GROUPED_RR, G16_GROUPED_A_ROWS, G16_GROUPED_B_ROWS, G16_GROUPED_EXT);
         } else if constexpr (MODE == NN) {
             G16_GROUPED_BLOCK(G16_GROUPED_RC, G16_GROUPED_A_ROWS, G16_GROUPED_B_COLS, [hk] "s"(masked), [kr] "v"(kr));
         } else {
@@ -787,16 +809,16 @@ struct Forms {
     int n = 0;
     Forms()
     {
-        if constexpr (MODE != TN) {
+        if constexpr (MODE != TN && MODE != EACH) {
             f[n++] = form<T, MODE, F32, Tiny, false>(1.3f, 1.3f);
             f[n++] = form<T, MODE, F32, Small, false>(2.0f, 2.0f);
         }
         if constexpr (MODE == NT || MODE == NN) f[n++] = form<T, MODE, F32, Flat, false>(5.4f, 7.8f);
-        f[n++] = form<T, MODE, F32, Square, true>(5.0f, 6.4f);
-        if constexpr (MODE != TN) f[n++] = form<T, MODE, F32, Oblong, true>(6.8f, 10.0f);
-        if constexpr (MODE != LOW) f[n++] = form<T, MODE, F32, Middle, true>(11.2f, 16.2f);
+        if constexpr (MODE != EACH) f[n++] = form<T, MODE, F32, Square, true>(5.0f, 6.4f);
+        if constexpr (MODE != TN && MODE != EACH) f[n++] = form<T, MODE, F32, Oblong, true>(6.8f, 10.0f);
+        if constexpr (MODE != LOW && MODE != EACH) f[n++] = form<T, MODE, F32, Middle, true>(11.2f, 16.2f);
         if constexpr (MODE == ADAPT) f[n++] = form<T, MODE, F32, Large, false>(28.f, 28.f);
-        if constexpr (MODE == NT || MODE == NN || MODE == TN)
+        if constexpr (MODE == NT || MODE == NN || MODE == TN || MODE == EACH)
             f[n++] = Form{grp::kRingTile, grp::kRingTile, grp::kRingStep, 256, 0, 20.6f, 20.6f, (const void*)&ring_kernel<T, MODE, F32>, nullptr,
                           (const void*)&ring_join_kernel<T, MODE, F32>};
     }
@@ -812,7 +834,7 @@ bool ring_takes(int mode, const Args& g)
         const int64_t reach = (int64_t)g.rows + 3 * grp::kRingStep;
         return g.x_cols >= grp::kRingTile && reach * g.x_ld < (int64_t(1) << 32) && reach * g.y_ld < (int64_t(1) << 32);
     }
-    return g.depth > grp::kRingStep && (mode == NT || ((int64_t)g.depth + 2 * grp::kRingStep) * g.y_ld < (int64_t(1) << 31));
+    return g.depth > grp::kRingStep && (mode != NN || ((int64_t)g.depth + 2 * grp::kRingStep) * g.y_ld < (int64_t(1) << 31));
 }
 
 struct Plan {
@@ -836,7 +858,7 @@ Plan plan(const Form* forms, int n, const Args& g, int cus, int* status)
     const int64_t used = MODE == ADAPT ? 1 : g.groups < g.rows ? g.groups : g.rows;   // groups with rows, at most
     const double depth = MODE == TN ? (g.groups > 0 ? (double)g.rows / g.groups : 0.) : g.depth;
     // matrices, rows read and rows written, at 5.5 TB/s
-    const double mats = MODE == TN ? (double)g.groups * g.x_cols * g.cols : (double)used * g.cols * depth;
+    const double mats = MODE == TN ? (double)g.groups * g.x_cols * g.cols : (MODE == EACH ? 1. : used) * g.cols * depth;
     const double rows = MODE == TN ? (double)g.rows * (g.x_cols + g.cols) : (double)g.rows * (depth + g.cols);
     const double memory = (mats + rows) * 2 / 5.5e6;
     Plan best = {nullptr, 0, 1, 0, false, 1e300};
@@ -1057,7 +1079,7 @@ int grouped_run(const grouped_desc* d, Written out, void* workspace, int64_t wor
 struct AdapterCall {
     Args low, rest;
     Plan low_plan, plan;
-    bool adapted;
+    bool adapted, each;
     const void* single;   // all in one launch
     int cus;
     int64_t low_bytes, bytes;   // of the projections, and of all of the workspace
@@ -1088,7 +1110,7 @@ int plan_adapters(const adapter_desc* d, AdapterCall* c)
         c->low.y_ld = 2 * d->ld_down;
         c->low.y_mat = 2 * d->stride_down;
         c->low.d_ld = 2 * d->rank;
-        c->low.cols = d->rank;
+        c->low.cols = c->low.low_rows = d->rank;
         c->low_plan = plan_for<LOW>(d->dtype, c->low, c->cus, &st);
         if (st != GEMM_F16_NT_OK) return st;
         c->low_bytes = ceil_div(2 * d->rows * d->rank, 256) * 256;
@@ -1106,7 +1128,24 @@ int plan_adapters(const adapter_desc* d, AdapterCall* c)
     g.up_ld = 2 * d->ld_up;
     g.up_mat = 2 * d->stride_up;
     c->rest = g;
+    c->each = false;
     c->plan = plan_for<ADAPT>(d->dtype, g, c->cus, &st);
+    if (c->adapted && d->rank <= 64 && g.up_ld < 2 * kRingPitch) {   // large tiles, of one request each
+        int each_st = GEMM_F16_NT_OK;
+        const Plan each = plan_for<EACH>(d->dtype, g, c->cus, &each_st);
+        if (each_st == GEMM_F16_NT_OK && (st != GEMM_F16_NT_OK || each.us < c->plan.us)) {
+            st = GEMM_F16_NT_OK;
+            c->each = true;
+            c->plan = each;
+            c->rest.rank = d->rank;
+            // rows of 64, zeros behind the rank
+            c->low.cols = 64;
+            c->low.d_ld = 128;
+            c->low_bytes = 128 * d->rows;
+            c->low_plan = plan_for<LOW>(d->dtype, c->low, c->cus, &st);
+            parts = c->low_plan.part_bytes;
+        }
+    }
     if (st != GEMM_F16_NT_OK) return st;
     const int64_t blocks = d->requests * ceil_div(d->rank, 16);
     if (c->adapted && d->rows <= 16 && blocks <= 3) {
@@ -1179,7 +1218,7 @@ int adapter_nt(const adapter_desc* d, void* workspace, int64_t workspace_bytes, 
         if ((st = run<LOW>(c.low_plan, c.low, parts, c.cus, (hipStream_t)stream)) != GEMM_F16_NT_OK) return st;
     }
     c.rest.low = (const char*)workspace;
-    return run<ADAPT>(c.plan, c.rest, parts, c.cus, (hipStream_t)stream);
+    return c.each ? run<EACH>(c.plan, c.rest, parts, c.cus, (hipStream_t)stream) : run<ADAPT>(c.plan, c.rest, parts, c.cus, (hipStream_t)stream);
 }
 
 }  // extern "C"

@@ -95,6 +95,8 @@ struct RingStore {
     [so0] "v"(out.so[0]), [so1] "v"(out.so[1]), [so2] "v"(out.so[2]), [so3] "v"(out.so[3]), [sw] "v"(out.sw)
 #define G16_GROUPED_A_ROWS [ra0] "v"(a.r[0]), [ra1] "v"(a.r[1]), [hm0] "v"(hm[0]), [hm1] "v"(hm[1])
 #define G16_GROUPED_B_ROWS [rb0] "v"(b.r[0]), [rb1] "v"(b.r[1])
+#define G16_GROUPED_EXT \
+    [ext] "s"(ext), [rsa0] "s"(rsa0), [rsb0] "s"(rsb0), [ha0] "v"(ha[0]), [ha1] "v"(ha[1]), [hb0] "v"(hb[0]), [hb1] "v"(hb[1]), [sb8] "s"(sb8)
 #define G16_GROUPED_A_COLS \
     [ra0] "v"(a.r[0]), [ra1] "v"(a.r[1]), [ra2] "v"(a.r[2]), [ra3] "v"(a.r[3]), [ra4] "v"(a.r[4]), [ra5] "v"(a.r[5]), [ra6] "v"(a.r[6]), \
     [ra7] "v"(a.r[7]), [sta] "s"(sta)

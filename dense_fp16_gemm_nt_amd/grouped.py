@@ -196,7 +196,7 @@ def grouped_product(A, B, cu, *, D=None, workspace=None):
     grouped_product_workspace(...) bytes, 16-byte aligned; allocated here when
     not given."""
     if D is None and A.dim() == 2 and B.dim() == 3:   # other tensors are refused below
-        D = A.new_empty((A.shape[0], B.shape[1]))
+        D = A.new_empty(A.shape[0], B.shape[1])
     _run("grouped_nt", *_product_desc(A, B, cu, D), workspace)
     return D
 
@@ -224,7 +224,7 @@ def grouped_product_grad_input(G, B, cu, *, dA=None, workspace=None):
     (rows, K); rows of no group are left as they were in a given dA.
     `workspace` as for grouped_product."""
     if dA is None and G.dim() == 2 and B.dim() == 3:   # other tensors are refused below
-        dA = G.new_empty((G.shape[0], B.shape[2]))
+        dA = G.new_empty(G.shape[0], B.shape[2])
     _run("grouped_nn", *_grad_input_desc(G, B, cu, dA), workspace)
     return dA
 
@@ -259,7 +259,7 @@ def grouped_product_grad_weight(G, A, cu, *, dB=None, dtype=None, workspace=None
     if dtype is None:
         dtype = G.dtype if dB is None else dB.dtype
     if dB is None and G.dim() == 2 and A.dim() == 2 and dtype in (G.dtype, (_torch or _module()).float32):   # others are refused below
-        dB = G.new_empty((_groups(cu), G.shape[1], A.shape[1]), dtype=dtype)
+        dB = G.new_empty(_groups(cu), G.shape[1], A.shape[1], dtype=dtype)
     _run("grouped_tn", *_grad_weight_desc(G, A, cu, dB, dtype), workspace)
     return dB
 
@@ -304,7 +304,7 @@ def adapter_product(A, B, down, up, cu, adapters, scales=None, *, D=None, worksp
     tensor of at least adapter_product_workspace(...) bytes, 16-byte aligned;
     allocated here when not given."""
     if D is None and A.dim() == 2 and B.dim() == 2:   # other tensors are refused below
-        D = A.new_empty((A.shape[0], B.shape[0]))
+        D = A.new_empty(A.shape[0], B.shape[0])
     _run("adapter_nt", *_adapter_desc(A, B, down, up, cu, adapters, scales, D), workspace)
     return D
 

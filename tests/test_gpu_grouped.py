@@ -177,6 +177,9 @@ ADAPTERS = [
     ([3, 0, 40, 1, 1, 0, 0, 17], [1, 0, 2, 2, -1, 9, 1, 0], 520, 520, 128),
     ([200, 1, 0, 77, 400], [0, 1, 2, -5, 3], 264, 136, 64),
     ([1500, 300, 1, 2, 700], [3, 3, 0, 1, 2], 4104, 200, 40),
+    ([2100, 0, 900, 3, 1500], [1, 0, -1, 2, 3], 4104, 1032, 64),   # large tiles of one request each
+    ([4352], [2], 4104, 2056, 24),                                 # and of a small last round, in parts
+    ([257, 4000, 255], [2, 3, 0], 4096, 2048, 8),
 ]
 
 

@@ -43,8 +43,8 @@ MFMA = re.compile(r"v_mfma_f32_16x16x32_@T@ a\[(\d+):\d+\], v\[(\d+):\d+\], v\[(
 
 
 class Sim:
-    def __init__(self, text, la, lb, wide, kt):
-        self.lines, self.kt, self.wide = text.split("\n"), kt, wide
+    def __init__(self, text, la, lb, wide, kt, ext=0):
+        self.lines, self.kt, self.wide, self.ext = text.split("\n"), kt, wide, ext
         self.layout = {"a": la, "b": lb}
         self.labels = {}
         for i, ln in enumerate(self.lines):
@@ -96,6 +96,22 @@ class Sim:
                 scc = int(rem == int(m.group(1)))
             elif ln == "s_cmp_eq_u32 %[wide], 0":
                 scc = int(not self.wide)
+            elif ln == "s_cmp_eq_u32 %[ext], 0":
+                scc = int(not self.ext)
+            elif m := re.match(r"s_mov_b32 %\[kha\], (\d+)$", ln):
+                s["far"] = int(m.group(1))
+            elif m := re.match(r"s_mul_i32 %\[khb\], %\[sb8\], (\d)$", ln):
+                s["rows8"] = int(m.group(1))
+            elif m := re.match(r"buffer_load_dwordx4 %\[h([ab])([01])\], %\[rs([ab])0\], %\[kh([ab])\] offen(?: offset:(\d+))? lds$", ln):
+                op, odd, imm = m.group(1), int(m.group(2)), int(m.group(5) or 0)
+                assert op == m.group(3) == m.group(4) and m0 is not None and pc - m0[1] > 1
+                q, rest = divmod(m0[0] + imm - (65536 if op == "b" else 0), 1024)
+                assert rest == 0 and 0 <= q < 8 and q % 2 == odd
+                assert s["far"] + imm == 1024 * q if op == "a" else s["rows8"] == q and imm == 0   # rows 8 q further on
+                assert (op, 0, q) not in loaded
+                loaded.add((op, 0, q))
+                content[op, 0, q] = (0, "flight")
+                vm.append(("load", (op, 0, q)))
             elif ln.startswith("s_cbranch_scc1 "):
                 if scc:
                     pc = self.target(ln.split()[1], pc)
@@ -135,9 +151,10 @@ class Sim:
                 at -= 65536 if op == "b" else 0
                 stage, at = divmod(at + imm, 32768)
                 assert stage in (0, 1) and at == 1024 * q
-                step = s[kreg + op]
+                first = s[kreg + op] == 0
+                step = s[kreg + op] + self.ext
                 assert step < kt and step % 2 == stage, "a step behind the last, or in the wrong stage"
-                assert (r is None) == (step == 0 and self.layout["a"] == "r"), "step 0 alone goes by masked offsets"
+                assert (r is None) == (first and self.layout["a"] == "r"), "the first step alone goes by masked offsets"
                 assert (op, step, q) not in loaded
                 loaded.add((op, step, q))
                 assert (op, stage) not in unread, "a load into a stage that is still read"
@@ -220,10 +237,13 @@ class Sim:
 
 @pytest.mark.parametrize("name", sorted(GEN.LOOPS))
 @pytest.mark.parametrize("wide", [False, True])
+@pytest.mark.parametrize("ext", [0, 1])
 @pytest.mark.parametrize("kt", [2, 3, 4, 5, 6, 7, 12, 33])
-def test_loop(name, wide, kt):
+def test_loop(name, kt, ext, wide):
+    if ext and name != "G16_GROUPED_RR":
+        pytest.skip("this loop has no such step")
     la, lb, p = GEN.LOOPS[name]
-    r = Sim(GEN.generate(la, lb, p), la, lb, wide, kt).run()
+    r = Sim(GEN.generate(la, lb, p), la, lb, wide, kt, ext).run()
     assert r["loaded"] == {(op, s, q) for op in "ab" for s in range(kt) for q in range(8)}
     assert r["done"] == {b: 2 * kt for b in range(64)}
     assert r["read"] == set(range(256))
