@@ -179,14 +179,14 @@ __device__ __forceinline__ uint32_t all_tiles(const Args& g, Groups<BM, MODE>& g
 
 // A workgroup's tile and part; `slot` is the place of its sums among the parts'.
 template <int BM, int BN, int MODE, bool SPLIT>
-__device__ __forceinline__ Work find_work(const Args& g, uint32_t* part, uint32_t* slot)
+__device__ __forceinline__ Work find_work(const Args& g, uint32_t index, uint32_t* part, uint32_t* slot)
 {
     Groups<BM, MODE> groups;
     const uint32_t all = all_tiles<BM, MODE>(g, groups);
     uint32_t t;
     *part = 0;
     if (MODE == TN) {
-        uint32_t i = blockIdx.x;
+        uint32_t i = index;
         if (SPLIT) {
             const uint32_t launch = g.per_group.d * (uint32_t)g.groups;
             *part = i / launch;
@@ -200,9 +200,9 @@ __device__ __forceinline__ Work find_work(const Args& g, uint32_t* part, uint32_
         t += e * g.group_tiles;
     } else {
         const uint32_t n = SPLIT ? all * g.splits.d : all;
-        if (blockIdx.x >= n) return Work{0, 0, 0, 0, 0, false};
+        if (index >= n) return Work{0, 0, 0, 0, 0, false};
         // each XCD has a run of neighbouring tiles, whose rows and columns its L2 holds
-        t = (uint32_t)xcd_slot(blockIdx.x, n);
+        t = (uint32_t)xcd_slot(index, n);
         if (SPLIT) {
             *part = t / all;
             t -= *part * all;
@@ -297,13 +297,15 @@ __device__ __forceinline__ void load_requests(const Args& g, const Work& wk, con
 }
 
 // SPLIT: sums of a part of the contraction, in fp32, for the launch that joins them.
+template <class C, int MODE>
+constexpr int kTileLds = C::LDS + (MODE == ADAPT ? C::BM * (int)sizeof(Entry) + 16 : 0);
+
 template <typename T, class C, int MODE, bool F32, bool SPLIT>
-__global__ __launch_bounds__(C::THREADS, C::PER_CU * C::WAVES / 4) void tile_kernel(const Args g)
+__device__ __forceinline__ void tile_body(const Args& g, char* smem, uint32_t index)
 {
     constexpr bool XC = MODE == TN, YC = MODE == NN || MODE == TN;
-    __shared__ __attribute__((aligned(1024))) char smem[C::LDS + (MODE == ADAPT ? C::BM * sizeof(Entry) + 16 : 0)];
     uint32_t part, slot;
-    const Work wk = find_work<C::BM, C::BN, MODE, SPLIT>(g, &part, &slot);
+    const Work wk = find_work<C::BM, C::BN, MODE, SPLIT>(g, index, &part, &slot);
     if (!wk.found) return;
     const int tid = threadIdx.x, lane = tid & 63;
     const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -366,7 +368,7 @@ __global__ __launch_bounds__(C::THREADS, C::PER_CU * C::WAVES / 4) void tile_ker
             load();
         }
     };
-    if (MODE == ADAPT && (!SPLIT || part + 1 == g.splits.d)) {   // the requests go with the last part
+    if (MODE == ADAPT && g.adapters > 0 && (!SPLIT || part + 1 == g.splits.d)) {   // the requests go with the last part
         const int own = steps < C::STAGES - 1 ? steps : C::STAGES - 1;
         for (int s = 0; s < own; ++s) load();
         int* count = reinterpret_cast<int*>(table + C::BM);
@@ -544,6 +546,133 @@ __global__ __launch_bounds__(256, 1) void single_kernel(const Args g)
     using O = Cfg<16, 16, 512, 1, 1, 4, 4, 1>;
     Acc<O> out = {{d}};
     grp::store<T, O, false>(smem + 3 * FN * 4096, g.d + (int64_t)row0 * g.d_ld + 2 * (int64_t)col0, g.d_ld, rows, g.cols - col0, 1.f, out, lane);
+}
+
+template <typename T, class C, int MODE, bool F32, bool SPLIT>
+__global__ __launch_bounds__(C::THREADS, C::PER_CU * C::WAVES / 4) void tile_kernel(const Args g)
+{
+    __shared__ __attribute__((aligned(1024))) char smem[kTileLds<C, MODE>];
+    tile_body<T, C, MODE, F32, SPLIT>(g, smem, blockIdx.x);
+}
+
+// Up to 64 rows: the projections onto the rank, by the first workgroups, beside
+// the shared product, which waits for bytes; both leave their sums in fp32, and
+// the next launch puts them together.
+struct PairArgs {
+    Args low, base;
+    uint32_t low_wgs;
+};
+
+template <typename T, class L, class C>
+__global__ __launch_bounds__(256, 2) void pair_kernel(const PairArgs p)
+{
+    static_assert(L::THREADS == 256 && C::THREADS == 256, "one launch");
+    __shared__ __attribute__((aligned(1024))) char smem[kTileLds<C, ADAPT> > kTileLds<L, LOW> ? kTileLds<C, ADAPT> : kTileLds<L, LOW>];
+    if (blockIdx.x < p.low_wgs)
+        tile_body<T, L, LOW, true, false>(p.low, smem, blockIdx.x);
+    else
+        tile_body<T, C, ADAPT, false, true>(p.base, smem, blockIdx.x - p.low_wgs);
+}
+
+// Sum over groups of L neighbouring lanes, by the lanes' own data paths.
+template <int L>
+__device__ __forceinline__ float sum_lanes(float x)
+{
+    auto add = [&](auto ctrl) {
+        const int y = __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), decltype(ctrl)::value, 0xf, 0xf, false);
+        x += __builtin_bit_cast(float, y);
+    };
+    using std::integral_constant;
+    if constexpr (L > 1) add(integral_constant<int, 0xb1>());    // lane ^ 1
+    if constexpr (L > 2) add(integral_constant<int, 0x4e>());    // lane ^ 2
+    if constexpr (L > 4) add(integral_constant<int, 0x141>());   // 7 - lane within 8: the other four
+    if constexpr (L > 8) add(integral_constant<int, 0x140>());   // 15 - lane within 16: the other eight
+    return x;
+}
+
+// A row and 512 columns for a workgroup: the shared product's parts, which lie
+// in one row of tiles, and the second product of the row's adapter, a dot
+// product of `rank` for each column, in fp32.  L lanes, 8 ranks each, have a
+// column, so that a load covers whole rows of `up` (with a lane to a column
+// those of rank 64 took 3 times as long).  What bounds it is the bytes of `up`,
+// read once for each row of its request.
+template <typename T, int L>
+__global__ __launch_bounds__(256) void finish_kernel(const Args g, const int bm, const int bn)
+{
+    __shared__ float dots[512];
+    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, c0 = (int)blockIdx.x * 512 + 128 * w;
+    const int row0 = clampi(g.cu[0], 0, g.rows), r = (int)blockIdx.y, row = row0 + r;
+    if (row >= clampi(g.cu[g.groups], row0, g.rows)) return;
+    int id = -1;   // the adapter of the row's request
+    for (int base = 0; base < g.groups; base += 64) {
+        const int b = base + lane;
+        const uint64_t mine = __builtin_amdgcn_ballot_w64(b < g.groups && g.cu[b] <= row && row < g.cu[b + 1]);
+        if (mine != 0) {
+            id = g.ids[base + __builtin_ctzll(mine)];
+            break;
+        }
+    }
+    const bool adapted = (uint32_t)id < (uint32_t)g.adapters;
+    if (adapted) {
+        const int chunk = lane % L, first = c0 + lane / L;
+        const bool there = chunk < (int)g.rank_chunks.d;
+        f32x4 h0 = {0.f, 0.f, 0.f, 0.f}, h1 = h0;
+        if (there) {
+            const f32x4* h = reinterpret_cast<const f32x4*>(g.low) + ((int64_t)row * g.rank_chunks.d + chunk) * 2;
+            h0 = h[0];
+            h1 = h[1];
+        }
+        // chunks that are not there are read as ones that are and cleared, so
+        // that all loads are in flight together
+        const char* up = g.up + (int64_t)id * g.up_mat + (there ? 16 * chunk : 0);
+        const uint32_t keep = there ? 0xffffffffu : 0u;
+        constexpr int N = 2 * L < 8 ? 2 * L : 8;
+        for (int base = 0; base < 2 * L; base += N) {
+            u32x4 a[N];
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const int c = first + (base + i) * (64 / L);
+                a[i] = *reinterpret_cast<const u32x4*>(up + (int64_t)(c < g.cols ? c : g.cols - 1) * g.up_ld);
+            }
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                float x = 0.f;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const attn::f32x2 u = T::unpack(a[i][j] & keep);
+                    x = __builtin_fmaf(j < 2 ? h0[2 * j] : h1[2 * j - 4], u[0], x);
+                    x = __builtin_fmaf(j < 2 ? h0[2 * j + 1] : h1[2 * j - 3], u[1], x);
+                }
+                x = sum_lanes<L>(x);
+                if (chunk == 0) dots[128 * w + (base + i) * (64 / L) + lane / L] = x;
+            }
+        }
+    }
+    const int c = c0 + 2 * lane;
+    if (c >= g.cols) return;
+    const uint32_t tile = (uint32_t)c / (uint32_t)bn;
+    const float* at = g.parts + ((int64_t)tile * bm + r) * bn + (c - (int)tile * bn);
+    float x = 0.f, y = 0.f;
+    for (uint32_t p = 0; p < g.splits.d; ++p, at += (int64_t)g.col_tiles.d * bm * bn) {
+        const attn::f32x2 v = *reinterpret_cast<const attn::f32x2*>(at);
+        x += v[0];
+        y += v[1];
+    }
+    if (adapted) {   // a wave's own values
+        x += dots[128 * w + 2 * lane];
+        y += dots[128 * w + 2 * lane + 1];
+    }
+    *reinterpret_cast<uint32_t*>(g.d + (int64_t)row * g.d_ld + 2 * (int64_t)c) = T::pack(x, y);
+}
+
+template <typename T>
+const void* finish(int64_t rank)
+{
+    return rank <= 8    ? (const void*)&finish_kernel<T, 1>
+           : rank <= 16 ? (const void*)&finish_kernel<T, 2>
+           : rank <= 32 ? (const void*)&finish_kernel<T, 4>
+           : rank <= 64 ? (const void*)&finish_kernel<T, 8>
+                        : (const void*)&finish_kernel<T, 16>;
 }
 
 // Eight columns of a row: the parts' sums added up in order, scaled, rounded once.
@@ -777,6 +906,8 @@ constexpr int64_t kMaxTiles = int64_t(1) << 22;       // workgroups of a launch,
 using Tiny = Cfg<16, 16, 512, 1, 1, 4, 4, 1>;
 using Small = Cfg<32, 32, 256, 1, 1, 4, 4, 1>;
 using Flat = Cfg<32, 128, 64, 1, 4, 1, 4, 2>;
+using Tiny2 = Cfg<16, 16, 256, 1, 1, 4, 4, 2>;    // two for a compute unit, of projections beside shared products
+using Small2 = Cfg<32, 32, 128, 1, 1, 4, 4, 2>;
 using Square = Cfg<64, 64, 64, 2, 2, 1, 4, 2>;
 using Oblong = Cfg<64, 128, 64, 2, 2, 1, 3, 2>;
 using Middle = Cfg<128, 128, 64, 2, 2, 1, 2, 2>;
@@ -900,8 +1031,13 @@ Plan plan(const Form* forms, int n, const Args& g, int cus, int* status)
             continue;
         }
         const double slots = (double)cus * f.per_cu;
+        double length = depth;
+        if (MODE == ADAPT && g.adapters > 0) {   // a tile's requests, `rank` of the contraction each, at half the speed
+            const double requests = g.groups < g.rows ? g.groups : g.rows, mean = g.rows / requests, mine = f.bm / mean + 1;
+            length += 16. * g.rank_chunks.d * (mine < requests ? mine : requests) + 256;
+        }
         for (int64_t s = 1; s <= (f.split == nullptr ? 1 : kMaxSplits); s += s < 4 ? 1 : s / 2) {
-            const int64_t steps = ceil_div((int64_t)depth, f.bk * s);
+            const int64_t steps = ceil_div((int64_t)length, f.bk * s);
             if (s > 1 && (steps < 4 || most * s > kMaxTiles)) break;
             const double d = (double)(steps * f.bk) / 1024, wgs = tiles * s;
             const double full = (double)(int64_t)(wgs / slots), rest = wgs - full * slots;
@@ -1081,16 +1217,88 @@ struct AdapterCall {
     Plan low_plan, plan;
     bool adapted, each;
     const void* single;   // all in one launch
+    const void* pair;     // projections and shared product in one
+    int bm, bn;           // and its tiles
+    int64_t low_wgs;
     int cus;
     int64_t low_bytes, bytes;   // of the projections, and of all of the workspace
 };
+
+// The pair of launches for up to 64 rows, where the model finds it faster.
+void plan_pair(const adapter_desc* d, AdapterCall* c, int64_t* parts)
+{
+    const int bm = d->rows <= 16 ? 16 : d->rows <= 32 ? 32 : 64, bk = bm == 16 ? 256 : bm == 32 ? 128 : 64;
+    const double one = bm == 16 ? 1.6 : bm == 32 ? 2.4 : 5.0, two = bm == 16 ? 2.6 : bm == 32 ? 3.9 : 6.4;
+    const int64_t ct = ceil_div(d->N, bm), used = d->requests < d->rows ? d->requests : d->rows;
+    const int64_t low_wgs = (d->rows + used * 15) / 16 * ceil_div(d->rank, 16);
+    if (low_wgs > 2 * c->cus) return;
+    double best = 1e300;
+    int64_t splits = 1;
+    for (int64_t s = 1; s <= 8; s *= 2) {
+        const int64_t steps = ceil_div(d->K, bk * s), wgs = ct * s + low_wgs;
+        if (s > 1 && steps < 4) break;
+        const double depth = (double)(steps * bk) / 1024;
+        const int64_t full = wgs / (2 * c->cus), rest = wgs % (2 * c->cus);
+        double us = 1.5 + full * (2.3 + two * depth) + (rest > c->cus ? 2.3 + two * depth : rest > 0 ? 2.3 + one * depth : 0);
+        const double low = 1.5 + 2.3 + 1.8 * (double)d->K / 1024, memory = 3 + (double)d->N * d->K * 2 / 5.5e6;
+        if (us < low) us = low;
+        if (us < memory) us = memory;
+        us += (double)ct * s * bm * bm * 8 / 8e6;
+        if (us < best) {
+            best = us;
+            splits = s;
+        }
+    }
+    best += 4 + (double)d->rows * d->N * d->rank * 2 / 1e7;   // rows of `up` come from L2 more often than from memory
+    if (best >= c->plan.us + c->low_plan.us + 2) return;
+    const bool f16 = d->dtype == GROUPED_F16;
+    if (bm == 16)
+        c->pair = f16 ? (const void*)&pair_kernel<F16, Tiny2, Tiny2> : (const void*)&pair_kernel<BF16, Tiny2, Tiny2>;
+    else if (bm == 32)
+        c->pair = f16 ? (const void*)&pair_kernel<F16, Tiny2, Small2> : (const void*)&pair_kernel<BF16, Tiny2, Small2>;
+    else
+        c->pair = f16 ? (const void*)&pair_kernel<F16, Tiny2, Square> : (const void*)&pair_kernel<BF16, Tiny2, Square>;
+    c->bm = c->bn = bm;
+    c->low_wgs = low_wgs;
+    c->plan.splits = splits;
+    c->plan.wgs = ct * splits;
+    c->low.d_ld = 4 * d->rank;
+    c->low.cols = c->low.low_rows = d->rank;
+    c->low.col_tiles = attn::div_by(ceil_div(d->rank, 16));
+    c->rest.col_tiles = attn::div_by(ct);
+    c->rest.splits = attn::div_by(splits);
+    c->low_bytes = ceil_div(4 * d->rows * d->rank, 256) * 256;
+    *parts = ct * splits * bm * bm * 4;
+}
+
+int run_pair(const AdapterCall& c, int dtype, int64_t rows, void* workspace, hipStream_t s)
+{
+    PairArgs p;
+    p.low = c.low;
+    p.low.d = (char*)workspace;
+    p.base = c.rest;
+    p.base.adapters = 0;   // none in this launch
+    p.base.parts = (float*)((char*)workspace + c.low_bytes);
+    p.low_wgs = (uint32_t)c.low_wgs;
+    int st = launch(c.pair, c.low_wgs + c.plan.wgs, 256, &p, s);
+    if (st != GEMM_F16_NT_OK) return st;
+    Args g = p.base;
+    g.adapters = c.rest.adapters;
+    g.low = (const char*)workspace;
+    int bm = c.bm, bn = c.bn;
+    void* a[] = {&g, &bm, &bn};
+    const int64_t rank = 8 * (int64_t)g.rank_chunks.d;
+    const void* f = dtype == GROUPED_F16 ? finish<F16>(rank) : finish<BF16>(rank);
+    const dim3 grid((unsigned)ceil_div(g.cols, 512), (unsigned)rows);
+    return hipLaunchKernel(f, grid, dim3(256), a, 0, s) == hipSuccess ? GEMM_F16_NT_OK : GEMM_F16_NT_LAUNCH;
+}
 
 int plan_adapters(const adapter_desc* d, AdapterCall* c)
 {
     int st = device_cus(&c->cus);
     if (st != GEMM_F16_NT_OK) return st;
     c->adapted = d->adapters > 0 && d->rank > 0;
-    c->single = nullptr;
+    c->single = c->pair = nullptr;
     Args g = {};
     g.x = (const char*)d->A;
     g.cu = d->cu;
@@ -1164,7 +1372,8 @@ int plan_adapters(const adapter_desc* d, AdapterCall* c)
             return GEMM_F16_NT_OK;
         }
     }
-    if (c->plan.part_bytes > parts) parts = c->plan.part_bytes;
+    if (c->adapted && d->rows <= 64) plan_pair(d, c, &parts);
+    if (c->pair == nullptr && c->plan.part_bytes > parts) parts = c->plan.part_bytes;
     c->bytes = c->low_bytes + parts;
     return GEMM_F16_NT_OK;
 }
@@ -1212,6 +1421,7 @@ int adapter_nt(const adapter_desc* d, void* workspace, int64_t workspace_bytes, 
     if ((st = check_workspace(workspace, workspace_bytes, c.bytes)) != GEMM_F16_NT_OK) return st;
     if ((st = check_adapters(d, {workspace, c.bytes})) != GEMM_F16_NT_OK) return st;
     if (c.single != nullptr) return launch(c.single, ceil_div(c.rest.cols, 16), 256, &c.rest, (hipStream_t)stream);
+    if (c.pair != nullptr) return run_pair(c, d->dtype, d->rows, workspace, (hipStream_t)stream);
     char* parts = (char*)workspace + c.low_bytes;
     if (c.adapted) {
         c.low.d = (char*)workspace;

@@ -171,6 +171,10 @@ ADAPTERS = [
     ([0], [1], 64, 64, 8),
     ([2, 0, 5, 1, 1, 0, 3], [1, 0, -1, 3, 7, 2, 0], 72, 264, 16),
     ([1, 1], [2, 2], 520, 1024, 40),
+    ([1] * 7 + [0, 5], [0, 1, 2, 3, -1, 9, 3, 1, 2], 2056, 4096, 16),   # up to 16, 32 and 64 rows
+    ([20, 1, 3], [3, -1, 1], 1032, 2056, 128),
+    ([1] * 64, [b % 4 for b in range(64)], 4104, 520, 24),
+    ([64], [2], 72, 8200, 64),
     ([17], [2], 136, 520, 40),
     ([1] * 40, [b % 7 - 1 for b in range(40)], 136, 264, 16),
     ([1] * 130, [b % 3 for b in range(130)], 264, 128, 24),
