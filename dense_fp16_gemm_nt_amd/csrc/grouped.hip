@@ -44,6 +44,7 @@ struct Args {
     Div col_tiles;
     Div per_group;       // TN: tiles of a group, padded to whole rounds of the XCDs
     uint32_t group_tiles;
+    uint32_t row_tiles;  // of all groups, at most
     Div splits;          // parts of the contraction, whose sums a second launch joins
     float* parts;
     uint32_t walkers;    // workgroups of the launch of large tiles
@@ -127,6 +128,9 @@ struct Groups {
             look(g, base + lane, groups);
             total += (uint32_t)__builtin_amdgcn_readlane((int)upto, 63);
         }
+        // a table that decreases can name rows more than once: no more tiles
+        // than the launch and the room for parts were made for
+        if (total > g.row_tiles) total = g.row_tiles;
     }
     // Tile t of `total`.
     __device__ __forceinline__ Work find(const Args& g, uint32_t t)
@@ -1070,6 +1074,8 @@ int run(const Plan& p, const Args& args, void* parts, int cus, hipStream_t s)
     g.splits = attn::div_by(p.splits);
     g.parts = p.part_bytes > 0 ? (float*)parts : nullptr;
     g.walkers = (uint32_t)p.wgs;
+    const int64_t used = MODE == ADAPT ? 1 : g.groups < g.rows ? g.groups : g.rows;   // groups with rows
+    g.row_tiles = (uint32_t)((g.rows + used * (f.bm - 1)) / f.bm);
     if (MODE == TN) {
         const int64_t t = ct * ceil_div(g.x_cols, f.bm);
         g.group_tiles = (uint32_t)t;
@@ -1265,6 +1271,8 @@ void plan_pair(const adapter_desc* d, AdapterCall* c, int64_t* parts)
     c->low.d_ld = 4 * d->rank;
     c->low.cols = c->low.low_rows = d->rank;
     c->low.col_tiles = attn::div_by(ceil_div(d->rank, 16));
+    c->low.row_tiles = (uint32_t)((d->rows + used * 15) / 16);
+    c->rest.row_tiles = 1;
     c->rest.col_tiles = attn::div_by(ct);
     c->rest.splits = attn::div_by(splits);
     c->low_bytes = ceil_div(4 * d->rows * d->rank, 256) * 256;

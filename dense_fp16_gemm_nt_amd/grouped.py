@@ -85,7 +85,7 @@ def _first(name, X, dims):
 def _rows(name, X, shape, dtype, device):
     """Elements from a row to the next of a 2-D tensor that has to have this shape and type."""
     st = X.stride()
-    if X.shape == shape and st[1] == 1 and st[0] >= shape[1] and shape[0] > 1 and X.dtype is dtype and X.device == device:
+    if X.shape == shape and st[1] == 1 and st[0] >= shape[1] > 0 and shape[0] > 1 and X.dtype is dtype and X.device == device:
         return st[0]
     return _explain(name, X, shape, dtype, device)[-1]
 
@@ -93,7 +93,7 @@ def _rows(name, X, shape, dtype, device):
 def _matrices(name, X, shape, dtype, device):
     """Elements from a row to the next, and from a matrix to the next, of a 3-D tensor that has to have this shape and type."""
     st = X.stride()
-    if X.shape == shape and st[2] == 1 and st[1] >= shape[2] and shape[1] > 1 and shape[0] > 1 and X.dtype is dtype and X.device == device:
+    if X.shape == shape and st[2] == 1 and st[1] >= shape[2] > 0 and shape[1] > 1 and shape[0] > 1 and X.dtype is dtype and X.device == device:
         return st[1], st[0]
     between, ld = _explain(name, X, shape, dtype, device)
     return ld, between

@@ -197,3 +197,18 @@ def test_null_descriptors():
         assert getattr(L, name)(None, None, 0, None) == INVALID and getattr(L, name + "_check")(None) == INVALID
     assert L.adapter_nt(None, None, 0, None) == INVALID and L.adapter_nt_check(None) == INVALID
     assert L.adapter_nt_workspace(None) == INVALID
+
+
+def test_host_tensors_are_refused():
+    torch = pytest.importorskip("torch")
+    t = torch.float16
+    A, B, G, cu = torch.zeros(4, 16, dtype=t), torch.zeros(2, 8, 16, dtype=t), torch.zeros(4, 8, dtype=t), torch.tensor([0, 1, 4], dtype=torch.int32)
+    down, up, ids = torch.zeros(3, 8, 16, dtype=t), torch.zeros(3, 8, 8, dtype=t), torch.zeros(2, dtype=torch.int32)
+    for call in (lambda: g.grouped_product(A, B, cu), lambda: g.grouped_product_grad_input(G, B, cu), lambda: g.grouped_product_grad_weight(G, A, cu),
+                 lambda: g.adapter_product(A, B[0], down, up, cu, ids), lambda: g.grouped_product_workspace(A, B, cu),
+                 lambda: g.grouped_product_grad_input_workspace(G, B, cu), lambda: g.grouped_product_grad_weight_workspace(G, A, cu),
+                 lambda: g.adapter_product_workspace(A, B[0], down, up, cu, ids)):
+        with pytest.raises(ValueError, match="device tensor"):
+            call()
+    with pytest.raises(TypeError):
+        g.grouped_product(A.float(), B, cu)
