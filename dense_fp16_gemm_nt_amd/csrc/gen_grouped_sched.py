@@ -43,6 +43,12 @@ zeros; a side by columns beside it begins that many rows early, and those
 rows' offsets are masked likewise.  With both sides by columns the rows behind
 the last load zeros by themselves: the buffers end there.
 
+From tile to tile: the last step also loads step 0 of the workgroup's next tile,
+from %[rsan] and %[rsbn], into the stage that it does not read, so that the
+next tile's block begins with its step 0 on the way (%[first] is 0 then, and
+%[par] the stage; otherwise a tile loads its own step 0 into stage 0).  Where
+there is no such tile these buffers are empty.
+
 RR can begin with a step of another product, whose operands have rows of their
 own (the second product of a low-rank adapter, up to 64 elements of its
 contraction): where %[ext] is not 0, step 0 is loaded from %[rsa0] (rows of 128
@@ -55,7 +61,8 @@ offset of the load); fragment addresses %[raN], %[rbN] (N: sub-step by rows,
 block by columns); resources %[rsa], %[rsb], %[rsd]; the wave's LDS load base
 %[lb]; the steps' byte offsets %[koa], %[kha], %[kob], %[khb] (next step and
 the one after; the first of each is 0 on entry), advanced by 128 by rows and
-by %[sta], %[stb] by columns; the count %[rem] of steps, at least 2; epilogue
+by %[sta], %[stb] by columns;
+the count %[rem] of steps, at least 2; epilogue
 %[ewJ], %[erQ], %[soQ], or %[sw] with %[wide], %[gstr], scratch %[sdo]; RC:
 %[hk] masked rows and %[kr], the lane's row of its first load.
 """
@@ -81,6 +88,7 @@ class Emitter(ring4.Emitter):
         super().__init__()
         self.layout = {"a": la, "b": lb}
         self.wide = False
+        self.behind: list[int] = []   # stores behind the next tile's loads, for each last step
 
     @staticmethod
     def m0(op: str, q: int, stage: int) -> str:
@@ -129,6 +137,19 @@ class Emitter(ring4.Emitter):
             out.append((f"buffer_store_dwordx4 v[{v}:{v + 3}], %[sw], %[rsd], %[sdo] offen{off}", False))
         out.append(("s_add_u32 %[sdo], %[sdo], %[gstr]", False))
         return out
+
+    def next_load(self, op: str, q: int) -> list[str]:
+        """Load q of the next tile's step 0, with what masks its offset."""
+        layout = self.layout
+        imm = 1024 * (q % 4)
+        off = f" offset:{imm}" if imm else ""
+        load = f"buffer_load_dwordx4 %[ht], %[rs{op}n], 0 offen{off} lds"
+        if layout["a"] == "c":
+            return [load.replace("%[ht]", f"%[{op}x{q}]")]
+        if layout[op] == "r":
+            return [f"v_or_b32 %[ht], %[{op}x{q}], %[hm{q % 2}]", load]
+        return [f"s_sub_i32 %[khb], %[hk], {2 * q}", "v_mov_b32 %[ht], 0x80000000", "v_cmp_le_i32 vcc, %[khb], %[kr]",
+                f"v_cndmask_b32 %[ht], %[ht], %[bx{q}], vcc", load]
 
     def epi_after(self, g: int, per_slot: int, delay: int, t: int) -> None:
         while self.epi_next < NB and g >= 2 * NB * self.epi_next + 2 * NB - 1 + delay:
@@ -215,12 +236,21 @@ def emit_step(e: Emitter, stage: int, first: bool, ahead: bool, has_next: bool, 
             gaps[g].append(("read", (op, h, idx, stage ^ 1, stage ^ 1, part)))
             at = g
         gaps[first_free(g + p["f0_lat"])].append(("text", "s_waitcnt lgkmcnt(0)", "clear"))
+    if last:
+        g = p["nxt_start"]
+        for op, q in LOAD3:
+            lines = ([Emitter.m0(op, q, stage ^ 1)] if q % 4 == 0 else []) + e.next_load(op, q)
+            for k, text in enumerate(lines):   # one to a gap, the load last
+                gaps[g + k].append(("text", text))
+            g += max(p["nxt_every"], len(lines))
+        assert g < ng, "next-tile loads beyond the step"
     texts = [(g, it[1]) for g in range(ng) for it in gaps[g] if it[0] == "text"]
     writers = [g for g, t in texts if t.startswith(("s_add_u32", "s_sub_u32"))]
     compares = [g for g, t in texts if t.startswith("s_cmp")]
-    assert not compares or max(writers, default=-1) < min(compares), "SCC clobbered before the branch"
+    assert last or not compares or max(writers, default=-1) < min(compares), "SCC clobbered before the branch"
 
     t_base = epi_set4(stage)
+    start = len(e.lines)
     for g in range(ng):
         pq, h = divmod(g, 2)
         i, j = mfma_block(pq, "snake")
@@ -238,6 +268,9 @@ def emit_step(e: Emitter, stage: int, first: bool, ahead: bool, has_next: bool, 
                     e.lgkm.clear()
     if last:
         e.epi_rest(t_base)
+        lines = e.lines[start:]
+        at = max(n for n, ln in enumerate(lines) if ln.startswith("buffer_load_dwordx4"))
+        e.behind.append(sum(ln.startswith("buffer_store_dwordx4") for ln in lines[at:]))
         for t in tail:
             e.op(t)
 
@@ -247,13 +280,46 @@ def generate(la: str, lb: str, p: dict) -> str:
     layout = e.layout
     head = {op: "none" if la == "c" else layout[op] for op in "ab"}
 
-    def loads(step: int, masked: bool) -> None:
+    def loads(step: int, masked: bool, stage: int) -> None:
         for op, q in LOAD3:
             if q % 4 == 0:
-                e.op(Emitter.m0(op, q, step))
+                e.op(Emitter.m0(op, q, stage))
                 e.op("s_nop 0")   # M0 write -> LDS-DMA read of M0
             e.op(Emitter.load(op, q, "ko", f"v{head_reg(op, q)}" if masked and head[op] != "none" else None))
 
+    def begin(stage: int, wait: str) -> None:
+        """The loads of step 1, and step 0's fragments from `stage`."""
+        loads(1, False, stage ^ 1)
+        rest(stage, wait)
+
+    def rest(stage: int, wait: str) -> None:
+        for op in "ab":
+            e.op(f"s_add_u32 %[kh{op}], %[ko{op}], {side_steps(op, layout[op])}")
+        e.op(f"s_waitcnt vmcnt({wait})")
+        e.op("s_barrier")
+        e.lgkm = []
+        order = [("a", h, 0) for h in range(KSUB)] + [("b", h, j) for j in range(NB) for h in range(KSUB)]
+        order += [("a", h, i) for i in range(1, NB) for h in range(KSUB)]
+        for op, h, idx in order:
+            for part in e.parts(op):
+                e.read(op, h, idx, stage, stage, part)
+
+    def advance() -> None:
+        for op in "ab":
+            e.op(f"s_add_u32 %[ko{op}], %[ko{op}], {side_steps(op, layout[op])}")
+
+    adv = [f"s_add_u32 %[kh{op}], %[kh{op}], {side_steps(op, layout[op])}" for op in "ab"]
+    sub, cmp2 = "s_sub_u32 %[rem], %[rem], 1", "s_cmp_eq_u32 %[rem], 2"
+
+    def step(stage, first, ahead, has_next, last, tail):
+        pending = list(e.lgkm) if first else []
+        e.lgkm = pending
+        emit_step(e, stage, first, ahead, has_next, last, tail, p)
+
+    e.op("s_cmp_eq_u32 %[first], 0")
+    e.op("s_cbranch_scc1 15f")
+    # this tile's own step 0, behind what the tile before loaded from empty buffers
+    e.op("s_waitcnt vmcnt(@BEHIND@)")
     for op, q in LOAD3:
         if head[op] == "r":
             e.op(f"v_or_b32 v{head_reg(op, q)}, %[{op}x{q}], %[hm{q % 2}]")
@@ -278,40 +344,46 @@ def generate(la: str, lb: str, p: dict) -> str:
             e.op(f"s_add_u32 m0, %[lb], {SIDE_B + 1024 * q}")
             e.op("s_nop 0")
             e.op(f"buffer_load_dwordx4 %[hb{q % 2}], %[rsb0], %[khb] offen lds")
-        loads(1, True)
+        loads(1, True, 1)
         e.op("s_branch 12f")
         e.label("11")
-    loads(0, True)
-    for op in "ab":
-        e.op(f"s_add_u32 %[ko{op}], %[ko{op}], {side_steps(op, layout[op])}")
-    loads(1, False)
+    loads(0, True, 0)
+    advance()
+    loads(1, False, 1)
     if layout == {"a": "r", "b": "r"}:
         e.label("12")
-    for op in "ab":
-        e.op(f"s_add_u32 %[kh{op}], %[ko{op}], {side_steps(op, layout[op])}")
-    e.op(f"s_waitcnt vmcnt({NLOAD})")
-    e.op("s_barrier")
-    order = [("a", h, 0) for h in range(KSUB)] + [("b", h, j) for j in range(NB) for h in range(KSUB)]
-    order += [("a", h, i) for i in range(1, NB) for h in range(KSUB)]
-    for op, h, idx in order:
-        for part in e.parts(op):
-            e.read(op, h, idx, 0, 0, part)
-    pro = list(e.lgkm)
+    rest(0, str(NLOAD))
+    zero = list(e.lgkm)   # the reads under way at label 20, from either side
+    e.op("s_branch 20f")
+    # carried from the tile before: @WAIT@ leaves step 1's loads in flight and
+    # the stores behind the next tile's loads
+    e.label("15")
+    advance()
+    e.op("s_cmp_eq_u32 %[par], 0")
+    e.op("s_cbranch_scc0 16f")
+    begin(0, "@WAIT@")
+    e.op("s_branch 20f")
+    e.label("16")
+    begin(1, "@WAIT@")
+    entry = list(e.lgkm)
+    e.op(cmp2)
+    e.op("s_cbranch_scc1 25f")
+    step(1, True, True, True, False, adv + [sub, cmp2, "s_cbranch_scc1 8f", "s_branch 17f"])
+    e.label("25")
+    e.lgkm = list(entry)
+    step(1, True, False, True, False, [sub, "s_branch 3f"])     # two steps in all
 
-    adv = [f"s_add_u32 %[{k}{op}], %[{k}{op}], {side_steps(op, layout[op])}" for k in ("kh",) for op in "ab"]
-    sub, cmp2 = "s_sub_u32 %[rem], %[rem], 1", "s_cmp_eq_u32 %[rem], 2"
-
-    def step(stage, first, ahead, has_next, last, tail):
-        e.lgkm = list(pro) if first else []
-        emit_step(e, stage, first, ahead, has_next, last, tail, p)
-
+    e.label("20")
+    e.lgkm = list(zero)
     e.op(cmp2)
     e.op("s_cbranch_scc1 5f")
     step(0, True, True, True, False, adv + [sub, cmp2, "s_cbranch_scc1 6f"])
     e.label("1")
     step(1, False, True, True, False, adv + [sub, cmp2, "s_cbranch_scc1 8f"])
+    e.label("17")
     step(0, False, True, True, False, adv + [sub, cmp2, "s_cbranch_scc1 6f", "s_branch 1b"])
     e.label("5")
+    e.lgkm = list(zero)
     step(0, True, False, True, False, [sub, "s_branch 2f"])     # two steps in all
     e.label("6")
     step(1, False, False, True, False, [sub, "s_branch 3f"])    # the step before the last, in stage 1
@@ -327,12 +399,12 @@ def generate(la: str, lb: str, p: dict) -> str:
         e.wide = False
         step(stage, False, False, False, True, ["s_branch 4f"] if stage else [])
     e.label("4")
-    return "\n".join(e.lines)
+    return "\n".join(e.lines).replace("@WAIT@", str(min(63, NLOAD + min(e.behind)))).replace("@BEHIND@", str(min(e.behind)))
 
 
 # Loads of step j + 2 all go out in step j, so that they have the rest of it
 # and the next step up to the publish barrier to land.
-ROWS = {"rel": 12, "load_every": 6, "pub": 64, "a_delay": 1, "read_limit": 112, "f0_lat": 8, "epi_slot": 8, "epi_delay": 2}
+ROWS = {"rel": 12, "load_every": 6, "pub": 64, "a_delay": 1, "read_limit": 112, "f0_lat": 8, "epi_slot": 8, "epi_delay": 2, "nxt_start": 2, "nxt_every": 4}
 MIXED = {**ROWS, "pub": 56}
 COLS = {**ROWS, "rel": 14, "pub": 48}
 

@@ -789,7 +789,16 @@ __global__ __launch_bounds__(256, 1) void ring_kernel(const Args g)
         hb[q] = MODE == EACH && 8 * c < g.rank ? (uint32_t)(r * g.up_ld + 16 * c) : grp::kBeyond;
     }
 
-    for (uint32_t slot = (uint32_t)xcd_slot(blockIdx.x, gridDim.x); slot < items; slot += gridDim.x) {
+    // One tile, or part of one: its operands, scalars all of them.
+    struct Item {
+        bool found;
+        u32x4 rsa, rsb, rsd;
+        uint32_t rem, wide, gstr, hk, ext;   // steps, ..., what the first step lacks, whether the adapter's step is the first
+        Work wk;
+    };
+    auto prepare = [&](uint32_t slot) {
+        Item it = {};
+        if (slot >= items) return it;
         uint32_t t = slot, part = 0;
         if (slot >= walk.full) {
             t = slot - walk.full;
@@ -797,14 +806,15 @@ __global__ __launch_bounds__(256, 1) void ring_kernel(const Args g)
             t = walk.full + t - part * walk.rest;
         }
         Work wk = tile_at<TILE, TILE, MODE>(g, groups, t);
-        uint32_t rem = place_large<MODE>(g, wk);
+        const uint32_t steps = place_large<MODE>(g, wk);
         // the contraction's first step is the partial one: see gen_grouped_sched.py
         int hk = MODE == TN ? 0 : (g.depth + STEP - 1) / STEP * STEP - g.depth;
-        uint32_t ext = MODE == EACH && (int)rem * STEP > g.depth + hk ? 1 : 0;
-        const uint32_t parts = slot < walk.full ? 1 : walk.of(rem);
-        if (part >= parts) continue;
-        const uint32_t first = part * rem / parts;
-        rem = grp::uniform((part + 1) * rem / parts - first);
+        uint32_t ext = MODE == EACH && (int)steps * STEP > g.depth + hk ? 1 : 0;
+        const uint32_t parts = slot < walk.full ? 1 : walk.of(steps);
+        if (part >= parts) return it;   // the last of the workgroup's anyway
+        const uint32_t first = part * steps / parts;
+        it.found = true;
+        it.rem = grp::uniform((part + 1) * steps / parts - first);
 
         const char *x, *y, *d;
         int64_t x_bytes, y_bytes;
@@ -832,24 +842,41 @@ __global__ __launch_bounds__(256, 1) void ring_kernel(const Args g)
             y += dy;
             x_bytes -= dx < x_bytes ? dx : x_bytes;
             y_bytes -= dy < y_bytes ? dy : y_bytes;
-            if (skip > 0) hk = 0;
+            hk = 0;
             ext = 0;
         }
-        uint32_t hm[2];
-#pragma unroll
-        for (int q = 0; q < 2; ++q) hm[q] = 8 * ((lane & 7) ^ grp::RingSide<false>::swz(8 * q + lane / 8)) < hk ? grp::kBeyond : 0u;
-        const uint32_t wide = F32 ? 1u : grp::uniform(parts) - 1u;   // not 0: outputs in 32 bits
         int64_t d_ld = g.d_ld;
         d += (int64_t)(wk.col0 + wn) * (F32 ? 4 : 2);
         if (parts > 1) {
             d_ld = PART_LD;
             d = (const char*)(g.parts + (int64_t)(slot - walk.full) * (TILE * TILE) + wm * TILE + wn);
         }
-        if (F32 && parts > 1) out.sw = (uint32_t)((lane & 15) * PART_LD + 16 * (lane >> 4));   // the last of the workgroup's items
-        const u32x4 rsa = grp::ring_rsrc(x, x_bytes), rsb = grp::ring_rsrc(y, y_bytes);
-        const u32x4 rsd = grp::ring_rsrc(d, rows == 0 ? 0 : (rows - 1) * d_ld + 128 * (F32 || parts > 1 ? 4 : 2));
-        const uint32_t gstr = grp::uniform((uint32_t)(16 * d_ld)), masked = grp::uniform((uint32_t)hk);
-        uint32_t koa = 0, kob = 0, kha, khb, sdo;
+        it.rsa = grp::ring_rsrc(x, x_bytes);
+        it.rsb = grp::ring_rsrc(y, y_bytes);
+        it.rsd = grp::ring_rsrc(d, rows == 0 ? 0 : (rows - 1) * d_ld + 128 * (F32 || parts > 1 ? 4 : 2));
+        it.wide = F32 ? 1u + (parts > 1) : grp::uniform(parts) - 1u;   // not 0: outputs in 32 bits
+        it.gstr = grp::uniform((uint32_t)(16 * d_ld));
+        it.hk = grp::uniform((uint32_t)hk);
+        it.ext = grp::uniform(ext);
+        it.wk = wk;
+        return it;
+    };
+
+    uint32_t slot = (uint32_t)xcd_slot(blockIdx.x, gridDim.x), own = 1, par = 0;   // see gen_grouped_sched.py: first, par
+    Item it = prepare(slot);
+    while (it.found) {
+        slot += gridDim.x;
+        const Item then = prepare(slot);
+        // its step 0 by the same masks, and not an adapter's
+        const bool carry = then.found && then.ext == 0 && then.hk == it.hk;
+        const u32x4 none = {0, 0, 0, 0x00020000u};
+        const u32x4 rsa = it.rsa, rsb = it.rsb, rsd = it.rsd, rsan = carry ? then.rsa : none, rsbn = carry ? then.rsb : none;
+        uint32_t hm[2];
+#pragma unroll
+        for (int q = 0; q < 2; ++q) hm[q] = 8 * ((lane & 7) ^ grp::RingSide<false>::swz(8 * q + lane / 8)) < (int)it.hk ? grp::kBeyond : 0u;
+        if (F32 && it.wide > 1) out.sw = (uint32_t)((lane & 15) * PART_LD + 16 * (lane >> 4));   // a part: the last of the workgroup's items
+        const uint32_t wide = it.wide, gstr = it.gstr, hk = it.hk, first = grp::uniform(own);
+        uint32_t rem = grp::uniform(it.rem), koa = 0, kob = 0, kha, khb, sdo, ht;
 #pragma clang diagnostic push
 #pragma clang diagnostic ignored "-Winline-asm"   // M0 is written inside, on purpose
 #define G16_GROUPED_BLOCK(LOOP, ...) \
@@ -860,21 +887,24 @@ __global__ __launch_bounds__(256, 1) void ring_kernel(const Args g)
         if constexpr (MODE == NT || MODE == EACH) {
             u32x4 rsa0 = rsa, rsb0 = rsb;
             if (MODE == EACH) {
-                const int64_t n = wk.rows < TILE ? wk.rows : TILE;
-                rsa0 = grp::ring_rsrc(g.low + (int64_t)wk.row0 * 128, n * 128);
-                rsb0 = grp::ring_rsrc(g.up + (ext ? (int64_t)g.ids[wk.group] * g.up_mat : 0) + wk.col0 * g.up_ld, (TILE - 1) * g.up_ld + 2 * g.rank);
+                const int64_t n = it.wk.rows < TILE ? it.wk.rows : TILE;
+                rsa0 = grp::ring_rsrc(g.low + (int64_t)it.wk.row0 * 128, n * 128);
+                rsb0 = grp::ring_rsrc(g.up + (it.ext ? (int64_t)g.ids[it.wk.group] * g.up_mat : 0) + it.wk.col0 * g.up_ld, (TILE - 1) * g.up_ld + 2 * g.rank);
             }
-            const uint32_t sb8 = grp::uniform((uint32_t)(8 * g.up_ld));
-            ext = grp::uniform(ext);
+            const uint32_t sb8 = grp::uniform((uint32_t)(8 * g.up_ld)), ext = it.ext;
             G16_GROUPED_BLOCK(G16_GROUPED_RR, G16_GROUPED_A_ROWS, G16_GROUPED_B_ROWS, G16_GROUPED_EXT);
         } else if constexpr (MODE == NN) {
-            G16_GROUPED_BLOCK(G16_GROUPED_RC, G16_GROUPED_A_ROWS, G16_GROUPED_B_COLS, [hk] "s"(masked), [kr] "v"(kr));
+            G16_GROUPED_BLOCK(G16_GROUPED_RC, G16_GROUPED_A_ROWS, G16_GROUPED_B_COLS, [hk] "s"(hk), [kr] "v"(kr));
         } else {
             G16_GROUPED_BLOCK(G16_GROUPED_CC, G16_GROUPED_A_COLS, G16_GROUPED_B_COLS);
         }
 #pragma clang diagnostic pop
         wg_barrier();   // every wave is done reading the ring before the next tile's loads
+        par = grp::uniform(carry ? (par + it.rem) & 1 : 0);
+        own = grp::uniform(carry ? 0 : 1);
+        it = then;
     }
+    attn::landed<0>();   // loads from empty buffers
 }
 
 // Joins what ring_kernel divided; a workgroup takes 2048 elements of a tile at a time.

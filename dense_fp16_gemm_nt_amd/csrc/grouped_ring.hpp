@@ -90,6 +90,7 @@ struct RingStore {
     [ax0] "v"(a.x[0]), [ax1] "v"(a.x[1]), [ax2] "v"(a.x[2]), [ax3] "v"(a.x[3]), [ax4] "v"(a.x[4]), [ax5] "v"(a.x[5]), [ax6] "v"(a.x[6]), \
     [ax7] "v"(a.x[7]), [bx0] "v"(b.x[0]), [bx1] "v"(b.x[1]), [bx2] "v"(b.x[2]), [bx3] "v"(b.x[3]), [bx4] "v"(b.x[4]), [bx5] "v"(b.x[5]), \
     [bx6] "v"(b.x[6]), [bx7] "v"(b.x[7]), [rsa] "s"(rsa), [rsb] "s"(rsb), [rsd] "s"(rsd), [lb] "s"(lb), [gstr] "s"(gstr), [wide] "s"(wide), \
+    [rsan] "s"(rsan), [rsbn] "s"(rsbn), [first] "s"(first), [par] "s"(par), \
     [ew0] "v"(out.ew[0]), [ew1] "v"(out.ew[1]), [ew2] "v"(out.ew[2]), [ew3] "v"(out.ew[3]), [ew4] "v"(out.ew[4]), [ew5] "v"(out.ew[5]), \
     [ew6] "v"(out.ew[6]), [ew7] "v"(out.ew[7]), [er0] "v"(out.er[0]), [er1] "v"(out.er[1]), [er2] "v"(out.er[2]), [er3] "v"(out.er[3]), \
     [so0] "v"(out.so[0]), [so1] "v"(out.so[1]), [so2] "v"(out.so[2]), [so3] "v"(out.so[3]), [sw] "v"(out.sw)
@@ -104,7 +105,8 @@ struct RingStore {
     [rb0] "v"(b.r[0]), [rb1] "v"(b.r[1]), [rb2] "v"(b.r[2]), [rb3] "v"(b.r[3]), [rb4] "v"(b.r[4]), [rb5] "v"(b.r[5]), [rb6] "v"(b.r[6]), \
     [rb7] "v"(b.r[7]), [stb] "s"(stb)
 #define G16_GROUPED_STATE \
-    [koa] "+s"(koa), [kob] "+s"(kob), [kha] "=&s"(kha), [khb] "=&s"(khb), [rem] "+s"(rem), [sdo] "=&s"(sdo)
+    [koa] "+s"(koa), [kob] "+s"(kob), [kha] "=&s"(kha), [khb] "=&s"(khb), [rem] "+s"(rem), [sdo] "=&s"(sdo), \
+    [ht] "=&v"(ht)
 
 #define G16_GROUPED_CLOBBERS \
     "memory", "m0", "scc", "vcc", \

@@ -7,6 +7,7 @@ A simulator runs each loop's control flow for a range of step counts and checks 
 * a fragment read sees a stage whose loads of one step were all waited for (vmcnt) and then published by a barrier;
 * every product takes the fragments of its own step, sub-step and block, whose reads were waited for (lgkmcnt; LDS reads
   complete in order), and a block's products follow each other from zero on;
+* the last step loads the next tile's step 0 into the stage that it does not read, and the next tile begins there;
 * the epilogue reads each accumulator once, long enough after its last product, and stores each row group at its own offset;
 * the committed include is what the generator writes.
 
@@ -43,8 +44,10 @@ MFMA = re.compile(r"v_mfma_f32_16x16x32_@T@ a\[(\d+):\d+\], v\[(\d+):\d+\], v\[(
 
 
 class Sim:
-    def __init__(self, text, la, lb, wide, kt, ext=0):
-        self.lines, self.kt, self.wide, self.ext = text.split("\n"), kt, wide, ext
+    """Runs the loop for tiles of kts[0], kts[1], ... steps, each carried on from the one before where `carry` says so."""
+
+    def __init__(self, text, la, lb, wide, kts, carry, ext=0):
+        self.lines, self.kts, self.wide, self.carry, self.ext = text.split("\n"), kts, wide, carry, ext
         self.layout = {"a": la, "b": lb}
         self.labels = {}
         for i, ln in enumerate(self.lines):
@@ -56,16 +59,31 @@ class Sim:
         return min(x for x in c if x > pc) if ref[-1] == "f" else max(x for x in c if x < pc)
 
     def run(self):
-        kt = self.kt
+        self.vm = []                        # loads and stores in issue order
+        self.content = {}                   # (side, stage, load) -> ((tile, step), "flight" | "landed" | "visible")
+        self.unread = {}                    # (side, stage) -> "open" | "done" (reads since the last barrier, completed or not)
+        self.loaded = set()
+        par, out = 0, []
+        for tile, kt in enumerate(self.kts):
+            carried = tile > 0 and self.carry
+            if not carried:
+                par = 0
+            out.append(self.tile(tile, kt, par, int(not carried)))
+            par = (par + kt) % 2
+            for k, (step, state) in list(self.content.items()):   # the barrier behind a tile
+                if state == "landed":
+                    self.content[k] = (step, "visible")
+            assert all(v == "done" for v in self.unread.values())
+            self.unread.clear()
+        return out
+
+    def tile(self, tile, kt, par, own):
+        vm, content, unread, loaded = self.vm, self.content, self.unread, self.loaded
         s = {"koa": 0, "kob": 0}            # offsets in steps
         rem, scc, m0, sdo = kt, 0, None, None
-        vm = []                             # loads and stores in issue order
-        content = {}                        # (side, stage, load) -> (step, "flight" | "landed" | "visible")
-        loaded = set()
         lgkm = []                           # LDS operations in issue order
-        unread = {}                         # (side, stage) -> "open" | "done" (reads since the last barrier, completed or not)
         frag, half = {}, {}                 # first VGPR -> (side, step, sub-step, block) once complete
-        head = {}
+        head, ht = {}, None
         done = {}                           # accumulator block -> products so far
         final, read_acc, stores, barriers = {}, set(), 0, 0
         clock, pc, steps = 0, 0, 0
@@ -96,6 +114,37 @@ class Sim:
                 scc = int(rem == int(m.group(1)))
             elif ln == "s_cmp_eq_u32 %[wide], 0":
                 scc = int(not self.wide)
+            elif m := re.match(r"s_cmp_eq_u32 %\[(first|par)\], 0$", ln):
+                scc = int((own if m.group(1) == "first" else par) == 0)
+            elif ln.startswith("s_cbranch_scc0 "):
+                if not scc:
+                    pc = self.target(ln.split()[1], pc)
+                    continue
+            elif m := re.match(r"v_or_b32 %\[ht\], %\[([ab])x(\d)\], %\[hm([01])\]$", ln):
+                assert self.layout[m.group(1)] == "r" and int(m.group(3)) == int(m.group(2)) % 2
+                ht = (m.group(1), int(m.group(2)))
+            elif ln == "v_mov_b32 %[ht], 0x80000000":
+                ht = "beyond"
+            elif ln == "v_cmp_le_i32 vcc, %[khb], %[kr]":
+                pass
+            elif m := re.match(r"v_cndmask_b32 %\[ht\], %\[ht\], %\[bx(\d)\], vcc$", ln):
+                assert masked == 2 * int(m.group(1)) and self.layout["b"] == "c" and ht == "beyond"
+                ht = ("b", int(m.group(1)))
+            elif m := re.match(r"buffer_load_dwordx4 (\S+), %\[rs([ab])n\], 0 offen(?: offset:(\d+))? lds$", ln):
+                op, imm = m.group(2), int(m.group(3) or 0)
+                r = re.match(r"%\[([ab])x(\d)\]$", m.group(1))
+                side, q = (r.group(1), int(r.group(2))) if r else ht
+                assert side == op and imm == 1024 * (q % 4) and m0 is not None and pc - m0[1] > 1
+                assert (r is None) == (self.layout["a"] == "r"), "masked where a first step can be partial"
+                stage, at = divmod(m0[0] + imm - (65536 if op == "b" else 0), 32768)
+                assert at == 1024 * q and stage == (par + kt) % 2, "the stage that the last step does not read"
+                assert (op, stage) not in unread and content[op, stage, q][1] != "flight"
+                on = self.carry and tile + 1 < len(self.kts)
+                if on:
+                    assert (tile + 1, op, 0, q) not in loaded
+                    loaded.add((tile + 1, op, 0, q))
+                content[op, stage, q] = ((tile + 1, 0) if on else ("empty", 0), "flight")
+                vm.append(("load", (op, stage, q)))
             elif ln == "s_cmp_eq_u32 %[ext], 0":
                 scc = int(not self.ext)
             elif m := re.match(r"s_mov_b32 %\[kha\], (\d+)$", ln):
@@ -108,9 +157,9 @@ class Sim:
                 q, rest = divmod(m0[0] + imm - (65536 if op == "b" else 0), 1024)
                 assert rest == 0 and 0 <= q < 8 and q % 2 == odd
                 assert s["far"] + imm == 1024 * q if op == "a" else s["rows8"] == q and imm == 0   # rows 8 q further on
-                assert (op, 0, q) not in loaded
-                loaded.add((op, 0, q))
-                content[op, 0, q] = (0, "flight")
+                assert (tile, op, 0, q) not in loaded
+                loaded.add((tile, op, 0, q))
+                content[op, 0, q] = ((tile, 0), "flight")
                 vm.append(("load", (op, 0, q)))
             elif ln.startswith("s_cbranch_scc1 "):
                 if scc:
@@ -153,12 +202,13 @@ class Sim:
                 assert stage in (0, 1) and at == 1024 * q
                 first = s[kreg + op] == 0
                 step = s[kreg + op] + self.ext
-                assert step < kt and step % 2 == stage, "a step behind the last, or in the wrong stage"
+                assert step < kt and (step + par) % 2 == stage, "a step behind the last, or in the wrong stage"
                 assert (r is None) == (first and self.layout["a"] == "r"), "the first step alone goes by masked offsets"
-                assert (op, step, q) not in loaded
-                loaded.add((op, step, q))
+                assert (tile, op, step, q) not in loaded
+                loaded.add((tile, op, step, q))
                 assert (op, stage) not in unread, "a load into a stage that is still read"
-                content[op, stage, q] = (step, "flight")
+                assert content.get((op, stage, q), (0, ""))[1] != "flight", "two loads to one place"
+                content[op, stage, q] = ((tile, step), "flight")
                 vm.append(("load", (op, stage, q)))
             elif m := re.match(r"s_waitcnt (?:vmcnt\((\d+)\))?\s*(?:lgkmcnt\((\d+)\))?$", ln):
                 if m.group(1) is not None:
@@ -174,7 +224,8 @@ class Sim:
                 for key, (step, state) in list(content.items()):
                     if state == "landed":
                         content[key] = (step, "visible")
-                unread = {k: v for k, v in unread.items() if v != "done"}
+                for k in [k for k, v in unread.items() if v == "done"]:
+                    del unread[k]
             elif (m := READ_R.match(ln)) or READ_C.match(ln):
                 if m:
                     reg, op, h, off = int(m.group(1)), m.group(2), int(m.group(3)), int(m.group(4))
@@ -193,8 +244,8 @@ class Sim:
                     reg -= 2 * part
                 held = {content[op, stage, q] for q in range(8)}
                 assert len(held) == 1, "a stage of two steps"
-                step, state = held.pop()
-                assert state == "visible"
+                (whose, step), state = held.pop()
+                assert state == "visible" and whose == tile
                 frag.pop(reg, None)
                 lgkm.append(("read", reg, (op, step, h, idx), part))
                 unread[op, stage] = "open"
@@ -232,23 +283,28 @@ class Sim:
             else:
                 raise AssertionError(f"unknown instruction {ln}")
             pc += 1
-        return dict(loaded=loaded, done=done, read=read_acc, stores=stores, barriers=barriers, rem=rem)
+        complete(0)
+        return dict(done=done, read=read_acc, stores=stores, barriers=barriers, rem=rem)
 
 
 @pytest.mark.parametrize("name", sorted(GEN.LOOPS))
 @pytest.mark.parametrize("wide", [False, True])
 @pytest.mark.parametrize("ext", [0, 1])
-@pytest.mark.parametrize("kt", [2, 3, 4, 5, 6, 7, 12, 33])
-def test_loop(name, kt, ext, wide):
-    if ext and name != "G16_GROUPED_RR":
-        pytest.skip("this loop has no such step")
+@pytest.mark.parametrize("kts,carry", [((2,), False), ((3,), False), ((4,), False), ((5,), False), ((6,), False), ((12,), False), ((33,), False),
+                                       ((4, 3), False), ((2, 2, 2), True), ((3, 3, 3), True), ((4, 5, 2, 3, 7, 6, 2), True), ((12, 13, 12), True)])
+def test_loop(name, kts, carry, ext, wide):
+    if ext and (name != "G16_GROUPED_RR" or carry):
+        pytest.skip("this loop has no such step, and tiles with one are not carried on to")
     la, lb, p = GEN.LOOPS[name]
-    r = Sim(GEN.generate(la, lb, p), la, lb, wide, kt, ext).run()
-    assert r["loaded"] == {(op, s, q) for op in "ab" for s in range(kt) for q in range(8)}
-    assert r["done"] == {b: 2 * kt for b in range(64)}
-    assert r["read"] == set(range(256))
-    assert r["stores"] == (64 if wide else 32)
-    assert r["barriers"] == 2 * kt - 2   # one for step 0, a release for each step that loads, a publish for each but the last
+    sim = Sim(GEN.generate(la, lb, p), la, lb, wide, kts, carry, ext)
+    runs = sim.run()
+    want = {(t, op, s, q) for t, kt in enumerate(kts) for op in "ab" for s in range(kt) for q in range(8)}
+    assert sim.loaded == want
+    for r, kt in zip(runs, kts):
+        assert r["done"] == {b: 2 * kt for b in range(64)}
+        assert r["read"] == set(range(256))
+        assert r["stores"] == (64 if wide else 32)
+        assert r["barriers"] == 2 * kt - 2   # one for step 0, a release for each step that loads, a publish for each but the last
 
 
 def test_committed_include():
