@@ -43,11 +43,12 @@ zeros; a side by columns beside it begins that many rows early, and those
 rows' offsets are masked likewise.  With both sides by columns the rows behind
 the last load zeros by themselves: the buffers end there.
 
-From tile to tile: the last step also loads step 0 of the workgroup's next tile,
-from %[rsan] and %[rsbn], into the stage that it does not read, so that the
-next tile's block begins with its step 0 on the way (%[first] is 0 then, and
-%[par] the stage; otherwise a tile loads its own step 0 into stage 0).  Where
-there is no such tile these buffers are empty.
+From tile to tile: the last step also loads steps 0 and 1 of the workgroup's
+next tile, from %[rsan] and %[rsbn], the first into the stage that it does not
+read, the second behind a release barrier into its own, so that the next tile's
+block begins with both on the way (%[first] is 0 then, and %[par] the stage of
+step 0; otherwise a tile loads them itself, step 0 into stage 0).  Where there
+is no such tile these buffers are empty.
 
 RR can begin with a step of another product, whose operands have rows of their
 own (the second product of a low-rank adapter, up to 64 elements of its
@@ -88,7 +89,7 @@ class Emitter(ring4.Emitter):
         super().__init__()
         self.layout = {"a": la, "b": lb}
         self.wide = False
-        self.behind: list[int] = []   # stores behind the next tile's loads, for each last step
+        self.behind: list[tuple] = []   # loads and stores behind the next tile's step 0, and its step 1, for each last step
 
     @staticmethod
     def m0(op: str, q: int, stage: int) -> str:
@@ -138,11 +139,13 @@ class Emitter(ring4.Emitter):
         out.append(("s_add_u32 %[sdo], %[sdo], %[gstr]", False))
         return out
 
-    def next_load(self, op: str, q: int) -> list[str]:
-        """Load q of the next tile's step 0, with what masks its offset."""
+    def next_load(self, op: str, q: int, step: int) -> list[str]:
+        """Load q of the next tile's step 0 or 1, with what masks its offset."""
         layout = self.layout
         imm = 1024 * (q % 4)
         off = f" offset:{imm}" if imm else ""
+        if step == 1:
+            return [f"buffer_load_dwordx4 %[{op}x{q}], %[rs{op}n], %[kh{op}] offen{off} lds"]
         load = f"buffer_load_dwordx4 %[ht], %[rs{op}n], 0 offen{off} lds"
         if layout["a"] == "c":
             return [load.replace("%[ht]", f"%[{op}x{q}]")]
@@ -237,13 +240,26 @@ def emit_step(e: Emitter, stage: int, first: bool, ahead: bool, has_next: bool, 
             at = g
         gaps[first_free(g + p["f0_lat"])].append(("text", "s_waitcnt lgkmcnt(0)", "clear"))
     if last:
-        g = p["nxt_start"]
+        # the late reads are the stage's last: behind this barrier it is free
+        gaps[rel - 1].append(("text", "s_waitcnt lgkmcnt(0)", "clear"))
+        gaps[rel].append(("text", "s_barrier"))
+        lines = []
         for op, q in LOAD3:
-            lines = ([Emitter.m0(op, q, stage ^ 1)] if q % 4 == 0 else []) + e.next_load(op, q)
-            for k, text in enumerate(lines):   # one to a gap, the load last
-                gaps[g + k].append(("text", text))
-            g += max(p["nxt_every"], len(lines))
-        assert g < ng, "next-tile loads beyond the step"
+            lines += ([Emitter.m0(op, q, stage ^ 1)] if q % 4 == 0 else []) + e.next_load(op, q, 0)
+        for op in "ab":
+            lines.append(f"s_mov_b32 %[kh{op}], {side_steps(op, e.layout[op])}")
+        for op, q in LOAD3:
+            lines += ([Emitter.m0(op, q, stage)] if q % 4 == 0 else []) + e.next_load(op, q, 1)
+        # one to a gap, or two where one each does not fit; those of this stage behind the barrier
+        from_gap, at = rel + 1, p["nxt_start"]
+        own = next(n for n, text in enumerate(lines) if text == Emitter.m0("a", 0, stage))
+        for n, text in enumerate(lines):
+            if n == own:
+                at = max(at, from_gap)
+            gaps[at].append(("text", text))
+            if sum(it[0] == "text" and it[1] in lines for it in gaps[at]) > (len(lines) - n) // max(1, ng - 2 - at):
+                at += 1
+        assert at < ng, "next-tile loads beyond the step"
     texts = [(g, it[1]) for g in range(ng) for it in gaps[g] if it[0] == "text"]
     writers = [g for g, t in texts if t.startswith(("s_add_u32", "s_sub_u32"))]
     compares = [g for g, t in texts if t.startswith("s_cmp")]
@@ -268,9 +284,9 @@ def emit_step(e: Emitter, stage: int, first: bool, ahead: bool, has_next: bool, 
                     e.lgkm.clear()
     if last:
         e.epi_rest(t_base)
-        lines = e.lines[start:]
-        at = max(n for n, ln in enumerate(lines) if ln.startswith("buffer_load_dwordx4"))
-        e.behind.append(sum(ln.startswith("buffer_store_dwordx4") for ln in lines[at:]))
+        vm = [ln for ln in e.lines[start:] if ln.startswith("buffer_")]
+        at = [n for n, ln in enumerate(vm) if ln.startswith("buffer_load")]
+        e.behind.append((len(vm) - 1 - at[NLOAD - 1], len(vm) - 1 - at[2 * NLOAD - 1]))
         for t in tail:
             e.op(t)
 
@@ -286,11 +302,6 @@ def generate(la: str, lb: str, p: dict) -> str:
                 e.op(Emitter.m0(op, q, stage))
                 e.op("s_nop 0")   # M0 write -> LDS-DMA read of M0
             e.op(Emitter.load(op, q, "ko", f"v{head_reg(op, q)}" if masked and head[op] != "none" else None))
-
-    def begin(stage: int, wait: str) -> None:
-        """The loads of step 1, and step 0's fragments from `stage`."""
-        loads(1, False, stage ^ 1)
-        rest(stage, wait)
 
     def rest(stage: int, wait: str) -> None:
         for op in "ab":
@@ -318,7 +329,7 @@ def generate(la: str, lb: str, p: dict) -> str:
 
     e.op("s_cmp_eq_u32 %[first], 0")
     e.op("s_cbranch_scc1 15f")
-    # this tile's own step 0, behind what the tile before loaded from empty buffers
+    # this tile's own first steps, behind what the tile before loaded from empty buffers
     e.op("s_waitcnt vmcnt(@BEHIND@)")
     for op, q in LOAD3:
         if head[op] == "r":
@@ -355,16 +366,15 @@ def generate(la: str, lb: str, p: dict) -> str:
     rest(0, str(NLOAD))
     zero = list(e.lgkm)   # the reads under way at label 20, from either side
     e.op("s_branch 20f")
-    # carried from the tile before: @WAIT@ leaves step 1's loads in flight and
-    # the stores behind the next tile's loads
+    # carried from the tile before: step 0 has to be there, what came behind it not
     e.label("15")
     advance()
     e.op("s_cmp_eq_u32 %[par], 0")
     e.op("s_cbranch_scc0 16f")
-    begin(0, "@WAIT@")
+    rest(0, "@WAIT@")
     e.op("s_branch 20f")
     e.label("16")
-    begin(1, "@WAIT@")
+    rest(1, "@WAIT@")
     entry = list(e.lgkm)
     e.op(cmp2)
     e.op("s_cbranch_scc1 25f")
@@ -399,7 +409,7 @@ def generate(la: str, lb: str, p: dict) -> str:
         e.wide = False
         step(stage, False, False, False, True, ["s_branch 4f"] if stage else [])
     e.label("4")
-    return "\n".join(e.lines).replace("@WAIT@", str(min(63, NLOAD + min(e.behind)))).replace("@BEHIND@", str(min(e.behind)))
+    return "\n".join(e.lines).replace("@WAIT@", str(min(63, *(w for w, _ in e.behind)))).replace("@BEHIND@", str(min(w for _, w in e.behind)))
 
 
 # Loads of step j + 2 all go out in step j, so that they have the rest of it

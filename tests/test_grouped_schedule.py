@@ -7,7 +7,8 @@ A simulator runs each loop's control flow for a range of step counts and checks 
 * a fragment read sees a stage whose loads of one step were all waited for (vmcnt) and then published by a barrier;
 * every product takes the fragments of its own step, sub-step and block, whose reads were waited for (lgkmcnt; LDS reads
   complete in order), and a block's products follow each other from zero on;
-* the last step loads the next tile's step 0 into the stage that it does not read, and the next tile begins there;
+* the last step loads the next tile's steps 0 and 1, the first into the stage that it does not read, and the next tile
+  begins there;
 * the epilogue reads each accumulator once, long enough after its last product, and stores each row group at its own offset;
 * the committed include is what the generator writes.
 
@@ -130,20 +131,25 @@ class Sim:
             elif m := re.match(r"v_cndmask_b32 %\[ht\], %\[ht\], %\[bx(\d)\], vcc$", ln):
                 assert masked == 2 * int(m.group(1)) and self.layout["b"] == "c" and ht == "beyond"
                 ht = ("b", int(m.group(1)))
-            elif m := re.match(r"buffer_load_dwordx4 (\S+), %\[rs([ab])n\], 0 offen(?: offset:(\d+))? lds$", ln):
-                op, imm = m.group(2), int(m.group(3) or 0)
+            elif m := re.match(r"s_mov_b32 %\[kh([ab])\], (128|%\[st([ab])\])$", ln):
+                assert m.group(2) == ("128" if self.layout[m.group(1)] == "r" else f"%[st{m.group(1)}]")
+                s["kh" + m.group(1)] = 1
+            elif m := re.match(r"buffer_load_dwordx4 (\S+), %\[rs([ab])n\], (?:0|%\[kh([ab])\]) offen(?: offset:(\d+))? lds$", ln):
+                op, imm = m.group(2), int(m.group(4) or 0)
+                nstep = 0 if m.group(3) is None else s["kh" + m.group(3)]
+                assert m.group(3) in (None, op) and nstep in (0, 1)
                 r = re.match(r"%\[([ab])x(\d)\]$", m.group(1))
                 side, q = (r.group(1), int(r.group(2))) if r else ht
                 assert side == op and imm == 1024 * (q % 4) and m0 is not None and pc - m0[1] > 1
-                assert (r is None) == (self.layout["a"] == "r"), "masked where a first step can be partial"
+                assert (r is None) == (self.layout["a"] == "r" and nstep == 0), "masked where a first step can be partial"
                 stage, at = divmod(m0[0] + imm - (65536 if op == "b" else 0), 32768)
-                assert at == 1024 * q and stage == (par + kt) % 2, "the stage that the last step does not read"
+                assert at == 1024 * q and stage == (par + kt + nstep) % 2, "step 0 goes to the stage that the last step does not read"
                 assert (op, stage) not in unread and content[op, stage, q][1] != "flight"
                 on = self.carry and tile + 1 < len(self.kts)
                 if on:
-                    assert (tile + 1, op, 0, q) not in loaded
-                    loaded.add((tile + 1, op, 0, q))
-                content[op, stage, q] = ((tile + 1, 0) if on else ("empty", 0), "flight")
+                    assert (tile + 1, op, nstep, q) not in loaded
+                    loaded.add((tile + 1, op, nstep, q))
+                content[op, stage, q] = ((tile + 1, nstep) if on else ("empty", 0), "flight")
                 vm.append(("load", (op, stage, q)))
             elif ln == "s_cmp_eq_u32 %[ext], 0":
                 scc = int(not self.ext)
@@ -304,7 +310,8 @@ def test_loop(name, kts, carry, ext, wide):
         assert r["done"] == {b: 2 * kt for b in range(64)}
         assert r["read"] == set(range(256))
         assert r["stores"] == (64 if wide else 32)
-        assert r["barriers"] == 2 * kt - 2   # one for step 0, a release for each step that loads, a publish for each but the last
+        # one for step 0, a release for each step that loads and the last, a publish for each but the last
+        assert r["barriers"] == 2 * kt - 1
 
 
 def test_committed_include():
