@@ -6,6 +6,8 @@
 
 #include <hip/hip_runtime.h>
 
+#include <cmath>
+
 #include "grouped_core.hpp"
 #include "grouped_ring.hpp"
 #include "host.hpp"
@@ -1017,7 +1019,7 @@ constexpr int64_t kMaxSplits = 16;
 // and for parts their bytes and the second launch.  The number of tiles is the
 // device's to know where there are several groups: half a tile for each group
 // is taken as lost.
-template <int MODE>
+template <int MODE, bool F32>
 Plan plan(const Form* forms, int n, const Args& g, int cus, int* status)
 {
     const int64_t used = MODE == ADAPT ? 1 : g.groups < g.rows ? g.groups : g.rows;   // groups with rows, at most
@@ -1025,7 +1027,11 @@ Plan plan(const Form* forms, int n, const Args& g, int cus, int* status)
     // matrices, rows read and rows written, at 5.5 TB/s
     const double mats = MODE == TN ? (double)g.groups * g.x_cols * g.cols : (MODE == EACH ? 1. : used) * g.cols * depth;
     const double rows = MODE == TN ? (double)g.rows * (g.x_cols + g.cols) : (double)g.rows * (depth + g.cols);
-    const double memory = (mats + rows) * 2 / 5.5e6;
+    const double memory = (mats * (MODE == TN && F32 ? 2 : 1) + rows) * 2 / 5.5e6;
+    // TN: matrices are written when a workgroup ends, half of it beside others'
+    // products; and a single round of workgroups takes as long as its longest
+    // group, with rows unevenly divided 1.6 times the mean
+    const double written = MODE == TN ? mats * (F32 ? 4 : 2) / 5.5e6 / 2 : 0., longest = MODE == TN && g.groups > 1 ? 1.6 : 1.;
     Plan best = {nullptr, 0, 1, 0, false, 1e300};
     for (int i = 0; i < n; ++i) {
         const Form& f = forms[i];
@@ -1040,26 +1046,27 @@ Plan plan(const Form* forms, int n, const Args& g, int cus, int* status)
             tiles = (double)g.groups * t;
         } else {
             most = (g.rows + used * (f.bm - 1)) / f.bm * ct;
-            const double r = used == 1 ? ceil_div(g.rows, f.bm) : (double)g.rows / f.bm + 0.5 * used;
+            const double r = used == 1 ? ceil_div(g.rows, f.bm) : (double)g.rows / f.bm + 0.5 * used + 0.29 * std::sqrt((double)used);
             tiles = (r < used ? used : r) * ct;
         }
         if (most > kMaxTiles) continue;
         if (ring) {
-            const double d = (depth < 128 ? 128 : depth) / 1024 * f.one + 6.5;
+            const double d = (depth < 128 ? 128 : depth) / 1024 * f.one + 6.0;
             const int64_t count = (int64_t)(tiles + 0.5), rest = count % cus;
-            double us = (count / cus) * d;
+            double us = (count / cus) * d + written;
             const bool split = rest > 0 && rest <= cus / 2 && depth >= 512 && count < 16 * cus;
             if (split) {
                 const double parts = cus / rest;
                 us += d / parts + 8 + (double)rest * parts * f.bm * f.bn * 8 / 8e6;
             } else if (rest > 0) {
-                us += d;
+                us += count < cus ? longest * d : d;
             }
             if (us < memory + 3) us = memory + 3;
             if (us < best.us) {
-                // where the device alone knows the tiles, parts are made possible for it
-                const bool known = MODE == TN || used == 1;
-                const bool parts = known ? split : depth >= 512 && count < 16 * cus;
+                // where the device alone knows the tiles, parts are made
+                // possible for it if its last round may be a small one
+                const bool known = MODE == TN || used == 1, may = 20 * rest <= 11 * cus || 10 * rest >= 9 * cus;
+                const bool parts = known ? split : may && depth >= 512 && count < 16 * cus;
                 best = Plan{&f, parts || most > cus ? cus : most, 1, parts ? (int64_t)cus * f.bm * f.bn * 4 : 0, true, us};
             }
             continue;
@@ -1075,8 +1082,8 @@ Plan plan(const Form* forms, int n, const Args& g, int cus, int* status)
             if (s > 1 && (steps < 4 || most * s > kMaxTiles)) break;
             const double d = (double)(steps * f.bk) / 1024, wgs = tiles * s;
             const double full = (double)(int64_t)(wgs / slots), rest = wgs - full * slots;
-            double us = 1.5 + full * (2.3 + f.two * d);
-            if (rest > 0) us += 2.3 + (rest > cus ? f.two : f.one) * d;
+            double us = 1.5 + full * (2.3 + f.two * d) + written;
+            if (rest > 0) us += 2.3 + (rest > cus ? f.two : f.one) * d * (full == 0 ? longest : 1.);
             if (us < memory + 3) us = memory + 3;
             if (s > 1) us += 6 + wgs * f.bm * f.bn * 8 / 8e6;
             if (us < best.us) best = Plan{&f, most * s, s, s > 1 ? most * s * f.bm * f.bn * 4 : 0, false, us};
@@ -1091,7 +1098,7 @@ Plan plan_for(int dtype, const Args& g, int cus, int* status)
 {
     static const Forms<F16, MODE, F32> f16;
     static const Forms<BF16, MODE, F32> bf16;
-    return dtype == GROUPED_F16 ? plan<MODE>(f16.f, f16.n, g, cus, status) : plan<MODE>(bf16.f, bf16.n, g, cus, status);
+    return dtype == GROUPED_F16 ? plan<MODE, F32>(f16.f, f16.n, g, cus, status) : plan<MODE, F32>(bf16.f, bf16.n, g, cus, status);
 }
 
 template <int MODE>
