@@ -302,6 +302,86 @@ __device__ __forceinline__ void load_requests(const Args& g, const Work& wk, con
     load_all<C::THREADS * 16>(py, dst + C::X_BYTES, std::make_integer_sequence<int, SY::LOADS>());
 }
 
+// The values of each half of a register that are an infinity or a NaN: the
+// sign's bit of the half is set.
+template <typename T>
+__device__ __forceinline__ uint32_t not_finite(uint32_t v)
+{
+    constexpr uint32_t EXP = std::is_same<T, F16>::value ? 0x7c007c00u : 0x7f807f80u;   // all ones, plus one
+    return ((v & EXP) + (0x80008000u - EXP)) & 0x80008000u;
+}
+
+// One step of the requests' part of the contraction.  The zeros that a row has
+// for other requests keep their matrices out of its sums as long as these are
+// finite, so what is not is left out here, and added by add_not_finite to the
+// rows that it belongs to.  Returns whether there was any.
+template <typename T, class C>
+__device__ __forceinline__ bool multiply_requests(const grp::Frags<C, false, C::BM, C::FM>& fx, const grp::Frags<C, false, C::BN, C::FN>& fy, uint32_t stage,
+                                                  Acc<C>& acc)
+{
+    bool any = false;
+#pragma unroll
+    for (int s = 0; s < C::KSUB; ++s) {
+        u32x4 x[C::FM], y[C::FN];
+#pragma unroll
+        for (int i = 0; i < C::FM; ++i) x[i] = fx.read(stage, i, s);
+        uint32_t bad = 0;
+#pragma unroll
+        for (int j = 0; j < C::FN; ++j) {
+            y[j] = fy.read(stage, j, s);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) bad |= not_finite<T>(y[j][e]);
+        }
+        if (__builtin_amdgcn_ballot_w64(bad != 0) != 0) {
+            any = true;
+#pragma unroll
+            for (int j = 0; j < C::FN; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) y[j][e] &= ~((not_finite<T>(y[j][e]) >> 15) * 0xffffu);
+        }
+#pragma unroll
+        for (int i = 0; i < C::FM; ++i)
+#pragma unroll
+            for (int j = 0; j < C::FN; ++j) acc[i][j] = T::mfma(y[j], x[i], acc[i][j]);
+    }
+    return any;
+}
+
+// Adds the products with what is not finite to a wave's outputs, which it has
+// stored: `rows` x `cols` of them at d, the first of the tile's row r0 and of
+// D's column c0; `low` is the tile's first row.  What the sums were rounded to
+// in between makes no difference to a result that is not finite.
+template <typename T, bool F32>
+__device__ __forceinline__ void add_not_finite(const Args& g, const Entry* table, int count, const char* low, char* d, int64_t ld, int r0, int c0, int rows,
+                                               int cols, int lane)
+{
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // the wave's own stores, by other lanes
+    for (int q = 0; q < count; ++q) {
+        const Entry e = table[q];
+        const int first = e.first > r0 ? e.first : r0, end = e.end < r0 + rows ? e.end : r0 + rows;
+        if (first >= end) continue;
+        for (int c = lane; c < cols; c += 64) {
+            const uint32_t* up = reinterpret_cast<const uint32_t*>(g.up + (int64_t)e.id * g.up_mat + (int64_t)(c0 + c) * g.up_ld);
+            for (int p = 0; p < 4 * (int)g.rank_chunks.d; ++p) {
+                const uint32_t bad = not_finite<T>(up[p]);
+                if (bad == 0) continue;
+                const attn::f32x2 u = T::unpack(up[p]);
+                for (int r = first; r < end; ++r) {
+                    const attn::f32x2 h = T::unpack(*reinterpret_cast<const uint32_t*>(low + (int64_t)r * (16 * g.rank_chunks.d) + 4 * p));
+                    const float x = (bad & 0x8000u ? h[0] * u[0] : 0.f) + (bad & 0x80000000u ? h[1] * u[1] : 0.f);
+                    char* at = d + (int64_t)(r - r0) * ld + (F32 ? 4 : 2) * c;
+                    if constexpr (F32) {
+                        *reinterpret_cast<float*>(at) += x;
+                    } else {
+                        const uint32_t sum = T::pack(T::unpack(*reinterpret_cast<const uint16_t*>(at))[0] + x, 0.f);
+                        *reinterpret_cast<uint16_t*>(at) = (uint16_t)sum;
+                    }
+                }
+            }
+        }
+    }
+}
+
 // SPLIT: sums of a part of the contraction, in fp32, for the launch that joins them.
 template <class C, int MODE>
 constexpr int kTileLds = C::LDS + (MODE == ADAPT ? C::BM * (int)sizeof(Entry) + 16 : 0);
@@ -365,6 +445,8 @@ __device__ __forceinline__ void tile_body(const Args& g, char* smem, uint32_t in
     };
     Entry* table = reinterpret_cast<Entry*>(smem + C::LDS);
     int requests = 0, next = 0;   // ADAPT: of the tile; the next step of theirs
+    const int shared = steps;     // the steps before theirs
+    bool bad = false;             // whether their matrices hold what is not finite
     const char* low = MODE != ADAPT ? nullptr : g.low + (int64_t)wk.row0 * (16 * g.rank_chunks.d);
     auto load_more = [&] {
         if (MODE == ADAPT && left <= 0 && requests > 0) {
@@ -374,13 +456,16 @@ __device__ __forceinline__ void tile_body(const Args& g, char* smem, uint32_t in
             load();
         }
     };
+    int* count = reinterpret_cast<int*>(table + C::BM);   // and, behind it, whether any wave found such values
     if (MODE == ADAPT && g.adapters > 0 && (!SPLIT || part + 1 == g.splits.d)) {   // the requests go with the last part
         const int own = steps < C::STAGES - 1 ? steps : C::STAGES - 1;
         for (int s = 0; s < own; ++s) load();
-        int* count = reinterpret_cast<int*>(table + C::BM);
         if (w == 0) {
             const int n = fill_table<C::BM>(g, wk, table);
-            if (lane == 0) *count = n;
+            if (lane == 0) {
+                count[0] = n;
+                count[1] = 0;
+            }
         }
         __syncthreads();
         requests = __builtin_amdgcn_readfirstlane(*count);
@@ -391,31 +476,44 @@ __device__ __forceinline__ void tile_body(const Args& g, char* smem, uint32_t in
     }
     const bool busy = MODE == TN || wk.rows > wm * C::FM * 32;   // the wave has rows
     uint32_t stage = 0;
-    for (int s = 0; s < steps; ++s) {
+    for (int s = 0; s < shared; ++s) {
         grp::publish<(C::STAGES - 2) * C::LOADS>();
         load_more();
         if (busy) grp::multiply<T, C>(fx, fy, stage, acc);
         stage = stage == (C::STAGES - 1) * C::STAGE ? 0 : stage + C::STAGE;
     }
+    if constexpr (MODE == ADAPT) {
+        for (int s = shared; s < steps; ++s) {
+            grp::publish<(C::STAGES - 2) * C::LOADS>();
+            load_more();
+            if (busy) bad |= multiply_requests<T, C>(fx, fy, stage, acc);
+            stage = stage == (C::STAGES - 1) * C::STAGE ? 0 : stage + C::STAGE;
+        }
+    }
+    if (MODE == ADAPT && bad) count[1] = 1;
     grp::publish<0>();
     grp::add_waves<C>(smem, k, lane, acc);
     if (k > 0) return;
+    bad = MODE == ADAPT && requests > 0 && __builtin_amdgcn_readfirstlane(count[1]) != 0;
 
     const int r0 = wm * C::FM * 32, c0 = wn * C::FN * 32, rows = (MODE == TN ? g.x_cols - wk.tile0 : wk.rows) - r0, cols = g.cols - wk.col0 - c0;
     constexpr bool WIDE = F32 || SPLIT;
     constexpr int STAGING = C::FN * 32 * 32 * (WIDE ? 4 : 2);
+    constexpr int OWN_ROWS = C::BM / C::WM, OWN_COLS = C::BN / C::WN;   // of the wave
     constexpr int AFTER = (C::WK - 1) * C::FM * C::FN * 4096;   // the other waves' sums
     static_assert(AFTER + C::WM * C::WN * STAGING <= C::LDS, "LDS budget");
     char* staging = smem + AFTER + (wm * C::WN + wn) * STAGING;
     if constexpr (SPLIT) {
         char* d = (char*)(g.parts + (int64_t)slot * (C::BM * C::BN) + r0 * C::BN + c0);
         grp::store<T, C, true>(staging, d, 4 * C::BN, rows, cols, 1.f, acc, lane);
+        if (MODE == ADAPT && bad) add_not_finite<T, true>(g, table, requests, low, d, 4 * C::BN, r0, wk.col0 + c0, min(rows, OWN_ROWS), min(cols, OWN_COLS), lane);
     } else {
         float scale = 1.f;
         if (MODE == LOW && g.scales != nullptr) scale = g.scales[g.ids[wk.group]];
         char* d = g.d + (MODE == TN ? (int64_t)wk.group * g.d_mat + (int64_t)(wk.tile0 + r0) * g.d_ld : (int64_t)(wk.row0 + r0) * g.d_ld) +
                   (int64_t)(wk.col0 + c0) * (F32 ? 4 : 2);
         grp::store<T, C, F32>(staging, d, g.d_ld, rows, cols, scale, acc, lane);
+        if (MODE == ADAPT && bad) add_not_finite<T, false>(g, table, requests, low, d, g.d_ld, r0, wk.col0 + c0, min(rows, OWN_ROWS), min(cols, OWN_COLS), lane);
     }
 }
 
@@ -543,11 +641,13 @@ __global__ __launch_bounds__(256, 1) void single_kernel(const Args g)
     for (int b = 0; b < RB; ++b) {
         const f32x16& h = sums[0][(b + 1) / 2];
         const int at = (b + 1) % 2 * 8;
-        const uint32_t keep = m >= first[b] && m < end[b] ? 0xffffffffu : 0u;
         u32x4 low;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) low[i] = T::pack(h[at + 2 * i] * scale[b], h[at + 2 * i + 1] * scale[b]) & keep;
-        d = T::mfma(u[b], low, d);
+        for (int i = 0; i < 4; ++i) low[i] = T::pack(h[at + 2 * i] * scale[b], h[at + 2 * i + 1] * scale[b]);
+        const f32x16 sum = T::mfma(u[b], low, d);
+        const bool own = m >= first[b] && m < end[b];   // a lane's sums are one row's
+#pragma unroll
+        for (int i = 0; i < 16; ++i) d[i] = own ? sum[i] : d[i];
     }
     using O = Cfg<16, 16, 512, 1, 1, 4, 4, 1>;
     Acc<O> out = {{d}};
@@ -1079,7 +1179,7 @@ Plan plan(const Form* forms, int n, const Args& g, int cus, int* status)
         }
         for (int64_t s = 1; s <= (f.split == nullptr ? 1 : kMaxSplits); s += s < 4 ? 1 : s / 2) {
             const int64_t steps = ceil_div((int64_t)length, f.bk * s);
-            if (s > 1 && (steps < 4 || most * s > kMaxTiles)) break;
+            if (s > 1 && (steps < 4 || most * s > kMaxTiles / 8)) break;   // a tile of the join has up to 8 workgroups
             const double d = (double)(steps * f.bk) / 1024, wgs = tiles * s;
             const double full = (double)(int64_t)(wgs / slots), rest = wgs - full * slots;
             double us = 1.5 + full * (2.3 + f.two * d) + written;

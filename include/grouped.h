@@ -21,8 +21,8 @@
  * are multiples of 8 and all rows start on 16-byte boundaries (strides are
  * multiples of 8, addresses of 16); others are UNSUPPORTED, as are widths and
  * row pitches of 2^22 elements or more, 2^22 groups, requests or adapters or
- * more, more than 2^31 - 1024 rows, and calls of more than 2^22 output tiles
- * (of 32 x 32 elements or more).  Row pitches are at least as long as a row;
+ * more, more than 2^31 - 1024 rows, and calls that take more than 2^22 output
+ * tiles of 128 x 128 (where a side is shorter than that, of 64 or 32).  Row pitches are at least as long as a row;
  * matrices that are read may repeat (stride_b 0).  What a call writes must not
  * overlap anything that it reads.
  *
@@ -99,9 +99,10 @@ int grouped_tn_check(const grouped_desc* d);
  * adapter: its rows are B A[r].  Any number of requests may share an adapter,
  * and a request is any number of rows: a prompt, or one token.
  *
- * scale_a * (down_a A[r]) is summed in fp32 and rounded to the operands' type
- * once, as the second product's operand, so it has to lie in that type's range;
- * everything else is one sum, rounded once. */
+ * scale_a * (down_a A[r]) is summed in fp32 and, as an operand of the second
+ * product, rounded to the operands' type at most once (calls of up to 64 rows
+ * may keep it in fp32), so it has to lie in that type's range; everything else
+ * is one sum in fp32, rounded once. */
 typedef struct adapter_desc {
     int32_t dtype;
     int32_t rank;          /* at most 128; smaller adapters are padded with zeros */

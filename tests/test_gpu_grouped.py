@@ -289,6 +289,29 @@ def test_adapters_that_no_row_asks_for(case):
     assert torch.equal(D, want.to(torch.float16))
 
 
+SPOILT = [ADAPTERS[i] for i in (6, 7, 8, 9, 10, 13, 14, 15, 16, 17, 18, 20)] + [
+    ([1, 2], [0, 1], 264, 1032, 16), ([2, 1, 1], [2, 0, 1], 72, 520, 8), ([3, 90], [1, 2], 136, 200, 8), ([1] * 200, [b % 4 for b in range(200)], 136, 72, 8)]
+
+
+@pytest.mark.parametrize("case", range(len(SPOILT)))
+@pytest.mark.parametrize("dtype", sorted(TYPES))
+@pytest.mark.parametrize("bad", [NAN, float("inf")])
+def test_an_adapter_that_is_not_finite_spoils_its_own_rows_alone(bad, dtype, case):
+    lens, ids, n, k, rank = SPOILT[case]
+    A, B, down, up, cu, ids = adapter_inputs(real, 900 + case, dtype, SPOILT[case])
+    spoilt = next(a for ln, a in zip(lens, ids) if ln and 0 <= a < down.shape[0])
+    clean = g.adapter_product(A, B, down / 8, up, ints(cu), ints(ids))
+    up = up.clone()
+    up[spoilt, 1::3, rank // 2] = bad
+    say(f"[gpu] adapter {spoilt} holds {bad}, {dtype} {SPOILT[case][2:]}")
+    D = g.adapter_product(A, B, down / 8, up, ints(cu), ints(ids))
+    torch.cuda.synchronize()
+    whose = torch.repeat_interleave(torch.tensor(ids[:len(lens)], device=DEV), torch.tensor(lens, device=DEV))
+    hit = (whose == spoilt)[:, None] & (torch.arange(n, device=DEV) % 3 == 1)[None]
+    assert bool(hit.any()) and not bool(torch.isfinite(D[hit]).any())
+    assert torch.equal(D[~hit], clean[~hit])
+
+
 def test_tables_that_decrease_or_run_past_the_rows():
     # not a valid call; it has to stay inside its tensors all the same
     gen = torch.Generator(device=DEV).manual_seed(3)
