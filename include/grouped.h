@@ -21,10 +21,10 @@
  * are multiples of 8 and all rows start on 16-byte boundaries (strides are
  * multiples of 8, addresses of 16); others are UNSUPPORTED, as are widths and
  * row pitches of 2^22 elements or more, 2^22 groups, requests or adapters or
- * more, more than 2^31 - 1024 rows, and calls that take more than 2^22 output
- * tiles of 128 x 128 (where a side is shorter than that, of 64 or 32).  Row pitches are at least as long as a row;
- * matrices that are read may repeat (stride_b 0).  What a call writes must not
- * overlap anything that it reads.
+ * more, more than 2^31 - 1024 rows, and calls of more than 2^22 output tiles
+ * (counted as 128 x 128 elements, for the low-rank projections 64 x 128).  Row
+ * pitches are at least as long as a row; matrices that are read may repeat
+ * (stride_b 0).  What a call writes must not overlap anything that it reads.
  *
  * Calls are asynchronous and stream-ordered: they validate, enqueue and
  * return; validation comes before any HIP call, and an invalid call launches
