@@ -218,6 +218,14 @@ __device__ __forceinline__ Work find_work(const Args& g, uint32_t index, uint32_
     return tile_at<BM, BN, MODE>(g, groups, t);
 }
 
+// How many tiles a part has.
+template <int BM, int MODE>
+__device__ __forceinline__ uint32_t slot_count(const Args& g)
+{
+    Groups<BM, MODE> groups;
+    return all_tiles<BM, MODE>(g, groups);
+}
+
 // 16 zero bytes for chunks that belong to no request.
 __device__ __attribute__((aligned(16))) uint32_t g_nothing[4] = {0, 0, 0, 0};
 
@@ -382,14 +390,19 @@ __device__ __forceinline__ void add_not_finite(const Args& g, const Entry* table
     }
 }
 
-// SPLIT: sums of a part of the contraction, in fp32, for the launch that joins them.
+// What becomes of a tile's sums.  ROUNDED: they are outputs.  PART: of a part of
+// the contraction, in fp32 and in rows, for the launch that joins them.  HELD:
+// the same as they lie in the lanes, for the launch of tiles that has them as
+// FIRST sums, before the requests' part of the contraction, and no other.
+enum Sums { ROUNDED, PART, HELD, FIRST };
+
 template <class C, int MODE>
 constexpr int kTileLds = C::LDS + (MODE == ADAPT ? C::BM * (int)sizeof(Entry) + 16 : 0);
 
-template <typename T, class C, int MODE, bool F32, bool SPLIT>
+template <typename T, class C, int MODE, bool F32, Sums SUMS>
 __device__ __forceinline__ void tile_body(const Args& g, char* smem, uint32_t index)
 {
-    constexpr bool XC = MODE == TN, YC = MODE == NN || MODE == TN;
+    constexpr bool XC = MODE == TN, YC = MODE == NN || MODE == TN, SPLIT = SUMS == PART || SUMS == HELD;
     uint32_t part, slot;
     const Work wk = find_work<C::BM, C::BN, MODE, SPLIT>(g, index, &part, &slot);
     if (!wk.found) return;
@@ -435,6 +448,23 @@ __device__ __forceinline__ void tile_body(const Args& g, char* smem, uint32_t in
         x.skip(first);
         y.skip(first);
         left = clampi(depth - first * C::BK, 0, steps * C::BK);
+    }
+    auto held = [&](uint32_t p, int block, int q) {   // a lane's four of the sums in part p
+        return (f32x4*)g.parts + ((((int64_t)p * C::WAVES + w) * (C::FM * C::FN) + block) * 4 + q) * 64 + lane;
+    };
+    if constexpr (SUMS == FIRST) {
+        static_assert(C::WK == 1, "every wave has sums");
+        steps = left = 0;
+        const uint32_t all = slot_count<C::BM, MODE>(g);
+        for (uint32_t p = 0; p < g.splits.d; ++p)
+#pragma unroll
+            for (int b = 0; b < C::FM * C::FN; ++b)
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const f32x4 v = *held(p * all + slot, b, q);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) acc[b / C::FN][b % C::FN][4 * q + e] += v[e];
+                }
     }
     uint32_t fill = 0;
     auto load = [&] {
@@ -503,7 +533,15 @@ __device__ __forceinline__ void tile_body(const Args& g, char* smem, uint32_t in
     constexpr int AFTER = (C::WK - 1) * C::FM * C::FN * 4096;   // the other waves' sums
     static_assert(AFTER + C::WM * C::WN * STAGING <= C::LDS, "LDS budget");
     char* staging = smem + AFTER + (wm * C::WN + wn) * STAGING;
-    if constexpr (SPLIT) {
+    if constexpr (SUMS == HELD) {
+#pragma unroll
+        for (int b = 0; b < C::FM * C::FN; ++b)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const f32x16& v = acc[b / C::FN][b % C::FN];
+                *held(slot, b, q) = f32x4{v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]};
+            }
+    } else if constexpr (SUMS == PART) {
         char* d = (char*)(g.parts + (int64_t)slot * (C::BM * C::BN) + r0 * C::BN + c0);
         grp::store<T, C, true>(staging, d, 4 * C::BN, rows, cols, 1.f, acc, lane);
         if (MODE == ADAPT && bad) add_not_finite<T, true>(g, table, requests, low, d, 4 * C::BN, r0, wk.col0 + c0, min(rows, OWN_ROWS), min(cols, OWN_COLS), lane);
@@ -654,30 +692,33 @@ __global__ __launch_bounds__(256, 1) void single_kernel(const Args g)
     grp::store<T, O, false>(smem + 3 * FN * 4096, g.d + (int64_t)row0 * g.d_ld + 2 * (int64_t)col0, g.d_ld, rows, g.cols - col0, 1.f, out, lane);
 }
 
-template <typename T, class C, int MODE, bool F32, bool SPLIT>
+template <typename T, class C, int MODE, bool F32, Sums SUMS>
 __global__ __launch_bounds__(C::THREADS, C::PER_CU * C::WAVES / 4) void tile_kernel(const Args g)
 {
     __shared__ __attribute__((aligned(1024))) char smem[kTileLds<C, MODE>];
-    tile_body<T, C, MODE, F32, SPLIT>(g, smem, blockIdx.x);
+    tile_body<T, C, MODE, F32, SUMS>(g, smem, blockIdx.x);
 }
 
-// Up to 64 rows: the projections onto the rank, by the first workgroups, beside
-// the shared product, which waits for bytes; both leave their sums in fp32, and
-// the next launch puts them together.
+// Few rows: the projections onto the rank, by the first workgroups, beside the
+// shared product, whose sums the next launch puts together with the adapters'
+// second products.  Up to 64 rows the shared product waits for bytes, the
+// projections stay in fp32 and finish_kernel ends the call (SUMS PART); above,
+// both wait for products, and tiles end it that have the sums as their FIRST
+// (SUMS HELD).
 struct PairArgs {
     Args low, base;
     uint32_t low_wgs;
 };
 
-template <typename T, class L, class C>
+template <typename T, class L, class C, Sums SUMS>
 __global__ __launch_bounds__(256, 2) void pair_kernel(const PairArgs p)
 {
     static_assert(L::THREADS == 256 && C::THREADS == 256, "one launch");
     __shared__ __attribute__((aligned(1024))) char smem[kTileLds<C, ADAPT> > kTileLds<L, LOW> ? kTileLds<C, ADAPT> : kTileLds<L, LOW>];
     if (blockIdx.x < p.low_wgs)
-        tile_body<T, L, LOW, true, false>(p.low, smem, blockIdx.x);
+        tile_body<T, L, LOW, SUMS == PART, ROUNDED>(p.low, smem, blockIdx.x);
     else
-        tile_body<T, C, ADAPT, false, true>(p.base, smem, blockIdx.x - p.low_wgs);
+        tile_body<T, C, ADAPT, false, SUMS>(p.base, smem, blockIdx.x - p.low_wgs);
 }
 
 // Sum over groups of L neighbouring lanes, by the lanes' own data paths.
@@ -1049,21 +1090,31 @@ using Oblong = Cfg<64, 128, 64, 2, 2, 1, 3, 2>;
 using Middle = Cfg<128, 128, 64, 2, 2, 1, 2, 2>;
 using Large = Cfg<256, 256, 64, 2, 4, 1, 2, 1>;
 
-// A shape's kernels, and what it takes: microseconds for 1024 of the
-// contraction with one and with two workgroups on a compute unit, all of them
-// busy (measured on MI355X, operands in L2).
+// What a shape takes: microseconds for 1024 of the contraction with one and
+// with two workgroups on a compute unit, all of them busy, and the same where a
+// row pitch is not a multiple of a cache line, so that rows of 128 bytes are
+// parts of two lines (measured on MI355X, operands in L2).
+struct Rate {
+    double one, two, odd_one, odd_two;
+};
+constexpr Rate kTiny = {1.3, 1.3, 1.4, 1.4}, kSmall = {2.0, 2.0, 2.1, 2.1}, kFlat = {5.4, 7.8, 5.9, 10.3}, kSquare = {5.0, 6.4, 5.2, 8.9};
+constexpr Rate kOblong = {6.8, 10.0, 7.0, 14.2}, kMiddle = {10.5, 16.8, 13.8, 19.8}, kLarge = {28., 28., 30., 30.}, kRing = {20.6, 20.6, 22.2, 22.2};
+constexpr Rate kTiny2 = {1.6, 2.6, 1.8, 2.8}, kSmall2 = {2.4, 3.9, 2.5, 4.2};
+bool odd_pitch(const Args& g) { return ((g.x_ld | g.y_ld) & 127) != 0; }
+
+// A shape's kernels.
 struct Form {
     int bm, bn, bk, threads, per_cu;
-    float one, two;
+    Rate rate;
     const void *whole, *split, *join;
 };
 
 template <typename T, int MODE, bool F32, class C, bool PARTS>
-Form form(float one, float two)
+Form form(const Rate& rate)
 {
-    Form f = {C::BM, C::BN, C::BK, C::THREADS, C::PER_CU, one, two, (const void*)&tile_kernel<T, C, MODE, F32, false>, nullptr, nullptr};
+    Form f = {C::BM, C::BN, C::BK, C::THREADS, C::PER_CU, rate, (const void*)&tile_kernel<T, C, MODE, F32, ROUNDED>, nullptr, nullptr};
     if constexpr (PARTS) {
-        f.split = (const void*)&tile_kernel<T, C, MODE, F32, true>;
+        f.split = (const void*)&tile_kernel<T, C, MODE, F32, PART>;
         f.join = (const void*)&join_kernel<T, C, MODE, F32>;
     }
     return f;
@@ -1077,16 +1128,16 @@ struct Forms {
     Forms()
     {
         if constexpr (MODE != TN && MODE != EACH) {
-            f[n++] = form<T, MODE, F32, Tiny, false>(1.3f, 1.3f);
-            f[n++] = form<T, MODE, F32, Small, false>(2.0f, 2.0f);
+            f[n++] = form<T, MODE, F32, Tiny, false>(kTiny);
+            f[n++] = form<T, MODE, F32, Small, false>(kSmall);
         }
-        if constexpr (MODE == NT || MODE == NN) f[n++] = form<T, MODE, F32, Flat, false>(5.4f, 7.8f);
-        if constexpr (MODE != EACH) f[n++] = form<T, MODE, F32, Square, true>(5.0f, 6.4f);
-        if constexpr (MODE != TN && MODE != EACH) f[n++] = form<T, MODE, F32, Oblong, true>(6.8f, 10.0f);
-        if constexpr (MODE != LOW && MODE != EACH) f[n++] = form<T, MODE, F32, Middle, true>(11.2f, 16.2f);
-        if constexpr (MODE == ADAPT) f[n++] = form<T, MODE, F32, Large, false>(28.f, 28.f);
+        if constexpr (MODE == NT || MODE == NN) f[n++] = form<T, MODE, F32, Flat, false>(kFlat);
+        if constexpr (MODE != EACH) f[n++] = form<T, MODE, F32, Square, true>(kSquare);
+        if constexpr (MODE != TN && MODE != EACH) f[n++] = form<T, MODE, F32, Oblong, true>(kOblong);
+        if constexpr (MODE != LOW && MODE != EACH) f[n++] = form<T, MODE, F32, Middle, true>(kMiddle);
+        if constexpr (MODE == ADAPT) f[n++] = form<T, MODE, F32, Large, false>(kLarge);
         if constexpr (MODE == NT || MODE == NN || MODE == TN || MODE == EACH)
-            f[n++] = Form{grp::kRingTile, grp::kRingTile, grp::kRingStep, 256, 0, 20.6f, 20.6f, (const void*)&ring_kernel<T, MODE, F32>, nullptr,
+            f[n++] = Form{grp::kRingTile, grp::kRingTile, grp::kRingStep, 256, 0, kRing, (const void*)&ring_kernel<T, MODE, F32>, nullptr,
                           (const void*)&ring_join_kernel<T, MODE, F32>};
     }
 };
@@ -1132,10 +1183,12 @@ Plan plan(const Form* forms, int n, const Args& g, int cus, int* status)
     // products; and a single round of workgroups takes as long as its longest
     // group, with rows unevenly divided 1.6 times the mean
     const double written = MODE == TN ? mats * (F32 ? 4 : 2) / 5.5e6 / 2 : 0., longest = MODE == TN && g.groups > 1 ? 1.6 : 1.;
+    const bool odd = odd_pitch(g);
     Plan best = {nullptr, 0, 1, 0, false, 1e300};
     for (int i = 0; i < n; ++i) {
         const Form& f = forms[i];
         const bool ring = f.per_cu == 0;
+        const double one = odd ? f.rate.odd_one : f.rate.one, two = odd ? f.rate.odd_two : f.rate.two;
         if (ring && !ring_takes(MODE, g)) continue;
         const int64_t ct = ceil_div(g.cols, f.bn);
         int64_t most;    // tiles, at most
@@ -1151,7 +1204,7 @@ Plan plan(const Form* forms, int n, const Args& g, int cus, int* status)
         }
         if (most > kMaxTiles) continue;
         if (ring) {
-            const double d = (depth < 128 ? 128 : depth) / 1024 * f.one + 6.0;
+            const double d = (depth < 128 ? 128 : depth) / 1024 * one + 6.0;
             const int64_t count = (int64_t)(tiles + 0.5), rest = count % cus;
             double us = (count / cus) * d + written;
             const bool split = rest > 0 && rest <= cus / 2 && depth >= 512 && count < 16 * cus;
@@ -1182,8 +1235,8 @@ Plan plan(const Form* forms, int n, const Args& g, int cus, int* status)
             if (s > 1 && (steps < 4 || most * s > kMaxTiles / 8)) break;   // a tile of the join has up to 8 workgroups
             const double d = (double)(steps * f.bk) / 1024, wgs = tiles * s;
             const double full = (double)(int64_t)(wgs / slots), rest = wgs - full * slots;
-            double us = 1.5 + full * (2.3 + f.two * d) + written;
-            if (rest > 0) us += 2.3 + (rest > cus ? f.two : f.one) * d * (full == 0 ? longest : 1.);
+            double us = 1.5 + full * (2.3 + two * d) + written;
+            if (rest > 0) us += 2.3 + (rest > cus ? two : one) * d * (full == 0 ? longest : 1.);
             if (us < memory + 3) us = memory + 3;
             if (s > 1) us += 6 + wgs * f.bm * f.bn * 8 / 8e6;
             if (us < best.us) best = Plan{&f, most * s, s, s > 1 ? most * s * f.bm * f.bn * 4 : 0, false, us};
@@ -1361,7 +1414,8 @@ struct AdapterCall {
     bool adapted, each;
     const void* single;   // all in one launch
     const void* pair;     // projections and shared product in one
-    int bm, bn;           // and its tiles
+    const void* close;    // and what puts them together, for more than 64 rows
+    int bm, bn;           // and the shared product's tiles
     int64_t low_wgs;
     int cus;
     int64_t low_bytes, bytes;   // of the projections, and of all of the workspace
@@ -1371,7 +1425,8 @@ struct AdapterCall {
 void plan_pair(const adapter_desc* d, AdapterCall* c, int64_t* parts)
 {
     const int bm = d->rows <= 16 ? 16 : d->rows <= 32 ? 32 : 64, bk = bm == 16 ? 256 : bm == 32 ? 128 : 64;
-    const double one = bm == 16 ? 1.6 : bm == 32 ? 2.4 : 5.0, two = bm == 16 ? 2.6 : bm == 32 ? 3.9 : 6.4;
+    const Rate& rate = bm == 16 ? kTiny2 : bm == 32 ? kSmall2 : kSquare;
+    const double one = odd_pitch(c->rest) ? rate.odd_one : rate.one, two = odd_pitch(c->rest) ? rate.odd_two : rate.two;
     const int64_t ct = ceil_div(d->N, bm), used = d->requests < d->rows ? d->requests : d->rows;
     const int64_t low_wgs = (d->rows + used * 15) / 16 * ceil_div(d->rank, 16);
     if (low_wgs > 2 * c->cus) return;
@@ -1396,11 +1451,11 @@ void plan_pair(const adapter_desc* d, AdapterCall* c, int64_t* parts)
     if (best >= c->plan.us + c->low_plan.us + 2) return;
     const bool f16 = d->dtype == GROUPED_F16;
     if (bm == 16)
-        c->pair = f16 ? (const void*)&pair_kernel<F16, Tiny2, Tiny2> : (const void*)&pair_kernel<BF16, Tiny2, Tiny2>;
+        c->pair = f16 ? (const void*)&pair_kernel<F16, Tiny2, Tiny2, PART> : (const void*)&pair_kernel<BF16, Tiny2, Tiny2, PART>;
     else if (bm == 32)
-        c->pair = f16 ? (const void*)&pair_kernel<F16, Tiny2, Small2> : (const void*)&pair_kernel<BF16, Tiny2, Small2>;
+        c->pair = f16 ? (const void*)&pair_kernel<F16, Tiny2, Small2, PART> : (const void*)&pair_kernel<BF16, Tiny2, Small2, PART>;
     else
-        c->pair = f16 ? (const void*)&pair_kernel<F16, Tiny2, Square> : (const void*)&pair_kernel<BF16, Tiny2, Square>;
+        c->pair = f16 ? (const void*)&pair_kernel<F16, Tiny2, Square, PART> : (const void*)&pair_kernel<BF16, Tiny2, Square, PART>;
     c->bm = c->bn = bm;
     c->low_wgs = low_wgs;
     c->plan.splits = splits;
@@ -1414,6 +1469,81 @@ void plan_pair(const adapter_desc* d, AdapterCall* c, int64_t* parts)
     c->rest.splits = attn::div_by(splits);
     c->low_bytes = ceil_div(4 * d->rows * d->rank, 256) * 256;
     *parts = ct * splits * bm * bm * 4;
+}
+
+// The pair of launches for more rows, where the model finds it faster: with a
+// long contraction and few tiles, where the projections take as long as the
+// rest.  (bf16, rank 16, 195 rows, 2304 x 5376: 24 us, and 32 with the
+// projections first; 1101 rows, 512 x 7680: 31 and 39.  1226 rows, 3032 x 384:
+// 20 and 17.)
+template <typename T, class C>
+void pair_of(AdapterCall* c)
+{
+    c->pair = (const void*)&pair_kernel<T, Tiny2, C, HELD>;
+    c->close = (const void*)&tile_kernel<T, C, ADAPT, false, FIRST>;
+    c->bm = C::BM;
+    c->bn = C::BN;
+}
+
+void plan_more(const adapter_desc* d, AdapterCall* c, int64_t* parts)
+{
+    const int64_t used = d->requests < d->rows ? d->requests : d->rows;
+    const double slots = 2. * c->cus, depth = (double)d->K / 1024, memory = 3 + (double)(d->N + d->rows) * d->K * 2 / 5.5e6;
+    const bool odd = odd_pitch(c->rest);
+    const int64_t low_wgs = (d->rows + used * 15) / 16 * ceil_div(d->rank, 16);   // at most
+    const double low_mean = ((double)d->rows / 16 + 0.5 * used) * ceil_div(d->rank, 16);
+    const double low_one = odd ? kTiny2.odd_one : kTiny2.one, low_two = odd ? kTiny2.odd_two : kTiny2.two;
+    double best = 1e300;
+    bool wide = false;
+    int64_t splits = 1;
+    for (int i = 0; i < 2; ++i) {
+        const Rate& rate = i == 0 ? kSquare : kOblong;
+        const double one = odd ? rate.odd_one : rate.one, two = odd ? rate.odd_two : rate.two;
+        const int bm = 64, bn = i == 0 ? 64 : 128;
+        const int64_t tiles = ceil_div(d->rows, bm) * ceil_div(d->N, bn);
+        for (int64_t s = 1; s <= kMaxSplits; s += s < 4 ? 1 : s / 2) {
+            const int64_t steps = ceil_div(d->K, 64 * s);
+            if (low_wgs + tiles * s > kMaxTiles || (s > 1 && steps < 4)) break;
+            // the launch's rounds, the projections counted as so many of the others
+            const double each = 2.3 + two * (double)(steps * 64) / 1024, wgs = (double)(tiles * s) + low_mean * (2.3 + low_two * depth) / each;
+            const double full = (double)(int64_t)(wgs / slots), rest = wgs - full * slots;
+            double us = full * each + (rest > c->cus ? each : rest > 0 ? 2.3 + one * (double)(steps * 64) / 1024 : 0.);
+            const double low = 2.3 + (low_mean > c->cus ? low_two : low_one) * depth;
+            if (us < low) us = low;
+            us += 1.5;
+            if (us < memory) us = memory;
+            // and the next one's: requests of a tile as in plan()
+            const double mine = (double)bm / d->rows * used + 1, length = (2. * d->rank * (mine < used ? mine : used) + 256) / 1024;
+            const int64_t rounds = (int64_t)(tiles / slots);
+            const double more = tiles - rounds * slots;
+            us += 3.5 + rounds * (2.3 + two * length) + (more > c->cus ? 2.3 + two * length : more > 0 ? 2.3 + one * length : 0.);
+            us += (double)tiles * s * bm * bn * 8 / 8e6;
+            if (us < best) {
+                best = us;
+                wide = i > 0;
+                splits = s;
+            }
+        }
+    }
+    if (best >= c->plan.us + c->low_plan.us) return;
+    if (d->dtype == GROUPED_F16)
+        wide ? pair_of<F16, Oblong>(c) : pair_of<F16, Square>(c);
+    else
+        wide ? pair_of<BF16, Oblong>(c) : pair_of<BF16, Square>(c);
+    const int64_t rt = ceil_div(d->rows, c->bm), ct = ceil_div(d->N, c->bn);
+    c->each = false;
+    c->low.d_ld = 2 * d->rank;
+    c->low.cols = c->low.low_rows = d->rank;
+    c->low.col_tiles = attn::div_by(ceil_div(d->rank, 16));
+    c->low.row_tiles = (uint32_t)((d->rows + used * 15) / 16);
+    c->low_wgs = low_wgs;
+    c->rest.row_tiles = (uint32_t)rt;
+    c->rest.col_tiles = attn::div_by(ct);
+    c->rest.splits = attn::div_by(splits);
+    c->plan.splits = splits;
+    c->plan.wgs = rt * ct * splits;
+    c->low_bytes = ceil_div(2 * d->rows * d->rank, 256) * 256;
+    *parts = rt * ct * splits * c->bm * c->bn * 4;
 }
 
 int run_pair(const AdapterCall& c, int dtype, int64_t rows, void* workspace, hipStream_t s)
@@ -1430,6 +1560,7 @@ int run_pair(const AdapterCall& c, int dtype, int64_t rows, void* workspace, hip
     Args g = p.base;
     g.adapters = c.rest.adapters;
     g.low = (const char*)workspace;
+    if (c.close != nullptr) return launch(c.close, c.plan.wgs / c.plan.splits, 256, &g, s);
     int bm = c.bm, bn = c.bn;
     void* a[] = {&g, &bm, &bn};
     const int64_t rank = 8 * (int64_t)g.rank_chunks.d;
@@ -1443,7 +1574,7 @@ int plan_adapters(const adapter_desc* d, AdapterCall* c)
     int st = device_cus(&c->cus);
     if (st != GEMM_F16_NT_OK) return st;
     c->adapted = d->adapters > 0 && d->rank > 0;
-    c->single = c->pair = nullptr;
+    c->single = c->pair = c->close = nullptr;
     Args g = {};
     g.x = (const char*)d->A;
     g.cu = d->cu;
@@ -1518,6 +1649,7 @@ int plan_adapters(const adapter_desc* d, AdapterCall* c)
         }
     }
     if (c->adapted && d->rows <= 64) plan_pair(d, c, &parts);
+    if (c->adapted && d->rows > 64) plan_more(d, c, &parts);
     if (c->pair == nullptr && c->plan.part_bytes > parts) parts = c->plan.part_bytes;
     c->bytes = c->low_bytes + parts;
     return GEMM_F16_NT_OK;

@@ -96,6 +96,7 @@ CASES = [
     ([700], 4352, 4352),
     ([2200], 4352, 4352),
     ([4000, 9, 352], 1032, 4104),
+    ([150, 120, 140, 90], 8200, 200),
 ]
 
 
@@ -184,6 +185,11 @@ ADAPTERS = [
     ([2100, 0, 900, 3, 1500], [1, 0, -1, 2, 3], 4104, 1032, 64),   # large tiles of one request each
     ([4352], [2], 4104, 2056, 24),                                 # and of a small last round, in parts
     ([257, 4000, 255], [2, 3, 0], 4096, 2048, 8),
+    ([100, 0, 60, 35], [1, 0, -1, 3], 520, 2056, 16),              # projections beside the shared product
+    ([1] * 90, [b % 5 - 1 for b in range(90)], 264, 4104, 40),
+    ([70], [2], 2056, 2048, 8),
+    ([300, 1, 411], [3, 3, 0], 1032, 4104, 128),
+    ([65, 2, 700, 0, 1], [-1, 0, 2, 1, 9], 264, 7688, 24),
 ]
 
 
@@ -276,7 +282,7 @@ def test_what_is_not_finite_stays_where_it_is(lens, n, k, dtype):
     assert torch.equal(dB[1], clean[2][1]) and torch.equal(dB[0][:, 1], clean[2][0][:, 1])
 
 
-@pytest.mark.parametrize("case", [2, 4, 5, 8, 11, 13, len(ADAPTERS) - 3])
+@pytest.mark.parametrize("case", [2, 4, 5, 8, 11, 13, 18, 22, 23, 25])
 def test_adapters_that_no_row_asks_for(case):
     lens, ids, n, k, rank = ADAPTERS[case]
     ids = [i if i % 2 == 0 else -1 for i in ids]
@@ -289,7 +295,7 @@ def test_adapters_that_no_row_asks_for(case):
     assert torch.equal(D, want.to(torch.float16))
 
 
-SPOILT = [ADAPTERS[i] for i in (6, 7, 8, 9, 10, 13, 14, 15, 16, 17, 18, 20)] + [
+SPOILT = [ADAPTERS[i] for i in (6, 7, 8, 9, 10, 13, 14, 15, 16, 17, 18, 20, 21, 22, 24, 25)] + [
     ([1, 2], [0, 1], 264, 1032, 16), ([2, 1, 1], [2, 0, 1], 72, 520, 8), ([3, 90], [1, 2], 136, 200, 8), ([1] * 200, [b % 4 for b in range(200)], 136, 72, 8)]
 
 
