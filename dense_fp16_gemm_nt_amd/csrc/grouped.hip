@@ -46,6 +46,7 @@ struct Args {
     Div col_tiles;
     Div per_group;       // TN: tiles of a group, padded to whole rounds of the XCDs
     uint32_t group_tiles;
+    int sorted;          // TN: the longest groups first
     uint32_t row_tiles;  // of all groups, at most
     Div splits;          // parts of the contraction, whose sums a second launch joins
     float* parts;
@@ -106,6 +107,7 @@ template <int BM, int MODE>
 struct Groups {
     Rows s;
     uint32_t tiles, upto, total;
+    uint32_t place;   // TN: the lane's group among all, the longest first
 
     __device__ __forceinline__ void look(const Args& g, int e, int groups)
     {
@@ -133,6 +135,24 @@ struct Groups {
         // a table that decreases can name rows more than once: no more tiles
         // than the launch and the room for parts were made for
         if (total > g.row_tiles) total = g.row_tiles;
+    }
+    // TN: all groups have as many tiles, which take as long as their groups do.
+    // Where the host says so the longest come first, so that what is left for
+    // the end is short.
+    __device__ __forceinline__ void order(const Args& g)
+    {
+        const int lane = threadIdx.x & 63;
+        place = 0;
+        if (!g.sorted) return;
+        const int mine = lane < g.groups ? rows_of(g, lane).count : -1;
+        for (int e = 0; e < g.groups; ++e) {
+            const int other = __builtin_amdgcn_readlane(mine, e);
+            place += other > mine || (other == mine && e < lane);
+        }
+    }
+    __device__ __forceinline__ uint32_t at(const Args& g, uint32_t p) const
+    {
+        return !g.sorted ? p : (uint32_t)__builtin_ctzll(__builtin_amdgcn_ballot_w64(place == p));
     }
     // Tile t of `total`.
     __device__ __forceinline__ Work find(const Args& g, uint32_t t)
@@ -162,8 +182,8 @@ __device__ __forceinline__ Work tile_at(const Args& g, Groups<BM, MODE>& groups,
     uint32_t ti, tj;
     Work r;
     if (MODE == TN) {
-        const uint32_t e = t / g.group_tiles;
-        grouped_tile_in<uint32_t>(t - e * g.group_tiles, g.group_tiles / g.col_tiles.d, g.col_tiles.d, kGroupTiles, &ti, &tj);
+        const uint32_t p = t / g.group_tiles, e = groups.at(g, p);
+        grouped_tile_in<uint32_t>(t - p * g.group_tiles, g.group_tiles / g.col_tiles.d, g.col_tiles.d, kGroupTiles, &ti, &tj);
         const Rows s = rows_of(g, (int)e);
         r = Work{(int)e, s.first, s.count, (int)ti * BM, 0, true};
     } else {
@@ -178,7 +198,10 @@ __device__ __forceinline__ Work tile_at(const Args& g, Groups<BM, MODE>& groups,
 template <int BM, int MODE>
 __device__ __forceinline__ uint32_t all_tiles(const Args& g, Groups<BM, MODE>& groups)
 {
-    if (MODE == TN) return (uint32_t)g.groups * g.group_tiles;
+    if (MODE == TN) {
+        groups.order(g);
+        return (uint32_t)g.groups * g.group_tiles;
+    }
     groups.start(g);
     return groups.total * g.col_tiles.d;
 }
@@ -939,8 +962,13 @@ __global__ __launch_bounds__(256, 1) void ring_kernel(const Args g)
         uint32_t rem, wide, gstr, hk, ext;   // steps, ..., what the first step lacks, whether the adapter's step is the first
         Work wk;
     };
-    auto prepare = [&](uint32_t slot) {
+    // Sorted: the first round has the longest tiles, in order, and every second
+    // round is dealt the other way round.
+    const uint32_t own_slot = (uint32_t)xcd_slot(blockIdx.x, gridDim.x);
+    bool back = false;
+    auto prepare = [&](uint32_t base) {
         Item it = {};
+        const uint32_t slot = base + (back ? gridDim.x - 1 - own_slot : own_slot);
         if (slot >= items) return it;
         uint32_t t = slot, part = 0;
         if (slot >= walk.full) {
@@ -1005,11 +1033,12 @@ __global__ __launch_bounds__(256, 1) void ring_kernel(const Args g)
         return it;
     };
 
-    uint32_t slot = (uint32_t)xcd_slot(blockIdx.x, gridDim.x), own = 1, par = 0;   // see gen_grouped_sched.py: first, par
-    Item it = prepare(slot);
+    uint32_t base = 0, own = 1, par = 0;   // see gen_grouped_sched.py: first, par
+    Item it = prepare(base);
     while (it.found) {
-        slot += gridDim.x;
-        const Item then = prepare(slot);
+        base += gridDim.x;
+        back = MODE == TN && g.sorted && !back;
+        const Item then = prepare(base);
         // its step 0 by the same masks, and not an adapter's
         const bool carry = then.found && then.ext == 0 && then.hk == it.hk;
         const u32x4 none = {0, 0, 0, 0x00020000u};
@@ -1164,6 +1193,16 @@ struct Plan {
 
 constexpr int64_t kMaxSplits = 16;
 
+// TN: whether the longest groups come first.  Large tiles' workgroups find the
+// order once, the others for each tile, and with many rounds the order makes no
+// difference.  (7901 rows over 8 matrices of 1024 x 4864, large tiles: 101 us in
+// the groups' own order, 75 so; 9630 rows, 8 of 2048 x 1536, tiles of 128 x 128:
+// 85 and 76; but 1500 rows, 64 of 2048 x 1024, 16 rounds of them: 102 and 136.)
+bool sorts(bool walks, int64_t groups, int64_t tiles, int cus)
+{
+    return groups > 1 && groups <= (walks ? 64 : 16) && tiles <= (int64_t)(walks ? 8 : 16) * cus;
+}
+
 // The shape and the parts of the contraction that a model of the time finds
 // best: rounds of the compute units, each with what starting a workgroup costs
 // and the contraction's share, not less than the operands take from memory;
@@ -1206,14 +1245,20 @@ Plan plan(const Form* forms, int n, const Args& g, int cus, int* status)
         if (ring) {
             const double d = (depth < 128 ? 128 : depth) / 1024 * one + 6.0;
             const int64_t count = (int64_t)(tiles + 0.5), rest = count % cus;
-            double us = (count / cus) * d + written;
-            const bool split = rest > 0 && rest <= cus / 2 && depth >= 512 && count < 16 * cus;
-            if (split) {
-                const double parts = cus / rest;
-                us += d / parts + 8 + (double)rest * parts * f.bm * f.bn * 8 / 8e6;
-            } else if (rest > 0) {
-                us += count < cus ? longest * d : d;
+            // whole tiles: in rounds; sorted ones of unequal length pack better
+            double us = (count / cus) * d + (rest == 0 ? 0. : count < cus ? longest * d : d);
+            if (MODE == TN && sorts(true, g.groups, count, cus)) {
+                us = d * ((double)count / cus + 0.25);
+                if (us < longest * d) us = longest * d;
             }
+            // or the last round's in parts
+            bool split = rest > 0 && rest <= cus / 2 && depth >= 512 && count < 16 * cus;
+            if (split) {
+                const double parts = cus / rest, in_parts = (count / cus) * d + d / parts + 8 + (double)rest * parts * f.bm * f.bn * 8 / 8e6;
+                split = in_parts < us;
+                if (split) us = in_parts;
+            }
+            us += written;
             if (us < memory + 3) us = memory + 3;
             if (us < best.us) {
                 // where the device alone knows the tiles, parts are made
@@ -1269,6 +1314,7 @@ int run(const Plan& p, const Args& args, void* parts, int cus, hipStream_t s)
     if (MODE == TN) {
         const int64_t t = ct * ceil_div(g.x_cols, f.bm);
         g.group_tiles = (uint32_t)t;
+        g.sorted = sorts(p.walks, g.groups, g.groups * t, cus);
         g.per_group = attn::div_by(p.walks || t < 8 * kNumXcd ? t : ceil_div(t, kNumXcd) * kNumXcd);
     }
     int st = launch(p.splits > 1 ? f.split : f.whole, p.wgs, f.threads, &g, s);
