@@ -27,7 +27,9 @@ using grp::F16;
 // LOW the adapters' projections onto their rank, a product NT whose matrix a
 // table chooses and whose result is scaled; ADAPT the shared projection, with
 // the adapters' second products added to the same sums; EACH the same in large
-// tiles, which have rows of one request each.
+// tiles, which have rows of one request each.  LOW's results are operands of
+// the second product, and rounded to its type for that: the matrix cores take
+// 32-bit operands at a sixteenth of the rate.
 enum Mode { NT, NN, TN, LOW, ADAPT, EACH };
 
 struct Args {
@@ -422,6 +424,16 @@ enum Sums { ROUNDED, PART, HELD, FIRST };
 template <class C, int MODE>
 constexpr int kTileLds = C::LDS + (MODE == ADAPT ? C::BM * (int)sizeof(Entry) + 16 : 0);
 
+// A tile, or a part of its contraction: steps come to LDS, STAGES - 1 of them
+// ahead, while the one that is there is multiplied.
+//
+// Few rows wait for the matrices' bytes, so tiles are small, for many
+// workgroups, and their steps long: 96 KiB are on the way on each compute unit
+// and four waves divide the step among them (512 rows over 64 matrices of 2048 x
+// 4096: 194 us, 5.2 TB/s; 8 rows over 16 of 1024 x 2048: 8 us).  With 50 to some
+// hundreds of rows for a matrix tiles grow, since LDS reads and loads from L2
+// bound them: 64 x 128 by two workgroups on a compute unit have 775 TFLOP/s, 128
+// x 128 some 1000.  Larger ones are ring_kernel's.
 template <typename T, class C, int MODE, bool F32, Sums SUMS>
 __device__ __forceinline__ void tile_body(const Args& g, char* smem, uint32_t index)
 {
@@ -722,12 +734,14 @@ __global__ __launch_bounds__(C::THREADS, C::PER_CU * C::WAVES / 4) void tile_ker
     tile_body<T, C, MODE, F32, SUMS>(g, smem, blockIdx.x);
 }
 
-// Few rows: the projections onto the rank, by the first workgroups, beside the
-// shared product, whose sums the next launch puts together with the adapters'
-// second products.  Up to 64 rows the shared product waits for bytes, the
-// projections stay in fp32 and finish_kernel ends the call (SUMS PART); above,
-// both wait for products, and tiles end it that have the sums as their FIRST
-// (SUMS HELD).
+// Few rows, or few tiles of a long contraction (plan_more): the projections onto
+// the rank, by the first workgroups, beside the shared product, whose sums the
+// next launch puts together with the adapters' second products.  Up to 64 rows
+// the shared product waits for bytes, the projections stay in fp32 and
+// finish_kernel ends the call (SUMS PART); above, both wait for products, and
+// tiles end it that have the sums as their FIRST (SUMS HELD).  64 rows, 14336 x
+// 4096, rank 16: 23 us, 5.2 TB/s; the call takes 39, and with the launches in
+// turn 53.
 struct PairArgs {
     Args low, base;
     uint32_t low_wgs;
@@ -765,7 +779,7 @@ __device__ __forceinline__ float sum_lanes(float x)
 // product of `rank` for each column, in fp32.  L lanes, 8 ranks each, have a
 // column, so that a load covers whole rows of `up` (with a lane to a column
 // those of rank 64 took 3 times as long).  What bounds it is the bytes of `up`,
-// read once for each row of its request.
+// read once for each row of its request (64 rows of 14336, rank 16: 6.8 us).
 template <typename T, int L>
 __global__ __launch_bounds__(256) void finish_kernel(const Args g, const int bm, const int bn)
 {
@@ -864,7 +878,8 @@ __device__ __forceinline__ void join8(const float* at, int64_t step, int parts, 
     }
 }
 
-// Joins the parts of every tile; a workgroup has 2048 elements of one.
+// Joins the parts of every tile; a workgroup has 2048 elements of one.  Bound by
+// the parts' bytes, 6 TB/s (and where they are few by the launch, 4 us).
 template <typename T, class C, int MODE, bool F32>
 __global__ __launch_bounds__(256) void join_kernel(const Args g)
 {
@@ -885,7 +900,14 @@ __global__ __launch_bounds__(256) void join_kernel(const Args g)
     join8<T, F32>(g.parts + (int64_t)t * (C::BM * C::BN) + x, (int64_t)all * (C::BM * C::BN), (int)g.splits.d, scale, d);
 }
 
-// Large tiles of NT, NN and TN: a workgroup for each compute unit walks them.
+// Large tiles of NT, NN, TN and EACH: a workgroup for each compute unit walks
+// them.  Four waves of 128 x 128 outputs read a third less from LDS than eight
+// of half of it, and the next tile's first loads are on the way while a tile's
+// outputs are written.  The matrix cores are busy for 89 to 90 % of the time
+// (by columns on both sides 71 %) and the board's power limits them: 16384 rows
+// over 8 matrices of 14336 x 4096 1306 us, 1473 TFLOP/s; gradients of 8192 rows
+// 686 us, 1402 TFLOP/s, and 749 us, 1284.  A tile costs some 5 us beside its
+// products, for its operands and its 65536 outputs.
 //
 // The tiles that are left for the last round, where they are half a round or
 // less, are divided along the contraction, so that all workgroups have a part;

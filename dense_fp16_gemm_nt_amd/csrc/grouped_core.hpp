@@ -30,7 +30,10 @@ using attn::Div;
 using attn::F16;
 using attn::s16x4;
 
-constexpr uint32_t kBeyond = 0x80000000u;   // an offset past the end of every buffer (they have less than 2^31 bytes)
+// An offset past the end of every buffer: they have less than 2^31 bytes (steps
+// of 512 rows by columns up to 2^32: there it names rows of the same matrix, for
+// columns that are not stored).
+constexpr uint32_t kBeyond = 0x80000000u;
 
 // Tile of BM rows of X by BN rows of Y, BK of the contraction at a time in a
 // ring of STAGES; WM x WN waves over the tile, and WK along the contraction,
