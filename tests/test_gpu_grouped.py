@@ -582,3 +582,52 @@ def test_a_serving_step():
     from tests import attention_ref
 
     attention_ref.prompt(q.cpu(), k.cpu(), v.cpu(), cu_host, cu_host, True, hd ** -0.5, O.cpu(), lse.cpu(), "attention of the projections")
+
+
+@pytest.mark.parametrize("lens", [[1], [3, 37], [100, 1, 60], [700, 0, 1500], [4352]])
+def test_adapters_of_no_contraction(lens):
+    rows, n, rank = sum(lens), 264, 16
+    A, B = torch.empty(rows, 0, dtype=torch.float16, device=DEV), torch.empty(n, 0, dtype=torch.float16, device=DEV)
+    down, up = torch.empty(2, rank, 0, dtype=torch.float16, device=DEV), torch.full((2, n, rank), 3.0, dtype=torch.float16, device=DEV)
+    D = g.adapter_product(A, B, down, up, ints(starts(lens)), ints([b % 3 - 1 for b in range(len(lens))]), D=kept("fp16", rows, n))
+    torch.cuda.synchronize()
+    assert bool((D == 0).all())
+
+
+@pytest.mark.parametrize("lens,n,k", [([5, 0, 9], 72, 264), ([300, 411, 77], 1032, 520), ([2100, 900, 2000], 4104, 264)])
+def test_one_matrix_for_all_groups(lens, n, k):
+    # matrices that are read may repeat
+    A, G, B, cu = inputs(whole, 17, "bf16", lens, n, k)
+    same, first = B[:1].expand(len(lens), n, k), B[:1]
+    D, dA = g.grouped_product(A, same, ints(cu)), g.grouped_product_grad_input(G, same, ints(cu))
+    one = ints([0, sum(lens)])
+    want, want_A = ref.product(A, first, [0, sum(lens)], D)[0], ref.grad_input(G, first, [0, sum(lens)], dA)[0]
+    torch.cuda.synchronize()
+    assert torch.equal(D, want.to(torch.bfloat16)) and torch.equal(dA, want_A.to(torch.bfloat16))
+    assert torch.equal(g.grouped_product(A, first, one), D)
+    with pytest.raises(g.GemmError):   # but not those that are written
+        g.grouped_product_grad_weight(G, A, ints(cu), dB=torch.empty_like(first).expand(len(lens), n, k))
+
+
+@pytest.mark.parametrize("rows", [64, 500, 6000])
+def test_few_rows_of_a_long_tensor(rows):
+    # a batch padded to its largest size: the tables say how many rows there are
+    gen = torch.Generator(device=DEV).manual_seed(rows)
+    n, k = 1032, 2056
+    A, B, down, up = whole(gen, "fp16", rows, k), whole(gen, "fp16", 2, n, k), whole(gen, "fp16", 2, 24, k), whole(gen, "fp16", 2, n, 24)
+    down[:, 8:] = 0
+    A[5:], G = NAN, whole(gen, "fp16", rows, n)
+    G[5:] = NAN
+    for cu in ([0, 2, 5], [0, 0, 0]):
+        D, E, dA = kept("fp16", rows, n), kept("fp16", rows, n), kept("fp16", rows, k)
+        g.grouped_product(A, B, ints(cu), D=D)
+        g.grouped_product_grad_input(G, B, ints(cu), dA=dA)
+        dB = g.grouped_product_grad_weight(G, A, ints(cu))
+        g.adapter_product(A / 8, B[0], down, up, ints(cu), ints([1, 0]), D=E)
+        torch.cuda.synchronize()
+        assert torch.equal(D, ref.product(A, B, cu, kept("fp16", rows, n))[0].to(torch.float16))
+        assert torch.equal(dA, ref.grad_input(G, B, cu, kept("fp16", rows, k))[0].to(torch.float16))
+        assert torch.equal(dB, ref.grad_weight(G, A, cu)[0].to(torch.float16))
+        assert bool((E[cu[-1]:] == 7).all())
+        if cu[-1]:
+            ref.check(E[:5], *[x[:5] for x in ref.adapters(A / 8, B[0], down, up, cu, [1, 0], None, kept("fp16", rows, n))], "adapters")
