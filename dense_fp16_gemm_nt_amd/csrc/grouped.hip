@@ -416,10 +416,11 @@ __device__ __forceinline__ void add_not_finite(const Args& g, const Entry* table
 }
 
 // What becomes of a tile's sums.  ROUNDED: they are outputs.  PART: of a part of
-// the contraction, in fp32 and in rows, for the launch that joins them.  HELD:
-// the same as they lie in the lanes, for the launch of tiles that has them as
-// FIRST sums, before the requests' part of the contraction, and no other.
-enum Sums { ROUNDED, PART, HELD, FIRST };
+// the contraction, in fp32, tile by tile, for the launch that joins them.
+// PLANE: the same as rows of a matrix like D, for finish_kernel.  HELD: as they
+// lie in the lanes, for the launch of tiles that has them as FIRST sums, before
+// the requests' part of the contraction, and no other.
+enum Sums { ROUNDED, PART, PLANE, HELD, FIRST };
 
 template <class C, int MODE>
 constexpr int kTileLds = C::LDS + (MODE == ADAPT ? C::BM * (int)sizeof(Entry) + 16 : 0);
@@ -437,7 +438,7 @@ constexpr int kTileLds = C::LDS + (MODE == ADAPT ? C::BM * (int)sizeof(Entry) + 
 template <typename T, class C, int MODE, bool F32, Sums SUMS>
 __device__ __forceinline__ void tile_body(const Args& g, char* smem, uint32_t index)
 {
-    constexpr bool XC = MODE == TN, YC = MODE == NN || MODE == TN, SPLIT = SUMS == PART || SUMS == HELD;
+    constexpr bool XC = MODE == TN, YC = MODE == NN || MODE == TN, SPLIT = SUMS == PART || SUMS == PLANE || SUMS == HELD;
     uint32_t part, slot;
     const Work wk = find_work<C::BM, C::BN, MODE, SPLIT>(g, index, &part, &slot);
     if (!wk.found) return;
@@ -576,6 +577,9 @@ __device__ __forceinline__ void tile_body(const Args& g, char* smem, uint32_t in
                 const f32x16& v = acc[b / C::FN][b % C::FN];
                 *held(slot, b, q) = f32x4{v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]};
             }
+    } else if constexpr (SUMS == PLANE) {
+        float* d = g.parts + ((int64_t)part * g.rows + wk.row0 + r0) * g.cols + wk.col0 + c0;
+        grp::store<T, C, true>(staging, (char*)d, 4 * (int64_t)g.cols, rows, cols, 1.f, acc, lane);
     } else if constexpr (SUMS == PART) {
         char* d = (char*)(g.parts + (int64_t)slot * (C::BM * C::BN) + r0 * C::BN + c0);
         grp::store<T, C, true>(staging, d, 4 * C::BN, rows, cols, 1.f, acc, lane);
@@ -734,14 +738,12 @@ __global__ __launch_bounds__(C::THREADS, C::PER_CU * C::WAVES / 4) void tile_ker
     tile_body<T, C, MODE, F32, SUMS>(g, smem, blockIdx.x);
 }
 
-// Few rows, or few tiles of a long contraction (plan_more): the projections onto
-// the rank, by the first workgroups, beside the shared product, whose sums the
-// next launch puts together with the adapters' second products.  Up to 64 rows
-// the shared product waits for bytes, the projections stay in fp32 and
-// finish_kernel ends the call (SUMS PART); above, both wait for products, and
-// tiles end it that have the sums as their FIRST (SUMS HELD).  64 rows, 14336 x
-// 4096, rank 16: 23 us, 5.2 TB/s; the call takes 39, and with the launches in
-// turn 53.
+// Few rows, or few tiles of a long contraction: the projections onto the rank,
+// by the first workgroups, beside the shared product, whose sums the next launch
+// puts together with the adapters' second products: finish_kernel, for which
+// both are in fp32 (SUMS PLANE), or, where requests have many rows, tiles that
+// have the sums as their FIRST (SUMS HELD).  64 rows, 14336 x 4096, rank 16: 23
+// us, 5.2 TB/s; the call takes 39, and with the launches in turn 53.
 struct PairArgs {
     Args low, base;
     uint32_t low_wgs;
@@ -753,7 +755,7 @@ __global__ __launch_bounds__(256, 2) void pair_kernel(const PairArgs p)
     static_assert(L::THREADS == 256 && C::THREADS == 256, "one launch");
     __shared__ __attribute__((aligned(1024))) char smem[kTileLds<C, ADAPT> > kTileLds<L, LOW> ? kTileLds<C, ADAPT> : kTileLds<L, LOW>];
     if (blockIdx.x < p.low_wgs)
-        tile_body<T, L, LOW, SUMS == PART, ROUNDED>(p.low, smem, blockIdx.x);
+        tile_body<T, L, LOW, SUMS == PLANE, ROUNDED>(p.low, smem, blockIdx.x);
     else
         tile_body<T, C, ADAPT, false, SUMS>(p.base, smem, blockIdx.x - p.low_wgs);
 }
@@ -774,18 +776,18 @@ __device__ __forceinline__ float sum_lanes(float x)
     return x;
 }
 
-// A row and 512 columns for a workgroup: the shared product's parts, which lie
-// in one row of tiles, and the second product of the row's adapter, a dot
+// A row and 512 columns for a workgroup: the shared product's parts, and the
+// second product of the row's adapter, a dot
 // product of `rank` for each column, in fp32.  L lanes, 8 ranks each, have a
 // column, so that a load covers whole rows of `up` (with a lane to a column
 // those of rank 64 took 3 times as long).  What bounds it is the bytes of `up`,
 // read once for each row of its request (64 rows of 14336, rank 16: 6.8 us).
 template <typename T, int L>
-__global__ __launch_bounds__(256) void finish_kernel(const Args g, const int bm, const int bn)
+__global__ __launch_bounds__(256) void finish_kernel(const Args g)
 {
     __shared__ float dots[512];
     const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, c0 = (int)blockIdx.x * 512 + 128 * w;
-    const int row0 = clampi(g.cu[0], 0, g.rows), r = (int)blockIdx.y, row = row0 + r;
+    const int row0 = clampi(g.cu[0], 0, g.rows), row = row0 + (int)blockIdx.y;
     if (row >= clampi(g.cu[g.groups], row0, g.rows)) return;
     int id = -1;   // the adapter of the row's request
     for (int base = 0; base < g.groups; base += 64) {
@@ -834,10 +836,9 @@ __global__ __launch_bounds__(256) void finish_kernel(const Args g, const int bm,
     }
     const int c = c0 + 2 * lane;
     if (c >= g.cols) return;
-    const uint32_t tile = (uint32_t)c / (uint32_t)bn;
-    const float* at = g.parts + ((int64_t)tile * bm + r) * bn + (c - (int)tile * bn);
+    const float* at = g.parts + (int64_t)row * g.cols + c;
     float x = 0.f, y = 0.f;
-    for (uint32_t p = 0; p < g.splits.d; ++p, at += (int64_t)g.col_tiles.d * bm * bn) {
+    for (uint32_t p = 0; p < g.splits.d; ++p, at += (int64_t)g.rows * g.cols) {
         const attn::f32x2 v = *reinterpret_cast<const attn::f32x2*>(at);
         x += v[0];
         y += v[1];
@@ -1292,19 +1293,20 @@ Plan plan(const Form* forms, int n, const Args& g, int cus, int* status)
             continue;
         }
         const double slots = (double)cus * f.per_cu;
-        double length = depth;
+        double extra = 0;
         if (MODE == ADAPT && g.adapters > 0) {   // a tile's requests, `rank` of the contraction each, at half the speed
             const double requests = g.groups < g.rows ? g.groups : g.rows, mean = g.rows / requests, mine = f.bm / mean + 1;
-            length += 16. * g.rank_chunks.d * (mine < requests ? mine : requests) + 256;
+            extra = (16. * g.rank_chunks.d * (mine < requests ? mine : requests) + 256) / 1024;
         }
         for (int64_t s = 1; s <= (f.split == nullptr ? 1 : kMaxSplits); s += s < 4 ? 1 : s / 2) {
-            const int64_t steps = ceil_div((int64_t)length, f.bk * s);
+            const int64_t steps = ceil_div((int64_t)depth, f.bk * s);
             if (s > 1 && (steps < 4 || most * s > kMaxTiles / 8)) break;   // a tile of the join has up to 8 workgroups
-            const double d = (double)(steps * f.bk) / 1024, wgs = tiles * s;
+            const double d = (double)(steps * f.bk) / 1024 + extra / s, wgs = tiles * s;
             const double full = (double)(int64_t)(wgs / slots), rest = wgs - full * slots;
             double us = 1.5 + full * (2.3 + two * d) + written;
             if (rest > 0) us += 2.3 + (rest > cus ? two : one) * d * (full == 0 ? longest : 1.);
             if (us < memory + 3) us = memory + 3;
+            if (s > 1) us += one * extra * (1 - 1. / s);   // they all go with the last part
             if (s > 1) us += 6 + wgs * f.bm * f.bn * 8 / 8e6;
             if (us < best.us) best = Plan{&f, most * s, s, s > 1 ? most * s * f.bm * f.bn * 4 : 0, false, us};
         }
@@ -1482,125 +1484,101 @@ struct AdapterCall {
     bool adapted, each;
     const void* single;   // all in one launch
     const void* pair;     // projections and shared product in one
-    const void* close;    // and what puts them together, for more than 64 rows
-    int bm, bn;           // and the shared product's tiles
+    const void* end;      // and what puts them together
+    bool dots;            // finish_kernel
     int64_t low_wgs;
     int cus;
     int64_t low_bytes, bytes;   // of the projections, and of all of the workspace
 };
 
-// The pair of launches for up to 64 rows, where the model finds it faster.
+// The pairs of launches, by the shared product's tiles and what ends the call.
+struct PairForm {
+    int bm, bn, bk;
+    Rate rate;
+    const void *plane, *held, *first;
+};
+
+template <typename T>
+struct PairForms {
+    PairForm f[4] = {{16, 16, 256, kTiny2, (const void*)&pair_kernel<T, Tiny2, Tiny2, PLANE>, nullptr, nullptr},
+                     {32, 32, 128, kSmall2, (const void*)&pair_kernel<T, Tiny2, Small2, PLANE>, nullptr, nullptr},
+                     {64, 64, 64, kSquare, (const void*)&pair_kernel<T, Tiny2, Square, PLANE>, nullptr, nullptr},
+                     {64, 128, 64, kOblong, (const void*)&pair_kernel<T, Tiny2, Oblong, PLANE>, (const void*)&pair_kernel<T, Tiny2, Oblong, HELD>,
+                      (const void*)&tile_kernel<T, Oblong, ADAPT, false, FIRST>}};
+};
+
+// A pair of launches, where the model finds it faster than the projections by
+// themselves and then the rest: for few rows, for requests of few rows, whose
+// parts of the contraction would fill their tiles with zeros, and with a long
+// contraction and few tiles, where the projections take as long as the rest.
+// (bf16, 4096 x 4096, 256 requests of one row, rank 64: 65 us, and 117
+// with the projections first; rank 16, one request of 195 rows, 2304 x 5376: 24 and,
+// with the projections first, 32; seven of 1226, 3032 x 384: 20 and 17.)
 void plan_pair(const adapter_desc* d, AdapterCall* c, int64_t* parts)
 {
-    const int bm = d->rows <= 16 ? 16 : d->rows <= 32 ? 32 : 64, bk = bm == 16 ? 256 : bm == 32 ? 128 : 64;
-    const Rate& rate = bm == 16 ? kTiny2 : bm == 32 ? kSmall2 : kSquare;
-    const double one = odd_pitch(c->rest) ? rate.odd_one : rate.one, two = odd_pitch(c->rest) ? rate.odd_two : rate.two;
-    const int64_t ct = ceil_div(d->N, bm), used = d->requests < d->rows ? d->requests : d->rows;
-    const int64_t low_wgs = (d->rows + used * 15) / 16 * ceil_div(d->rank, 16);
-    if (low_wgs > 2 * c->cus) return;
-    double best = 1e300;
-    int64_t splits = 1;
-    for (int64_t s = 1; s <= 8; s *= 2) {
-        const int64_t steps = ceil_div(d->K, bk * s), wgs = ct * s + low_wgs;
-        if (s > 1 && steps < 4) break;
-        const double depth = (double)(steps * bk) / 1024;
-        const int64_t full = wgs / (2 * c->cus), rest = wgs % (2 * c->cus);
-        double us = 1.5 + full * (2.3 + two * depth) + (rest > c->cus ? 2.3 + two * depth : rest > 0 ? 2.3 + one * depth : 0);
-        const double low = 1.5 + 2.3 + 1.8 * (double)d->K / 1024, memory = 3 + (double)d->N * d->K * 2 / 5.5e6;
-        if (us < low) us = low;
-        if (us < memory) us = memory;
-        us += (double)ct * s * bm * bm * 8 / 8e6;
-        if (us < best) {
-            best = us;
-            splits = s;
-        }
-    }
-    best += 4 + (double)d->rows * d->N * d->rank * 2 / 1e7;   // rows of `up` come from L2 more often than from memory
-    if (best >= c->plan.us + c->low_plan.us + 2) return;
-    const bool f16 = d->dtype == GROUPED_F16;
-    if (bm == 16)
-        c->pair = f16 ? (const void*)&pair_kernel<F16, Tiny2, Tiny2, PART> : (const void*)&pair_kernel<BF16, Tiny2, Tiny2, PART>;
-    else if (bm == 32)
-        c->pair = f16 ? (const void*)&pair_kernel<F16, Tiny2, Small2, PART> : (const void*)&pair_kernel<BF16, Tiny2, Small2, PART>;
-    else
-        c->pair = f16 ? (const void*)&pair_kernel<F16, Tiny2, Square, PART> : (const void*)&pair_kernel<BF16, Tiny2, Square, PART>;
-    c->bm = c->bn = bm;
-    c->low_wgs = low_wgs;
-    c->plan.splits = splits;
-    c->plan.wgs = ct * splits;
-    c->low.d_ld = 4 * d->rank;
-    c->low.cols = c->low.low_rows = d->rank;
-    c->low.col_tiles = attn::div_by(ceil_div(d->rank, 16));
-    c->low.row_tiles = (uint32_t)((d->rows + used * 15) / 16);
-    c->rest.row_tiles = 1;
-    c->rest.col_tiles = attn::div_by(ct);
-    c->rest.splits = attn::div_by(splits);
-    c->low_bytes = ceil_div(4 * d->rows * d->rank, 256) * 256;
-    *parts = ct * splits * bm * bm * 4;
-}
-
-// The pair of launches for more rows, where the model finds it faster: with a
-// long contraction and few tiles, where the projections take as long as the
-// rest.  (bf16, rank 16, 195 rows, 2304 x 5376: 24 us, and 32 with the
-// projections first; 1101 rows, 512 x 7680: 31 and 39.  1226 rows, 3032 x 384:
-// 20 and 17.)
-template <typename T, class C>
-void pair_of(AdapterCall* c)
-{
-    c->pair = (const void*)&pair_kernel<T, Tiny2, C, HELD>;
-    c->close = (const void*)&tile_kernel<T, C, ADAPT, false, FIRST>;
-    c->bm = C::BM;
-    c->bn = C::BN;
-}
-
-void plan_more(const adapter_desc* d, AdapterCall* c, int64_t* parts)
-{
+    static const PairForms<F16> f16;
+    static const PairForms<BF16> bf16;
+    const PairForm* forms = d->dtype == GROUPED_F16 ? f16.f : bf16.f;
     const int64_t used = d->requests < d->rows ? d->requests : d->rows;
-    const double slots = 2. * c->cus, depth = (double)d->K / 1024, memory = 3 + (double)(d->N + d->rows) * d->K * 2 / 5.5e6;
     const bool odd = odd_pitch(c->rest);
+    const double slots = 2. * c->cus, depth = (double)d->K / 1024, kinds = (double)(used < d->adapters ? used : d->adapters) * d->rank * 2;
+    const double memory = 1.5 + ((double)(d->N + d->rows) * d->K * 2 + kinds * d->K) / 5.6e6;
     const int64_t low_wgs = (d->rows + used * 15) / 16 * ceil_div(d->rank, 16);   // at most
-    const double low_mean = ((double)d->rows / 16 + 0.5 * used) * ceil_div(d->rank, 16);
+    const double low_rows = (double)d->rows / 16 + 0.5 * used, low_mean = (low_rows > used ? low_rows : (double)used) * ceil_div(d->rank, 16);
     const double low_one = odd ? kTiny2.odd_one : kTiny2.one, low_two = odd ? kTiny2.odd_two : kTiny2.two;
+    // finish_kernel reads `up` for each row, more often from L2 than from memory,
+    // and has 8 workgroups on a compute unit, each a chain of some 5 us
+    double dots = (double)d->rows * d->N * d->rank * 2 / 1e7;
+    if (dots < kinds * d->N / 5e6) dots = kinds * d->N / 5e6;
+    if (dots < (double)d->rows * ceil_div(d->N, 512) * 2.5e-3) dots = (double)d->rows * ceil_div(d->N, 512) * 2.5e-3;
+    dots = d->rows > 4096 ? 1e300 : dots + 4;
     double best = 1e300;
-    bool wide = false;
+    const PairForm* form = nullptr;
     int64_t splits = 1;
-    for (int i = 0; i < 2; ++i) {
-        const Rate& rate = i == 0 ? kSquare : kOblong;
-        const double one = odd ? rate.odd_one : rate.one, two = odd ? rate.odd_two : rate.two;
-        const int bm = 64, bn = i == 0 ? 64 : 128;
-        const int64_t tiles = ceil_div(d->rows, bm) * ceil_div(d->N, bn);
+    for (int i = d->rows <= 16 ? 0 : d->rows <= 32 ? 1 : 2; i < 4; ++i) {
+        const PairForm& f = forms[i];
+        const double one = odd ? f.rate.odd_one : f.rate.one, two = odd ? f.rate.odd_two : f.rate.two;
+        const int64_t tiles = ceil_div(d->rows, f.bm) * ceil_div(d->N, f.bn);
         for (int64_t s = 1; s <= kMaxSplits; s += s < 4 ? 1 : s / 2) {
-            const int64_t steps = ceil_div(d->K, 64 * s);
+            const int64_t steps = ceil_div(d->K, f.bk * s);
             if (low_wgs + tiles * s > kMaxTiles || (s > 1 && steps < 4)) break;
             // the launch's rounds, the projections counted as so many of the others
-            const double each = 2.3 + two * (double)(steps * 64) / 1024, wgs = (double)(tiles * s) + low_mean * (2.3 + low_two * depth) / each;
+            const double k = (double)(steps * f.bk) / 1024, each = 2.3 + two * k, wgs = (double)(tiles * s) + low_mean * (2.3 + low_two * depth) / each;
             const double full = (double)(int64_t)(wgs / slots), rest = wgs - full * slots;
-            double us = full * each + (rest > c->cus ? each : rest > 0 ? 2.3 + one * (double)(steps * 64) / 1024 : 0.);
+            const bool alone = full == 0 ? (double)(tiles * s) + low_mean <= c->cus : rest <= c->cus;   // on a compute unit
+            double us = full * each + (rest == 0 ? 0. : alone ? 2.3 + one * k : each);
             const double low = 2.3 + (low_mean > c->cus ? low_two : low_one) * depth;
             if (us < low) us = low;
             us += 1.5;
             if (us < memory) us = memory;
-            // and the next one's: requests of a tile as in plan()
-            const double mine = (double)bm / d->rows * used + 1, length = (2. * d->rank * (mine < used ? mine : used) + 256) / 1024;
+            const double by_dots = us + dots + (double)d->rows * d->N * s * 8 / 8e6;
+            if (by_dots < best) {
+                best = by_dots;
+                form = &f;
+                splits = s;
+                c->dots = true;
+            }
+            if (f.held == nullptr) continue;
+            // tiles with their requests' parts of the contraction as in plan()
+            const double mine = (double)f.bm / d->rows * used + 1, length = (2. * d->rank * (mine < used ? mine : used) + 256) / 1024;
             const int64_t rounds = (int64_t)(tiles / slots);
             const double more = tiles - rounds * slots;
-            us += 3.5 + rounds * (2.3 + two * length) + (more > c->cus ? 2.3 + two * length : more > 0 ? 2.3 + one * length : 0.);
-            us += (double)tiles * s * bm * bn * 8 / 8e6;
+            us += 3.5 + rounds * (2.3 + two * length) + (more > c->cus ? 2.3 + two * length : more > 0 ? 2.3 + one * length : 0.) +
+                  (double)tiles * s * f.bm * f.bn * 8 / 8e6;
             if (us < best) {
                 best = us;
-                wide = i > 0;
+                form = &f;
                 splits = s;
+                c->dots = false;
             }
         }
     }
-    if (best >= c->plan.us + c->low_plan.us) return;
-    if (d->dtype == GROUPED_F16)
-        wide ? pair_of<F16, Oblong>(c) : pair_of<F16, Square>(c);
-    else
-        wide ? pair_of<BF16, Oblong>(c) : pair_of<BF16, Square>(c);
-    const int64_t rt = ceil_div(d->rows, c->bm), ct = ceil_div(d->N, c->bn);
+    if (form == nullptr || best >= c->plan.us + c->low_plan.us + 1) return;
+    const int64_t rt = ceil_div(d->rows, form->bm), ct = ceil_div(d->N, form->bn), size = c->dots ? 4 : 2;
+    c->pair = c->dots ? form->plane : form->held;
+    c->end = !c->dots ? form->first : d->dtype == GROUPED_F16 ? finish<F16>(d->rank) : finish<BF16>(d->rank);
     c->each = false;
-    c->low.d_ld = 2 * d->rank;
+    c->low.d_ld = size * d->rank;
     c->low.cols = c->low.low_rows = d->rank;
     c->low.col_tiles = attn::div_by(ceil_div(d->rank, 16));
     c->low.row_tiles = (uint32_t)((d->rows + used * 15) / 16);
@@ -1610,11 +1588,11 @@ void plan_more(const adapter_desc* d, AdapterCall* c, int64_t* parts)
     c->rest.splits = attn::div_by(splits);
     c->plan.splits = splits;
     c->plan.wgs = rt * ct * splits;
-    c->low_bytes = ceil_div(2 * d->rows * d->rank, 256) * 256;
-    *parts = rt * ct * splits * c->bm * c->bn * 4;
+    c->low_bytes = ceil_div(size * d->rows * d->rank, 256) * 256;
+    *parts = c->dots ? d->rows * d->N * splits * 4 : rt * ct * splits * form->bm * form->bn * 4;
 }
 
-int run_pair(const AdapterCall& c, int dtype, int64_t rows, void* workspace, hipStream_t s)
+int run_pair(const AdapterCall& c, void* workspace, hipStream_t s)
 {
     PairArgs p;
     p.low = c.low;
@@ -1628,13 +1606,10 @@ int run_pair(const AdapterCall& c, int dtype, int64_t rows, void* workspace, hip
     Args g = p.base;
     g.adapters = c.rest.adapters;
     g.low = (const char*)workspace;
-    if (c.close != nullptr) return launch(c.close, c.plan.wgs / c.plan.splits, 256, &g, s);
-    int bm = c.bm, bn = c.bn;
-    void* a[] = {&g, &bm, &bn};
-    const int64_t rank = 8 * (int64_t)g.rank_chunks.d;
-    const void* f = dtype == GROUPED_F16 ? finish<F16>(rank) : finish<BF16>(rank);
-    const dim3 grid((unsigned)ceil_div(g.cols, 512), (unsigned)rows);
-    return hipLaunchKernel(f, grid, dim3(256), a, 0, s) == hipSuccess ? GEMM_F16_NT_OK : GEMM_F16_NT_LAUNCH;
+    if (!c.dots) return launch(c.end, c.plan.wgs / c.plan.splits, 256, &g, s);
+    void* a[] = {&g};
+    const dim3 grid((unsigned)ceil_div(g.cols, 512), (unsigned)g.rows);
+    return hipLaunchKernel(c.end, grid, dim3(256), a, 0, s) == hipSuccess ? GEMM_F16_NT_OK : GEMM_F16_NT_LAUNCH;
 }
 
 int plan_adapters(const adapter_desc* d, AdapterCall* c)
@@ -1642,7 +1617,8 @@ int plan_adapters(const adapter_desc* d, AdapterCall* c)
     int st = device_cus(&c->cus);
     if (st != GEMM_F16_NT_OK) return st;
     c->adapted = d->adapters > 0 && d->rank > 0;
-    c->single = c->pair = c->close = nullptr;
+    c->single = c->pair = c->end = nullptr;
+    c->dots = false;
     Args g = {};
     g.x = (const char*)d->A;
     g.cu = d->cu;
@@ -1716,8 +1692,7 @@ int plan_adapters(const adapter_desc* d, AdapterCall* c)
             return GEMM_F16_NT_OK;
         }
     }
-    if (c->adapted && d->rows <= 64) plan_pair(d, c, &parts);
-    if (c->adapted && d->rows > 64) plan_more(d, c, &parts);
+    if (c->adapted) plan_pair(d, c, &parts);
     if (c->pair == nullptr && c->plan.part_bytes > parts) parts = c->plan.part_bytes;
     c->bytes = c->low_bytes + parts;
     return GEMM_F16_NT_OK;
@@ -1766,7 +1741,7 @@ int adapter_nt(const adapter_desc* d, void* workspace, int64_t workspace_bytes, 
     if ((st = check_workspace(workspace, workspace_bytes, c.bytes)) != GEMM_F16_NT_OK) return st;
     if ((st = check_adapters(d, {workspace, c.bytes})) != GEMM_F16_NT_OK) return st;
     if (c.single != nullptr) return launch(c.single, ceil_div(c.rest.cols, 16), 256, &c.rest, (hipStream_t)stream);
-    if (c.pair != nullptr) return run_pair(c, d->dtype, d->rows, workspace, (hipStream_t)stream);
+    if (c.pair != nullptr) return run_pair(c, workspace, (hipStream_t)stream);
     char* parts = (char*)workspace + c.low_bytes;
     if (c.adapted) {
         c.low.d = (char*)workspace;

@@ -100,9 +100,9 @@ int grouped_tn_check(const grouped_desc* d);
  * and a request is any number of rows: a prompt, or one token.
  *
  * scale_a * (down_a A[r]) is summed in fp32 and, as an operand of the second
- * product, rounded to the operands' type at most once (calls of up to 64 rows
- * may keep it in fp32), so it has to lie in that type's range; everything else
- * is one sum in fp32, rounded once. */
+ * product, rounded to the operands' type at most once (calls with few rows for
+ * a request keep it in fp32), so it has to lie in that type's range;
+ * everything else is one sum in fp32, rounded once. */
 typedef struct adapter_desc {
     int32_t dtype;
     int32_t rank;          /* at most 128; smaller adapters are padded with zeros */

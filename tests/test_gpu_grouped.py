@@ -190,6 +190,12 @@ ADAPTERS = [
     ([70], [2], 2056, 2048, 8),
     ([300, 1, 411], [3, 3, 0], 1032, 4104, 128),
     ([65, 2, 700, 0, 1], [-1, 0, 2, 1, 9], 264, 7688, 24),
+    ([1] * 300, [b % 5 - 1 for b in range(300)], 4104, 2056, 64),   # more single tokens than tiles have rows
+    ([2, 1, 0, 3] * 25, [b * 7 % 4 for b in range(100)], 1032, 1032, 128),
+    ([1] * 100, [b % 6 - 1 for b in range(100)], 14344, 520, 8),
+    ([200, 200], [1, 0], 2048, 4096, 64),                           # few tiles, requests of many rows
+    ([128, 70, 1, 57], [2, 0, -1, 3], 520, 4104, 64),
+    ([100, 90], [3, 1], 1032, 1544, 128),
 ]
 
 
@@ -295,7 +301,7 @@ def test_adapters_that_no_row_asks_for(case):
     assert torch.equal(D, want.to(torch.float16))
 
 
-SPOILT = [ADAPTERS[i] for i in (6, 7, 8, 9, 10, 13, 14, 15, 16, 17, 18, 20, 21, 22, 24, 25)] + [
+SPOILT = [ADAPTERS[i] for i in (6, 7, 8, 9, 10, 13, 14, 15, 16, 17, 18, 20, 21, 22, 24, 25, 26, 27, 28, 29, 30, 31)] + [
     ([1, 2], [0, 1], 264, 1032, 16), ([2, 1, 1], [2, 0, 1], 72, 520, 8), ([3, 90], [1, 2], 136, 200, 8), ([1] * 200, [b % 4 for b in range(200)], 136, 72, 8)]
 
 
