@@ -637,3 +637,34 @@ def test_few_rows_of_a_long_tensor(rows):
         assert bool((E[cu[-1]:] == 7).all())
         if cu[-1]:
             ref.check(E[:5], *[x[:5] for x in ref.adapters(A / 8, B[0], down, up, cu, [1, 0], None, kept("fp16", rows, n))], "adapters")
+
+
+@pytest.mark.parametrize("lens,n,k,rank", [([1], 264, 1032, 16), ([1] * 8, 264, 520, 24), ([1] * 100, 1032, 2056, 16), ([200, 200], 2048, 4096, 64), ([700, 3, 90], 520, 264, 40), ([2100, 900], 4104, 1032, 64)])
+def test_adapters_captured_and_on_two_streams(lens, n, k, rank):
+    gen = torch.Generator(device=DEV).manual_seed(51)
+    rows = sum(lens)
+    A, B, down, up = whole(gen, "fp16", rows, k), whole(gen, "fp16", n, k), whole(gen, "fp16", 4, rank, k), whole(gen, "fp16", 4, n, rank)
+    down[:, 8:] = 0
+    cu, ids = ints(starts(lens)), ints([b % 5 - 1 for b in range(len(lens))])
+    scales = torch.tensor([1.0, 0.5, 0.25, -0.125], device=DEV)
+    D = torch.zeros(rows, n, dtype=torch.float16, device=DEV)
+    g.adapter_product(A, B, down, up, cu, ids, scales, D=D)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        g.adapter_product(A, B, down, up, cu, ids, scales, D=D)
+    other = torch.cuda.Stream()
+    for step in range(4):
+        A.copy_(whole(gen, "fp16", rows, k))
+        ids.copy_(torch.randint(-1, 5, ids.shape, generator=gen, device=DEV))
+        if step > 1:   # fewer rows in use
+            cu.clamp_(max=max(1, rows // step))
+        D.fill_(7)
+        torch.cuda.synchronize()
+        graph.replay()
+        with torch.cuda.stream(other):   # at the same time
+            beside = g.adapter_product(A, B, down, up, cu, ids, scales, D=torch.full_like(D, 7))
+        torch.cuda.synchronize()
+        alone = g.adapter_product(A, B, down, up, cu, ids, scales, D=torch.full_like(D, 7))
+        torch.cuda.synchronize()
+        assert torch.equal(D, alone) and torch.equal(beside, alone), step
