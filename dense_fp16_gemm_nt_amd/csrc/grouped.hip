@@ -1514,7 +1514,7 @@ struct PairForms {
 // (bf16, 4096 x 4096, 256 requests of one row, rank 64: 65 us, and 117
 // with the projections first; rank 16, one request of 195 rows, 2304 x 5376: 24 and,
 // with the projections first, 32; seven of 1226, 3032 x 384: 20 and 17.)
-void plan_pair(const adapter_desc* d, AdapterCall* c, int64_t* parts)
+void plan_pair(const adapter_desc* d, AdapterCall* c, int64_t* parts, double* two)
 {
     static const PairForms<F16> f16;
     static const PairForms<BF16> bf16;
@@ -1573,7 +1573,8 @@ void plan_pair(const adapter_desc* d, AdapterCall* c, int64_t* parts)
             }
         }
     }
-    if (form == nullptr || best >= c->plan.us + c->low_plan.us + 1) return;
+    if (form == nullptr || best >= *two) return;
+    *two = best;
     const int64_t rt = ceil_div(d->rows, form->bm), ct = ceil_div(d->N, form->bn), size = c->dots ? 4 : 2;
     c->pair = c->dots ? form->plane : form->held;
     c->end = !c->dots ? form->first : d->dtype == GROUPED_F16 ? finish<F16>(d->rank) : finish<BF16>(d->rank);
@@ -1675,15 +1676,18 @@ int plan_adapters(const adapter_desc* d, AdapterCall* c)
         }
     }
     if (st != GEMM_F16_NT_OK) return st;
+    double two = c->plan.us + (c->adapted ? c->low_plan.us : 0.) + 1;   // what two launches take
+    if (c->adapted) plan_pair(d, c, &parts, &two);
     const int64_t blocks = d->requests * ceil_div(d->rank, 16);
     if (c->adapted && d->rows <= 16 && blocks <= 3) {
         // rounds of the compute units, each with what starting a workgroup
-        // costs and its tile's share of the contraction.  Measured on MI355X:
-        // 4096 x 4096, one request of rank 16 10.2 us (two launches 22), three
-        // 16.0, 1024 x 1024 5.0 and 7.5 (13); 14336 x 4096 34.4 and, in two
-        // launches, 39.6.  Seven blocks took as long as two launches do.
+        // costs and its tile's share of the contraction.  Measured on MI355X,
+        // in one launch and in a pair: one request of rank 16, 4096 x 4096 10.3
+        // and 13.0 us, 1024 x 1024 5.3 and 7.6, 4096 x 14336 23 and 29; three
+        // 16.0 and 13.8, 8.0 and 7.5 (where the host's second launch counts),
+        // 30 and 30.
         const double us = 1.5 + (double)ceil_div(ceil_div(d->N, 16), c->cus) * (2.0 + (blocks == 1 ? 1.65 : 3.0) * (double)d->K / 1024);
-        if (us < c->plan.us + c->low_plan.us + 2) {
+        if (us < two) {
             if (d->dtype == GROUPED_F16)
                 c->single = blocks == 1 ? (const void*)&single_kernel<F16, 1> : (const void*)&single_kernel<F16, 3>;
             else
@@ -1692,7 +1696,6 @@ int plan_adapters(const adapter_desc* d, AdapterCall* c)
             return GEMM_F16_NT_OK;
         }
     }
-    if (c->adapted) plan_pair(d, c, &parts);
     if (c->pair == nullptr && c->plan.part_bytes > parts) parts = c->plan.part_bytes;
     c->bytes = c->low_bytes + parts;
     return GEMM_F16_NT_OK;
