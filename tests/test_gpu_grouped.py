@@ -196,6 +196,7 @@ ADAPTERS = [
     ([200, 200], [1, 0], 2048, 4096, 64),                           # few tiles, requests of many rows
     ([128, 70, 1, 57], [2, 0, -1, 3], 520, 4104, 64),
     ([100, 90], [3, 1], 1032, 1544, 128),
+    ([4096, 2, 4094], [1, 3, 2], 4096, 2048, 128),                  # large tiles of several requests, a rank above 64
 ]
 
 
