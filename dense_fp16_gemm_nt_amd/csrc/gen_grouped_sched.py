@@ -19,10 +19,10 @@ to back), two LDS stages.  The A side (rows of the output) and the B side
       ds_read_b64_tr_b16, each 4 elements of the contraction for 16 columns
       and 4 groups of lanes.
 
-Three loops are generated: RR, RC and CC, for the grouped products NT, NN and
-TN.  Each is a macro with the operands' type, "f16" or "bf16", as its argument,
-and ends with one of two epilogues: outputs rounded to that type, or, where
-%[wide] is not 0, in 32 bits.
+The loops that are generated are RR, RC and CC, for the grouped products NT, NN
+and TN, and RR2, for adapters.  Each is a macro with the operands' type, "f16"
+or "bf16", as its argument, and ends with one of two epilogues: outputs rounded
+to that type, or, where %[wide] is not 0, in 32 bits.
 
 LDS: the A side's stages at 0 and 32 KiB, the B side's at 64 and 96 KiB, so
 that one address and an instruction offset reach both stages, then 8 KiB for
@@ -55,7 +55,9 @@ own (the second product of a low-rank adapter, up to 64 elements of its
 contraction): where %[ext] is not 0, step 0 is loaded from %[rsa0] (rows of 128
 bytes, lane offsets %[ha0], %[ha1] for even and odd loads) and %[rsb0] (lane
 offsets %[hb0], %[hb1], %[sb8] bytes for 8 rows), and the contraction's first
-step, with its masks, is step 1.
+step, with its masks, is step 1.  RR2 is RR with two such steps, the second from
+%[rsa1] and again %[rsb0]; a step 0 of its own then loads the contraction's
+first, masked, as step 2.  It needs four steps in all where it has these.
 
 Operands: load offsets %[axQ], %[bxQ] (less 1024 * (Q mod 4), the instruction
 offset of the load); fragment addresses %[raN], %[rbN] (N: sub-step by rows,
@@ -171,8 +173,9 @@ class Emitter(ring4.Emitter):
             self.epi_emit(*self.epi_q.pop(0))
 
 
-def emit_step(e: Emitter, stage: int, first: bool, ahead: bool, has_next: bool, last: bool, tail: list[str], p: dict) -> None:
-    """One step reading `stage`.  ahead: it loads step j + 2; has_next: step j + 1 exists; last: with the epilogue."""
+def emit_step(e: Emitter, stage: int, first: bool, ahead: bool, has_next: bool, last: bool, tail: list[str], p: dict, masked: bool = False) -> None:
+    """One step reading `stage`.  ahead: it loads step j + 2 (masked: which is the contraction's first); has_next: step j + 1
+    exists; last: with the epilogue."""
     ng = KSUB * NQ
     gaps: list[list[tuple]] = [[] for _ in range(ng)]
     late = late_rows4(p)
@@ -217,7 +220,9 @@ def emit_step(e: Emitter, stage: int, first: bool, ahead: bool, has_next: bool, 
                     g = first_free(m + 1)
                 gaps[m].append(("text", Emitter.m0(op, q, stage)))
                 group = (op, q // 4)
-            gaps[g].append(("text", Emitter.load(op, q, "kh")))
+            if masked:
+                gaps[g].append(("text", f"v_or_b32 %[ht], %[{op}x{q}], %[hm{q % 2}]"))
+            gaps[g].append(("text", Emitter.load(op, q, "kh", "%[ht]" if masked else None)))
             loads.append(g)
             prev = g
         assert prev < ng - 8, "loads run into the tail"
@@ -322,10 +327,10 @@ def generate(la: str, lb: str, p: dict) -> str:
     adv = [f"s_add_u32 %[kh{op}], %[kh{op}], {side_steps(op, layout[op])}" for op in "ab"]
     sub, cmp2 = "s_sub_u32 %[rem], %[rem], 1", "s_cmp_eq_u32 %[rem], 2"
 
-    def step(stage, first, ahead, has_next, last, tail):
+    def step(stage, first, ahead, has_next, last, tail, masked=False):
         pending = list(e.lgkm) if first else []
         e.lgkm = pending
-        emit_step(e, stage, first, ahead, has_next, last, tail, p)
+        emit_step(e, stage, first, ahead, has_next, last, tail, p, masked)
 
     e.op("s_cmp_eq_u32 %[first], 0")
     e.op("s_cbranch_scc1 15f")
@@ -343,25 +348,32 @@ def generate(la: str, lb: str, p: dict) -> str:
     if layout == {"a": "r", "b": "r"}:
         e.op("s_cmp_eq_u32 %[ext], 0")
         e.op("s_cbranch_scc1 11f")
-        for q in range(8):
-            if q % 4 == 0:
-                e.op(f"s_mov_b32 %[kha], {4096 * (q // 4)}")
-                e.op(Emitter.m0("a", q, 0))
+        for term in range(p.get("leads", 1)):
+            for q in range(8):
+                if q % 4 == 0:
+                    e.op(f"s_mov_b32 %[kha], {4096 * (q // 4)}")
+                    e.op(Emitter.m0("a", q, term))
+                    e.op("s_nop 0")
+                off = f" offset:{1024 * (q % 4)}" if q % 4 else ""
+                e.op(f"buffer_load_dwordx4 %[ha{q % 2}], %[rsa{term}], %[kha] offen{off} lds")
+            for q in range(8):
+                e.op(f"s_mul_i32 %[khb], %[sb8], {q}")
+                e.op(f"s_add_u32 m0, %[lb], {SIDE_B + STAGE_BYTES * term + 1024 * q}")
                 e.op("s_nop 0")
-            off = f" offset:{1024 * (q % 4)}" if q % 4 else ""
-            e.op(f"buffer_load_dwordx4 %[ha{q % 2}], %[rsa0], %[kha] offen{off} lds")
-        for q in range(8):
-            e.op(f"s_mul_i32 %[khb], %[sb8], {q}")
-            e.op(f"s_add_u32 m0, %[lb], {SIDE_B + 1024 * q}")
-            e.op("s_nop 0")
-            e.op(f"buffer_load_dwordx4 %[hb{q % 2}], %[rsb0], %[khb] offen lds")
-        loads(1, True, 1)
-        e.op("s_branch 12f")
+                e.op(f"buffer_load_dwordx4 %[hb{q % 2}], %[rsb0], %[khb] offen lds")
+        if p.get("leads", 1) == 1:
+            loads(1, True, 1)
+            e.op("s_branch 12f")
+        else:   # a step 0 of its own, which loads the contraction's first
+            rest(0, str(NLOAD))
+            for op in "ab":
+                e.op(f"s_mov_b32 %[kh{op}], 0")
+            step(0, True, True, True, False, adv + [sub, cmp2, "s_cbranch_scc1 6f", "s_branch 1f"], True)
         e.label("11")
     loads(0, True, 0)
     advance()
     loads(1, False, 1)
-    if layout == {"a": "r", "b": "r"}:
+    if layout == {"a": "r", "b": "r"} and p.get("leads", 1) == 1:
         e.label("12")
     rest(0, str(NLOAD))
     zero = list(e.lgkm)   # the reads under way at label 20, from either side
@@ -420,6 +432,7 @@ COLS = {**ROWS, "rel": 14, "pub": 48}
 
 LOOPS = {   # macro: A side, B side, schedule
     "G16_GROUPED_RR": ("r", "r", ROWS),
+    "G16_GROUPED_RR2": ("r", "r", {**ROWS, "leads": 2}),
     "G16_GROUPED_RC": ("r", "c", MIXED),
     "G16_GROUPED_CC": ("c", "c", COLS),
 }

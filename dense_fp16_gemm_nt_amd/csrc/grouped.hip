@@ -27,10 +27,16 @@ using grp::F16;
 // LOW the adapters' projections onto their rank, a product NT whose matrix a
 // table chooses and whose result is scaled; ADAPT the shared projection, with
 // the adapters' second products added to the same sums; EACH the same in large
-// tiles, which have rows of one request each.  LOW's results are operands of
-// the second product, and rounded to its type for that: the matrix cores take
-// 32-bit operands at a sixteenth of the rate.
-enum Mode { NT, NN, TN, LOW, ADAPT, EACH };
+// tiles, which have rows of one request each, for ranks up to 32, and EACH2 for
+// ranks above.  LOW's results are operands of the second product, as two terms
+// each (grp::upper): the matrix cores take 32-bit operands at a sixteenth of
+// the rate, and one term of 16 bits shows in the outputs (bf16, rank 64: 1.4e-3
+// of their norm off the 32-bit values; with two 8.6e-5, as sums in another
+// order).  What that costs: requests of some ten rows and a rank of 16, 35.0 us
+// for 34.1, of 128 58.3 for 49.8 (90 of them, 2304 x 2048); prompts of rank 64
+// 177.6 for 177.0 (4096 x 4096, 6206 rows).
+enum Mode { NT, NN, TN, LOW, ADAPT, EACH, EACH2 };
+constexpr bool each_request(int mode) { return mode == EACH || mode == EACH2; }
 
 struct Args {
     const char* x;
@@ -44,7 +50,7 @@ struct Args {
     int x_cols;          // TN: rows of a group's D, which are columns of X
     int depth;           // the contraction, except for TN
     int low_rows;        // LOW: rows of `down`; columns behind them are zeros
-    int rank;            // EACH
+    int rank;            // EACH, EACH2
     Div col_tiles;
     Div per_group;       // TN: tiles of a group, padded to whole rounds of the XCDs
     uint32_t group_tiles;
@@ -56,13 +62,15 @@ struct Args {
     // adapters
     const int32_t* ids;
     const float* scales;
-    const char* low;     // LOW's results, rows of `rank`
+    const char* low;     // LOW's results, rows of `rank` (EACH, EACH2: of 128 bytes)
+    int64_t low_rest;    // bytes from their upper to their lower terms
     const char* down;
     int64_t down_ld, down_mat;
     const char* up;
     int64_t up_ld, up_mat;
     int adapters;
     Div rank_chunks;
+    Div term_chunks;     // twice as many: both terms
 };
 
 __device__ __forceinline__ int clampi(int x, int lo, int hi) { return x < lo ? lo : x > hi ? hi : x; }
@@ -271,9 +279,10 @@ __device__ __forceinline__ void load_all(const char* const* p, uint32_t dst, std
 
 // ADAPT: the adapters' second products are more of the contraction.  The
 // requests with an adapter that a tile's rows belong to, one after the other,
-// have `rank` elements of it each, in which a row meets its own request's part
-// and zeros elsewhere.  A table in LDS says which they are.
-struct Entry {
+// have twice `rank` elements of it each, the upper and the lower terms of what
+// LOW left, in which a row meets its own request's part and zeros elsewhere.  A
+// table in LDS says which they are.
+struct alignas(8) Entry {
     int16_t first, end;   // rows of the tile
     int32_t id;
 };
@@ -303,6 +312,20 @@ __device__ __forceinline__ int fill_table(const Args& g, const Work& wk, Entry* 
     return count < BM ? count : BM;
 }
 
+// Whose a chunk of the requests' part of the contraction is, and which of its.
+// Without a branch: loads of several chunks then look it up at once.
+__device__ __forceinline__ Entry entry_of(const Args& g, const Entry* table, int count, int at, int* in)
+{
+    const int q = (int)g.term_chunks.of((uint32_t)at);
+    *in = at - q * (int)g.term_chunks.d;
+    Entry e = table[q < count ? q : count - 1];
+    if (q >= count) {
+        e.end = e.first;
+        e.id = -1;
+    }
+    return e;
+}
+
 // The loads of step s of the requests' part of the contraction; `low` is the
 // tile's first row.
 template <class C>
@@ -312,24 +335,24 @@ __device__ __forceinline__ void load_requests(const Args& g, const Work& wk, con
     using SY = grp::Side<C, false, C::BN>;
     const char* px[SX::LOADS];
     const char* py[SY::LOADS];
+    const int chunks = (int)g.rank_chunks.d;
     auto where = [&](int chunk, int* in) {
-        const int at = s * (C::BK / 8) + chunk, q = (int)g.rank_chunks.of((uint32_t)at);
-        *in = at - q * (int)g.rank_chunks.d;
-        return q < count ? table[q] : Entry{0, 0, -1};
+        return entry_of(g, table, count, s * (C::BK / 8) + chunk, in);
     };
 #pragma unroll
     for (int i = 0; i < SX::LOADS; ++i) {
         int in;
         const Entry e = where(SX::chunk(i, tid), &in);
         const int r = SX::row(i, tid);
-        px[i] = r >= e.first && r < e.end ? low + ((int64_t)r * g.rank_chunks.d + in) * 16 : (const char*)g_nothing;
+        const char* p = low + (int64_t)r * (16 * chunks) + 16 * in + (in < chunks ? 0 : g.low_rest - 16 * chunks);
+        px[i] = r >= e.first && r < e.end ? p : (const char*)g_nothing;
     }
 #pragma unroll
     for (int i = 0; i < SY::LOADS; ++i) {
         int in;
         const Entry e = where(SY::chunk(i, tid), &in);
         const int r = wk.col0 + SY::row(i, tid);
-        py[i] = e.id >= 0 && r < g.cols ? g.up + (int64_t)e.id * g.up_mat + (int64_t)r * g.up_ld + 16 * in : (const char*)g_nothing;
+        py[i] = e.id >= 0 && r < g.cols ? g.up + (int64_t)e.id * g.up_mat + (int64_t)r * g.up_ld + 16 * (in < chunks ? in : in - chunks) : (const char*)g_nothing;
     }
     load_all<C::THREADS * 16>(px, dst, std::make_integer_sequence<int, SX::LOADS>());
     load_all<C::THREADS * 16>(py, dst + C::X_BYTES, std::make_integer_sequence<int, SY::LOADS>());
@@ -400,7 +423,8 @@ __device__ __forceinline__ void add_not_finite(const Args& g, const Entry* table
                 if (bad == 0) continue;
                 const attn::f32x2 u = T::unpack(up[p]);
                 for (int r = first; r < end; ++r) {
-                    const attn::f32x2 h = T::unpack(*reinterpret_cast<const uint32_t*>(low + (int64_t)r * (16 * g.rank_chunks.d) + 4 * p));
+                    const attn::f32x2 h = T::unpack(*reinterpret_cast<const uint32_t*>(low + (int64_t)r * (16 * g.rank_chunks.d) + 4 * p)) +
+                                          T::unpack(*reinterpret_cast<const uint32_t*>(low + g.low_rest + (int64_t)r * (16 * g.rank_chunks.d) + 4 * p));
                     const float x = (bad & 0x8000u ? h[0] * u[0] : 0.f) + (bad & 0x80000000u ? h[1] * u[1] : 0.f);
                     char* at = d + (int64_t)(r - r0) * ld + (F32 ? 4 : 2) * c;
                     if constexpr (F32) {
@@ -536,7 +560,7 @@ __device__ __forceinline__ void tile_body(const Args& g, char* smem, uint32_t in
         __syncthreads();
         requests = __builtin_amdgcn_readfirstlane(*count);
         for (int s = own; s < C::STAGES - 1; ++s) load_more();
-        steps += (requests * (int)g.rank_chunks.d + C::BK / 8 - 1) / (C::BK / 8);
+        steps += (requests * (int)g.term_chunks.d + C::BK / 8 - 1) / (C::BK / 8);
     } else {
         for (int s = 0; s < C::STAGES - 1; ++s) load();
     }
@@ -579,17 +603,25 @@ __device__ __forceinline__ void tile_body(const Args& g, char* smem, uint32_t in
             }
     } else if constexpr (SUMS == PLANE) {
         float* d = g.parts + ((int64_t)part * g.rows + wk.row0 + r0) * g.cols + wk.col0 + c0;
-        grp::store<T, C, true>(staging, (char*)d, 4 * (int64_t)g.cols, rows, cols, 1.f, acc, lane);
+        grp::store<T, C, true>(staging, (char*)d, 4 * (int64_t)g.cols, rows, cols, acc, lane);
     } else if constexpr (SUMS == PART) {
         char* d = (char*)(g.parts + (int64_t)slot * (C::BM * C::BN) + r0 * C::BN + c0);
-        grp::store<T, C, true>(staging, d, 4 * C::BN, rows, cols, 1.f, acc, lane);
+        grp::store<T, C, true>(staging, d, 4 * C::BN, rows, cols, acc, lane);
         if (MODE == ADAPT && bad) add_not_finite<T, true>(g, table, requests, low, d, 4 * C::BN, r0, wk.col0 + c0, min(rows, OWN_ROWS), min(cols, OWN_COLS), lane);
     } else {
-        float scale = 1.f;
-        if (MODE == LOW && g.scales != nullptr) scale = g.scales[g.ids[wk.group]];
         char* d = g.d + (MODE == TN ? (int64_t)wk.group * g.d_mat + (int64_t)(wk.tile0 + r0) * g.d_ld : (int64_t)(wk.row0 + r0) * g.d_ld) +
                   (int64_t)(wk.col0 + c0) * (F32 ? 4 : 2);
-        grp::store<T, C, F32>(staging, d, g.d_ld, rows, cols, scale, acc, lane);
+        if constexpr (MODE == LOW) {
+            const float scale = g.scales != nullptr ? g.scales[g.ids[wk.group]] : 1.f;
+            if constexpr (F32) {
+                grp::store<T, C, true>(staging, d, g.d_ld, rows, cols, acc, lane, [&](float v) { return v * scale; });
+            } else {
+                grp::store<T, C, false>(staging, d, g.d_ld, rows, cols, acc, lane, [&](float v) { return grp::upper<T>(v * scale); });
+                grp::store<T, C, false>(staging, d + g.low_rest, g.d_ld, rows, cols, acc, lane, [&](float v) { return v * scale - grp::upper<T>(v * scale); });
+            }
+        } else {
+            grp::store<T, C, F32>(staging, d, g.d_ld, rows, cols, acc, lane);
+        }
         if (MODE == ADAPT && bad) add_not_finite<T, false>(g, table, requests, low, d, g.d_ld, r0, wk.col0 + c0, min(rows, OWN_ROWS), min(cols, OWN_COLS), lane);
     }
 }
@@ -598,10 +630,10 @@ __device__ __forceinline__ void tile_body(const Args& g, char* smem, uint32_t in
 // projections come with the shared one, as further columns of the same
 // product, whose tile has 16 rows of the shared matrix and RB blocks of 16 rows
 // of `down`, so many of each request.  Their sums are the second product's
-// operand as they lie in the accumulators: the order of that contraction is
-// free, and `up` is read to match.  What bounds it is the latency of a chain:
-// arguments, the first loads, the bytes (24 to 40 KiB in flight on a compute
-// unit), the sums of four waves.  So the shared matrix is asked for before the
+// operand as they lie in the accumulators, two terms of each: the order of that
+// contraction is free, and `up` is read to match.  What bounds it is the latency
+// of a chain: arguments, the first loads, the bytes (24 to 40 KiB in flight on a
+// compute unit), the sums of four waves.  So the shared matrix is asked for before the
 // requests' rows are known, which are read as scalars, by themselves.
 template <typename T, int RB>
 __global__ __launch_bounds__(256, 1) void single_kernel(const Args g)
@@ -718,17 +750,21 @@ __global__ __launch_bounds__(256, 1) void single_kernel(const Args g)
     for (int b = 0; b < RB; ++b) {
         const f32x16& h = sums[0][(b + 1) / 2];
         const int at = (b + 1) % 2 * 8;
-        u32x4 low;
+        u32x4 upper, lower;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) low[i] = T::pack(h[at + 2 * i] * scale[b], h[at + 2 * i + 1] * scale[b]);
-        const f32x16 sum = T::mfma(u[b], low, d);
+        for (int i = 0; i < 4; ++i) {
+            const grp::Terms t = grp::terms<T>(h[at + 2 * i] * scale[b], h[at + 2 * i + 1] * scale[b]);
+            upper[i] = t.upper;
+            lower[i] = t.lower;
+        }
+        const f32x16 sum = T::mfma(u[b], lower, T::mfma(u[b], upper, d));
         const bool own = m >= first[b] && m < end[b];   // a lane's sums are one row's
 #pragma unroll
         for (int i = 0; i < 16; ++i) d[i] = own ? sum[i] : d[i];
     }
     using O = Cfg<16, 16, 512, 1, 1, 4, 4, 1>;
     Acc<O> out = {{d}};
-    grp::store<T, O, false>(smem + 3 * FN * 4096, g.d + (int64_t)row0 * g.d_ld + 2 * (int64_t)col0, g.d_ld, rows, g.cols - col0, 1.f, out, lane);
+    grp::store<T, O, false>(smem + 3 * FN * 4096, g.d + (int64_t)row0 * g.d_ld + 2 * (int64_t)col0, g.d_ld, rows, g.cols - col0, out, lane);
 }
 
 template <typename T, class C, int MODE, bool F32, Sums SUMS>
@@ -860,22 +896,30 @@ const void* finish(int64_t rank)
                         : (const void*)&finish_kernel<T, 16>;
 }
 
-// Eight columns of a row: the parts' sums added up in order, scaled, rounded once.
-template <typename T, bool F32>
-__device__ __forceinline__ void join8(const float* at, int64_t step, int parts, float scale, char* d)
+// Eight columns of a row: the parts' sums added up in order.
+__device__ __forceinline__ void join8(const float* at, int64_t step, int parts, float (&v)[8])
 {
     f32x4 lo = {0.f, 0.f, 0.f, 0.f}, hi = lo;
     for (int p = 0; p < parts; ++p, at += step) {
         lo += *reinterpret_cast<const f32x4*>(at);
         hi += *reinterpret_cast<const f32x4*>(at + 4);
     }
-    lo *= scale;
-    hi *= scale;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        v[e] = lo[e];
+        v[4 + e] = hi[e];
+    }
+}
+
+// Writes them, rounded (or as they are, F32).
+template <typename T, bool F32>
+__device__ __forceinline__ void store8(char* d, const float (&v)[8])
+{
     if constexpr (F32) {
-        *reinterpret_cast<f32x4*>(d) = lo;
-        *reinterpret_cast<f32x4*>(d + 16) = hi;
+        *reinterpret_cast<f32x4*>(d) = f32x4{v[0], v[1], v[2], v[3]};
+        *reinterpret_cast<f32x4*>(d + 16) = f32x4{v[4], v[5], v[6], v[7]};
     } else {
-        *reinterpret_cast<u32x4*>(d) = u32x4{T::pack(lo[0], lo[1]), T::pack(lo[2], lo[3]), T::pack(hi[0], hi[1]), T::pack(hi[2], hi[3])};
+        *reinterpret_cast<u32x4*>(d) = u32x4{T::pack(v[0], v[1]), T::pack(v[2], v[3]), T::pack(v[4], v[5]), T::pack(v[6], v[7])};
     }
 }
 
@@ -894,16 +938,28 @@ __global__ __launch_bounds__(256) void join_kernel(const Args g)
     const int x = (int)(blockIdx.x % SUB) * 2048 + (int)threadIdx.x * 8, r = x / C::BN, c = x % C::BN;
     const int rows = MODE == TN ? g.x_cols - wk.tile0 : wk.rows;
     if (r >= rows || wk.col0 + c >= g.cols) return;
-    float scale = 1.f;
-    if (MODE == LOW && g.scales != nullptr) scale = g.scales[g.ids[wk.group]];
     char* d = g.d + (MODE == TN ? (int64_t)wk.group * g.d_mat + (int64_t)(wk.tile0 + r) * g.d_ld : (int64_t)(wk.row0 + r) * g.d_ld) +
               (int64_t)(wk.col0 + c) * (F32 ? 4 : 2);
-    join8<T, F32>(g.parts + (int64_t)t * (C::BM * C::BN) + x, (int64_t)all * (C::BM * C::BN), (int)g.splits.d, scale, d);
+    float v[8];
+    join8(g.parts + (int64_t)t * (C::BM * C::BN) + x, (int64_t)all * (C::BM * C::BN), (int)g.splits.d, v);
+    if constexpr (MODE == LOW) {
+        const float scale = g.scales != nullptr ? g.scales[g.ids[wk.group]] : 1.f;
+        float hi[8], lo[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            hi[e] = grp::upper<T>(v[e] * scale);
+            lo[e] = v[e] * scale - hi[e];
+        }
+        store8<T, false>(d, hi);
+        store8<T, false>(d + g.low_rest, lo);
+    } else {
+        store8<T, F32>(d, v);
+    }
 }
 
-// Large tiles of NT, NN, TN and EACH: a workgroup for each compute unit walks
-// them.  Four waves of 128 x 128 outputs read a third less from LDS than eight
-// of half of it, and the next tile's first loads are on the way while a tile's
+// Large tiles of NT, NN, TN, EACH and EACH2: a workgroup for each compute unit
+// walks them.  Four waves of 128 x 128 outputs read a third less from LDS than
+// eight of half of it, and the next tile's first loads are on the way while a tile's
 // outputs are written.  The matrix cores are busy for 89 to 90 % of the time
 // (by columns on both sides 71 %) and the board's power limits them: 16384 rows
 // over 8 matrices of 14336 x 4096 1306 us, 1473 TFLOP/s; gradients of 8192 rows
@@ -942,7 +998,8 @@ __device__ __forceinline__ uint32_t place_large(const Args& g, Work& wk)
         depth = wk.rows;
     }
     uint32_t steps = (uint32_t)(depth + grp::kRingStep - 1) / grp::kRingStep;
-    if (MODE == EACH) steps += (uint32_t)g.ids[wk.group] < (uint32_t)g.adapters;   // the adapter's second product is a step
+    // the adapter's second product, both terms, is a step, or with EACH2 two
+    if (each_request(MODE) && (uint32_t)g.ids[wk.group] < (uint32_t)g.adapters) steps += MODE == EACH2 ? 2 : 1;
     return steps < 2 ? 2 : steps;
 }
 
@@ -970,19 +1027,20 @@ __global__ __launch_bounds__(256, 1) void ring_kernel(const Args g)
     out.start(lds, g.d_ld, F32 ? g.d_ld : PART_LD, w, lane);
     const uint32_t sta = (uint32_t)(STEP * g.x_ld), stb = (uint32_t)(STEP * g.y_ld);
     const int kr = 16 * w + lane / 32;
-    uint32_t ha[2], hb[2];   // EACH: see gen_grouped_sched.py
+    uint32_t ha[2], hb[2];   // the adapter's steps: see gen_grouped_sched.py
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
         const int r = 64 * w + lane / 8, c = (lane & 7) ^ grp::RingSide<false>::swz(8 * q + lane / 8);
+        const int u = MODE == EACH ? c & 3 : c;   // EACH: `up` twice, for 32 upper terms and 32 lower ones
         ha[q] = (uint32_t)(r * 128 + 16 * c);
-        hb[q] = MODE == EACH && 8 * c < g.rank ? (uint32_t)(r * g.up_ld + 16 * c) : grp::kBeyond;
+        hb[q] = each_request(MODE) && 8 * u < g.rank ? (uint32_t)(r * g.up_ld + 16 * u) : grp::kBeyond;
     }
 
     // One tile, or part of one: its operands, scalars all of them.
     struct Item {
         bool found;
         u32x4 rsa, rsb, rsd;
-        uint32_t rem, wide, gstr, hk, ext;   // steps, ..., what the first step lacks, whether the adapter's step is the first
+        uint32_t rem, wide, gstr, hk, ext;   // steps, ..., what the first step lacks, how many of the first are the adapter's
         Work wk;
     };
     // Sorted: the first round has the longest tiles, in order, and every second
@@ -1003,7 +1061,7 @@ __global__ __launch_bounds__(256, 1) void ring_kernel(const Args g)
         const uint32_t steps = place_large<MODE>(g, wk);
         // the contraction's first step is the partial one: see gen_grouped_sched.py
         int hk = MODE == TN ? 0 : (g.depth + STEP - 1) / STEP * STEP - g.depth;
-        uint32_t ext = MODE == EACH && (int)steps * STEP > g.depth + hk ? 1 : 0;
+        uint32_t ext = each_request(MODE) && (int)steps * STEP > g.depth + hk ? (MODE == EACH2 ? 2 : 1) : 0;
         const uint32_t parts = slot < walk.full ? 1 : walk.of(steps);
         if (part >= parts) return it;   // the last of the workgroup's anyway
         const uint32_t first = part * steps / parts;
@@ -1079,15 +1137,20 @@ __global__ __launch_bounds__(256, 1) void ring_kernel(const Args g)
         asm volatile(LOOP("f16") : G16_GROUPED_STATE : G16_GROUPED_COMMON, __VA_ARGS__ : G16_GROUPED_CLOBBERS); \
     else \
         asm volatile(LOOP("bf16") : G16_GROUPED_STATE : G16_GROUPED_COMMON, __VA_ARGS__ : G16_GROUPED_CLOBBERS)
-        if constexpr (MODE == NT || MODE == EACH) {
-            u32x4 rsa0 = rsa, rsb0 = rsb;
-            if (MODE == EACH) {
+        if constexpr (MODE == NT || each_request(MODE)) {
+            u32x4 rsa0 = rsa, rsb0 = rsb, rsa1 = rsa;
+            if (each_request(MODE)) {
                 const int64_t n = it.wk.rows < TILE ? it.wk.rows : TILE;
                 rsa0 = grp::ring_rsrc(g.low + (int64_t)it.wk.row0 * 128, n * 128);
+                rsa1 = grp::ring_rsrc(g.low + g.low_rest + (int64_t)it.wk.row0 * 128, n * 128);
                 rsb0 = grp::ring_rsrc(g.up + (it.ext ? (int64_t)g.ids[it.wk.group] * g.up_mat : 0) + it.wk.col0 * g.up_ld, (TILE - 1) * g.up_ld + 2 * g.rank);
             }
             const uint32_t sb8 = grp::uniform((uint32_t)(8 * g.up_ld)), ext = it.ext;
-            G16_GROUPED_BLOCK(G16_GROUPED_RR, G16_GROUPED_A_ROWS, G16_GROUPED_B_ROWS, G16_GROUPED_EXT);
+            if constexpr (MODE == EACH2) {
+                G16_GROUPED_BLOCK(G16_GROUPED_RR2, G16_GROUPED_A_ROWS, G16_GROUPED_B_ROWS, G16_GROUPED_EXT, [rsa1] "s"(rsa1));
+            } else {
+                G16_GROUPED_BLOCK(G16_GROUPED_RR, G16_GROUPED_A_ROWS, G16_GROUPED_B_ROWS, G16_GROUPED_EXT);
+            }
         } else if constexpr (MODE == NN) {
             G16_GROUPED_BLOCK(G16_GROUPED_RC, G16_GROUPED_A_ROWS, G16_GROUPED_B_COLS, [hk] "s"(hk), [kr] "v"(kr));
         } else {
@@ -1120,7 +1183,9 @@ __global__ __launch_bounds__(256) void ring_join_kernel(const Args g)
         if (parts < 2 || (MODE != TN && r >= wk.rows)) continue;
         char* d = g.d + (MODE == TN ? (int64_t)wk.group * g.d_mat + (int64_t)(wk.tile0 + r) * g.d_ld : (int64_t)(wk.row0 + r) * g.d_ld) +
                   (int64_t)(wk.col0 + c) * (F32 ? 4 : 2);
-        join8<T, F32>(g.parts + (int64_t)t * (TILE * TILE) + x, (int64_t)walk.rest * (TILE * TILE), (int)parts, 1.f, d);
+        float v[8];
+        join8(g.parts + (int64_t)t * (TILE * TILE) + x, (int64_t)walk.rest * (TILE * TILE), (int)parts, v);
+        store8<T, F32>(d, v);
     }
 }
 
@@ -1179,16 +1244,16 @@ struct Forms {
     int n = 0;
     Forms()
     {
-        if constexpr (MODE != TN && MODE != EACH) {
+        if constexpr (MODE != TN && !each_request(MODE)) {
             f[n++] = form<T, MODE, F32, Tiny, false>(kTiny);
             f[n++] = form<T, MODE, F32, Small, false>(kSmall);
         }
         if constexpr (MODE == NT || MODE == NN) f[n++] = form<T, MODE, F32, Flat, false>(kFlat);
-        if constexpr (MODE != EACH) f[n++] = form<T, MODE, F32, Square, true>(kSquare);
-        if constexpr (MODE != TN && MODE != EACH) f[n++] = form<T, MODE, F32, Oblong, true>(kOblong);
-        if constexpr (MODE != LOW && MODE != EACH) f[n++] = form<T, MODE, F32, Middle, true>(kMiddle);
+        if constexpr (!each_request(MODE)) f[n++] = form<T, MODE, F32, Square, true>(kSquare);
+        if constexpr (MODE != TN && !each_request(MODE)) f[n++] = form<T, MODE, F32, Oblong, true>(kOblong);
+        if constexpr (MODE != LOW && !each_request(MODE)) f[n++] = form<T, MODE, F32, Middle, true>(kMiddle);
         if constexpr (MODE == ADAPT) f[n++] = form<T, MODE, F32, Large, false>(kLarge);
-        if constexpr (MODE == NT || MODE == NN || MODE == TN || MODE == EACH)
+        if constexpr (MODE == NT || MODE == NN || MODE == TN || each_request(MODE))
             f[n++] = Form{grp::kRingTile, grp::kRingTile, grp::kRingStep, 256, 0, kRing, (const void*)&ring_kernel<T, MODE, F32>, nullptr,
                           (const void*)&ring_join_kernel<T, MODE, F32>};
     }
@@ -1238,7 +1303,7 @@ Plan plan(const Form* forms, int n, const Args& g, int cus, int* status)
     const int64_t used = MODE == ADAPT ? 1 : g.groups < g.rows ? g.groups : g.rows;   // groups with rows, at most
     const double depth = MODE == TN ? (g.groups > 0 ? (double)g.rows / g.groups : 0.) : g.depth;
     // matrices, rows read and rows written, at 5.5 TB/s
-    const double mats = MODE == TN ? (double)g.groups * g.x_cols * g.cols : (MODE == EACH ? 1. : used) * g.cols * depth;
+    const double mats = MODE == TN ? (double)g.groups * g.x_cols * g.cols : (each_request(MODE) ? 1. : used) * g.cols * depth;
     const double rows = MODE == TN ? (double)g.rows * (g.x_cols + g.cols) : (double)g.rows * (depth + g.cols);
     const double memory = (mats * (MODE == TN && F32 ? 2 : 1) + rows) * 2 / 5.5e6;
     // TN: matrices are written when a workgroup ends, half of it beside others'
@@ -1294,7 +1359,7 @@ Plan plan(const Form* forms, int n, const Args& g, int cus, int* status)
         }
         const double slots = (double)cus * f.per_cu;
         double extra = 0;
-        if (MODE == ADAPT && g.adapters > 0) {   // a tile's requests, `rank` of the contraction each, at half the speed
+        if (MODE == ADAPT && g.adapters > 0) {   // a tile's requests, twice `rank` of the contraction each
             const double requests = g.groups < g.rows ? g.groups : g.rows, mean = g.rows / requests, mine = f.bm / mean + 1;
             extra = (16. * g.rank_chunks.d * (mine < requests ? mine : requests) + 256) / 1024;
         }
@@ -1575,11 +1640,12 @@ void plan_pair(const adapter_desc* d, AdapterCall* c, int64_t* parts, double* tw
     }
     if (form == nullptr || best >= *two) return;
     *two = best;
-    const int64_t rt = ceil_div(d->rows, form->bm), ct = ceil_div(d->N, form->bn), size = c->dots ? 4 : 2;
+    const int64_t rt = ceil_div(d->rows, form->bm), ct = ceil_div(d->N, form->bn);
     c->pair = c->dots ? form->plane : form->held;
     c->end = !c->dots ? form->first : d->dtype == GROUPED_F16 ? finish<F16>(d->rank) : finish<BF16>(d->rank);
     c->each = false;
-    c->low.d_ld = size * d->rank;
+    c->low.d_ld = (c->dots ? 4 : 2) * d->rank;   // in fp32, or in two terms
+    c->low.low_rest = c->rest.low_rest = 2 * d->rows * d->rank;
     c->low.cols = c->low.low_rows = d->rank;
     c->low.col_tiles = attn::div_by(ceil_div(d->rank, 16));
     c->low.row_tiles = (uint32_t)((d->rows + used * 15) / 16);
@@ -1589,7 +1655,7 @@ void plan_pair(const adapter_desc* d, AdapterCall* c, int64_t* parts, double* tw
     c->rest.splits = attn::div_by(splits);
     c->plan.splits = splits;
     c->plan.wgs = rt * ct * splits;
-    c->low_bytes = ceil_div(size * d->rows * d->rank, 256) * 256;
+    c->low_bytes = ceil_div(4 * d->rows * d->rank, 256) * 256;
     *parts = c->dots ? d->rows * d->N * splits * 4 : rt * ct * splits * form->bm * form->bn * 4;
 }
 
@@ -1631,6 +1697,8 @@ int plan_adapters(const adapter_desc* d, AdapterCall* c)
     g.scales = d->scales;
     g.adapters = c->adapted ? (int)d->adapters : 0;
     g.rank_chunks = attn::div_by(c->adapted ? d->rank / 8 : 1);
+    g.low_rest = 2 * d->rows * d->rank;
+    g.term_chunks = attn::div_by(2 * g.rank_chunks.d);
     c->low_bytes = 0;
     int64_t parts = 0;
     if (c->adapted) {
@@ -1642,7 +1710,7 @@ int plan_adapters(const adapter_desc* d, AdapterCall* c)
         c->low.cols = c->low.low_rows = d->rank;
         c->low_plan = plan_for<LOW>(d->dtype, c->low, c->cus, &st);
         if (st != GEMM_F16_NT_OK) return st;
-        c->low_bytes = ceil_div(2 * d->rows * d->rank, 256) * 256;
+        c->low_bytes = ceil_div(4 * d->rows * d->rank, 256) * 256;
         parts = c->low_plan.part_bytes;
     }
     g.down = (const char*)d->down;
@@ -1661,16 +1729,18 @@ int plan_adapters(const adapter_desc* d, AdapterCall* c)
     c->plan = plan_for<ADAPT>(d->dtype, g, c->cus, &st);
     if (c->adapted && d->rank <= 64 && g.up_ld < 2 * kRingPitch) {   // large tiles, of one request each
         int each_st = GEMM_F16_NT_OK;
-        const Plan each = plan_for<EACH>(d->dtype, g, c->cus, &each_st);
+        const Plan each = d->rank <= 32 ? plan_for<EACH>(d->dtype, g, c->cus, &each_st) : plan_for<EACH2>(d->dtype, g, c->cus, &each_st);
         if (each_st == GEMM_F16_NT_OK && (st != GEMM_F16_NT_OK || each.us < c->plan.us)) {
             st = GEMM_F16_NT_OK;
             c->each = true;
             c->plan = each;
             c->rest.rank = d->rank;
-            // rows of 64, zeros behind the rank
-            c->low.cols = 64;
+            // rows of 64 elements: 32 upper and 32 lower terms, or 64 of one kind; zeros behind the rank
+            const bool both = d->rank <= 32;
+            c->low.cols = both ? 32 : 64;
             c->low.d_ld = 128;
-            c->low_bytes = 128 * d->rows;
+            c->low.low_rest = c->rest.low_rest = both ? 64 : 128 * d->rows;
+            c->low_bytes = (both ? 128 : 256) * d->rows;
             c->low_plan = plan_for<LOW>(d->dtype, c->low, c->cus, &st);
             parts = c->low_plan.part_bytes;
         }
@@ -1751,7 +1821,8 @@ int adapter_nt(const adapter_desc* d, void* workspace, int64_t workspace_bytes, 
         if ((st = run<LOW>(c.low_plan, c.low, parts, c.cus, (hipStream_t)stream)) != GEMM_F16_NT_OK) return st;
     }
     c.rest.low = (const char*)workspace;
-    return c.each ? run<EACH>(c.plan, c.rest, parts, c.cus, (hipStream_t)stream) : run<ADAPT>(c.plan, c.rest, parts, c.cus, (hipStream_t)stream);
+    if (!c.each) return run<ADAPT>(c.plan, c.rest, parts, c.cus, (hipStream_t)stream);
+    return d->rank <= 32 ? run<EACH>(c.plan, c.rest, parts, c.cus, (hipStream_t)stream) : run<EACH2>(c.plan, c.rest, parts, c.cus, (hipStream_t)stream);
 }
 
 }  // extern "C"

@@ -16,6 +16,7 @@
 // Sums are held in fp32 by the matrix cores; an output is rounded once.
 #pragma once
 
+#include <type_traits>
 #include <utility>
 
 #include "attn_core.hpp"
@@ -227,11 +228,45 @@ __device__ __forceinline__ void add_waves(char* smem, int wk, int lane, Acc<C>& 
     }
 }
 
-// Writes a wave's blocks, its first row and column at `d`: rounded (or as they
-// are, F32), through LDS so that a store covers whole lines.  `rows` and `cols`
-// say how many are there; columns come in eights.
-template <typename T, class C, bool F32>
-__device__ __forceinline__ void store(char* lds, char* d, int64_t ld, int rows, int cols, float scale, const Acc<C>& acc, int lane)
+// A 32-bit value as two operands of 16 bits: the upper one, and what it leaves,
+// which T::pack rounds.  Off by at most 2^-16 of the value in bf16, by 2^-20 of
+// it or 2^-25 in fp16, where they reach twice the type's largest value.  Both
+// have the value's sign, and neither is zero unless the value is (in fp16: is
+// below 2^-24), so that an infinite factor of theirs makes one infinity; of an
+// infinite value the upper is the type's largest and the lower infinite.
+template <typename T>
+__device__ __forceinline__ float upper(float x)
+{
+    const uint32_t b = __builtin_bit_cast(uint32_t, x);
+    if constexpr (std::is_same<T, F16>::value) {
+        // a step of 32 bits less, so that something is left, and 2^-24 less, so
+        // that it is no less than that; of 0 the first is no number, and 0 is what is left
+        const float least = __builtin_bit_cast(float, b - 1u) - __builtin_copysignf(0x1p-24f, x);
+        return (float)__builtin_amdgcn_cvt_pkrtz(__builtin_amdgcn_fmed3f(least, 0.f, x), 0.f)[0];
+    } else {
+        return __builtin_bit_cast(float, (x != 0.f ? b - 1u : 0u) & 0xffff0000u);
+    }
+}
+// Both terms of two values.
+struct Terms {
+    uint32_t upper, lower;
+};
+template <typename T>
+__device__ __forceinline__ Terms terms(float x, float y)
+{
+    const float a = upper<T>(x), b = upper<T>(y);
+    return {T::pack(a, b), T::pack(x - a, y - b)};
+}
+
+struct AsItIs {
+    __device__ __forceinline__ float operator()(float v) const { return v; }
+};
+
+// Writes a wave's blocks, its first row and column at `d`: what `f` makes of
+// them, rounded (or in 32 bits, F32), through LDS so that a store covers whole
+// lines.  `rows` and `cols` say how many are there; columns come in eights.
+template <typename T, class C, bool F32, typename F = AsItIs>
+__device__ __forceinline__ void store(char* lds, char* d, int64_t ld, int rows, int cols, const Acc<C>& acc, int lane, F f = F())
 {
     constexpr int SIZE = F32 ? 4 : 2, PITCH = C::FN * 32 * SIZE, CH = PITCH / 16, PER = 64 / CH;
     static_assert(CH <= 64, "a store covers whole rows");
@@ -242,7 +277,7 @@ __device__ __forceinline__ void store(char* lds, char* d, int64_t ld, int rows, 
         for (int j = 0; j < C::FN; ++j)
 #pragma unroll
             for (int g = 0; g < 4; ++g) {
-                const f32x4 v = f32x4{acc[i][j][4 * g], acc[i][j][4 * g + 1], acc[i][j][4 * g + 2], acc[i][j][4 * g + 3]} * scale;
+                const f32x4 v = f32x4{f(acc[i][j][4 * g]), f(acc[i][j][4 * g + 1]), f(acc[i][j][4 * g + 2]), f(acc[i][j][4 * g + 3])};
                 if constexpr (F32) {
                     const int c = 8 * j + 2 * g + half;
                     *reinterpret_cast<f32x4*>(lds + r * PITCH + ((c ^ (r % CH)) << 4)) = v;

@@ -100,8 +100,9 @@ int grouped_tn_check(const grouped_desc* d);
  * and a request is any number of rows: a prompt, or one token.
  *
  * scale_a * (down_a A[r]) is summed in fp32 and, as an operand of the second
- * product, rounded to the operands' type at most once (calls with few rows for
- * a request keep it in fp32), so it has to lie in that type's range;
+ * product, held in two terms of the operands' type, which are off by at most
+ * 2^-16 of it in bf16, by 2^-20 of it or 2^-25 in fp16 (calls with few rows for
+ * a request keep it in fp32).  In fp16 it has to lie in that type's range;
  * everything else is one sum in fp32, rounded once. */
 typedef struct adapter_desc {
     int32_t dtype;
