@@ -49,7 +49,7 @@ struct Args {
     int cols;            // of D
     int x_cols;          // TN: rows of a group's D, which are columns of X
     int depth;           // the contraction, except for TN
-    int low_rows;        // LOW: rows of `down`; columns behind them are zeros
+    int low_rows;        // LOW: rows of `down`; columns behind them are zeros, whatever A holds
     int rank;            // EACH, EACH2
     Div col_tiles;
     Div per_group;       // TN: tiles of a group, padded to whole rounds of the XCDs
@@ -614,10 +614,12 @@ __device__ __forceinline__ void tile_body(const Args& g, char* smem, uint32_t in
         if constexpr (MODE == LOW) {
             const float scale = g.scales != nullptr ? g.scales[g.ids[wk.group]] : 1.f;
             if constexpr (F32) {
-                grp::store<T, C, true>(staging, d, g.d_ld, rows, cols, acc, lane, [&](float v) { return v * scale; });
+                grp::store<T, C, true>(staging, d, g.d_ld, rows, cols, acc, lane, [&](float v, int) { return v * scale; });
             } else {
-                grp::store<T, C, false>(staging, d, g.d_ld, rows, cols, acc, lane, [&](float v) { return grp::upper<T>(v * scale); });
-                grp::store<T, C, false>(staging, d + g.low_rest, g.d_ld, rows, cols, acc, lane, [&](float v) { return v * scale - grp::upper<T>(v * scale); });
+                const int end = g.low_rows - wk.col0 - c0;
+                grp::store<T, C, false>(staging, d, g.d_ld, rows, cols, acc, lane, [&](float v, int c) { return c < end ? grp::upper<T>(v * scale) : 0.f; });
+                grp::store<T, C, false>(staging, d + g.low_rest, g.d_ld, rows, cols, acc, lane,
+                                        [&](float v, int c) { return c < end ? v * scale - grp::upper<T>(v * scale) : 0.f; });
             }
         } else {
             grp::store<T, C, F32>(staging, d, g.d_ld, rows, cols, acc, lane);
@@ -754,8 +756,10 @@ __global__ __launch_bounds__(256, 1) void single_kernel(const Args g)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const grp::Terms t = grp::terms<T>(h[at + 2 * i] * scale[b], h[at + 2 * i + 1] * scale[b]);
-            upper[i] = t.upper;
-            lower[i] = t.lower;
+            // no row of `down` behind the rank: zeros, whatever A holds
+            const bool there = 16 * (b % each) + 4 * (i & ~1) < rank;
+            upper[i] = there ? t.upper : 0;
+            lower[i] = there ? t.lower : 0;
         }
         const f32x16 sum = T::mfma(u[b], lower, T::mfma(u[b], upper, d));
         const bool own = m >= first[b] && m < end[b];   // a lane's sums are one row's
@@ -944,11 +948,12 @@ __global__ __launch_bounds__(256) void join_kernel(const Args g)
     join8(g.parts + (int64_t)t * (C::BM * C::BN) + x, (int64_t)all * (C::BM * C::BN), (int)g.splits.d, v);
     if constexpr (MODE == LOW) {
         const float scale = g.scales != nullptr ? g.scales[g.ids[wk.group]] : 1.f;
+        const bool there = wk.col0 + c < g.low_rows;
         float hi[8], lo[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            hi[e] = grp::upper<T>(v[e] * scale);
-            lo[e] = v[e] * scale - hi[e];
+            hi[e] = there ? grp::upper<T>(v[e] * scale) : 0.f;
+            lo[e] = there ? v[e] * scale - hi[e] : 0.f;
         }
         store8<T, false>(d, hi);
         store8<T, false>(d + g.low_rest, lo);

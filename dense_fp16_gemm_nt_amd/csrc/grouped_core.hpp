@@ -259,12 +259,12 @@ __device__ __forceinline__ Terms terms(float x, float y)
 }
 
 struct AsItIs {
-    __device__ __forceinline__ float operator()(float v) const { return v; }
+    __device__ __forceinline__ float operator()(float v, int) const { return v; }
 };
 
 // Writes a wave's blocks, its first row and column at `d`: what `f` makes of
-// them, rounded (or in 32 bits, F32), through LDS so that a store covers whole
-// lines.  `rows` and `cols` say how many are there; columns come in eights.
+// them (and of the first of four columns that they are in), rounded (or in 32
+// bits, F32), through LDS so that a store covers whole lines.  `rows` and `cols` say how many are there; columns come in eights.
 template <typename T, class C, bool F32, typename F = AsItIs>
 __device__ __forceinline__ void store(char* lds, char* d, int64_t ld, int rows, int cols, const Acc<C>& acc, int lane, F f = F())
 {
@@ -277,7 +277,9 @@ __device__ __forceinline__ void store(char* lds, char* d, int64_t ld, int rows, 
         for (int j = 0; j < C::FN; ++j)
 #pragma unroll
             for (int g = 0; g < 4; ++g) {
-                const f32x4 v = f32x4{f(acc[i][j][4 * g]), f(acc[i][j][4 * g + 1]), f(acc[i][j][4 * g + 2]), f(acc[i][j][4 * g + 3])};
+                const f32x16& a = acc[i][j];
+                const int first = 32 * j + 8 * g + 4 * half;   // of the four columns
+                const f32x4 v = f32x4{f(a[4 * g], first), f(a[4 * g + 1], first), f(a[4 * g + 2], first), f(a[4 * g + 3], first)};
                 if constexpr (F32) {
                     const int c = 8 * j + 2 * g + half;
                     *reinterpret_cast<f32x4*>(lds + r * PITCH + ((c ^ (r % CH)) << 4)) = v;

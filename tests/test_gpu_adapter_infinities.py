@@ -1,0 +1,49 @@
+"""Adapters beside values that are not finite, on every way through the kernels: an output is what the formula gives for its
+own row, whatever the rank is padded to inside."""
+import sys
+
+import pytest
+
+import dense_fp16_gemm_nt_amd as g
+from tests.test_gpu_grouped import ADAPTERS, DEV, TYPES, adapter_inputs, ints, real
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+INF = float("inf")
+
+# ranks that are no multiple of 16, of 32 or of 64
+PADDED = ADAPTERS + [
+    ([1], [1], 4104, 4096, 8),
+    ([9], [2], 520, 1032, 24),
+    ([5], [2], 1032, 520, 40),
+    ([1, 2, 1], [0, 1, 2], 256, 264, 8),
+    ([4352], [1], 4104, 2056, 40),
+    ([2100, 900, 1500], [1, 0, 3], 4104, 1032, 56),
+    ([2100, 900, 1500], [1, 0, 3], 4104, 1032, 8),
+    ([2100, 900, 1500], [1, 0, 3], 4104, 1032, 32),
+]
+
+
+@pytest.mark.parametrize("case", range(len(PADDED)))
+@pytest.mark.parametrize("dtype", sorted(TYPES))
+def test_an_infinity_in_a_row_of_positive_values(dtype, case):
+    # everything that the infinity meets is positive, so its row is infinite, and no number anywhere is missing
+    lens, ids, n, k, rank = PADDED[case]
+    A, B, down, up, cu, ids = adapter_inputs(real, 800 + case, dtype, PADDED[case])
+    if A.shape[0] == 0:
+        pytest.skip("no rows")
+    B, down, up = B.abs() + 0.25, down.abs() / 8 + 0.25, up.abs() + 0.25
+    print(f"[gpu] an infinity in A, {dtype} {PADDED[case][2:]}", file=sys.stderr, flush=True)
+    clean = g.adapter_product(A, B, down, up, ints(cu), ints(ids))
+    hit = sorted({0, A.shape[0] // 2, A.shape[0] - 1})
+    A = A.clone()
+    for i, r in enumerate(hit):
+        A[r, (7 * r) % k] = INF if i % 2 == 0 else -INF
+    D = g.adapter_product(A, B, down, up, ints(cu), ints(ids))
+    torch.cuda.synchronize()
+    for i, r in enumerate(hit):
+        assert bool((D[r] == (INF if i % 2 == 0 else -INF)).all()), r
+    others = torch.ones(A.shape[0], dtype=torch.bool, device=DEV)
+    others[hit] = False
+    assert torch.equal(D[others], clean[others])
