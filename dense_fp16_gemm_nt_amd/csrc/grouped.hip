@@ -369,7 +369,7 @@ __device__ __forceinline__ uint32_t not_finite(uint32_t v)
 
 // One step of the requests' part of the contraction.  The zeros that a row has
 // for other requests keep their matrices out of its sums as long as these are
-// finite, so what is not is left out here, and added by add_not_finite to the
+// finite, so what is not is left out here, and added by store_not_finite to the
 // rows that it belongs to.  Returns whether there was any.
 template <typename T, class C>
 __device__ __forceinline__ bool multiply_requests(const grp::Frags<C, false, C::BM, C::FM>& fx, const grp::Frags<C, false, C::BN, C::FN>& fy, uint32_t stage,
@@ -403,39 +403,51 @@ __device__ __forceinline__ bool multiply_requests(const grp::Frags<C, false, C::
     return any;
 }
 
-// Adds the products with what is not finite to a wave's outputs, which it has
-// stored: `rows` x `cols` of them at d, the first of the tile's row r0 and of
-// D's column c0; `low` is the tile's first row.  What the sums were rounded to
-// in between makes no difference to a result that is not finite.
-template <typename T, bool F32>
-__device__ __forceinline__ void add_not_finite(const Args& g, const Entry* table, int count, const char* low, char* d, int64_t ld, int r0, int c0, int rows,
-                                               int cols, int lane)
+// Writes a wave's blocks as grp::store does, one value at a time, and adds the
+// products with what is not finite to them before they are rounded: a finite
+// sum beyond fp16's largest value is no infinity here.  The blocks are the
+// tile's rows from r0 on and D's columns from c0 on; `low` is the tile's first
+// row.
+template <typename T, class C, bool F32>
+__device__ __forceinline__ void store_not_finite(const Args& g, const Entry* table, int count, const char* low, char* lds, char* d, int64_t ld, int r0, int c0,
+                                                 int rows, int cols, const Acc<C>& acc, int lane)
 {
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // the wave's own stores, by other lanes
-    for (int q = 0; q < count; ++q) {
-        const Entry e = table[q];
-        const int first = e.first > r0 ? e.first : r0, end = e.end < r0 + rows ? e.end : r0 + rows;
-        if (first >= end) continue;
-        for (int c = lane; c < cols; c += 64) {
-            const uint32_t* up = reinterpret_cast<const uint32_t*>(g.up + (int64_t)e.id * g.up_mat + (int64_t)(c0 + c) * g.up_ld);
-            for (int p = 0; p < 4 * (int)g.rank_chunks.d; ++p) {
-                const uint32_t bad = not_finite<T>(up[p]);
-                if (bad == 0) continue;
-                const attn::f32x2 u = T::unpack(up[p]);
-                for (int r = first; r < end; ++r) {
-                    const attn::f32x2 h = T::unpack(*reinterpret_cast<const uint32_t*>(low + (int64_t)r * (16 * g.rank_chunks.d) + 4 * p)) +
-                                          T::unpack(*reinterpret_cast<const uint32_t*>(low + g.low_rest + (int64_t)r * (16 * g.rank_chunks.d) + 4 * p));
-                    const float x = (bad & 0x8000u ? h[0] * u[0] : 0.f) + (bad & 0x80000000u ? h[1] * u[1] : 0.f);
-                    char* at = d + (int64_t)(r - r0) * ld + (F32 ? 4 : 2) * c;
-                    if constexpr (F32) {
-                        *reinterpret_cast<float*>(at) += x;
-                    } else {
-                        const uint32_t sum = T::pack(T::unpack(*reinterpret_cast<const uint16_t*>(at))[0] + x, 0.f);
-                        *reinterpret_cast<uint16_t*>(at) = (uint16_t)sum;
-                    }
+    constexpr int W = 32 * C::FN, ROWS = C::BM == 16 ? 16 : 32, COLS = C::BN == 16 ? 16 : W;
+    const int64_t low_ld = 16 * (int64_t)g.rank_chunks.d;
+    float* to = reinterpret_cast<float*>(lds);
+#pragma unroll
+    for (int i = 0; i < C::FM; ++i) {
+#pragma unroll
+        for (int b = 0; b < 4 * C::FN; ++b) {
+            const f32x16& v = acc[i][b / 4];
+            const int at = 4 * (b % 4);
+            *reinterpret_cast<f32x4*>(to + (lane & 31) * W + 8 * b + 4 * (lane >> 5)) = f32x4{v[at], v[at + 1], v[at + 2], v[at + 3]};
+        }
+        __builtin_amdgcn_wave_barrier();
+        for (int x = lane; x < 32 * W; x += 64) {
+            const int r = x / W, c = x % W, row = r0 + 32 * i + r;
+            if (r >= ROWS || c >= COLS || 32 * i + r >= rows || c >= cols) continue;
+            float v = to[x];
+            for (int q = 0; q < count; ++q) {
+                const Entry e = table[q];
+                if (row < e.first || row >= e.end) continue;
+                const char* up = g.up + (int64_t)e.id * g.up_mat + (int64_t)(c0 + c) * g.up_ld;
+                for (int p = 0; p < (int)low_ld; p += 4) {   // two ranks
+                    const uint32_t u2 = *reinterpret_cast<const uint32_t*>(up + p), bad = not_finite<T>(u2);
+                    if (bad == 0) continue;
+                    const char* h2 = low + row * low_ld + p;
+                    const attn::f32x2 u = T::unpack(u2), h = T::unpack(*reinterpret_cast<const uint32_t*>(h2)) +
+                                                             T::unpack(*reinterpret_cast<const uint32_t*>(h2 + g.low_rest));
+                    v += (bad & 0x8000u ? h[0] * u[0] : 0.f) + (bad & 0x80000000u ? h[1] * u[1] : 0.f);
                 }
             }
+            char* at = d + (int64_t)(32 * i + r) * ld + (F32 ? 4 : 2) * c;
+            if constexpr (F32)
+                *reinterpret_cast<float*>(at) = v;
+            else
+                *reinterpret_cast<uint16_t*>(at) = (uint16_t)T::pack(v, 0.f);
         }
+        __builtin_amdgcn_wave_barrier();
     }
 }
 
@@ -587,9 +599,8 @@ __device__ __forceinline__ void tile_body(const Args& g, char* smem, uint32_t in
     bad = MODE == ADAPT && requests > 0 && __builtin_amdgcn_readfirstlane(count[1]) != 0;
 
     const int r0 = wm * C::FM * 32, c0 = wn * C::FN * 32, rows = (MODE == TN ? g.x_cols - wk.tile0 : wk.rows) - r0, cols = g.cols - wk.col0 - c0;
-    constexpr bool WIDE = F32 || SPLIT;
+    constexpr bool WIDE = F32 || SPLIT || MODE == ADAPT;
     constexpr int STAGING = C::FN * 32 * 32 * (WIDE ? 4 : 2);
-    constexpr int OWN_ROWS = C::BM / C::WM, OWN_COLS = C::BN / C::WN;   // of the wave
     constexpr int AFTER = (C::WK - 1) * C::FM * C::FN * 4096;   // the other waves' sums
     static_assert(AFTER + C::WM * C::WN * STAGING <= C::LDS, "LDS budget");
     char* staging = smem + AFTER + (wm * C::WN + wn) * STAGING;
@@ -606,8 +617,10 @@ __device__ __forceinline__ void tile_body(const Args& g, char* smem, uint32_t in
         grp::store<T, C, true>(staging, (char*)d, 4 * (int64_t)g.cols, rows, cols, acc, lane);
     } else if constexpr (SUMS == PART) {
         char* d = (char*)(g.parts + (int64_t)slot * (C::BM * C::BN) + r0 * C::BN + c0);
-        grp::store<T, C, true>(staging, d, 4 * C::BN, rows, cols, acc, lane);
-        if (MODE == ADAPT && bad) add_not_finite<T, true>(g, table, requests, low, d, 4 * C::BN, r0, wk.col0 + c0, min(rows, OWN_ROWS), min(cols, OWN_COLS), lane);
+        if (MODE == ADAPT && bad)
+            store_not_finite<T, C, true>(g, table, requests, low, staging, d, 4 * C::BN, r0, wk.col0 + c0, rows, cols, acc, lane);
+        else
+            grp::store<T, C, true>(staging, d, 4 * C::BN, rows, cols, acc, lane);
     } else {
         char* d = g.d + (MODE == TN ? (int64_t)wk.group * g.d_mat + (int64_t)(wk.tile0 + r0) * g.d_ld : (int64_t)(wk.row0 + r0) * g.d_ld) +
                   (int64_t)(wk.col0 + c0) * (F32 ? 4 : 2);
@@ -621,10 +634,11 @@ __device__ __forceinline__ void tile_body(const Args& g, char* smem, uint32_t in
                 grp::store<T, C, false>(staging, d + g.low_rest, g.d_ld, rows, cols, acc, lane,
                                         [&](float v, int c) { return c < end ? v * scale - grp::upper<T>(v * scale) : 0.f; });
             }
+        } else if (MODE == ADAPT && bad) {
+            store_not_finite<T, C, F32>(g, table, requests, low, staging, d, g.d_ld, r0, wk.col0 + c0, rows, cols, acc, lane);
         } else {
             grp::store<T, C, F32>(staging, d, g.d_ld, rows, cols, acc, lane);
         }
-        if (MODE == ADAPT && bad) add_not_finite<T, false>(g, table, requests, low, d, g.d_ld, r0, wk.col0 + c0, min(rows, OWN_ROWS), min(cols, OWN_COLS), lane);
     }
 }
 

@@ -47,3 +47,24 @@ def test_an_infinity_in_a_row_of_positive_values(dtype, case):
     others = torch.ones(A.shape[0], dtype=torch.bool, device=DEV)
     others[hit] = False
     assert torch.equal(D[others], clean[others])
+
+
+@pytest.mark.parametrize("case", range(len(PADDED)))
+@pytest.mark.parametrize("sign", [1, -1])
+def test_an_infinite_adapter_beside_sums_beyond_the_largest_value(sign, case):
+    # the shared product alone is 131008 or so, finite in the sums and infinite when rounded to fp16: an adapter's infinity of
+    # the other sign decides, as it does before any rounding
+    lens, ids, n, k, rank = PADDED[case]
+    A, B, down, up, cu, ids = adapter_inputs(real, 850 + case, "fp16", PADDED[case])
+    owners = [a for ln, a in zip(lens, ids) if ln and 0 <= a < down.shape[0]]
+    if not owners:
+        pytest.skip("no row has an adapter")
+    A, B = torch.ones_like(A), torch.full_like(B, sign * 2 * 65504 / k)
+    down, up = down.abs() / (8 * k) + 1 / k, up.abs() / 8
+    up[owners[0], 1::3, rank // 2] = -sign * INF
+    print(f"[gpu] sums beyond the largest value, {PADDED[case][2:]}", file=sys.stderr, flush=True)
+    D = g.adapter_product(A, B, down, up, ints(cu), ints(ids))
+    torch.cuda.synchronize()
+    whose = torch.repeat_interleave(torch.tensor(ids[:len(lens)], device=DEV), torch.tensor(lens, device=DEV))
+    hit = (whose == owners[0])[:, None] & (torch.arange(n, device=DEV) % 3 == 1)[None]
+    assert bool(hit.any()) and bool((D[hit] == -sign * INF).all()) and bool((D[~hit] == sign * INF).all())
