@@ -626,14 +626,29 @@ __device__ __forceinline__ void tile_body(const Args& g, char* smem, uint32_t in
                   (int64_t)(wk.col0 + c0) * (F32 ? 4 : 2);
         if constexpr (MODE == LOW) {
             const float scale = g.scales != nullptr ? g.scales[g.ids[wk.group]] : 1.f;
-            if constexpr (F32) {
-                grp::store<T, C, true>(staging, d, g.d_ld, rows, cols, acc, lane, [&](float v, int) { return v * scale; });
-            } else {
-                const int end = g.low_rows - wk.col0 - c0;
-                grp::store<T, C, false>(staging, d, g.d_ld, rows, cols, acc, lane, [&](float v, int c) { return c < end ? grp::upper<T>(v * scale) : 0.f; });
-                grp::store<T, C, false>(staging, d + g.low_rest, g.d_ld, rows, cols, acc, lane,
-                                        [&](float v, int c) { return c < end ? v * scale - grp::upper<T>(v * scale) : 0.f; });
+            const int end = F32 ? C::BN : g.low_rows - wk.col0 - c0;   // the columns there are
+            Acc<C> rest;   // the lower terms
+#pragma unroll
+            for (int i = 0; i < C::FM; ++i)
+#pragma unroll
+                for (int j = 0; j < C::FN; ++j)
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        const float v = acc[i][j][e] * scale;
+                        acc[i][j][e] = F32 ? v : grp::upper<T>(v);
+                        rest[i][j][e] = v - acc[i][j][e];
+                    }
+            if (end < 32 * C::FN && end < cols) {
+#pragma unroll
+                for (int i = 0; i < C::FM; ++i)
+#pragma unroll
+                    for (int j = 0; j < C::FN; ++j)
+#pragma unroll
+                        for (int e = 0; e < 16; ++e)
+                            if (32 * j + 8 * (e / 4) + 4 * (lane >> 5) >= end) acc[i][j][e] = rest[i][j][e] = 0.f;
             }
+            grp::store<T, C, F32>(staging, d, g.d_ld, rows, cols, acc, lane);
+            if constexpr (!F32) grp::store<T, C, false>(staging, d + g.low_rest, g.d_ld, rows, cols, rest, lane);
         } else if (MODE == ADAPT && bad) {
             store_not_finite<T, C, F32>(g, table, requests, low, staging, d, g.d_ld, r0, wk.col0 + c0, rows, cols, acc, lane);
         } else {

@@ -258,15 +258,11 @@ __device__ __forceinline__ Terms terms(float x, float y)
     return {T::pack(a, b), T::pack(x - a, y - b)};
 }
 
-struct AsItIs {
-    __device__ __forceinline__ float operator()(float v, int) const { return v; }
-};
-
-// Writes a wave's blocks, its first row and column at `d`: what `f` makes of
-// them (and of the first of four columns that they are in), rounded (or in 32
-// bits, F32), through LDS so that a store covers whole lines.  `rows` and `cols` say how many are there; columns come in eights.
-template <typename T, class C, bool F32, typename F = AsItIs>
-__device__ __forceinline__ void store(char* lds, char* d, int64_t ld, int rows, int cols, const Acc<C>& acc, int lane, F f = F())
+// Writes a wave's blocks, its first row and column at `d`: rounded (or as they
+// are, F32), through LDS so that a store covers whole lines.  `rows` and `cols`
+// say how many are there; columns come in eights.
+template <typename T, class C, bool F32>
+__device__ __forceinline__ void store(char* lds, char* d, int64_t ld, int rows, int cols, const Acc<C>& acc, int lane)
 {
     constexpr int SIZE = F32 ? 4 : 2, PITCH = C::FN * 32 * SIZE, CH = PITCH / 16, PER = 64 / CH;
     static_assert(CH <= 64, "a store covers whole rows");
@@ -277,9 +273,7 @@ __device__ __forceinline__ void store(char* lds, char* d, int64_t ld, int rows, 
         for (int j = 0; j < C::FN; ++j)
 #pragma unroll
             for (int g = 0; g < 4; ++g) {
-                const f32x16& a = acc[i][j];
-                const int first = 32 * j + 8 * g + 4 * half;   // of the four columns
-                const f32x4 v = f32x4{f(a[4 * g], first), f(a[4 * g + 1], first), f(a[4 * g + 2], first), f(a[4 * g + 3], first)};
+                const f32x4 v = f32x4{acc[i][j][4 * g], acc[i][j][4 * g + 1], acc[i][j][4 * g + 2], acc[i][j][4 * g + 3]};
                 if constexpr (F32) {
                     const int c = 8 * j + 2 * g + half;
                     *reinterpret_cast<f32x4*>(lds + r * PITCH + ((c ^ (r % CH)) << 4)) = v;
