@@ -1542,12 +1542,11 @@ Args grouped_args(const grouped_desc* d, int mode)
     return g;
 }
 
-int plan_grouped(const grouped_desc* d, int mode, const Args& g, Plan* p, int* cus)
+int plan_grouped(const grouped_desc* d, int mode, const Args& g, int cus, Plan* p)
 {
-    int st = device_cus(cus);
-    if (st != GEMM_F16_NT_OK) return st;
-    *p = mode == NT ? plan_for<NT>(d->dtype, g, *cus, &st) : mode == NN ? plan_for<NN>(d->dtype, g, *cus, &st)
-         : d->b_fp32 ? plan_for<TN, true>(d->dtype, g, *cus, &st) : plan_for<TN>(d->dtype, g, *cus, &st);
+    int st = GEMM_F16_NT_OK;
+    *p = mode == NT ? plan_for<NT>(d->dtype, g, cus, &st) : mode == NN ? plan_for<NN>(d->dtype, g, cus, &st)
+         : d->b_fp32 ? plan_for<TN, true>(d->dtype, g, cus, &st) : plan_for<TN>(d->dtype, g, cus, &st);
     return st;
 }
 
@@ -1556,9 +1555,8 @@ int64_t grouped_bytes(const grouped_desc* d, Written out)
 {
     int st = check_grouped(d, out), cus = 0;
     if (st != GEMM_F16_NT_OK) return st > 0 ? 0 : st;
-    const Args g = grouped_args(d, MODE);
     Plan p;
-    if ((st = plan_grouped(d, MODE, g, &p, &cus)) != GEMM_F16_NT_OK) return st;
+    if ((st = device_cus(&cus)) != GEMM_F16_NT_OK || (st = plan_grouped(d, MODE, grouped_args(d, MODE), cus, &p)) != GEMM_F16_NT_OK) return st;
     return p.part_bytes;
 }
 
@@ -1569,7 +1567,7 @@ int grouped_run(const grouped_desc* d, Written out, void* workspace, int64_t wor
     if (st != GEMM_F16_NT_OK) return st > 0 ? GEMM_F16_NT_OK : st;
     const Args g = grouped_args(d, MODE);
     Plan p;
-    if ((st = plan_grouped(d, MODE, g, &p, &cus)) != GEMM_F16_NT_OK) return st;
+    if ((st = device_cus(&cus)) != GEMM_F16_NT_OK || (st = plan_grouped(d, MODE, g, cus, &p)) != GEMM_F16_NT_OK) return st;
     if ((st = check_workspace(workspace, workspace_bytes, p.part_bytes)) != GEMM_F16_NT_OK) return st;
     if ((st = check_grouped(d, out, {workspace, p.part_bytes})) != GEMM_F16_NT_OK) return st;
     return run<MODE>(p, g, workspace, cus, (hipStream_t)stream);
@@ -1584,6 +1582,7 @@ struct AdapterCall {
     const void* single;   // all in one launch
     const void* pair;     // projections and shared product in one
     const void* end;      // and what puts them together
+    int bm, bn;           // the shared product's tile there
     bool dots;            // finish_kernel
     int64_t low_wgs;
     int cus;
@@ -1676,6 +1675,8 @@ void plan_pair(const adapter_desc* d, AdapterCall* c, int64_t* parts, double* tw
     *two = best;
     const int64_t rt = ceil_div(d->rows, form->bm), ct = ceil_div(d->N, form->bn);
     c->pair = c->dots ? form->plane : form->held;
+    c->bm = form->bm;
+    c->bn = form->bn;
     c->end = !c->dots ? form->first : d->dtype == GROUPED_F16 ? finish<F16>(d->rank) : finish<BF16>(d->rank);
     c->each = false;
     c->low.d_ld = (c->dots ? 4 : 2) * d->rank;   // in fp32, or in two terms
@@ -1713,10 +1714,10 @@ int run_pair(const AdapterCall& c, void* workspace, hipStream_t s)
     return hipLaunchKernel(c.end, grid, dim3(256), a, 0, s) == hipSuccess ? GEMM_F16_NT_OK : GEMM_F16_NT_LAUNCH;
 }
 
-int plan_adapters(const adapter_desc* d, AdapterCall* c)
+int plan_adapters(const adapter_desc* d, int cus, AdapterCall* c)
 {
-    int st = device_cus(&c->cus);
-    if (st != GEMM_F16_NT_OK) return st;
+    int st = GEMM_F16_NT_OK;
+    c->cus = cus;
     c->adapted = d->adapters > 0 && d->rank > 0;
     c->single = c->pair = c->end = nullptr;
     c->dots = false;
@@ -1831,20 +1832,66 @@ int grouped_tn(const grouped_desc* d, void* workspace, int64_t workspace_bytes, 
     return grouped_run<TN>(d, B_, workspace, workspace_bytes, stream);
 }
 
+int gemm_f16_nt_grouped_plan(const grouped_desc* d, int product, int cus, int tile[2], int64_t* parts)
+{
+    if (product < GROUPED_NT || product > GROUPED_TN || cus < 1 || tile == nullptr || parts == nullptr) return GEMM_F16_NT_INVALID_ARG;
+    const int mode = product == GROUPED_NT ? NT : product == GROUPED_NN ? NN : TN;
+    int st = check_grouped(d, mode == NT ? D_ : mode == NN ? A_ : B_);
+    if (st < 0) return st;
+    tile[0] = tile[1] = 0;
+    *parts = 0;
+    if (st > 0) return GEMM_F16_NT_OK;
+    Plan p;
+    if ((st = plan_grouped(d, mode, grouped_args(d, mode), cus, &p)) != GEMM_F16_NT_OK) return st;
+    tile[0] = p.form->bm;
+    tile[1] = p.form->bn;
+    *parts = p.walks ? (p.part_bytes > 0 ? 0 : 1) : p.splits;
+    return GEMM_F16_NT_OK;
+}
+
+int gemm_f16_nt_adapter_plan(const adapter_desc* d, int cus, int* way, int tile[2], int64_t* parts, int low_tile[2], int64_t* low_parts)
+{
+    if (cus < 1 || way == nullptr || tile == nullptr || parts == nullptr || low_tile == nullptr || low_parts == nullptr) return GEMM_F16_NT_INVALID_ARG;
+    int st = check_adapters(d);
+    if (st < 0) return st;
+    *way = tile[0] = tile[1] = low_tile[0] = low_tile[1] = 0;
+    *parts = *low_parts = 0;
+    if (st > 0) return GEMM_F16_NT_OK;
+    AdapterCall c;
+    if ((st = plan_adapters(d, cus, &c)) != GEMM_F16_NT_OK) return st;
+    if (c.single != nullptr) {
+        *way = ADAPTER_ONE_LAUNCH;
+        tile[0] = tile[1] = 16;
+        *parts = 1;
+        return GEMM_F16_NT_OK;
+    }
+    const bool pair = c.pair != nullptr;
+    *way = pair ? (c.dots ? ADAPTER_DOTS : ADAPTER_SUMS) : c.each ? ADAPTER_EACH : ADAPTER_TILES;
+    tile[0] = pair ? c.bm : c.plan.form->bm;
+    tile[1] = pair ? c.bn : c.plan.form->bn;
+    *parts = !pair && c.plan.walks ? (c.plan.part_bytes > 0 ? 0 : 1) : c.plan.splits;
+    if (c.adapted) {
+        low_tile[0] = pair ? 16 : c.low_plan.form->bm;
+        low_tile[1] = pair ? 16 : c.low_plan.form->bn;
+        *low_parts = pair ? 1 : c.low_plan.splits;
+    }
+    return GEMM_F16_NT_OK;
+}
+
 int64_t adapter_nt_workspace(const adapter_desc* d)
 {
-    int st = check_adapters(d);
+    int st = check_adapters(d), cus = 0;
     if (st != GEMM_F16_NT_OK) return st > 0 ? 0 : st;
     AdapterCall c;
-    return (st = plan_adapters(d, &c)) != GEMM_F16_NT_OK ? st : c.bytes;
+    return (st = device_cus(&cus)) != GEMM_F16_NT_OK || (st = plan_adapters(d, cus, &c)) != GEMM_F16_NT_OK ? st : c.bytes;
 }
 
 int adapter_nt(const adapter_desc* d, void* workspace, int64_t workspace_bytes, void* stream)
 {
-    int st = check_adapters(d);
+    int st = check_adapters(d), cus = 0;
     if (st != GEMM_F16_NT_OK) return st > 0 ? GEMM_F16_NT_OK : st;
     AdapterCall c;
-    if ((st = plan_adapters(d, &c)) != GEMM_F16_NT_OK) return st;
+    if ((st = device_cus(&cus)) != GEMM_F16_NT_OK || (st = plan_adapters(d, cus, &c)) != GEMM_F16_NT_OK) return st;
     if ((st = check_workspace(workspace, workspace_bytes, c.bytes)) != GEMM_F16_NT_OK) return st;
     if ((st = check_adapters(d, {workspace, c.bytes})) != GEMM_F16_NT_OK) return st;
     if (c.single != nullptr) return launch(c.single, ceil_div(c.rest.cols, 16), 256, &c.rest, (hipStream_t)stream);

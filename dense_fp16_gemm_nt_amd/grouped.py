@@ -53,6 +53,31 @@ def declare(L: ctypes.CDLL) -> None:
         f.restype, f.argtypes = i64, [vp]
         f = getattr(L, name + "_check")
         f.restype, f.argtypes = i32, [vp]
+    ip, i64p = ctypes.POINTER(i32), ctypes.POINTER(i64)
+    L.gemm_f16_nt_grouped_plan.restype, L.gemm_f16_nt_grouped_plan.argtypes = i32, [vp, i32, i32, ip, i64p]
+    L.gemm_f16_nt_adapter_plan.restype, L.gemm_f16_nt_adapter_plan.argtypes = i32, [vp, i32, ip, ip, i64p, ip, i64p]
+
+
+def plan(product: str, desc: GroupedDesc, cus: int):
+    """(tile rows, tile columns, parts of the contraction) that "nt", "nn" or "tn" runs with on a device with `cus` compute
+    units (host evaluation, no GPU needed); 0 parts: the device divides a small last round of large tiles."""
+    tile, parts = (ctypes.c_int * 2)(), ctypes.c_int64()
+    st = lib().gemm_f16_nt_grouped_plan(ctypes.byref(desc), ("nt", "nn", "tn").index(product), int(cus), tile, ctypes.byref(parts))
+    if st != OK:
+        raise GemmError(st, "gemm_f16_nt_grouped_plan")
+    return tile[0], tile[1], parts.value
+
+
+ONE_LAUNCH, DOTS, SUMS, TILES, EACH = 1, 2, 3, 4, 5   # ways of an adapter_nt call
+
+
+def adapter_plan(desc: AdapterDesc, cus: int):
+    """(way, (tile rows, tile columns, parts), the same of the projections) of an adapter_nt call, as `plan`."""
+    way, tile, low, parts, low_parts = ctypes.c_int(), (ctypes.c_int * 2)(), (ctypes.c_int * 2)(), ctypes.c_int64(), ctypes.c_int64()
+    st = lib().gemm_f16_nt_adapter_plan(ctypes.byref(desc), int(cus), ctypes.byref(way), tile, ctypes.byref(parts), low, ctypes.byref(low_parts))
+    if st != OK:
+        raise GemmError(st, "gemm_f16_nt_adapter_plan")
+    return way.value, (tile[0], tile[1], parts.value), (low[0], low[1], low_parts.value)
 
 
 _torch = None

@@ -53,6 +53,10 @@ extern "C" {
 #define GROUPED_F16 0
 #define GROUPED_BF16 1
 
+#define GROUPED_NT 0
+#define GROUPED_NN 1
+#define GROUPED_TN 2
+
 /* Rows r of group e and the group's matrix B_e (N x K):
  *
  *   grouped_nt   D[r] = B_e A[r]                            reads A, B, writes D
@@ -90,6 +94,13 @@ int grouped_nt_check(const grouped_desc* d);
 int grouped_nn_check(const grouped_desc* d);
 int grouped_tn_check(const grouped_desc* d);
 
+/* Host evaluation of what a call (`product`: GROUPED_NT, ...) runs on a device
+ * with `cus` compute units, no HIP call: tiles of tile[0] rows and tile[1]
+ * columns, and *parts parts of the contraction (0: the device divides a last
+ * round of large tiles where that is a small one).  All are 0 for a call that
+ * writes nothing.  Returns 0 or a negative status. */
+int gemm_f16_nt_grouped_plan(const grouped_desc* d, int product, int cus, int tile[2], int64_t* parts);
+
 /* One projection for all rows, and beside it the adapter that a row's request
  * asks for:
  *
@@ -125,6 +136,17 @@ typedef struct adapter_desc {
 int adapter_nt(const adapter_desc* d, void* workspace, int64_t workspace_bytes, void* stream);
 int64_t adapter_nt_workspace(const adapter_desc* d);
 int adapter_nt_check(const adapter_desc* d);
+
+/* The ways of a call: */
+#define ADAPTER_ONE_LAUNCH 1   /* the projections as columns of the shared product's tiles */
+#define ADAPTER_DOTS 2         /* the projections beside the shared product, then a dot product for each output */
+#define ADAPTER_SUMS 3         /* the same, then tiles that begin with the shared product's sums */
+#define ADAPTER_TILES 4        /* the projections, then tiles with the adapters as more of the contraction */
+#define ADAPTER_EACH 5         /* the same in large tiles of one request each */
+
+/* Host evaluation as above: the way, the shared product's tiles and parts, and
+ * the projections' (0 without adapters or in one launch). */
+int gemm_f16_nt_adapter_plan(const adapter_desc* d, int cus, int* way, int tile[2], int64_t* parts, int low_tile[2], int64_t* low_parts);
 
 #ifdef __cplusplus
 }

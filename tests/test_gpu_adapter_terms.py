@@ -14,7 +14,8 @@ import pytest
 
 import dense_fp16_gemm_nt_amd as g
 from tests import grouped_ref as ref
-from tests.test_gpu_grouped import ADAPTERS, DEV, TYPES, ints, kept, starts, whole
+from tests.adapter_cases import EVERY_WAY
+from tests.test_gpu_grouped import DEV, TYPES, adapter_inputs, ints, kept, real, starts, whole
 
 pytestmark = pytest.mark.gpu
 
@@ -34,12 +35,44 @@ def cancelling(seed, dtype, case):
     return whole(gen, dtype, sum(lens), k), -base[j], down, up, starts(lens), ids
 
 
-@pytest.mark.parametrize("case", range(len(ADAPTERS)))
+@pytest.mark.parametrize("case", range(len(EVERY_WAY)))
 @pytest.mark.parametrize("dtype", sorted(TYPES))
 def test_low_rank_values_are_held_in_two_terms(dtype, case):
-    A, B, down, up, cu, ids = cancelling(700 + case, dtype, ADAPTERS[case])
-    print(f"[gpu] cancelling adapters {dtype} {ADAPTERS[case][2:]}", file=sys.stderr, flush=True)
+    A, B, down, up, cu, ids = cancelling(700 + case, dtype, EVERY_WAY[case])
+    print(f"[gpu] cancelling adapters {dtype} {EVERY_WAY[case][2:]}", file=sys.stderr, flush=True)
     D = g.adapter_product(A, B, down, up, ints(cu), ints(ids), D=kept(dtype, A.shape[0], B.shape[0]))
     torch.cuda.synchronize()
     want, _ = ref.adapters(A, B, down, up, cu, ids, None, kept(dtype, A.shape[0], B.shape[0]))
     assert torch.equal(D, want.to(TYPES[dtype]))
+
+
+@pytest.mark.parametrize("case", range(len(EVERY_WAY)))
+@pytest.mark.parametrize("dtype", sorted(TYPES))
+def test_values_on_every_way(dtype, case):
+    A, B, down, up, cu, ids = adapter_inputs(real, 750 + case, dtype, EVERY_WAY[case], 3, 5, 8)
+    scales = torch.linspace(-1.5, 2.0, down.shape[0], device=DEV)
+    down = down / 8
+    print(f"[gpu] adapter values {dtype} {EVERY_WAY[case][2:]}", file=sys.stderr, flush=True)
+    D = kept(dtype, A.shape[0], B.shape[0], 8)
+    g.adapter_product(A, B, down, up, ints(cu), ints(ids), scales, D=D)
+    torch.cuda.synchronize()
+    # rows of no request keep what they held; the others' bound is that of products whose low-rank values are off by 2^-16 of
+    # themselves in bf16, and in fp16 by 2^-20 or 2^-25
+    own = slice(cu[0], cu[-1])
+    assert bool((D[:cu[0]] == 7).all()) and bool((D[cu[-1]:] == 7).all())
+    t, rank = TYPES[dtype], down.shape[1]
+    want, bound = kept(dtype, A.shape[0], B.shape[0]).double(), torch.zeros(D.shape, dtype=torch.float64, device=DEV)
+    for q, (a, b) in enumerate(zip(cu[:-1], cu[1:])):
+        if a == b:
+            continue
+        x, i = A[a:b].double(), ids[q]
+        want[a:b], bound[a:b] = ref._sum(x, B.double().t(), A.shape[1])
+        if 0 <= i < down.shape[0]:
+            h, off = ref._sum(x, down[i].double().t(), A.shape[1])
+            s = float(scales[i])
+            h, off = h * s, off * abs(s) + h.abs() * abs(s) * ref.STEP
+            off = off + (2.0 ** -16 if t is torch.bfloat16 else 2.0 ** -20) * (h.abs() + off) + (2.0 ** -25 if t is torch.float16 else 0.0)
+            w = up[i].double().t()
+            want[a:b] += torch.mm(h, w)
+            bound[a:b] += torch.mm(off, w.abs()) + (2 * rank + 8) * ref.STEP * torch.mm(h.abs() + off, w.abs())
+    ref.check(D[own], want[own], bound[own], "adapters")
