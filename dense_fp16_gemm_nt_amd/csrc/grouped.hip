@@ -423,7 +423,7 @@ __device__ __forceinline__ void store_not_finite(const Args& g, const Entry* tab
             const int at = 4 * (b % 4);
             *reinterpret_cast<f32x4*>(to + (lane & 31) * W + 8 * b + 4 * (lane >> 5)) = f32x4{v[at], v[at + 1], v[at + 2], v[at + 3]};
         }
-        __builtin_amdgcn_wave_barrier();
+        grp::wave_in_order();
         for (int x = lane; x < 32 * W; x += 64) {
             const int r = x / W, c = x % W, row = r0 + 32 * i + r;
             if (r >= ROWS || c >= COLS || 32 * i + r >= rows || c >= cols) continue;
@@ -447,7 +447,7 @@ __device__ __forceinline__ void store_not_finite(const Args& g, const Entry* tab
             else
                 *reinterpret_cast<uint16_t*>(at) = (uint16_t)T::pack(v, 0.f);
         }
-        __builtin_amdgcn_wave_barrier();
+        grp::wave_in_order();
     }
 }
 
@@ -913,6 +913,7 @@ __global__ __launch_bounds__(256) void finish_kernel(const Args g)
         y += v[1];
     }
     if (adapted) {   // a wave's own values
+        grp::wave_in_order();
         x += dots[128 * w + 2 * lane];
         y += dots[128 * w + 2 * lane + 1];
     }

@@ -195,6 +195,14 @@ __device__ __forceinline__ void multiply(const Frags<C, XC, C::BM, C::FM>& fx, c
     }
 }
 
+// Between what lanes of a wave write to LDS and what others of it read: the wave
+// does both in order, and the compiler has to keep that order.
+__device__ __forceinline__ void wave_in_order()
+{
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+}
+
 // Adds the sums of the waves along the contraction to those of the first.
 template <class C>
 __device__ __forceinline__ void add_waves(char* smem, int wk, int lane, Acc<C>& acc)
@@ -282,7 +290,7 @@ __device__ __forceinline__ void store(char* lds, char* d, int64_t ld, int rows, 
                     *reinterpret_cast<u32x2*>(lds + r * PITCH + ((c ^ (r % CH)) << 4) + 8 * half) = u32x2{T::pack(v[0], v[1]), T::pack(v[2], v[3])};
                 }
             }
-        __builtin_amdgcn_wave_barrier();
+        wave_in_order();
 #pragma unroll
         for (int q = 0; q < 32 / PER; ++q) {
             const int y = q * PER + lane / CH, c = lane % CH;
@@ -290,7 +298,7 @@ __device__ __forceinline__ void store(char* lds, char* d, int64_t ld, int rows, 
             if ((C::BM > 16 || y < 16) && (C::BN > 16 || c * (16 / SIZE) < 16) && 32 * i + y < rows && c * (16 / SIZE) < cols)
                 *reinterpret_cast<u32x4*>(d + (int64_t)(32 * i + y) * ld + 16 * c) = v;
         }
-        __builtin_amdgcn_wave_barrier();
+        wave_in_order();
     }
 }
 
