@@ -426,7 +426,7 @@ def generate(la: str, lb: str, p: dict) -> str:
 
 # Loads of step j + 2 all go out in step j, so that they have the rest of it
 # and the next step up to the publish barrier to land.
-ROWS = {"rel": 12, "load_every": 6, "pub": 64, "a_delay": 1, "read_limit": 112, "f0_lat": 8, "epi_slot": 8, "epi_delay": 2, "nxt_start": 2, "nxt_every": 4}
+ROWS = {"rel": 12, "load_every": 6, "pub": 64, "a_delay": 1, "read_limit": 112, "f0_lat": 8, "epi_slot": 8, "epi_delay": 2, "nxt_start": 2}
 MIXED = {**ROWS, "pub": 56}
 COLS = {**ROWS, "rel": 14, "pub": 48}
 
