@@ -663,9 +663,10 @@ __device__ __forceinline__ void tile_body(const Args& g, char* smem, uint32_t in
 // of `down`, so many of each request.  Their sums are the second product's
 // operand as they lie in the accumulators, two terms of each: the order of that
 // contraction is free, and `up` is read to match.  What bounds it is the latency
-// of a chain: arguments, the first loads, the bytes (24 to 40 KiB in flight on a
-// compute unit), the sums of four waves.  So the shared matrix is asked for before the
-// requests' rows are known, which are read as scalars, by themselves.
+// of a chain: arguments, the first loads, the bytes (120 KiB in flight on a
+// compute unit, in stages of 24 or 40 KiB, of which 8 are the shared matrix's),
+// the sums of four waves.  So the shared matrix is asked for before the requests'
+// rows are known, which are read as scalars, by themselves.
 template <typename T, int RB>
 __global__ __launch_bounds__(256, 1) void single_kernel(const Args g)
 {
@@ -851,6 +852,9 @@ __device__ __forceinline__ float sum_lanes(float x)
 // column, so that a load covers whole rows of `up` (with a lane to a column
 // those of rank 64 took 3 times as long).  What bounds it is the bytes of `up`,
 // read once for each row of its request (64 rows of 14336, rank 16: 6.8 us).
+// Every workgroup looks for its row's request from the first on, 64 at a time,
+// so that single tokens take longer than their number says (1024 x 1024, rank
+// 16: 256 of them 13 us a call, 1000 41, 2000 101, 4096 318).
 template <typename T, int L>
 __global__ __launch_bounds__(256) void finish_kernel(const Args g)
 {
@@ -1320,7 +1324,8 @@ constexpr int64_t kMaxSplits = 16;
 // order once, the others for each tile, and with many rounds the order makes no
 // difference.  (7901 rows over 8 matrices of 1024 x 4864, large tiles: 101 us in
 // the groups' own order, 75 so; 9630 rows, 8 of 2048 x 1536, tiles of 128 x 128:
-// 85 and 76; but 1500 rows, 64 of 2048 x 1024, 16 rounds of them: 102 and 136.)
+// 85 and 76; but 1500 rows, 64 of 2048 x 1024, 16 rounds of them: 102 and 136.
+// Between 8 groups and 64 of the small tiles nothing was measured.)
 bool sorts(bool walks, int64_t groups, int64_t tiles, int cus)
 {
     return groups > 1 && groups <= (walks ? 64 : 16) && tiles <= (int64_t)(walks ? 8 : 16) * cus;
@@ -1343,7 +1348,8 @@ Plan plan(const Form* forms, int n, const Args& g, int cus, int* status)
     const double memory = (mats * (MODE == TN && F32 ? 2 : 1) + rows) * 2 / 5.5e6;
     // TN: matrices are written when a workgroup ends, half of it beside others'
     // products; and a single round of workgroups takes as long as its longest
-    // group, with rows unevenly divided 1.6 times the mean
+    // group, taken as 1.6 times the mean (of 8 groups whose likelihoods are even
+    // from 0.2 to 1.8 it is 1.3 to 2.1 times that, mostly 1.6)
     const double written = MODE == TN ? mats * (F32 ? 4 : 2) / 5.5e6 / 2 : 0., longest = MODE == TN && g.groups > 1 ? 1.6 : 1.;
     const bool odd = odd_pitch(g);
     Plan best = {nullptr, 0, 1, 0, false, 1e300};
@@ -1626,7 +1632,9 @@ void plan_pair(const adapter_desc* d, AdapterCall* c, int64_t* parts, double* tw
     const double low_rows = (double)d->rows / 16 + 0.5 * used, low_mean = (low_rows > used ? low_rows : (double)used) * ceil_div(d->rank, 16);
     const double low_one = odd ? kTiny2.odd_one : kTiny2.one, low_two = odd ? kTiny2.odd_two : kTiny2.two;
     // finish_kernel reads `up` for each row, more often from L2 than from memory,
-    // and has 8 workgroups on a compute unit, each a chain of some 5 us
+    // and has 8 workgroups on a compute unit, each a chain of some 5 us.  It was
+    // measured up to 4096 rows and is not taken beyond (1024 x 1024, rank 16, one
+    // row a request: 318 us, and 361 for 4104 in tiles).
     double dots = (double)d->rows * d->N * d->rank * 2 / 1e7;
     if (dots < kinds * d->N / 5e6) dots = kinds * d->N / 5e6;
     if (dots < (double)d->rows * ceil_div(d->N, 512) * 2.5e-3) dots = (double)d->rows * ceil_div(d->N, 512) * 2.5e-3;

@@ -290,7 +290,8 @@ def grouped_product_grad_weight(G, A, cu, *, dB=None, dtype=None, workspace=None
 
 
 def grouped_product_grad_weight_workspace(G, A, cu, *, dtype=None) -> int:
-    """Bytes of workspace grouped_product_grad_weight needs for tensors of these shapes (0: none)."""
+    """Bytes of workspace grouped_product_grad_weight needs for tensors of these shapes (0: none), and a dB, if one is given,
+    whose rows begin less than 2^21 elements apart."""
     return _workspace_bytes("grouped_tn", *_grad_weight_desc(G, A, cu, None, G.dtype if dtype is None else dtype))
 
 
